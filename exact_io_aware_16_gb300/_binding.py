@@ -29,6 +29,13 @@ STATUS_NAMES = {
 }
 
 
+class _CacheStruct(ctypes.Structure):
+    """fa_cache of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("B", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("cap", ctypes.c_int), ("d", ctypes.c_int), ("format", ctypes.c_int)]
+
+
 class FaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -84,6 +91,17 @@ def library():
         lib.fa_decode_workspace_size.restype = sz
         lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp, sz, vp]
         lib.fa_decode.restype = i
+        pc = ctypes.POINTER(_CacheStruct)
+        lib.fa_cache_write.argtypes = [pc, vp, vp, vp, vp, i, vp]
+        lib.fa_cache_write.restype = i
+        lib.fa_cache_read.argtypes = [pc, vp, vp, vp, vp, i, vp]
+        lib.fa_cache_read.restype = i
+        lib.fa_cache_commit.argtypes = [pc, vp, vp, vp, vp, i, vp]
+        lib.fa_cache_commit.restype = i
+        lib.fa_decode_tree_workspace_size.argtypes = [pc, i, i]
+        lib.fa_decode_tree_workspace_size.restype = sz
+        lib.fa_decode_tree.argtypes = [pc, vp, vp, vp, ll, vp, vp, i, i, f, vp, sz, vp]
+        lib.fa_decode_tree.restype = i
         lib.fa_backward_preprocess.argtypes = [vp, vp, vp, i, i, i, i, vp]
         lib.fa_backward_preprocess.restype = i
         lib.fa_backward_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i,
@@ -449,6 +467,222 @@ def fa_decode(q, k, v, causal: bool = False, scale: float | None = None, o=None,
                                  ctypes.c_void_p(_stream_handle(stream, q.device)))
     if st != FA_OK:
         raise FaError(st, "fa_decode")
+    return o, lse
+
+
+class KvCache:
+    """A key/value cache on one GPU: B sequences of up to `capacity` tokens for
+    Hkv key heads of d elements, in bf16 or quantised to e4m3 (one power-of-two
+    scale a row) as rows are written.
+
+    k, v: [B, Hkv, capacity, d], torch.bfloat16 or torch.float8_e4m3fn (codes);
+    k_scale, v_scale: torch.uint8 [B, Hkv, capacity] (exponent + 127), None for
+    bf16; lens: torch.int32 [B], the committed tokens of each sequence, which
+    the calls below use where they are given no other lengths.  The tensors may
+    be written in place; the object keeps these very tensors for its life.
+    `capacity` must be a multiple of 16 for e4m3.
+    """
+
+    def __init__(self, B: int, Hkv: int, capacity: int, d: int, format: str = "e4m3",
+                 device=None):
+        if format not in ("e4m3", "bf16"):
+            raise ValueError(f"format must be 'e4m3' or 'bf16', got {format!r}")
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        dt = torch.float8_e4m3fn if format == "e4m3" else torch.bfloat16
+        shape = (int(B), int(Hkv), int(capacity), int(d))
+        scales = [None, None] if format == "bf16" else \
+            [torch.zeros(shape[:3], dtype=torch.uint8, device=dev) for _ in range(2)]
+        self._hold(torch.zeros(shape, dtype=dt, device=dev),
+                   torch.zeros(shape, dtype=dt, device=dev), *scales, None)
+
+    @classmethod
+    def from_tensors(cls, k, v, k_scale=None, v_scale=None, lens=None):
+        """A cache over tensors that the caller already holds."""
+        self = cls.__new__(cls)
+        self._hold(k, v, k_scale, v_scale, lens)
+        return self
+
+    def _hold(self, k, v, k_scale, v_scale, lens):
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError(f"k must be torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if k.dim() != 4:
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected [B, Hkv, capacity, d]")
+        B, Hkv, cap, d = k.shape
+        _check(k, "k", k.dtype)
+        _check(v, "v", k.dtype, k.shape)
+        if e4m3:
+            if k_scale is None or v_scale is None:
+                raise ValueError("an e4m3 cache needs k_scale and v_scale")
+            _check(k_scale, "k_scale", torch.uint8, (B, Hkv, cap))
+            _check(v_scale, "v_scale", torch.uint8, (B, Hkv, cap))
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        if lens is None:
+            lens = torch.zeros(B, dtype=torch.int32, device=k.device)
+        _check(lens, "lens", torch.int32, (B,))
+        self._dev = _one_device((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale"),
+                                (lens, "lens"))
+        self._t = (k, v, k_scale, v_scale, lens)
+        self._shape = (B, Hkv, cap, d)
+        self._struct = _CacheStruct(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+            v_scale.data_ptr() if e4m3 else None, B, Hkv, cap, d, int(e4m3))
+        self._ref = ctypes.byref(self._struct)
+
+    k = property(lambda self: self._t[0])
+    v = property(lambda self: self._t[1])
+    k_scale = property(lambda self: self._t[2])
+    v_scale = property(lambda self: self._t[3])
+    lens = property(lambda self: self._t[4])
+    shape = property(lambda self: self._shape)
+    format = property(lambda self: "e4m3" if self._struct.format else "bf16")
+
+
+def _check_on(cache, t, name, dtype, shape):
+    """_check, and the cache's GPU."""
+    _check(t, name, dtype, shape)
+    if _device_index(t) != cache._dev:
+        raise ValueError(f"{name} is on device {_device_index(t)}, the cache on device "
+                         f"{cache._dev}")
+
+
+def _check_ints(cache, t, name, shape):
+    if t is not None:
+        _check_on(cache, t, name, torch.int32, shape)
+
+
+def fa_cache_write(cache: KvCache, k, v, lens=None, counts=None, stream=None):
+    """Write rows k, v (bf16 [B,Hkv,N,d]) to positions lens[b] + i of the cache
+    (lens: cache.lens unless given; it is not advanced), quantised if the
+    cache is; counts (int32 [B], optional): rows i >= counts[b] are not
+    written.  Positions outside the cache are not written."""
+    B, Hkv, cap, d = cache._shape
+    if k.dim() != 4:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [B, Hkv, N, d]")
+    N = k.shape[2]
+    lens = cache._t[4] if lens is None else lens
+    _check_on(cache, k, "k", torch.bfloat16, (B, Hkv, N, d))
+    _check_on(cache, v, "v", torch.bfloat16, (B, Hkv, N, d))
+    _check_ints(cache, lens, "lens", (B,))
+    _check_ints(cache, counts, "counts", (B,))
+    with _device_guard(cache._dev):
+        st = library().fa_cache_write(cache._ref, _ptr(k), _ptr(v), _ptr(lens), _ptr(counts), N,
+                                      ctypes.c_void_p(_stream_handle(stream, k.device)))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_write")
+
+
+def fa_cache_read(cache: KvCache, N: int, first=None, counts=None, k=None, v=None, stream=None):
+    """(k, v), bf16 [B,Hkv,N,d]: positions first[b] + i (first: 0 unless given)
+    for i < counts[b] (cache.lens unless given), zero for the other i < N and
+    for positions outside the cache."""
+    B, Hkv, cap, d = cache._shape
+    shape = (B, Hkv, int(N), d)
+    dev = cache._t[0].device
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    counts = cache._t[4] if counts is None else counts
+    _check_on(cache, k, "k", torch.bfloat16, shape)
+    _check_on(cache, v, "v", torch.bfloat16, shape)
+    _check_ints(cache, first, "first", (B,))
+    _check_ints(cache, counts, "counts", (B,))
+    with _device_guard(cache._dev):
+        st = library().fa_cache_read(cache._ref, _ptr(k), _ptr(v), _ptr(first), _ptr(counts),
+                                     int(N), ctypes.c_void_p(_stream_handle(stream, dev)))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_read")
+    return k, v
+
+
+def fa_cache_commit(cache: KvCache, path, n_accept, lens=None, new_lens=None, stream=None):
+    """Move the rows of drafts path[b, 0 .. n_accept[b]) (int32 [B,T], int32 [B])
+    to positions lens[b] + i and return new_lens = lens + n_accept.  lens and
+    new_lens: cache.lens, advanced in place, unless given (new_lens: lens
+    itself if only lens is given)."""
+    B = cache._shape[0]
+    if path.dim() != 2:
+        raise ValueError(f"path has shape {tuple(path.shape)}, expected [B, T]")
+    T = path.shape[1]
+    lens = cache._t[4] if lens is None else lens
+    new_lens = lens if new_lens is None else new_lens
+    _check_on(cache, path, "path", torch.int32, (B, T))
+    _check_ints(cache, n_accept, "n_accept", (B,))
+    _check_ints(cache, lens, "lens", (B,))
+    _check_ints(cache, new_lens, "new_lens", (B,))
+    with _device_guard(cache._dev):
+        st = library().fa_cache_commit(cache._ref, _ptr(lens), _ptr(path), _ptr(n_accept),
+                                       _ptr(new_lens), T,
+                                       ctypes.c_void_p(_stream_handle(stream, path.device)))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_commit")
+    return new_lens
+
+
+def tree_mask(parents):
+    """The mask row of each draft (torch.int64 [T] on the CPU; bit j: draft j is
+    seen) of the tree in which draft t's parent is draft parents[t] < t, or
+    none for -1: a draft sees itself and its ancestors."""
+    if not 1 <= len(parents) <= 64:
+        raise ValueError(f"a tree has 1 .. 64 drafts, got {len(parents)}")
+    rows = []
+    for t, p in enumerate(int(p) for p in parents):
+        if not -1 <= p < t:
+            raise ValueError(f"parents[{t}] must be -1 or an earlier draft, got {p}")
+        rows.append((rows[p] if p >= 0 else 0) | 1 << t)
+    return torch.tensor([r - (1 << 64) if r >> 63 else r for r in rows], dtype=torch.int64)
+
+
+def fa_decode_tree_workspace_size(cache: KvCache, Hq: int, T: int) -> int:
+    return int(library().fa_decode_tree_workspace_size(cache._ref, Hq, T))
+
+
+def fa_decode_tree(cache: KvCache, q, mask=None, lens=None, scale: float | None = None, o=None,
+                   lse=None, workspace=None, stream=None):
+    """Attention of T (<= 64) drafted tokens q (bf16 [B,Hq,T,d], Hq a multiple of
+    the cache's Hkv) over the cache: (o, lse).
+
+    Draft j lies at position lens[b] + j (lens: cache.lens unless given; write
+    the drafts there first).  Each draft sees the lens[b] committed tokens and
+    the drafts of its mask row: mask is torch.int64 [B,T], or [T] for one tree
+    shared by the batch, bit j for draft j; None: the drafts j <= t.  A draft
+    that sees nothing has o = 0 and lse = -inf.  Calls that may overlap on the
+    GPU need workspaces of their own (a new one is allocated by default)."""
+    B, Hkv, cap, d = cache._shape
+    if q.dim() != 4:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, Hq, T, d]")
+    Hq, T = q.shape[1], q.shape[2]
+    _check_on(cache, q, "q", torch.bfloat16, (B, Hq, T, d))
+    lens = cache._t[4] if lens is None else lens
+    _check_ints(cache, lens, "lens", (B,))
+    stride = 0
+    if mask is not None:
+        stride = T if mask.dim() == 2 else 0
+        _check_on(cache, mask, "mask", torch.int64, (B, T) if stride else (T,))
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _check_on(cache, o, "o", torch.bfloat16, (B, Hq, T, d))
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    else:
+        _check_on(cache, lse, "lse", torch.float32, (B, Hq, T))
+    if workspace is None:
+        need = fa_decode_tree_workspace_size(cache, Hq, T)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    else:
+        _check_workspace(workspace)
+        if _device_index(workspace) != cache._dev:
+            raise ValueError(f"workspace is on device {_device_index(workspace)}, the cache on "
+                             f"device {cache._dev}")
+    with _device_guard(cache._dev):
+        st = library().fa_decode_tree(cache._ref, _ptr(q), _ptr(lens), _ptr(mask), stride,
+                                      _ptr(o), _ptr(lse), Hq, T, float(scale), _ptr(workspace),
+                                      workspace.numel(),
+                                      ctypes.c_void_p(_stream_handle(stream, q.device)))
+    if st != FA_OK:
+        raise FaError(st, "fa_decode_tree")
     return o, lse
 
 

@@ -467,6 +467,145 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, 
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// The shape and pointer rules of a cache descriptor, in the order of fa.h.
+static int check_cache(const fa_cache* c) {
+  if (!c || !c->k || !c->v) return FA_ERR_NULL;
+  if (c->format != FA_CACHE_BF16 && c->format != FA_CACHE_E4M3) return FA_ERR_SHAPE;
+  const bool e4m3 = c->format == FA_CACHE_E4M3;
+  if (e4m3 && (!c->k_scale || !c->v_scale)) return FA_ERR_NULL;
+  const int st = fa::check_bhnd(c->B, c->Hkv, c->cap, c->d);
+  if (st != FA_OK) return st;
+  const long long BH = static_cast<long long>(c->B) * c->Hkv;
+  if (BH * fa::num_tiles(c->cap, 64) > 0x7fffffffll) return FA_ERR_SHAPE;
+  if (e4m3 && c->cap % 16 != 0) return FA_ERR_SHAPE;
+  return FA_OK;
+}
+
+static int check_cache_align(const fa_cache* c) {
+  if (!aligned16(c->k) || !aligned16(c->v)) return FA_ERR_ALIGN;
+  if (c->format == FA_CACHE_E4M3 && (!aligned16(c->k_scale) || !aligned16(c->v_scale)))
+    return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Rows a sequence of a write or read: at least one, all of them an int32 count.
+static int check_cache_rows(const fa_cache* c, int N) {
+  if (N < 1) return FA_ERR_SHAPE;
+  return static_cast<long long>(c->B) * c->Hkv > (0x3fffffffll / N) ? FA_ERR_SHAPE : FA_OK;
+}
+
+int fa_cache_write(const fa_cache* cache, const void* k, const void* v, const int* lens,
+                   const int* counts, int N, void* stream) {
+  int st = check_cache(cache);
+  if (st != FA_OK) return st;
+  if (!k || !v || !lens) return FA_ERR_NULL;
+  if ((st = check_cache_rows(cache, N)) != FA_OK) return st;
+  if ((st = check_cache_align(cache)) != FA_OK) return st;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(lens) || !aligned4(counts)) return FA_ERR_ALIGN;
+  if ((st = check_arch()) != FA_OK) return st;
+  fa::CacheMoveArgs a{};
+  a.c = *cache;
+  a.in_k = k;
+  a.in_v = v;
+  a.at = lens;
+  a.counts = counts;
+  a.N = N;
+  return fa::launch_cache_write(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                     : FA_ERR_CUDA;
+}
+
+int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, const int* counts,
+                  int N, void* stream) {
+  int st = check_cache(cache);
+  if (st != FA_OK) return st;
+  if (!k || !v || !counts) return FA_ERR_NULL;
+  if ((st = check_cache_rows(cache, N)) != FA_OK) return st;
+  if ((st = check_cache_align(cache)) != FA_OK) return st;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(first) || !aligned4(counts)) return FA_ERR_ALIGN;
+  if ((st = check_arch()) != FA_OK) return st;
+  fa::CacheMoveArgs a{};
+  a.c = *cache;
+  a.out_k = k;
+  a.out_v = v;
+  a.at = first;
+  a.counts = counts;
+  a.N = N;
+  return fa::launch_cache_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                    : FA_ERR_CUDA;
+}
+
+int fa_cache_commit(const fa_cache* cache, const int* lens, const int* path,
+                    const int* n_accept, int* new_lens, int T, void* stream) {
+  int st = check_cache(cache);
+  if (st != FA_OK) return st;
+  if (!lens || !path || !n_accept || !new_lens) return FA_ERR_NULL;
+  if (T < 1 || T > FA_TREE_MAX_DRAFTS) return FA_ERR_SHAPE;
+  if ((st = check_cache_align(cache)) != FA_OK) return st;
+  if (!aligned4(lens) || !aligned4(path) || !aligned4(n_accept) || !aligned4(new_lens))
+    return FA_ERR_ALIGN;
+  if ((st = check_arch()) != FA_OK) return st;
+  fa::CacheMoveArgs a{};
+  a.c = *cache;
+  a.at = lens;
+  a.counts = n_accept;
+  a.path = path;
+  a.new_lens = new_lens;
+  a.N = T;
+  return fa::launch_cache_commit(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+// Query shapes of a tree decode over a valid cache.
+static int check_tree_shape(const fa_cache* c, int Hq, int T) {
+  if (Hq < 1 || T < 1 || T > FA_TREE_MAX_DRAFTS || Hq % c->Hkv != 0) return FA_ERR_SHAPE;
+  if (static_cast<long long>(c->B) * Hq > 0x7fffffffll / T) return FA_ERR_SHAPE;
+  return FA_OK;
+}
+
+size_t fa_decode_tree_workspace_size(const fa_cache* cache, int Hq, int T) {
+  if (check_cache(cache) != FA_OK || check_tree_shape(cache, Hq, T) != FA_OK) return 0;
+  return fa::tree_workspace_bytes(*cache, Hq, T);
+}
+
+int fa_decode_tree(const fa_cache* cache, const void* q, const int* lens,
+                   const unsigned long long* mask, long long mask_stride, void* o, float* lse,
+                   int Hq, int T, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  int st = check_cache(cache);
+  if (st != FA_OK) return st;
+  if (!q || !lens || !o || !lse) return FA_ERR_NULL;
+  if ((st = check_tree_shape(cache, Hq, T)) != FA_OK) return st;
+  if (mask && mask_stride != 0 && mask_stride != T) return FA_ERR_SHAPE;
+  if ((st = check_scale(scale)) != FA_OK) return st;
+  if (!workspace || workspace_bytes < fa::tree_workspace_bytes(*cache, Hq, T) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return FA_ERR_WORKSPACE;
+  if ((st = check_cache_align(cache)) != FA_OK) return st;
+  if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(lens) ||
+      (reinterpret_cast<uintptr_t>(mask) & 7u) != 0)
+    return FA_ERR_ALIGN;
+  if ((st = check_arch()) != FA_OK) return st;
+  fa::TreeArgs a{};
+  a.c = *cache;
+  a.q = q;
+  a.lens = lens;
+  a.mask = mask;
+  a.mask_stride = mask_stride;
+  a.o = o;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.Hq = Hq;
+  a.T = T;
+  a.scale = scale;
+  a.num_sms = num_sms();
+  return fa::launch_decode_tree(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
 int fa_selftest_wait_timeout(void* stream) {
   const int st = check_arch();
   if (st != FA_OK) return st;

@@ -1,0 +1,278 @@
+// fa_cache.cu — the key/value cache: writing new rows (kept in bf16, or
+// quantised to e4m3 with a power-of-two scale for each row), reading rows back
+// in bf16, and moving the accepted path of a drafted tree into place.
+//
+// All three are copies with a conversion on the way: every byte is touched
+// once, so the calls are bound by HBM for prompts and by launch latency for
+// single tokens.  A row of d elements belongs to a group of d / 8 lanes, eight
+// elements a lane: 16-byte bf16 accesses and 8-byte code accesses, both
+// contiguous over the group, and a row's maximum takes log2(d / 8) shuffles.
+// Each thread has kRows rows in flight, so that a load's latency is paid once
+// for all of them.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kMoveThreads = 256;
+constexpr int kRows = 4;  // rows in flight a thread
+
+// Scale exponent of a row whose largest finite |x| has the bf16 bits `a`: the
+// least e with max|x| 2^-e <= 448 = 1.75 * 2^8, within -100 .. 119.
+__device__ __forceinline__ int scale_exponent(uint32_t a) {
+  const int e = static_cast<int>(a >> 7) - 135 + ((a & 0x7fu) > 0x60u ? 1 : 0);
+  return min(max(e, kScaleExpMin), kScaleExpMax);
+}
+
+__device__ __forceinline__ float pow2_of(int e) {  // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Largest finite magnitude of eight bf16, as bf16 bits in both halves' maximum.
+__device__ __forceinline__ uint32_t finite_max8(const uint4& x) {
+  uint32_t m = 0;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i] & 0x7fff7fffu;
+    m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7f807f80u));
+  }
+  return m;
+}
+
+// Two bf16 (one word) times s as two e4m3 codes.  x * 0 turns an infinity into
+// NaN before the saturating conversion would make it 448.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, float s) {
+  const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+  return __nv_cvt_float2_to_fp8x2(
+      make_float2(fmaf(lo, 0.0f, lo * s), fmaf(hi, 0.0f, hi * s)), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Two e4m3 codes times s as two bf16 (exact: four significant bits).
+__device__ __forceinline__ uint32_t values2(uint32_t c, float s) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
+  const float2 f = __half22float2(__half2(h));
+  return pack_bf16x2(f.x * s, f.y * s);
+}
+
+// One block: kMoveThreads / (D / 8) * kRows consecutive rows of one tensor.
+// Rows run over [B][Hkv][N]; blockIdx.y picks keys or values.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const CacheMoveArgs a) {
+  constexpr int kLanes = D / 8;
+  constexpr int kGroups = kMoveThreads / kLanes;
+  const bool val = blockIdx.y != 0;
+  const uint4* __restrict__ in = static_cast<const uint4*>(val ? a.in_v : a.in_k);
+  void* out = val ? a.c.v : a.c.k;
+  uint8_t* scale = val ? a.c.v_scale : a.c.k_scale;
+  const int lane = threadIdx.x % kLanes;
+  const int rows = a.c.B * a.c.Hkv * a.N;
+  const int r0 = blockIdx.x * (kGroups * kRows) + threadIdx.x / kLanes;
+  uint4 x[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int r = r0 + u * kGroups;
+    x[u] = r < rows ? in[static_cast<long long>(r) * kLanes + lane] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int r = r0 + u * kGroups;
+    const int bh = r / a.N, i = r - bh * a.N;
+    const int b = bh / a.c.Hkv;
+    uint32_t m = 0;
+    if (E4M3) {
+      m = finite_max8(x[u]);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = max(m & 0xffffu, m >> 16);
+    }
+    if (r >= rows) continue;
+    const long long pos = static_cast<long long>(a.at[b]) + i;
+    if ((a.counts && i >= a.counts[b]) || pos < 0 || pos >= a.c.cap) continue;
+    const long long dst = static_cast<long long>(bh) * a.c.cap + pos;
+    if (E4M3) {
+      const int e = scale_exponent(m);
+      const float s = pow2_of(-e);
+      static_cast<uint2*>(out)[dst * kLanes + lane] =
+          make_uint2(codes2(x[u].x, s) | codes2(x[u].y, s) << 16,
+                     codes2(x[u].z, s) | codes2(x[u].w, s) << 16);
+      if (lane == 0) scale[dst] = static_cast<uint8_t>(e + 127);
+    } else {
+      static_cast<uint4*>(out)[dst * kLanes + lane] = x[u];
+    }
+  }
+}
+
+// The inverse, with zeros in rows that are not read.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kMoveThreads) fa_cache_read_kernel(const CacheMoveArgs a) {
+  constexpr int kLanes = D / 8;
+  constexpr int kGroups = kMoveThreads / kLanes;
+  const bool val = blockIdx.y != 0;
+  const void* in = val ? a.c.v : a.c.k;
+  uint4* __restrict__ out = static_cast<uint4*>(val ? a.out_v : a.out_k);
+  const uint8_t* scale = val ? a.c.v_scale : a.c.k_scale;
+  const int lane = threadIdx.x % kLanes;
+  const int rows = a.c.B * a.c.Hkv * a.N;
+  const int r0 = blockIdx.x * (kGroups * kRows) + threadIdx.x / kLanes;
+  uint4 x[kRows];
+  uint32_t s[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int r = r0 + u * kGroups;
+    x[u] = make_uint4(0, 0, 0, 0);
+    s[u] = 127;
+    if (r >= rows) continue;
+    const int bh = r / a.N, i = r - bh * a.N;
+    const int b = bh / a.c.Hkv;
+    const long long pos = static_cast<long long>(a.at ? a.at[b] : 0) + i;
+    if (i >= a.counts[b] || pos < 0 || pos >= a.c.cap) continue;
+    const long long src = static_cast<long long>(bh) * a.c.cap + pos;
+    if (E4M3) {
+      const uint2 c = static_cast<const uint2*>(in)[src * kLanes + lane];
+      x[u].x = c.x;
+      x[u].y = c.y;
+      s[u] = scale[src];
+    } else {
+      x[u] = static_cast<const uint4*>(in)[src * kLanes + lane];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int r = r0 + u * kGroups;
+    if (r >= rows) continue;
+    if (E4M3) {
+      const float f = pow2_of(static_cast<int>(s[u]) - 127);
+      x[u] = make_uint4(values2(x[u].x & 0xffffu, f), values2(x[u].x >> 16, f),
+                        values2(x[u].y & 0xffffu, f), values2(x[u].y >> 16, f));
+    }
+    out[static_cast<long long>(r) * kLanes + lane] = x[u];
+  }
+}
+
+// One cluster of kCommitCtas CTAs a sequence; its CTAs share the (head, tensor)
+// pairs.  A pair's rows (at most 64 of at most 256 bytes) pass through
+// registers: all are read, then all are written.  The cluster barrier lies
+// between the last read of lens[b] and the write of new_lens[b], which may be
+// the same word.
+constexpr int kCommitCtas = 8;
+
+template <int ROW_BYTES, bool E4M3>
+__global__ void __launch_bounds__(kMoveThreads) __cluster_dims__(kCommitCtas, 1, 1)
+    fa_cache_commit_kernel(const CacheMoveArgs a) {
+  constexpr int kLanes = ROW_BYTES / 16;
+  constexpr int kGroups = kMoveThreads / kLanes;
+  constexpr int kSteps = FA_TREE_MAX_DRAFTS / kGroups > 0 ? FA_TREE_MAX_DRAFTS / kGroups : 1;
+  const int b = blockIdx.x / kCommitCtas, rank = blockIdx.x % kCommitCtas;
+  const int len = a.at[b];
+  const int n = min(max(a.counts[b], 0), a.N);
+  const bool valid = len >= 0 && len <= a.c.cap;
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  const int lane = threadIdx.x % kLanes;
+  const int group = threadIdx.x / kLanes;
+  if (valid && n > 0) {
+    // source and destination of this thread's rows (-1: the row stays)
+    int src[kSteps], src_s = -1;
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const int i = group + u * kGroups;
+      src[u] = -1;
+      if (i < n && i < a.c.cap - len) {
+        const int p = a.path[static_cast<long long>(b) * a.N + i];
+        if (p >= 0 && p < a.N && p < a.c.cap - len) src[u] = len + p;
+      }
+    }
+    if (E4M3 && static_cast<int>(threadIdx.x) < n && static_cast<int>(threadIdx.x) < a.c.cap - len) {
+      const int p = a.path[static_cast<long long>(b) * a.N + threadIdx.x];
+      if (p >= 0 && p < a.N && p < a.c.cap - len) src_s = len + p;
+    }
+    for (int unit = rank; unit < 2 * a.c.Hkv; unit += kCommitCtas) {
+      const long long base =
+          (static_cast<long long>(b) * a.c.Hkv + unit / 2) * a.c.cap;
+      uint4* rows = static_cast<uint4*>((unit & 1) ? a.c.v : a.c.k) + base * kLanes;
+      uint8_t* scale = (E4M3 ? ((unit & 1) ? a.c.v_scale : a.c.k_scale) + base : nullptr);
+      uint4 x[kSteps];
+      uint8_t s = 0;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+        if (src[u] >= 0) x[u] = rows[static_cast<long long>(src[u]) * kLanes + lane];
+      if (E4M3 && src_s >= 0) s = scale[src_s];
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+        if (src[u] >= 0)
+          rows[static_cast<long long>(len + group + u * kGroups) * kLanes + lane] = x[u];
+      if (E4M3 && src_s >= 0) scale[len + static_cast<int>(threadIdx.x)] = s;
+    }
+  }
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (rank == 0 && threadIdx.x == 0) a.new_lens[b] = valid ? min(len + min(n, a.c.cap), a.c.cap) : len;
+}
+
+template <int D, bool E4M3>
+dim3 move_grid(const CacheMoveArgs& a) {
+  constexpr long long per = kMoveThreads / (D / 8) * kRows;
+  const long long rows = static_cast<long long>(a.c.B) * a.c.Hkv * a.N;
+  return dim3(static_cast<unsigned>((rows + per - 1) / per), 2, 1);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheMoveArgs& a, cudaStream_t s) {
+  const bool f8 = a.c.format == FA_CACHE_E4M3;
+  if (a.c.d == 64) {
+    if (f8)
+      fa_cache_write_kernel<64, true><<<move_grid<64, true>(a), kMoveThreads, 0, s>>>(a);
+    else
+      fa_cache_write_kernel<64, false><<<move_grid<64, false>(a), kMoveThreads, 0, s>>>(a);
+  } else {
+    if (f8)
+      fa_cache_write_kernel<128, true><<<move_grid<128, true>(a), kMoveThreads, 0, s>>>(a);
+    else
+      fa_cache_write_kernel<128, false><<<move_grid<128, false>(a), kMoveThreads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const CacheMoveArgs& a, cudaStream_t s) {
+  const bool f8 = a.c.format == FA_CACHE_E4M3;
+  if (a.c.d == 64) {
+    if (f8)
+      fa_cache_read_kernel<64, true><<<move_grid<64, true>(a), kMoveThreads, 0, s>>>(a);
+    else
+      fa_cache_read_kernel<64, false><<<move_grid<64, false>(a), kMoveThreads, 0, s>>>(a);
+  } else {
+    if (f8)
+      fa_cache_read_kernel<128, true><<<move_grid<128, true>(a), kMoveThreads, 0, s>>>(a);
+    else
+      fa_cache_read_kernel<128, false><<<move_grid<128, false>(a), kMoveThreads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t s) {
+  if (static_cast<long long>(a.c.B) * kCommitCtas > 0x7fffffffll) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(a.c.B) * kCommitCtas;
+  if (a.c.format == FA_CACHE_E4M3) {
+    if (a.c.d == 64)
+      fa_cache_commit_kernel<64, true><<<grid, kMoveThreads, 0, s>>>(a);
+    else
+      fa_cache_commit_kernel<128, true><<<grid, kMoveThreads, 0, s>>>(a);
+  } else {
+    if (a.c.d == 64)
+      fa_cache_commit_kernel<128, false><<<grid, kMoveThreads, 0, s>>>(a);
+    else
+      fa_cache_commit_kernel<256, false><<<grid, kMoveThreads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -101,7 +101,45 @@ inline int decode_splits_run(long long BH, int Nk, int num_sms) {
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
+// Scale exponents of an e4m3 cache row (fa.h): at least -100, so that the
+// reciprocal scale 2^100 times any probability sum stays finite in fp32; at
+// most 119, so that 448 * 2^119 is still a finite bf16.
+constexpr int kScaleExpMin = -100;
+constexpr int kScaleExpMax = 119;
+
+// Rows of a cache tensor moved by a cache write, read or commit.
+struct CacheMoveArgs {
+  fa_cache c;
+  const void* in_k;   // write: new rows
+  const void* in_v;
+  void* out_k;        // read: destination
+  void* out_v;
+  const int* at;      // write: lens; read: first (or nullptr); commit: lens
+  const int* counts;  // write: counts (or nullptr); read: counts; commit: n_accept
+  const int* path;    // commit
+  int* new_lens;      // commit
+  int N;              // rows a sequence (commit: T)
+};
+
+struct TreeArgs {
+  fa_cache c;
+  const void* q;
+  const int* lens;
+  const unsigned long long* mask;
+  long long mask_stride;
+  void* o;
+  float* lse;
+  void* workspace;
+  int Hq, T;
+  float scale;
+  int num_sms;
+};
+
 cudaError_t launch_forward(const FwdArgs& a, cudaStream_t s);
+cudaError_t launch_cache_write(const CacheMoveArgs& a, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheMoveArgs& a, cudaStream_t s);
+cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t s);
+cudaError_t launch_decode_tree(const TreeArgs& a, cudaStream_t s);
 // Decode (split on the tensor core, then combine): tq maps q as (d, Nq, BH)
 // with 128-row boxes, tk / tv map k / v as (d, Nk, BH) with 64-row boxes.
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap* tq, const CUtensorMap* tk,
@@ -188,5 +226,8 @@ inline int check_bhnd(int B, int H, int N, int d) {
   if (BH * num_tiles(N, kTileM) > 0x7fffffffll) return FA_ERR_SHAPE;
   return FA_OK;
 }
+
+// Workspace of a tree decode (checked shapes).
+inline size_t tree_workspace_bytes(const fa_cache&, int, int) { return 256; }
 
 }  // namespace fa

@@ -260,6 +260,101 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, 
               size_t workspace_bytes, void* stream);
 
 /*
+ * Key/value cache (the KV cache the transcript of "What is Flash Attention?"
+ * names as the next stop, 11:33): B sequences of up to `cap` tokens for Hkv key
+ * heads, held in bf16 or quantised to e4m3 as they are written.
+ *  - k, v: DEVICE [B][Hkv][cap][d], two bytes (FA_CACHE_BF16) or one byte
+ *    (FA_CACHE_E4M3) an element, 16-byte aligned.
+ *  - k_scale, v_scale: DEVICE uint8 [B][Hkv][cap], 16-byte aligned, for
+ *    FA_CACHE_E4M3; ignored for FA_CACHE_BF16.  A row x[0..d) of one token and
+ *    key head is held as codes c and one scale byte s with x ~ c * 2^(s - 127):
+ *    e = s - 127 is the least exponent with max|x| * 2^-e <= 448 over the
+ *    finite elements, kept within -100 .. 119, and c = x * 2^-e rounded to
+ *    nearest even (|x| above 448 * 2^119 saturates).  A power of two loses
+ *    nothing against a finer scale (the codes are floating point) and makes the
+ *    products with it exact: a row read back is bf16 without another rounding.
+ *    NaN and infinities are stored as the NaN code; a row without finite
+ *    non-zero elements has e = -100.
+ *  - 1 <= B, Hkv, cap; d in {64, 128}; B*Hkv below 2^31 and
+ *    B*Hkv*ceil(cap/64) too; cap a multiple of 16 for FA_CACHE_E4M3 (rows of
+ *    the scale tensors are 16-byte aligned).  FA_ERR_SHAPE / FA_ERR_HEADDIM
+ *    otherwise; FA_ERR_SHAPE for an unknown format.
+ * The struct is read during the call only; the caller owns it and the memory.
+ * Lengths, counts and paths are DEVICE int32 arrays, so that a captured graph
+ * can be replayed while they change; what they hold is checked on the device
+ * as each call says, and no call reads or writes outside the cache.
+ */
+typedef enum { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_format;
+
+typedef struct fa_cache {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int B, Hkv, cap, d;
+  int format;
+} fa_cache;
+
+/*
+ * Writes new tokens: row i of sequence b, for 0 <= i < N and (counts != NULL)
+ * i < counts[b], goes to position lens[b] + i of the cache.  k, v: bf16
+ * [B][Hkv][N][d].  Rows whose position lies outside 0 .. cap-1 are not
+ * written, and every other position stays as it was.  lens is not changed.
+ * B*Hkv*N below 2^30.
+ */
+int fa_cache_write(const fa_cache* cache, const void* k, const void* v, const int* lens,
+                   const int* counts, int N, void* stream);
+
+/*
+ * Reads a window back in bf16: row i of k, v (bf16 [B][Hkv][N][d]) is position
+ * first[b] + i of sequence b (first NULL: i) for i < counts[b], and zero for the
+ * other i < N and for positions outside 0 .. cap-1.  B*Hkv*N below 2^30.
+ */
+int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, const int* counts,
+                  int N, void* stream);
+
+/*
+ * Attention of T drafted tokens a sequence over the cache; T = 1 is the
+ * decode step of single tokens.  q: bf16 [B][Hq][T][d], Hq a multiple of
+ * Hkv: query head h reads key head h / (Hq / Hkv).  o: bf16 [B][Hq][T][d],
+ * lse: fp32 [B][Hq][T].  Draft t of sequence b sees the lens[b] committed
+ * tokens (positions 0 .. lens[b]-1) and, of the drafts (position lens[b] + j
+ * holds draft j, 0 <= j < T), those whose bit j is set in
+ * mask[b * mask_stride + t]; mask NULL: the drafts j <= t.  mask_stride is T, or
+ * 0 for one tree shared by the batch.  lens[b] is taken as 0 below 0 and as cap
+ * above cap; positions from cap on do not exist.  A draft that sees nothing has
+ * o = 0 and lse = -inf.  What lies in the cache behind the drafts, or in drafts
+ * that no row of the sequence sees, never reaches a result, and a NaN or
+ * infinity in a draft's value row reaches only the rows that see that draft.
+ *  - 1 <= T <= 64, Hq >= 1, B * Hq * T below 2^31.  scale > 0 and finite.
+ *  - workspace: device memory, 256-byte aligned, contents irrelevant, of
+ *    fa_decode_tree_workspace_size() bytes (0 for an invalid shape).  Calls
+ *    that may overlap on the GPU need workspaces of their own.
+ *  - Accuracy: as fa_decode (probabilities rounded to bf16 before the product
+ *    with V); with an e4m3 cache the products run on e4m3 operands, with q and
+ *    the probabilities each as the sum of two e4m3 pieces.
+ */
+#define FA_TREE_MAX_DRAFTS 64
+size_t fa_decode_tree_workspace_size(const fa_cache* cache, int Hq, int T);
+int fa_decode_tree(const fa_cache* cache, const void* q, const int* lens,
+                   const unsigned long long* mask, long long mask_stride, void* o, float* lse,
+                   int Hq, int T, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * Commits the accepted path of a tree: for 0 <= i < n_accept[b] the row of
+ * draft path[b * T + i] moves to position lens[b] + i, in both tensors, and
+ * new_lens[b] = lens[b] + n_accept[b] (at most cap).  All rows of a sequence are
+ * read before any is written, so a path may be in any order and name a draft
+ * twice.  n_accept[b] counts as 0 below 0 and as T above T; an entry outside
+ * 0 .. T-1, or a position outside the cache, leaves its row as it was; where
+ * lens[b] is outside 0 .. cap nothing moves and new_lens[b] = lens[b].  path:
+ * int32 [B][T], 1 <= T <= 64.  new_lens may be lens itself.
+ */
+int fa_cache_commit(const fa_cache* cache, const int* lens, const int* path,
+                    const int* n_accept, int* new_lens, int T, void* stream);
+
+/*
  * Host-buffer runtime: training steps (fa_forward + fa_backward) whose
  * inputs and outputs live in HOST memory.  The paper has no counterpart
  * (its kernels start from tensors in HBM); this is the call a host program
