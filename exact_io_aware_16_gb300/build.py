@@ -19,7 +19,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_decode.cu", "fa_host.cu",
            "fa_selftest.cu", "fa_cache.cu", "fa_tree.cu"]
-HEADERS = ["fa_internal.h", "sm103_ptx.cuh", "philox.cuh"]
+HEADERS = ["fa_internal.h", "fa_rows.cuh", "sm103_ptx.cuh", "philox.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

@@ -90,6 +90,27 @@ int encode_u8(CUtensorMap* map, const void* base, int BH, int rows, int cols) {
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
+// A key or value cache as a 3-D tensor (d, cap, B*Hkv) with boxes of one key
+// tile of the tree decode, swizzled over the row of the box (128 bytes; 64 for
+// 64 e4m3).
+int encode_cache(CUtensorMap* map, const void* base, const fa_cache& c) {
+  const int BH = c.B * c.Hkv, rows = fa::tree_tile(c);
+  if (c.format == FA_CACHE_BF16) return encode_bhnd(map, base, BH, c.cap, c.d, rows);
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return FA_ERR_CUDA;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.cap),
+                        static_cast<cuuint64_t>(BH)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d),
+                           static_cast<cuuint64_t>(c.cap) * static_cast<cuuint64_t>(c.d)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(c.d), static_cast<cuuint32_t>(rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   c.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 // SM count of the current device (cached per device ordinal).
 int num_sms() {
   int dev = 0;
@@ -476,7 +497,8 @@ static int check_cache(const fa_cache* c) {
   const int st = fa::check_bhnd(c->B, c->Hkv, c->cap, c->d);
   if (st != FA_OK) return st;
   const long long BH = static_cast<long long>(c->B) * c->Hkv;
-  if (BH * fa::num_tiles(c->cap, 64) > 0x7fffffffll) return FA_ERR_SHAPE;
+  if (c->cap > FA_CACHE_MAX_TOKENS || BH * fa::num_tiles(c->cap, 64) > 0x7fffffffll)
+    return FA_ERR_SHAPE;
   if (e4m3 && c->cap % 16 != 0) return FA_ERR_SHAPE;
   return FA_OK;
 }
@@ -601,7 +623,10 @@ int fa_decode_tree(const fa_cache* cache, const void* q, const int* lens,
   a.T = T;
   a.scale = scale;
   a.num_sms = num_sms();
-  return fa::launch_decode_tree(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  CUtensorMap tk, tv;
+  if (encode_cache(&tk, cache->k, *cache) != FA_OK || encode_cache(&tv, cache->v, *cache) != FA_OK)
+    return FA_ERR_CUDA;
+  return fa::launch_decode_tree(a, tk, tv, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
@@ -615,15 +640,16 @@ int fa_selftest_wait_timeout(void* stream) {
 
 int fa_get_device_error(void* stream, uint32_t* detail) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t w_fwd = 0, w_bwd = 0, w_dtc = 0, w_st = 0;
+  uint32_t w_fwd = 0, w_bwd = 0, w_dtc = 0, w_tree = 0, w_st = 0;
   if (fa::fwd_read_clear_error(&w_fwd, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::bwd_read_clear_error(&w_bwd, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::dtc_read_clear_error(&w_dtc, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (fa::tree_read_clear_error(&w_tree, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::st_read_clear_error(&w_st, s) != cudaSuccess) return FA_ERR_CUDA;
   // a launch that gave up may have left its work-item counters dirty
   if (w_fwd && fa::fwd_reset_sched(s) != cudaSuccess) return FA_ERR_CUDA;
   if (w_bwd && fa::bwd_reset_sched(s) != cudaSuccess) return FA_ERR_CUDA;
-  const uint32_t w = w_fwd ? w_fwd : (w_bwd ? w_bwd : (w_dtc ? w_dtc : w_st));
+  const uint32_t w = w_fwd ? w_fwd : (w_bwd ? w_bwd : (w_dtc ? w_dtc : (w_tree ? w_tree : w_st)));
   if (detail) *detail = w;
   return w ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }

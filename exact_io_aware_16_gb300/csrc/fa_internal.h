@@ -139,7 +139,10 @@ cudaError_t launch_forward(const FwdArgs& a, cudaStream_t s);
 cudaError_t launch_cache_write(const CacheMoveArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheMoveArgs& a, cudaStream_t s);
 cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t s);
-cudaError_t launch_decode_tree(const TreeArgs& a, cudaStream_t s);
+// Tree decode: tk / tv map the key and value cache as (d, cap, B*Hkv) with
+// boxes of one key tile.
+cudaError_t launch_decode_tree(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t s);
 // Decode (split on the tensor core, then combine): tq maps q as (d, Nq, BH)
 // with 128-row boxes, tk / tv map k / v as (d, Nk, BH) with 64-row boxes.
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap* tq, const CUtensorMap* tk,
@@ -157,6 +160,7 @@ cudaError_t fwd_reset_sched(cudaStream_t s);
 cudaError_t bwd_reset_sched(cudaStream_t s);
 cudaError_t bwd_read_clear_error(uint32_t* out, cudaStream_t s);
 cudaError_t dtc_read_clear_error(uint32_t* out, cudaStream_t s);
+cudaError_t tree_read_clear_error(uint32_t* out, cudaStream_t s);
 
 // Self-test of failure reporting: one CTA whose barrier wait runs out (its
 // code, kSelftestWaitCode, lands in the self-test error word).
@@ -227,7 +231,40 @@ inline int check_bhnd(int B, int H, int N, int d) {
   return FA_OK;
 }
 
-// Workspace of a tree decode (checked shapes).
-inline size_t tree_workspace_bytes(const fa_cache&, int, int) { return 256; }
+// Keys a tile of the tree decode: 16 KB of a 128-wide cache in either format.
+inline int tree_tile(const fa_cache& c) { return c.format == FA_CACHE_E4M3 ? 128 : 64; }
+
+// How a tree decode is split (checked shapes): R = Hq / Hkv * T query rows a
+// (sequence, key head) pair in row tiles of 128, and `shares` CTAs a row tile,
+// each an equal share of all pairs' key tiles; at most `ctas` CTAs, and no more
+// shares than key tiles could exist.  slots: partial results the workspace
+// holds (two a CTA) of prow rows each; none where no pair can be split.
+constexpr int kTreeMaxCtas = 304;  // two an SM of 152
+
+struct TreePlan {
+  int row_tiles, shares, slots, prow;
+};
+
+inline TreePlan tree_plan(const fa_cache& c, int Hq, int T, int ctas) {
+  TreePlan p;
+  const long long R = static_cast<long long>(Hq) / c.Hkv * T;
+  p.row_tiles = static_cast<int>((R + 127) / 128);
+  p.prow = static_cast<int>(R < 128 ? R : 128);
+  const int tiles = num_tiles(c.cap, tree_tile(c));
+  const long long most = static_cast<long long>(c.B) * c.Hkv * tiles;
+  long long sh = (ctas < kTreeMaxCtas ? ctas : kTreeMaxCtas) / p.row_tiles;
+  if (sh > most) sh = most;
+  p.shares = static_cast<int>(sh < 1 ? 1 : sh);
+  p.slots = (p.shares == 1 || tiles == 1) ? 0 : 2 * p.shares * p.row_tiles;
+  return p;
+}
+
+// Workspace of a tree decode: o and (m, l) of each partial row, for the largest
+// split of any GPU.
+inline size_t tree_workspace_bytes(const fa_cache& c, int Hq, int T) {
+  const TreePlan p = tree_plan(c, Hq, T, kTreeMaxCtas);
+  const size_t bytes = static_cast<size_t>(p.slots) * p.prow * (c.d + 2) * sizeof(float);
+  return bytes < 256 ? 256 : (bytes + 255) & ~static_cast<size_t>(255);
+}
 
 }  // namespace fa

@@ -275,8 +275,8 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, 
  *    products with it exact: a row read back is bf16 without another rounding.
  *    NaN and infinities are stored as the NaN code; a row without finite
  *    non-zero elements has e = -100.
- *  - 1 <= B, Hkv, cap; d in {64, 128}; B*Hkv below 2^31 and
- *    B*Hkv*ceil(cap/64) too; cap a multiple of 16 for FA_CACHE_E4M3 (rows of
+ *  - 1 <= B, Hkv; 1 <= cap <= FA_CACHE_MAX_TOKENS; d in {64, 128}; B*Hkv and
+ *    B*Hkv*ceil(cap/64) below 2^31; cap a multiple of 16 for FA_CACHE_E4M3 (rows of
  *    the scale tensors are 16-byte aligned).  FA_ERR_SHAPE / FA_ERR_HEADDIM
  *    otherwise; FA_ERR_SHAPE for an unknown format.
  * The struct is read during the call only; the caller owns it and the memory.
@@ -284,6 +284,7 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, 
  * can be replayed while they change; what they hold is checked on the device
  * as each call says, and no call reads or writes outside the cache.
  */
+#define FA_CACHE_MAX_TOKENS 2147483392 /* 2^31 - 256: positions are int32 */
 typedef enum { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_format;
 
 typedef struct fa_cache {
