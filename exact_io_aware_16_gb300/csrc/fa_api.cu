@@ -94,7 +94,7 @@ int encode_u8(CUtensorMap* map, const void* base, int BH, int rows, int cols) {
 // tile of the tree decode, swizzled over the row of the box (128 bytes; 64 for
 // 64 e4m3).
 int encode_cache(CUtensorMap* map, const void* base, const fa_cache& c) {
-  const int BH = c.B * c.Hkv, rows = fa::tree_tile(c);
+  const int BH = c.B * c.Hkv, rows = fa::kTreeTile;
   if (c.format == FA_CACHE_BF16) return encode_bhnd(map, base, BH, c.cap, c.d, rows);
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return FA_ERR_CUDA;

@@ -231,11 +231,11 @@ inline int check_bhnd(int B, int H, int N, int d) {
   return FA_OK;
 }
 
-// Keys a tile of the tree decode: 16 KB of a 128-wide cache in either format.
-inline int tree_tile(const fa_cache& c) { return c.format == FA_CACHE_E4M3 ? 128 : 64; }
+constexpr int kTreeTile = 128;  // keys a tile of the tree decode
+constexpr int kTreeRows = 64;   // query rows a row tile, at most
 
 // How a tree decode is split (checked shapes): R = Hq / Hkv * T query rows a
-// (sequence, key head) pair in row tiles of 128, and `shares` CTAs a row tile,
+// (sequence, key head) pair in row tiles of 64, and `shares` CTAs a row tile,
 // each an equal share of all pairs' key tiles; at most `ctas` CTAs, and no more
 // shares than key tiles could exist.  slots: partial results the workspace
 // holds (two a CTA) of prow rows each; none where no pair can be split.
@@ -248,9 +248,9 @@ struct TreePlan {
 inline TreePlan tree_plan(const fa_cache& c, int Hq, int T, int ctas) {
   TreePlan p;
   const long long R = static_cast<long long>(Hq) / c.Hkv * T;
-  p.row_tiles = static_cast<int>((R + 127) / 128);
-  p.prow = static_cast<int>(R < 128 ? R : 128);
-  const int tiles = num_tiles(c.cap, tree_tile(c));
+  p.row_tiles = static_cast<int>((R + kTreeRows - 1) / kTreeRows);
+  p.prow = static_cast<int>(R < kTreeRows ? R : kTreeRows);
+  const int tiles = num_tiles(c.cap, kTreeTile);
   const long long most = static_cast<long long>(c.B) * c.Hkv * tiles;
   long long sh = (ctas < kTreeMaxCtas ? ctas : kTreeMaxCtas) / p.row_tiles;
   if (sh > most) sh = most;

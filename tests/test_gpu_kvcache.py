@@ -258,6 +258,9 @@ CASES = [  # B, Hq, Hkv, T, cap, lens
     (1, 8, 2, 4, 9600, [9590]),              # split over many CTAs
     (40, 2, 1, 2, 272, [(37 * i) % 271 for i in range(40)]),  # more sequences than a warp's lanes
     (1, 700, 1, 64, 64, [20]),               # more row tiles than CTA slots
+    (4, 80, 40, 5, 1200, [1190, 700, 900, 3]),   # several tiles and pairs a CTA, 10 rows
+    (3, 192, 32, 4, 2400, [2390, 1800, 2000]),   # 24 rows
+    (3, 32, 32, 48, 2400, [2300, 1800, 2011]),   # 48 rows
 ]
 
 
@@ -272,13 +275,16 @@ def test_tree_matches_the_definition(fa, fmt, d, case):
     scale = 1.0 / math.sqrt(d)
     o, lse = fa.fa_decode_tree(cache, q.cuda(), mask_tensor(mask), lens=i32(lens))
     ok(fa)
-    rows = slice(None)
-    if Hq * T > 3000:  # the definition is slow: a sample of the heads
-        rows = slice(0, None, 97)
-        q, o, lse = q[:, rows], o[:, rows], lse[:, rows]
+    heads = range(Hq)
+    if Hq * T > 300:  # the definition is slow: a sample of the heads
+        heads = range(0, Hq, 97 if Hq > 192 else 13)
     k, v = ref.cache_values(cache)
     vs = None if fmt == "bf16" else cache.v_scale.cpu().numpy()
-    check_tree(o, lse, ref.tree(ref.to64(q), k, v, lens, mask, scale, fmt, vs))
+    for h in heads:
+        kv = slice(h // (Hq // Hkv), h // (Hq // Hkv) + 1)
+        want = ref.tree(ref.to64(q[:, h:h + 1]), k[:, kv], v[:, kv], lens, mask, scale, fmt,
+                        None if vs is None else vs[:, kv])
+        check_tree(o[:, h:h + 1], lse[:, h:h + 1], want)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
