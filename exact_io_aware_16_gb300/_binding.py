@@ -480,7 +480,6 @@ class KvCache:
     bf16; lens: torch.int32 [B], the committed tokens of each sequence, which
     the calls below use where they are given no other lengths.  The tensors may
     be written in place; the object keeps these very tensors for its life.
-    `capacity` must be a multiple of 16 for e4m3.
     """
 
     def __init__(self, B: int, Hkv: int, capacity: int, d: int, format: str = "e4m3",

@@ -90,11 +90,10 @@ int encode_u8(CUtensorMap* map, const void* base, int BH, int rows, int cols) {
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
-// A key or value cache as a 3-D tensor (d, cap, B*Hkv) with boxes of one key
-// tile of the tree decode, swizzled over the row of the box (128 bytes; 64 for
-// 64 e4m3).
-int encode_cache(CUtensorMap* map, const void* base, const fa_cache& c) {
-  const int BH = c.B * c.Hkv, rows = fa::kTreeTile;
+// A key or value cache as a 3-D tensor (d, cap, B*Hkv) with boxes of `rows`
+// tokens, swizzled over the row of the box (128 bytes; 64 for 64 e4m3).
+int encode_cache(CUtensorMap* map, const void* base, const fa_cache& c, int rows) {
+  const int BH = c.B * c.Hkv;
   if (c.format == FA_CACHE_BF16) return encode_bhnd(map, base, BH, c.cap, c.d, rows);
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return FA_ERR_CUDA;
@@ -499,7 +498,6 @@ static int check_cache(const fa_cache* c) {
   const long long BH = static_cast<long long>(c->B) * c->Hkv;
   if (c->cap > FA_CACHE_MAX_TOKENS || BH * fa::num_tiles(c->cap, 64) > 0x7fffffffll)
     return FA_ERR_SHAPE;
-  if (e4m3 && c->cap % 16 != 0) return FA_ERR_SHAPE;
   return FA_OK;
 }
 
@@ -624,7 +622,11 @@ int fa_decode_tree(const fa_cache* cache, const void* q, const int* lens,
   a.scale = scale;
   a.num_sms = num_sms();
   CUtensorMap tk, tv;
-  if (encode_cache(&tk, cache->k, *cache) != FA_OK || encode_cache(&tv, cache->v, *cache) != FA_OK)
+  // boxes of one slot of the kernel's ring: a tile's keys; half its values where
+  // they fill two slots
+  const bool two = cache->format == FA_CACHE_BF16 && cache->d == 128;
+  if (encode_cache(&tk, cache->k, *cache, fa::kTreeTile) != FA_OK ||
+      encode_cache(&tv, cache->v, *cache, two ? fa::kTreeTile / 2 : fa::kTreeTile) != FA_OK)
     return FA_ERR_CUDA;
   return fa::launch_decode_tree(a, tk, tv, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK

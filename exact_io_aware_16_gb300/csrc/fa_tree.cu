@@ -8,10 +8,11 @@
 // elements, so the step is bound by HBM up to a few dozen rows and the products
 // run on the tensor core for all of them.
 //
-// Split.  The (sequence, key head) pairs are cut into tiles of 128 keys and the
-// list of all tiles into equal shares, one CTA a share (times the row tiles of
-// 64 rows, which run side by side so that they read a key tile while it is in
-// L2).  Lengths live on the device, so each CTA finds its share from lens
+// Split.  The (sequence, key head) pairs are cut into tiles of 128 keys; a pair
+// counts as many units as it has tiles and kPairCost for its start and end, and
+// the list of all units is cut into equal shares, one CTA a share (times the row
+// tiles of 64 rows, which run side by side so that they read a key tile while it
+// is in L2).  Lengths live on the device, so each CTA finds its share from lens
 // itself.  A pair that one CTA covers is finished there; the partial results of
 // the others ((m, l) and o, at most two a CTA) go to the workspace, and
 // fa_tree_combine merges them by the running-maximum update.
@@ -31,8 +32,10 @@
 //   * warps 0-3, a key a thread: softmax over the columns, P^T to shared
 //     memory ([key][row] in 16-byte units, an operand as it lies), epilogue with
 //     a channel a thread.  A row's reference M is shared by the CTA; one
-//     barrier with an OR a tile tells whether some score passed it by more than
-//     kLazy binades, and only then maxima are exchanged and O is rescaled.
+//     barrier a tile tells in which 16 rows some score passed it by more than
+//     kLazy binades, and only there maxima are exchanged and O is rescaled.
+//     The next pair's queries are stored during a pair's last tile, so that its
+//     first scores are ready when the epilogue ends.
 //
 // e4m3 operands: kind::f8f6f4 takes the cache as it lies in memory.  Two e4m3
 // pieces of 4 significant bits hold the 8 bits of a bf16 query exactly (its row
@@ -67,13 +70,17 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 static_assert(kTile == kSoftThreads, "a key a thread");
 
+constexpr int kPairCost = 2;  // units of a pair besides its tiles
+
 // A row's accumulator is rescaled only when its maximum grows by more than
 // kLazy binades.  bf16 has the range for any P; the e4m3 pieces of P are scaled
-// so that 2^kLazy times the largest P at the last rescale is still 448.
+// so that 2^kLazy times the largest P at the last rescale is 448, which is 1.75
+// in P's units (2^8 of the pieces': see split4).
 template <bool F8>
 struct Lazy {
-  static constexpr float kLog2 = F8 ? 2.0f : 8.0f;
-  static constexpr float kPScaleLog2 = F8 ? 6.8073549220576f : 0.0f;  // log2(448 / 4)
+  static constexpr float kLog2 = F8 ? 3.0f : 8.0f;
+  static constexpr float kTop = F8 ? 0.80735492f : 8.0f;  // log2 of the largest P
+  static constexpr float kOScale = F8 ? 0.00390625f : 1.0f;
 };
 
 struct TreeBars {
@@ -82,21 +89,22 @@ struct TreeBars {
   uint64_t s_full[2], p_ready[2], pv_done[2], drain;  // by tile parity
   uint32_t tmem_base;
   int abort_flag;
-  unsigned int bad_lo, bad_hi;  // drafts whose value row holds NaN or infinities
-  int start_b, start_h, start_t, count;  // this CTA's share
-  int pair_tiles, pair_len;              // the pair at hand, as the softmax warps agree on it
-  int fresh;                             // some row has seen no key yet
+  unsigned int bad[2][2];  // by pair parity: drafts whose value row holds NaN or infinities
+  int start_b, start_h, start_u0, unit0, unit1;  // this CTA's share
+  int next_tiles[2], next_len[2];                // by pair parity
+  uint8_t over[2][4];      // by tile parity: chunks of rows that a warp saw grow
+  unsigned int fresh;      // chunks with a row that has seen no key yet
 };
 
-// What the softmax threads know of each query row.
+// What the softmax threads know of a pair's query rows.
 template <int NR>
 struct TreeRows {
   unsigned long long seen[NR];  // mask row
   float f[NR];      // scale log2(e), times 2^e of the query row for e4m3
   float m[NR];      // reference exponent, -inf before the first key
-  float m_use[NR];  // the same, 0 before the first key
+  float neg_m[NR];  // its negative: 0 before the first key, -inf for rows past R
   float alpha[NR], shift[NR];   // of the last move
-  float inv[NR];    // epilogue: 1 / l, or 1 for a partial result
+  float inv[NR];    // epilogue: what O is multiplied by
   float part[4][NR];            // a warp's maximum or sum
 };
 
@@ -104,25 +112,27 @@ template <int D, bool F8, int NR>
 struct TreeLayout {
   static constexpr uint32_t kRow = F8 ? D : 2 * D;             // bytes of a cache row
   static constexpr uint32_t kAtom = F8 && D == 64 ? 64 : 128;  // swizzle width in bytes
-  static constexpr int kParts = kRow / kAtom;                  // TMA boxes of a tile
-  static constexpr uint32_t kSlot = kTile * kRow;
+  // A tile comes in kParts slots: 64 columns of K, 64 keys of V (bf16, d = 128).
+  static constexpr int kParts = !F8 && D == 128 ? 2 : 1;
+  static constexpr uint32_t kSlot = kTile * kRow / kParts;     // 16 KB or 8 KB
+  static constexpr int kVKeys = kTile / kParts;
   static constexpr int kPieces = F8 ? 2 : 1;                   // of q and of P
-  static constexpr uint32_t kQPart = NR * kAtom;
-  static constexpr uint32_t kQPiece = NR * kRow;
+  static constexpr uint32_t kQPiece = NR * kRow;               // 64 columns at a time for bf16
   static constexpr int kUnit = F8 ? 16 : 8;                    // rows in 16 bytes of P
   static constexpr uint32_t kPPiece = kTile * NR * (F8 ? 1 : 2);
   static constexpr uint32_t kPBytes = kPieces * kPPiece;
-  // two buffers of P, but one where two would leave the ring less than two slots
-  static constexpr uint32_t kRoom = 113u * 1024 - 1024 - 1024 - sizeof(TreeRows<NR>) - kPieces * kQPiece;
-  static constexpr int kPBufs = kRoom >= 2 * kPBytes + 2 * kSlot ? 2 : 1;
+  static constexpr uint32_t kRoom =
+      113u * 1024 - 1024 - 1024 - 2 * sizeof(TreeRows<NR>) - kPieces * kQPiece;
+  // two buffers of P, but one where two would leave the ring less than four slots
+  static constexpr int kPBufs = kRoom >= 2 * kPBytes + 4 * kSlot ? 2 : 1;
   static constexpr int kFit = (kRoom - kPBufs * kPBytes) / kSlot;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
-  static_assert(kSlots >= 2, "K(t + 1) is loaded before V(t)");
+  static_assert(kSlots >= 2 * kParts, "K(t + 1) is loaded before V(t)");
   static constexpr uint32_t kRing = 0;
   static constexpr uint32_t kQ = kRing + kSlots * kSlot;
   static constexpr uint32_t kP = kQ + kPieces * kQPiece;
   static constexpr uint32_t kRows = kP + kPBufs * kPBytes;
-  static constexpr uint32_t kBar = kRows + sizeof(TreeRows<NR>);
+  static constexpr uint32_t kBar = kRows + 2 * sizeof(TreeRows<NR>);
   static constexpr uint32_t kUsed = kBar + 1024 + 1024;  // + alignment slack
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kRows % 16 == 0 && kBar % 8 == 0, "aligned");
   // two CTAs an SM, never three: the ring is sized for two
@@ -169,37 +179,40 @@ __device__ __forceinline__ int warp_sum(int x) {
   return x;
 }
 
-// Tiles of all (sequence, key head) pairs; the whole warp calls it.
-__device__ __forceinline__ int all_tiles(const TreeParams& p) {
+// Units of all (sequence, key head) pairs; the whole warp calls it.
+__device__ __forceinline__ int all_units(const TreeParams& p) {
   int n = 0;
-  for (int b = threadIdx.x & 31; b < p.B; b += 32) n += seq_tiles(p, b);
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) n += seq_tiles(p, b) + kPairCost;
   return warp_sum(n) * p.Hkv;
 }
 
-// Tiles a share: all shares but the last have this many.
-__device__ __forceinline__ int share_size(int total, int shares) {
-  return (total + shares - 1) / shares;
+// Units a share: all shares but the last have this many.
+__device__ __forceinline__ int share_size(int units, int shares) {
+  return (units + shares - 1) / shares;
 }
 
-// A CTA's walk over the pairs that its share touches.
+// A CTA's walk over the pairs whose tiles its share holds.  Pair (b, h) begins
+// at unit u0, its tiles at u0 + kPairCost.
 struct Walk {
-  int b, h, t0, left;
-  int n;       // tiles of this pair in the share
-  int nt;      // tiles of the pair
-  __device__ __forceinline__ Walk(const TreeBars* bars)
-      : b(bars->start_b), h(bars->start_h), t0(bars->start_t), left(bars->count), n(0), nt(0) {}
+  int b, h, u0, unit0, unit1;
+  int t0, n, nt;  // first tile here, tiles here, tiles of the pair
+  __device__ __forceinline__ explicit Walk(const TreeBars* bars)
+      : b(bars->start_b), h(bars->start_h), u0(bars->start_u0), unit0(bars->unit0),
+        unit1(bars->unit1), t0(0), n(0), nt(0) {}
+  // Can the pair have tiles here?  (True for the first pair of a share with any.)
+  __device__ __forceinline__ bool inside() const { return u0 + kPairCost < unit1; }
+  __device__ __forceinline__ void set(int tiles) {
+    nt = tiles;
+    t0 = max(unit0 - u0 - kPairCost, 0);
+    n = min(nt, unit1 - u0 - kPairCost) - t0;
+  }
   __device__ __forceinline__ bool valid(const TreeParams& p) {
-    if (left <= 0) return false;
+    if (!inside()) return false;
     set(seq_tiles(p, b));
     return true;
   }
-  __device__ __forceinline__ void set(int tiles) {
-    nt = tiles;
-    n = min(left, nt - t0);
-  }
   __device__ __forceinline__ void next(const TreeParams& p) {
-    left -= n;
-    t0 = 0;
+    u0 += nt + kPairCost;
     if (++h == p.Hkv) {
       h = 0;
       ++b;
@@ -229,44 +242,79 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// Barrier 1 of the softmax threads; true if `any` was true in one of them.
-__device__ __forceinline__ bool soft_bar_or(bool any) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(any)), "n"(kSoftThreads)
-      : "memory");
-  return r != 0;
-}
+// Barrier 1: the softmax threads.
 __device__ __forceinline__ void soft_bar() { named_bar_sync(1, kSoftThreads); }
 
 // ------------------------------------------------------------ conversions
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-
-// Two fp32 as two e4m3 pieces each: hi = e4m3(x), lo = e4m3(x - hi).  The
-// subtraction is exact in fp16 (both are multiples of x's fp16 unit, of at most
-// 11 bits), x in fp16 is good to 2^-12.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x0, x1);
-  const __nv_fp8x2_storage_t a =
-      __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-  const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3));
-  const __nv_fp8x2_storage_t b = __nv_cvt_halfraw2_to_fp8x2(
-      static_cast<__half2_raw>(__hsub2(h, back)), __NV_SATFINITE, __NV_E4M3);
-  hi = a;
-  lo = b;
-}
-
-// Four fp32 as a word of high pieces and a word of low pieces.
+// Four fp32 P of 0 .. 1.75 as e4m3 pieces of 2^8 P: a word of high pieces, a word
+// of low ones.  fp16 with 2^8 less than e4m3's value has e4m3's exponent field,
+// so that bits 14..7 of the fp16 P are the code of 2^8 P cut to 4 significant
+// bits (subnormal codes included); the rest R is exact in fp16 and rounded (half
+// up) to its 4 bits the same way: 2^-8 of P together.  Shifts, adds and byte
+// permutes run at four times the rate of the e4m3 conversions, which bounded
+// the softmax (64 rows: 2200 cycles a tile).
 __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t& hi,
                                        uint32_t& lo) {
-  uint32_t h0, l0, h1, l1;
-  split2(x0, x1, h0, l0);
-  split2(x2, x3, h1, l1);
-  hi = h0 | (h1 << 16);
-  lo = l0 | (l1 << 16);
+  const __half2 h0 = __floats2half2_rn(x0, x1), h1 = __floats2half2_rn(x2, x3);
+  const uint32_t w0 = *reinterpret_cast<const uint32_t*>(&h0);
+  const uint32_t w1 = *reinterpret_cast<const uint32_t*>(&h1);
+  const uint32_t c0 = w0 & 0x7f807f80u, c1 = w1 & 0x7f807f80u;
+  const __half2 r0 = __hsub2(h0, *reinterpret_cast<const __half2*>(&c0));
+  const __half2 r1 = __hsub2(h1, *reinterpret_cast<const __half2*>(&c1));
+  const uint32_t v0 = *reinterpret_cast<const uint32_t*>(&r0) * 2 + 0x00800080u;
+  const uint32_t v1 = *reinterpret_cast<const uint32_t*>(&r1) * 2 + 0x00800080u;
+  hi = __byte_perm(w0 << 1, w1 << 1, 0x7531);
+  lo = __byte_perm(v0, v1, 0x7531);
+}
+
+// Four fp32 of at most 448 as two e4m3 pieces each: hi = e4m3(x), lo = e4m3(x - hi).
+// The subtraction is exact in fp16, and x has at most 8 bits here (a query).
+__device__ __forceinline__ void split4_signed(const float (&x)[4], uint32_t& hi, uint32_t& lo) {
+  hi = lo = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_fp8x2_storage_t a =
+        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3));
+    const __nv_fp8x2_storage_t b = __nv_cvt_halfraw2_to_fp8x2(
+        static_cast<__half2_raw>(__hsub2(h, back)), __NV_SATFINITE, __NV_E4M3);
+    hi |= static_cast<uint32_t>(a) << (16 * i);
+    lo |= static_cast<uint32_t>(b) << (16 * i);
+  }
+}
+
+// ------------------------------------------------------------ pairs of fp32
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -297,7 +345,7 @@ __device__ __forceinline__ uint64_t sdesc_plain_mn(uint32_t addr, uint32_t kstep
 }
 
 // ------------------------------------------------------------ query rows
-// The row tile's query rows as the swizzled operand of S^T (rows past R are
+// The row tile's query rows as the swizzled operand of S^T (rows past `have` are
 // zeros), kSoftThreads / NR threads a row.  e4m3: two pieces of the row times
 // 2^-e, its factor takes 2^e.
 template <int D, bool F8, int NR>
@@ -319,7 +367,7 @@ __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, c
 #pragma unroll
     for (int i = 0; i < kGran; ++i) {
       const int c = part * kGran + i;  // 16-byte unit of the row
-      *reinterpret_cast<uint4*>(sq + (c >> 3) * L::kQPart + swizzled<128>(r, c & 7)) = x[i];
+      *reinterpret_cast<uint4*>(sq + (c >> 3) * (NR * 128) + swizzled<128>(r, c & 7)) = x[i];
     }
     if (part == 0) rows->f[r] = scale_log2;
   } else {
@@ -336,7 +384,7 @@ __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, c
         float f[4] = {bf_lo(w[2 * k]), bf_hi(w[2 * k]), bf_lo(w[2 * k + 1]), bf_hi(w[2 * k + 1])};
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = fmaf(f[j], 0.0f, f[j] * s);  // infinities to NaN
-        split4(f[0], f[1], f[2], f[3], hi[k], lo[k]);
+        split4_signed(f, hi[k], lo[k]);
       }
       const int c = part * kGran + i;  // 8-byte half of a unit
       uint8_t* at = sq + swizzled<L::kAtom>(r, c >> 1) + (c & 1) * 8;
@@ -345,24 +393,53 @@ __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, c
     }
     if (part == 0) rows->f[r] = scale_log2 * pow2_of(e);
   }
+  if (part == 0) {
+    rows->m[r] = -INFINITY;
+    rows->neg_m[r] = r < have ? 0.0f : -INFINITY;
+  }
+}
+
+// Mask rows of the tile's query rows.
+template <int NR>
+__device__ __forceinline__ void store_masks(TreeRows<NR>* rows, const TreeParams& p, int b, int rt) {
+  if (threadIdx.x < NR) {
+    const int t = (rt * kTreeRows + threadIdx.x) % p.T;
+    rows->seen[threadIdx.x] =
+        p.mask ? __ldg(p.mask + b * p.mask_stride + t) : (2ull << t) - 1;
+  }
+}
+
+// The drafts that some row of sequence b sees.
+__device__ __forceinline__ unsigned long long drafts_seen(const TreeParams& p, int b) {
+  if (!p.mask) return (2ull << (p.T - 1)) - 1;
+  const unsigned long long* mk = p.mask + b * p.mask_stride;
+  const int lane = threadIdx.x & 31;
+  unsigned long long any = 0;
+  if (lane < p.T) any = __ldg(mk + lane);
+  if (lane + 32 < p.T) any |= __ldg(mk + lane + 32);
+  return static_cast<unsigned long long>(
+             __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any >> 32)))
+             << 32 |
+         __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any));
 }
 
 // ------------------------------------------------------------ value rows
 // A tile that reaches past the committed tokens: value rows that no query row
 // of the sequence sees become zero (P is zero there, but 0 * NaN is not), and
 // in drafts that some row sees NaN and infinities become zero and the draft is
-// noted: the epilogue adds them to the rows that see it.  Key a thread.
-template <uint32_t ATOM, int PARTS, bool F8>
-__device__ __forceinline__ void clean_values(uint8_t* sv, int pos, int len, int end,
-                                             unsigned long long any, TreeBars* bars) {
+// noted: the epilogue adds them to the rows that see it.  Key a thread; sv is
+// its row, COLS boxes of ATOM bytes `stride` apart.
+template <uint32_t ATOM, int COLS, bool F8>
+__device__ __forceinline__ void clean_values(uint8_t* sv, uint32_t stride, int pos, int len,
+                                             int end, unsigned long long any, unsigned int* note) {
   if (pos < len) return;
   const int j = pos - len;
   const bool live = pos < end && (any >> (j & 63) & 1);
   bool bad = false;
 #pragma unroll
-  for (int part = 0; part < PARTS; ++part) {
-    uint4* row = reinterpret_cast<uint4*>(sv + part * (kTile * ATOM) + threadIdx.x * ATOM);
-#pragma unroll
+  for (int box = 0; box < COLS; ++box) {
+    uint4* row = reinterpret_cast<uint4*>(sv + box * stride);
+#pragma unroll 2
     for (int i = 0; i < static_cast<int>(ATOM) / 16; ++i) {
       if (!live) {
         row[i] = make_uint4(0, 0, 0, 0);
@@ -383,14 +460,13 @@ __device__ __forceinline__ void clean_values(uint8_t* sv, int pos, int len, int 
       }
     }
   }
-  if (bad) atomicOr(j < 32 ? &bars->bad_lo : &bars->bad_hi, 1u << (j & 31));
+  if (bad) atomicOr(note + (j >> 5 & 1), 1u << (j & 31));
 }
 
 // ------------------------------------------------------------ across lanes
-// x[16] of 32 lanes reduced over the lanes: the result of row l % 16 in lane l.
-// Each step halves the rows a lane holds: 16 shuffles for 16 rows.
-template <bool MAX>
-__device__ __forceinline__ float reduce_lanes(float (&x)[16]) {
+// The sums of x[16] over the lanes: that of row l % 16 in lane l.  Each step
+// halves the rows a lane holds.
+__device__ __forceinline__ float sum_lanes(float (&x)[16]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int n = 8; n > 0; n >>= 1) {  // rows that a lane keeps
@@ -399,26 +475,10 @@ __device__ __forceinline__ float reduce_lanes(float (&x)[16]) {
     for (int i = 0; i < n; ++i) {
       const float send = up ? x[i] : x[i + n];
       const float keep = up ? x[i + n] : x[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, n);
-      x[i] = MAX ? fmaxf(keep, got) : keep + got;
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, n);
     }
   }
-  const float got = __shfl_xor_sync(0xffffffffu, x[0], 16);
-  return MAX ? fmaxf(x[0], got) : x[0] + got;
-}
-
-// The warp's maximum or sum of every row into part[warp].
-template <int NR, bool MAX>
-__device__ __forceinline__ void reduce_rows(const float (&x)[NR], TreeRows<NR>* rows) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int c = 0; c < NR; c += 16) {
-    float y[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = x[c + i];
-    const float z = reduce_lanes<MAX>(y);
-    if (lane < 16) rows->part[warp][c + lane] = z;
-  }
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
 // PV(i) of the share's tile i is complete (and with it all earlier ones).  Tiles
@@ -436,15 +496,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
                    const __grid_constant__ TreeParams p) {
   using L = TreeLayout<D, F8, NR>;
   constexpr int kSlots = L::kSlots;
+  constexpr int kParts = L::kParts;
+  constexpr int kChunks = NR / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   TreeBars* bars = reinterpret_cast<TreeBars*>(smem + L::kBar);
-  TreeRows<NR>* rows = reinterpret_cast<TreeRows<NR>*>(smem + L::kRows);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int share = blockIdx.x / p.row_tiles;
   const int rt = blockIdx.x % p.row_tiles;
+  // the merge may be launched: it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_ready, kSoftThreads);
@@ -452,32 +515,36 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
-    mbar_init(&bars->s_full[0], 1);
-    mbar_init(&bars->s_full[1], 1);
-    mbar_init(&bars->p_ready[0], kSoftThreads);
-    mbar_init(&bars->p_ready[1], kSoftThreads);
-    mbar_init(&bars->pv_done[0], 1);
-    mbar_init(&bars->pv_done[1], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_ready[s], kSoftThreads);
+      mbar_init(&bars->pv_done[s], 1);
+      bars->bad[s][0] = bars->bad[s][1] = 0;
+    }
     mbar_init(&bars->drain, 1);
     // an earlier CTA already recorded a pipeline timeout: exit without work
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_tree_error) != 0) ? 1 : 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    // the share: tiles [x0, x0 + count) of the list of all pairs' tiles
-    const int total = all_tiles(p);
+    // the share: units [unit0, unit1) of the list of all pairs
+    const int total = all_units(p);
     const int size = share_size(total, p.shares);
-    const long long x0 = static_cast<long long>(share) * size;
-    const int count = static_cast<int>(min(max(total - x0, 0ll), static_cast<long long>(size)));
+    const int unit0 = static_cast<int>(min(static_cast<long long>(share) * size,
+                                           static_cast<long long>(total)));
+    const int unit1 = min(unit0 + size, total);
     if (lane == 0) {
-      bars->count = count;
-      bars->start_b = bars->start_h = bars->start_t = 0;
+      bars->unit0 = unit0;
+      bars->unit1 = unit1;
+      bars->start_u0 = unit1;  // no pair
+      bars->start_b = bars->start_h = 0;
     }
     __syncwarp();
-    if (count > 0) {
-      int before = 0;  // tiles of the sequences before this batch of 32
+    if (unit0 < unit1) {
+      int before = 0;  // units of the sequences before this batch of 32
       for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int n = b0 + lane < p.B ? seq_tiles(p, b0 + lane) * p.Hkv : 0;
+        const int nt = b0 + lane < p.B ? seq_tiles(p, b0 + lane) : 0;
+        const int n = nt > 0 ? (nt + kPairCost) * p.Hkv : 0;
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -485,19 +552,22 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           if (lane >= o) incl += y;
         }
         const int lo = before + incl - n;
-        if (n > 0 && x0 >= lo && x0 < lo + n) {
-          const int off = static_cast<int>(x0) - lo, nt = n / p.Hkv;
+        if (n > 0 && unit0 >= lo && unit0 < lo + n) {
+          const int h = (unit0 - lo) / (nt + kPairCost);
+          const int u0 = lo + h * (nt + kPairCost);
           bars->start_b = b0 + lane;
-          bars->start_h = off / nt;
-          bars->start_t = off % nt;
+          bars->start_h = h;
+          bars->start_u0 = u0;
+          bars->next_tiles[0] = nt;
+          bars->next_len[0] = seq_len(p, b0 + lane);
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
-        if (x0 < before) break;
+        if (unit0 < before) break;
       }
     }
   }
   __syncthreads();
-  if (bars->abort_flag || bars->count == 0) return;
+  if (bars->abort_flag || !Walk(bars).inside()) return;
   if (warp == kTreeMmaWarp) {
     tmem_alloc(&bars->tmem_base, L::kCols);
     tmem_relinquish();
@@ -513,25 +583,41 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     if (lane == 0) {
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
-      int n = 0;  // loads so far
+      int n = 0;  // slots filled so far
       bool ok = true;
-      auto load = [&](const CUtensorMap* map, int row0, int bh) {
+      auto slot = [&]() -> int {
         const int s = n % kSlots;
-        if (!(ok = ok && t_wait(&bars->empty[s], ((n / kSlots) & 1) ^ 1, bars, 0x501))) return;
+        if (!(ok = ok && t_wait(&bars->empty[s], ((n / kSlots) & 1) ^ 1, bars, 0x501))) return -1;
         mbar_arrive_expect_tx(&bars->full[s], L::kSlot);
-#pragma unroll
-        for (int c = 0; c < L::kParts; ++c)
-          tma_load_3d(smem + L::kRing + s * L::kSlot + c * (kTile * L::kAtom), map,
-                      &bars->full[s], c * 64, row0, bh);
         ++n;
+        return s;
+      };
+      auto load_k = [&](int row0, int bh) {
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
+          const int s = slot();
+          if (s >= 0)
+            tma_load_3d(smem + L::kRing + s * L::kSlot, &tk, &bars->full[s], c * 64, row0, bh);
+        }
+      };
+      auto load_v = [&](int row0, int bh) {
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
+          const int s = slot();
+          if (s < 0) return;
+#pragma unroll
+          for (int x = 0; x < kParts; ++x)  // 64 columns each
+            tma_load_3d(smem + L::kRing + s * L::kSlot + x * (L::kVKeys * 128), &tv,
+                        &bars->full[s], x * 64, row0 + c * L::kVKeys, bh);
+        }
       };
       for (Walk w(bars); ok && w.valid(p); w.next(p)) {
         const int bh = w.b * p.Hkv + w.h, row0 = w.t0 * kTile;
-        load(&tk, row0, bh);
-        if (w.n > 1) load(&tk, row0 + kTile, bh);
+        load_k(row0, bh);
+        if (w.n > 1) load_k(row0 + kTile, bh);
         for (int t = 0; ok && t < w.n; ++t) {
-          load(&tv, row0 + t * kTile, bh);
-          if (t + 2 < w.n) load(&tk, row0 + (t + 2) * kTile, bh);
+          load_v(row0 + t * kTile, bh);
+          if (t + 2 < w.n) load_k(row0 + (t + 2) * kTile, bh);
         }
       }
     }
@@ -541,34 +627,37 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     if (lane == 0) {
       const uint32_t sQ = smem_u32(smem + L::kQ);
       const uint32_t sP = smem_u32(smem + L::kP);
-      int n = 0, it = 0, seg = 0;  // loads taken, tiles and pairs done
+      int n = 0, it = 0, seg = 0;  // slots taken, tiles and pairs done
       bool ok = true;
-      auto issue_s = [&](int i) {  // S^T of tile i (counted over the share) = K Q^T
-        const int s = n % kSlots;
-        if (!(ok = ok && t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) return;
-        tc_fence_after_sync();
-        const uint32_t kbase = sRing + s * L::kSlot;
+      auto issue_s = [&](int i) {  // S^T of the share's tile i = K Q^T
         const uint32_t d = tmem + (i & 1) * NR;
-        if constexpr (F8) {
-          constexpr uint32_t idesc = idesc_e4m3_f32(128, NR);
 #pragma unroll
-          for (int x = 0; x < 2 * (D / 32); ++x) {
-            const int piece = x / (D / 32), kk = x % (D / 32);
-            umma_ss_f8(d, sdesc<L::kAtom>(kbase + kk * 32, 16, 8 * L::kAtom),
-                       sdesc<L::kAtom>(sQ + piece * L::kQPiece + kk * 32, 16, 8 * L::kAtom), idesc,
-                       x > 0 ? 1u : 0u);
+        for (int c = 0; c < kParts; ++c) {
+          const int s = n % kSlots;
+          if (!(ok = ok && t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) return;
+          tc_fence_after_sync();
+          const uint32_t kbase = sRing + s * L::kSlot;
+          if constexpr (F8) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(128, NR);
+#pragma unroll
+            for (int x = 0; x < 2 * (D / 32); ++x) {
+              const int piece = x / (D / 32), kk = x % (D / 32);
+              umma_ss_f8(d, sdesc<L::kAtom>(kbase + kk * 32, 16, 8 * L::kAtom),
+                         sdesc<L::kAtom>(sQ + piece * L::kQPiece + kk * 32, 16, 8 * L::kAtom),
+                         idesc, x > 0 ? 1u : 0u);
+            }
+          } else {
+            constexpr uint32_t idesc = idesc_bf16_f32(128, NR, false, false);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 64 columns
+              umma_ss(d, sdesc_sw128(kbase + kk * 32, 16, 1024),
+                      sdesc_sw128(sQ + c * (NR * 128) + kk * 32, 16, 1024), idesc,
+                      (c > 0 || kk > 0) ? 1u : 0u);
           }
-        } else {
-          constexpr uint32_t idesc = idesc_bf16_f32(128, NR, false, false);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(d, sdesc_sw128(kbase + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024),
-                    sdesc_sw128(sQ + (kk >> 2) * L::kQPart + (kk & 3) * 32, 16, 1024), idesc,
-                    kk > 0 ? 1u : 0u);
+          umma_commit(&bars->empty[s]);
+          ++n;
         }
-        umma_commit(&bars->empty[s]);
         umma_commit(&bars->s_full[i & 1]);
-        ++n;
       };
       for (Walk w(bars); ok && w.valid(p); w.next(p), ++seg) {
         if (!(ok = t_wait(&bars->q_ready, seg & 1, bars, 0x512))) break;
@@ -576,34 +665,36 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (w.n > 1) issue_s(it + 1);
         for (int t = 0; ok && t < w.n; ++t, ++it) {
           // O^T += V^T P^T
-          const int s = n % kSlots;
-          if (!(ok = t_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513) &&
-                     t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514)))
-            break;
-          tc_fence_after_sync();
-          const uint32_t vbase = sRing + s * L::kSlot;
+          if (!(ok = t_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513))) break;
           const uint32_t pbase = sP + (it % L::kPBufs) * L::kPBytes;
           const uint32_t d = tmem + L::kOCol;
-          if constexpr (F8) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(D, NR) | (3u << 15);  // both MN-major
 #pragma unroll
-            for (int x = 0; x < 2 * (kTile / 32); ++x) {
-              const int piece = x / (kTile / 32), kk = x % (kTile / 32);
-              umma_ss_f8(d, sdesc<L::kAtom>(vbase + kk * 32 * L::kAtom, 16, 8 * L::kAtom),
-                         sdesc_plain_mn(pbase + piece * L::kPPiece + kk * 512, 128, kTile * 16),
-                         idesc, (t > 0 || x > 0) ? 1u : 0u);
+          for (int c = 0; c < kParts; ++c) {
+            const int s = n % kSlots;
+            if (!(ok = ok && t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514))) break;
+            tc_fence_after_sync();
+            const uint32_t vbase = sRing + s * L::kSlot;
+            if constexpr (F8) {
+              constexpr uint32_t idesc = idesc_e4m3_f32(D, NR) | (3u << 15);  // both MN-major
+#pragma unroll
+              for (int x = 0; x < 2 * (kTile / 32); ++x) {
+                const int piece = x / (kTile / 32), kk = x % (kTile / 32);
+                umma_ss_f8(d, sdesc<L::kAtom>(vbase + kk * 32 * L::kAtom, 16, 8 * L::kAtom),
+                           sdesc_plain_mn(pbase + piece * L::kPPiece + kk * 512, 128, kTile * 16),
+                           idesc, (t > 0 || x > 0) ? 1u : 0u);
+              }
+            } else {
+              constexpr uint32_t idesc = idesc_bf16_f32(D, NR, true, true);
+#pragma unroll
+              for (int kk = 0; kk < L::kVKeys / 16; ++kk)
+                umma_ss(d, sdesc_sw128(vbase + kk * 2048, L::kVKeys * 128, 1024),
+                        sdesc_plain_mn(pbase + (c * (L::kVKeys / 16) + kk) * 256, 128, kTile * 16),
+                        idesc, (t > 0 || c > 0 || kk > 0) ? 1u : 0u);
             }
-          } else {
-            constexpr uint32_t idesc = idesc_bf16_f32(D, NR, true, true);
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_ss(d, sdesc_sw128(vbase + kk * 2048, kTile * 128, 1024),
-                      sdesc_plain_mn(pbase + kk * 256, 128, kTile * 16), idesc,
-                      (t > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bars->empty[s]);
+            ++n;
           }
-          umma_commit(&bars->empty[s]);
           umma_commit(&bars->pv_done[it & 1]);
-          ++n;
           if (t + 2 < w.n) issue_s(it + 2);  // into the buffer that softmax(it) has read
         }
       }
@@ -616,56 +707,50 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     // none of the barriers, which the four warps pass together.
     const int tid = threadIdx.x;
     const uint32_t tlane = tmem_addr(tmem, warp * 32, 0);
+    TreeRows<NR>* const both = reinterpret_cast<TreeRows<NR>*>(smem + L::kRows);
     int it = 0, seg = 0, n = 0;
     bool ok = true;
-    for (Walk w(bars); w.left > 0; w.next(p), ++seg) {
-      if (tid == 0) {
-        bars->pair_tiles = seq_tiles(p, w.b);
-        bars->pair_len = seq_len(p, w.b);
-        bars->bad_lo = bars->bad_hi = 0;
-        bars->fresh = 1;
+    const int have = min(p.R - rt * kTreeRows, NR);  // query rows of this tile
+    Walk w(bars);
+    w.set(bars->next_tiles[0]);
+    int len = bars->next_len[0];
+    unsigned long long any = drafts_seen(p, w.b);
+    // this thread's scale bytes of the next tile, loaded a tile ahead
+    uint32_t kb = 127, vb = 127;
+    auto load_scales = [&](int b, int h, int pos, int end) {
+      kb = vb = 127;
+      if (F8 && pos < end) {
+        const long long at = (static_cast<long long>(b) * p.Hkv + h) * p.cap + pos;
+        kb = __ldg(p.k_scale + at);
+        vb = __ldg(p.v_scale + at);
       }
-      soft_bar();
-      w.set(bars->pair_tiles);
-      const int len = bars->pair_len;
+    };
+    load_scales(w.b, w.h, w.t0 * kTile + tid, min(len + p.T, p.cap));
+    store_queries<D, F8, NR>(
+        smem + L::kQ, both,
+        p.q + ((static_cast<long long>(w.b) * p.Hkv + w.h) * p.R + rt * kTreeRows) * (D / 8), have,
+        p.scale_log2);
+    store_masks<NR>(both, p, w.b, rt);
+    fence_proxy_async_smem();
+    mbar_arrive(&bars->q_ready);
+    if (tid == 0) bars->fresh = (1u << ((have + 15) / 16)) - 1;
+    soft_bar();
+
+    for (bool more = true; more; ++seg) {
+      TreeRows<NR>* const rows = both + (seg & 1);
       const int end = min(len + p.T, p.cap);
       const long long bh = static_cast<long long>(w.b) * p.Hkv + w.h;
       const long long row0 = bh * p.R + rt * kTreeRows;  // of o and lse
-      const int have = min(p.R - rt * kTreeRows, NR);    // query rows of this tile
-      const uint8_t* ksc = F8 ? p.k_scale + bh * p.cap : nullptr;
-      const uint8_t* vsc = F8 ? p.v_scale + bh * p.cap : nullptr;
-      // this thread's key of the first tile: its scales are loaded a tile ahead
-      int pos = w.t0 * kTile + tid;
-      uint32_t kb = 127, vb = 127;
-      if (F8 && pos < end) {
-        kb = __ldg(ksc + pos);
-        vb = __ldg(vsc + pos);
-      }
-      store_queries<D, F8, NR>(smem + L::kQ, rows, p.q + row0 * (D / 8), have, p.scale_log2);
-      fence_proxy_async_smem();
-      mbar_arrive(&bars->q_ready);
-      // mask rows, and the drafts that some row of the sequence sees
-      unsigned long long any = (2ull << (p.T - 1)) - 1;
-      if (p.mask) {
-        const unsigned long long* mk = p.mask + w.b * p.mask_stride;
-        any = 0;
-        if (lane < p.T) any = __ldg(mk + lane);
-        if (lane + 32 < p.T) any |= __ldg(mk + lane + 32);
-        any = static_cast<unsigned long long>(
-                  __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any >> 32)))
-                  << 32 |
-              __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any));
-      }
-      if (tid < NR) {
-        const int t = (rt * kTreeRows + tid) % p.T;
-        rows->seen[tid] = p.mask ? __ldg(p.mask + w.b * p.mask_stride + t) : (2ull << t) - 1;
-        rows->m[tid] = -INFINITY;
-        rows->m_use[tid] = 0.0f;
-      }
-      soft_bar();
-      float l[NR];
+      // the pair after this one; thread 0's view of its length is everybody's
+      Walk w2 = w;
+      w2.next(p);
+      more = w2.inside();
+      int len2 = 0;
+      if (tid == 0 && more) len2 = w2.b == w.b ? len : seq_len(p, w2.b);
+      f32x2 l[NR / 2];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+      for (int r = 0; r < NR / 2; ++r) l[r] = 0;
+      int pos = w.t0 * kTile + tid;
 
       for (int t = 0; t < w.n; ++t, ++it, pos += kTile) {
         const bool edge = pos - tid + kTile > len;
@@ -676,122 +761,156 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           ks = __uint_as_float(kb << 23);
           ev = static_cast<float>(e);
           wv = pow2_of(-e);
-          kb = vb = 127;
-          if (t + 1 < w.n && pos + kTile < end) {
-            kb = __ldg(ksc + pos + kTile);
-            vb = __ldg(vsc + pos + kTile);
-          }
         }
+        if (t + 1 < w.n) load_scales(w.b, w.h, pos + kTile, end);
         ok = ok && __all_sync(0xffffffffu, t_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, 0x522));
         if (edge) {
           // V(t) in the order of loads.  With S(it) and PV(it - 1) complete, so are
           // all loads that its slot had before: the parity is V(t)'s.
-          const int v = n + 2 + t + min(t, w.n - 2);
+          const int v = n + kParts * (2 + t + min(t, w.n - 2)) + tid / L::kVKeys;
           if (t > 0) ok = product_done(it - 1, ok, bars, 0x523);
           ok = ok && __all_sync(0xffffffffu, t_wait(&bars->full[v % kSlots], (v / kSlots) & 1,
                                                     bars, 0x521));
           if (ok)
-            clean_values<L::kAtom, L::kParts, F8>(smem + L::kRing + (v % kSlots) * L::kSlot, pos,
-                                                  len, end, any, bars);
+            clean_values<L::kAtom, kParts, F8>(
+                smem + L::kRing + (v % kSlots) * L::kSlot + (tid % L::kVKeys) * L::kAtom,
+                L::kVKeys * 128, pos, len, end, any, bars->bad[seg & 1]);
         }
         // ---- x = t - M of this key for every row
-        float x[NR];
+        f32x2 x[NR / 2];
         tc_fence_after_sync();
+        {
+          uint32_t s[NR];
 #pragma unroll
-        for (int c = 0; c < NR; c += 16)
-          tmem_ld16(tlane + (it & 1) * NR + c, reinterpret_cast<uint32_t*>(x) + c);
-        tmem_ld_wait();
+          for (int c = 0; c < NR; c += 16) tmem_ld16(tlane + (it & 1) * NR + c, s + c);
+          tmem_ld_wait();
+          reg_pin(s);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) asm volatile("" : "+f"(x[r]));
-        float mx = -INFINITY;
+          for (int r = 0; r < NR / 2; ++r)
+            x[r] = pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1]));
+        }
+        const f32x2 ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
 #pragma unroll
-        for (int r = 0; r < NR; r += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&rows->f[r]);
-          const float4 m = *reinterpret_cast<const float4*>(&rows->m_use[r]);
+        for (int r = 0; r < NR / 2; r += 2) {
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&rows->f[2 * r]);
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&rows->neg_m[2 * r]);
           if constexpr (F8) {
-            x[r] = fmaf(x[r] * f.x, ks, ev) - m.x;
-            x[r + 1] = fmaf(x[r + 1] * f.y, ks, ev) - m.y;
-            x[r + 2] = fmaf(x[r + 2] * f.z, ks, ev) - m.z;
-            x[r + 3] = fmaf(x[r + 3] * f.w, ks, ev) - m.w;
+            x[r] = add2(fma2(mul2(x[r], f.x), ks2, ev2), m.x);
+            x[r + 1] = add2(fma2(mul2(x[r + 1], f.y), ks2, ev2), m.y);
           } else {
-            x[r] = fmaf(x[r], f.x, -m.x);
-            x[r + 1] = fmaf(x[r + 1], f.y, -m.y);
-            x[r + 2] = fmaf(x[r + 2], f.z, -m.z);
-            x[r + 3] = fmaf(x[r + 3], f.w, -m.w);
+            x[r] = fma2(x[r], f.x, m.x);
+            x[r + 1] = fma2(x[r + 1], f.y, m.y);
           }
         }
         if (edge && pos >= len) {
           const int j = (pos - len) & 63;
 #pragma unroll
           for (int r = 0; r < NR; ++r)
-            if (pos >= end || !(rows->seen[r] >> j & 1)) x[r] = -INFINITY;
+            if (pos >= end || !(rows->seen[r] >> j & 1)) {
+              float2 y = unpack2(x[r / 2]);
+              (r & 1 ? y.y : y.x) = -INFINITY;
+              x[r / 2] = pack2(y.x, y.y);
+            }
         }
+        const unsigned int fresh = bars->fresh;
+        unsigned int grown = 0;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) mx = fmaxf(mx, x[r]);
-        const bool fresh = bars->fresh != 0;
-        if (soft_bar_or(fresh || mx > Lazy<F8>::kLog2 + Lazy<F8>::kPScaleLog2)) {
-          // ---- new references: row maxima over the CTA's keys
-          reduce_rows<NR, true>(x, rows);
+        for (int c = 0; c < kChunks; ++c) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int r = 8 * c; r < 8 * c + 8; ++r) {
+            const float2 y = unpack2(x[r]);
+            mx = fmax3f(mx, y.x, y.y);
+          }
+          if (__any_sync(0xffffffffu, mx > Lazy<F8>::kTop || (fresh >> c & 1))) grown |= 1u << c;
+        }
+        if (lane == 0) bars->over[it & 1][warp] = static_cast<uint8_t>(grown);
+        if (tid == 0 && t == 0 && more) {
+          bars->next_len[(seg + 1) & 1] = len2;
+          bars->next_tiles[(seg + 1) & 1] = (min(len2 + p.T, p.cap) + kTile - 1) / kTile;
+        }
+        soft_bar();
+        grown = *reinterpret_cast<const uint32_t*>(bars->over[it & 1]);
+        grown = (grown | grown >> 8 | grown >> 16 | grown >> 24) & 0xffu;
+        if (grown) {
+          // ---- new references where a row grew: maxima over the CTA's keys
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (!(grown >> c & 1)) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float2 y = unpack2(x[8 * c + r / 2]);
+              const float z = redux_max(r & 1 ? y.y : y.x);
+              if (lane == r) top = z;
+            }
+            if (lane < 16) rows->part[warp][16 * c + lane] = top;
+          }
           soft_bar();
-          if (tid < NR) {
+          if (tid < have && (grown >> (tid / 16) & 1)) {
             const float top = fmaxf(fmaxf(rows->part[0][tid], rows->part[1][tid]),
                                     fmaxf(rows->part[2][tid], rows->part[3][tid]));
-            const float m_old = rows->m[tid], u_old = rows->m_use[tid];
-            const float m_new = fmaxf(m_old, u_old + top - Lazy<F8>::kPScaleLog2);
+            const float m_old = rows->m[tid], u_old = -rows->neg_m[tid];
+            const float m_new = fmaxf(m_old, u_old + top + (Lazy<F8>::kLog2 - Lazy<F8>::kTop));
             const float u_new = m_new == -INFINITY ? 0.0f : m_new;
             rows->m[tid] = m_new;
-            rows->m_use[tid] = u_new;
+            rows->neg_m[tid] = -u_new;
             rows->alpha[tid] = m_new == -INFINITY ? 1.0f : ex2_approx(m_old - m_new);
             rows->shift[tid] = u_old - u_new;
+          } else if (tid >= have && tid < NR) {
+            rows->alpha[tid] = 1.0f;
+            rows->shift[tid] = 0.0f;
           }
           if (tid == 0) bars->fresh = 0;
           soft_bar();
-          if (tid < have && rows->m[tid] == -INFINITY) bars->fresh = 1;
+          if (tid < have && rows->m[tid] == -INFINITY) atomicOr(&bars->fresh, 1u << (tid / 16));
           // PV(it - 1) must be done before O is rescaled
           if (t > 0) ok = product_done(it - 1, ok, bars, 0x524);
           tc_fence_after_sync();
 #pragma unroll
-          for (int c = 0; c < NR; c += 16) {
+          for (int c = 0; c < kChunks; ++c) {
+            if (!(grown >> c & 1)) continue;
             uint32_t o[16];
             if (t > 0) {
-              tmem_ld16(tlane + L::kOCol + c, o);
+              tmem_ld16(tlane + L::kOCol + 16 * c, o);
               tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
+              reg_pin(o);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float al = rows->alpha[c + i];
-              x[c + i] += rows->shift[c + i];
-              l[c + i] *= al;
-              if (t > 0) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            for (int i = 0; i < 8; ++i) {
+              const float2 al = *reinterpret_cast<const float2*>(&rows->alpha[16 * c + 2 * i]);
+              const f32x2 sh = *reinterpret_cast<const f32x2*>(&rows->shift[16 * c + 2 * i]);
+              x[8 * c + i] = add2(x[8 * c + i], sh);
+              l[8 * c + i] = mul2(l[8 * c + i], pack2(al.x, al.y));
+              o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * al.x);
+              o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * al.y);
             }
-            if (t > 0) tmem_st16(tlane + L::kOCol + c, o);
+            if (t > 0) tmem_st16(tlane + L::kOCol + 16 * c, o);
           }
           tmem_st_wait();
         }
         // ---- P = 2^x over the P buffer that PV(it - kPBufs) has read
         if (it >= L::kPBufs) ok = product_done(it - L::kPBufs, ok, bars, 0x525);
         uint8_t* pb = smem + L::kP + (it % L::kPBufs) * L::kPBytes + tid * 16;
+        const f32x2 wv2 = pack2(wv, wv);
 #pragma unroll
         for (int u = 0; u < NR / L::kUnit; ++u) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if constexpr (F8) {
-              const int r = u * 16 + i * 4;
-              float pr[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                pr[k] = ex2_approx(x[r + k]);
-                l[r + k] = fmaf(pr[k], wv, l[r + k]);
-              }
-              split4(pr[0], pr[1], pr[2], pr[3], hi[i], lo[i]);
-            } else {
               const int r = u * 8 + i * 2;
-              const float p0 = ex2_approx(x[r]), p1 = ex2_approx(x[r + 1]);
-              l[r] += p0;
-              l[r + 1] += p1;
+              const float2 a = unpack2(x[r]), b = unpack2(x[r + 1]);
+              const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
+              const float p2 = ex2_approx(b.x), p3 = ex2_approx(b.y);
+              l[r] = fma2(pack2(p0, p1), wv2, l[r]);
+              l[r + 1] = fma2(pack2(p2, p3), wv2, l[r + 1]);
+              split4(p0, p1, p2, p3, hi[i], lo[i]);
+            } else {
+              const int r = u * 4 + i;
+              const float2 a = unpack2(x[r]);
+              const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
+              l[r] = add2(l[r], pack2(p0, p1));
               hi[i] = pack_bf16x2(p0, p1);
             }
           }
@@ -804,67 +923,105 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         tc_fence_before_sync();
         mbar_arrive(&bars->p_ready[it & 1]);
       }
-      n += 2 * w.n;
+      n += 2 * kParts * w.n;
+      // ---- the next pair's queries: S of this pair's last tile is complete, so
+      // that Q is free, and its scores are formed during this pair's epilogue
+      if (more) {
+        len2 = bars->next_len[(seg + 1) & 1];
+        w2.set(bars->next_tiles[(seg + 1) & 1]);
+        load_scales(w2.b, w2.h, tid, min(len2 + p.T, p.cap));
+        store_queries<D, F8, NR>(
+            smem + L::kQ, both + ((seg + 1) & 1),
+            p.q + ((static_cast<long long>(w2.b) * p.Hkv + w2.h) * p.R + rt * kTreeRows) * (D / 8),
+            have, p.scale_log2);
+        if (w2.b == w.b) {
+          if (tid < NR) both[(seg + 1) & 1].seen[tid] = rows->seen[tid];
+        } else {
+          store_masks<NR>(both + ((seg + 1) & 1), p, w2.b, rt);
+          any = drafts_seen(p, w2.b);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_ready);
+        if (tid == 0) bars->fresh = (1u << ((have + 15) / 16)) - 1;
+      }
       // ---- epilogue: sums over the keys, then a channel a thread
-      reduce_rows<NR, false>(l, rows);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 z = unpack2(l[8 * c + i]);
+          y[2 * i] = z.x;
+          y[2 * i + 1] = z.y;
+        }
+        const float z = sum_lanes(y);
+        if (lane < 16) rows->part[warp][16 * c + lane] = z;
+      }
       ok = product_done(it - 1, ok, bars, 0x526);
       tc_fence_after_sync();
       soft_bar();
+      const bool whole = w.n == w.nt;
+      // a pair that began in an earlier share goes to slot 0, one that goes on in
+      // the next to slot 1
+      const long long prow0 = (2ll * blockIdx.x + (w.t0 > 0 ? 0 : 1)) * p.prow;
       const unsigned long long bad =
-          static_cast<unsigned long long>(bars->bad_hi) << 32 | bars->bad_lo;
-      const bool whole = w.t0 == 0 && w.n == w.nt;
-      // a share's first pair goes to slot 0, its last to slot 1
-      const long long prow0 = (2ll * blockIdx.x + (seg == 0 ? 0 : 1)) * p.prow;
+          static_cast<unsigned long long>(bars->bad[seg & 1][1]) << 32 | bars->bad[seg & 1][0];
       if (tid < NR) {
         const float sum = (rows->part[0][tid] + rows->part[1][tid]) +
                           (rows->part[2][tid] + rows->part[3][tid]);
-        rows->inv[tid] = !whole ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+        rows->inv[tid] =
+            Lazy<F8>::kOScale * (!whole ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum));
         if (tid < have && ok) {
           if (whole)
             p.lse[row0 + tid] =
-                sum == 0.0f ? -INFINITY : (rows->m_use[tid] + log2f(sum)) * kLn2;
+                sum == 0.0f ? -INFINITY : (log2f(sum) - rows->neg_m[tid]) * kLn2;
           else
             p.part_ml[prow0 + tid] = make_float2(rows->m[tid], sum);
         }
       }
       soft_bar();
+      if (tid == 0) bars->bad[seg & 1][0] = bars->bad[seg & 1][1] = 0;
       // channel of this thread: with d = 64 the accumulator's rows are spread over
       // the first 16 lanes of each warp
       const int ch = D == 128 ? tid : warp * 16 + lane;
       const bool mine = ok && (D == 128 || lane < 16);
 #pragma unroll 1
-      for (int c = 0; c < NR; c += 16) {
-        if (c >= have) break;
-        float o[16];
-        tmem_ld16(tlane + L::kOCol + c, reinterpret_cast<uint32_t*>(o));
+      for (int c = 0; c < have; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(tlane + L::kOCol + c, o);
         tmem_ld_wait();
+        reg_pin(o);
+        if (bad && mine) {
+          // drafts with NaN or infinities, to the rows that see them
+#pragma unroll 1
+          for (int j = 0; j < 64; ++j) {
+            if (!(bad >> j & 1)) continue;
+            const long long at = (bh * p.cap + len + j) * D + ch;
+            float v;
+            if constexpr (F8)
+              v = (p.v[at] & 0x7f) == 0x7f ? NAN : 0.0f;
+            else
+              v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[at]);
+            if (isfinite(v)) continue;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (rows->seen[c + i] >> j & 1)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          asm volatile("" : "+f"(o[i]));
           const int r = c + i;
-          float y = o[i] * rows->inv[r];
+          const float y = __uint_as_float(o[i]) * rows->inv[r];
           if (!mine || r >= have) continue;
-          if (bad) {
-            // drafts with NaN or infinities that this row sees
-            unsigned long long hit = bad & rows->seen[r];
-            while (hit) {
-              const int j = __ffsll(static_cast<long long>(hit)) - 1;
-              hit &= hit - 1;
-              const long long at = (bh * p.cap + len + j) * D + ch;
-              if constexpr (F8) {
-                if ((p.v[at] & 0x7f) == 0x7f) y = NAN;
-              } else {
-                const float v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[at]);
-                if (!isfinite(v)) y += v;
-              }
-            }
-          }
           if (whole)
             p.o[(row0 + r) * D + ch] = __float2bfloat16_rn(y);
           else
             p.part_o[(prow0 + r) * D + ch] = y;
         }
       }
+      w = w2;
+      len = len2;
     }
   }
 
@@ -885,66 +1042,92 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 }
 
 // ------------------------------------------------------------ merge
-// One block a query row: where several shares cover the row's pair, the row's
-// partials are merged, four warps over the shares.
-template <int D>
-__global__ void __launch_bounds__(128) fa_tree_combine(const __grid_constant__ TreeParams p) {
+// Where several shares cover a pair, its rows' partials are merged.  A block has
+// ROWS query rows of a pair and 8 / ROWS warps for each, over the shares.
+constexpr int kMergeThreads = 256;
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kMergeThreads)
+    fa_tree_combine(const __grid_constant__ TreeParams p, int blocks) {
   constexpr int kC = D / 32;
+  constexpr int kWarps = 8 / ROWS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long row = blockIdx.x;  // of o: ((b * Hkv + h) * R + r)
-  const int r = static_cast<int>(row % p.R);
-  const long long bh = row / p.R;
+  const long long bh = blockIdx.x / blocks;
   const int b = static_cast<int>(bh / p.Hkv), h = static_cast<int>(bh % p.Hkv);
   int total = 0, before = 0;
   for (int i = lane; i < p.B; i += 32) {
-    const int n = seq_tiles(p, i);
+    const int n = seq_tiles(p, i) + kPairCost;
     total += n;
     if (i < b) before += n;
   }
-  total = warp_sum(total) * p.Hkv;
   const int nt = seq_tiles(p, b);
-  const int s0 = warp_sum(before) * p.Hkv + h * nt;
+  total = warp_sum(total) * p.Hkv;
+  const int u0 = warp_sum(before) * p.Hkv + (h + 1) * kPairCost + h * nt;  // of its first tile
   const int size = share_size(total, p.shares);
-  const int first = s0 / size, last = (s0 + nt - 1) / size;
+  const int first = u0 / size, last = (u0 + nt - 1) / size;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (first == last) return;
+  const int r = static_cast<int>(blockIdx.x % blocks) * ROWS + warp / kWarps;
   const int rt = r / kTreeRows, rs = r % kTreeRows;
-  __shared__ float sl[4], so[4][D];
-  float m = -INFINITY;
-  for (int c = first + lane; c <= last; c += 32) {
-    // the pair is the share's first unless it starts inside the share
-    const long long slot = 2ll * (static_cast<long long>(c) * p.row_tiles + rt) +
-                           (c == first && s0 != c * size ? 1 : 0);
-    m = fmaxf(m, p.part_ml[slot * p.prow + rs].x);
-  }
+  // rows of the partials of share c: slot 1 where the pair begins, else slot 0
+  auto slot_row = [&](int c) -> long long {
+    return (2ll * (static_cast<long long>(c) * p.row_tiles + rt) + (c == first ? 1 : 0)) * p.prow + rs;
+  };
+  __shared__ float sl[8], so[8][D];
+  float m = -INFINITY, l = 0.0f, acc[kC];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float m_ref = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, acc[kC];
+  for (int k = 0; k < kC; ++k) acc[k] = 0.0f;
+  float m_ref = 0.0f;
+  if (r < p.R) {
+    for (int c = first + lane; c <= last; c += 32) m = fmaxf(m, p.part_ml[slot_row(c)].x);
 #pragma unroll
-  for (int c = 0; c < kC; ++c) acc[c] = 0.0f;
-  for (int c = first + warp; c <= last; c += 4) {
-    const long long slot = 2ll * (static_cast<long long>(c) * p.row_tiles + rt) +
-                           (c == first && s0 != c * size ? 1 : 0);
-    const float2 ml = p.part_ml[slot * p.prow + rs];
-    if (ml.y == 0.0f) continue;  // this share's keys are all unseen
-    const float wgt = ex2_approx(ml.x - m_ref);
-    l = fmaf(wgt, ml.y, l);
-    const float* src = p.part_o + (slot * p.prow + rs) * D + lane * kC;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m_ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
+    for (int c = first + warp % kWarps; c <= last; c += kWarps) {
+      const long long at = slot_row(c);
+      const float2 ml = p.part_ml[at];
+      const float wgt = ml.y == 0.0f ? 0.0f : ex2_approx(ml.x - m_ref);  // 0: no key seen there
+      l = fmaf(wgt, ml.y, l);
+      const float* src = p.part_o + at * D + lane * kC;
 #pragma unroll
-    for (int k = 0; k < kC; ++k) acc[k] = fmaf(wgt, src[k], acc[k]);
+      for (int k = 0; k < kC; ++k) acc[k] = fmaf(wgt, src[k], acc[k]);
+    }
   }
 #pragma unroll
   for (int k = 0; k < kC; ++k) so[warp][lane * kC + k] = acc[k];
   if (lane == 0) sl[warp] = l;
   __syncthreads();
-  const float l_all = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-  const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
-  if (threadIdx.x < D)
-    p.o[row * D + threadIdx.x] =
-        __float2bfloat16_rn(((so[0][threadIdx.x] + so[1][threadIdx.x]) +
-                             (so[2][threadIdx.x] + so[3][threadIdx.x])) * inv);
-  if (threadIdx.x == 0)
-    p.lse[row] = l_all == 0.0f ? -INFINITY : (m_ref + log2f(l_all)) * kLn2;
+  if (warp % kWarps == 0 && r < p.R) {
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) l += sl[warp + i];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const long long row = bh * p.R + r;
+#pragma unroll
+    for (int k = 0; k < kC; ++k) {
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) acc[k] += so[warp + i][lane * kC + k];
+      p.o[row * D + lane * kC + k] = __float2bfloat16_rn(acc[k] * inv);
+    }
+    if (lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+  }
+}
+
+template <int D, int ROWS>
+cudaError_t launch_combine(const TreeParams& p, cudaStream_t s) {
+  // launched while the shares still run: it finds its pair meanwhile and then waits
+  // for them (griddepcontrol.wait)
+  const int blocks = (p.R + ROWS - 1) / ROWS;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * blocks));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_tree_combine<D, ROWS>, p, blocks);
 }
 
 template <int D, bool F8, int NR>
@@ -988,9 +1171,9 @@ cudaError_t launch_type(const TreeArgs& a, const CUtensorMap& tk, const CUtensor
                         : p.R <= 32 ? launch_tile<D, F8, 32>(p, tk, tv, s)
                                     : launch_tile<D, F8, 64>(p, tk, tv, s);
   if (e != cudaSuccess || plan.slots == 0) return e;
-  const long long rows = static_cast<long long>(p.B) * a.Hq * a.T;
-  fa_tree_combine<D><<<static_cast<unsigned>(rows), 128, 0, s>>>(p);
-  return cudaGetLastError();
+  // eight rows a block, but one where there are too few rows to fill the GPU
+  return static_cast<long long>(p.B) * a.Hq * a.T >= 2048 ? launch_combine<D, 8>(p, s)
+                                                          : launch_combine<D, 1>(p, s);
 }
 
 }  // namespace

@@ -276,9 +276,8 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, 
  *    NaN and infinities are stored as the NaN code; a row without finite
  *    non-zero elements has e = -100.
  *  - 1 <= B, Hkv; 1 <= cap <= FA_CACHE_MAX_TOKENS; d in {64, 128}; B*Hkv and
- *    B*Hkv*ceil(cap/64) below 2^31; cap a multiple of 16 for FA_CACHE_E4M3 (rows of
- *    the scale tensors are 16-byte aligned).  FA_ERR_SHAPE / FA_ERR_HEADDIM
- *    otherwise; FA_ERR_SHAPE for an unknown format.
+ *    B*Hkv*ceil(cap/64) below 2^31.  FA_ERR_SHAPE / FA_ERR_HEADDIM otherwise;
+ *    FA_ERR_SHAPE for an unknown format.
  * The struct is read during the call only; the caller owns it and the memory.
  * Lengths, counts and paths are DEVICE int32 arrays, so that a captured graph
  * can be replayed while they change; what they hold is checked on the device

@@ -28,7 +28,7 @@ def cache(k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, B=2, Hkv=3, cap=64, d=64, fmt=1):
 BAD_CACHES = [
     (dict(k=None), -1), (dict(v=None), -1), (dict(ks=None), -1), (dict(vs=None), -1),
     (dict(B=0), -2), (dict(Hkv=-1), -2), (dict(cap=0), -2), (dict(d=96), -3), (dict(d=0), -3),
-    (dict(cap=72), -2),                       # an e4m3 cache holds a multiple of 16 tokens
+    (dict(cap=(1 << 31) - 1), -2),            # positions and a tile fit an int32
     (dict(fmt=2), -2), (dict(fmt=-1), -2),
     (dict(B=1 << 16, Hkv=1 << 15), -2),       # B*Hkv = 2^31
     (dict(B=1 << 20, Hkv=64, cap=2048), -2),  # 2^31 tiles of 64 tokens
@@ -69,7 +69,8 @@ def test_null_cache(lib):
     assert lib.fa_decode_tree_workspace_size(None, 6, 4) == 0
 
 
-def test_a_bf16_cache_needs_no_scales_and_any_capacity(lib):
+def test_a_bf16_cache_needs_no_scales_and_any_capacity_will_do(lib):
+    assert write(lib, cache(cap=73), k=FAKE + 8) == -4
     c = cache(ks=None, vs=None, cap=71, fmt=0)
     assert write(lib, c, k=FAKE + 8) == -4  # past the shape checks
     assert tree(lib, c, q=FAKE + 8) == -4
