@@ -26,21 +26,21 @@
 // (its scale, its visibility), and any R keeps all four softmax warps busy.
 //
 // One CTA (two an SM):
-//   * warp 4 streams K and V tiles through one TMA ring, in the order the
+//   * one warp streams K and V tiles through one TMA ring, in the order the
 //     tensor core takes them: K0 K1 V0 K2 V1 ...;
-//   * warp 5 issues S^T(t + 2) behind PV(t): S^T has two buffers in tensor memory;
-//   * warps 0-3, a key a thread: softmax over the columns, P^T to shared
+//   * one issues S^T(t + 2) behind PV(t): S^T has two buffers in tensor memory;
+//   * warps 0-3 (0-7 from 32 rows on, half of the rows each), a key a thread: softmax over the columns, P^T to shared
 //     memory ([key][row] in 16-byte units, an operand as it lies), epilogue with
 //     a channel a thread.  A row's reference M is shared by the CTA; one
 //     barrier a tile tells in which 16 rows some score passed it by more than
-//     kLazy binades, and only there maxima are exchanged and O is rescaled.
+//     Lazy binades, and only there maxima are exchanged and O is rescaled.
 //     The next pair's queries are stored during a pair's last tile, so that its
 //     first scores are ready when the epilogue ends.
 //
 // e4m3 operands: kind::f8f6f4 takes the cache as it lies in memory.  Two e4m3
 // pieces of 4 significant bits hold the 8 bits of a bf16 query exactly (its row
-// scaled by a power of two into 448), and a probability to 2^-8: S and O
-// accumulate both pieces, twice the MMAs at twice the bf16 rate.  The scales of
+// scaled by a power of two into 448), and an e4m3 and an e5m2 piece a probability
+// to 2^-7: S and O accumulate both pieces, twice the MMAs at twice the bf16 rate.  The scales of
 // keys and values join in the softmax: with e_j the exponent of value row j, the
 // thread forms t_j = scale log2(e) 2^(k_j) S_j + e_j, keeps M = max t_j, and
 // gives P_j = 2^(t_j - M) to the product with the codes, while the sum takes
@@ -60,27 +60,20 @@ namespace {
 
 __device__ unsigned int g_tree_error;
 
-constexpr int kTreeThreads = 192;
-constexpr int kSoftThreads = 128;
-constexpr int kTreeTmaWarp = 4;
-constexpr int kTreeMmaWarp = 5;
 constexpr int kTile = kTreeTile;  // keys a tile: one a softmax thread
 constexpr int kMaxSlots = 8;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
-static_assert(kTile == kSoftThreads, "a key a thread");
 
 constexpr int kPairCost = 2;  // units of a pair besides its tiles
 
 // A row's accumulator is rescaled only when its maximum grows by more than
-// kLazy binades.  bf16 has the range for any P; the e4m3 pieces of P are scaled
-// so that 2^kLazy times the largest P at the last rescale is 448, which is 1.75
-// in P's units (2^8 of the pieces': see split4).
+// kLog2 binades.  bf16 has the range for any P; the e4m3 pieces of P are scaled
+// so that 2^kLog2 times the largest P at the last rescale is 448, the largest code.
 template <bool F8>
 struct Lazy {
-  static constexpr float kLog2 = F8 ? 3.0f : 8.0f;
-  static constexpr float kTop = F8 ? 0.80735492f : 8.0f;  // log2 of the largest P
-  static constexpr float kOScale = F8 ? 0.00390625f : 1.0f;
+  static constexpr float kLog2 = F8 ? 6.0f : 8.0f;
+  static constexpr float kTop = F8 ? 8.80735492f : 8.0f;  // log2 of the largest P
 };
 
 struct TreeBars {
@@ -92,7 +85,7 @@ struct TreeBars {
   unsigned int bad[2][2];  // by pair parity: drafts whose value row holds NaN or infinities
   int start_b, start_h, start_u0, unit0, unit1;  // this CTA's share
   int next_tiles[2], next_len[2];                // by pair parity
-  uint8_t over[2][4];      // by tile parity: chunks of rows that a warp saw grow
+  alignas(8) uint8_t over[2][8];      // by tile parity: chunks of 16 rows that a warp saw grow
   unsigned int fresh;      // chunks with a row that has seen no key yet
 };
 
@@ -103,7 +96,7 @@ struct TreeRows {
   float f[NR];      // scale log2(e), times 2^e of the query row for e4m3
   float m[NR];      // reference exponent, -inf before the first key
   float neg_m[NR];  // its negative: 0 before the first key, -inf for rows past R
-  float alpha[NR], shift[NR];   // of the last move
+  float alpha[NR];  // of the last move
   float inv[NR];    // epilogue: what O is multiplied by
   float part[4][NR];            // a warp's maximum or sum
 };
@@ -116,6 +109,12 @@ struct TreeLayout {
   static constexpr int kParts = !F8 && D == 128 ? 2 : 1;
   static constexpr uint32_t kSlot = kTile * kRow / kParts;     // 16 KB or 8 KB
   static constexpr int kVKeys = kTile / kParts;
+  // softmax: a group of 128 threads (a key each) for every 16 or 32 rows
+  static constexpr int kGroups = NR >= 32 ? 2 : 1;
+  static constexpr int kOwn = NR / kGroups;  // rows of a thread
+  static constexpr int kSoft = kTile * kGroups;
+  static constexpr int kTmaWarp = kSoft / 32, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = kSoft + 64;
   static constexpr int kPieces = F8 ? 2 : 1;                   // of q and of P
   static constexpr uint32_t kQPiece = NR * kRow;               // 64 columns at a time for bf16
   static constexpr int kUnit = F8 ? 16 : 8;                    // rows in 16 bytes of P
@@ -161,8 +160,15 @@ struct TreeParams {
   float scale_log2;
 };
 
-__device__ __forceinline__ bool t_wait(uint64_t* bar, uint32_t parity, TreeBars* b, uint32_t code) {
+// The bounded wait; its loop is out of line, so that a wait costs the kernel's
+// hot code a few instructions (with the loops and other rare paths inlined the
+// code was 100 KB, and warps waited for instructions a quarter of the time).
+__device__ __noinline__ bool t_wait_loop(uint64_t* bar, uint32_t parity, TreeBars* b,
+                                         uint32_t code) {
   return mbar_wait(bar, parity, &b->abort_flag, &g_tree_error, code);
+}
+__device__ __forceinline__ bool t_wait(uint64_t* bar, uint32_t parity, TreeBars* b, uint32_t code) {
+  return mbar_try_wait(smem_u32(bar), parity) || t_wait_loop(bar, parity, b, code);
 }
 
 // Keys of sequence b that exist: its committed tokens and its drafts.
@@ -242,29 +248,32 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// Barrier 1: the softmax threads.
-__device__ __forceinline__ void soft_bar() { named_bar_sync(1, kSoftThreads); }
-
 // ------------------------------------------------------------ conversions
-// Four fp32 P of 0 .. 1.75 as e4m3 pieces of 2^8 P: a word of high pieces, a word
-// of low ones.  fp16 with 2^8 less than e4m3's value has e4m3's exponent field,
-// so that bits 14..7 of the fp16 P are the code of 2^8 P cut to 4 significant
-// bits (subnormal codes included); the rest R is exact in fp16 and rounded (half
-// up) to its 4 bits the same way: 2^-8 of P together.  Shifts, adds and byte
-// permutes run at four times the rate of the e4m3 conversions, which bounded
-// the softmax (64 rows: 2200 cycles a tile).
+// Four fp32 P of 0 .. 448 as two pieces each: a word of e4m3 (high) and a word of
+// e5m2 (the rest).  fp16 times 2^-8 has e4m3's exponent field, so that bits 14..7
+// of the rounded (half up) fp16 are the code, subnormal ones included; the rest R
+// is exact in fp16, and its upper byte, rounded the same way, is e5m2.  R is at
+// most 2^-4 of P and its code off by at most 2^-3 of R: 2^-7 of P (2^-9.6 in the
+// mean square, like bf16's 2^-9.3), down to P of 2^-6; e5m2 keeps R's
+// leading bits through seven more binades than e4m3 would, which is the room that
+// kLazy takes.  Shifts, adds and byte permutes run at four times the rate of the
+// e4m3 conversions.  (A NaN is lost here: the row's sum carries it.)
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const __half2 s = __hmul2(h, __half2half2(__ushort_as_half(0x1c00)));  // 2^-8
+  const uint32_t c = (*reinterpret_cast<const uint32_t*>(&s) + 0x00400040u) & 0x7f807f80u;
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&c),
+                            __half2half2(__ushort_as_half(0xdc00)), h);  // -2^8
+  hi = c << 1;
+  lo = *reinterpret_cast<const uint32_t*>(&r) + 0x00800080u;
+}
 __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t& hi,
                                        uint32_t& lo) {
-  const __half2 h0 = __floats2half2_rn(x0, x1), h1 = __floats2half2_rn(x2, x3);
-  const uint32_t w0 = *reinterpret_cast<const uint32_t*>(&h0);
-  const uint32_t w1 = *reinterpret_cast<const uint32_t*>(&h1);
-  const uint32_t c0 = w0 & 0x7f807f80u, c1 = w1 & 0x7f807f80u;
-  const __half2 r0 = __hsub2(h0, *reinterpret_cast<const __half2*>(&c0));
-  const __half2 r1 = __hsub2(h1, *reinterpret_cast<const __half2*>(&c1));
-  const uint32_t v0 = *reinterpret_cast<const uint32_t*>(&r0) * 2 + 0x00800080u;
-  const uint32_t v1 = *reinterpret_cast<const uint32_t*>(&r1) * 2 + 0x00800080u;
-  hi = __byte_perm(w0 << 1, w1 << 1, 0x7531);
-  lo = __byte_perm(v0, v1, 0x7531);
+  uint32_t h0, l0, h1, l1;
+  split2(x0, x1, h0, l0);
+  split2(x2, x3, h1, l1);
+  hi = __byte_perm(h0, h1, 0x7531);
+  lo = __byte_perm(l0, l1, 0x7531);
 }
 
 // Four fp32 of at most 448 as two e4m3 pieces each: hi = e4m3(x), lo = e4m3(x - hi).
@@ -346,14 +355,14 @@ __device__ __forceinline__ uint64_t sdesc_plain_mn(uint32_t addr, uint32_t kstep
 
 // ------------------------------------------------------------ query rows
 // The row tile's query rows as the swizzled operand of S^T (rows past `have` are
-// zeros), kSoftThreads / NR threads a row.  e4m3: two pieces of the row times
-// 2^-e, its factor takes 2^e.
+// zeros), kSoft / NR threads a row.  e4m3: two pieces of the row times 2^-e, its
+// factor takes 2^e.
 template <int D, bool F8, int NR>
 __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, const uint4* q,
                                               int have, float scale_log2) {
   using L = TreeLayout<D, F8, NR>;
-  constexpr int kPer = kSoftThreads / NR;   // threads a row
-  constexpr int kGran = D / 8 / kPer;       // eight channels each
+  constexpr int kPer = L::kSoft / NR;   // threads a row
+  constexpr int kGran = D / 8 / kPer;   // eight channels each
   const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
   uint4 x[kGran];
   uint32_t m = 0;
@@ -491,13 +500,16 @@ __device__ __forceinline__ bool product_done(int i, bool ok, TreeBars* bars, uin
 
 // ------------------------------------------------------------ the kernel
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(kTreeThreads, 2)
+__global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                    const __grid_constant__ TreeParams p) {
   using L = TreeLayout<D, F8, NR>;
   constexpr int kSlots = L::kSlots;
   constexpr int kParts = L::kParts;
-  constexpr int kChunks = NR / 16;
+  constexpr int kChunks = L::kOwn / 16;  // of 16 rows, of a thread
+  // x of a tile stays in registers up to 16 rows a thread; for 32 it is formed
+  // again from tensor memory for each use (held, it spilled to local memory)
+  constexpr bool kKeep = kChunks == 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -510,14 +522,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_ready, kSoftThreads);
+    mbar_init(&bars->q_ready, L::kSoft);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_ready[s], kSoftThreads);
+      mbar_init(&bars->p_ready[s], L::kSoft);
       mbar_init(&bars->pv_done[s], 1);
       bars->bad[s][0] = bars->bad[s][1] = 0;
     }
@@ -568,7 +580,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
   __syncthreads();
   if (bars->abort_flag || !Walk(bars).inside()) return;
-  if (warp == kTreeMmaWarp) {
+  if (warp == L::kMmaWarp) {
     tmem_alloc(&bars->tmem_base, L::kCols);
     tmem_relinquish();
   }
@@ -578,7 +590,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   const uint32_t tmem = bars->tmem_base;
   const uint32_t sRing = smem_u32(smem + L::kRing);
 
-  if (warp == kTreeTmaWarp) {
+  if (warp == L::kTmaWarp) {
     // ------------------------------------------------ TMA producer
     if (lane == 0) {
       tma_prefetch_desc(&tk);
@@ -613,89 +625,91 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       };
       for (Walk w(bars); ok && w.valid(p); w.next(p)) {
         const int bh = w.b * p.Hkv + w.h, row0 = w.t0 * kTile;
-        load_k(row0, bh);
-        if (w.n > 1) load_k(row0 + kTile, bh);
-        for (int t = 0; ok && t < w.n; ++t) {
-          load_v(row0 + t * kTile, bh);
+#pragma unroll 1
+        for (int t = -2; ok && t < w.n; ++t) {
+          if (t >= 0) load_v(row0 + t * kTile, bh);
           if (t + 2 < w.n) load_k(row0 + (t + 2) * kTile, bh);
         }
       }
     }
     __syncwarp();
-  } else if (warp == kTreeMmaWarp) {
+  } else if (warp == L::kMmaWarp) {
     // ------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t sQ = smem_u32(smem + L::kQ);
       const uint32_t sP = smem_u32(smem + L::kP);
       int n = 0, it = 0, seg = 0;  // slots taken, tiles and pairs done
       bool ok = true;
-      auto issue_s = [&](int i) {  // S^T of the share's tile i = K Q^T
-        const uint32_t d = tmem + (i & 1) * NR;
-#pragma unroll
-        for (int c = 0; c < kParts; ++c) {
-          const int s = n % kSlots;
-          if (!(ok = ok && t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) return;
-          tc_fence_after_sync();
-          const uint32_t kbase = sRing + s * L::kSlot;
-          if constexpr (F8) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(128, NR);
-#pragma unroll
-            for (int x = 0; x < 2 * (D / 32); ++x) {
-              const int piece = x / (D / 32), kk = x % (D / 32);
-              umma_ss_f8(d, sdesc<L::kAtom>(kbase + kk * 32, 16, 8 * L::kAtom),
-                         sdesc<L::kAtom>(sQ + piece * L::kQPiece + kk * 32, 16, 8 * L::kAtom),
-                         idesc, x > 0 ? 1u : 0u);
-            }
-          } else {
-            constexpr uint32_t idesc = idesc_bf16_f32(128, NR, false, false);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 64 columns
-              umma_ss(d, sdesc_sw128(kbase + kk * 32, 16, 1024),
-                      sdesc_sw128(sQ + c * (NR * 128) + kk * 32, 16, 1024), idesc,
-                      (c > 0 || kk > 0) ? 1u : 0u);
-          }
-          umma_commit(&bars->empty[s]);
-          ++n;
-        }
-        umma_commit(&bars->s_full[i & 1]);
-      };
       for (Walk w(bars); ok && w.valid(p); w.next(p), ++seg) {
         if (!(ok = t_wait(&bars->q_ready, seg & 1, bars, 0x512))) break;
-        issue_s(it);
-        if (w.n > 1) issue_s(it + 1);
-        for (int t = 0; ok && t < w.n; ++t, ++it) {
-          // O^T += V^T P^T
-          if (!(ok = t_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513))) break;
-          const uint32_t pbase = sP + (it % L::kPBufs) * L::kPBytes;
-          const uint32_t d = tmem + L::kOCol;
+#pragma unroll 1
+        for (int t = -2; ok && t < w.n; ++t) {
+          if (t >= 0) {
+            // O^T += V^T P^T
+            if (!(ok = t_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513))) break;
+            const uint32_t pbase = sP + (it % L::kPBufs) * L::kPBytes;
+            const uint32_t d = tmem + L::kOCol;
+#pragma unroll 1
+            for (int c = 0; c < kParts; ++c, ++n) {
+              const int s = n % kSlots;
+              if (!(ok = t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514))) break;
+              tc_fence_after_sync();
+              const uint32_t vbase = sRing + s * L::kSlot;
+              if constexpr (F8) {
+                constexpr uint32_t both_mn = idesc_e4m3_f32(D, NR) | (3u << 15);
 #pragma unroll
-          for (int c = 0; c < kParts; ++c) {
-            const int s = n % kSlots;
-            if (!(ok = ok && t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514))) break;
-            tc_fence_after_sync();
-            const uint32_t vbase = sRing + s * L::kSlot;
-            if constexpr (F8) {
-              constexpr uint32_t idesc = idesc_e4m3_f32(D, NR) | (3u << 15);  // both MN-major
+                for (int x = 0; x < 2 * (kTile / 32); ++x) {
+                  const int piece = x / (kTile / 32), kk = x % (kTile / 32);
+                  const uint32_t idesc = both_mn | (piece ? 1u << 10 : 0u);  // B: e4m3, e5m2
+                  umma_ss_f8(d, sdesc<L::kAtom>(vbase + kk * 32 * L::kAtom, 16, 8 * L::kAtom),
+                             sdesc_plain_mn(pbase + piece * L::kPPiece + kk * 512, 128, kTile * 16),
+                             idesc, (t > 0 || x > 0) ? 1u : 0u);
+                }
+              } else {
+                constexpr uint32_t idesc = idesc_bf16_f32(D, NR, true, true);
 #pragma unroll
-              for (int x = 0; x < 2 * (kTile / 32); ++x) {
-                const int piece = x / (kTile / 32), kk = x % (kTile / 32);
-                umma_ss_f8(d, sdesc<L::kAtom>(vbase + kk * 32 * L::kAtom, 16, 8 * L::kAtom),
-                           sdesc_plain_mn(pbase + piece * L::kPPiece + kk * 512, 128, kTile * 16),
-                           idesc, (t > 0 || x > 0) ? 1u : 0u);
+                for (int kk = 0; kk < L::kVKeys / 16; ++kk)
+                  umma_ss(d, sdesc_sw128(vbase + kk * 2048, L::kVKeys * 128, 1024),
+                          sdesc_plain_mn(pbase + (c * (L::kVKeys / 16) + kk) * 256, 128, kTile * 16),
+                          idesc, (t > 0 || c > 0 || kk > 0) ? 1u : 0u);
               }
-            } else {
-              constexpr uint32_t idesc = idesc_bf16_f32(D, NR, true, true);
-#pragma unroll
-              for (int kk = 0; kk < L::kVKeys / 16; ++kk)
-                umma_ss(d, sdesc_sw128(vbase + kk * 2048, L::kVKeys * 128, 1024),
-                        sdesc_plain_mn(pbase + (c * (L::kVKeys / 16) + kk) * 256, 128, kTile * 16),
-                        idesc, (t > 0 || c > 0 || kk > 0) ? 1u : 0u);
+              umma_commit(&bars->empty[s]);
             }
-            umma_commit(&bars->empty[s]);
-            ++n;
+            if (!ok) break;
+            umma_commit(&bars->pv_done[it & 1]);
+            ++it;
           }
-          umma_commit(&bars->pv_done[it & 1]);
-          if (t + 2 < w.n) issue_s(it + 2);  // into the buffer that softmax(it) has read
+          if (t + 2 < w.n) {
+            // S^T of tile t + 2 = K Q^T, into the buffer that softmax(t) has read
+            const int i = it + (t < 0 ? t + 2 : 1);
+            const uint32_t d = tmem + (i & 1) * NR;
+#pragma unroll 1
+            for (int c = 0; c < kParts; ++c, ++n) {
+              const int s = n % kSlots;
+              if (!(ok = t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) break;
+              tc_fence_after_sync();
+              const uint32_t kbase = sRing + s * L::kSlot;
+              if constexpr (F8) {
+                constexpr uint32_t idesc = idesc_e4m3_f32(128, NR);
+#pragma unroll
+                for (int x = 0; x < 2 * (D / 32); ++x) {
+                  const int piece = x / (D / 32), kk = x % (D / 32);
+                  umma_ss_f8(d, sdesc<L::kAtom>(kbase + kk * 32, 16, 8 * L::kAtom),
+                             sdesc<L::kAtom>(sQ + piece * L::kQPiece + kk * 32, 16, 8 * L::kAtom),
+                             idesc, x > 0 ? 1u : 0u);
+                }
+              } else {
+                constexpr uint32_t idesc = idesc_bf16_f32(128, NR, false, false);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // 64 columns
+                  umma_ss(d, sdesc_sw128(kbase + kk * 32, 16, 1024),
+                          sdesc_sw128(sQ + c * (NR * 128) + kk * 32, 16, 1024), idesc,
+                          (c > 0 || kk > 0) ? 1u : 0u);
+              }
+              umma_commit(&bars->empty[s]);
+            }
+            if (ok) umma_commit(&bars->s_full[i & 1]);
+          }
         }
       }
       umma_commit(&bars->drain);
@@ -706,54 +720,152 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     // A failed wait clears ok: the warp then skips the work that is left, but
     // none of the barriers, which the four warps pass together.
     const int tid = threadIdx.x;
-    const uint32_t tlane = tmem_addr(tmem, warp * 32, 0);
+    const int key = tid % kTile, group = tid / kTile;
+    const int quad = warp & 3;  // its tensor-memory lanes: keys, and channels
+    const int own = group * L::kOwn, own_c = own / 16;  // first row and chunk
+    const uint32_t tlane = tmem_addr(tmem, quad * 32, 0);
+    auto soft_bar = [] { named_bar_sync(1, L::kSoft); };
     TreeRows<NR>* const both = reinterpret_cast<TreeRows<NR>*>(smem + L::kRows);
     int it = 0, seg = 0, n = 0;
     bool ok = true;
     const int have = min(p.R - rt * kTreeRows, NR);  // query rows of this tile
-    Walk w(bars);
-    w.set(bars->next_tiles[0]);
-    int len = bars->next_len[0];
-    unsigned long long any = drafts_seen(p, w.b);
     // this thread's scale bytes of the next tile, loaded a tile ahead
     uint32_t kb = 127, vb = 127;
-    auto load_scales = [&](int b, int h, int pos, int end) {
+    auto load_scales = [&](long long bh, int pos, int end) {
       kb = vb = 127;
       if (F8 && pos < end) {
-        const long long at = (static_cast<long long>(b) * p.Hkv + h) * p.cap + pos;
-        kb = __ldg(p.k_scale + at);
-        vb = __ldg(p.v_scale + at);
+        kb = __ldg(p.k_scale + bh * p.cap + pos);
+        vb = __ldg(p.v_scale + bh * p.cap + pos);
       }
     };
-    load_scales(w.b, w.h, w.t0 * kTile + tid, min(len + p.T, p.cap));
-    store_queries<D, F8, NR>(
-        smem + L::kQ, both,
-        p.q + ((static_cast<long long>(w.b) * p.Hkv + w.h) * p.R + rt * kTreeRows) * (D / 8), have,
-        p.scale_log2);
-    store_masks<NR>(both, p, w.b, rt);
-    fence_proxy_async_smem();
-    mbar_arrive(&bars->q_ready);
-    if (tid == 0) bars->fresh = (1u << ((have + 15) / 16)) - 1;
-    soft_bar();
-
-    for (bool more = true; more; ++seg) {
-      TreeRows<NR>* const rows = both + (seg & 1);
-      const int end = min(len + p.T, p.cap);
-      const long long bh = static_cast<long long>(w.b) * p.Hkv + w.h;
-      const long long row0 = bh * p.R + rt * kTreeRows;  // of o and lse
-      // the pair after this one; thread 0's view of its length is everybody's
-      Walk w2 = w;
-      w2.next(p);
-      more = w2.inside();
-      int len2 = 0;
-      if (tid == 0 && more) len2 = w2.b == w.b ? len : seq_len(p, w2.b);
-      f32x2 l[NR / 2];
+    Walk w(bars);           // the pair at hand, and from its last tile on the next one
+    bool more = true;       // there is a next one
+    f32x2 l[L::kOwn / 2];   // sums of this key column, by row
+    // the pair in work: its length, its first row of o, its slot of partials (-1: none)
+    int len = 0, end = 0;
+    long long bh = 0, slot = -1;
+    unsigned long long any = 0;
+#pragma unroll 1
+    for (;; ++seg) {
+      // ---- the next pair's queries: S of the last tile is complete, so that Q is
+      // free, and the first scores are formed during this pair's epilogue
+      const int len2 = more ? bars->next_len[seg & 1] : 0;
+      const long long bh2 = static_cast<long long>(w.b) * p.Hkv + w.h;
+      unsigned long long any2 = 0;
+      if (more) {
+        TreeRows<NR>* const rows = both + (seg & 1);
+        w.set(bars->next_tiles[seg & 1]);
+        load_scales(bh2, w.t0 * kTile + key, min(len2 + p.T, p.cap));
+        store_queries<D, F8, NR>(smem + L::kQ, rows, p.q + (bh2 * p.R + rt * kTreeRows) * (D / 8),
+                                 have, p.scale_log2);
+        store_masks<NR>(rows, p, w.b, rt);
+        any2 = drafts_seen(p, w.b);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_ready);
+        if (tid == 0) bars->fresh = (1u << ((have + 15) / 16)) - 1;
+      }
+      if (seg > 0) {
+        // ---- epilogue: sums over the keys, then a channel a thread
+        TreeRows<NR>* const rows = both + ((seg - 1) & 1);
+        unsigned int* const note = bars->bad[(seg - 1) & 1];
 #pragma unroll
-      for (int r = 0; r < NR / 2; ++r) l[r] = 0;
-      int pos = w.t0 * kTile + tid;
+        for (int c = 0; c < kChunks; ++c) {
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 z = unpack2(l[8 * c + i]);
+            y[2 * i] = z.x;
+            y[2 * i + 1] = z.y;
+          }
+          const float z = sum_lanes(y);
+          if (lane < 16) rows->part[quad][own + 16 * c + lane] = z;
+        }
+        ok = product_done(it - 1, ok, bars, 0x526);
+        tc_fence_after_sync();
+        soft_bar();
+        const long long row0 = bh * p.R + rt * kTreeRows;  // of o and lse
+        const unsigned long long bad = static_cast<unsigned long long>(note[1]) << 32 | note[0];
+        if (tid < NR) {
+          const float sum = (rows->part[0][tid] + rows->part[1][tid]) +
+                            (rows->part[2][tid] + rows->part[3][tid]);
+          rows->inv[tid] = slot >= 0 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+          if (tid < have && ok) {
+            if (slot < 0)
+              p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (log2f(sum) - rows->neg_m[tid]) * kLn2;
+            else
+              p.part_ml[slot * p.prow + tid] = make_float2(rows->m[tid], sum);
+          }
+        }
+        soft_bar();
+        if (tid == 0) note[0] = note[1] = 0;
+        // channel of this thread: with d = 64 the accumulator's rows are spread over
+        // the first 16 lanes of each warp
+        const int ch = D == 128 ? key : quad * 16 + lane;
+        const bool mine = ok && (D == 128 || lane < 16);
+#pragma unroll 1
+        for (int c = own; c < min(have, own + L::kOwn); c += 16) {
+          uint32_t o[16];
+          tmem_ld16(tlane + L::kOCol + c, o);
+          tmem_ld_wait();
+          reg_pin(o);
+          if (bad && mine) {
+            // drafts with NaN or infinities, to the rows that see them
+#pragma unroll 1
+            for (int j = 0; j < 64; ++j) {
+              if (!(bad >> j & 1)) continue;
+              const long long at = (bh * p.cap + len + j) * D + ch;
+              float v;
+              if constexpr (F8)
+                v = (p.v[at] & 0x7f) == 0x7f ? NAN : 0.0f;
+              else
+                v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[at]);
+              if (isfinite(v)) continue;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (rows->seen[c + i] >> j & 1)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+            }
+          }
+          if (slot < 0) {
+            __nv_bfloat16* dst = p.o + (row0 + c) * D + ch;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (mine && c + i < have)
+                dst[i * D] = __float2bfloat16_rn(__uint_as_float(o[i]) * rows->inv[c + i]);
+          } else {
+            float* dst = p.part_o + (slot * p.prow + c) * D + ch;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (mine && c + i < have) dst[i * D] = __uint_as_float(o[i]);
+          }
+        }
+      } else {
+        soft_bar();  // the first pair's rows are stored
+      }
+      if (!more) break;
 
-      for (int t = 0; t < w.n; ++t, ++it, pos += kTile) {
-        const bool edge = pos - tid + kTile > len;
+      // ---- the pair's tiles
+      TreeRows<NR>* const rows = both + (seg & 1);
+      len = len2;
+      end = min(len + p.T, p.cap);
+      bh = bh2;
+      any = any2;
+      // partials of a pair that began in an earlier share go to slot 0, of one that
+      // goes on in the next to slot 1
+      slot = w.n == w.nt ? -1 : 2ll * blockIdx.x + (w.t0 > 0 ? 0 : 1);
+      const int tiles = w.n;
+      int pos = w.t0 * kTile + key;
+      const int b = w.b;
+      w.next(p);
+      more = w.inside();
+      // thread 0's view of the next pair's length is everybody's
+      int len3 = 0;
+      if (tid == 0 && more) len3 = w.b == b ? len : seq_len(p, w.b);
+#pragma unroll
+      for (int r = 0; r < L::kOwn / 2; ++r) l[r] = 0;
+
+#pragma unroll 1
+      for (int t = 0; t < tiles; ++t, ++it, pos += kTile) {
         float ks = 1.0f, ev = 0.0f, wv = 1.0f;
         if constexpr (F8) {
           // 2^k_j, e_j and 2^-e_j; bytes of rows that are not there stay finite
@@ -762,271 +874,188 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           ev = static_cast<float>(e);
           wv = pow2_of(-e);
         }
-        if (t + 1 < w.n) load_scales(w.b, w.h, pos + kTile, end);
+        if (t + 1 < tiles) load_scales(bh, pos + kTile, end);
         ok = ok && __all_sync(0xffffffffu, t_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, 0x522));
-        if (edge) {
+        // ---- which rows see this key: bit r of the thread's own rows
+        uint32_t hidden = 0;
+        if (pos - key + kTile > len) {
           // V(t) in the order of loads.  With S(it) and PV(it - 1) complete, so are
           // all loads that its slot had before: the parity is V(t)'s.
-          const int v = n + kParts * (2 + t + min(t, w.n - 2)) + tid / L::kVKeys;
+          const int v = n + kParts * (2 + t + min(t, tiles - 2)) + key / L::kVKeys;
           if (t > 0) ok = product_done(it - 1, ok, bars, 0x523);
           ok = ok && __all_sync(0xffffffffu, t_wait(&bars->full[v % kSlots], (v / kSlots) & 1,
                                                     bars, 0x521));
-          if (ok)
+          if (ok && group == 0)
             clean_values<L::kAtom, kParts, F8>(
-                smem + L::kRing + (v % kSlots) * L::kSlot + (tid % L::kVKeys) * L::kAtom,
+                smem + L::kRing + (v % kSlots) * L::kSlot + (key % L::kVKeys) * L::kAtom,
                 L::kVKeys * 128, pos, len, end, any, bars->bad[seg & 1]);
+          if (pos >= end) {
+            hidden = 0xffffffffu;
+          } else if (pos >= len) {
+            const int j = pos - len;
+#pragma unroll 4
+            for (int r = 0; r < L::kOwn; ++r)
+              hidden |= (rows->seen[own + r] >> j & 1 ? 0u : 1u) << r;
+          }
         }
-        // ---- x = t - M of this key for every row
-        f32x2 x[NR / 2];
+        // ---- x = t - M of this key for 16 rows (chunk c)
         tc_fence_after_sync();
-        {
-          uint32_t s[NR];
-#pragma unroll
-          for (int c = 0; c < NR; c += 16) tmem_ld16(tlane + (it & 1) * NR + c, s + c);
+        const f32x2 ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
+        auto form = [&](int c0, f32x2* x) {
+          const int c = own_c + c0;
+          uint32_t s[16];
+          tmem_ld16(tlane + (it & 1) * NR + 16 * c, s);
           tmem_ld_wait();
           reg_pin(s);
 #pragma unroll
-          for (int r = 0; r < NR / 2; ++r)
-            x[r] = pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1]));
-        }
-        const f32x2 ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
-#pragma unroll
-        for (int r = 0; r < NR / 2; r += 2) {
-          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&rows->f[2 * r]);
-          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&rows->neg_m[2 * r]);
-          if constexpr (F8) {
-            x[r] = add2(fma2(mul2(x[r], f.x), ks2, ev2), m.x);
-            x[r + 1] = add2(fma2(mul2(x[r + 1], f.y), ks2, ev2), m.y);
-          } else {
-            x[r] = fma2(x[r], f.x, m.x);
-            x[r + 1] = fma2(x[r + 1], f.y, m.y);
-          }
-        }
-        if (edge && pos >= len) {
-          const int j = (pos - len) & 63;
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (pos >= end || !(rows->seen[r] >> j & 1)) {
-              float2 y = unpack2(x[r / 2]);
-              (r & 1 ? y.y : y.x) = -INFINITY;
-              x[r / 2] = pack2(y.x, y.y);
+          for (int r = 0; r < 8; r += 2) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&rows->f[16 * c + 2 * r]);
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&rows->neg_m[16 * c + 2 * r]);
+            const f32x2 a = pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1]));
+            const f32x2 b = pack2(__uint_as_float(s[2 * r + 2]), __uint_as_float(s[2 * r + 3]));
+            if constexpr (F8) {
+              x[r] = add2(fma2(mul2(a, f.x), ks2, ev2), m.x);
+              x[r + 1] = add2(fma2(mul2(b, f.y), ks2, ev2), m.y);
+            } else {
+              x[r] = fma2(a, f.x, m.x);
+              x[r + 1] = fma2(b, f.y, m.y);
             }
-        }
-        const unsigned int fresh = bars->fresh;
-        unsigned int grown = 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int r = 8 * c; r < 8 * c + 8; ++r) {
-            const float2 y = unpack2(x[r]);
-            mx = fmax3f(mx, y.x, y.y);
           }
-          if (__any_sync(0xffffffffu, mx > Lazy<F8>::kTop || (fresh >> c & 1))) grown |= 1u << c;
-        }
-        if (lane == 0) bars->over[it & 1][warp] = static_cast<uint8_t>(grown);
-        if (tid == 0 && t == 0 && more) {
-          bars->next_len[(seg + 1) & 1] = len2;
-          bars->next_tiles[(seg + 1) & 1] = (min(len2 + p.T, p.cap) + kTile - 1) / kTile;
-        }
-        soft_bar();
-        grown = *reinterpret_cast<const uint32_t*>(bars->over[it & 1]);
-        grown = (grown | grown >> 8 | grown >> 16 | grown >> 24) & 0xffu;
-        if (grown) {
+          if (hidden) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              float2 y = unpack2(x[r]);
+              if (hidden >> (16 * c0 + 2 * r) & 1) y.x = -INFINITY;
+              if (hidden >> (16 * c0 + 2 * r + 1) & 1) y.y = -INFINITY;
+              x[r] = pack2(y.x, y.y);
+            }
+          }
+        };
+        f32x2 x[8];
+        unsigned int grown = 0;
+        const unsigned int fresh = bars->fresh;
+#pragma unroll 1
+        for (bool moved = false;; moved = true) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            form(c, x);
+            float mx = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const float2 y = unpack2(x[r]);
+              mx = fmax3f(mx, y.x, y.y);
+            }
+            if (__any_sync(0xffffffffu, mx > Lazy<F8>::kTop || (fresh >> (own_c + c) & 1)))
+              grown |= 1u << (own_c + c);
+          }
+          if (moved) break;
+          if (lane == 0) bars->over[it & 1][warp] = static_cast<uint8_t>(grown);
+          if (tid == 0 && t == 0 && more) {
+            bars->next_len[(seg + 1) & 1] = len3;
+            bars->next_tiles[(seg + 1) & 1] = (min(len3 + p.T, p.cap) + kTile - 1) / kTile;
+          }
+          soft_bar();
+          {
+            const uint2 o = *reinterpret_cast<const uint2*>(bars->over[it & 1]);
+            grown = L::kGroups == 2 ? o.x | o.y : o.x;
+            grown = (grown | grown >> 8 | grown >> 16 | grown >> 24) & 0xffu;
+          }
+          if (!grown) break;
           // ---- new references where a row grew: maxima over the CTA's keys
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            if (!(grown >> c & 1)) continue;
+            if (!(grown >> (own_c + c) & 1)) continue;
+            if (!kKeep) form(c, x);
             float top = -INFINITY;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-              const float2 y = unpack2(x[8 * c + r / 2]);
+              const float2 y = unpack2(x[r / 2]);
               const float z = redux_max(r & 1 ? y.y : y.x);
               if (lane == r) top = z;
             }
-            if (lane < 16) rows->part[warp][16 * c + lane] = top;
+            if (lane < 16) rows->part[quad][own + 16 * c + lane] = top;
           }
           soft_bar();
           if (tid < have && (grown >> (tid / 16) & 1)) {
             const float top = fmaxf(fmaxf(rows->part[0][tid], rows->part[1][tid]),
                                     fmaxf(rows->part[2][tid], rows->part[3][tid]));
-            const float m_old = rows->m[tid], u_old = -rows->neg_m[tid];
-            const float m_new = fmaxf(m_old, u_old + top + (Lazy<F8>::kLog2 - Lazy<F8>::kTop));
-            const float u_new = m_new == -INFINITY ? 0.0f : m_new;
+            const float m_old = rows->m[tid];
+            const float m_new = fmaxf(m_old, top - rows->neg_m[tid] + (Lazy<F8>::kLog2 - Lazy<F8>::kTop));
             rows->m[tid] = m_new;
-            rows->neg_m[tid] = -u_new;
+            rows->neg_m[tid] = m_new == -INFINITY ? 0.0f : -m_new;
             rows->alpha[tid] = m_new == -INFINITY ? 1.0f : ex2_approx(m_old - m_new);
-            rows->shift[tid] = u_old - u_new;
           } else if (tid >= have && tid < NR) {
             rows->alpha[tid] = 1.0f;
-            rows->shift[tid] = 0.0f;
           }
           if (tid == 0) bars->fresh = 0;
           soft_bar();
           if (tid < have && rows->m[tid] == -INFINITY) atomicOr(&bars->fresh, 1u << (tid / 16));
-          // PV(it - 1) must be done before O is rescaled
-          if (t > 0) ok = product_done(it - 1, ok, bars, 0x524);
-          tc_fence_after_sync();
+          if (t > 0) {
+            // PV(it - 1) must be done before O is rescaled
+            ok = product_done(it - 1, ok, bars, 0x524);
+            tc_fence_after_sync();
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (!(grown >> c & 1)) continue;
-            uint32_t o[16];
-            if (t > 0) {
-              tmem_ld16(tlane + L::kOCol + 16 * c, o);
+            for (int c = 0; c < kChunks; ++c) {
+              if (!(grown >> (own_c + c) & 1)) continue;
+              const float* al = rows->alpha + own + 16 * c;
+              uint32_t o[16];
+              tmem_ld16(tlane + L::kOCol + own + 16 * c, o);
               tmem_ld_wait();
               reg_pin(o);
-            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 al = *reinterpret_cast<const float2*>(&rows->alpha[16 * c + 2 * i]);
-              const f32x2 sh = *reinterpret_cast<const f32x2*>(&rows->shift[16 * c + 2 * i]);
-              x[8 * c + i] = add2(x[8 * c + i], sh);
-              l[8 * c + i] = mul2(l[8 * c + i], pack2(al.x, al.y));
-              o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * al.x);
-              o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * al.y);
+              for (int i = 0; i < 8; ++i) {
+                l[8 * c + i] = mul2(l[8 * c + i], pack2(al[2 * i], al[2 * i + 1]));
+                o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * al[2 * i]);
+                o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * al[2 * i + 1]);
+              }
+              tmem_st16(tlane + L::kOCol + own + 16 * c, o);
             }
-            if (t > 0) tmem_st16(tlane + L::kOCol + 16 * c, o);
+            tmem_st_wait();
           }
-          tmem_st_wait();
+          if (!kKeep) break;
         }
         // ---- P = 2^x over the P buffer that PV(it - kPBufs) has read
         if (it >= L::kPBufs) ok = product_done(it - L::kPBufs, ok, bars, 0x525);
-        uint8_t* pb = smem + L::kP + (it % L::kPBufs) * L::kPBytes + tid * 16;
+        uint8_t* pb = smem + L::kP + (it % L::kPBufs) * L::kPBytes + key * 16;
         const f32x2 wv2 = pack2(wv, wv);
 #pragma unroll
-        for (int u = 0; u < NR / L::kUnit; ++u) {
-          uint32_t hi[4], lo[4];
+        for (int c = 0; c < kChunks; ++c) {
+          if (!kKeep) form(c, x);
+          uint32_t hi[8], lo[F8 ? 4 : 1];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
+            const float2 a = unpack2(x[2 * i]), b = unpack2(x[2 * i + 1]);
+            const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
+            const float p2 = ex2_approx(b.x), p3 = ex2_approx(b.y);
+            f32x2* const lc = l + 8 * c + 2 * i;
             if constexpr (F8) {
-              const int r = u * 8 + i * 2;
-              const float2 a = unpack2(x[r]), b = unpack2(x[r + 1]);
-              const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
-              const float p2 = ex2_approx(b.x), p3 = ex2_approx(b.y);
-              l[r] = fma2(pack2(p0, p1), wv2, l[r]);
-              l[r + 1] = fma2(pack2(p2, p3), wv2, l[r + 1]);
+              lc[0] = fma2(pack2(p0, p1), wv2, lc[0]);
+              lc[1] = fma2(pack2(p2, p3), wv2, lc[1]);
               split4(p0, p1, p2, p3, hi[i], lo[i]);
             } else {
-              const int r = u * 4 + i;
-              const float2 a = unpack2(x[r]);
-              const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
-              l[r] = add2(l[r], pack2(p0, p1));
-              hi[i] = pack_bf16x2(p0, p1);
+              lc[0] = add2(lc[0], pack2(p0, p1));
+              lc[1] = add2(lc[1], pack2(p2, p3));
+              hi[2 * i] = pack_bf16x2(p0, p1);
+              hi[2 * i + 1] = pack_bf16x2(p2, p3);
             }
           }
-          *reinterpret_cast<uint4*>(pb + u * (kTile * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          uint8_t* const at = pb + (own_c + c) * (16 / L::kUnit) * (kTile * 16);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           if constexpr (F8)
-            *reinterpret_cast<uint4*>(pb + L::kPPiece + u * (kTile * 16)) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(at + L::kPPiece) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          else
+            *reinterpret_cast<uint4*>(at + kTile * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
         }
         fence_proxy_async_smem();  // P, and cleaned values
         tc_fence_before_sync();
         mbar_arrive(&bars->p_ready[it & 1]);
       }
-      n += 2 * kParts * w.n;
-      // ---- the next pair's queries: S of this pair's last tile is complete, so
-      // that Q is free, and its scores are formed during this pair's epilogue
-      if (more) {
-        len2 = bars->next_len[(seg + 1) & 1];
-        w2.set(bars->next_tiles[(seg + 1) & 1]);
-        load_scales(w2.b, w2.h, tid, min(len2 + p.T, p.cap));
-        store_queries<D, F8, NR>(
-            smem + L::kQ, both + ((seg + 1) & 1),
-            p.q + ((static_cast<long long>(w2.b) * p.Hkv + w2.h) * p.R + rt * kTreeRows) * (D / 8),
-            have, p.scale_log2);
-        if (w2.b == w.b) {
-          if (tid < NR) both[(seg + 1) & 1].seen[tid] = rows->seen[tid];
-        } else {
-          store_masks<NR>(both + ((seg + 1) & 1), p, w2.b, rt);
-          any = drafts_seen(p, w2.b);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bars->q_ready);
-        if (tid == 0) bars->fresh = (1u << ((have + 15) / 16)) - 1;
-      }
-      // ---- epilogue: sums over the keys, then a channel a thread
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        float y[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 z = unpack2(l[8 * c + i]);
-          y[2 * i] = z.x;
-          y[2 * i + 1] = z.y;
-        }
-        const float z = sum_lanes(y);
-        if (lane < 16) rows->part[warp][16 * c + lane] = z;
-      }
-      ok = product_done(it - 1, ok, bars, 0x526);
-      tc_fence_after_sync();
-      soft_bar();
-      const bool whole = w.n == w.nt;
-      // a pair that began in an earlier share goes to slot 0, one that goes on in
-      // the next to slot 1
-      const long long prow0 = (2ll * blockIdx.x + (w.t0 > 0 ? 0 : 1)) * p.prow;
-      const unsigned long long bad =
-          static_cast<unsigned long long>(bars->bad[seg & 1][1]) << 32 | bars->bad[seg & 1][0];
-      if (tid < NR) {
-        const float sum = (rows->part[0][tid] + rows->part[1][tid]) +
-                          (rows->part[2][tid] + rows->part[3][tid]);
-        rows->inv[tid] =
-            Lazy<F8>::kOScale * (!whole ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum));
-        if (tid < have && ok) {
-          if (whole)
-            p.lse[row0 + tid] =
-                sum == 0.0f ? -INFINITY : (log2f(sum) - rows->neg_m[tid]) * kLn2;
-          else
-            p.part_ml[prow0 + tid] = make_float2(rows->m[tid], sum);
-        }
-      }
-      soft_bar();
-      if (tid == 0) bars->bad[seg & 1][0] = bars->bad[seg & 1][1] = 0;
-      // channel of this thread: with d = 64 the accumulator's rows are spread over
-      // the first 16 lanes of each warp
-      const int ch = D == 128 ? tid : warp * 16 + lane;
-      const bool mine = ok && (D == 128 || lane < 16);
-#pragma unroll 1
-      for (int c = 0; c < have; c += 16) {
-        uint32_t o[16];
-        tmem_ld16(tlane + L::kOCol + c, o);
-        tmem_ld_wait();
-        reg_pin(o);
-        if (bad && mine) {
-          // drafts with NaN or infinities, to the rows that see them
-#pragma unroll 1
-          for (int j = 0; j < 64; ++j) {
-            if (!(bad >> j & 1)) continue;
-            const long long at = (bh * p.cap + len + j) * D + ch;
-            float v;
-            if constexpr (F8)
-              v = (p.v[at] & 0x7f) == 0x7f ? NAN : 0.0f;
-            else
-              v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[at]);
-            if (isfinite(v)) continue;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (rows->seen[c + i] >> j & 1)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = c + i;
-          const float y = __uint_as_float(o[i]) * rows->inv[r];
-          if (!mine || r >= have) continue;
-          if (whole)
-            p.o[(row0 + r) * D + ch] = __float2bfloat16_rn(y);
-          else
-            p.part_o[(prow0 + r) * D + ch] = y;
-        }
-      }
-      w = w2;
-      len = len2;
+      n += 2 * kParts * tiles;
     }
   }
 
   // ------------------------------------------------ teardown
-  if (warp == kTreeMmaWarp) mbar_wait(&bars->drain, 0, &bars->abort_flag, &g_tree_error, 0x5ff);
+  if (warp == L::kMmaWarp) mbar_wait(&bars->drain, 0, &bars->abort_flag, &g_tree_error, 0x5ff);
   if (bars->abort_flag) {
     // let any bulk copy already in flight land before the CTA exits
     const uint64_t t0 = globaltimer_ns();
@@ -1035,7 +1064,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kTreeMmaWarp) {
+  if (warp == L::kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kCols);
   }
@@ -1138,7 +1167,7 @@ cudaError_t launch_tile(const TreeParams& p, const CUtensorMap& tk, const CUtens
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   fa_tree_kernel<D, F8, NR>
-      <<<static_cast<unsigned>(p.shares) * p.row_tiles, kTreeThreads, smem, s>>>(tk, tv, p);
+      <<<static_cast<unsigned>(p.shares) * p.row_tiles, TreeLayout<D, F8, NR>::kThreads, smem, s>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
