@@ -236,23 +236,26 @@ constexpr int kTreeRows = 64;   // query rows a row tile, at most
 
 // How a tree decode is split (checked shapes): R = Hq / Hkv * T query rows a
 // (sequence, key head) pair in row tiles of 64, and `shares` CTAs a row tile,
-// each an equal share of all pairs' key tiles; at most `ctas` CTAs, and no more
-// shares than key tiles could exist.  slots: partial results the workspace
-// holds (two a CTA) of prow rows each; none where no pair can be split.
-constexpr int kTreeMaxCtas = 304;  // two an SM of 152
+// each an equal share of all pairs' key tiles; at most as many CTAs as run at
+// once on `sms` SMs, and no more shares than key tiles could exist.  slots:
+// partial results the workspace holds (two a CTA) of prow rows each; none where
+// no pair can be split.
+constexpr int kTreeMaxSms = 152;
+constexpr int tree_ctas(long long rows) { return rows <= 32 ? 2 : 1; }  // an SM
 
 struct TreePlan {
   int row_tiles, shares, slots, prow;
 };
 
-inline TreePlan tree_plan(const fa_cache& c, int Hq, int T, int ctas) {
+inline TreePlan tree_plan(const fa_cache& c, int Hq, int T, int sms) {
   TreePlan p;
   const long long R = static_cast<long long>(Hq) / c.Hkv * T;
   p.row_tiles = static_cast<int>((R + kTreeRows - 1) / kTreeRows);
   p.prow = static_cast<int>(R < kTreeRows ? R : kTreeRows);
   const int tiles = num_tiles(c.cap, kTreeTile);
   const long long most = static_cast<long long>(c.B) * c.Hkv * tiles;
-  long long sh = (ctas < kTreeMaxCtas ? ctas : kTreeMaxCtas) / p.row_tiles;
+  const int ctas = (sms < kTreeMaxSms ? sms : kTreeMaxSms) * tree_ctas(R);
+  long long sh = ctas / p.row_tiles;
   if (sh > most) sh = most;
   p.shares = static_cast<int>(sh < 1 ? 1 : sh);
   p.slots = (p.shares == 1 || tiles == 1) ? 0 : 2 * p.shares * p.row_tiles;
@@ -262,7 +265,7 @@ inline TreePlan tree_plan(const fa_cache& c, int Hq, int T, int ctas) {
 // Workspace of a tree decode: o and (m, l) of each partial row, for the largest
 // split of any GPU.
 inline size_t tree_workspace_bytes(const fa_cache& c, int Hq, int T) {
-  const TreePlan p = tree_plan(c, Hq, T, kTreeMaxCtas);
+  const TreePlan p = tree_plan(c, Hq, T, kTreeMaxSms);
   const size_t bytes = static_cast<size_t>(p.slots) * p.prow * (c.d + 2) * sizeof(float);
   return bytes < 256 ? 256 : (bytes + 255) & ~static_cast<size_t>(255);
 }

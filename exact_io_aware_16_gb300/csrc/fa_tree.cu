@@ -25,11 +25,11 @@
 // 1434 that HBM gives.  This way a tile costs 512 or less, one thread owns one key
 // (its scale, its visibility), and any R keeps all four softmax warps busy.
 //
-// One CTA (two an SM):
+// One CTA (two an SM up to 32 rows, one for 64):
 //   * one warp streams K and V tiles through one TMA ring, in the order the
 //     tensor core takes them: K0 K1 V0 K2 V1 ...;
 //   * one issues S^T(t + 2) behind PV(t): S^T has two buffers in tensor memory;
-//   * warps 0-3 (0-7 from 32 rows on, half of the rows each), a key a thread: softmax over the columns, P^T to shared
+//   * four warps for every 16 rows, a key a thread: softmax over the columns, P^T to shared
 //     memory ([key][row] in 16-byte units, an operand as it lies), epilogue with
 //     a channel a thread.  A row's reference M is shared by the CTA; one
 //     barrier a tile tells in which 16 rows some score passed it by more than
@@ -67,6 +67,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 constexpr int kPairCost = 2;  // units of a pair besides its tiles
 
+// -M of a row that has seen no key: any finite score passes the reference, and
+// -inf stays -inf.
+constexpr float kUnseen = 1e38f;
+
 // A row's accumulator is rescaled only when its maximum grows by more than
 // kLog2 binades.  bf16 has the range for any P; the e4m3 pieces of P are scaled
 // so that 2^kLog2 times the largest P at the last rescale is 448, the largest code.
@@ -85,8 +89,6 @@ struct TreeBars {
   unsigned int bad[2][2];  // by pair parity: drafts whose value row holds NaN or infinities
   int start_b, start_h, start_u0, unit0, unit1;  // this CTA's share
   int next_tiles[2], next_len[2];                // by pair parity
-  alignas(8) uint8_t over[2][8];      // by tile parity: chunks of 16 rows that a warp saw grow
-  unsigned int fresh;      // chunks with a row that has seen no key yet
 };
 
 // What the softmax threads know of a pair's query rows.
@@ -95,7 +97,7 @@ struct TreeRows {
   unsigned long long seen[NR];  // mask row
   float f[NR];      // scale log2(e), times 2^e of the query row for e4m3
   float m[NR];      // reference exponent, -inf before the first key
-  float neg_m[NR];  // its negative: 0 before the first key, -inf for rows past R
+  float neg_m[NR];  // its negative: kUnseen before the first key, -inf for rows past R
   float alpha[NR];  // of the last move
   float inv[NR];    // epilogue: what O is multiplied by
   float part[4][NR];            // a warp's maximum or sum
@@ -109,9 +111,7 @@ struct TreeLayout {
   static constexpr int kParts = !F8 && D == 128 ? 2 : 1;
   static constexpr uint32_t kSlot = kTile * kRow / kParts;     // 16 KB or 8 KB
   static constexpr int kVKeys = kTile / kParts;
-  // softmax: a group of 128 threads (a key each) for every 16 or 32 rows
-  static constexpr int kGroups = NR >= 32 ? 2 : 1;
-  static constexpr int kOwn = NR / kGroups;  // rows of a thread
+  static constexpr int kGroups = NR / 16;  // softmax: 128 threads (a key each) for 16 rows
   static constexpr int kSoft = kTile * kGroups;
   static constexpr int kTmaWarp = kSoft / 32, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = kSoft + 64;
@@ -120,23 +120,21 @@ struct TreeLayout {
   static constexpr int kUnit = F8 ? 16 : 8;                    // rows in 16 bytes of P
   static constexpr uint32_t kPPiece = kTile * NR * (F8 ? 1 : 2);
   static constexpr uint32_t kPBytes = kPieces * kPPiece;
-  static constexpr uint32_t kRoom =
-      113u * 1024 - 1024 - 1024 - 2 * sizeof(TreeRows<NR>) - kPieces * kQPiece;
-  // two buffers of P, but one where two would leave the ring less than four slots
-  static constexpr int kPBufs = kRoom >= 2 * kPBytes + 4 * kSlot ? 2 : 1;
-  static constexpr int kFit = (kRoom - kPBufs * kPBytes) / kSlot;
+  static constexpr int kCtas = tree_ctas(NR);                  // an SM
+  static constexpr uint32_t kRoom = (kCtas == 2 ? 113u : 227u) * 1024 - 1024 - 1024 -
+                                    2 * sizeof(TreeRows<NR>) - kPieces * kQPiece - 2 * kPBytes;
+  static constexpr int kFit = kRoom / kSlot;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
   static_assert(kSlots >= 2 * kParts, "K(t + 1) is loaded before V(t)");
   static constexpr uint32_t kRing = 0;
   static constexpr uint32_t kQ = kRing + kSlots * kSlot;
   static constexpr uint32_t kP = kQ + kPieces * kQPiece;
-  static constexpr uint32_t kRows = kP + kPBufs * kPBytes;
+  static constexpr uint32_t kRows = kP + 2 * kPBytes;
   static constexpr uint32_t kBar = kRows + 2 * sizeof(TreeRows<NR>);
   static constexpr uint32_t kUsed = kBar + 1024 + 1024;  // + alignment slack
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kRows % 16 == 0 && kBar % 8 == 0, "aligned");
-  // two CTAs an SM, never three: the ring is sized for two
-  static constexpr uint32_t kSmem = kUsed > 81920u ? kUsed : 81920u;
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+  static constexpr uint32_t kSmem = kUsed > 81920u ? kUsed : 81920u;  // never three CTAs
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "fits");
   // tensor memory: S^T twice, O^T
   static constexpr uint32_t kOCol = 2 * NR;
   static constexpr uint32_t kCols = NR == 16 ? 64 : NR == 32 ? 128 : 256;
@@ -404,7 +402,7 @@ __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, c
   }
   if (part == 0) {
     rows->m[r] = -INFINITY;
-    rows->neg_m[r] = r < have ? 0.0f : -INFINITY;
+    rows->neg_m[r] = r < have ? kUnseen : -INFINITY;
   }
 }
 
@@ -439,7 +437,7 @@ __device__ __forceinline__ unsigned long long drafts_seen(const TreeParams& p, i
 // noted: the epilogue adds them to the rows that see it.  Key a thread; sv is
 // its row, COLS boxes of ATOM bytes `stride` apart.
 template <uint32_t ATOM, int COLS, bool F8>
-__device__ __forceinline__ void clean_values(uint8_t* sv, uint32_t stride, int pos, int len,
+__device__ __noinline__ void clean_values(uint8_t* sv, uint32_t stride, int pos, int len,
                                              int end, unsigned long long any, unsigned int* note) {
   if (pos < len) return;
   const int j = pos - len;
@@ -490,26 +488,129 @@ __device__ __forceinline__ float sum_lanes(float (&x)[16]) {
   return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
+// t (without a reference: `neg_m` null) or x = t - M of a key for 16 rows.
+template <bool F8>
+__device__ __forceinline__ void form_scores(uint32_t taddr, const float* f, const float* neg_m,
+                                            float ks, float ev, f32x2 (&x)[8]) {
+  uint32_t s[16];
+  tmem_ld16(taddr, s);
+  tmem_ld_wait();
+  reg_pin(s);
+  const f32x2 ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
+#pragma unroll
+  for (int r = 0; r < 8; r += 2) {
+    const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(f + 2 * r);
+    ulonglong2 m = make_ulonglong2(0, 0);
+    if (neg_m) m = *reinterpret_cast<const ulonglong2*>(neg_m + 2 * r);
+    const f32x2 a = pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1]));
+    const f32x2 b = pack2(__uint_as_float(s[2 * r + 2]), __uint_as_float(s[2 * r + 3]));
+    if constexpr (F8) {
+      x[r] = add2(fma2(mul2(a, g.x), ks2, ev2), m.x);
+      x[r + 1] = add2(fma2(mul2(b, g.y), ks2, ev2), m.y);
+    } else {
+      x[r] = fma2(a, g.x, m.x);
+      x[r + 1] = fma2(b, g.y, m.y);
+    }
+  }
+}
+
+// Rows that do not see the key: -inf.
+__device__ __forceinline__ void hide_rows(f32x2 (&x)[8], uint32_t hidden) {
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    float2 y = unpack2(x[r]);
+    if (hidden >> (2 * r) & 1) y.x = -INFINITY;
+    if (hidden >> (2 * r + 1) & 1) y.y = -INFINITY;
+    x[r] = pack2(y.x, y.y);
+  }
+}
+
+// The rare parts of the softmax loop are functions of their own, out of the way
+// of its instructions.
+// Bit r: row r (mask rows `seen`) does not see draft j.
+__device__ __noinline__ uint32_t hidden_rows(const unsigned long long* seen, int j) {
+  uint32_t h = 0;
+#pragma unroll 4
+  for (int r = 0; r < 16; ++r) h |= (seen[r] >> j & 1 ? 0u : 1u) << r;
+  return h;
+}
+
+// The warp's maximum of each row's scores into out[16].
+template <bool F8>
+__device__ __noinline__ void row_maxima(uint32_t taddr, const float* f, float ks, float ev,
+                                        uint32_t hidden, float* out) {
+  const int lane = threadIdx.x & 31;
+  f32x2 t[8];
+  form_scores<F8>(taddr, f, nullptr, ks, ev, t);
+  hide_rows(t, hidden);
+  float top = -INFINITY;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const float2 y = unpack2(t[r / 2]);
+    const float z = redux_max(r & 1 ? y.y : y.x);
+    if (lane == r) top = z;
+  }
+  if (lane < 16) out[lane] = top;
+}
+
+// Row r's new reference from the four warps' maxima, and what its sums are
+// multiplied by.
+template <bool F8, int NR>
+__device__ __noinline__ void new_reference(TreeRows<NR>* rows, int r, int have) {
+  rows->alpha[r] = 1.0f;
+  if (r >= have) return;
+  const float top = fmaxf(fmaxf(rows->part[0][r], rows->part[1][r]),
+                          fmaxf(rows->part[2][r], rows->part[3][r]));
+  const float m_old = rows->m[r];
+  const float m_new = fmaxf(m_old, top + (Lazy<F8>::kLog2 - Lazy<F8>::kTop));
+  if (m_new == -INFINITY) return;
+  rows->m[r] = m_new;
+  rows->neg_m[r] = -m_new;
+  rows->alpha[r] = ex2_approx(m_old - m_new);
+}
+
+// 16 columns of O times alpha.
+__device__ __noinline__ void rescale(uint32_t taddr, const float* alpha) {
+  tc_fence_after_sync();
+  uint32_t o[16];
+  tmem_ld16(taddr, o);
+  tmem_ld_wait();
+  reg_pin(o);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
+  tmem_st16(taddr, o);
+  tmem_st_wait();
+}
+
+// Barrier 1 of the softmax threads with an OR over them.
+template <int THREADS>
+__device__ __forceinline__ bool soft_bar_or(bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(any)), "n"(THREADS)
+      : "memory");
+  return r != 0;
+}
+
 // PV(i) of the share's tile i is complete (and with it all earlier ones).  Tiles
-// alternate between two barriers; a softmax warp at tile `it` knows PV(it - 3)
-// to be complete and PV(it) not to be, so that the parity of PV(it - 1) and of
-// PV(it - 2) on its barrier tells it from its neighbours.
+// alternate between two barriers; a softmax thread at tile `it` knows PV(it - 2)
+// to be complete (S(it) was issued behind it) and PV(it) not to be, so that the
+// parity of PV(it - 1) on its barrier tells it from its neighbours.
 __device__ __forceinline__ bool product_done(int i, bool ok, TreeBars* bars, uint32_t code) {
-  return ok && __all_sync(0xffffffffu, t_wait(&bars->pv_done[i & 1], (i >> 1) & 1, bars, code));
+  return ok && t_wait(&bars->pv_done[i & 1], (i >> 1) & 1, bars, code);
 }
 
 // ------------------------------------------------------------ the kernel
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
+__global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D, F8, NR>::kCtas)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                    const __grid_constant__ TreeParams p) {
   using L = TreeLayout<D, F8, NR>;
   constexpr int kSlots = L::kSlots;
   constexpr int kParts = L::kParts;
-  constexpr int kChunks = L::kOwn / 16;  // of 16 rows, of a thread
-  // x of a tile stays in registers up to 16 rows a thread; for 32 it is formed
-  // again from tensor memory for each use (held, it spilled to local memory)
-  constexpr bool kKeep = kChunks == 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -529,7 +630,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_ready[s], L::kSoft);
+      mbar_init(&bars->p_ready[s], L::kSoft / 32);
       mbar_init(&bars->pv_done[s], 1);
       bars->bad[s][0] = bars->bad[s][1] = 0;
     }
@@ -635,7 +736,10 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
     __syncwarp();
   } else if (warp == L::kMmaWarp) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    // The whole warp runs the loop, so that the compiler may keep descriptors in
+    // uniform registers; lane 0 issues.
+    {
+      const bool lead = lane == 0;
       const uint32_t sQ = smem_u32(smem + L::kQ);
       const uint32_t sP = smem_u32(smem + L::kP);
       int n = 0, it = 0, seg = 0;  // slots taken, tiles and pairs done
@@ -647,7 +751,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
           if (t >= 0) {
             // O^T += V^T P^T
             if (!(ok = t_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513))) break;
-            const uint32_t pbase = sP + (it % L::kPBufs) * L::kPBytes;
+            const uint32_t pbase = sP + (it & 1) * L::kPBytes;
             const uint32_t d = tmem + L::kOCol;
 #pragma unroll 1
             for (int c = 0; c < kParts; ++c, ++n) {
@@ -655,6 +759,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
               if (!(ok = t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514))) break;
               tc_fence_after_sync();
               const uint32_t vbase = sRing + s * L::kSlot;
+              if (!lead) continue;
               if constexpr (F8) {
                 constexpr uint32_t both_mn = idesc_e4m3_f32(D, NR) | (3u << 15);
 #pragma unroll
@@ -676,7 +781,8 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
               umma_commit(&bars->empty[s]);
             }
             if (!ok) break;
-            umma_commit(&bars->pv_done[it & 1]);
+            __syncwarp();
+            if (lead) umma_commit(&bars->pv_done[it & 1]);
             ++it;
           }
           if (t + 2 < w.n) {
@@ -689,6 +795,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
               if (!(ok = t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) break;
               tc_fence_after_sync();
               const uint32_t kbase = sRing + s * L::kSlot;
+              if (!lead) continue;
               if constexpr (F8) {
                 constexpr uint32_t idesc = idesc_e4m3_f32(128, NR);
 #pragma unroll
@@ -708,11 +815,13 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
               }
               umma_commit(&bars->empty[s]);
             }
-            if (ok) umma_commit(&bars->s_full[i & 1]);
+            __syncwarp();
+            if (ok && lead) umma_commit(&bars->s_full[i & 1]);
           }
         }
       }
-      umma_commit(&bars->drain);
+      __syncwarp();
+      if (lead) umma_commit(&bars->drain);
     }
     __syncwarp();
   } else {
@@ -722,7 +831,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
     const int tid = threadIdx.x;
     const int key = tid % kTile, group = tid / kTile;
     const int quad = warp & 3;  // its tensor-memory lanes: keys, and channels
-    const int own = group * L::kOwn, own_c = own / 16;  // first row and chunk
+    const int own = group * 16;  // first of the thread's rows
     const uint32_t tlane = tmem_addr(tmem, quad * 32, 0);
     auto soft_bar = [] { named_bar_sync(1, L::kSoft); };
     TreeRows<NR>* const both = reinterpret_cast<TreeRows<NR>*>(smem + L::kRows);
@@ -740,7 +849,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
     };
     Walk w(bars);           // the pair at hand, and from its last tile on the next one
     bool more = true;       // there is a next one
-    f32x2 l[L::kOwn / 2];   // sums of this key column, by row
+    f32x2 l[8];             // sums of this key column, by row
     // the pair in work: its length, its first row of o, its slot of partials (-1: none)
     int len = 0, end = 0;
     long long bh = 0, slot = -1;
@@ -762,25 +871,24 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
         any2 = drafts_seen(p, w.b);
         fence_proxy_async_smem();
         mbar_arrive(&bars->q_ready);
-        if (tid == 0) bars->fresh = (1u << ((have + 15) / 16)) - 1;
       }
       if (seg > 0) {
         // ---- epilogue: sums over the keys, then a channel a thread
         TreeRows<NR>* const rows = both + ((seg - 1) & 1);
         unsigned int* const note = bars->bad[(seg - 1) & 1];
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
+        {
           float y[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 z = unpack2(l[8 * c + i]);
+            const float2 z = unpack2(l[i]);
             y[2 * i] = z.x;
             y[2 * i + 1] = z.y;
           }
           const float z = sum_lanes(y);
-          if (lane < 16) rows->part[quad][own + 16 * c + lane] = z;
+          if (lane < 16) rows->part[quad][own + lane] = z;
         }
         ok = product_done(it - 1, ok, bars, 0x526);
+        __syncwarp();
         tc_fence_after_sync();
         soft_bar();
         const long long row0 = bh * p.R + rt * kTreeRows;  // of o and lse
@@ -802,10 +910,9 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
         // the first 16 lanes of each warp
         const int ch = D == 128 ? key : quad * 16 + lane;
         const bool mine = ok && (D == 128 || lane < 16);
-#pragma unroll 1
-        for (int c = own; c < min(have, own + L::kOwn); c += 16) {
+        if (own < have) {
           uint32_t o[16];
-          tmem_ld16(tlane + L::kOCol + c, o);
+          tmem_ld16(tlane + L::kOCol + own, o);
           tmem_ld_wait();
           reg_pin(o);
           if (bad && mine) {
@@ -822,21 +929,21 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
               if (isfinite(v)) continue;
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (rows->seen[c + i] >> j & 1)
+                if (rows->seen[own + i] >> j & 1)
                   o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
             }
           }
           if (slot < 0) {
-            __nv_bfloat16* dst = p.o + (row0 + c) * D + ch;
+            __nv_bfloat16* dst = p.o + (row0 + own) * D + ch;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (mine && c + i < have)
-                dst[i * D] = __float2bfloat16_rn(__uint_as_float(o[i]) * rows->inv[c + i]);
+              if (mine && own + i < have)
+                dst[i * D] = __float2bfloat16_rn(__uint_as_float(o[i]) * rows->inv[own + i]);
           } else {
-            float* dst = p.part_o + (slot * p.prow + c) * D + ch;
+            float* dst = p.part_o + (slot * p.prow + own) * D + ch;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (mine && c + i < have) dst[i * D] = __uint_as_float(o[i]);
+              if (mine && own + i < have) dst[i * D] = __uint_as_float(o[i]);
           }
         }
       } else {
@@ -862,184 +969,99 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
       int len3 = 0;
       if (tid == 0 && more) len3 = w.b == b ? len : seq_len(p, w.b);
 #pragma unroll
-      for (int r = 0; r < L::kOwn / 2; ++r) l[r] = 0;
+      for (int r = 0; r < 8; ++r) l[r] = 0;
 
+      const int first_edge = (len - (pos - key)) / kTile;  // first tile past the committed tokens
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t, ++it, pos += kTile) {
         float ks = 1.0f, ev = 0.0f, wv = 1.0f;
-        if constexpr (F8) {
-          // 2^k_j, e_j and 2^-e_j; bytes of rows that are not there stay finite
-          const int e = min(max(static_cast<int>(vb), 1), 253) - 127;
+        if constexpr (F8) {  // 2^k_j, e_j and 2^-e_j
           ks = __uint_as_float(kb << 23);
-          ev = static_cast<float>(e);
-          wv = pow2_of(-e);
+          ev = __uint_as_float(0x4b000000u | vb) - 8388735.0f;  // 2^23 + 127
+          wv = __uint_as_float((254u - vb) << 23);
         }
         if (t + 1 < tiles) load_scales(bh, pos + kTile, end);
-        ok = ok && __all_sync(0xffffffffu, t_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, 0x522));
-        // ---- which rows see this key: bit r of the thread's own rows
+        ok = ok && t_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, 0x522);
+        // ---- which rows see this key
         uint32_t hidden = 0;
-        if (pos - key + kTile > len) {
+        if (t >= first_edge) {
           // V(t) in the order of loads.  With S(it) and PV(it - 1) complete, so are
           // all loads that its slot had before: the parity is V(t)'s.
           const int v = n + kParts * (2 + t + min(t, tiles - 2)) + key / L::kVKeys;
           if (t > 0) ok = product_done(it - 1, ok, bars, 0x523);
-          ok = ok && __all_sync(0xffffffffu, t_wait(&bars->full[v % kSlots], (v / kSlots) & 1,
-                                                    bars, 0x521));
+          ok = ok && t_wait(&bars->full[v % kSlots], (v / kSlots) & 1, bars, 0x521);
+          __syncwarp();
           if (ok && group == 0)
             clean_values<L::kAtom, kParts, F8>(
                 smem + L::kRing + (v % kSlots) * L::kSlot + (key % L::kVKeys) * L::kAtom,
                 L::kVKeys * 128, pos, len, end, any, bars->bad[seg & 1]);
-          if (pos >= end) {
-            hidden = 0xffffffffu;
-          } else if (pos >= len) {
-            const int j = pos - len;
-#pragma unroll 4
-            for (int r = 0; r < L::kOwn; ++r)
-              hidden |= (rows->seen[own + r] >> j & 1 ? 0u : 1u) << r;
+          if (pos >= len) hidden = pos < end ? hidden_rows(rows->seen + own, pos - len) : 0xffffu;
+          if (hidden == 0xffffu) {  // perhaps never written: finite scales for P = 0
+            ks = wv = 1.0f;
+            ev = 0.0f;
           }
+          __syncwarp();
         }
-        // ---- x = t - M of this key for 16 rows (chunk c)
+        // ---- x = t - M of this key for the thread's rows
         tc_fence_after_sync();
-        const f32x2 ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
-        auto form = [&](int c0, f32x2* x) {
-          const int c = own_c + c0;
-          uint32_t s[16];
-          tmem_ld16(tlane + (it & 1) * NR + 16 * c, s);
-          tmem_ld_wait();
-          reg_pin(s);
-#pragma unroll
-          for (int r = 0; r < 8; r += 2) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&rows->f[16 * c + 2 * r]);
-            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&rows->neg_m[16 * c + 2 * r]);
-            const f32x2 a = pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1]));
-            const f32x2 b = pack2(__uint_as_float(s[2 * r + 2]), __uint_as_float(s[2 * r + 3]));
-            if constexpr (F8) {
-              x[r] = add2(fma2(mul2(a, f.x), ks2, ev2), m.x);
-              x[r + 1] = add2(fma2(mul2(b, f.y), ks2, ev2), m.y);
-            } else {
-              x[r] = fma2(a, f.x, m.x);
-              x[r + 1] = fma2(b, f.y, m.y);
-            }
-          }
-          if (hidden) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              float2 y = unpack2(x[r]);
-              if (hidden >> (16 * c0 + 2 * r) & 1) y.x = -INFINITY;
-              if (hidden >> (16 * c0 + 2 * r + 1) & 1) y.y = -INFINITY;
-              x[r] = pack2(y.x, y.y);
-            }
-          }
-        };
+        const uint32_t scol = tlane + (it & 1) * NR + own;
         f32x2 x[8];
-        unsigned int grown = 0;
-        const unsigned int fresh = bars->fresh;
-#pragma unroll 1
-        for (bool moved = false;; moved = true) {
+        form_scores<F8>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
+        if (hidden) hide_rows(x, hidden);
+        float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            form(c, x);
-            float mx = -INFINITY;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const float2 y = unpack2(x[r]);
-              mx = fmax3f(mx, y.x, y.y);
-            }
-            if (__any_sync(0xffffffffu, mx > Lazy<F8>::kTop || (fresh >> (own_c + c) & 1)))
-              grown |= 1u << (own_c + c);
-          }
-          if (moved) break;
-          if (lane == 0) bars->over[it & 1][warp] = static_cast<uint8_t>(grown);
-          if (tid == 0 && t == 0 && more) {
-            bars->next_len[(seg + 1) & 1] = len3;
-            bars->next_tiles[(seg + 1) & 1] = (min(len3 + p.T, p.cap) + kTile - 1) / kTile;
-          }
+        for (int r = 0; r < 8; ++r) {
+          const float2 y = unpack2(x[r]);
+          mx = fmax3f(mx, y.x, y.y);
+        }
+        if (tid == 0 && t == 0 && more) {  // read behind this barrier, after the last tile
+          bars->next_len[(seg + 1) & 1] = len3;
+          bars->next_tiles[(seg + 1) & 1] = (min(len3 + p.T, p.cap) + kTile - 1) / kTile;
+        }
+        if (soft_bar_or<L::kSoft>(mx > Lazy<F8>::kTop)) {
+          // ---- some row grew: new references from the maxima over the CTA's keys
+          row_maxima<F8>(scol, rows->f + own, ks, ev, hidden, rows->part[quad] + own);
           soft_bar();
-          {
-            const uint2 o = *reinterpret_cast<const uint2*>(bars->over[it & 1]);
-            grown = L::kGroups == 2 ? o.x | o.y : o.x;
-            grown = (grown | grown >> 8 | grown >> 16 | grown >> 24) & 0xffu;
-          }
-          if (!grown) break;
-          // ---- new references where a row grew: maxima over the CTA's keys
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (!(grown >> (own_c + c) & 1)) continue;
-            if (!kKeep) form(c, x);
-            float top = -INFINITY;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const float2 y = unpack2(x[r / 2]);
-              const float z = redux_max(r & 1 ? y.y : y.x);
-              if (lane == r) top = z;
-            }
-            if (lane < 16) rows->part[quad][own + 16 * c + lane] = top;
-          }
+          if (tid < NR) new_reference<F8, NR>(rows, tid, have);
           soft_bar();
-          if (tid < have && (grown >> (tid / 16) & 1)) {
-            const float top = fmaxf(fmaxf(rows->part[0][tid], rows->part[1][tid]),
-                                    fmaxf(rows->part[2][tid], rows->part[3][tid]));
-            const float m_old = rows->m[tid];
-            const float m_new = fmaxf(m_old, top - rows->neg_m[tid] + (Lazy<F8>::kLog2 - Lazy<F8>::kTop));
-            rows->m[tid] = m_new;
-            rows->neg_m[tid] = m_new == -INFINITY ? 0.0f : -m_new;
-            rows->alpha[tid] = m_new == -INFINITY ? 1.0f : ex2_approx(m_old - m_new);
-          } else if (tid >= have && tid < NR) {
-            rows->alpha[tid] = 1.0f;
-          }
-          if (tid == 0) bars->fresh = 0;
-          soft_bar();
-          if (tid < have && rows->m[tid] == -INFINITY) atomicOr(&bars->fresh, 1u << (tid / 16));
           if (t > 0) {
             // PV(it - 1) must be done before O is rescaled
             ok = product_done(it - 1, ok, bars, 0x524);
-            tc_fence_after_sync();
+            __syncwarp();
+            rescale(tlane + L::kOCol + own, rows->alpha + own);
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              if (!(grown >> (own_c + c) & 1)) continue;
-              const float* al = rows->alpha + own + 16 * c;
-              uint32_t o[16];
-              tmem_ld16(tlane + L::kOCol + own + 16 * c, o);
-              tmem_ld_wait();
-              reg_pin(o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                l[8 * c + i] = mul2(l[8 * c + i], pack2(al[2 * i], al[2 * i + 1]));
-                o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * al[2 * i]);
-                o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * al[2 * i + 1]);
-              }
-              tmem_st16(tlane + L::kOCol + own + 16 * c, o);
+            for (int r = 0; r < 8; r += 2) {
+              const ulonglong2 al = *reinterpret_cast<const ulonglong2*>(&rows->alpha[own + 2 * r]);
+              l[r] = mul2(l[r], al.x);
+              l[r + 1] = mul2(l[r + 1], al.y);
             }
-            tmem_st_wait();
           }
-          if (!kKeep) break;
+          form_scores<F8>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
+          if (hidden) hide_rows(x, hidden);
         }
-        // ---- P = 2^x over the P buffer that PV(it - kPBufs) has read
-        if (it >= L::kPBufs) ok = product_done(it - L::kPBufs, ok, bars, 0x525);
-        uint8_t* pb = smem + L::kP + (it % L::kPBufs) * L::kPBytes + key * 16;
-        const f32x2 wv2 = pack2(wv, wv);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (!kKeep) form(c, x);
+        // ---- P = 2^x over the P buffer that PV(it - 2) has read: it is complete, for
+        // S(it) was issued behind it
+        {
+          const f32x2 wv2 = pack2(wv, wv);
           uint32_t hi[8], lo[F8 ? 4 : 1];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 a = unpack2(x[2 * i]), b = unpack2(x[2 * i + 1]);
             const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
             const float p2 = ex2_approx(b.x), p3 = ex2_approx(b.y);
-            f32x2* const lc = l + 8 * c + 2 * i;
             if constexpr (F8) {
-              lc[0] = fma2(pack2(p0, p1), wv2, lc[0]);
-              lc[1] = fma2(pack2(p2, p3), wv2, lc[1]);
+              l[2 * i] = fma2(pack2(p0, p1), wv2, l[2 * i]);
+              l[2 * i + 1] = fma2(pack2(p2, p3), wv2, l[2 * i + 1]);
               split4(p0, p1, p2, p3, hi[i], lo[i]);
             } else {
-              lc[0] = add2(lc[0], pack2(p0, p1));
-              lc[1] = add2(lc[1], pack2(p2, p3));
+              l[2 * i] = add2(l[2 * i], pack2(p0, p1));
+              l[2 * i + 1] = add2(l[2 * i + 1], pack2(p2, p3));
               hi[2 * i] = pack_bf16x2(p0, p1);
               hi[2 * i + 1] = pack_bf16x2(p2, p3);
             }
           }
-          uint8_t* const at = pb + (own_c + c) * (16 / L::kUnit) * (kTile * 16);
+          uint8_t* const at = smem + L::kP + (it & 1) * L::kPBytes +
+                              (own / L::kUnit) * (kTile * 16) + key * 16;
           *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           if constexpr (F8)
             *reinterpret_cast<uint4*>(at + L::kPPiece) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -1048,7 +1070,8 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, 2)
         }
         fence_proxy_async_smem();  // P, and cleaned values
         tc_fence_before_sync();
-        mbar_arrive(&bars->p_ready[it & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_ready[it & 1]);
       }
       n += 2 * kParts * tiles;
     }
@@ -1174,7 +1197,7 @@ cudaError_t launch_tile(const TreeParams& p, const CUtensorMap& tk, const CUtens
 template <int D, bool F8>
 cudaError_t launch_type(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t s) {
-  const TreePlan plan = tree_plan(a.c, a.Hq, a.T, 2 * a.num_sms);
+  const TreePlan plan = tree_plan(a.c, a.Hq, a.T, a.num_sms);
   TreeParams p{};
   p.q = static_cast<const uint4*>(a.q);
   p.lens = a.lens;
