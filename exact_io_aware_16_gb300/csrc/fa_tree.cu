@@ -30,8 +30,8 @@
 //     tensor core takes them: K0 K1 V0 K2 V1 ...;
 //   * one issues S^T(t + 2) behind PV(t): S^T has two buffers in tensor memory;
 //   * four warps for every 16 rows, a key a thread: softmax over the columns, P^T to shared
-//     memory ([key][row] in 16-byte units, an operand as it lies), epilogue with
-//     a channel a thread.  A row's reference M is shared by the CTA; one
+//     memory ([key][row], an operand as it lies), epilogue with a channel a thread.
+//      A row's reference M is shared by the CTA; one
 //     barrier a tile tells in which 16 rows some score passed it by more than
 //     Lazy binades, and only there maxima are exchanged and O is rescaled.
 //     The next pair's queries are stored during a pair's last tile, so that its
@@ -117,8 +117,8 @@ struct TreeLayout {
   static constexpr int kThreads = kSoft + 64;
   static constexpr int kPieces = F8 ? 2 : 1;                   // of q and of P
   static constexpr uint32_t kQPiece = NR * kRow;               // 64 columns at a time for bf16
-  static constexpr int kUnit = F8 ? 16 : 8;                    // rows in 16 bytes of P
-  static constexpr uint32_t kPPiece = kTile * NR * (F8 ? 1 : 2);
+  static constexpr uint32_t kPRow = NR * (F8 ? 1 : 2);         // bytes of a key's P: 16 .. 128
+  static constexpr uint32_t kPPiece = kTile * kPRow;
   static constexpr uint32_t kPBytes = kPieces * kPPiece;
   static constexpr int kCtas = tree_ctas(NR);                  // an SM
   static constexpr uint32_t kRoom = (kCtas == 2 ? 113u : 227u) * 1024 - 1024 - 1024 -
@@ -167,6 +167,20 @@ __device__ __noinline__ bool t_wait_loop(uint64_t* bar, uint32_t parity, TreeBar
 }
 __device__ __forceinline__ bool t_wait(uint64_t* bar, uint32_t parity, TreeBars* b, uint32_t code) {
   return mbar_try_wait(smem_u32(bar), parity) || t_wait_loop(bar, parity, b, code);
+}
+
+// The same wait by a whole warp, with one answer.
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, TreeBars* b, uint32_t code) {
+  return __all_sync(0xffffffffu, t_wait(bar, parity, b, code));
+}
+
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // Keys of sequence b that exist: its committed tokens and its drafts.
@@ -327,28 +341,27 @@ __device__ __forceinline__ float redux_max(float x) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Address of 16-byte unit c of row r in a swizzled tile of `atom`-byte rows.
+// Address of 16-byte unit c of row r in a tile of ATOM-byte rows, swizzled over the
+// row (128, 64 or 32 bytes; 16: nothing to swizzle).
 template <uint32_t ATOM>
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
-  const uint32_t x = ATOM == 128 ? (c ^ (r & 7u)) : (c ^ ((r >> 1) & 3u));
-  return r * ATOM + x * 16u;
+  constexpr uint32_t kUnits = ATOM / 16;
+  return r * ATOM + (c ^ (r / (8 / kUnits) % kUnits)) * 16u;
 }
 
-// sdesc_sw128 with the swizzle of 64-byte rows (layout 4).
-__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t smem_addr, uint32_t lbo_bytes,
-                                               uint32_t sbo_bytes) {
-  return (sdesc_sw128(smem_addr, lbo_bytes, sbo_bytes) & ~(7ull << 61)) | (4ull << 61);
-}
+// sdesc_sw128 with the swizzle of ATOM-byte rows.
 template <uint32_t ATOM>
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return ATOM == 128 ? sdesc_sw128(addr, lbo, sbo) : sdesc_sw64(addr, lbo, sbo);
+  constexpr uint64_t kLayout = ATOM == 128 ? 2 : ATOM == 64 ? 4 : ATOM == 32 ? 6 : 0;
+  return (sdesc_sw128(addr, lbo, sbo) & ~(7ull << 61)) | (kLayout << 61);
 }
 
-// sdesc_sw128 without a swizzle (layout 0), MN-major: 16-byte units of M/N,
-// eight K rows of a unit in 128 bytes; `kstep` bytes between groups of eight K
-// rows, `mstep` bytes between units.
-__device__ __forceinline__ uint64_t sdesc_plain_mn(uint32_t addr, uint32_t kstep, uint32_t mstep) {
-  return sdesc_sw128(addr, kstep, mstep) & ~(7ull << 61);
+// P of a piece, [key][row] (MN-major): one swizzled row of ATOM bytes a key, groups
+// of eight keys one behind the other.  Rows of 16 bytes are not swizzled, and take
+// the distance between the groups in the other field.
+template <uint32_t ATOM>
+__device__ __forceinline__ uint64_t sdesc_p(uint32_t addr) {
+  return sdesc<ATOM>(addr, ATOM == 16 ? 8 * ATOM : 16, 8 * ATOM);
 }
 
 // ------------------------------------------------------------ query rows
@@ -736,30 +749,31 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
     __syncwarp();
   } else if (warp == L::kMmaWarp) {
     // ------------------------------------------------ MMA issuer
-    // The whole warp runs the loop, so that the compiler may keep descriptors in
-    // uniform registers; lane 0 issues.
+    // The whole warp runs the loop on values that are uniform by construction
+    // (votes and reductions), so that descriptors live in uniform registers,
+    // where the instruction wants them; one elected lane issues.
     {
-      const bool lead = lane == 0;
       const uint32_t sQ = smem_u32(smem + L::kQ);
       const uint32_t sP = smem_u32(smem + L::kP);
       int n = 0, it = 0, seg = 0;  // slots taken, tiles and pairs done
       bool ok = true;
-      for (Walk w(bars); ok && w.valid(p); w.next(p), ++seg) {
-        if (!(ok = t_wait(&bars->q_ready, seg & 1, bars, 0x512))) break;
+      for (Walk w(bars); __all_sync(0xffffffffu, ok && w.valid(p)); w.next(p), ++seg) {
+        const int tiles = __reduce_max_sync(0xffffffffu, w.n);
+        if (!(ok = all_wait(&bars->q_ready, seg & 1, bars, 0x512))) break;
 #pragma unroll 1
-        for (int t = -2; ok && t < w.n; ++t) {
+        for (int t = -2; ok && t < tiles; ++t) {
           if (t >= 0) {
             // O^T += V^T P^T
-            if (!(ok = t_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513))) break;
+            if (!(ok = all_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513))) break;
             const uint32_t pbase = sP + (it & 1) * L::kPBytes;
             const uint32_t d = tmem + L::kOCol;
 #pragma unroll 1
             for (int c = 0; c < kParts; ++c, ++n) {
               const int s = n % kSlots;
-              if (!(ok = t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514))) break;
+              if (!(ok = all_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514))) break;
               tc_fence_after_sync();
               const uint32_t vbase = sRing + s * L::kSlot;
-              if (!lead) continue;
+              if (!elect_one()) continue;
               if constexpr (F8) {
                 constexpr uint32_t both_mn = idesc_e4m3_f32(D, NR) | (3u << 15);
 #pragma unroll
@@ -767,7 +781,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
                   const int piece = x / (kTile / 32), kk = x % (kTile / 32);
                   const uint32_t idesc = both_mn | (piece ? 1u << 10 : 0u);  // B: e4m3, e5m2
                   umma_ss_f8(d, sdesc<L::kAtom>(vbase + kk * 32 * L::kAtom, 16, 8 * L::kAtom),
-                             sdesc_plain_mn(pbase + piece * L::kPPiece + kk * 512, 128, kTile * 16),
+                             sdesc_p<L::kPRow>(pbase + piece * L::kPPiece + kk * 32 * L::kPRow),
                              idesc, (t > 0 || x > 0) ? 1u : 0u);
                 }
               } else {
@@ -775,27 +789,27 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
 #pragma unroll
                 for (int kk = 0; kk < L::kVKeys / 16; ++kk)
                   umma_ss(d, sdesc_sw128(vbase + kk * 2048, L::kVKeys * 128, 1024),
-                          sdesc_plain_mn(pbase + (c * (L::kVKeys / 16) + kk) * 256, 128, kTile * 16),
+                          sdesc_p<L::kPRow>(pbase + (c * L::kVKeys + kk * 16) * L::kPRow),
                           idesc, (t > 0 || c > 0 || kk > 0) ? 1u : 0u);
               }
               umma_commit(&bars->empty[s]);
             }
             if (!ok) break;
             __syncwarp();
-            if (lead) umma_commit(&bars->pv_done[it & 1]);
+            if (elect_one()) umma_commit(&bars->pv_done[it & 1]);
             ++it;
           }
-          if (t + 2 < w.n) {
+          if (t + 2 < tiles) {
             // S^T of tile t + 2 = K Q^T, into the buffer that softmax(t) has read
             const int i = it + (t < 0 ? t + 2 : 1);
             const uint32_t d = tmem + (i & 1) * NR;
 #pragma unroll 1
             for (int c = 0; c < kParts; ++c, ++n) {
               const int s = n % kSlots;
-              if (!(ok = t_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) break;
+              if (!(ok = all_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) break;
               tc_fence_after_sync();
               const uint32_t kbase = sRing + s * L::kSlot;
-              if (!lead) continue;
+              if (!elect_one()) continue;
               if constexpr (F8) {
                 constexpr uint32_t idesc = idesc_e4m3_f32(128, NR);
 #pragma unroll
@@ -816,12 +830,12 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               umma_commit(&bars->empty[s]);
             }
             __syncwarp();
-            if (ok && lead) umma_commit(&bars->s_full[i & 1]);
+            if (ok && elect_one()) umma_commit(&bars->s_full[i & 1]);
           }
         }
       }
       __syncwarp();
-      if (lead) umma_commit(&bars->drain);
+      if (elect_one()) umma_commit(&bars->drain);
     }
     __syncwarp();
   } else {
@@ -1060,13 +1074,17 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               hi[2 * i + 1] = pack_bf16x2(p2, p3);
             }
           }
-          uint8_t* const at = smem + L::kP + (it & 1) * L::kPBytes +
-                              (own / L::kUnit) * (kTile * 16) + key * 16;
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if constexpr (F8)
-            *reinterpret_cast<uint4*>(at + L::kPPiece) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          else
-            *reinterpret_cast<uint4*>(at + kTile * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          uint8_t* const at = smem + L::kP + (it & 1) * L::kPBytes;
+          if constexpr (F8) {
+            const uint32_t to = swizzled<L::kPRow>(key, group);
+            *reinterpret_cast<uint4*>(at + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + L::kPPiece + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, 2 * group)) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, 2 * group + 1)) =
+                make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          }
         }
         fence_proxy_async_smem();  // P, and cleaned values
         tc_fence_before_sync();
