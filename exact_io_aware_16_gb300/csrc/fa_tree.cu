@@ -39,8 +39,8 @@
 //
 // e4m3 operands: kind::f8f6f4 takes the cache as it lies in memory.  Two e4m3
 // pieces of 4 significant bits hold the 8 bits of a bf16 query exactly (its row
-// scaled by a power of two into 448), and an e4m3 and an e5m2 piece a probability
-// to 2^-7: S and O accumulate both pieces, twice the MMAs at twice the bf16 rate.  The scales of
+// scaled by a power of two into 448), and a probability to 2^-8.  S accumulates both
+// pieces; those of P are columns side by side, so that V is read once.  The scales of
 // keys and values join in the softmax: with e_j the exponent of value row j, the
 // thread forms t_j = scale log2(e) 2^(k_j) S_j + e_j, keeps M = max t_j, and
 // gives P_j = 2^(t_j - M) to the product with the codes, while the sum takes
@@ -72,12 +72,14 @@ constexpr int kPairCost = 2;  // units of a pair besides its tiles
 constexpr float kUnseen = 1e38f;
 
 // A row's accumulator is rescaled only when its maximum grows by more than
-// kLog2 binades.  bf16 has the range for any P; the e4m3 pieces of P are scaled
-// so that 2^kLog2 times the largest P at the last rescale is 448, the largest code.
+// kLog2 binades.  bf16 has the range for any P; for e4m3 P is scaled so that 2^kLog2
+// times the largest P at the last rescale is 1.75, 448 in the units of its pieces.
 template <bool F8>
 struct Lazy {
   static constexpr float kLog2 = F8 ? 6.0f : 8.0f;
-  static constexpr float kTop = F8 ? 8.80735492f : 8.0f;  // log2 of the largest P
+  static constexpr float kTop = F8 ? 0.80735492f : 8.0f;      // log2 of the largest P
+  static constexpr float kOScale = F8 ? 0.00390625f : 1.0f;   // unit of the high pieces
+  [[maybe_unused]] static constexpr float kLowScale = 0.125f;  // of the low pieces in it
 };
 
 struct TreeBars {
@@ -95,7 +97,7 @@ struct TreeBars {
 template <int NR>
 struct TreeRows {
   unsigned long long seen[NR];  // mask row
-  float f[NR];      // scale log2(e), times 2^e of the query row for e4m3
+  float f[NR];      // 2^e of the query row (e4m3)
   float m[NR];      // reference exponent, -inf before the first key
   float neg_m[NR];  // its negative: kUnseen before the first key, -inf for rows past R
   float alpha[NR];  // of the last move
@@ -115,11 +117,10 @@ struct TreeLayout {
   static constexpr int kSoft = kTile * kGroups;
   static constexpr int kTmaWarp = kSoft / 32, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = kSoft + 64;
-  static constexpr int kPieces = F8 ? 2 : 1;                   // of q and of P
+  static constexpr int kPieces = F8 ? 2 : 1;                   // of q, and of P along its row
   static constexpr uint32_t kQPiece = NR * kRow;               // 64 columns at a time for bf16
-  static constexpr uint32_t kPRow = NR * (F8 ? 1 : 2);         // bytes of a key's P: 16 .. 128
-  static constexpr uint32_t kPPiece = kTile * kPRow;
-  static constexpr uint32_t kPBytes = kPieces * kPPiece;
+  static constexpr uint32_t kPRow = 2 * NR;                    // bytes of a key's P
+  static constexpr uint32_t kPBytes = kTile * kPRow;
   static constexpr int kCtas = tree_ctas(NR);                  // an SM
   static constexpr uint32_t kRoom = (kCtas == 2 ? 113u : 227u) * 1024 - 1024 - 1024 -
                                     2 * sizeof(TreeRows<NR>) - kPieces * kQPiece - 2 * kPBytes;
@@ -135,9 +136,11 @@ struct TreeLayout {
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kRows % 16 == 0 && kBar % 8 == 0, "aligned");
   static constexpr uint32_t kSmem = kUsed > 81920u ? kUsed : 81920u;  // never three CTAs
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "fits");
-  // tensor memory: S^T twice, O^T
+  // tensor memory: S^T twice, O^T (of each piece)
   static constexpr uint32_t kOCol = 2 * NR;
+  static constexpr uint32_t kOCols = kPieces * NR;
   static constexpr uint32_t kCols = NR == 16 ? 64 : NR == 32 ? 128 : 256;
+  static_assert(kOCol + kOCols <= kCols, "columns");
 };
 static_assert(sizeof(TreeBars) <= 1024, "barrier block");
 
@@ -261,23 +264,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 
 // ------------------------------------------------------------ conversions
-// Four fp32 P of 0 .. 448 as two pieces each: a word of e4m3 (high) and a word of
-// e5m2 (the rest).  fp16 times 2^-8 has e4m3's exponent field, so that bits 14..7
-// of the rounded (half up) fp16 are the code, subnormal ones included; the rest R
-// is exact in fp16, and its upper byte, rounded the same way, is e5m2.  R is at
-// most 2^-4 of P and its code off by at most 2^-3 of R: 2^-7 of P (2^-9.6 in the
-// mean square, like bf16's 2^-9.3), down to P of 2^-6; e5m2 keeps R's
-// leading bits through seven more binades than e4m3 would, which is the room that
-// kLazy takes.  Shifts, adds and byte permutes run at four times the rate of the
-// e4m3 conversions.  (A NaN is lost here: the row's sum carries it.)
+// Four fp32 P of 0 .. 1.75 as two e4m3 pieces each: a word of high pieces of 2^8 P,
+// and a word of the rests times 2^3 (their product has accumulator columns of its
+// own).  fp16 P has the exponent field of e4m3 2^8 P, so that bits 14..7 of the
+// fp16 are the code cut to 4 significant bits, subnormal ones included.  The rest R
+// is exact in fp16, below 2^-3 of P's binade, and rounded (half up) to its 4 bits the
+// same way: 2^-8 of P together as in bf16, down to 2^8 P of 2^-6, and 2^-13 below: the
+// room that Lazy takes.  Masks, shifts and byte permutes run at four times the rate
+// of the e4m3 conversions.  (A NaN is lost here: the row's sum carries it.)
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x0, x1);
-  const __half2 s = __hmul2(h, __half2half2(__ushort_as_half(0x1c00)));  // 2^-8
-  const uint32_t c = (*reinterpret_cast<const uint32_t*>(&s) + 0x00400040u) & 0x7f807f80u;
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&c),
-                            __half2half2(__ushort_as_half(0xdc00)), h);  // -2^8
-  hi = c << 1;
-  lo = *reinterpret_cast<const uint32_t*>(&r) + 0x00800080u;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&h), c = w & 0x7f807f80u;
+  const __half2 r = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&c)),
+                            __half2half2(__ushort_as_half(0x4800)));  // 2^3
+  hi = w << 1;
+  lo = *reinterpret_cast<const uint32_t*>(&r) * 2 + 0x00800080u;
 }
 __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t& hi,
                                        uint32_t& lo) {
@@ -342,7 +343,7 @@ __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w <<
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // Address of 16-byte unit c of row r in a tile of ATOM-byte rows, swizzled over the
-// row (128, 64 or 32 bytes; 16: nothing to swizzle).
+// row (128, 64 or 32 bytes).
 template <uint32_t ATOM>
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
   constexpr uint32_t kUnits = ATOM / 16;
@@ -352,16 +353,8 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
 // sdesc_sw128 with the swizzle of ATOM-byte rows.
 template <uint32_t ATOM>
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  constexpr uint64_t kLayout = ATOM == 128 ? 2 : ATOM == 64 ? 4 : ATOM == 32 ? 6 : 0;
+  constexpr uint64_t kLayout = ATOM == 128 ? 2 : ATOM == 64 ? 4 : 6;
   return (sdesc_sw128(addr, lbo, sbo) & ~(7ull << 61)) | (kLayout << 61);
-}
-
-// P of a piece, [key][row] (MN-major): one swizzled row of ATOM bytes a key, groups
-// of eight keys one behind the other.  Rows of 16 bytes are not swizzled, and take
-// the distance between the groups in the other field.
-template <uint32_t ATOM>
-__device__ __forceinline__ uint64_t sdesc_p(uint32_t addr) {
-  return sdesc<ATOM>(addr, ATOM == 16 ? 8 * ATOM : 16, 8 * ATOM);
 }
 
 // ------------------------------------------------------------ query rows
@@ -370,7 +363,7 @@ __device__ __forceinline__ uint64_t sdesc_p(uint32_t addr) {
 // factor takes 2^e.
 template <int D, bool F8, int NR>
 __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, const uint4* q,
-                                              int have, float scale_log2) {
+                                              int have) {
   using L = TreeLayout<D, F8, NR>;
   constexpr int kPer = L::kSoft / NR;   // threads a row
   constexpr int kGran = D / 8 / kPer;   // eight channels each
@@ -389,7 +382,6 @@ __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, c
       const int c = part * kGran + i;  // 16-byte unit of the row
       *reinterpret_cast<uint4*>(sq + (c >> 3) * (NR * 128) + swizzled<128>(r, c & 7)) = x[i];
     }
-    if (part == 0) rows->f[r] = scale_log2;
   } else {
 #pragma unroll
     for (int o = kPer / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -411,7 +403,7 @@ __device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, c
       *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(at + L::kQPiece) = make_uint2(lo[0], lo[1]);
     }
-    if (part == 0) rows->f[r] = scale_log2 * pow2_of(e);
+    if (part == 0) rows->f[r] = pow2_of(e);
   }
   if (part == 0) {
     rows->m[r] = -INFINITY;
@@ -501,8 +493,9 @@ __device__ __forceinline__ float sum_lanes(float (&x)[16]) {
   return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
-// t (without a reference: `neg_m` null) or x = t - M of a key for 16 rows.
-template <bool F8>
+// x = t - M of a key for 16 rows (t itself without M), t = scale log2(e) q.k + e.
+// ks: scale log2(e), times 2^k for e4m3.
+template <bool F8, bool M>
 __device__ __forceinline__ void form_scores(uint32_t taddr, const float* f, const float* neg_m,
                                             float ks, float ev, f32x2 (&x)[8]) {
   uint32_t s[16];
@@ -512,17 +505,17 @@ __device__ __forceinline__ void form_scores(uint32_t taddr, const float* f, cons
   const f32x2 ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
 #pragma unroll
   for (int r = 0; r < 8; r += 2) {
-    const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(f + 2 * r);
-    ulonglong2 m = make_ulonglong2(0, 0);
-    if (neg_m) m = *reinterpret_cast<const ulonglong2*>(neg_m + 2 * r);
+    ulonglong2 m = make_ulonglong2(0, 0), g = make_ulonglong2(0, 0);
+    if (M) m = *reinterpret_cast<const ulonglong2*>(neg_m + 2 * r);
+    if (F8) g = *reinterpret_cast<const ulonglong2*>(f + 2 * r);
     const f32x2 a = pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1]));
     const f32x2 b = pack2(__uint_as_float(s[2 * r + 2]), __uint_as_float(s[2 * r + 3]));
     if constexpr (F8) {
-      x[r] = add2(fma2(mul2(a, g.x), ks2, ev2), m.x);
-      x[r + 1] = add2(fma2(mul2(b, g.y), ks2, ev2), m.y);
+      x[r] = fma2(mul2(a, g.x), ks2, M ? add2(ev2, m.x) : ev2);
+      x[r + 1] = fma2(mul2(b, g.y), ks2, M ? add2(ev2, m.y) : ev2);
     } else {
-      x[r] = fma2(a, g.x, m.x);
-      x[r + 1] = fma2(b, g.y, m.y);
+      x[r] = fma2(a, ks2, m.x);
+      x[r + 1] = fma2(b, ks2, m.y);
     }
   }
 }
@@ -554,7 +547,7 @@ __device__ __noinline__ void row_maxima(uint32_t taddr, const float* f, float ks
                                         uint32_t hidden, float* out) {
   const int lane = threadIdx.x & 31;
   f32x2 t[8];
-  form_scores<F8>(taddr, f, nullptr, ks, ev, t);
+  form_scores<F8, false>(taddr, f, nullptr, ks, ev, t);
   hide_rows(t, hidden);
   float top = -INFINITY;
 #pragma unroll
@@ -582,28 +575,30 @@ __device__ __noinline__ void new_reference(TreeRows<NR>* rows, int r, int have) 
   rows->alpha[r] = ex2_approx(m_old - m_new);
 }
 
-// 16 columns of O times alpha.
-__device__ __noinline__ void rescale(uint32_t taddr, const float* alpha) {
+// 16 columns of O, `pieces` times `stride` columns apart, times alpha.
+__device__ __noinline__ void rescale(uint32_t taddr, int pieces, int stride, const float* alpha) {
   tc_fence_after_sync();
-  uint32_t o[16];
-  tmem_ld16(taddr, o);
-  tmem_ld_wait();
-  reg_pin(o);
+#pragma unroll 1
+  for (int k = 0; k < pieces; ++k) {
+    uint32_t o[16];
+    tmem_ld16(taddr + k * stride, o);
+    tmem_ld_wait();
+    reg_pin(o);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
-  tmem_st16(taddr, o);
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
+    tmem_st16(taddr + k * stride, o);
+  }
   tmem_st_wait();
 }
 
-// Barrier 1 of the softmax threads with an OR over them.
-template <int THREADS>
-__device__ __forceinline__ bool soft_bar_or(bool any) {
+// Barrier `id` of a softmax group with an OR over it.
+__device__ __forceinline__ bool group_bar_or(int id, bool any) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(any)), "n"(THREADS)
+      : "r"(static_cast<uint32_t>(any)), "r"(id), "n"(kTile)
       : "memory");
   return r != 0;
 }
@@ -775,21 +770,19 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               const uint32_t vbase = sRing + s * L::kSlot;
               if (!elect_one()) continue;
               if constexpr (F8) {
-                constexpr uint32_t both_mn = idesc_e4m3_f32(D, NR) | (3u << 15);
+                // both pieces' columns at once; both operands MN-major
+                constexpr uint32_t idesc = idesc_e4m3_f32(D, 2 * NR) | (3u << 15);
 #pragma unroll
-                for (int x = 0; x < 2 * (kTile / 32); ++x) {
-                  const int piece = x / (kTile / 32), kk = x % (kTile / 32);
-                  const uint32_t idesc = both_mn | (piece ? 1u << 10 : 0u);  // B: e4m3, e5m2
+                for (int kk = 0; kk < kTile / 32; ++kk)
                   umma_ss_f8(d, sdesc<L::kAtom>(vbase + kk * 32 * L::kAtom, 16, 8 * L::kAtom),
-                             sdesc_p<L::kPRow>(pbase + piece * L::kPPiece + kk * 32 * L::kPRow),
-                             idesc, (t > 0 || x > 0) ? 1u : 0u);
-                }
+                             sdesc<L::kPRow>(pbase + kk * 32 * L::kPRow, 16, 8 * L::kPRow), idesc,
+                             (t > 0 || kk > 0) ? 1u : 0u);
               } else {
                 constexpr uint32_t idesc = idesc_bf16_f32(D, NR, true, true);
 #pragma unroll
                 for (int kk = 0; kk < L::kVKeys / 16; ++kk)
                   umma_ss(d, sdesc_sw128(vbase + kk * 2048, L::kVKeys * 128, 1024),
-                          sdesc_p<L::kPRow>(pbase + (c * L::kVKeys + kk * 16) * L::kPRow),
+                          sdesc<L::kPRow>(pbase + (c * L::kVKeys + kk * 16) * L::kPRow, 16, 8 * L::kPRow),
                           idesc, (t > 0 || c > 0 || kk > 0) ? 1u : 0u);
               }
               umma_commit(&bars->empty[s]);
@@ -875,16 +868,26 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       const int len2 = more ? bars->next_len[seg & 1] : 0;
       const long long bh2 = static_cast<long long>(w.b) * p.Hkv + w.h;
       unsigned long long any2 = 0;
+      int len3 = 0;  // of the pair after the next one: thread 0's view of it is everybody's
+      bool more3 = false;
       if (more) {
         TreeRows<NR>* const rows = both + (seg & 1);
         w.set(bars->next_tiles[seg & 1]);
+        Walk w3 = w;
+        w3.next(p);
+        more3 = w3.inside();
+        if (tid == 0 && more3) len3 = w3.b == w.b ? len2 : seq_len(p, w3.b);
         load_scales(bh2, w.t0 * kTile + key, min(len2 + p.T, p.cap));
         store_queries<D, F8, NR>(smem + L::kQ, rows, p.q + (bh2 * p.R + rt * kTreeRows) * (D / 8),
-                                 have, p.scale_log2);
+                                 have);
         store_masks<NR>(rows, p, w.b, rt);
         any2 = drafts_seen(p, w.b);
         fence_proxy_async_smem();
         mbar_arrive(&bars->q_ready);
+      }
+      if (tid == 0 && more3) {  // read at the next turn, behind the barrier below
+        bars->next_len[(seg + 1) & 1] = len3;
+        bars->next_tiles[(seg + 1) & 1] = (min(len3 + p.T, p.cap) + kTile - 1) / kTile;
       }
       if (seg > 0) {
         // ---- epilogue: sums over the keys, then a channel a thread
@@ -910,10 +913,11 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         if (tid < NR) {
           const float sum = (rows->part[0][tid] + rows->part[1][tid]) +
                             (rows->part[2][tid] + rows->part[3][tid]);
-          rows->inv[tid] = slot >= 0 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
+          rows->inv[tid] =
+              Lazy<F8>::kOScale * (slot >= 0 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum));
           if (tid < have && ok) {
             if (slot < 0)
-              p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (log2f(sum) - rows->neg_m[tid]) * kLn2;
+              p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (log2f(sum) + rows->m[tid]) * kLn2;
             else
               p.part_ml[slot * p.prow + tid] = make_float2(rows->m[tid], sum);
           }
@@ -929,6 +933,16 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           tmem_ld16(tlane + L::kOCol + own, o);
           tmem_ld_wait();
           reg_pin(o);
+          if constexpr (F8) {
+            uint32_t lo[16];
+            tmem_ld16(tlane + L::kOCol + NR + own, lo);
+            tmem_ld_wait();
+            reg_pin(lo);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(lo[i]), Lazy<F8>::kLowScale,
+                                          __uint_as_float(o[i])));
+          }
           if (bad && mine) {
             // drafts with NaN or infinities, to the rows that see them
 #pragma unroll 1
@@ -957,7 +971,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
             float* dst = p.part_o + (slot * p.prow + own) * D + ch;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (mine && own + i < have) dst[i * D] = __uint_as_float(o[i]);
+              if (mine && own + i < have) dst[i * D] = __uint_as_float(o[i]) * Lazy<F8>::kOScale;
           }
         }
       } else {
@@ -976,21 +990,17 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       slot = w.n == w.nt ? -1 : 2ll * blockIdx.x + (w.t0 > 0 ? 0 : 1);
       const int tiles = w.n;
       int pos = w.t0 * kTile + key;
-      const int b = w.b;
       w.next(p);
-      more = w.inside();
-      // thread 0's view of the next pair's length is everybody's
-      int len3 = 0;
-      if (tid == 0 && more) len3 = w.b == b ? len : seq_len(p, w.b);
+      more = more3;
 #pragma unroll
       for (int r = 0; r < 8; ++r) l[r] = 0;
 
       const int first_edge = (len - (pos - key)) / kTile;  // first tile past the committed tokens
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t, ++it, pos += kTile) {
-        float ks = 1.0f, ev = 0.0f, wv = 1.0f;
-        if constexpr (F8) {  // 2^k_j, e_j and 2^-e_j
-          ks = __uint_as_float(kb << 23);
+        float ks = p.scale_log2, ev = 0.0f, wv = 1.0f;
+        if constexpr (F8) {  // scale log2(e) 2^k_j, e_j and 2^-e_j
+          ks *= __uint_as_float(kb << 23);
           ev = __uint_as_float(0x4b000000u | vb) - 8388735.0f;  // 2^23 + 127
           wv = __uint_as_float((254u - vb) << 23);
         }
@@ -1020,7 +1030,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         tc_fence_after_sync();
         const uint32_t scol = tlane + (it & 1) * NR + own;
         f32x2 x[8];
-        form_scores<F8>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
+        form_scores<F8, true>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
         if (hidden) hide_rows(x, hidden);
         float mx = -INFINITY;
 #pragma unroll
@@ -1028,21 +1038,17 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           const float2 y = unpack2(x[r]);
           mx = fmax3f(mx, y.x, y.y);
         }
-        if (tid == 0 && t == 0 && more) {  // read behind this barrier, after the last tile
-          bars->next_len[(seg + 1) & 1] = len3;
-          bars->next_tiles[(seg + 1) & 1] = (min(len3 + p.T, p.cap) + kTile - 1) / kTile;
-        }
-        if (soft_bar_or<L::kSoft>(mx > Lazy<F8>::kTop)) {
-          // ---- some row grew: new references from the maxima over the CTA's keys
+        if (group_bar_or(2 + group, mx > Lazy<F8>::kTop)) {
+          // ---- some row grew: new references from the maxima over the group's keys
           row_maxima<F8>(scol, rows->f + own, ks, ev, hidden, rows->part[quad] + own);
-          soft_bar();
-          if (tid < NR) new_reference<F8, NR>(rows, tid, have);
-          soft_bar();
+          named_bar_sync(2 + group, kTile);
+          if (key < 16) new_reference<F8, NR>(rows, own + key, have);
+          named_bar_sync(2 + group, kTile);
           if (t > 0) {
             // PV(it - 1) must be done before O is rescaled
             ok = product_done(it - 1, ok, bars, 0x524);
             __syncwarp();
-            rescale(tlane + L::kOCol + own, rows->alpha + own);
+            rescale(tlane + L::kOCol + own, L::kPieces, NR, rows->alpha + own);
 #pragma unroll
             for (int r = 0; r < 8; r += 2) {
               const ulonglong2 al = *reinterpret_cast<const ulonglong2*>(&rows->alpha[own + 2 * r]);
@@ -1050,7 +1056,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               l[r + 1] = mul2(l[r + 1], al.y);
             }
           }
-          form_scores<F8>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
+          form_scores<F8, true>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
           if (hidden) hide_rows(x, hidden);
         }
         // ---- P = 2^x over the P buffer that PV(it - 2) has read: it is complete, for
@@ -1076,9 +1082,10 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           }
           uint8_t* const at = smem + L::kP + (it & 1) * L::kPBytes;
           if constexpr (F8) {
-            const uint32_t to = swizzled<L::kPRow>(key, group);
-            *reinterpret_cast<uint4*>(at + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + L::kPPiece + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, group)) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, L::kGroups + group)) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
           } else {
             *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, 2 * group)) =
                 make_uint4(hi[0], hi[1], hi[2], hi[3]);

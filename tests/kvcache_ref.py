@@ -83,10 +83,9 @@ def tree(q, k, v, lens, mask, scale, fmt, v_scale=None):
        the maximum.  ds is the sum of both; e^s is off by at most 2 ds + 2^-20
        (ex2 and the fp32 sums).
      - probabilities: rounded to bf16 (2^-8 of the value), or through fp16 (2^-11)
-       to an e4m3 piece and an e5m2 piece of the rest (2^-4 of 2^-3, 2^-7), where
-       the first is subnormal off by at most 2^-3 of its half step 2^-10, in units
-       in which the largest p_j 2^e_j of the row is 7 .. 448: 2^-15.8 of that
-       largest one, times the codes.
+       to two e4m3 pieces (cut to four bits, the rest rounded to four: 2^-8), where
+       the first is subnormal off by at most 2^-13, in units in which the largest
+       p_j 2^e_j of the row is 7 .. 448: 2^-15.8 of that largest one, times the codes.
      - o: rounded to bf16 once (2^-8).
     """
     B, Hq, T, d = q.shape
@@ -119,7 +118,7 @@ def tree(q, k, v, lens, mask, scale, fmt, v_scale=None):
                         ds += 2.0 ** -17.8 * scale * np.abs(q[b, h, t]).max() * np.abs(kk).sum(-1).max()
                         w = 2.0 ** (v_scale[b, h // G, see].astype(float) - 127)
                         floor = 2.0 ** -15.8 * (p * w).max() * (np.abs(vv) / w[:, None]).sum(0)
-                    each = 2.0 ** -8 if fmt == "bf16" else 2.0 ** -7 + 2.0 ** -11
+                    each = 2.0 ** -8 if fmt == "bf16" else 2.0 ** -8 + 2.0 ** -11
                     o_tol[b, h, t] = a * (each + 2 * ds + 2.0 ** -18) + floor \
                         + 2.0 ** -8 * 1.02 * np.abs(o[b, h, t])
                     lse_tol[b, h, t] = ds + 2.0 ** -20 * (1 + abs(lse[b, h, t]))
