@@ -82,22 +82,31 @@ struct Lazy {
   [[maybe_unused]] static constexpr float kLowScale = 0.125f;  // of the low pieces in it
 };
 
+// A pair of the share: its tiles t0 .. t0 + tiles - 1 are worked on here.
+struct PairInfo {
+  long long bh;
+  int b, h, u0, len, nt, t0, tiles;
+  int valid;               // 0 behind the last pair
+  unsigned int bad[2];     // drafts whose value row holds NaN or infinities
+  unsigned long long any;  // drafts that some row of the sequence sees
+  unsigned int qmax;       // largest finite |q| of the row tile, as bf16 bits (e4m3)
+};
+
 struct TreeBars {
   uint64_t q_ready;
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2], p_ready[2], pv_done[2], drain;  // by tile parity
   uint32_t tmem_base;
   int abort_flag;
-  unsigned int bad[2][2];  // by pair parity: drafts whose value row holds NaN or infinities
   int start_b, start_h, start_u0, unit0, unit1;  // this CTA's share
-  int next_tiles[2], next_len[2];                // by pair parity
+  int lens[32];                                  // lengths of sequences start_b, start_b + 1, ...
+  PairInfo pair[4];                              // by pair, as the softmax warps agree on them
 };
 
 // What the softmax threads know of a pair's query rows.
 template <int NR>
 struct TreeRows {
   unsigned long long seen[NR];  // mask row
-  float f[NR];      // 2^e of the query row (e4m3)
   float m[NR];      // reference exponent, -inf before the first key
   float neg_m[NR];  // its negative: kUnseen before the first key, -inf for rows past R
   float alpha[NR];  // of the last move
@@ -200,6 +209,16 @@ __device__ __forceinline__ int warp_sum(int x) {
   return x;
 }
 
+// The same through the share's first 32 lengths (a load behind the streams of all
+// SMs takes 2 to 3 us).
+__device__ __forceinline__ int near_len(const TreeParams& p, const TreeBars* bars, int b) {
+  const int i = b - bars->start_b;
+  return i < 32 ? bars->lens[i] : seq_len(p, b);
+}
+__device__ __forceinline__ int len_tiles(const TreeParams& p, int len) {
+  return (min(len + p.T, p.cap) + kTile - 1) / kTile;
+}
+
 // Units of all (sequence, key head) pairs; the whole warp calls it.
 __device__ __forceinline__ int all_units(const TreeParams& p) {
   int n = 0;
@@ -227,9 +246,9 @@ struct Walk {
     t0 = max(unit0 - u0 - kPairCost, 0);
     n = min(nt, unit1 - u0 - kPairCost) - t0;
   }
-  __device__ __forceinline__ bool valid(const TreeParams& p) {
+  __device__ __forceinline__ bool valid(const TreeParams& p, const TreeBars* bars) {
     if (!inside()) return false;
-    set(seq_tiles(p, b));
+    set(len_tiles(p, near_len(p, bars, b)));
     return true;
   }
   __device__ __forceinline__ void next(const TreeParams& p) {
@@ -240,6 +259,27 @@ struct Walk {
     }
   }
 };
+
+// The pair behind pair `from` (one thread).
+__device__ __forceinline__ void next_pair(const TreeParams& p, TreeBars* bars, const PairInfo& from,
+                                          PairInfo& to) {
+  to.u0 = from.u0 + from.nt + kPairCost;
+  to.valid = to.u0 + kPairCost < bars->unit1;
+  if (!to.valid) return;
+  to.h = from.h + 1;
+  to.b = from.b;
+  to.len = from.len;
+  if (to.h == p.Hkv) {
+    to.h = 0;
+    ++to.b;
+    to.len = near_len(p, bars, to.b);
+  }
+  to.bh = static_cast<long long>(to.b) * p.Hkv + to.h;
+  to.nt = len_tiles(p, to.len);
+  to.t0 = 0;
+  to.tiles = min(to.nt, bars->unit1 - to.u0 - kPairCost);
+  to.bad[0] = to.bad[1] = to.qmax = 0;
+}
 
 // ------------------------------------------------------------ tensor memory
 // 32 lanes x 16 columns, thread t of the warp gets lane (its warp's base + t).
@@ -252,6 +292,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -289,21 +336,20 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
   lo = __byte_perm(l0, l1, 0x7531);
 }
 
-// Four fp32 of at most 448 as two e4m3 pieces each: hi = e4m3(x), lo = e4m3(x - hi).
+// Two fp32 of at most 448 as two e4m3 pieces each: hi = e4m3(x), lo = e4m3(x - hi).
 // The subtraction is exact in fp16, and x has at most 8 bits here (a query).
-__device__ __forceinline__ void split4_signed(const float (&x)[4], uint32_t& hi, uint32_t& lo) {
-  hi = lo = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-    const __nv_fp8x2_storage_t a =
-        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3));
-    const __nv_fp8x2_storage_t b = __nv_cvt_halfraw2_to_fp8x2(
-        static_cast<__half2_raw>(__hsub2(h, back)), __NV_SATFINITE, __NV_E4M3);
-    hi |= static_cast<uint32_t>(a) << (16 * i);
-    lo |= static_cast<uint32_t>(b) << (16 * i);
-  }
+__device__ __forceinline__ void split2_query(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const __nv_fp8x2_storage_t a =
+      __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+  const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3));
+  hi = a;
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(h, back)), __NV_SATFINITE,
+                                  __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& x, int k) {
+  return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
 }
 
 // ------------------------------------------------------------ pairs of fp32
@@ -358,81 +404,105 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t 
 }
 
 // ------------------------------------------------------------ query rows
+// What a softmax thread reads of a pair besides keys and values.  It is asked for, into
+// L2, a pair ahead, and loaded while the last product of the pair before runs.
+template <int D, int NR>
+struct PairLoads {
+  static constexpr int kPer = kTile * (NR / 16) / NR;  // threads a query row
+  static constexpr int kGran = D / 8 / kPer;           // eight channels each
+  uint4 q[kGran];
+  unsigned long long seen, any;  // mask rows: of row threadIdx.x, of drafts lane and lane + 32
+
+  // trow: the draft of row threadIdx.x
+  __device__ __forceinline__ void load(const TreeParams& p, int b, long long bh, int rt, int have,
+                                       int trow) {
+    const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
+    const uint4* src = p.q + ((bh * p.R + rt * kTreeRows + r) * (D / 8) + part * kGran);
+    const bool exists = r < have;
+#pragma unroll
+    for (int i = 0; i < kGran; ++i) q[i] = exists ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    const int lane = threadIdx.x & 31;
+    seen = (2ull << trow) - 1;
+    any = 0;
+    if (p.mask) {
+      const unsigned long long* mk = p.mask + b * p.mask_stride;
+      seen = __ldg(mk + trow);
+      if (lane < p.T) any = __ldg(mk + lane);
+      if (lane + 32 < p.T) any |= __ldg(mk + lane + 32);
+    }
+  }
+  static __device__ __forceinline__ void ask(const TreeParams& p, int b, long long bh, int rt,
+                                             int have, int trow) {
+    const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
+    if (r < have)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          p.q + ((bh * p.R + rt * kTreeRows + r) * (D / 8) + part * kGran)));
+    if (p.mask && threadIdx.x < NR)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.mask + b * p.mask_stride + trow));
+  }
+  // The drafts that some row of the sequence sees.
+  __device__ __forceinline__ unsigned long long drafts(const TreeParams& p) const {
+    if (!p.mask) return (2ull << (p.T - 1)) - 1;
+    return static_cast<unsigned long long>(
+               __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any >> 32)))
+               << 32 |
+           __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any));
+  }
+};
+
 // The row tile's query rows as the swizzled operand of S^T (rows past `have` are
-// zeros), kSoft / NR threads a row.  e4m3: two pieces of the row times 2^-e, its
-// factor takes 2^e.
+// zeros), and their mask rows.  e4m3: two pieces of the rows times 2^-e, e from the
+// largest of the tile's elements; the return value is 2^e.  (An exponent for every
+// row would cost the softmax a product for every score.  A score is off by what the
+// largest row's is: 2^-17.8 max|q| sum|k|, scaled.)
 template <int D, bool F8, int NR>
-__device__ __forceinline__ void store_queries(uint8_t* sq, TreeRows<NR>* rows, const uint4* q,
-                                              int have) {
+__device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
+                                               const PairLoads<D, NR>& in, int have,
+                                               unsigned int* qmax) {
   using L = TreeLayout<D, F8, NR>;
-  constexpr int kPer = L::kSoft / NR;   // threads a row
-  constexpr int kGran = D / 8 / kPer;   // eight channels each
+  constexpr int kPer = PairLoads<D, NR>::kPer, kGran = PairLoads<D, NR>::kGran;
   const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
-  uint4 x[kGran];
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < kGran; ++i) {
-    x[i] = r < have ? __ldg(q + static_cast<long long>(r) * (D / 8) + part * kGran + i)
-                    : make_uint4(0, 0, 0, 0);
-    if (F8) m = __vmaxu2(m, finite_max8(x[i]));
-  }
-  if constexpr (!F8) {
-#pragma unroll
-    for (int i = 0; i < kGran; ++i) {
-      const int c = part * kGran + i;  // 16-byte unit of the row
-      *reinterpret_cast<uint4*>(sq + (c >> 3) * (NR * 128) + swizzled<128>(r, c & 7)) = x[i];
-    }
-  } else {
-#pragma unroll
-    for (int o = kPer / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int e = scale_exponent(max(m & 0xffffu, m >> 16));
-    const float s = pow2_of(-e);
-#pragma unroll
-    for (int i = 0; i < kGran; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float f[4] = {bf_lo(w[2 * k]), bf_hi(w[2 * k]), bf_lo(w[2 * k + 1]), bf_hi(w[2 * k + 1])};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = fmaf(f[j], 0.0f, f[j] * s);  // infinities to NaN
-        split4_signed(f, hi[k], lo[k]);
-      }
-      const int c = part * kGran + i;  // 8-byte half of a unit
-      uint8_t* at = sq + swizzled<L::kAtom>(r, c >> 1) + (c & 1) * 8;
-      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(at + L::kQPiece) = make_uint2(lo[0], lo[1]);
-    }
-    if (part == 0) rows->f[r] = pow2_of(e);
-  }
+  float unit = 1.0f;
   if (part == 0) {
     rows->m[r] = -INFINITY;
     rows->neg_m[r] = r < have ? kUnseen : -INFINITY;
   }
-}
-
-// Mask rows of the tile's query rows.
-template <int NR>
-__device__ __forceinline__ void store_masks(TreeRows<NR>* rows, const TreeParams& p, int b, int rt) {
-  if (threadIdx.x < NR) {
-    const int t = (rt * kTreeRows + threadIdx.x) % p.T;
-    rows->seen[threadIdx.x] =
-        p.mask ? __ldg(p.mask + b * p.mask_stride + t) : (2ull << t) - 1;
+  if (threadIdx.x < NR) rows->seen[threadIdx.x] = in.seen;
+  if constexpr (!F8) {
+#pragma unroll
+    for (int i = 0; i < kGran; ++i) {
+      const int c = part * kGran + i;  // 16-byte unit of the row
+      *reinterpret_cast<uint4*>(sq + (c >> 3) * (NR * 128) + swizzled<128>(r, c & 7)) = in.q[i];
+    }
+  } else {
+    uint32_t m = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kGran; ++i) {
+      m = __vmaxu2(m, finite_max8(in.q[i]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) all = __vmaxu2(all, word(in.q[i], k) & 0x7fff7fffu);
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    if ((threadIdx.x & 31) == 0) atomicMax(qmax, m);
+    named_bar_sync(1, L::kSoft);
+    const int e = scale_exponent(*static_cast<volatile unsigned int*>(qmax));
+    const float s = pow2_of(-e);
+    unit = pow2_of(e);
+#pragma unroll
+    for (int i = 0; i < kGran; ++i) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        split2_query(bf_lo(word(in.q[i], k)) * s, bf_hi(word(in.q[i], k)) * s, hi[k], lo[k]);
+      const int c = part * kGran + i;  // 8-byte half of a unit
+      uint8_t* at = sq + swizzled<L::kAtom>(r, c >> 1) + (c & 1) * 8;
+      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2*>(at + L::kQPiece) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    }
+    // NaN or infinities in the row: its scores are NaN
+    if (max(all & 0xffffu, all >> 16) >= 0x7f80u && r < have) rows->neg_m[r] = NAN;
   }
-}
-
-// The drafts that some row of sequence b sees.
-__device__ __forceinline__ unsigned long long drafts_seen(const TreeParams& p, int b) {
-  if (!p.mask) return (2ull << (p.T - 1)) - 1;
-  const unsigned long long* mk = p.mask + b * p.mask_stride;
-  const int lane = threadIdx.x & 31;
-  unsigned long long any = 0;
-  if (lane < p.T) any = __ldg(mk + lane);
-  if (lane + 32 < p.T) any |= __ldg(mk + lane + 32);
-  return static_cast<unsigned long long>(
-             __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any >> 32)))
-             << 32 |
-         __reduce_or_sync(0xffffffffu, static_cast<unsigned>(any));
+  return unit;
 }
 
 // ------------------------------------------------------------ value rows
@@ -493,11 +563,11 @@ __device__ __forceinline__ float sum_lanes(float (&x)[16]) {
   return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
-// x = t - M of a key for 16 rows (t itself without M), t = scale log2(e) q.k + e.
-// ks: scale log2(e), times 2^k for e4m3.
+// x = t - M of a key for 16 rows (t itself where neg_m is null), t = ks S + e;
+// ks: scale log2(e), times 2^k and the unit of the query pieces for e4m3.
 template <bool F8, bool M>
-__device__ __forceinline__ void form_scores(uint32_t taddr, const float* f, const float* neg_m,
-                                            float ks, float ev, f32x2 (&x)[8]) {
+__device__ __forceinline__ void form_scores(uint32_t taddr, const float* neg_m, float ks, float ev,
+                                            f32x2 (&x)[8]) {
   uint32_t s[16];
   tmem_ld16(taddr, s);
   tmem_ld_wait();
@@ -505,18 +575,13 @@ __device__ __forceinline__ void form_scores(uint32_t taddr, const float* f, cons
   const f32x2 ks2 = pack2(ks, ks), ev2 = pack2(ev, ev);
 #pragma unroll
   for (int r = 0; r < 8; r += 2) {
-    ulonglong2 m = make_ulonglong2(0, 0), g = make_ulonglong2(0, 0);
-    if (M) m = *reinterpret_cast<const ulonglong2*>(neg_m + 2 * r);
-    if (F8) g = *reinterpret_cast<const ulonglong2*>(f + 2 * r);
-    const f32x2 a = pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1]));
-    const f32x2 b = pack2(__uint_as_float(s[2 * r + 2]), __uint_as_float(s[2 * r + 3]));
-    if constexpr (F8) {
-      x[r] = fma2(mul2(a, g.x), ks2, M ? add2(ev2, m.x) : ev2);
-      x[r + 1] = fma2(mul2(b, g.y), ks2, M ? add2(ev2, m.y) : ev2);
-    } else {
-      x[r] = fma2(a, ks2, m.x);
-      x[r + 1] = fma2(b, ks2, m.y);
+    ulonglong2 m = make_ulonglong2(ev2, ev2);
+    if (M) {
+      m = *reinterpret_cast<const ulonglong2*>(neg_m + 2 * r);
+      if (F8) m = make_ulonglong2(add2(ev2, m.x), add2(ev2, m.y));
     }
+    x[r] = fma2(pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1])), ks2, m.x);
+    x[r + 1] = fma2(pack2(__uint_as_float(s[2 * r + 2]), __uint_as_float(s[2 * r + 3])), ks2, m.y);
   }
 }
 
@@ -543,11 +608,11 @@ __device__ __noinline__ uint32_t hidden_rows(const unsigned long long* seen, int
 
 // The warp's maximum of each row's scores into out[16].
 template <bool F8>
-__device__ __noinline__ void row_maxima(uint32_t taddr, const float* f, float ks, float ev,
-                                        uint32_t hidden, float* out) {
+__device__ __noinline__ void row_maxima(uint32_t taddr, float ks, float ev, uint32_t hidden,
+                                        float* out) {
   const int lane = threadIdx.x & 31;
   f32x2 t[8];
-  form_scores<F8, false>(taddr, f, nullptr, ks, ev, t);
+  form_scores<F8, false>(taddr, nullptr, ks, ev, t);
   hide_rows(t, hidden);
   float top = -INFINITY;
 #pragma unroll
@@ -569,10 +634,32 @@ __device__ __noinline__ void new_reference(TreeRows<NR>* rows, int r, int have) 
                           fmaxf(rows->part[2][r], rows->part[3][r]));
   const float m_old = rows->m[r];
   const float m_new = fmaxf(m_old, top + (Lazy<F8>::kLog2 - Lazy<F8>::kTop));
-  if (m_new == -INFINITY) return;
+  if (m_new == -INFINITY || isnan(rows->neg_m[r])) return;
   rows->m[r] = m_new;
   rows->neg_m[r] = -m_new;
   rows->alpha[r] = ex2_approx(m_old - m_new);
+}
+
+// y of four rows of a channel, plus the NaN and infinities of the drafts `bad` that
+// the rows see; v: the channel in the value row of draft 0.
+template <int D, bool F8>
+__device__ __noinline__ float4 add_bad(float4 y, unsigned long long bad,
+                                       const unsigned long long* seen, const uint8_t* v) {
+#pragma unroll 1
+  for (int j = 0; j < 64; ++j) {
+    if (!(bad >> j & 1)) continue;
+    float z;
+    if constexpr (F8)
+      z = (v[j * D] & 0x7f) == 0x7f ? NAN : 0.0f;
+    else
+      z = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(v)[j * D]);
+    if (isfinite(z)) continue;
+    if (seen[0] >> j & 1) y.x += z;
+    if (seen[1] >> j & 1) y.y += z;
+    if (seen[2] >> j & 1) y.z += z;
+    if (seen[3] >> j & 1) y.w += z;
+  }
+  return y;
 }
 
 // 16 columns of O, `pieces` times `stride` columns apart, times alpha.
@@ -640,7 +727,6 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_ready[s], L::kSoft / 32);
       mbar_init(&bars->pv_done[s], 1);
-      bars->bad[s][0] = bars->bad[s][1] = 0;
     }
     mbar_init(&bars->drain, 1);
     // an earlier CTA already recorded a pipeline timeout: exit without work
@@ -679,12 +765,24 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           bars->start_b = b0 + lane;
           bars->start_h = h;
           bars->start_u0 = u0;
-          bars->next_tiles[0] = nt;
-          bars->next_len[0] = seq_len(p, b0 + lane);
+          PairInfo& first = bars->pair[0];
+          first.b = b0 + lane;
+          first.h = h;
+          first.bh = static_cast<long long>(b0 + lane) * p.Hkv + h;
+          first.u0 = u0;
+          first.len = seq_len(p, b0 + lane);
+          first.nt = nt;
+          first.t0 = max(unit0 - u0 - kPairCost, 0);
+          first.tiles = min(nt, unit1 - u0 - kPairCost) - first.t0;
+          first.valid = 1;
+          first.bad[0] = first.bad[1] = first.qmax = 0;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
         if (unit0 < before) break;
       }
+      __syncwarp();
+      const int b = bars->start_b + lane;
+      bars->lens[lane] = b < p.B ? seq_len(p, b) : 0;
     }
   }
   __syncthreads();
@@ -693,6 +791,11 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
     tmem_alloc(&bars->tmem_base, L::kCols);
     tmem_relinquish();
   }
+  // the first pair's queries are asked for before the streams begin
+  const int have = min(p.R - rt * kTreeRows, NR);  // query rows of this tile
+  const int trow = (rt * kTreeRows + static_cast<int>(threadIdx.x)) % p.T;
+  PairLoads<D, NR> in;
+  if (warp < L::kTmaWarp) in.load(p, bars->pair[0].b, bars->pair[0].bh, rt, have, trow);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -714,6 +817,14 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         return s;
       };
       auto load_k = [&](int row0, int bh) {
+        if constexpr (F8) {  // the scales of the tile, on their way into L2 meanwhile
+          const long long at = static_cast<long long>(bh) * p.cap + row0;
+          const int last = min(kTile, p.cap - row0) - 1;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.k_scale + at));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.k_scale + at + last));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.v_scale + at));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.v_scale + at + last));
+        }
 #pragma unroll
         for (int c = 0; c < kParts; ++c) {
           const int s = slot();
@@ -732,7 +843,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
                         &bars->full[s], x * 64, row0 + c * L::kVKeys, bh);
         }
       };
-      for (Walk w(bars); ok && w.valid(p); w.next(p)) {
+      for (Walk w(bars); ok && w.valid(p, bars); w.next(p)) {
         const int bh = w.b * p.Hkv + w.h, row0 = w.t0 * kTile;
 #pragma unroll 1
         for (int t = -2; ok && t < w.n; ++t) {
@@ -752,7 +863,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       const uint32_t sP = smem_u32(smem + L::kP);
       int n = 0, it = 0, seg = 0;  // slots taken, tiles and pairs done
       bool ok = true;
-      for (Walk w(bars); __all_sync(0xffffffffu, ok && w.valid(p)); w.next(p), ++seg) {
+      for (Walk w(bars); __all_sync(0xffffffffu, ok && w.valid(p, bars)); w.next(p), ++seg) {
         const int tiles = __reduce_max_sync(0xffffffffu, w.n);
         if (!(ok = all_wait(&bars->q_ready, seg & 1, bars, 0x512))) break;
 #pragma unroll 1
@@ -844,7 +955,6 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
     TreeRows<NR>* const both = reinterpret_cast<TreeRows<NR>*>(smem + L::kRows);
     int it = 0, seg = 0, n = 0;
     bool ok = true;
-    const int have = min(p.R - rt * kTreeRows, NR);  // query rows of this tile
     // this thread's scale bytes of the next tile, loaded a tile ahead
     uint32_t kb = 127, vb = 127;
     auto load_scales = [&](long long bh, int pos, int end) {
@@ -854,45 +964,35 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         vb = __ldg(p.v_scale + bh * p.cap + pos);
       }
     };
-    Walk w(bars);           // the pair at hand, and from its last tile on the next one
-    bool more = true;       // there is a next one
     f32x2 l[8];             // sums of this key column, by row
-    // the pair in work: its length, its first row of o, its slot of partials (-1: none)
-    int len = 0, end = 0;
-    long long bh = 0, slot = -1;
-    unsigned long long any = 0;
+    float factor = 0.0f;    // scale log2(e) and the unit of the query pieces
 #pragma unroll 1
     for (;; ++seg) {
       // ---- the next pair's queries: S of the last tile is complete, so that Q is
       // free, and the first scores are formed during this pair's epilogue
-      const int len2 = more ? bars->next_len[seg & 1] : 0;
-      const long long bh2 = static_cast<long long>(w.b) * p.Hkv + w.h;
-      unsigned long long any2 = 0;
-      int len3 = 0;  // of the pair after the next one: thread 0's view of it is everybody's
-      bool more3 = false;
-      if (more) {
+      PairInfo& next = bars->pair[seg & 3];
+      if (next.valid) {
         TreeRows<NR>* const rows = both + (seg & 1);
-        w.set(bars->next_tiles[seg & 1]);
-        Walk w3 = w;
-        w3.next(p);
-        more3 = w3.inside();
-        if (tid == 0 && more3) len3 = w3.b == w.b ? len2 : seq_len(p, w3.b);
-        load_scales(bh2, w.t0 * kTile + key, min(len2 + p.T, p.cap));
-        store_queries<D, F8, NR>(smem + L::kQ, rows, p.q + (bh2 * p.R + rt * kTreeRows) * (D / 8),
-                                 have);
-        store_masks<NR>(rows, p, w.b, rt);
-        any2 = drafts_seen(p, w.b);
+        if (seg > 0) in.load(p, next.b, next.bh, rt, have, trow);
+        load_scales(next.bh, next.t0 * kTile + key, min(next.len + p.T, p.cap));
+        if (tid == 0) next_pair(p, bars, next, bars->pair[(seg + 1) & 3]);
+        if (seg > 0) ok = product_done(it - 1, ok, bars, 0x526);
+        __syncwarp();
+        factor = p.scale_log2 *
+                 store_queries<D, F8, NR>(smem + L::kQ, rows, in, have, &next.qmax);
+        const unsigned long long any = in.drafts(p);
+        if (tid == 0) next.any = any;
         fence_proxy_async_smem();
         mbar_arrive(&bars->q_ready);
-      }
-      if (tid == 0 && more3) {  // read at the next turn, behind the barrier below
-        bars->next_len[(seg + 1) & 1] = len3;
-        bars->next_tiles[(seg + 1) & 1] = (min(len3 + p.T, p.cap) + kTile - 1) / kTile;
+      } else if (seg > 0) {
+        ok = product_done(it - 1, ok, bars, 0x526);
+        __syncwarp();
       }
       if (seg > 0) {
         // ---- epilogue: sums over the keys, then a channel a thread
         TreeRows<NR>* const rows = both + ((seg - 1) & 1);
-        unsigned int* const note = bars->bad[(seg - 1) & 1];
+        const PairInfo& pair = bars->pair[(seg - 1) & 3];
+        tc_fence_after_sync();
         {
           float y[16];
 #pragma unroll
@@ -904,102 +1004,87 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           const float z = sum_lanes(y);
           if (lane < 16) rows->part[quad][own + lane] = z;
         }
-        ok = product_done(it - 1, ok, bars, 0x526);
-        __syncwarp();
-        tc_fence_after_sync();
         soft_bar();
-        const long long row0 = bh * p.R + rt * kTreeRows;  // of o and lse
-        const unsigned long long bad = static_cast<unsigned long long>(note[1]) << 32 | note[0];
-        if (tid < NR) {
+        // partials of a pair that began in an earlier share go to slot 0, of one that
+        // goes on in the next to slot 1
+        const long long slot =
+            pair.tiles == pair.nt ? -1 : 2ll * blockIdx.x + (pair.t0 > 0 ? 0 : 1);
+        const long long row0 = pair.bh * p.R + rt * kTreeRows;  // of o and lse
+        if (tid < have) {
           const float sum = (rows->part[0][tid] + rows->part[1][tid]) +
                             (rows->part[2][tid] + rows->part[3][tid]);
-          rows->inv[tid] =
-              Lazy<F8>::kOScale * (slot >= 0 ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum));
-          if (tid < have && ok) {
-            if (slot < 0)
-              p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (log2f(sum) + rows->m[tid]) * kLn2;
-            else
-              p.part_ml[slot * p.prow + tid] = make_float2(rows->m[tid], sum);
+          float inv = Lazy<F8>::kOScale;
+          if (slot < 0) {
+            inv *= sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+            if (ok) p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (__log2f(sum) + rows->m[tid]) * kLn2;
+          } else if (ok) {
+            p.part_ml[slot * p.prow + tid] = make_float2(rows->m[tid], sum);
           }
+          rows->inv[tid] = inv;
         }
         soft_bar();
-        if (tid == 0) note[0] = note[1] = 0;
+        const unsigned long long bad =
+            static_cast<unsigned long long>(pair.bad[1]) << 32 | pair.bad[0];
         // channel of this thread: with d = 64 the accumulator's rows are spread over
         // the first 16 lanes of each warp
         const int ch = D == 128 ? key : quad * 16 + lane;
         const bool mine = ok && (D == 128 || lane < 16);
-        if (own < have) {
-          uint32_t o[16];
-          tmem_ld16(tlane + L::kOCol + own, o);
+#pragma unroll 1
+        for (int r = own; r < min(have, own + 16); r += 4) {
+          uint32_t o[4], lo[4];
+          tmem_ld4(tlane + L::kOCol + r, o);
+          if (F8) tmem_ld4(tlane + L::kOCol + NR + r, lo);
           tmem_ld_wait();
           reg_pin(o);
-          if constexpr (F8) {
-            uint32_t lo[16];
-            tmem_ld16(tlane + L::kOCol + NR + own, lo);
-            tmem_ld_wait();
-            reg_pin(lo);
+          if (F8) reg_pin(lo);
+          float y[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = __float_as_uint(fmaf(__uint_as_float(lo[i]), Lazy<F8>::kLowScale,
-                                          __uint_as_float(o[i])));
+          for (int i = 0; i < 4; ++i) {
+            y[i] = __uint_as_float(o[i]);
+            if (F8) y[i] = fmaf(__uint_as_float(lo[i]), Lazy<F8>::kLowScale, y[i]);
           }
-          if (bad && mine) {
-            // drafts with NaN or infinities, to the rows that see them
-#pragma unroll 1
-            for (int j = 0; j < 64; ++j) {
-              if (!(bad >> j & 1)) continue;
-              const long long at = (bh * p.cap + len + j) * D + ch;
-              float v;
-              if constexpr (F8)
-                v = (p.v[at] & 0x7f) == 0x7f ? NAN : 0.0f;
-              else
-                v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[at]);
-              if (isfinite(v)) continue;
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (rows->seen[own + i] >> j & 1)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
-            }
+          if (bad) {
+            const float4 z = add_bad<D, F8>(
+                make_float4(y[0], y[1], y[2], y[3]), bad, rows->seen + r,
+                p.v + ((pair.bh * p.cap + pair.len) * D + (mine ? ch : 0)) * (F8 ? 1 : 2));
+            y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
           }
-          if (slot < 0) {
-            __nv_bfloat16* dst = p.o + (row0 + own) * D + ch;
+          const float4 inv = *reinterpret_cast<const float4*>(rows->inv + r);
+          const float f[4] = {inv.x, inv.y, inv.z, inv.w};
+          const long long to = ((slot < 0 ? row0 : slot * p.prow) + r) * D + ch;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (mine && own + i < have)
-                dst[i * D] = __float2bfloat16_rn(__uint_as_float(o[i]) * rows->inv[own + i]);
-          } else {
-            float* dst = p.part_o + (slot * p.prow + own) * D + ch;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (mine && own + i < have) dst[i * D] = __uint_as_float(o[i]) * Lazy<F8>::kOScale;
+          for (int i = 0; i < 4; ++i) {
+            if (!mine || r + i >= have) continue;
+            if (slot < 0)
+              p.o[to + i * D] = __float2bfloat16_rn(y[i] * f[i]);
+            else
+              p.part_o[to + i * D] = y[i] * f[i];
           }
         }
       } else {
         soft_bar();  // the first pair's rows are stored
       }
-      if (!more) break;
+      if (!next.valid) break;
 
       // ---- the pair's tiles
       TreeRows<NR>* const rows = both + (seg & 1);
-      len = len2;
-      end = min(len + p.T, p.cap);
-      bh = bh2;
-      any = any2;
-      // partials of a pair that began in an earlier share go to slot 0, of one that
-      // goes on in the next to slot 1
-      slot = w.n == w.nt ? -1 : 2ll * blockIdx.x + (w.t0 > 0 ? 0 : 1);
-      const int tiles = w.n;
-      int pos = w.t0 * kTile + key;
-      w.next(p);
-      more = more3;
+      const long long bh = next.bh;
+      const int len = next.len, end = min(len + p.T, p.cap);
+      const int tiles = next.tiles;
+      int pos = next.t0 * kTile + key;
+      {
+        const PairInfo& then = bars->pair[(seg + 1) & 3];
+        if (then.valid) PairLoads<D, NR>::ask(p, then.b, then.bh, rt, have, trow);
+      }
 #pragma unroll
       for (int r = 0; r < 8; ++r) l[r] = 0;
-
       const int first_edge = (len - (pos - key)) / kTile;  // first tile past the committed tokens
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t, ++it, pos += kTile) {
-        float ks = p.scale_log2, ev = 0.0f, wv = 1.0f;
+        float ks = factor, ev = 0.0f, wv = 1.0f;
         if constexpr (F8) {  // scale log2(e) 2^k_j, e_j and 2^-e_j
+          // not before here: converted where they are loaded, a tile would wait for them
+          asm volatile("" : "+r"(kb), "+r"(vb));
           ks *= __uint_as_float(kb << 23);
           ev = __uint_as_float(0x4b000000u | vb) - 8388735.0f;  // 2^23 + 127
           wv = __uint_as_float((254u - vb) << 23);
@@ -1009,28 +1094,17 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         // ---- which rows see this key
         uint32_t hidden = 0;
         if (t >= first_edge) {
-          // V(t) in the order of loads.  With S(it) and PV(it - 1) complete, so are
-          // all loads that its slot had before: the parity is V(t)'s.
-          const int v = n + kParts * (2 + t + min(t, tiles - 2)) + key / L::kVKeys;
-          if (t > 0) ok = product_done(it - 1, ok, bars, 0x523);
-          ok = ok && t_wait(&bars->full[v % kSlots], (v / kSlots) & 1, bars, 0x521);
-          __syncwarp();
-          if (ok && group == 0)
-            clean_values<L::kAtom, kParts, F8>(
-                smem + L::kRing + (v % kSlots) * L::kSlot + (key % L::kVKeys) * L::kAtom,
-                L::kVKeys * 128, pos, len, end, any, bars->bad[seg & 1]);
           if (pos >= len) hidden = pos < end ? hidden_rows(rows->seen + own, pos - len) : 0xffffu;
           if (hidden == 0xffffu) {  // perhaps never written: finite scales for P = 0
             ks = wv = 1.0f;
             ev = 0.0f;
           }
-          __syncwarp();
         }
         // ---- x = t - M of this key for the thread's rows
         tc_fence_after_sync();
         const uint32_t scol = tlane + (it & 1) * NR + own;
         f32x2 x[8];
-        form_scores<F8, true>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
+        form_scores<F8, true>(scol, rows->neg_m + own, ks, ev, x);
         if (hidden) hide_rows(x, hidden);
         float mx = -INFINITY;
 #pragma unroll
@@ -1040,7 +1114,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         }
         if (group_bar_or(2 + group, mx > Lazy<F8>::kTop)) {
           // ---- some row grew: new references from the maxima over the group's keys
-          row_maxima<F8>(scol, rows->f + own, ks, ev, hidden, rows->part[quad] + own);
+          row_maxima<F8>(scol, ks, ev, hidden, rows->part[quad] + own);
           named_bar_sync(2 + group, kTile);
           if (key < 16) new_reference<F8, NR>(rows, own + key, have);
           named_bar_sync(2 + group, kTile);
@@ -1056,7 +1130,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               l[r + 1] = mul2(l[r + 1], al.y);
             }
           }
-          form_scores<F8, true>(scol, rows->f + own, rows->neg_m + own, ks, ev, x);
+          form_scores<F8, true>(scol, rows->neg_m + own, ks, ev, x);
           if (hidden) hide_rows(x, hidden);
         }
         // ---- P = 2^x over the P buffer that PV(it - 2) has read: it is complete, for
@@ -1092,6 +1166,17 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
             *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, 2 * group + 1)) =
                 make_uint4(hi[4], hi[5], hi[6], hi[7]);
           }
+        }
+        if (t >= first_edge) {
+          // V(t) in the order of loads.  With S(it) and PV(it - 1) complete, so are
+          // all loads that its slot had before: the parity is V(t)'s.
+          const int v = n + kParts * (2 + t + min(t, tiles - 2)) + key / L::kVKeys;
+          if (t > 0) ok = product_done(it - 1, ok, bars, 0x523);
+          ok = ok && t_wait(&bars->full[v % kSlots], (v / kSlots) & 1, bars, 0x521);
+          if (ok && group == 0)
+            clean_values<L::kAtom, kParts, F8>(
+                smem + L::kRing + (v % kSlots) * L::kSlot + (key % L::kVKeys) * L::kAtom,
+                L::kVKeys * 128, pos, len, end, next.any, next.bad);
         }
         fence_proxy_async_smem();  // P, and cleaned values
         tc_fence_before_sync();

@@ -70,7 +70,7 @@ def cache_values(cache):
                  for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
 
 
-def tree(q, k, v, lens, mask, scale, fmt, v_scale=None):
+def tree(q, k, v, lens, mask, scale, fmt, v_scale=None, qmax=None):
     """(o, lse, o_tol, lse_tol) of fa_decode_tree in fp64.
 
     q [B,Hq,T,d], k, v [B,Hkv,cap,d] fp64; mask: python ints [B][T].
@@ -78,9 +78,9 @@ def tree(q, k, v, lens, mask, scale, fmt, v_scale=None):
     The bounds follow from the arithmetic, for the keys a row sees:
      - scores: products are exact and added in fp32 (at most d + 8 roundings or
        truncations of 2^-23 of sum|q k|, scaled); an e4m3 cache splits q into
-       two e4m3 pieces of a power-of-two scale that puts the row's maximum in
-       [224, 448]: an element is off by at most 2^-10 of those units, 2^-17.8 of
-       the maximum.  ds is the sum of both; e^s is off by at most 2 ds + 2^-20
+       two e4m3 pieces of a power-of-two scale that puts the largest |q| of the rows
+       that share a tile (qmax; all of q unless given) in (224, 448]: an element is
+       off by at most 2^-10 of those units, 2^-17.8 of qmax.  ds is the sum of both; e^s is off by at most 2 ds + 2^-20
        (ex2 and the fp32 sums).
      - probabilities: rounded to bf16 (2^-8 of the value), or through fp16 (2^-11)
        to two e4m3 pieces (cut to four bits, the rest rounded to four: 2^-8), where
@@ -91,6 +91,7 @@ def tree(q, k, v, lens, mask, scale, fmt, v_scale=None):
     B, Hq, T, d = q.shape
     Hkv, cap = k.shape[1], k.shape[2]
     G = Hq // Hkv
+    qmax = np.abs(q).max() if qmax is None else qmax
     o = np.zeros((B, Hq, T, d))
     lse = np.full((B, Hq, T), -np.inf)
     o_tol = np.zeros_like(o)
@@ -115,7 +116,7 @@ def tree(q, k, v, lens, mask, scale, fmt, v_scale=None):
                     a = p @ np.abs(vv)
                     floor = 0.0
                     if fmt == "e4m3":
-                        ds += 2.0 ** -17.8 * scale * np.abs(q[b, h, t]).max() * np.abs(kk).sum(-1).max()
+                        ds += 2.0 ** -17.8 * scale * qmax * np.abs(kk).sum(-1).max()
                         w = 2.0 ** (v_scale[b, h // G, see].astype(float) - 127)
                         floor = 2.0 ** -15.8 * (p * w).max() * (np.abs(vv) / w[:, None]).sum(0)
                     each = 2.0 ** -8 if fmt == "bf16" else 2.0 ** -8 + 2.0 ** -11

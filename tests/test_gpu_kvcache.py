@@ -283,7 +283,7 @@ def test_tree_matches_the_definition(fa, fmt, d, case):
     for h in heads:
         kv = slice(h // (Hq // Hkv), h // (Hq // Hkv) + 1)
         want = ref.tree(ref.to64(q[:, h:h + 1]), k[:, kv], v[:, kv], lens, mask, scale, fmt,
-                        None if vs is None else vs[:, kv])
+                        None if vs is None else vs[:, kv], qmax=float(q.abs().max()))
         check_tree(o[:, h:h + 1], lse[:, h:h + 1], want)
 
 
@@ -353,6 +353,27 @@ def test_tree_nan_reaches_only_the_rows_that_see_it(fa, fmt, d, T, Hq):
     rest = ref.to64(o)[1][:, ~sees]
     rest[:, 2:4, 5] = 0
     assert np.all(np.isfinite(rest))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", (64, 128))
+def test_tree_nan_query_and_queries_of_many_sizes(fa, fmt, d):
+    """A query row with a NaN or an infinity is NaN and leaves the others alone; rows
+    whose sizes differ by 2^20 each keep their result."""
+    B, Hq, Hkv, T, cap, lens = 1, 6, 2, 4, 300, [290]
+    cache = make_cache(fa, fmt, B, Hkv, cap, d, lens, T, seed=70)
+    q = rnd(71, B, Hq, T, d) * (2.0 ** torch.linspace(1, -19, Hq * T)).reshape(Hq, T, 1).to(torch.bfloat16)
+    k, v = ref.cache_values(cache)
+    vs = None if fmt == "bf16" else cache.v_scale.cpu().numpy()
+    chain = [[(2 << t) - 1 for t in range(T)]]
+    want = ref.tree(ref.to64(q), k, v, lens, chain, 0.2, fmt, vs)
+    q[0, 1, 2, 7], q[0, 4, 0, 3] = math.nan, math.inf
+    o, lse = fa.fa_decode_tree(cache, q.cuda(), lens=i32(lens), scale=0.2)
+    ok(fa)
+    for h, t in ((1, 2), (4, 0)):
+        assert torch.isnan(o[0, h, t]).all() and torch.isnan(lse[0, h, t])
+        o[0, h, t], lse[0, h, t] = torch.from_numpy(want[0][0, h, t]).cuda(), float(want[1][0, h, t])
+    check_tree(o, lse, want)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
