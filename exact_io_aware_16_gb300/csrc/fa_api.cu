@@ -622,11 +622,10 @@ int fa_decode_tree(const fa_cache* cache, const void* q, const int* lens,
   a.scale = scale;
   a.num_sms = num_sms();
   CUtensorMap tk, tv;
-  // boxes of one slot of the kernel's ring: a tile's keys; half its values where
-  // they fill two slots
-  const bool two = cache->format == FA_CACHE_BF16 && cache->d == 128;
+  const long long rows = static_cast<long long>(Hq) / cache->Hkv * T;
+  const int v_keys = fa::tree_v_keys(cache->format == FA_CACHE_BF16, cache->d, rows);
   if (encode_cache(&tk, cache->k, *cache, fa::kTreeTile) != FA_OK ||
-      encode_cache(&tv, cache->v, *cache, two ? fa::kTreeTile / 2 : fa::kTreeTile) != FA_OK)
+      encode_cache(&tv, cache->v, *cache, v_keys) != FA_OK)
     return FA_ERR_CUDA;
   return fa::launch_decode_tree(a, tk, tv, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK

@@ -242,6 +242,10 @@ constexpr int kTreeRows = 64;   // query rows a row tile, at most
 // no pair can be split.
 constexpr int kTreeMaxSms = 152;
 constexpr int tree_ctas(long long rows) { return rows <= 32 ? 2 : 1; }  // an SM
+// Keys of a value tile in one box (and slot of the kernel's ring).
+constexpr int tree_v_keys(bool bf16, int d, long long rows) {
+  return bf16 && d == 128 && tree_ctas(rows) == 2 ? kTreeTile / 2 : kTreeTile;
+}
 
 struct TreePlan {
   int row_tiles, shares, slots, prow;

@@ -28,7 +28,8 @@
 // One CTA (two an SM up to 32 rows, one for 64):
 //   * one warp streams K and V tiles through one TMA ring, in the order the
 //     tensor core takes them: K0 K1 V0 K2 V1 ...;
-//   * one issues S^T(t + 2) behind PV(t): S^T has two buffers in tensor memory;
+//   * one (two where the CTA has the SM alone) issues S^T(t + 2) once softmax(t) has
+//     read the buffer before it, and PV(t): S^T has two buffers in tensor memory;
 //   * four warps for every 16 rows, a key a thread: softmax over the columns, P^T to shared
 //     memory ([key][row], an operand as it lies), epilogue with a channel a thread.
 //      A row's reference M is shared by the CTA; one
@@ -118,14 +119,19 @@ template <int D, bool F8, int NR>
 struct TreeLayout {
   static constexpr uint32_t kRow = F8 ? D : 2 * D;             // bytes of a cache row
   static constexpr uint32_t kAtom = F8 && D == 64 ? 64 : 128;  // swizzle width in bytes
-  // A tile comes in kParts slots: 64 columns of K, 64 keys of V (bf16, d = 128).
-  static constexpr int kParts = !F8 && D == 128 ? 2 : 1;
+  static constexpr int kBoxes = kRow / kAtom;                  // boxes of columns in a row
+  // A tile comes in kParts slots: 64 columns of K, 64 keys of V (bf16, d = 128, where
+  // two CTAs share the SM).
+  static constexpr int kParts = tree_v_keys(!F8, D, NR) == kTile ? 1 : 2;
   static constexpr uint32_t kSlot = kTile * kRow / kParts;     // 16 KB or 8 KB
   static constexpr int kVKeys = kTile / kParts;
   static constexpr int kGroups = NR / 16;  // softmax: 128 threads (a key each) for 16 rows
   static constexpr int kSoft = kTile * kGroups;
-  static constexpr int kTmaWarp = kSoft / 32, kMmaWarp = kTmaWarp + 1;
-  static constexpr int kThreads = kSoft + 64;
+  // With one CTA an SM the two products have an issuing warp each: one warp's 16
+  // instructions and their waits took 2000 cycles a tile, more than the softmax.
+  static constexpr int kMmaWarps = tree_ctas(NR) == 1 ? 2 : 1;
+  static constexpr int kTmaWarp = kSoft / 32, kMmaWarp = kTmaWarp + 1;  // and the S warp behind
+  static constexpr int kThreads = kSoft + 32 + 32 * kMmaWarps;
   static constexpr int kPieces = F8 ? 2 : 1;                   // of q, and of P along its row
   static constexpr uint32_t kQPiece = NR * kRow;               // 64 columns at a time for bf16
   static constexpr uint32_t kPRow = 2 * NR;                    // bytes of a key's P
@@ -134,7 +140,9 @@ struct TreeLayout {
   static constexpr uint32_t kRoom = (kCtas == 2 ? 113u : 227u) * 1024 - 1024 - 1024 -
                                     2 * sizeof(TreeRows<NR>) - kPieces * kQPiece - 2 * kPBytes;
   static constexpr int kFit = kRoom / kSlot;
-  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  // an even number, so that K and V tiles (K0 K1 V0 K2 V1 ...) each keep to their own
+  // slots and a warp that waits for one of them knows the load before it complete
+  static constexpr int kSlots = (kFit < kMaxSlots ? kFit : kMaxSlots) / 2 * 2;
   static_assert(kSlots >= 2 * kParts, "K(t + 1) is loaded before V(t)");
   static constexpr uint32_t kRing = 0;
   static constexpr uint32_t kQ = kRing + kSlots * kSlot;
@@ -690,10 +698,15 @@ __device__ __forceinline__ bool group_bar_or(int id, bool any) {
   return r != 0;
 }
 
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
+
 // PV(i) of the share's tile i is complete (and with it all earlier ones).  Tiles
-// alternate between two barriers; a softmax thread at tile `it` knows PV(it - 2)
-// to be complete (S(it) was issued behind it) and PV(it) not to be, so that the
-// parity of PV(it - 1) on its barrier tells it from its neighbours.
+// alternate between two barriers; a softmax thread at tile `it` knows PV(it - 3) to be
+// complete (it wrote P(it - 1) over what that read) and PV(it) not to be, so that the
+// parities of PV(it - 1) and PV(it - 2) on their barriers tell them from their neighbours.
 __device__ __forceinline__ bool product_done(int i, bool ok, TreeBars* bars, uint32_t code) {
   return ok && t_wait(&bars->pv_done[i & 1], (i >> 1) & 1, bars, code);
 }
@@ -728,7 +741,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       mbar_init(&bars->p_ready[s], L::kSoft / 32);
       mbar_init(&bars->pv_done[s], 1);
     }
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, L::kMmaWarps);
     // an earlier CTA already recorded a pipeline timeout: exit without work
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_tree_error) != 0) ? 1 : 0;
     fence_mbar_init();
@@ -828,8 +841,11 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
 #pragma unroll
         for (int c = 0; c < kParts; ++c) {
           const int s = slot();
-          if (s >= 0)
-            tma_load_3d(smem + L::kRing + s * L::kSlot, &tk, &bars->full[s], c * 64, row0, bh);
+          if (s < 0) return;
+#pragma unroll
+          for (int x = 0; x < L::kBoxes / kParts; ++x)
+            tma_load_3d(smem + L::kRing + s * L::kSlot + x * (kTile * 128), &tk, &bars->full[s],
+                        (c + x) * 64, row0, bh);
         }
       };
       auto load_v = [&](int row0, int bh) {
@@ -838,7 +854,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           const int s = slot();
           if (s < 0) return;
 #pragma unroll
-          for (int x = 0; x < kParts; ++x)  // 64 columns each
+          for (int x = 0; x < L::kBoxes; ++x)  // 64 columns each
             tma_load_3d(smem + L::kRing + s * L::kSlot + x * (L::kVKeys * 128), &tv,
                         &bars->full[s], x * 64, row0 + c * L::kVKeys, bh);
         }
@@ -853,30 +869,32 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       }
     }
     __syncwarp();
-  } else if (warp == L::kMmaWarp) {
-    // ------------------------------------------------ MMA issuer
-    // The whole warp runs the loop on values that are uniform by construction
-    // (votes and reductions), so that descriptors live in uniform registers,
-    // where the instruction wants them; one elected lane issues.
-    {
-      const uint32_t sQ = smem_u32(smem + L::kQ);
-      const uint32_t sP = smem_u32(smem + L::kP);
-      int n = 0, it = 0, seg = 0;  // slots taken, tiles and pairs done
+  } else if (warp >= L::kMmaWarp) {
+    // ------------------------------------------------ MMA issuers
+    // A whole warp runs the loop on values that are uniform by construction (votes
+    // and reductions), so that descriptors live in uniform registers, where the
+    // instruction wants them; one elected lane issues.
+    const uint32_t sQ = smem_u32(smem + L::kQ);
+    const uint32_t sP = smem_u32(smem + L::kP);
+    auto issue = [&](auto pv, auto scores) {
+      int n = 0, it = 0, seg = 0;  // slots, tiles and pairs done
       bool ok = true;
       for (Walk w(bars); __all_sync(0xffffffffu, ok && w.valid(p, bars)); w.next(p), ++seg) {
         const int tiles = __reduce_max_sync(0xffffffffu, w.n);
         if (!(ok = all_wait(&bars->q_ready, seg & 1, bars, 0x512))) break;
 #pragma unroll 1
-        for (int t = -2; ok && t < tiles; ++t) {
-          if (t >= 0) {
+        for (int t = -2; t < tiles; ++t) {
+          const int i = it + t;  // the share's tile
+          if (t >= 0 && !(ok = all_wait(&bars->p_ready[i & 1], (i >> 1) & 1, bars, 0x513))) break;
+          if (pv.value && t >= 0) {
             // O^T += V^T P^T
-            if (!(ok = all_wait(&bars->p_ready[it & 1], (it >> 1) & 1, bars, 0x513))) break;
-            const uint32_t pbase = sP + (it & 1) * L::kPBytes;
+            const uint32_t pbase = sP + (i & 1) * L::kPBytes;
             const uint32_t d = tmem + L::kOCol;
+            const int first = n + kParts * (2 + t + min(t, tiles - 2));
 #pragma unroll 1
-            for (int c = 0; c < kParts; ++c, ++n) {
-              const int s = n % kSlots;
-              if (!(ok = all_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x514))) break;
+            for (int c = 0; c < kParts; ++c) {
+              const int s = (first + c) % kSlots;
+              if (!(ok = all_wait(&bars->full[s], ((first + c) / kSlots) & 1, bars, 0x514))) break;
               tc_fence_after_sync();
               const uint32_t vbase = sRing + s * L::kSlot;
               if (!elect_one()) continue;
@@ -898,19 +916,18 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               }
               umma_commit(&bars->empty[s]);
             }
-            if (!ok) break;
             __syncwarp();
-            if (elect_one()) umma_commit(&bars->pv_done[it & 1]);
-            ++it;
+            if (!ok) break;
+            if (elect_one()) umma_commit(&bars->pv_done[i & 1]);
           }
-          if (t + 2 < tiles) {
+          if (scores.value && t + 2 < tiles) {
             // S^T of tile t + 2 = K Q^T, into the buffer that softmax(t) has read
-            const int i = it + (t < 0 ? t + 2 : 1);
             const uint32_t d = tmem + (i & 1) * NR;
+            const int first = n + kParts * (t < 0 ? t + 2 : 2 * t + 3);
 #pragma unroll 1
-            for (int c = 0; c < kParts; ++c, ++n) {
-              const int s = n % kSlots;
-              if (!(ok = all_wait(&bars->full[s], (n / kSlots) & 1, bars, 0x511))) break;
+            for (int c = 0; c < kParts; ++c) {
+              const int s = (first + c) % kSlots;
+              if (!(ok = all_wait(&bars->full[s], ((first + c) / kSlots) & 1, bars, 0x511))) break;
               tc_fence_after_sync();
               const uint32_t kbase = sRing + s * L::kSlot;
               if (!elect_one()) continue;
@@ -925,21 +942,32 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
                 }
               } else {
                 constexpr uint32_t idesc = idesc_bf16_f32(128, NR, false, false);
+                constexpr int kSteps = D / 16 / kParts;  // of 16 columns, in this slot
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // 64 columns
-                  umma_ss(d, sdesc_sw128(kbase + kk * 32, 16, 1024),
-                          sdesc_sw128(sQ + c * (NR * 128) + kk * 32, 16, 1024), idesc,
-                          (c > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < kSteps; ++kk)
+                  umma_ss(d, sdesc_sw128(kbase + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024),
+                          sdesc_sw128(sQ + (c + (kk >> 2)) * (NR * 128) + (kk & 3) * 32, 16, 1024),
+                          idesc, (c > 0 || kk > 0) ? 1u : 0u);
               }
               umma_commit(&bars->empty[s]);
             }
             __syncwarp();
-            if (ok && elect_one()) umma_commit(&bars->s_full[i & 1]);
+            if (!ok) break;
+            if (elect_one()) umma_commit(&bars->s_full[i & 1]);
           }
         }
+        n += 2 * kParts * tiles;
+        it += tiles;
       }
       __syncwarp();
       if (elect_one()) umma_commit(&bars->drain);
+    };
+    if constexpr (L::kMmaWarps == 1) {
+      issue(Flag<true>{}, Flag<true>{});
+    } else if (warp == L::kMmaWarp) {
+      issue(Flag<true>{}, Flag<false>{});
+    } else {
+      issue(Flag<false>{}, Flag<true>{});
     }
     __syncwarp();
   } else {
@@ -1133,8 +1161,9 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           form_scores<F8, true>(scol, rows->neg_m + own, ks, ev, x);
           if (hidden) hide_rows(x, hidden);
         }
-        // ---- P = 2^x over the P buffer that PV(it - 2) has read: it is complete, for
-        // S(it) was issued behind it
+        // ---- P = 2^x over the P buffer that PV(it - 2) has read.  With one issuing warp
+        // it is complete: S(it) was issued behind it.
+        if (L::kMmaWarps > 1 && it >= 2) ok = product_done(it - 2, ok, bars, 0x525);
         {
           const f32x2 wv2 = pack2(wv, wv);
           uint32_t hi[8], lo[F8 ? 4 : 1];
@@ -1174,9 +1203,9 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           if (t > 0) ok = product_done(it - 1, ok, bars, 0x523);
           ok = ok && t_wait(&bars->full[v % kSlots], (v / kSlots) & 1, bars, 0x521);
           if (ok && group == 0)
-            clean_values<L::kAtom, kParts, F8>(
+            clean_values<L::kAtom, L::kBoxes, F8>(
                 smem + L::kRing + (v % kSlots) * L::kSlot + (key % L::kVKeys) * L::kAtom,
-                L::kVKeys * 128, pos, len, end, next.any, next.bad);
+                L::kVKeys * L::kAtom, pos, len, end, next.any, next.bad);
         }
         fence_proxy_async_smem();  // P, and cleaned values
         tc_fence_before_sync();
@@ -1188,7 +1217,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
   }
 
   // ------------------------------------------------ teardown
-  if (warp == L::kMmaWarp) mbar_wait(&bars->drain, 0, &bars->abort_flag, &g_tree_error, 0x5ff);
+  if (warp >= L::kMmaWarp) mbar_wait(&bars->drain, 0, &bars->abort_flag, &g_tree_error, 0x5ff);
   if (bars->abort_flag) {
     // let any bulk copy already in flight land before the CTA exits
     const uint64_t t0 = globaltimer_ns();
