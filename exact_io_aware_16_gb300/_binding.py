@@ -528,6 +528,7 @@ class KvCache:
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
             v_scale.data_ptr() if e4m3 else None, B, Hkv, cap, d, int(e4m3))
         self._ref = ctypes.byref(self._struct)
+        self._sizes = {}  # workspace bytes by (Hq, T)
 
     k = property(lambda self: self._t[0])
     v = property(lambda self: self._t[1])
@@ -539,7 +540,11 @@ class KvCache:
 
 
 def _check_on(cache, t, name, dtype, shape):
-    """_check, and the cache's GPU."""
+    """_check, and the cache's GPU.  The calls on a cache take a few microseconds on
+    the GPU, so what is as it should be passes on one line."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() \
+            and _device_index(t) == cache._dev and _on_device(t):
+        return
     _check(t, name, dtype, shape)
     if _device_index(t) != cache._dev:
         raise ValueError(f"{name} is on device {_device_index(t)}, the cache on device "
@@ -549,6 +554,32 @@ def _check_on(cache, t, name, dtype, shape):
 def _check_ints(cache, t, name, shape):
     if t is not None:
         _check_on(cache, t, name, torch.int32, shape)
+
+
+def _alloc_on(cache, stream):
+    """Tensors that a call allocates for itself belong to the stream that it runs on:
+    the memory they get, and give back, is in no other stream's use."""
+    if stream is None or cache._dev < 0:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=cache._dev)
+    return torch.cuda.stream(stream)
+
+
+def _cache_call(cache, fn, stream, *args):
+    """fn(cache, *args, stream) with the cache's device current."""
+    dev = cache._dev
+    if stream is None and dev >= 0:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = _stream_handle(stream, cache._t[0].device)
+    if dev < 0 or dev == torch.cuda.current_device():
+        st = fn(cache._ref, *args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(cache._ref, *args, stream)
+    if st != FA_OK:
+        raise FaError(st, fn.__name__)
 
 
 def fa_cache_write(cache: KvCache, k, v, lens=None, counts=None, stream=None):
@@ -565,11 +596,8 @@ def fa_cache_write(cache: KvCache, k, v, lens=None, counts=None, stream=None):
     _check_on(cache, v, "v", torch.bfloat16, (B, Hkv, N, d))
     _check_ints(cache, lens, "lens", (B,))
     _check_ints(cache, counts, "counts", (B,))
-    with _device_guard(cache._dev):
-        st = library().fa_cache_write(cache._ref, _ptr(k), _ptr(v), _ptr(lens), _ptr(counts), N,
-                                      ctypes.c_void_p(_stream_handle(stream, k.device)))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_write")
+    _cache_call(cache, library().fa_cache_write, stream, k.data_ptr(), v.data_ptr(),
+                lens.data_ptr(), None if counts is None else counts.data_ptr(), N)
 
 
 def fa_cache_read(cache: KvCache, N: int, first=None, counts=None, k=None, v=None, stream=None):
@@ -579,18 +607,17 @@ def fa_cache_read(cache: KvCache, N: int, first=None, counts=None, k=None, v=Non
     B, Hkv, cap, d = cache._shape
     shape = (B, Hkv, int(N), d)
     dev = cache._t[0].device
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    if k is None or v is None:
+        with _alloc_on(cache, stream):
+            k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+            v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
     counts = cache._t[4] if counts is None else counts
     _check_on(cache, k, "k", torch.bfloat16, shape)
     _check_on(cache, v, "v", torch.bfloat16, shape)
     _check_ints(cache, first, "first", (B,))
     _check_ints(cache, counts, "counts", (B,))
-    with _device_guard(cache._dev):
-        st = library().fa_cache_read(cache._ref, _ptr(k), _ptr(v), _ptr(first), _ptr(counts),
-                                     int(N), ctypes.c_void_p(_stream_handle(stream, dev)))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_read")
+    _cache_call(cache, library().fa_cache_read, stream, k.data_ptr(), v.data_ptr(),
+                None if first is None else first.data_ptr(), counts.data_ptr(), int(N))
     return k, v
 
 
@@ -609,12 +636,8 @@ def fa_cache_commit(cache: KvCache, path, n_accept, lens=None, new_lens=None, st
     _check_ints(cache, n_accept, "n_accept", (B,))
     _check_ints(cache, lens, "lens", (B,))
     _check_ints(cache, new_lens, "new_lens", (B,))
-    with _device_guard(cache._dev):
-        st = library().fa_cache_commit(cache._ref, _ptr(lens), _ptr(path), _ptr(n_accept),
-                                       _ptr(new_lens), T,
-                                       ctypes.c_void_p(_stream_handle(stream, path.device)))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_commit")
+    _cache_call(cache, library().fa_cache_commit, stream, lens.data_ptr(), path.data_ptr(),
+                n_accept.data_ptr(), new_lens.data_ptr(), T)
     return new_lens
 
 
@@ -633,7 +656,12 @@ def tree_mask(parents):
 
 
 def fa_decode_tree_workspace_size(cache: KvCache, Hq: int, T: int) -> int:
-    return int(library().fa_decode_tree_workspace_size(cache._ref, Hq, T))
+    """Bytes of workspace of fa_decode_tree (0 for an invalid shape)."""
+    size = cache._sizes.get((Hq, T))
+    if size is None:
+        size = int(library().fa_decode_tree_workspace_size(cache._ref, Hq, T))
+        cache._sizes[(Hq, T)] = size
+    return size
 
 
 def fa_decode_tree(cache: KvCache, q, mask=None, lens=None, scale: float | None = None, o=None,
@@ -650,8 +678,9 @@ def fa_decode_tree(cache: KvCache, q, mask=None, lens=None, scale: float | None 
     B, Hkv, cap, d = cache._shape
     if q.dim() != 4:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, Hq, T, d]")
-    Hq, T = q.shape[1], q.shape[2]
-    _check_on(cache, q, "q", torch.bfloat16, (B, Hq, T, d))
+    _, Hq, T, _ = q.shape
+    shape = (B, Hq, T, d)
+    _check_on(cache, q, "q", torch.bfloat16, shape)
     lens = cache._t[4] if lens is None else lens
     _check_ints(cache, lens, "lens", (B,))
     stride = 0
@@ -659,29 +688,26 @@ def fa_decode_tree(cache: KvCache, q, mask=None, lens=None, scale: float | None 
         stride = T if mask.dim() == 2 else 0
         _check_on(cache, mask, "mask", torch.int64, (B, T) if stride else (T,))
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if o is None:
-        o = torch.empty_like(q)
-    else:
-        _check_on(cache, o, "o", torch.bfloat16, (B, Hq, T, d))
-    if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-    else:
-        _check_on(cache, lse, "lse", torch.float32, (B, Hq, T))
-    if workspace is None:
-        need = fa_decode_tree_workspace_size(cache, Hq, T)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    else:
+    for t, name, dtype, shp in ((o, "o", torch.bfloat16, shape),
+                                (lse, "lse", torch.float32, shape[:3])):
+        if t is not None:
+            _check_on(cache, t, name, dtype, shp)
+    if workspace is not None:
         _check_workspace(workspace)
         if _device_index(workspace) != cache._dev:
             raise ValueError(f"workspace is on device {_device_index(workspace)}, the cache on "
                              f"device {cache._dev}")
-    with _device_guard(cache._dev):
-        st = library().fa_decode_tree(cache._ref, _ptr(q), _ptr(lens), _ptr(mask), stride,
-                                      _ptr(o), _ptr(lse), Hq, T, float(scale), _ptr(workspace),
-                                      workspace.numel(),
-                                      ctypes.c_void_p(_stream_handle(stream, q.device)))
-    if st != FA_OK:
-        raise FaError(st, "fa_decode_tree")
+    if o is None or lse is None or workspace is None:
+        with _alloc_on(cache, stream):
+            o = torch.empty_like(q) if o is None else o
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device) \
+                if lse is None else lse
+            if workspace is None:
+                need = fa_decode_tree_workspace_size(cache, Hq, T)
+                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _cache_call(cache, library().fa_decode_tree, stream, q.data_ptr(), lens.data_ptr(),
+                None if mask is None else mask.data_ptr(), stride, o.data_ptr(), lse.data_ptr(),
+                Hq, T, float(scale), workspace.data_ptr(), workspace.numel())
     return o, lse
 
 

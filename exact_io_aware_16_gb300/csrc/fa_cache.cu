@@ -2,13 +2,13 @@
 // quantised to e4m3 with a power-of-two scale for each row), reading rows back
 // in bf16, and moving the accepted path of a drafted tree into place.
 //
-// All three are copies with a conversion on the way: every byte is touched
-// once, so the calls are bound by HBM for prompts and by launch latency for
-// single tokens.  A row of d elements belongs to a group of d / 8 lanes, eight
-// elements a lane: 16-byte bf16 accesses and 8-byte code accesses, both
-// contiguous over the group, and a row's maximum takes log2(d / 8) shuffles.
-// Each thread has kRows rows in flight, so that a load's latency is paid once
-// for all of them.
+// All three are copies with a conversion on the way: every byte is touched once, so
+// the calls are bound by HBM for prompts and by launch latency for single tokens.
+// A row of d elements belongs to d / 16 lanes, sixteen elements a lane: two 16-byte
+// accesses in bf16 and one in e4m3, and a row's maximum takes log2(d / 16) shuffles.
+// (Eight elements a lane spent 9 instructions an element on the quantiser, and
+// wrote a prompt of 4 x 8 x 8192 rows at 3.9 TB/s.)  Each thread has kRows rows in
+// flight, so that a load's latency is paid once for all of them.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,9 +25,16 @@ namespace {
 constexpr int kMoveThreads = 256;
 constexpr int kRows = 4;  // rows in flight a thread
 
-// Two bf16 (one word) times s as two e4m3 codes.  x * 0 turns an infinity into
-// NaN before the saturating conversion would make it 448.
+// Two bf16 (one word) times s as two e4m3 codes.
 __device__ __forceinline__ uint32_t codes2(uint32_t w, float s) {
+  return __nv_cvt_float2_to_fp8x2(
+      make_float2(__uint_as_float(w << 16) * s, __uint_as_float(w & 0xffff0000u) * s),
+      __NV_SATFINITE, __NV_E4M3);
+}
+
+// The same where the word may hold infinities, which the saturating conversion
+// would make 448: x * 0 turns them into NaN.
+__device__ __noinline__ uint32_t codes2_any(uint32_t w, float s) {
   const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
   return __nv_cvt_float2_to_fp8x2(
       make_float2(fmaf(lo, 0.0f, lo * s), fmaf(hi, 0.0f, hi * s)), __NV_SATFINITE, __NV_E4M3);
@@ -41,11 +48,23 @@ __device__ __forceinline__ uint32_t values2(uint32_t c, float s) {
   return pack_bf16x2(f.x * s, f.y * s);
 }
 
-// One block: kMoveThreads / (D / 8) * kRows consecutive rows of one tensor.
+__device__ __forceinline__ uint32_t abs_max(const uint4& x) {
+  return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                  __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+}
+
+// Where row r of [B][Hkv][N] lies: its (sequence, head) pair, sequence and index.
+struct RowAt {
+  int bh, b, i;
+  __device__ __forceinline__ RowAt(const CacheMoveArgs& a, int r)
+      : bh(a.by_n.divide(r)), b(a.by_heads.divide(bh)), i(r - bh * a.N) {}
+};
+
+// One block: kMoveThreads / (D / 16) * kRows consecutive rows of one tensor.
 // Rows run over [B][Hkv][N]; blockIdx.y picks keys or values.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const CacheMoveArgs a) {
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 16;
   constexpr int kGroups = kMoveThreads / kLanes;
   const bool val = blockIdx.y != 0;
   const uint4* __restrict__ in = static_cast<const uint4*>(val ? a.in_v : a.in_k);
@@ -54,37 +73,55 @@ __global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const Cach
   const int lane = threadIdx.x % kLanes;
   const int rows = a.c.B * a.c.Hkv * a.N;
   const int r0 = blockIdx.x * (kGroups * kRows) + threadIdx.x / kLanes;
-  uint4 x[kRows];
+  uint4 x[kRows][2];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const int r = r0 + u * kGroups;
-    x[u] = r < rows ? in[static_cast<long long>(r) * kLanes + lane] : make_uint4(0, 0, 0, 0);
+    const uint4* src = in + (static_cast<long long>(r) * kLanes + lane) * 2;
+    x[u][0] = r < rows ? __ldcs(src) : make_uint4(0, 0, 0, 0);
+    x[u][1] = r < rows ? __ldcs(src + 1) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const int r = r0 + u * kGroups;
-    const int bh = r / a.N, i = r - bh * a.N;
-    const int b = bh / a.c.Hkv;
     uint32_t m = 0;
     if (E4M3) {
-      m = finite_max8(x[u]);
+      m = __vmaxu2(abs_max(x[u][0]), abs_max(x[u][1]));
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
       m = max(m & 0xffffu, m >> 16);
     }
+    const bool finite = m < 0x7f80u;
+    if (E4M3 && !__all_sync(0xffffffffu, finite)) {  // some row here: over its finite elements
+      uint32_t f = __vmaxu2(finite_max8(x[u][0]), finite_max8(x[u][1]));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) f = __vmaxu2(f, __shfl_xor_sync(0xffffffffu, f, o));
+      if (!finite) m = max(f & 0xffffu, f >> 16);
+    }
     if (r >= rows) continue;
-    const long long pos = static_cast<long long>(a.at[b]) + i;
-    if ((a.counts && i >= a.counts[b]) || pos < 0 || pos >= a.c.cap) continue;
-    const long long dst = static_cast<long long>(bh) * a.c.cap + pos;
+    const RowAt at(a, r);
+    const long long pos = static_cast<long long>(__ldg(a.at + at.b)) + at.i;
+    if ((a.counts && at.i >= __ldg(a.counts + at.b)) || pos < 0 || pos >= a.c.cap) continue;
+    const long long dst = static_cast<long long>(at.bh) * a.c.cap + pos;
     if (E4M3) {
       const int e = scale_exponent(m);
       const float s = pow2_of(-e);
-      static_cast<uint2*>(out)[dst * kLanes + lane] =
-          make_uint2(codes2(x[u].x, s) | codes2(x[u].y, s) << 16,
-                     codes2(x[u].z, s) | codes2(x[u].w, s) << 16);
+      uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w,
+                       x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+      if (finite) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = codes2(w[i], s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = codes2_any(w[i], s);
+      }
+      static_cast<uint4*>(out)[dst * kLanes + lane] =
+          make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
       if (lane == 0) scale[dst] = static_cast<uint8_t>(e + 127);
     } else {
-      static_cast<uint4*>(out)[dst * kLanes + lane] = x[u];
+      uint4* to = static_cast<uint4*>(out) + (dst * kLanes + lane) * 2;
+      to[0] = x[u][0];
+      to[1] = x[u][1];
     }
   }
 }
@@ -92,7 +129,7 @@ __global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const Cach
 // The inverse, with zeros in rows that are not read.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) fa_cache_read_kernel(const CacheMoveArgs a) {
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 16;
   constexpr int kGroups = kMoveThreads / kLanes;
   const bool val = blockIdx.y != 0;
   const void* in = val ? a.c.v : a.c.k;
@@ -101,38 +138,44 @@ __global__ void __launch_bounds__(kMoveThreads) fa_cache_read_kernel(const Cache
   const int lane = threadIdx.x % kLanes;
   const int rows = a.c.B * a.c.Hkv * a.N;
   const int r0 = blockIdx.x * (kGroups * kRows) + threadIdx.x / kLanes;
-  uint4 x[kRows];
+  uint4 x[kRows][E4M3 ? 1 : 2];
   uint32_t s[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const int r = r0 + u * kGroups;
-    x[u] = make_uint4(0, 0, 0, 0);
+    x[u][0] = make_uint4(0, 0, 0, 0);
+    if (!E4M3) x[u][E4M3 ? 0 : 1] = make_uint4(0, 0, 0, 0);
     s[u] = 127;
     if (r >= rows) continue;
-    const int bh = r / a.N, i = r - bh * a.N;
-    const int b = bh / a.c.Hkv;
-    const long long pos = static_cast<long long>(a.at ? a.at[b] : 0) + i;
-    if (i >= a.counts[b] || pos < 0 || pos >= a.c.cap) continue;
-    const long long src = static_cast<long long>(bh) * a.c.cap + pos;
-    if (E4M3) {
-      const uint2 c = static_cast<const uint2*>(in)[src * kLanes + lane];
-      x[u].x = c.x;
-      x[u].y = c.y;
+    const RowAt at(a, r);
+    const long long pos = static_cast<long long>(a.at ? __ldg(a.at + at.b) : 0) + at.i;
+    if (at.i >= __ldg(a.counts + at.b) || pos < 0 || pos >= a.c.cap) continue;
+    const long long src = static_cast<long long>(at.bh) * a.c.cap + pos;
+    if constexpr (E4M3) {
+      x[u][0] = static_cast<const uint4*>(in)[src * kLanes + lane];
       s[u] = scale[src];
     } else {
-      x[u] = static_cast<const uint4*>(in)[src * kLanes + lane];
+      const uint4* from = static_cast<const uint4*>(in) + (src * kLanes + lane) * 2;
+      x[u][0] = from[0];
+      x[u][1] = from[1];
     }
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const int r = r0 + u * kGroups;
     if (r >= rows) continue;
-    if (E4M3) {
+    uint4* to = out + (static_cast<long long>(r) * kLanes + lane) * 2;
+    if constexpr (E4M3) {
       const float f = pow2_of(static_cast<int>(s[u]) - 127);
-      x[u] = make_uint4(values2(x[u].x & 0xffffu, f), values2(x[u].x >> 16, f),
-                        values2(x[u].y & 0xffffu, f), values2(x[u].y >> 16, f));
+      const uint4 c = x[u][0];
+      to[0] = make_uint4(values2(c.x & 0xffffu, f), values2(c.x >> 16, f),
+                         values2(c.y & 0xffffu, f), values2(c.y >> 16, f));
+      to[1] = make_uint4(values2(c.z & 0xffffu, f), values2(c.z >> 16, f),
+                         values2(c.w & 0xffffu, f), values2(c.w >> 16, f));
+    } else {
+      to[0] = x[u][0];
+      to[1] = x[u][1];
     }
-    out[static_cast<long long>(r) * kLanes + lane] = x[u];
   }
 }
 
@@ -197,14 +240,17 @@ __global__ void __launch_bounds__(kMoveThreads) __cluster_dims__(kCommitCtas, 1,
 
 template <int D, bool E4M3>
 dim3 move_grid(const CacheMoveArgs& a) {
-  constexpr long long per = kMoveThreads / (D / 8) * kRows;
+  constexpr long long per = kMoveThreads / (D / 16) * kRows;
   const long long rows = static_cast<long long>(a.c.B) * a.c.Hkv * a.N;
   return dim3(static_cast<unsigned>((rows + per - 1) / per), 2, 1);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_write(const CacheMoveArgs& a, cudaStream_t s) {
+cudaError_t launch_cache_write(const CacheMoveArgs& args, cudaStream_t s) {
+  CacheMoveArgs a = args;
+  a.by_n = FastDivide(a.N);
+  a.by_heads = FastDivide(a.c.Hkv);
   const bool f8 = a.c.format == FA_CACHE_E4M3;
   if (a.c.d == 64) {
     if (f8)
@@ -220,7 +266,10 @@ cudaError_t launch_cache_write(const CacheMoveArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_read(const CacheMoveArgs& a, cudaStream_t s) {
+cudaError_t launch_cache_read(const CacheMoveArgs& args, cudaStream_t s) {
+  CacheMoveArgs a = args;
+  a.by_n = FastDivide(a.N);
+  a.by_heads = FastDivide(a.c.Hkv);
   const bool f8 = a.c.format == FA_CACHE_E4M3;
   if (a.c.d == 64) {
     if (f8)

@@ -107,6 +107,26 @@ inline int decode_splits_run(long long BH, int Nk, int num_sms) {
 constexpr int kScaleExpMin = -100;
 constexpr int kScaleExpMax = 119;
 
+// Division of 0 <= n < 2^31 by a number fixed before the launch: with L = ceil(log2 d)
+// and M = ceil(2^(31 + L) / d), M d exceeds 2^(31 + L) by less than d <= 2^L, so that
+// floor(n M / 2^(31 + L)) = floor(n / d) for n < 2^31.
+struct FastDivide {
+  uint32_t m = 0;
+  int shift = 0;
+  FastDivide() = default;
+  explicit FastDivide(int d) {
+    if (d <= 1) return;  // m = 0: n itself
+    int L = 0;
+    while ((1ll << L) < d) ++L;
+    m = static_cast<uint32_t>(((1ull << (31 + L)) + d - 1) / d);
+    shift = L - 1;
+  }
+  __host__ __device__ __forceinline__ int divide(int n) const {
+    if (m == 0) return n;
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> 32 >> shift);
+  }
+};
+
 // Rows of a cache tensor moved by a cache write, read or commit.
 struct CacheMoveArgs {
   fa_cache c;
@@ -119,6 +139,7 @@ struct CacheMoveArgs {
   const int* path;    // commit
   int* new_lens;      // commit
   int N;              // rows a sequence (commit: T)
+  FastDivide by_n, by_heads;
 };
 
 struct TreeArgs {

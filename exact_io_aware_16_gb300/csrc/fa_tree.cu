@@ -46,6 +46,7 @@
 // thread forms t_j = scale log2(e) 2^(k_j) S_j + e_j, keeps M = max t_j, and
 // gives P_j = 2^(t_j - M) to the product with the codes, while the sum takes
 // P_j 2^(-e_j); o = O / l needs no further factor.
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1325,9 +1326,18 @@ template <int D, bool F8, int NR>
 cudaError_t launch_tile(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t s) {
   constexpr uint32_t smem = TreeLayout<D, F8, NR>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(fa_tree_kernel<D, F8, NR>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // once a device (it outlasts the call)
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(fa_tree_kernel<D, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
   fa_tree_kernel<D, F8, NR>
       <<<static_cast<unsigned>(p.shares) * p.row_tiles, TreeLayout<D, F8, NR>::kThreads, smem, s>>>(tk, tv, p);
   return cudaGetLastError();

@@ -121,6 +121,7 @@ class StubLib:
             self.calls.append(name)
             return 512 if name.endswith("workspace_size") else 0
 
+        fn.__name__ = name
         return fn
 
 
