@@ -521,3 +521,38 @@ def test_tree_on_two_streams_and_repeated(fa):
     ok(fa)
     for o, lse in got:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("Hkv", (1, 8))
+@pytest.mark.parametrize("T", (1, 5, 24))
+def test_tree_one_workspace_for_many_calls(fa, Hkv, T):
+    """One workspace, its contents arbitrary at first, serves calls of changing lengths
+    one after the other: each gives the bits of a call with a workspace of its own."""
+    B, d, cap = 3, 128, 6000
+    cache = make_cache(fa, "e4m3", B, Hkv, cap, d, [cap] * B, T, seed=80, junk=False)
+    q = rnd(81, B, 4 * Hkv, T, d).cuda()
+    ws = torch.full((fa.fa_decode_tree_workspace_size(cache, 4 * Hkv, T),), 0xA5, dtype=torch.uint8, device="cuda")
+    g = np.random.RandomState(82)
+    got, want = [], []
+    for i in range(40):
+        n = i32([int(x) for x in g.randint(0, cap - T, B)])
+        got.append(fa.fa_decode_tree(cache, q, lens=n, workspace=ws))
+        want.append(fa.fa_decode_tree(cache, q, lens=n))
+    ok(fa)
+    for (o, lse), (o2, lse2) in zip(got, want):
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_tree_on_a_raw_stream_allocates_there(fa):
+    """A call given a stream by its handle: its own tensors belong to that stream."""
+    cache = make_cache(fa, "bf16", 1, 2, 2000, 64, [1900], 4, seed=90)
+    q, n = rnd(91, 1, 4, 4, 64).cuda(), i32([1900])
+    want = fa.fa_decode_tree(cache, q, lens=n)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        o, lse = fa.fa_decode_tree(cache, q, lens=n, stream=stream)
+        k, v = fa.fa_cache_read(cache, 10, counts=n, stream=stream)
+        ok(fa)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert torch.equal(k, cache.k[:, :, :10]) and torch.equal(v, cache.v[:, :, :10])
