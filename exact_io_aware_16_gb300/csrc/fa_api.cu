@@ -581,8 +581,11 @@ int fa_cache_commit(const fa_cache* cache, const int* lens, const int* path,
 // Query shapes of a tree decode over a valid cache.
 static int check_tree_shape(const fa_cache* c, int Hq, int T) {
   if (Hq < 1 || T < 1 || T > FA_TREE_MAX_DRAFTS || Hq % c->Hkv != 0) return FA_ERR_SHAPE;
-  if (static_cast<long long>(c->B) * Hq > 0x7fffffffll / T) return FA_ERR_SHAPE;
-  return FA_OK;
+  if (c->B > fa::kTreeMaxBatch || static_cast<long long>(c->B) * Hq > 0x7fffffffll / T)
+    return FA_ERR_SHAPE;
+  // the units of the split are an int32 count
+  const long long units = fa::num_tiles(c->cap, fa::kTreeTile) + fa::kTreePairCost;
+  return static_cast<long long>(c->B) * c->Hkv * units > 0x3fffffffll ? FA_ERR_SHAPE : FA_OK;
 }
 
 size_t fa_decode_tree_workspace_size(const fa_cache* cache, int Hq, int T) {

@@ -67,11 +67,7 @@ constexpr int kMaxSlots = 8;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Units of a pair besides its tiles: its start and end take about 4 us of a CTA, a
-// tile 0.7 to 1.5 us.  16 sequences of 333 to 8192 tokens x 8 heads, 4 rows, e4m3:
-// 50.6 us with 2, 49.1 with 4, 49.2 with 5; 4 sequences of up to 32K tokens 115 and
-// 114 us.
-constexpr int kPairCost = 4;
+constexpr int kPairCost = kTreePairCost;
 
 // -M of a row that has seen no key: any finite score passes the reference, and
 // -inf stays -inf.

@@ -266,7 +266,8 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, 
  *  - k, v: DEVICE [B][Hkv][cap][d], two bytes (FA_CACHE_BF16) or one byte
  *    (FA_CACHE_E4M3) an element, 16-byte aligned.
  *  - k_scale, v_scale: DEVICE uint8 [B][Hkv][cap], 16-byte aligned, for
- *    FA_CACHE_E4M3; ignored for FA_CACHE_BF16.  A row x[0..d) of one token and
+ *    FA_CACHE_E4M3 (bytes 27 .. 246 in rows that are read or attended to, as
+ *    fa_cache_write stores them); ignored for FA_CACHE_BF16.  A row x[0..d) of one token and
  *    key head is held as codes c and one scale byte s with x ~ c * 2^(s - 127):
  *    e = s - 127 is the least exponent with max|x| * 2^-e <= 448 over the
  *    finite elements, kept within -100 .. 119, and c = x * 2^-e rounded to
@@ -300,7 +301,7 @@ typedef struct fa_cache {
  * i < counts[b], goes to position lens[b] + i of the cache.  k, v: bf16
  * [B][Hkv][N][d].  Rows whose position lies outside 0 .. cap-1 are not
  * written, and every other position stays as it was.  lens is not changed.
- * B*Hkv*N below 2^30.
+ * N >= 1, B*Hkv*N below 2^30.
  */
 int fa_cache_write(const fa_cache* cache, const void* k, const void* v, const int* lens,
                    const int* counts, int N, void* stream);
@@ -308,7 +309,8 @@ int fa_cache_write(const fa_cache* cache, const void* k, const void* v, const in
 /*
  * Reads a window back in bf16: row i of k, v (bf16 [B][Hkv][N][d]) is position
  * first[b] + i of sequence b (first NULL: i) for i < counts[b], and zero for the
- * other i < N and for positions outside 0 .. cap-1.  B*Hkv*N below 2^30.
+ * other i < N and for positions outside 0 .. cap-1.  N >= 1, B*Hkv*N below
+ * 2^30.
  */
 int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, const int* counts,
                   int N, void* stream);
@@ -326,13 +328,19 @@ int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, con
  * o = 0 and lse = -inf.  What lies in the cache behind the drafts, or in drafts
  * that no row of the sequence sees, never reaches a result, and a NaN or
  * infinity in a draft's value row reaches only the rows that see that draft.
- *  - 1 <= T <= 64, Hq >= 1, B * Hq * T below 2^31.  scale > 0 and finite.
+ *  - 1 <= T <= 64, Hq >= 1, B <= 65536, B * Hq * T below 2^31, B * Hkv *
+ *    (ceil(cap / 128) + 4) below 2^30.  scale > 0 and finite.
  *  - workspace: device memory, 256-byte aligned, contents irrelevant, of
  *    fa_decode_tree_workspace_size() bytes (0 for an invalid shape).  Calls
  *    that may overlap on the GPU need workspaces of their own.
- *  - Accuracy: as fa_decode (probabilities rounded to bf16 before the product
- *    with V); with an e4m3 cache the products run on e4m3 operands, with q and
- *    the probabilities each as the sum of two e4m3 pieces.
+ *  - Accuracy, bf16: as fa_decode (probabilities rounded to bf16 before the
+ *    product with V).  e4m3: the products run on the cache's codes, with q and the
+ *    probabilities each as the sum of two e4m3 pieces; an element of q is held to
+ *    2^-17.8 of the largest finite |q| of the 64 query rows that share a tile (to
+ *    all its bits if it is within 2^-9 of it), a probability to 2^-8 of its value.
+ *  - A NaN or infinity in q makes its own row NaN.  Scores are taken in fp32 and
+ *    in units of ln 2: a row whose scores are all below -1e38 counts as one that
+ *    sees nothing.
  */
 #define FA_TREE_MAX_DRAFTS 64
 size_t fa_decode_tree_workspace_size(const fa_cache* cache, int Hq, int T);

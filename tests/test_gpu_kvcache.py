@@ -543,6 +543,30 @@ def test_tree_one_workspace_for_many_calls(fa, Hkv, T):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_two_graphs_share_a_workspace(fa):
+    """Two captured calls of different shapes on one workspace, replayed in turn."""
+    d, cap, T = 128, 5000, 12
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    calls = []
+    for fmt, B, Hkv, seed in (("e4m3", 1, 1, 100), ("bf16", 2, 4, 101)):
+        cache = make_cache(fa, fmt, B, Hkv, cap, d, [cap] * B, T, seed=seed, junk=False)
+        q, n = rnd(seed + 10, B, 2 * Hkv, T, d).cuda(), i32([4900] * B)
+        assert fa.fa_decode_tree_workspace_size(cache, 2 * Hkv, T) <= ws.numel()
+        fa.fa_decode_tree(cache, q, lens=n, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = fa.fa_decode_tree(cache, q, lens=n, workspace=ws)
+        calls.append((cache, q, n, g, out))
+    for i in range(6):
+        for cache, q, n, g, (o, lse) in calls:
+            n.fill_(4900 - 700 * i)
+            g.replay()
+            oe, le = fa.fa_decode_tree(cache, q, lens=n)
+            ok(fa)
+            assert torch.equal(o, oe) and torch.equal(lse, le)
+
+
 def test_tree_on_a_raw_stream_allocates_there(fa):
     """A call given a stream by its handle: its own tensors belong to that stream."""
     cache = make_cache(fa, "bf16", 1, 2, 2000, 64, [1900], 4, seed=90)

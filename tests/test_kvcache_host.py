@@ -108,6 +108,20 @@ def test_tree_refusals(lib):
         assert lib.fa_decode_tree_workspace_size(c, Hq, T) == 0
 
 
+@pytest.mark.parametrize("B,Hkv,cap,st", [
+    (65537, 1, 16, -2),          # more sequences than a CTA walks over
+    (65536, 1, 16, -6),
+    (65536, 1 << 12, 16, -2),    # 2^28 pairs of 5 units
+    (2, 1, 2147483392, -6),      # the largest capacity
+    (65, 1, 2147483392, -2),     # more than 2^30 units
+])
+def test_tree_size_limits(lib, B, Hkv, cap, st):
+    """-6: the shape passes, and the workspace of no bytes is refused."""
+    c = cache(B=B, Hkv=Hkv, cap=cap)
+    assert tree(lib, c, Hq=Hkv, T=1, wb=0) == st
+    assert (lib.fa_decode_tree_workspace_size(c, Hkv, 1) > 0) == (st == -6)
+
+
 # ---------------------------------------------------------------- binding
 class StubLib:
     def __init__(self):
