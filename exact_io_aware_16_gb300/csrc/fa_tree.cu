@@ -69,9 +69,22 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 constexpr int kPairCost = kTreePairCost;
 
+constexpr int kNoExponent = 1000;  // of rows of zeros
+
 // -M of a row that has seen no key: any finite score passes the reference, and
 // -inf stays -inf.
 constexpr float kUnseen = 1e38f;
+
+// e4m3 queries: the pieces of a row tile's queries share one power of two, 2^e of the
+// tile's largest element, where each row's own would be at most 2^kNear smaller; a
+// product of an element and a code is then off by at most 2^-12.8 of the row's largest.  Rows
+// that differ by more (a padded row may hold anything) have each its own power of two
+// and the softmax a product more for two scores: 64 rows over 4 x 8 heads of 32K to
+// 64K keys take 127 instead of 114 us so.
+struct Queries {
+  static constexpr int kNear = 4;
+  static constexpr float kByRow = -1.0f;  // in place of the factor of all rows
+};
 
 // A row's accumulator is rescaled only when its maximum grows by more than
 // kLog2 binades.  bf16 has the range for any P; for e4m3 P is scaled so that 2^kLog2
@@ -91,7 +104,7 @@ struct PairInfo {
   int valid;               // 0 behind the last pair
   unsigned int bad[2];     // drafts whose value row holds NaN or infinities
   unsigned long long any;  // drafts that some row of the sequence sees
-  unsigned int qmax;       // largest finite |q| of the row tile, as bf16 bits (e4m3)
+  int qmax, qmin;          // e4m3: greatest and least exponent of the tile's queries
 };
 
 struct TreeBars {
@@ -111,6 +124,7 @@ struct TreeRows {
   unsigned long long seen[NR];  // mask row
   float m[NR];      // reference exponent, -inf before the first key
   float neg_m[NR];  // its negative: kUnseen before the first key, -inf for rows past R
+  float unit[NR];   // scale log2(e) times the unit of the row's query pieces (see Queries)
   float alpha[NR];  // of the last move
   float inv[NR];    // epilogue: what O is multiplied by
   float part[4][NR];            // a warp's maximum or sum
@@ -287,7 +301,9 @@ __device__ __forceinline__ void next_pair(const TreeParams& p, TreeBars* bars, c
   to.nt = len_tiles(p, to.len);
   to.t0 = 0;
   to.tiles = min(to.nt, bars->unit1 - to.u0 - kPairCost);
-  to.bad[0] = to.bad[1] = to.qmax = 0;
+  to.bad[0] = to.bad[1] = 0;
+  to.qmax = -kNoExponent;
+  to.qmin = kNoExponent;
 }
 
 // ------------------------------------------------------------ tensor memory
@@ -460,18 +476,16 @@ struct PairLoads {
 };
 
 // The row tile's query rows as the swizzled operand of S^T (rows past `have` are
-// zeros), and their mask rows.  e4m3: two pieces of the rows times 2^-e, e from the
-// largest of the tile's elements; the return value is 2^e.  (An exponent for every
-// row would cost the softmax a product for every score.  A score is off by what the
-// largest row's is: 2^-17.8 max|q| sum|k|, scaled.)
+// zeros), and their mask rows.  e4m3: two pieces of the rows times 2^-e (Queries).  The
+// return value is scale log2(e), times 2^e, or kByRow.
 template <int D, bool F8, int NR>
 __device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
                                                const PairLoads<D, NR>& in, int have,
-                                               unsigned int* qmax) {
+                                               float scale_log2, PairInfo* pair) {
   using L = TreeLayout<D, F8, NR>;
   constexpr int kPer = PairLoads<D, NR>::kPer, kGran = PairLoads<D, NR>::kGran;
   const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
-  float unit = 1.0f;
+  float factor = scale_log2;
   if (part == 0) {
     rows->m[r] = -INFINITY;
     rows->neg_m[r] = r < have ? kUnseen : -INFINITY;
@@ -491,12 +505,26 @@ __device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
 #pragma unroll
       for (int k = 0; k < 4; ++k) all = __vmaxu2(all, word(in.q[i], k) & 0x7fff7fffu);
     }
-    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-    if ((threadIdx.x & 31) == 0) atomicMax(qmax, m);
+#pragma unroll
+    for (int o = kPer / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = max(m & 0xffffu, m >> 16);
+    int e = scale_exponent(m);
+    const int e_max = __reduce_max_sync(0xffffffffu, m ? e : -kNoExponent);
+    const int e_min = __reduce_min_sync(0xffffffffu, m ? e : kNoExponent);
+    if ((threadIdx.x & 31) == 0) {
+      atomicMax(&pair->qmax, e_max);
+      atomicMin(&pair->qmin, e_min);
+    }
     named_bar_sync(1, L::kSoft);
-    const int e = scale_exponent(*static_cast<volatile unsigned int*>(qmax));
+    const int top = *static_cast<volatile int*>(&pair->qmax);
+    if (top - *static_cast<volatile int*>(&pair->qmin) <= Queries::kNear) {
+      e = top == -kNoExponent ? 0 : top;
+      factor *= pow2_of(e);
+    } else {
+      if (part == 0) rows->unit[r] = scale_log2 * pow2_of(e);
+      factor = Queries::kByRow;
+    }
     const float s = pow2_of(-e);
-    unit = pow2_of(e);
 #pragma unroll
     for (int i = 0; i < kGran; ++i) {
       uint32_t hi[4], lo[4];
@@ -511,7 +539,7 @@ __device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
     // NaN or infinities in the row: its scores are NaN
     if (max(all & 0xffffu, all >> 16) >= 0x7f80u && r < have) rows->neg_m[r] = NAN;
   }
-  return unit;
+  return factor;
 }
 
 // ------------------------------------------------------------ value rows
@@ -594,6 +622,23 @@ __device__ __forceinline__ void form_scores(uint32_t taddr, const float* neg_m, 
   }
 }
 
+// The same with a factor for each row.
+template <bool M>
+__device__ __noinline__ void form_scores_by_row(uint32_t taddr, const float* neg_m,
+                                                const float* unit, float ks, float ev,
+                                                f32x2 (&x)[8]) {
+  uint32_t s[16];
+  tmem_ld16(taddr, s);
+  tmem_ld_wait();
+  reg_pin(s);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const float m0 = M ? ev + neg_m[2 * r] : ev, m1 = M ? ev + neg_m[2 * r + 1] : ev;
+    x[r] = pack2(fmaf(__uint_as_float(s[2 * r]), ks * unit[2 * r], m0),
+                 fmaf(__uint_as_float(s[2 * r + 1]), ks * unit[2 * r + 1], m1));
+  }
+}
+
 // Rows that do not see the key: -inf.
 __device__ __forceinline__ void hide_rows(f32x2 (&x)[8], uint32_t hidden) {
 #pragma unroll
@@ -616,12 +661,16 @@ __device__ __noinline__ uint32_t hidden_rows(const unsigned long long* seen, int
 }
 
 // The warp's maximum of each row's scores into out[16].
+// unit: null where all rows have one factor.
 template <bool F8>
-__device__ __noinline__ void row_maxima(uint32_t taddr, float ks, float ev, uint32_t hidden,
-                                        float* out) {
+__device__ __noinline__ void row_maxima(uint32_t taddr, const float* unit, float ks, float ev,
+                                        uint32_t hidden, float* out) {
   const int lane = threadIdx.x & 31;
   f32x2 t[8];
-  form_scores<F8, false>(taddr, nullptr, ks, ev, t);
+  if (F8 && unit)
+    form_scores_by_row<false>(taddr, nullptr, unit, ks, ev, t);
+  else
+    form_scores<F8, false>(taddr, nullptr, ks, ev, t);
   hide_rows(t, hidden);
   float top = -INFINITY;
 #pragma unroll
@@ -789,7 +838,9 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           first.t0 = max(unit0 - u0 - kPairCost, 0);
           first.tiles = min(nt, unit1 - u0 - kPairCost) - first.t0;
           first.valid = 1;
-          first.bad[0] = first.bad[1] = first.qmax = 0;
+          first.bad[0] = first.bad[1] = 0;
+          first.qmax = -kNoExponent;
+          first.qmin = kNoExponent;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
         if (unit0 < before) break;
@@ -994,7 +1045,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       }
     };
     f32x2 l[8];             // sums of this key column, by row
-    float factor = 0.0f;    // scale log2(e) and the unit of the query pieces
+    float factor = 0.0f;    // scale log2(e) and the unit of the query pieces, or kByRow
 #pragma unroll 1
     for (;; ++seg) {
       // ---- the next pair's queries: S of the last tile is complete, so that Q is
@@ -1007,8 +1058,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         if (tid == 0) next_pair(p, bars, next, bars->pair[(seg + 1) & 3]);
         if (seg > 0) ok = product_done(it - 1, ok, bars, 0x526);
         __syncwarp();
-        factor = p.scale_log2 *
-                 store_queries<D, F8, NR>(smem + L::kQ, rows, in, have, &next.qmax);
+        factor = store_queries<D, F8, NR>(smem + L::kQ, rows, in, have, p.scale_log2, &next);
         const unsigned long long any = in.drafts(p);
         if (tid == 0) next.any = any;
         fence_proxy_async_smem();
@@ -1125,15 +1175,29 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         if (t >= first_edge) {
           if (pos >= len) hidden = pos < end ? hidden_rows(rows->seen + own, pos - len) : 0xffffu;
           if (hidden == 0xffffu) {  // perhaps never written: finite scales for P = 0
-            ks = wv = 1.0f;
+            ks = factor;
+            wv = 1.0f;
             ev = 0.0f;
           }
         }
         // ---- x = t - M of this key for the thread's rows
         tc_fence_after_sync();
         const uint32_t scol = tlane + (it & 1) * NR + own;
+        float sign = factor;
+        asm volatile("" : "+f"(sign));  // one loop for both
+        const bool by_row = F8 && sign < 0.0f;
+        auto scores = [&](f32x2 (&x)[8]) {
+          if (F8 && by_row) {
+            f32x2 y[8];
+            form_scores_by_row<true>(scol, rows->neg_m + own, rows->unit + own, -ks, ev, y);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) x[r] = y[r];
+          } else {
+            form_scores<F8, true>(scol, rows->neg_m + own, ks, ev, x);
+          }
+        };
         f32x2 x[8];
-        form_scores<F8, true>(scol, rows->neg_m + own, ks, ev, x);
+        scores(x);
         if (hidden) hide_rows(x, hidden);
         float mx = -INFINITY;
 #pragma unroll
@@ -1143,7 +1207,8 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         }
         if (group_bar_or(2 + group, mx > Lazy<F8>::kTop)) {
           // ---- some row grew: new references from the maxima over the group's keys
-          row_maxima<F8>(scol, ks, ev, hidden, rows->part[quad] + own);
+          row_maxima<F8>(scol, by_row ? rows->unit + own : nullptr, by_row ? -ks : ks, ev,
+                         hidden, rows->part[quad] + own);
           named_bar_sync(2 + group, kTile);
           if (key < 16) new_reference<F8, NR>(rows, own + key, have);
           named_bar_sync(2 + group, kTile);
@@ -1159,7 +1224,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               l[r + 1] = mul2(l[r + 1], al.y);
             }
           }
-          form_scores<F8, true>(scol, rows->neg_m + own, ks, ev, x);
+          scores(x);
           if (hidden) hide_rows(x, hidden);
         }
         // ---- P = 2^x over the P buffer that PV(it - 2) has read.  With one issuing warp

@@ -336,9 +336,10 @@ int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, con
  *  - Accuracy, bf16: as fa_decode (probabilities rounded to bf16 before the
  *    product with V).  e4m3: the products run on the cache's codes, with q and the
  *    probabilities each as the sum of two e4m3 pieces; an element of q is held to
- *    2^-17.8 of the largest finite |q| of the 64 query rows that share a tile (to
- *    all its bits if it is within 2^-9 of it), a probability to 2^-8 of its value.
- *  - A NaN or infinity in q makes its own row NaN.  Scores are taken in fp32 and
+ *    2^-12.8 of the largest finite one of its row or better, a probability to 2^-8
+ *    of its value.
+ *  - What a row of q holds reaches no other row, and a NaN or infinity in it makes
+ *    its own row NaN.  Scores are taken in fp32 and
  *    in units of ln 2: a row whose scores are all below -1e38 counts as one that
  *    sees nothing.
  */

@@ -78,10 +78,12 @@ def tree(q, k, v, lens, mask, scale, fmt, v_scale=None, qmax=None):
     The bounds follow from the arithmetic, for the keys a row sees:
      - scores: products are exact and added in fp32 (at most d + 8 roundings or
        truncations of 2^-23 of sum|q k|, scaled); an e4m3 cache splits q into
-       two e4m3 pieces of a power-of-two scale that puts the largest |q| of the rows
-       that share a tile (qmax; all of q unless given) in (224, 448]: an element is
-       off by at most 2^-10 of those units, 2^-17.8 of qmax.  ds is the sum of both; e^s is off by at most 2 ds + 2^-20
-       (ex2 and the fp32 sums).
+       two e4m3 pieces of a power-of-two scale.  An element is off by at most 2^-10
+       in the units in which the largest |q| of the rows that share a tile (qmax; all
+       of q unless given) is in (224, 448], 2^-17.8 of qmax; or, where the rows'
+       exponents differ by more than 4, in those of its own row, so by no more than
+       2^-12.8 of the row's largest.  ds is the sum of both; e^s is off by at most
+       2 ds + 2^-20 (ex2 and the fp32 sums).
      - probabilities: rounded to bf16 (2^-8 of the value), or through fp16 (2^-11)
        to two e4m3 pieces (cut to four bits, the rest rounded to four: 2^-8), where
        the first is subnormal off by at most 2^-13, in units in which the largest
@@ -116,7 +118,8 @@ def tree(q, k, v, lens, mask, scale, fmt, v_scale=None, qmax=None):
                     a = p @ np.abs(vv)
                     floor = 0.0
                     if fmt == "e4m3":
-                        ds += 2.0 ** -17.8 * scale * qmax * np.abs(kk).sum(-1).max()
+                        off = min(2.0 ** -17.8 * qmax, 2.0 ** -12.8 * np.abs(q[b, h, t]).max())
+                        ds += off * scale * np.abs(kk).sum(-1).max()
                         w = 2.0 ** (v_scale[b, h // G, see].astype(float) - 127)
                         floor = 2.0 ** -15.8 * (p * w).max() * (np.abs(vv) / w[:, None]).sum(0)
                     each = 2.0 ** -8 if fmt == "bf16" else 2.0 ** -8 + 2.0 ** -11

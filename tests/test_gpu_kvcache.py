@@ -377,6 +377,26 @@ def test_tree_nan_query_and_queries_of_many_sizes(fa, fmt, d):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("Hq,T", ((2, 6), (4, 12), (6, 40)))
+def test_tree_padded_rows_leave_the_others_alone(fa, fmt, Hq, T):
+    """Drafts behind a sequence's own hold anything, in q too: the rows of the others
+    are within their own bounds, over several tiles of keys."""
+    B, Hkv, d, cap, lens = 2, 2, 128, 600, [560, 140]
+    cache = make_cache(fa, fmt, B, Hkv, cap, d, lens, T, seed=75)
+    q = rnd(76, B, Hq, T, d)
+    q[0, :, T - 2] = 1e30
+    q[0, :, T - 1] = -3e38
+    k, v = ref.cache_values(cache)
+    vs = None if fmt == "bf16" else cache.v_scale.cpu().numpy()
+    mask = [[(2 << t) - 1 for t in range(T - 2)] + [0, 0]] * B
+    o, lse = fa.fa_decode_tree(cache, q.cuda(), mask_tensor(mask), lens=i32(lens))
+    ok(fa)
+    t = T - 2
+    want = ref.tree(ref.to64(q[:, :, :t]), k, v, lens, [m[:t] for m in mask], 1 / math.sqrt(d), fmt, vs, qmax=math.inf)
+    check_tree(o[:, :, :t], lse[:, :, :t], want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_tree_large_scores_and_scales(fa, fmt):
     """Rows whose scores spread over hundreds, keys and values over many binades."""
     B, Hq, Hkv, T, d, cap, lens = 1, 4, 1, 3, 128, 704, [690]
