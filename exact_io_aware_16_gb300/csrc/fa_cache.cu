@@ -7,8 +7,11 @@
 // A row of d elements belongs to d / 16 lanes, sixteen elements a lane: two 16-byte
 // accesses in bf16 and one in e4m3, and a row's maximum takes log2(d / 16) shuffles.
 // (Eight elements a lane spent 9 instructions an element on the quantiser, and
-// wrote a prompt of 4 x 8 x 8192 rows at 3.9 TB/s.)  Each thread has kRows rows in
-// flight, so that a load's latency is paid once for all of them.
+// wrote a prompt of 4 x 8 x 8192 rows at 3.9 TB/s.)
+//
+// Measured (d = 128, e4m3; a plain copy runs at 6.79 TB/s): writing 4 x 8 x 8192 rows
+// of keys and values 37 us, 5.5 TB/s; reading them back 34 us, 5.8 TB/s; a token of 8
+// sequences written, or a path of 5 of 16 drafts committed for 4 sequences, 5.5 us.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,7 +26,7 @@ namespace fa {
 namespace {
 
 constexpr int kMoveThreads = 256;
-constexpr int kRows = 4;  // rows in flight a thread
+constexpr int kRows = 4;  // rows in flight a thread (write)
 
 // Two bf16 (one word) times s as two e4m3 codes.
 __device__ __forceinline__ uint32_t codes2(uint32_t w, float s) {
@@ -53,6 +56,18 @@ __device__ __forceinline__ uint32_t abs_max(const uint4& x) {
                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
 }
 
+// 32 bytes at p, in one access where `wide` says that addresses allow it.
+__device__ __forceinline__ void store32(uint4* p, bool wide, const uint4& a, const uint4& b) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    p[0] = a;
+    p[1] = b;
+  }
+}
+
 // Where row r of [B][Hkv][N] lies: its (sequence, head) pair, sequence and index.
 struct RowAt {
   int bh, b, i;
@@ -60,7 +75,8 @@ struct RowAt {
       : bh(a.by_n.divide(r)), b(a.by_heads.divide(bh)), i(r - bh * a.N) {}
 };
 
-// One block: kMoveThreads / (D / 16) * kRows consecutive rows of one tensor.
+// One block: kMoveThreads / (D / 16) * kRows consecutive rows of one tensor; with kRows
+// rows in flight a thread, a load's latency is paid once for all of them.
 // Rows run over [B][Hkv][N]; blockIdx.y picks keys or values.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const CacheMoveArgs a) {
@@ -126,57 +142,39 @@ __global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const Cach
   }
 }
 
-// The inverse, with zeros in rows that are not read.
+// The inverse, with zeros in rows that are not read: one row a group of D / 16 lanes.
+// Two thirds of the bytes are stores, so that more rows in flight a thread gain
+// nothing (4 x 8 x 8192 rows of keys and values in e4m3: 33.9 us with one row, 34.7
+// with two, 34.9 with four), but whole 32-byte sectors do: 36.9 us with two 16-byte
+// stores in place of one of 32 bytes.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) fa_cache_read_kernel(const CacheMoveArgs a) {
   constexpr int kLanes = D / 16;
-  constexpr int kGroups = kMoveThreads / kLanes;
   const bool val = blockIdx.y != 0;
-  const void* in = val ? a.c.v : a.c.k;
-  uint4* __restrict__ out = static_cast<uint4*>(val ? a.out_v : a.out_k);
-  const uint8_t* scale = val ? a.c.v_scale : a.c.k_scale;
   const int lane = threadIdx.x % kLanes;
-  const int rows = a.c.B * a.c.Hkv * a.N;
-  const int r0 = blockIdx.x * (kGroups * kRows) + threadIdx.x / kLanes;
-  uint4 x[kRows][E4M3 ? 1 : 2];
-  uint32_t s[kRows];
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int r = r0 + u * kGroups;
-    x[u][0] = make_uint4(0, 0, 0, 0);
-    if (!E4M3) x[u][E4M3 ? 0 : 1] = make_uint4(0, 0, 0, 0);
-    s[u] = 127;
-    if (r >= rows) continue;
-    const RowAt at(a, r);
-    const long long pos = static_cast<long long>(a.at ? __ldg(a.at + at.b) : 0) + at.i;
-    if (at.i >= __ldg(a.counts + at.b) || pos < 0 || pos >= a.c.cap) continue;
-    const long long src = static_cast<long long>(at.bh) * a.c.cap + pos;
+  const int r = blockIdx.x * (kMoveThreads / kLanes) + threadIdx.x / kLanes;
+  if (r >= a.c.B * a.c.Hkv * a.N) return;
+  const RowAt at(a, r);
+  const long long pos = static_cast<long long>(a.at ? __ldg(a.at + at.b) : 0) + at.i;
+  uint4 x = make_uint4(0, 0, 0, 0), y = x;
+  if (at.i < __ldg(a.counts + at.b) && pos >= 0 && pos < a.c.cap) {
+    const long long row = static_cast<long long>(at.bh) * a.c.cap + pos;
+    const uint4* in = static_cast<const uint4*>(val ? a.c.v : a.c.k);
     if constexpr (E4M3) {
-      x[u][0] = static_cast<const uint4*>(in)[src * kLanes + lane];
-      s[u] = scale[src];
+      const float f = pow2_of(static_cast<int>((val ? a.c.v_scale : a.c.k_scale)[row]) - 127);
+      const uint4 c = in[row * kLanes + lane];
+      x = make_uint4(values2(c.x & 0xffffu, f), values2(c.x >> 16, f),
+                     values2(c.y & 0xffffu, f), values2(c.y >> 16, f));
+      y = make_uint4(values2(c.z & 0xffffu, f), values2(c.z >> 16, f),
+                     values2(c.w & 0xffffu, f), values2(c.w >> 16, f));
     } else {
-      const uint4* from = static_cast<const uint4*>(in) + (src * kLanes + lane) * 2;
-      x[u][0] = from[0];
-      x[u][1] = from[1];
+      const uint4* from = in + (row * kLanes + lane) * 2;
+      x = from[0];
+      y = from[1];
     }
   }
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int r = r0 + u * kGroups;
-    if (r >= rows) continue;
-    uint4* to = out + (static_cast<long long>(r) * kLanes + lane) * 2;
-    if constexpr (E4M3) {
-      const float f = pow2_of(static_cast<int>(s[u]) - 127);
-      const uint4 c = x[u][0];
-      to[0] = make_uint4(values2(c.x & 0xffffu, f), values2(c.x >> 16, f),
-                         values2(c.y & 0xffffu, f), values2(c.y >> 16, f));
-      to[1] = make_uint4(values2(c.z & 0xffffu, f), values2(c.z >> 16, f),
-                         values2(c.w & 0xffffu, f), values2(c.w >> 16, f));
-    } else {
-      to[0] = x[u][0];
-      to[1] = x[u][1];
-    }
-  }
+  store32(static_cast<uint4*>(val ? a.out_v : a.out_k) + (static_cast<long long>(r) * kLanes + lane) * 2,
+          a.wide, x, y);
 }
 
 // One cluster of kCommitCtas CTAs a sequence; its CTAs share the (head, tensor)
@@ -238,7 +236,10 @@ __global__ void __launch_bounds__(kMoveThreads) __cluster_dims__(kCommitCtas, 1,
   if (rank == 0 && threadIdx.x == 0) a.new_lens[b] = valid ? min(len + min(n, a.c.cap), a.c.cap) : len;
 }
 
-template <int D, bool E4M3>
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+// kRows: rows a thread
+template <int D, int kRows>
 dim3 move_grid(const CacheMoveArgs& a) {
   constexpr long long per = kMoveThreads / (D / 16) * kRows;
   const long long rows = static_cast<long long>(a.c.B) * a.c.Hkv * a.N;
@@ -254,14 +255,14 @@ cudaError_t launch_cache_write(const CacheMoveArgs& args, cudaStream_t s) {
   const bool f8 = a.c.format == FA_CACHE_E4M3;
   if (a.c.d == 64) {
     if (f8)
-      fa_cache_write_kernel<64, true><<<move_grid<64, true>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<64, true><<<move_grid<64, kRows>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_write_kernel<64, false><<<move_grid<64, false>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<64, false><<<move_grid<64, kRows>(a), kMoveThreads, 0, s>>>(a);
   } else {
     if (f8)
-      fa_cache_write_kernel<128, true><<<move_grid<128, true>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<128, true><<<move_grid<128, kRows>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_write_kernel<128, false><<<move_grid<128, false>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<128, false><<<move_grid<128, kRows>(a), kMoveThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }
@@ -270,17 +271,18 @@ cudaError_t launch_cache_read(const CacheMoveArgs& args, cudaStream_t s) {
   CacheMoveArgs a = args;
   a.by_n = FastDivide(a.N);
   a.by_heads = FastDivide(a.c.Hkv);
+  a.wide = aligned32(a.out_k) && aligned32(a.out_v);
   const bool f8 = a.c.format == FA_CACHE_E4M3;
   if (a.c.d == 64) {
     if (f8)
-      fa_cache_read_kernel<64, true><<<move_grid<64, true>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<64, true><<<move_grid<64, 1>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_read_kernel<64, false><<<move_grid<64, false>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<64, false><<<move_grid<64, 1>(a), kMoveThreads, 0, s>>>(a);
   } else {
     if (f8)
-      fa_cache_read_kernel<128, true><<<move_grid<128, true>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<128, true><<<move_grid<128, 1>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_read_kernel<128, false><<<move_grid<128, false>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<128, false><<<move_grid<128, 1>(a), kMoveThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }

@@ -46,6 +46,15 @@
 // thread forms t_j = scale log2(e) 2^(k_j) S_j + e_j, keeps M = max t_j, and
 // gives P_j = 2^(t_j - M) to the product with the codes, while the sum takes
 // P_j 2^(-e_j); o = O / l needs no further factor.
+//
+// Measured (d = 128, 8 key heads, the cache larger than L2; % of the rate of a plain
+// copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 92 us in e4m3 (86 %) and
+// 164 us in bf16 (96 %): HBM.  64 rows over 4 sequences of 32K to 64K keys in e4m3
+// 116 us (50 %) and 256 rows over 8 sequences of 4K to 8K keys in bf16 99 us: the
+// softmax, 16 warps that issue half of the cycles (2650 a tile of 128 keys by 64
+// rows), with long waits for tensor memory and the group barrier.  32 rows over 32
+// sequences of 500 to 4096 keys in e4m3 48 us (49 %): starts and ends of pairs, the
+// first loads (5 us) and the merge (3 us or more).  One token over 1000 keys 14 us.
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -105,6 +105,37 @@ def test_write_and_read(fa, fmt, d, B, H, N, cap, lens, counts):
         np.testing.assert_array_equal(ref.to64(r), w)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", (64, 128))
+def test_rows_aligned_to_sixteen_bytes(fa, fmt, d):
+    """Tensors whose addresses allow 16-byte accesses but none of 32 bytes."""
+    B, H, N, cap = 2, 3, 37, 64
+    shape = (B, H, N, d)
+
+    def odd(x):
+        t = torch.full((x.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        t[8:-8] = x.cuda().reshape(-1)
+        v = t[8:-8].view(x.shape)
+        assert v.data_ptr() % 32 == 16
+        return t, v
+
+    k, v = rnd(3, *shape), rnd(4, *shape)
+    caches = [fa.KvCache(B, H, cap, d, fmt) for _ in range(2)]
+    fa.fa_cache_write(caches[0], k.cuda(), v.cuda())
+    fa.fa_cache_write(caches[1], odd(k)[1], odd(v)[1])
+    for x, y in zip(state(caches[0]), state(caches[1])):
+        assert torch.equal(x, y)
+    n = i32([N, 11])
+    want = fa.fa_cache_read(caches[0], N, counts=n)
+    (tk, ok_), (tv, ov) = odd(torch.zeros(shape)), odd(torch.zeros(shape))
+    fa.fa_cache_read(caches[0], N, counts=n, k=ok_, v=ov)
+    fa.fa_cache_read(caches[1], N, counts=n, k=ok_)  # one of each
+    ok(fa)
+    assert torch.equal(ok_, want[0]) and torch.equal(ov, want[1])
+    for t in (tk, tv):
+        assert (t[:8] == 7).all() and (t[-8:] == 7).all()
+
+
 def special_rows():
     """Rows at the borders of the quantiser, d = 64."""
     rows = []
