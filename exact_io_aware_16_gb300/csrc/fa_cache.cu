@@ -26,7 +26,6 @@ namespace fa {
 namespace {
 
 constexpr int kMoveThreads = 256;
-constexpr int kRows = 4;  // rows in flight a thread (write)
 
 // Two bf16 (one word) times s as two e4m3 codes.
 __device__ __forceinline__ uint32_t codes2(uint32_t w, float s) {
@@ -75,78 +74,62 @@ struct RowAt {
       : bh(a.by_n.divide(r)), b(a.by_heads.divide(bh)), i(r - bh * a.N) {}
 };
 
-// One block: kMoveThreads / (D / 16) * kRows consecutive rows of one tensor; with kRows
-// rows in flight a thread, a load's latency is paid once for all of them.
-// Rows run over [B][Hkv][N]; blockIdx.y picks keys or values.
+// Rows run over [B][Hkv][N]; blockIdx.y picks keys or values.  One row a group of D / 16
+// lanes: two or four rows in flight a thread gain 2 % on a prompt and lose 1 us where
+// there are few rows.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const CacheMoveArgs a) {
   constexpr int kLanes = D / 16;
-  constexpr int kGroups = kMoveThreads / kLanes;
   const bool val = blockIdx.y != 0;
-  const uint4* __restrict__ in = static_cast<const uint4*>(val ? a.in_v : a.in_k);
-  void* out = val ? a.c.v : a.c.k;
-  uint8_t* scale = val ? a.c.v_scale : a.c.k_scale;
   const int lane = threadIdx.x % kLanes;
-  const int rows = a.c.B * a.c.Hkv * a.N;
-  const int r0 = blockIdx.x * (kGroups * kRows) + threadIdx.x / kLanes;
-  uint4 x[kRows][2];
+  const int r = blockIdx.x * (kMoveThreads / kLanes) + threadIdx.x / kLanes;
+  const bool exists = r < a.c.B * a.c.Hkv * a.N;
+  const uint4* src = static_cast<const uint4*>(val ? a.in_v : a.in_k) +
+                     (static_cast<long long>(r) * kLanes + lane) * 2;
+  const uint4 x = exists ? __ldcs(src) : make_uint4(0, 0, 0, 0);
+  const uint4 y = exists ? __ldcs(src + 1) : make_uint4(0, 0, 0, 0);
+  const RowAt at(a, exists ? r : 0);
+  // (lens[b] + i wraps to a position from 2^31 on where it is negative or too large)
+  const uint32_t pos = static_cast<uint32_t>(__ldg(a.at + at.b)) + static_cast<uint32_t>(at.i);
+  const bool moves = exists && pos < static_cast<uint32_t>(a.c.cap) &&
+                     (!a.counts || at.i < __ldg(a.counts + at.b));
+  const long long dst = static_cast<long long>(at.bh) * a.c.cap + pos;
+  if constexpr (E4M3) {
+    uint32_t m = __vmaxu2(abs_max(x), abs_max(y));
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int r = r0 + u * kGroups;
-    const uint4* src = in + (static_cast<long long>(r) * kLanes + lane) * 2;
-    x[u][0] = r < rows ? __ldcs(src) : make_uint4(0, 0, 0, 0);
-    x[u][1] = r < rows ? __ldcs(src + 1) : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const int r = r0 + u * kGroups;
-    uint32_t m = 0;
-    if (E4M3) {
-      m = __vmaxu2(abs_max(x[u][0]), abs_max(x[u][1]));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      m = max(m & 0xffffu, m >> 16);
-    }
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = max(m & 0xffffu, m >> 16);
     const bool finite = m < 0x7f80u;
-    if (E4M3 && !__all_sync(0xffffffffu, finite)) {  // some row here: over its finite elements
-      uint32_t f = __vmaxu2(finite_max8(x[u][0]), finite_max8(x[u][1]));
+    if (!__all_sync(0xffffffffu, finite)) {  // some row here: over its finite elements
+      uint32_t f = __vmaxu2(finite_max8(x), finite_max8(y));
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) f = __vmaxu2(f, __shfl_xor_sync(0xffffffffu, f, o));
       if (!finite) m = max(f & 0xffffu, f >> 16);
     }
-    if (r >= rows) continue;
-    const RowAt at(a, r);
-    const long long pos = static_cast<long long>(__ldg(a.at + at.b)) + at.i;
-    if ((a.counts && at.i >= __ldg(a.counts + at.b)) || pos < 0 || pos >= a.c.cap) continue;
-    const long long dst = static_cast<long long>(at.bh) * a.c.cap + pos;
-    if (E4M3) {
-      const int e = scale_exponent(m);
-      const float s = pow2_of(-e);
-      uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w,
-                       x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-      if (finite) {
+    if (!moves) return;
+    const int e = scale_exponent(m);
+    const float s = pow2_of(-e);
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    if (finite) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = codes2(w[i], s);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = codes2_any(w[i], s);
-      }
-      static_cast<uint4*>(out)[dst * kLanes + lane] =
-          make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-      if (lane == 0) scale[dst] = static_cast<uint8_t>(e + 127);
+      for (int i = 0; i < 8; ++i) w[i] = codes2(w[i], s);
     } else {
-      uint4* to = static_cast<uint4*>(out) + (dst * kLanes + lane) * 2;
-      to[0] = x[u][0];
-      to[1] = x[u][1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = codes2_any(w[i], s);
     }
+    static_cast<uint4*>(val ? a.c.v : a.c.k)[dst * kLanes + lane] =
+        make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    if (lane == 0) (val ? a.c.v_scale : a.c.k_scale)[dst] = static_cast<uint8_t>(e + 127);
+  } else if (moves) {
+    store32(static_cast<uint4*>(val ? a.c.v : a.c.k) + (dst * kLanes + lane) * 2, a.wide, x, y);
   }
 }
 
 // The inverse, with zeros in rows that are not read: one row a group of D / 16 lanes.
 // Two thirds of the bytes are stores, so that more rows in flight a thread gain
 // nothing (4 x 8 x 8192 rows of keys and values in e4m3: 33.9 us with one row, 34.7
-// with two, 34.9 with four), but whole 32-byte sectors do: 36.9 us with two 16-byte
-// stores in place of one of 32 bytes.
+// with two, 34.9 with four), but stores of whole 32-byte sectors do: two rows and two
+// stores of 16 bytes took 36.9 us.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) fa_cache_read_kernel(const CacheMoveArgs a) {
   constexpr int kLanes = D / 16;
@@ -238,10 +221,9 @@ __global__ void __launch_bounds__(kMoveThreads) __cluster_dims__(kCommitCtas, 1,
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-// kRows: rows a thread
-template <int D, int kRows>
+template <int D>
 dim3 move_grid(const CacheMoveArgs& a) {
-  constexpr long long per = kMoveThreads / (D / 16) * kRows;
+  constexpr long long per = kMoveThreads / (D / 16);
   const long long rows = static_cast<long long>(a.c.B) * a.c.Hkv * a.N;
   return dim3(static_cast<unsigned>((rows + per - 1) / per), 2, 1);
 }
@@ -252,17 +234,18 @@ cudaError_t launch_cache_write(const CacheMoveArgs& args, cudaStream_t s) {
   CacheMoveArgs a = args;
   a.by_n = FastDivide(a.N);
   a.by_heads = FastDivide(a.c.Hkv);
+  a.wide = aligned32(a.c.k) && aligned32(a.c.v);
   const bool f8 = a.c.format == FA_CACHE_E4M3;
   if (a.c.d == 64) {
     if (f8)
-      fa_cache_write_kernel<64, true><<<move_grid<64, kRows>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<64, true><<<move_grid<64>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_write_kernel<64, false><<<move_grid<64, kRows>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<64, false><<<move_grid<64>(a), kMoveThreads, 0, s>>>(a);
   } else {
     if (f8)
-      fa_cache_write_kernel<128, true><<<move_grid<128, kRows>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<128, true><<<move_grid<128>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_write_kernel<128, false><<<move_grid<128, kRows>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_write_kernel<128, false><<<move_grid<128>(a), kMoveThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }
@@ -275,14 +258,14 @@ cudaError_t launch_cache_read(const CacheMoveArgs& args, cudaStream_t s) {
   const bool f8 = a.c.format == FA_CACHE_E4M3;
   if (a.c.d == 64) {
     if (f8)
-      fa_cache_read_kernel<64, true><<<move_grid<64, 1>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<64, true><<<move_grid<64>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_read_kernel<64, false><<<move_grid<64, 1>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<64, false><<<move_grid<64>(a), kMoveThreads, 0, s>>>(a);
   } else {
     if (f8)
-      fa_cache_read_kernel<128, true><<<move_grid<128, 1>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<128, true><<<move_grid<128>(a), kMoveThreads, 0, s>>>(a);
     else
-      fa_cache_read_kernel<128, false><<<move_grid<128, 1>(a), kMoveThreads, 0, s>>>(a);
+      fa_cache_read_kernel<128, false><<<move_grid<128>(a), kMoveThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }

@@ -139,7 +139,7 @@ struct CacheMoveArgs {
   const int* path;    // commit
   int* new_lens;      // commit
   int N;              // rows a sequence (commit: T)
-  bool wide;          // read: out_k and out_v are aligned to 32 bytes
+  bool wide;          // where bf16 rows go is aligned to 32 bytes
   FastDivide by_n, by_heads;
 };
 
