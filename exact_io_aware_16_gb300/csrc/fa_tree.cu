@@ -805,6 +805,15 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_tree_error) != 0) ? 1 : 0;
     fence_mbar_init();
   }
+  // what needs no share comes first, beside the warp that finds it
+  if (warp == L::kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == L::kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, L::kCols);
+    tmem_relinquish();
+  }
   if (warp == 0) {
     // the share: units [unit0, unit1) of the list of all pairs
     const int total = all_units(p);
@@ -859,28 +868,24 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       bars->lens[lane] = b < p.B ? seq_len(p, b) : 0;
     }
   }
+  tc_fence_before_sync();
   __syncthreads();
-  if (bars->abort_flag || !Walk(bars).inside()) return;
-  if (warp == L::kMmaWarp) {
-    tmem_alloc(&bars->tmem_base, L::kCols);
-    tmem_relinquish();
+  tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  if (bars->abort_flag || !Walk(bars).inside()) {
+    if (warp == L::kMmaWarp) tmem_dealloc(tmem, L::kCols);
+    return;
   }
   // the first pair's queries are asked for before the streams begin
   const int have = min(p.R - rt * kTreeRows, NR);  // query rows of this tile
   const int trow = (rt * kTreeRows + static_cast<int>(threadIdx.x)) % p.T;
   PairLoads<D, NR> in;
   if (warp < L::kTmaWarp) in.load(p, bars->pair[0].b, bars->pair[0].bh, rt, have, trow);
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = bars->tmem_base;
   const uint32_t sRing = smem_u32(smem + L::kRing);
 
   if (warp == L::kTmaWarp) {
     // ------------------------------------------------ TMA producer
     if (lane == 0) {
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
       int n = 0;  // slots filled so far
       bool ok = true;
       auto slot = [&]() -> int {
