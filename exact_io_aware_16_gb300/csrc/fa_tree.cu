@@ -1317,6 +1317,15 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
 // ROWS query rows of a pair and 8 / ROWS warps for each, over the shares.
 constexpr int kMergeThreads = 256;
 
+__device__ __forceinline__ void load_row(const float* src, float (&x)[4]) {
+  const float4 z = *reinterpret_cast<const float4*>(src);
+  x[0] = z.x, x[1] = z.y, x[2] = z.z, x[3] = z.w;
+}
+__device__ __forceinline__ void load_row(const float* src, float (&x)[2]) {
+  const float2 z = *reinterpret_cast<const float2*>(src);
+  x[0] = z.x, x[1] = z.y;
+}
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads)
     fa_tree_combine(const __grid_constant__ TreeParams p, int blocks) {
@@ -1344,43 +1353,77 @@ __global__ void __launch_bounds__(kMergeThreads)
   auto slot_row = [&](int c) -> long long {
     return (2ll * (static_cast<long long>(c) * p.row_tiles + rt) + (c == first ? 1 : 0)) * p.prow + rs;
   };
-  __shared__ float sl[8], so[8][D];
+  __shared__ float sm[8], sl[8], so[8][D];
   float m = -INFINITY, l = 0.0f, acc[kC];
 #pragma unroll
   for (int k = 0; k < kC; ++k) acc[k] = 0.0f;
-  float m_ref = 0.0f;
   if (r < p.R) {
-    for (int c = first + lane; c <= last; c += 32) m = fmaxf(m, p.part_ml[slot_row(c)].x);
+    // four parts at a time, all of whose loads are under way together
+#pragma unroll 1
+    for (int c = first + warp % kWarps; c <= last; c += 4 * kWarps) {
+      float2 ml[4];
+      float x[4][kC];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m_ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll 4
-    for (int c = first + warp % kWarps; c <= last; c += kWarps) {
-      const long long at = slot_row(c);
-      const float2 ml = p.part_ml[at];
-      const float wgt = ml.y == 0.0f ? 0.0f : ex2_approx(ml.x - m_ref);  // 0: no key seen there
-      l = fmaf(wgt, ml.y, l);
-      const float* src = p.part_o + at * D + lane * kC;
+      for (int i = 0; i < 4; ++i) {
+        const bool there = c + i * kWarps <= last;
+        const long long at = slot_row(there ? c + i * kWarps : c);
+        ml[i] = p.part_ml[at];
+        load_row(p.part_o + at * D + lane * kC, x[i]);
+        if (!there) ml[i] = make_float2(-INFINITY, 0.0f);
+      }
+      const float old = m;
+      m = fmaxf(fmaxf(fmaxf(m, ml[0].x), ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      const float ref = m == -INFINITY ? 0.0f : m;
+      const float keep = ex2_approx(old - ref);
+      l *= keep;
 #pragma unroll
-      for (int k = 0; k < kC; ++k) acc[k] = fmaf(wgt, src[k], acc[k]);
+      for (int k = 0; k < kC; ++k) acc[k] *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (ml[i].y == 0.0f) continue;  // no key seen there
+        const float w = ex2_approx(ml[i].x - ref);
+        l = fmaf(w, ml[i].y, l);
+#pragma unroll
+        for (int k = 0; k < kC; ++k) acc[k] = fmaf(w, x[i][k], acc[k]);
+      }
     }
   }
+  if constexpr (kWarps > 1) {
 #pragma unroll
-  for (int k = 0; k < kC; ++k) so[warp][lane * kC + k] = acc[k];
-  if (lane == 0) sl[warp] = l;
-  __syncthreads();
-  if (warp % kWarps == 0 && r < p.R) {
+    for (int k = 0; k < kC; ++k) so[warp][lane * kC + k] = acc[k];
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (warp % kWarps != 0) return;
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) l += sl[warp + i];
+    for (int i = 1; i < kWarps; ++i) m = fmaxf(m, sm[warp + i]);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kC; ++k) acc[k] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (sl[warp + i] == 0.0f) continue;
+      const float w = ex2_approx(sm[warp + i] - ref);
+      l = fmaf(w, sl[warp + i], l);
+#pragma unroll
+      for (int k = 0; k < kC; ++k) acc[k] = fmaf(w, so[warp + i][lane * kC + k], acc[k]);
+    }
+  }
+  if (r < p.R) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const long long row = bh * p.R + r;
 #pragma unroll
-    for (int k = 0; k < kC; ++k) {
-#pragma unroll
-      for (int i = 1; i < kWarps; ++i) acc[k] += so[warp + i][lane * kC + k];
-      p.o[row * D + lane * kC + k] = __float2bfloat16_rn(acc[k] * inv);
-    }
-    if (lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+    for (int k = 0; k < kC; ++k) acc[k] *= inv;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + lane * (kC / 2);
+    if constexpr (kC == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    else
+      *dst = pack_bf16x2(acc[0], acc[1]);
+    if (lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (log2f(l) + (m == -INFINITY ? 0.0f : m)) * kLn2;
   }
 }
 
