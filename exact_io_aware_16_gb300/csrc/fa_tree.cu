@@ -48,13 +48,13 @@
 // P_j 2^(-e_j); o = O / l needs no further factor.
 //
 // Measured (d = 128, 8 key heads, the cache larger than L2; % of the rate of a plain
-// copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 92 us in e4m3 (86 %) and
-// 164 us in bf16 (96 %): HBM.  64 rows over 4 sequences of 32K to 64K keys in e4m3
-// 116 us (50 %) and 256 rows over 8 sequences of 4K to 8K keys in bf16 99 us: the
-// softmax, 16 warps that issue half of the cycles (2650 a tile of 128 keys by 64
+// copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 91 us in e4m3 (87 %) and
+// 164 us in bf16 (97 %): HBM.  64 rows over 4 sequences of 32K to 64K keys in e4m3
+// 113 us (52 %) and 256 rows over 8 sequences of 4K to 8K keys in bf16 98 us: the
+// softmax, 16 warps that issue half of the cycles (1900 a tile of 128 keys by 64
 // rows), with long waits for tensor memory and the group barrier.  32 rows over 32
-// sequences of 500 to 4096 keys in e4m3 48 us (49 %): starts and ends of pairs, the
-// first loads (5 us) and the merge (3 us or more).  One token over 1000 keys 14 us.
+// sequences of 500 to 4096 keys in e4m3 46 us (51 %): starts and ends of pairs, the
+// first loads (5 us) and the merge (5 us).  One token over 1000 keys 14 us.
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -555,37 +555,41 @@ __device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
 // A tile that reaches past the committed tokens: value rows that no query row
 // of the sequence sees become zero (P is zero there, but 0 * NaN is not), and
 // in drafts that some row sees NaN and infinities become zero and the draft is
-// noted: the epilogue adds them to the rows that see it.  Key a thread; sv is
-// its row, COLS boxes of ATOM bytes `stride` apart.
-template <uint32_t ATOM, int COLS, bool F8>
-__device__ __noinline__ void clean_values(uint8_t* sv, uint32_t stride, int pos, int len,
-                                             int end, unsigned long long any, unsigned int* note) {
+// noted: the epilogue adds them to the rows that see it.  Key a thread and group of
+// softmax warps: each group takes its part of the 16-byte units of the key's row sv,
+// which is COLS boxes of ATOM bytes `stride` apart.  Neighbouring keys take the units
+// in another order: in the same one, their rows' units lie in the same banks (6000
+// cycles for a tile of 64 drafts in bf16 on one group).
+template <uint32_t ATOM, int COLS, int GROUPS, bool F8>
+__device__ __noinline__ void clean_values(uint8_t* sv, uint32_t stride, int key, int group, int pos,
+                                          int len, int end, unsigned long long any,
+                                          unsigned int* note) {
+  constexpr int kBox = ATOM / 16, kUnits = COLS * kBox / GROUPS;  // of a box, of a group
+  static_assert(kUnits * GROUPS == COLS * kBox, "units");
   if (pos < len) return;
   const int j = pos - len;
   const bool live = pos < end && (any >> (j & 63) & 1);
+  const int order = key / (8 / kBox) % kBox;
   bool bad = false;
-#pragma unroll
-  for (int box = 0; box < COLS; ++box) {
-    uint4* row = reinterpret_cast<uint4*>(sv + box * stride);
 #pragma unroll 2
-    for (int i = 0; i < static_cast<int>(ATOM) / 16; ++i) {
-      if (!live) {
-        row[i] = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      const uint4 x = row[i];
-      uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
+  for (int i = group * kUnits; i < (group + 1) * kUnits; ++i) {
+    uint4* at = reinterpret_cast<uint4*>(sv + i / kBox * stride) + (i % kBox ^ order);
+    if (!live) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 x = *at;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w}, hit = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t n = F8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                              : __vcmpgeu2(w[k] & 0x7fff7fffu, 0x7f807f80u);
-        hit |= n;
-        w[k] &= ~n;
-      }
-      if (hit) {
-        row[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        bad = true;
-      }
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t n = F8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                            : __vcmpgeu2(w[k] & 0x7fff7fffu, 0x7f807f80u);
+      hit |= n;
+      w[k] &= ~n;
+    }
+    if (hit) {
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+      bad = true;
     }
   }
   if (bad) atomicOr(note + (j >> 5 & 1), 1u << (j & 31));
@@ -1282,10 +1286,10 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           const int v = n + kParts * (2 + t + min(t, tiles - 2)) + key / L::kVKeys;
           if (t > 0) ok = product_done(it - 1, ok, bars, 0x523);
           ok = ok && t_wait(&bars->full[v % kSlots], (v / kSlots) & 1, bars, 0x521);
-          if (ok && group == 0)
-            clean_values<L::kAtom, L::kBoxes, F8>(
+          if (ok)
+            clean_values<L::kAtom, L::kBoxes, L::kGroups, F8>(
                 smem + L::kRing + (v % kSlots) * L::kSlot + (key % L::kVKeys) * L::kAtom,
-                L::kVKeys * L::kAtom, pos, len, end, next.any, next.bad);
+                L::kVKeys * L::kAtom, key, group, pos, len, end, next.any, next.bad);
         }
         fence_proxy_async_smem();  // P, and cleaned values
         tc_fence_before_sync();
@@ -1494,9 +1498,12 @@ cudaError_t launch_type(const TreeArgs& a, const CUtensorMap& tk, const CUtensor
                         : p.R <= 32 ? launch_tile<D, F8, 32>(p, tk, tv, s)
                                     : launch_tile<D, F8, 64>(p, tk, tv, s);
   if (e != cudaSuccess || plan.slots == 0) return e;
-  // eight rows a block, but one where there are too few rows to fill the GPU
-  return static_cast<long long>(p.B) * a.Hq * a.T >= 2048 ? launch_combine<D, 8>(p, s)
-                                                          : launch_combine<D, 1>(p, s);
+  // eight rows a block, a warp each, where rows are many or have few parts, else one row:
+  // 1280 rows of 1.2 parts on average 26.2 us instead of 26.8 for the call, 512 rows of
+  // 4.8 parts 92.4 instead of 91.1
+  const bool few_parts = plan.shares <= 2ll * p.B * p.Hkv;
+  return few_parts || static_cast<long long>(p.B) * a.Hq * a.T >= 2048 ? launch_combine<D, 8>(p, s)
+                                                                       : launch_combine<D, 1>(p, s);
 }
 
 }  // namespace
