@@ -10,8 +10,9 @@
 // wrote a prompt of 4 x 8 x 8192 rows at 3.9 TB/s.)
 //
 // Measured (d = 128, e4m3; a plain copy runs at 6.79 TB/s): writing 4 x 8 x 8192 rows
-// of keys and values 37 us, 5.5 TB/s; reading them back 34 us, 5.8 TB/s; a token of 8
-// sequences written, or a path of 5 of 16 drafts committed for 4 sequences, 5.5 us.
+// of keys and values 35 us, 5.8 TB/s (in bf16 43 us, 6.2 TB/s); reading them back
+// 33 us, 6.0 TB/s; a token of 8 sequences written 4.1 us, a path of 5 of 16 drafts
+// committed for 4 sequences 5 us.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kMoveThreads) fa_cache_write_kernel(const Cach
 
 // The inverse, with zeros in rows that are not read: one row a group of D / 16 lanes.
 // Two thirds of the bytes are stores, so that more rows in flight a thread gain
-// nothing (4 x 8 x 8192 rows of keys and values in e4m3: 33.9 us with one row, 34.7
+// nothing (4 x 8 x 8192 rows of keys and values in e4m3: 33 us with one row, 34.7
 // with two, 34.9 with four), but stores of whole 32-byte sectors do: two rows and two
 // stores of 16 bytes took 36.9 us.
 template <int D, bool E4M3>

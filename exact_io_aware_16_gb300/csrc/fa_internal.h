@@ -256,10 +256,10 @@ inline int check_bhnd(int B, int H, int N, int d) {
 constexpr int kTreeTile = 128;  // keys a tile of the tree decode
 constexpr int kTreeRows = 64;   // query rows a row tile, at most
 
-// Units of a pair besides its tiles in the split: its start and end take about 4 us
-// of a CTA, a tile 0.7 to 1.5 us.  32 sequences of 500 to 4096 tokens x 8 heads, 32
-// rows, e4m3: 50.6 us with 2, 49.1 with 4, 49.2 with 5; 4 sequences of 32K to 64K
-// tokens x 8 heads, 64 rows: 115, 114 and 114 us.
+// Units of a pair besides its tiles in the split: its start and end take 3 to 5 us of a
+// CTA, a tile 0.7 to 1 us.  32 sequences of 500 to 4096 tokens x 8 heads, 32 rows, e4m3:
+// 48.5 us with 2, 46.1 with 3, 45.4 with 4; 4 sequences of 32K to 64K tokens x 8 heads,
+// 64 rows: 114.8, 113.6 and 113.0 us.
 constexpr int kTreePairCost = 4;
 // Each CTA walks over the lengths of all sequences to find its share.
 constexpr int kTreeMaxBatch = 65536;

@@ -50,11 +50,13 @@
 // Measured (d = 128, 8 key heads, the cache larger than L2; % of the rate of a plain
 // copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 91 us in e4m3 (87 %) and
 // 164 us in bf16 (97 %): HBM.  64 rows over 4 sequences of 32K to 64K keys in e4m3
-// 113 us (52 %) and 256 rows over 8 sequences of 4K to 8K keys in bf16 98 us: the
-// softmax, 16 warps that issue half of the cycles (1900 a tile of 128 keys by 64
-// rows), with long waits for tensor memory and the group barrier.  32 rows over 32
-// sequences of 500 to 4096 keys in e4m3 46 us (51 %): starts and ends of pairs, the
-// first loads (5 us) and the merge (5 us).  One token over 1000 keys 14 us.
+// 113 us (52 %): the softmax, 16 warps that issue half of the cycles (1900 a tile of
+// 128 keys by 64 rows), with long waits for tensor memory and the group barrier.  256
+// rows over 8 sequences of 4K to 8K keys in bf16 92 us: shared memory, whose 176 KB a
+// tile of 64 rows take 1375 of its 1400 cycles, and starts and ends of pairs (5 us
+// each).  32 rows over 32 sequences of 500 to 4096 keys in e4m3 46 us (51 %): starts
+// and ends of pairs, the first loads (5 us) and the merge (5 us).  One token over 1000
+// keys 13 us.
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -89,7 +91,7 @@ constexpr float kUnseen = 1e38f;
 // product of an element and a code is then off by at most 2^-12.8 of the row's largest.  Rows
 // that differ by more (a padded row may hold anything) have each its own power of two
 // and the softmax a product more for two scores: 64 rows over 4 x 8 heads of 32K to
-// 64K keys take 127 instead of 114 us so.
+// 64K keys take 127 instead of 113 us so.
 struct Queries {
   static constexpr int kNear = 4;
   static constexpr float kByRow = -1.0f;  // in place of the factor of all rows
