@@ -101,9 +101,8 @@ inline int decode_splits_run(long long BH, int Nk, int num_sms) {
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
-// Scale exponents of an e4m3 cache row (fa.h): at least -100, so that the
-// reciprocal scale 2^100 times any probability sum stays finite in fp32; at
-// most 119, so that 448 * 2^119 is still a finite bf16.
+// Scale exponents of an e4m3 cache row (fa.h): at least -100, for rows of zeros
+// as for the smallest that are worth their codes; at most 119, so that 448 * 2^119 is still a finite bf16.
 constexpr int kScaleExpMin = -100;
 constexpr int kScaleExpMax = 119;
 
@@ -296,11 +295,11 @@ inline TreePlan tree_plan(const fa_cache& c, int Hq, int T, int sms) {
   return p;
 }
 
-// Workspace of a tree decode: o and (m, l) of each partial row, for the largest
-// split of any GPU.
+// Workspace of a tree decode: o and the log-sum-exp of each partial row, for the
+// largest split of any GPU.
 inline size_t tree_workspace_bytes(const fa_cache& c, int Hq, int T) {
   const TreePlan p = tree_plan(c, Hq, T, kTreeMaxSms);
-  const size_t bytes = static_cast<size_t>(p.slots) * p.prow * (c.d + 2) * sizeof(float);
+  const size_t bytes = static_cast<size_t>(p.slots) * p.prow * (c.d + 1) * sizeof(float);
   return bytes < 256 ? 256 : (bytes + 255) & ~static_cast<size_t>(255);
 }
 

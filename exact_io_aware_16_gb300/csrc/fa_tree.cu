@@ -14,7 +14,7 @@
 // tiles of 64 rows, which run side by side so that they read a key tile while it
 // is in L2).  Lengths live on the device, so each CTA finds its share from lens
 // itself.  A pair that one CTA covers is finished there; the partial results of
-// the others ((m, l) and o, at most two a CTA) go to the workspace, and
+// the others (o and its log-sum-exp, at most two a CTA) go to the workspace, and
 // fa_tree_combine merges them by the running-maximum update.
 //
 // Products.  The keys take the tensor core's 128 rows and the query rows its
@@ -42,10 +42,11 @@
 // pieces of 4 significant bits hold the 8 bits of a bf16 query exactly (its row
 // scaled by a power of two into 448), and a probability to 2^-8.  S accumulates both
 // pieces; those of P are columns side by side, so that V is read once.  The scales of
-// keys and values join in the softmax: with e_j the exponent of value row j, the
-// thread forms t_j = scale log2(e) 2^(k_j) S_j + e_j, keeps M = max t_j, and
-// gives P_j = 2^(t_j - M) to the product with the codes, while the sum takes
-// P_j 2^(-e_j); o = O / l needs no further factor.
+// keys and values join in the softmax: with e_j the exponent of value row j and s_j =
+// scale log2(e) 2^(k_j) S_j, a row keeps M = max (s_j + e_j); the sum takes
+// p_j = 2^(s_j - M) and the product with the codes P_j = 2^(e_j) p_j, so that
+// o = O / l needs no further factor.  A value row of zeros has the least e_j there is:
+// its p_j may be far above 1, and is not lost however large the other rows are.
 //
 // Measured (d = 128, 8 key heads, the cache larger than L2; % of the rate of a plain
 // copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 91 us in e4m3 (87 %) and
@@ -106,6 +107,9 @@ struct Lazy {
   static constexpr float kTop = F8 ? 0.80735492f : 8.0f;      // log2 of the largest P
   static constexpr float kOScale = F8 ? 0.00390625f : 1.0f;   // unit of the high pieces
   [[maybe_unused]] static constexpr float kLowScale = 0.125f;  // of the low pieces in it
+  // Value rows of smaller exponents enter M with this one: their p = 2^(s - M) is at most
+  // 2^(kTop + 82), and a sum over 2^28 keys stays below 2^126 (as 1 / l is formed).
+  [[maybe_unused]] static constexpr float kLeastExponent = -82.0f;
 };
 
 // A pair of the share: its tiles t0 .. t0 + tiles - 1 are worked on here.
@@ -136,7 +140,7 @@ struct TreeRows {
   float m[NR];      // reference exponent, -inf before the first key
   float neg_m[NR];  // its negative: kUnseen before the first key, -inf for rows past R
   float unit[NR];   // scale log2(e) times the unit of the row's query pieces (see Queries)
-  float alpha[NR];  // of the last move
+  float alpha[NR];  // of the last move, its square root
   float inv[NR];    // epilogue: what O is multiplied by
   float part[4][NR];            // a warp's maximum or sum
 };
@@ -195,7 +199,7 @@ struct TreeParams {
   __nv_bfloat16* o;
   float* lse;
   float* part_o;     // [slots][prow][D]
-  float2* part_ml;   // [slots][prow]
+  float* part_lse;   // [slots][prow], in units of ln 2
   const uint8_t* k_scale;
   const uint8_t* v_scale;
   const uint8_t* v;  // the value cache, for rows with NaN or infinities
@@ -615,9 +619,9 @@ __device__ __forceinline__ float sum_lanes(float (&x)[16]) {
   return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
-// x = t - M of a key for 16 rows (t itself where neg_m is null), t = ks S + e;
-// ks: scale log2(e), times 2^k and the unit of the query pieces for e4m3.
-template <bool F8, bool M>
+// x = s - M of a key for 16 rows, or s + ev (where M is false), s = ks S; ks: scale
+// log2(e), times 2^k and the unit of the query pieces for e4m3.
+template <bool M>
 __device__ __forceinline__ void form_scores(uint32_t taddr, const float* neg_m, float ks, float ev,
                                             f32x2 (&x)[8]) {
   uint32_t s[16];
@@ -628,10 +632,7 @@ __device__ __forceinline__ void form_scores(uint32_t taddr, const float* neg_m, 
 #pragma unroll
   for (int r = 0; r < 8; r += 2) {
     ulonglong2 m = make_ulonglong2(ev2, ev2);
-    if (M) {
-      m = *reinterpret_cast<const ulonglong2*>(neg_m + 2 * r);
-      if (F8) m = make_ulonglong2(add2(ev2, m.x), add2(ev2, m.y));
-    }
+    if (M) m = *reinterpret_cast<const ulonglong2*>(neg_m + 2 * r);
     x[r] = fma2(pack2(__uint_as_float(s[2 * r]), __uint_as_float(s[2 * r + 1])), ks2, m.x);
     x[r + 1] = fma2(pack2(__uint_as_float(s[2 * r + 2]), __uint_as_float(s[2 * r + 3])), ks2, m.y);
   }
@@ -648,7 +649,7 @@ __device__ __noinline__ void form_scores_by_row(uint32_t taddr, const float* neg
   reg_pin(s);
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    const float m0 = M ? ev + neg_m[2 * r] : ev, m1 = M ? ev + neg_m[2 * r + 1] : ev;
+    const float m0 = M ? neg_m[2 * r] : ev, m1 = M ? neg_m[2 * r + 1] : ev;
     x[r] = pack2(fmaf(__uint_as_float(s[2 * r]), ks * unit[2 * r], m0),
                  fmaf(__uint_as_float(s[2 * r + 1]), ks * unit[2 * r + 1], m1));
   }
@@ -675,7 +676,7 @@ __device__ __noinline__ uint32_t hidden_rows(const unsigned long long* seen, int
   return h;
 }
 
-// The warp's maximum of each row's scores into out[16].
+// The warp's maximum of each row's s + ev into out[16].
 // unit: null where all rows have one factor.
 template <bool F8>
 __device__ __noinline__ void row_maxima(uint32_t taddr, const float* unit, float ks, float ev,
@@ -685,7 +686,7 @@ __device__ __noinline__ void row_maxima(uint32_t taddr, const float* unit, float
   if (F8 && unit)
     form_scores_by_row<false>(taddr, nullptr, unit, ks, ev, t);
   else
-    form_scores<F8, false>(taddr, nullptr, ks, ev, t);
+    form_scores<false>(taddr, nullptr, ks, ev, t);
   hide_rows(t, hidden);
   float top = -INFINITY;
 #pragma unroll
@@ -698,7 +699,8 @@ __device__ __noinline__ void row_maxima(uint32_t taddr, const float* unit, float
 }
 
 // Row r's new reference from the four warps' maxima, and what its sums are
-// multiplied by.
+// multiplied by twice: a sum of zero rows' weights may be 2^100 while the reference
+// moves by more than the 126 binades of one factor.
 template <bool F8, int NR>
 __device__ __noinline__ void new_reference(TreeRows<NR>* rows, int r, int have) {
   rows->alpha[r] = 1.0f;
@@ -710,7 +712,7 @@ __device__ __noinline__ void new_reference(TreeRows<NR>* rows, int r, int have) 
   if (m_new == -INFINITY || isnan(rows->neg_m[r])) return;
   rows->m[r] = m_new;
   rows->neg_m[r] = -m_new;
-  rows->alpha[r] = ex2_approx(m_old - m_new);
+  rows->alpha[r] = ex2_approx(0.5f * (m_old - m_new));
 }
 
 // y of four rows of a channel, plus the NaN and infinities of the drafts `bad` that
@@ -735,7 +737,7 @@ __device__ __noinline__ float4 add_bad(float4 y, unsigned long long bad,
   return y;
 }
 
-// 16 columns of O, `pieces` times `stride` columns apart, times alpha.
+// 16 columns of O, `pieces` times `stride` columns apart, times alpha^2.
 __device__ __noinline__ void rescale(uint32_t taddr, int pieces, int stride, const float* alpha) {
   tc_fence_after_sync();
 #pragma unroll 1
@@ -745,7 +747,7 @@ __device__ __noinline__ void rescale(uint32_t taddr, int pieces, int stride, con
     tmem_ld_wait();
     reg_pin(o);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (alpha[i] * alpha[i]));
     tmem_st16(taddr + k * stride, o);
   }
   tmem_st_wait();
@@ -1112,14 +1114,14 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         if (tid < have) {
           const float sum = (rows->part[0][tid] + rows->part[1][tid]) +
                             (rows->part[2][tid] + rows->part[3][tid]);
-          float inv = Lazy<F8>::kOScale;
-          if (slot < 0) {
-            inv *= sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-            if (ok) p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (__log2f(sum) + rows->m[tid]) * kLn2;
-          } else if (ok) {
-            p.part_ml[slot * p.prow + tid] = make_float2(rows->m[tid], sum);
+          const float lse2 = sum == 0.0f ? -INFINITY : __log2f(sum) + rows->m[tid];
+          if (ok) {
+            if (slot < 0)
+              p.lse[row0 + tid] = lse2 * kLn2;
+            else
+              p.part_lse[slot * p.prow + tid] = lse2;
           }
-          rows->inv[tid] = inv;
+          rows->inv[tid] = sum == 0.0f ? 0.0f : Lazy<F8>::kOScale * __fdividef(1.0f, sum);
         }
         soft_bar();
         const unsigned long long bad =
@@ -1181,12 +1183,13 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t, ++it, pos += kTile) {
         float ks = factor, ev = 0.0f, wv = 1.0f;
-        if constexpr (F8) {  // scale log2(e) 2^k_j, e_j and 2^-e_j
+        if constexpr (F8) {  // scale log2(e) 2^k_j, e_j as it enters M, and 2^e_j
           // not before here: converted where they are loaded, a tile would wait for them
           asm volatile("" : "+r"(kb), "+r"(vb));
           ks *= __uint_as_float(kb << 23);
-          ev = __uint_as_float(0x4b000000u | vb) - 8388735.0f;  // 2^23 + 127
-          wv = __uint_as_float((254u - vb) << 23);
+          ev = fmaxf(__uint_as_float(0x4b000000u | vb) - 8388735.0f,  // 2^23 + 127
+                     Lazy<F8>::kLeastExponent);
+          wv = __uint_as_float(vb << 23);
         }
         if (t + 1 < tiles) load_scales(bh, pos + kTile, end);
         ok = ok && t_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, 0x522);
@@ -1200,7 +1203,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
             ev = 0.0f;
           }
         }
-        // ---- x = t - M of this key for the thread's rows
+        // ---- x = s - M of this key for the thread's rows
         tc_fence_after_sync();
         const uint32_t scol = tlane + (it & 1) * NR + own;
         float sign = factor;
@@ -1209,11 +1212,11 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         auto scores = [&](f32x2 (&x)[8]) {
           if (F8 && by_row) {
             f32x2 y[8];
-            form_scores_by_row<true>(scol, rows->neg_m + own, rows->unit + own, -ks, ev, y);
+            form_scores_by_row<true>(scol, rows->neg_m + own, rows->unit + own, -ks, 0.0f, y);
 #pragma unroll
             for (int r = 0; r < 8; ++r) x[r] = y[r];
           } else {
-            form_scores<F8, true>(scol, rows->neg_m + own, ks, ev, x);
+            form_scores<true>(scol, rows->neg_m + own, ks, 0.0f, x);
           }
         };
         f32x2 x[8];
@@ -1225,6 +1228,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           const float2 y = unpack2(x[r]);
           mx = fmax3f(mx, y.x, y.y);
         }
+        if (F8) mx += ev;
         if (group_bar_or(2 + group, mx > Lazy<F8>::kTop)) {
           // ---- some row grew: new references from the maxima over the group's keys
           row_maxima<F8>(scol, by_row ? rows->unit + own : nullptr, by_row ? -ks : ks, ev,
@@ -1240,14 +1244,14 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
 #pragma unroll
             for (int r = 0; r < 8; r += 2) {
               const ulonglong2 al = *reinterpret_cast<const ulonglong2*>(&rows->alpha[own + 2 * r]);
-              l[r] = mul2(l[r], al.x);
-              l[r + 1] = mul2(l[r + 1], al.y);
+              l[r] = mul2(mul2(l[r], al.x), al.x);
+              l[r + 1] = mul2(mul2(l[r + 1], al.y), al.y);
             }
           }
           scores(x);
           if (hidden) hide_rows(x, hidden);
         }
-        // ---- P = 2^x over the P buffer that PV(it - 2) has read.  With one issuing warp
+        // ---- p = 2^x, and P = 2^e p over the P buffer that PV(it - 2) has read.  With one issuing warp
         // it is complete: S(it) was issued behind it.
         if (L::kMmaWarps > 1 && it >= 2) ok = product_done(it - 2, ok, bars, 0x525);
         {
@@ -1258,13 +1262,13 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
             const float2 a = unpack2(x[2 * i]), b = unpack2(x[2 * i + 1]);
             const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
             const float p2 = ex2_approx(b.x), p3 = ex2_approx(b.y);
+            const f32x2 p01 = pack2(p0, p1), p23 = pack2(p2, p3);
+            l[2 * i] = add2(l[2 * i], p01);
+            l[2 * i + 1] = add2(l[2 * i + 1], p23);
             if constexpr (F8) {
-              l[2 * i] = fma2(pack2(p0, p1), wv2, l[2 * i]);
-              l[2 * i + 1] = fma2(pack2(p2, p3), wv2, l[2 * i + 1]);
-              split4(p0, p1, p2, p3, hi[i], lo[i]);
+              const float2 c = unpack2(mul2(p01, wv2)), d = unpack2(mul2(p23, wv2));
+              split4(c.x, c.y, d.x, d.y, hi[i], lo[i]);
             } else {
-              l[2 * i] = add2(l[2 * i], pack2(p0, p1));
-              l[2 * i + 1] = add2(l[2 * i + 1], pack2(p2, p3));
               hi[2 * i] = pack_bf16x2(p0, p1);
               hi[2 * i + 1] = pack_bf16x2(p2, p3);
             }
@@ -1367,18 +1371,18 @@ __global__ void __launch_bounds__(kMergeThreads)
     // four parts at a time, all of whose loads are under way together
 #pragma unroll 1
     for (int c = first + warp % kWarps; c <= last; c += 4 * kWarps) {
-      float2 ml[4];
+      float part[4];
       float x[4][kC];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool there = c + i * kWarps <= last;
         const long long at = slot_row(there ? c + i * kWarps : c);
-        ml[i] = p.part_ml[at];
+        part[i] = p.part_lse[at];
         load_row(p.part_o + at * D + lane * kC, x[i]);
-        if (!there) ml[i] = make_float2(-INFINITY, 0.0f);
+        if (!there) part[i] = -INFINITY;
       }
       const float old = m;
-      m = fmaxf(fmaxf(fmaxf(m, ml[0].x), ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      m = fmaxf(fmaxf(fmaxf(m, part[0]), part[1]), fmaxf(part[2], part[3]));
       const float ref = m == -INFINITY ? 0.0f : m;
       const float keep = ex2_approx(old - ref);
       l *= keep;
@@ -1386,9 +1390,9 @@ __global__ void __launch_bounds__(kMergeThreads)
       for (int k = 0; k < kC; ++k) acc[k] *= keep;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (ml[i].y == 0.0f) continue;  // no key seen there
-        const float w = ex2_approx(ml[i].x - ref);
-        l = fmaf(w, ml[i].y, l);
+        if (part[i] == -INFINITY) continue;  // no key seen there
+        const float w = ex2_approx(part[i] - ref);
+        l += w;
 #pragma unroll
         for (int k = 0; k < kC; ++k) acc[k] = fmaf(w, x[i][k], acc[k]);
       }
@@ -1491,7 +1495,7 @@ cudaError_t launch_type(const TreeArgs& a, const CUtensorMap& tk, const CUtensor
   p.shares = plan.shares;
   p.prow = plan.prow;
   p.part_o = static_cast<float*>(a.workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(plan.slots) * plan.prow * D);
+  p.part_lse = p.part_o + static_cast<size_t>(plan.slots) * plan.prow * D;
   p.k_scale = a.c.k_scale;
   p.v_scale = a.c.v_scale;
   p.v = static_cast<const uint8_t*>(a.c.v);

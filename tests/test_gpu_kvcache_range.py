@@ -1,0 +1,97 @@
+"""Tree decode where a row's weights or values span many binades.
+
+The bounds are those that the call promises, not the kernel's own: a probability to 2^-8
+of its value, so that their part of o is off by at most 2^-8 sum p|v|, whatever the number
+of keys; o rounded to bf16, off by 2^-8 of its value; scores off by ds, as the tests of the
+other cases derive it.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+FMTS = ("e4m3", "bf16")
+
+
+@pytest.fixture(scope="module")
+def fa():
+    import exact_io_aware_16_gb300 as m
+    from exact_io_aware_16_gb300 import build
+
+    build.build()
+    m.library()
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def values(t, s):
+    x = t.double()
+    return x if s is None else x * torch.exp2(s.double() - 127)[..., None]
+
+
+def check(fa, cache, q, lens, o, lse, scale, pairs, mask=None):
+    """The rows of `pairs` (sequence, key head) against 64 bits; masks causal unless given."""
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == (0, 0)
+    B, Hkv, cap, d = cache.shape
+    Hq, T = q.shape[1:3]
+    G = Hq // Hkv
+    j = torch.arange(T, device="cuda")
+    for b, h in pairs:
+        n = min(lens[b] + T, cap)
+        k = values(cache.k[b, h, :n], None if cache.k_scale is None else cache.k_scale[b, h, :n])
+        v = values(cache.v[b, h, :n], None if cache.v_scale is None else cache.v_scale[b, h, :n])
+        sees = torch.ones(T, n, dtype=torch.bool, device="cuda")
+        drafts = j[None] <= j[:, None] if mask is None else mask[b][:, None] >> j[None] & 1 != 0
+        sees[:, lens[b]:] = drafts[:, : n - lens[b]]
+        for r in range(h * G, h * G + G):
+            x = q[b, r].double()
+            s = torch.where(sees, x @ k.T * scale, -math.inf)
+            want_lse = torch.logsumexp(s, -1)
+            p = torch.where(sees, torch.exp(s - want_lse[:, None]), 0.0)
+            want, a = p @ v, p @ v.abs()
+            ds = 2.0 ** -23 * (d + 8) * scale * (x.abs() @ k.abs().T).amax(-1)
+            if cache.format == "e4m3":
+                ds = ds + 2.0 ** -12.8 * x.abs().amax(-1) * scale * k.abs().sum(-1).max()
+            tol = a * (2.0 ** -8 + 2 * ds[:, None] + 2.0 ** -18) + 2.0 ** -8 * want.abs()
+            err = (o[b, r].double() - want).abs()
+            assert torch.isfinite(o[b, r]).all() and torch.isfinite(lse[b, r]).all(), (b, r)
+            assert (err <= tol).all(), ("o", b, r, (err / tol.clamp(min=1e-300)).max().item())
+            off = (lse[b, r].double() - want_lse).abs()
+            assert (off <= ds + 2.0 ** -20 * (1 + want_lse.abs())).all(), ("lse", b, r, off.max().item())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("shape", ((1, 2, 1, 3), (1, 320, 320, 2), (2, 24, 1, 2), (1, 8, 1, 8)), ids=str)
+@pytest.mark.parametrize("size", (1.0, 1e13, 1e25))
+@pytest.mark.parametrize("where", ("first", "last", "all", "every second"))
+def test_value_rows_of_zeros_count_in_the_sum(fa, fmt, shape, size, where):
+    """A row of zeros has the least scale exponent; its weight counts all the same, beside
+    values of any size, in the same share and through the merge."""
+    B, Hq, Hkv, T = shape
+    d, n = 64, 40000 if Hkv == 1 else 700
+    g = gen(int(math.log10(size)))
+    cache = fa.KvCache(B, Hkv, n + T, d, fmt)
+    k = randn(g, B, Hkv, n + T, d) * 0.5
+    v = (randn(g, B, Hkv, n + T, d) + 0.5) * size
+    if where == "first":
+        v[:, :, : n // 2] = 0
+    elif where == "last":
+        v[:, :, n // 2:] = 0
+    elif where == "all":
+        v[:] = 0
+    else:
+        v[:, :, ::2] = 0
+    fa.fa_cache_write(cache, k.bfloat16(), v.bfloat16())
+    q = randn(g, B, Hq, T, d).bfloat16()
+    lens = [n, n - 5][:B]
+    o, lse = fa.fa_decode_tree(cache, q, lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    check(fa, cache, q, lens, o, lse, 1 / math.sqrt(d), [(b, h) for b in range(B) for h in range(0, Hkv, 97)])
