@@ -40,8 +40,11 @@
 //
 // e4m3 operands: kind::f8f6f4 takes the cache as it lies in memory.  Two e4m3
 // pieces of 4 significant bits hold the 8 bits of a bf16 query exactly (its row
-// scaled by a power of two into 448), and a probability to 2^-8.  S accumulates both
-// pieces; those of P are columns side by side, so that V is read once.  The scales of
+// scaled by a power of two into 448).  A probability is three e5m2 pieces of 3 bits,
+// 2^-9 of it, over the 30 binades of that type: two e4m3 pieces have the bits but 15
+// binades, and a long tail of small weights behind a heavy key was lost with them.  S
+// accumulates both pieces of q; those of P are columns side by side, so that V is read
+// once.  The scales of
 // keys and values join in the softmax: with e_j the exponent of value row j and s_j =
 // scale log2(e) 2^(k_j) S_j, a row keeps M = max (s_j + e_j); the sum takes
 // p_j = 2^(s_j - M) and the product with the codes P_j = 2^(e_j) p_j, so that
@@ -49,13 +52,13 @@
 // its p_j may be far above 1, and is not lost however large the other rows are.
 //
 // Measured (d = 128, 8 key heads, the cache larger than L2; % of the rate of a plain
-// copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 91 us in e4m3 (87 %) and
-// 164 us in bf16 (97 %): HBM.  64 rows over 4 sequences of 32K to 64K keys in e4m3
-// 113 us (52 %): the softmax, 16 warps that issue half of the cycles (1900 a tile of
+// copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 90 us in e4m3 (89 %) and
+// 163 us in bf16 (97 %): HBM.  64 rows over 4 sequences of 32K to 64K keys in e4m3
+// 119 us (49 %): the softmax, 16 warps that issue half of the cycles (2000 a tile of
 // 128 keys by 64 rows), with long waits for tensor memory and the group barrier.  256
 // rows over 8 sequences of 4K to 8K keys in bf16 92 us: shared memory, whose 176 KB a
 // tile of 64 rows take 1375 of its 1400 cycles, and starts and ends of pairs (5 us
-// each).  32 rows over 32 sequences of 500 to 4096 keys in e4m3 46 us (51 %): starts
+// each).  32 rows over 32 sequences of 500 to 4096 keys in e4m3 48 us (48 %): starts
 // and ends of pairs, the first loads (5 us) and the merge (5 us).  One token over 1000
 // keys 13 us.
 #include <atomic>
@@ -100,13 +103,12 @@ struct Queries {
 
 // A row's accumulator is rescaled only when its maximum grows by more than
 // kLog2 binades.  bf16 has the range for any P; for e4m3 P is scaled so that 2^kLog2
-// times the largest P at the last rescale is 1.75, 448 in the units of its pieces.
+// times the largest P at the last rescale is 2^15, about as much as fp16 holds.
 template <bool F8>
 struct Lazy {
   static constexpr float kLog2 = F8 ? 6.0f : 8.0f;
-  static constexpr float kTop = F8 ? 0.80735492f : 8.0f;      // log2 of the largest P
-  static constexpr float kOScale = F8 ? 0.00390625f : 1.0f;   // unit of the high pieces
-  [[maybe_unused]] static constexpr float kLowScale = 0.125f;  // of the low pieces in it
+  static constexpr float kTop = F8 ? 15.0f : 8.0f;             // log2 of the largest P
+  [[maybe_unused]] static constexpr float kLowScale = 0.125f;  // unit of the lower pieces
   // Value rows of smaller exponents enter M with this one: their p = 2^(s - M) is at most
   // 2^(kTop + 82), and a sum over 2^28 keys stays below 2^126 (as 1 / l is formed).
   [[maybe_unused]] static constexpr float kLeastExponent = -82.0f;
@@ -145,6 +147,14 @@ struct TreeRows {
   float part[4][NR];            // a warp's maximum or sum
 };
 
+// Address of 16-byte unit c of row r in a tile of ATOM-byte rows, swizzled over the
+// row (128, 64 or 32 bytes).
+template <uint32_t ATOM>
+__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
+  constexpr uint32_t kUnits = ATOM / 16;
+  return r * ATOM + (c ^ (r / (8 / kUnits) % kUnits)) * 16u;
+}
+
 template <int D, bool F8, int NR>
 struct TreeLayout {
   static constexpr uint32_t kRow = F8 ? D : 2 * D;             // bytes of a cache row
@@ -162,10 +172,19 @@ struct TreeLayout {
   static constexpr int kMmaWarps = tree_ctas(NR) == 1 ? 2 : 1;
   static constexpr int kTmaWarp = kSoft / 32, kMmaWarp = kTmaWarp + 1;  // and the S warp behind
   static constexpr int kThreads = kSoft + 32 + 32 * kMmaWarps;
-  static constexpr int kPieces = F8 ? 2 : 1;                   // of q, and of P along its row
+  static constexpr int kPieces = F8 ? 2 : 1;                   // of q
   static constexpr uint32_t kQPiece = NR * kRow;               // 64 columns at a time for bf16
-  static constexpr uint32_t kPRow = 2 * NR;                    // bytes of a key's P
-  static constexpr uint32_t kPBytes = kTile * kPRow;
+  // P lies as [key][row], for e4m3 its three pieces one behind the other in a key's row of
+  // 64 or 128 bytes (or two of 128 in boxes kPBox apart); the rest of the row is not used.
+  static constexpr int kPPieces = F8 ? 3 : 1;
+  static constexpr uint32_t kPAtom = F8 ? (NR == 16 ? 64 : 128) : 2 * NR;  // swizzle width
+  static constexpr uint32_t kPBox = kTile * kPAtom;
+  static constexpr uint32_t kPBytes = F8 && NR == 64 ? 2 * kPBox : kPBox;
+  // 16-byte unit u of a key's P
+  static __device__ __forceinline__ uint32_t p_at(int key, int u) {
+    constexpr int kUnits = kPAtom / 16;
+    return u / kUnits * kPBox + swizzled<kPAtom>(key, u % kUnits);
+  }
   static constexpr int kCtas = tree_ctas(NR);                  // an SM
   static constexpr uint32_t kRoom = (kCtas == 2 ? 113u : 227u) * 1024 - 1024 - 1024 -
                                     2 * sizeof(TreeRows<NR>) - kPieces * kQPiece - 2 * kPBytes;
@@ -185,8 +204,8 @@ struct TreeLayout {
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "fits");
   // tensor memory: S^T twice, O^T (of each piece)
   static constexpr uint32_t kOCol = 2 * NR;
-  static constexpr uint32_t kOCols = kPieces * NR;
-  static constexpr uint32_t kCols = NR == 16 ? 64 : NR == 32 ? 128 : 256;
+  static constexpr uint32_t kOCols = kPPieces * NR;
+  static constexpr uint32_t kCols = (F8 ? 8 : 4) * NR;
   static_assert(kOCol + kOCols <= kCols, "columns");
 };
 static_assert(sizeof(TreeBars) <= 1024, "barrier block");
@@ -351,28 +370,33 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 
 // ------------------------------------------------------------ conversions
-// Four fp32 P of 0 .. 1.75 as two e4m3 pieces each: a word of high pieces of 2^8 P,
-// and a word of the rests times 2^3 (their product has accumulator columns of its
-// own).  fp16 P has the exponent field of e4m3 2^8 P, so that bits 14..7 of the
-// fp16 are the code cut to 4 significant bits, subnormal ones included.  The rest R
-// is exact in fp16, below 2^-3 of P's binade, and rounded (half up) to its 4 bits the
-// same way: 2^-8 of P together as in bf16, down to 2^8 P of 2^-6, and 2^-13 below: the
-// room that Lazy takes.  Masks, shifts and byte permutes run at four times the rate
-// of the e4m3 conversions.  (A NaN is lost here: the row's sum carries it.)
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+// Four fp32 P of 0 .. 2^15 as three e5m2 pieces each: a word of high pieces, and words of
+// middle and low pieces times 2^3 (each has accumulator columns of its own).  e5m2 is
+// the high byte of fp16, so that the high piece is P in fp16 cut to 3 significant bits,
+// the rest of it, exact in fp16 and below 2^-2 of P's binade, is cut the same way, and
+// what then remains is rounded (half up): 2^-9 of P together, and 2^-20 where the last
+// two are subnormal.  With a row's largest P at 2^9 or more that is 2^-29 of it, and a
+// sum over 2^20 keys still within 2^-9.  Masks, additions and byte permutes run at four
+// times the rate of the conversions to 8 bits.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& mid,
+                                       uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x0, x1);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(&h), c = w & 0x7f807f80u;
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const uint32_t c = hi & 0xff00ff00u;
   const __half2 r = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&c)),
                             __half2half2(__ushort_as_half(0x4800)));  // 2^3
-  hi = w << 1;
-  lo = *reinterpret_cast<const uint32_t*>(&r) * 2 + 0x00800080u;
+  mid = *reinterpret_cast<const uint32_t*>(&r);
+  const uint32_t d = mid & 0xff00ff00u;
+  const __half2 z = __hsub2(r, *reinterpret_cast<const __half2*>(&d));
+  lo = *reinterpret_cast<const uint32_t*>(&z) + 0x00800080u;
 }
 __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t& hi,
-                                       uint32_t& lo) {
-  uint32_t h0, l0, h1, l1;
-  split2(x0, x1, h0, l0);
-  split2(x2, x3, h1, l1);
+                                       uint32_t& mid, uint32_t& lo) {
+  uint32_t h0, m0, l0, h1, m1, l1;
+  split2(x0, x1, h0, m0, l0);
+  split2(x2, x3, h1, m1, l1);
   hi = __byte_perm(h0, h1, 0x7531);
+  mid = __byte_perm(m0, m1, 0x7531);
   lo = __byte_perm(l0, l1, 0x7531);
 }
 
@@ -427,14 +451,6 @@ __device__ __forceinline__ float redux_max(float x) {
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Address of 16-byte unit c of row r in a tile of ATOM-byte rows, swizzled over the
-// row (128, 64 or 32 bytes).
-template <uint32_t ATOM>
-__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
-  constexpr uint32_t kUnits = ATOM / 16;
-  return r * ATOM + (c ^ (r / (8 / kUnits) % kUnits)) * 16u;
-}
 
 // sdesc_sw128 with the swizzle of ATOM-byte rows.
 template <uint32_t ATOM>
@@ -973,19 +989,22 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
               const uint32_t vbase = sRing + s * L::kSlot;
               if (!elect_one()) continue;
               if constexpr (F8) {
-                // both pieces' columns at once; both operands MN-major
-                constexpr uint32_t idesc = idesc_e4m3_f32(D, 2 * NR) | (3u << 15);
+                // all pieces' columns at once; both operands MN-major, P in e5m2
+                constexpr uint32_t idesc =
+                    idesc_e4m3_f32(D, L::kPPieces * NR) | (3u << 15) | (1u << 10);
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
                   umma_ss_f8(d, sdesc<L::kAtom>(vbase + kk * 32 * L::kAtom, 16, 8 * L::kAtom),
-                             sdesc<L::kPRow>(pbase + kk * 32 * L::kPRow, 16, 8 * L::kPRow), idesc,
+                             sdesc<L::kPAtom>(pbase + kk * 32 * L::kPAtom, L::kPBox, 8 * L::kPAtom),
+                             idesc,
                              (t > 0 || kk > 0) ? 1u : 0u);
               } else {
                 constexpr uint32_t idesc = idesc_bf16_f32(D, NR, true, true);
 #pragma unroll
                 for (int kk = 0; kk < L::kVKeys / 16; ++kk)
                   umma_ss(d, sdesc_sw128(vbase + kk * 2048, L::kVKeys * 128, 1024),
-                          sdesc<L::kPRow>(pbase + (c * L::kVKeys + kk * 16) * L::kPRow, 16, 8 * L::kPRow),
+                          sdesc<L::kPAtom>(pbase + (c * L::kVKeys + kk * 16) * L::kPAtom, 16,
+                                           8 * L::kPAtom),
                           idesc, (t > 0 || c > 0 || kk > 0) ? 1u : 0u);
               }
               umma_commit(&bars->empty[s]);
@@ -1121,7 +1140,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
             else
               p.part_lse[slot * p.prow + tid] = lse2;
           }
-          rows->inv[tid] = sum == 0.0f ? 0.0f : Lazy<F8>::kOScale * __fdividef(1.0f, sum);
+          rows->inv[tid] = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
         }
         soft_bar();
         const unsigned long long bad =
@@ -1132,17 +1151,24 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         const bool mine = ok && (D == 128 || lane < 16);
 #pragma unroll 1
         for (int r = own; r < min(have, own + 16); r += 4) {
-          uint32_t o[4], lo[4];
+          uint32_t o[4], mid[4], lo[4];
           tmem_ld4(tlane + L::kOCol + r, o);
-          if (F8) tmem_ld4(tlane + L::kOCol + NR + r, lo);
+          if (F8) {
+            tmem_ld4(tlane + L::kOCol + NR + r, mid);
+            tmem_ld4(tlane + L::kOCol + 2 * NR + r, lo);
+          }
           tmem_ld_wait();
           reg_pin(o);
-          if (F8) reg_pin(lo);
+          if (F8) {
+            reg_pin(mid);
+            reg_pin(lo);
+          }
           float y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             y[i] = __uint_as_float(o[i]);
-            if (F8) y[i] = fmaf(__uint_as_float(lo[i]), Lazy<F8>::kLowScale, y[i]);
+            if (F8)
+              y[i] = fmaf(__uint_as_float(mid[i]) + __uint_as_float(lo[i]), Lazy<F8>::kLowScale, y[i]);
           }
           if (bad) {
             const float4 z = add_bad<D, F8>(
@@ -1240,7 +1266,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
             // PV(it - 1) must be done before O is rescaled
             ok = product_done(it - 1, ok, bars, 0x524);
             __syncwarp();
-            rescale(tlane + L::kOCol + own, L::kPieces, NR, rows->alpha + own);
+            rescale(tlane + L::kOCol + own, L::kPPieces, NR, rows->alpha + own);
 #pragma unroll
             for (int r = 0; r < 8; r += 2) {
               const ulonglong2 al = *reinterpret_cast<const ulonglong2*>(&rows->alpha[own + 2 * r]);
@@ -1256,7 +1282,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
         if (L::kMmaWarps > 1 && it >= 2) ok = product_done(it - 2, ok, bars, 0x525);
         {
           const f32x2 wv2 = pack2(wv, wv);
-          uint32_t hi[8], lo[F8 ? 4 : 1];
+          uint32_t hi[8], mid[F8 ? 4 : 1], lo[F8 ? 4 : 1];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 a = unpack2(x[2 * i]), b = unpack2(x[2 * i + 1]);
@@ -1267,7 +1293,7 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
             l[2 * i + 1] = add2(l[2 * i + 1], p23);
             if constexpr (F8) {
               const float2 c = unpack2(mul2(p01, wv2)), d = unpack2(mul2(p23, wv2));
-              split4(c.x, c.y, d.x, d.y, hi[i], lo[i]);
+              split4(c.x, c.y, d.x, d.y, hi[i], mid[i], lo[i]);
             } else {
               hi[2 * i] = pack_bf16x2(p0, p1);
               hi[2 * i + 1] = pack_bf16x2(p2, p3);
@@ -1275,14 +1301,16 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           }
           uint8_t* const at = smem + L::kP + (it & 1) * L::kPBytes;
           if constexpr (F8) {
-            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, group)) =
+            *reinterpret_cast<uint4*>(at + L::p_at(key, group)) =
                 make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, L::kGroups + group)) =
+            *reinterpret_cast<uint4*>(at + L::p_at(key, L::kGroups + group)) =
+                make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            *reinterpret_cast<uint4*>(at + L::p_at(key, 2 * L::kGroups + group)) =
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           } else {
-            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, 2 * group)) =
+            *reinterpret_cast<uint4*>(at + L::p_at(key, 2 * group)) =
                 make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + swizzled<L::kPRow>(key, 2 * group + 1)) =
+            *reinterpret_cast<uint4*>(at + L::p_at(key, 2 * group + 1)) =
                 make_uint4(hi[4], hi[5], hi[6], hi[7]);
           }
         }

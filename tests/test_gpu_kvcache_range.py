@@ -1,9 +1,11 @@
-"""Tree decode where a row's weights or values span many binades.
+"""Tree decode where a row's weights or values span many binades: one key with much of
+the weight before a long flat tail, value rows of zeros among large ones.
 
 The bounds are those that the call promises, not the kernel's own: a probability to 2^-8
 of its value, so that their part of o is off by at most 2^-8 sum p|v|, whatever the number
-of keys; o rounded to bf16, off by 2^-8 of its value; scores off by ds, as the tests of the
-other cases derive it.
+of keys (the 2^-29 of the row's largest that it may be off by besides is 2^-13 over 65536
+keys, within what the kernel's 2^-9 leaves of the 2^-8); o rounded to bf16, off by 2^-8 of
+its value; scores off by ds, as the tests of the other cases derive it.
 """
 import math
 
@@ -67,6 +69,38 @@ def check(fa, cache, q, lens, o, lse, scale, pairs, mask=None):
             assert (err <= tol).all(), ("o", b, r, (err / tol.clamp(min=1e-300)).max().item())
             off = (lse[b, r].double() - want_lse).abs()
             assert (off <= ds + 2.0 ** -20 * (1 + want_lse.abs())).all(), ("lse", b, r, off.max().item())
+
+
+# (B, Hq, Hkv, T): 16, 32 and 64 rows a CTA, with as many pairs or row tiles as CTAs, so
+# that one CTA walks over whole pairs; and one pair that is spread over all CTAs
+SHAPES = [(1, 304, 304, 1), (1, 304, 304, 24), (1, 152, 1, 64), (1, 2, 1, 3)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("weight,spread", ((0.5, 0.0), (0.75, 0.3), (0.9, 1.0)))
+def test_one_heavy_key_before_a_long_tail(fa, fmt, d, shape, weight, spread):
+    """The tail's keys have 2^-16 of the first key's weight each and, together, 10 to 50 %
+    of the row's; the values have a mean, so that a lost weight shows."""
+    B, Hq, Hkv, T = shape
+    n = 65536 if Hkv == 1 else 8192
+    g = gen(d + T)
+    gap = math.log(weight / (1 - weight)) + math.log(n) + spread ** 2 / 2  # nats above the tail
+    cache = fa.KvCache(B, Hkv, n + T, d, fmt)
+    k = randn(g, B, Hkv, n, d) * (spread / math.sqrt(d))  # scores of the tail: spread nats
+    k[..., 0] = 0
+    k[:, :, 0] = 0
+    k[:, :, 0, 0] = gap / 4
+    v = randn(g, B, Hkv, n, d) + 0.5
+    v[..., 1] = 1.0  # a channel that is the sum of the weights
+    fa.fa_cache_write(cache, k.bfloat16(), v.bfloat16())
+    q = randn(g, B, Hq, T, d)
+    q[..., 0] = 4.0
+    q = q.bfloat16()
+    lens = [n - T]  # the last T of the tail are drafts
+    o, lse = fa.fa_decode_tree(cache, q, lens=torch.tensor(lens, dtype=torch.int32, device="cuda"), scale=1.0)
+    check(fa, cache, q, lens, o, lse, 1.0, [(0, h) for h in range(0, Hkv, 101)])
 
 
 @pytest.mark.parametrize("fmt", FMTS)
