@@ -517,9 +517,17 @@ __device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
   constexpr int kPer = PairLoads<D, NR>::kPer, kGran = PairLoads<D, NR>::kGran;
   const int r = threadIdx.x / kPer, part = threadIdx.x % kPer;
   float factor = scale_log2;
+  // a NaN or an infinity makes all scores of its row NaN, those too that would be -inf
+  uint32_t all = 0;
+#pragma unroll
+  for (int i = 0; i < kGran; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) all = __vmaxu2(all, word(in.q[i], k) & 0x7fff7fffu);
+  const uint32_t bad = __ballot_sync(0xffffffffu, max(all & 0xffffu, all >> 16) >= 0x7f80u);
   if (part == 0) {
+    const bool nan = bad >> (threadIdx.x & 31) & ((1u << kPer) - 1);
     rows->m[r] = -INFINITY;
-    rows->neg_m[r] = r < have ? kUnseen : -INFINITY;
+    rows->neg_m[r] = r >= have ? -INFINITY : nan ? NAN : kUnseen;
   }
   if (threadIdx.x < NR) rows->seen[threadIdx.x] = in.seen;
   if constexpr (!F8) {
@@ -529,13 +537,9 @@ __device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
       *reinterpret_cast<uint4*>(sq + (c >> 3) * (NR * 128) + swizzled<128>(r, c & 7)) = in.q[i];
     }
   } else {
-    uint32_t m = 0, all = 0;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kGran; ++i) {
-      m = __vmaxu2(m, finite_max8(in.q[i]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) all = __vmaxu2(all, word(in.q[i], k) & 0x7fff7fffu);
-    }
+    for (int i = 0; i < kGran; ++i) m = __vmaxu2(m, finite_max8(in.q[i]));
 #pragma unroll
     for (int o = kPer / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = max(m & 0xffffu, m >> 16);
@@ -567,8 +571,6 @@ __device__ __forceinline__ float store_queries(uint8_t* sq, TreeRows<NR>* rows,
       *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *reinterpret_cast<uint2*>(at + L::kQPiece) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
     }
-    // NaN or infinities in the row: its scores are NaN
-    if (max(all & 0xffffu, all >> 16) >= 0x7f80u && r < have) rows->neg_m[r] = NAN;
   }
   return factor;
 }

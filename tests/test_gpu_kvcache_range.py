@@ -1,5 +1,6 @@
-"""Tree decode where a row's weights or values span many binades: one key with much of
-the weight before a long flat tail, value rows of zeros among large ones.
+"""Tree decode where a row's weights, values or queries span many binades: one key with
+much of the weight before a long flat tail, value rows of zeros among large ones, an
+infinity in a query.
 
 The bounds are those that the call promises, not the kernel's own: a probability to 2^-8
 of its value, so that their part of o is off by at most 2^-8 sum p|v|, whatever the number
@@ -129,3 +130,28 @@ def test_value_rows_of_zeros_count_in_the_sum(fa, fmt, shape, size, where):
     lens = [n, n - 5][:B]
     o, lse = fa.fa_decode_tree(cache, q, lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
     check(fa, cache, q, lens, o, lse, 1 / math.sqrt(d), [(b, h) for b in range(B) for h in range(0, Hkv, 97)])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("Hq", (1, 20, 48))
+@pytest.mark.parametrize("sign", (1.0, -1.0))
+def test_an_infinity_in_a_query_makes_its_row_nan(fa, fmt, d, Hq, sign):
+    """Also where every score that the row sees is -inf, which no other row is."""
+    cache = fa.KvCache(1, 1, 16, d, fmt)
+    k = torch.ones(1, 1, 3, d, dtype=torch.bfloat16, device="cuda")
+    fa.fa_cache_write(cache, k, k)
+    q = torch.ones(1, Hq, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[0, Hq // 2, 0, 5] = sign * math.inf
+    lens = torch.tensor([2], dtype=torch.int32, device="cuda")
+    o, lse = fa.fa_decode_tree(cache, q, lens=lens)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == (0, 0)
+    bad = torch.zeros(Hq, dtype=torch.bool)
+    bad[Hq // 2] = True
+    assert torch.equal(torch.isnan(lse[0, :, 0]).cpu(), bad)
+    assert torch.equal(torch.isnan(o[0, :, 0]).cpu(), bad[:, None].expand(Hq, d))
+    # a row that sees nothing has no scores: o = 0 and lse = -inf
+    mask = torch.zeros(1, dtype=torch.int64, device="cuda")
+    o, lse = fa.fa_decode_tree(cache, q, mask, lens=torch.zeros_like(lens))
+    assert not o.any() and torch.isneginf(lse).all()
