@@ -295,11 +295,19 @@ inline TreePlan tree_plan(const fa_cache& c, int Hq, int T, int sms) {
   return p;
 }
 
-// Workspace of a tree decode: o and the log-sum-exp of each partial row, for the
-// largest split of any GPU.
+// Pairs that may be split over shares, and so the merge's groups of blocks: at most all
+// of them, and one for each end of a share but the last.
+inline int tree_merge_groups(int B, int Hkv, int shares) {
+  const long long pairs = static_cast<long long>(B) * Hkv;
+  return pairs < shares ? static_cast<int>(pairs) : shares - 1;
+}
+
+// Workspace of a tree decode: 16 bytes a share that say which pair is split there, and o
+// and the log-sum-exp of each partial row; for the largest split of any GPU.
 inline size_t tree_workspace_bytes(const fa_cache& c, int Hq, int T) {
   const TreePlan p = tree_plan(c, Hq, T, kTreeMaxSms);
-  const size_t bytes = static_cast<size_t>(p.slots) * p.prow * (c.d + 1) * sizeof(float);
+  const size_t bytes = static_cast<size_t>(p.slots) * p.prow * (c.d + 1) * sizeof(float) +
+                       (p.slots > 0 ? static_cast<size_t>(p.shares) * 16 : 0);
   return bytes < 256 ? 256 : (bytes + 255) & ~static_cast<size_t>(255);
 }
 

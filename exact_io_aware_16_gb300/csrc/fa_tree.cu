@@ -219,6 +219,7 @@ struct TreeParams {
   float* lse;
   float* part_o;     // [slots][prow][D]
   float* part_lse;   // [slots][prow], in units of ln 2
+  int4* split;       // [shares], or null: see fa_tree_combine
   const uint8_t* k_scale;
   const uint8_t* v_scale;
   const uint8_t* v;  // the value cache, for rows with NaN or infinities
@@ -893,6 +894,17 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
       const int b = bars->start_b + lane;
       bars->lens[lane] = b < p.B ? seq_len(p, b) : 0;
     }
+    if (p.split && rt == 0 && lane == 0) {
+      // for the merge: the pair whose second part begins this share
+      int4 d = make_int4(-1, 0, 0, 0);
+      const PairInfo& first = bars->pair[0];
+      if (unit0 < unit1 && first.t0 > 0) {
+        const int u = first.u0 + kPairCost;
+        if (u / size == share - 1)
+          d = make_int4(static_cast<int>(first.bh), share - 1, (u + first.nt - 1) / size, 0);
+      }
+      p.split[share] = d;
+    }
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -1354,7 +1366,13 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
 
 // ------------------------------------------------------------ merge
 // Where several shares cover a pair, its rows' partials are merged.  A block has
-// ROWS query rows of a pair and 8 / ROWS warps for each, over the shares.
+// ROWS query rows of a pair and 8 / ROWS warps for each, over the shares.  The pairs
+// that are split are at most as many as there are pairs, and as there are ends of shares
+// but the last; the grid has the smaller number of them.  Where that is the pairs, a block finds
+// its own from the lengths (a few hundred at most) while the shares still run; where
+// it is the shares, split[s] names the pair whose second part begins share s.  With a
+// block for every pair, each of which added up all lengths, 8 rows x 4 heads of 65536
+// sequences of up to 250 tokens took 75 ms; they take 5.2.
 constexpr int kMergeThreads = 256;
 
 __device__ __forceinline__ void load_row(const float* src, float (&x)[4]) {
@@ -1372,21 +1390,32 @@ __global__ void __launch_bounds__(kMergeThreads)
   constexpr int kC = D / 32;
   constexpr int kWarps = 8 / ROWS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long bh = blockIdx.x / blocks;
-  const int b = static_cast<int>(bh / p.Hkv), h = static_cast<int>(bh % p.Hkv);
-  int total = 0, before = 0;
-  for (int i = lane; i < p.B; i += 32) {
-    const int n = seq_tiles(p, i) + kPairCost;
-    total += n;
-    if (i < b) before += n;
+  long long bh = blockIdx.x / blocks;
+  int first, last;
+  if (p.split) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d = p.split[bh + 1];
+    if (d.x < 0) return;
+    bh = d.x;
+    first = d.y;
+    last = d.z;
+  } else {
+    const int b = static_cast<int>(bh / p.Hkv), h = static_cast<int>(bh % p.Hkv);
+    int total = 0, before = 0;
+    for (int i = lane; i < p.B; i += 32) {
+      const int n = seq_tiles(p, i) + kPairCost;
+      total += n;
+      if (i < b) before += n;
+    }
+    const int nt = seq_tiles(p, b);
+    total = warp_sum(total) * p.Hkv;
+    const int u0 = warp_sum(before) * p.Hkv + (h + 1) * kPairCost + h * nt;  // of its first tile
+    const int size = share_size(total, p.shares);
+    first = u0 / size;
+    last = (u0 + nt - 1) / size;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (first == last) return;
   }
-  const int nt = seq_tiles(p, b);
-  total = warp_sum(total) * p.Hkv;
-  const int u0 = warp_sum(before) * p.Hkv + (h + 1) * kPairCost + h * nt;  // of its first tile
-  const int size = share_size(total, p.shares);
-  const int first = u0 / size, last = (u0 + nt - 1) / size;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (first == last) return;
   const int r = static_cast<int>(blockIdx.x % blocks) * ROWS + warp / kWarps;
   const int rt = r / kTreeRows, rs = r % kTreeRows;
   // rows of the partials of share c: slot 1 where the pair begins, else slot 0
@@ -1469,11 +1498,10 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 template <int D, int ROWS>
 cudaError_t launch_combine(const TreeParams& p, cudaStream_t s) {
-  // launched while the shares still run: it finds its pair meanwhile and then waits
-  // for them (griddepcontrol.wait)
+  // launched while the shares still run, for which it waits (griddepcontrol.wait)
   const int blocks = (p.R + ROWS - 1) / ROWS;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(tree_merge_groups(p.B, p.Hkv, p.shares)) * blocks);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -1524,8 +1552,10 @@ cudaError_t launch_type(const TreeArgs& a, const CUtensorMap& tk, const CUtensor
   p.row_tiles = plan.row_tiles;
   p.shares = plan.shares;
   p.prow = plan.prow;
-  p.part_o = static_cast<float*>(a.workspace);
+  p.part_o = static_cast<float*>(a.workspace) + 4 * (plan.slots > 0 ? plan.shares : 0);
   p.part_lse = p.part_o + static_cast<size_t>(plan.slots) * plan.prow * D;
+  if (plan.slots > 0 && static_cast<long long>(a.c.B) * a.c.Hkv >= plan.shares)
+    p.split = static_cast<int4*>(a.workspace);
   p.k_scale = a.c.k_scale;
   p.v_scale = a.c.v_scale;
   p.v = static_cast<const uint8_t*>(a.c.v);
@@ -1534,11 +1564,12 @@ cudaError_t launch_type(const TreeArgs& a, const CUtensorMap& tk, const CUtensor
                         : p.R <= 32 ? launch_tile<D, F8, 32>(p, tk, tv, s)
                                     : launch_tile<D, F8, 64>(p, tk, tv, s);
   if (e != cudaSuccess || plan.slots == 0) return e;
-  // eight rows a block, a warp each, where rows are many or have few parts, else one row:
-  // 1280 rows of 1.2 parts on average 26.2 us instead of 26.8 for the call, 512 rows of
-  // 4.8 parts 92.4 instead of 91.1
+  // eight rows a block, a warp each, where rows are many or have few parts, else one row.
+  // One row and eight, e4m3 calls: 512 rows of 9.5 parts 26.7 and 28.6 us, 1024 of 9.5 26.8
+  // and 28.8, 1024 of 4.8 24.8 and 25.4; 2048 of 4.8 51.1 and 48.8, 2048 of 2.4 30.3 and 26.8,
+  // 4096 of 2.4 51.5 and 43.5; 1024 of 1.2 parts 26.7 and 26.3.
   const bool few_parts = plan.shares <= 2ll * p.B * p.Hkv;
-  return few_parts || static_cast<long long>(p.B) * a.Hq * a.T >= 2048 ? launch_combine<D, 8>(p, s)
+  return few_parts || static_cast<long long>(p.B) * a.Hq * a.T >= 1536 ? launch_combine<D, 8>(p, s)
                                                                        : launch_combine<D, 1>(p, s);
 }
 

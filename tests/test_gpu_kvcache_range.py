@@ -1,6 +1,6 @@
 """Tree decode where a row's weights, values or queries span many binades: one key with
 much of the weight before a long flat tail, value rows of zeros among large ones, an
-infinity in a query.
+infinity in a query; and batches of many more sequences than there are CTAs.
 
 The bounds are those that the call promises, not the kernel's own: a probability to 2^-8
 of its value, so that their part of o is off by at most 2^-8 sum p|v|, whatever the number
@@ -155,3 +155,40 @@ def test_an_infinity_in_a_query_makes_its_row_nan(fa, fmt, d, Hq, sign):
     mask = torch.zeros(1, dtype=torch.int64, device="cuda")
     o, lse = fa.fa_decode_tree(cache, q, mask, lens=torch.zeros_like(lens))
     assert not o.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("B,Hq,Hkv,T,cap", ((5000, 1, 1, 1, 700), (700, 12, 3, 5, 300), (600, 8, 1, 20, 520), (9000, 1, 1, 1, 100)))
+def test_batches_of_many_short_sequences(fa, fmt, B, Hq, Hkv, T, cap):
+    """Many more pairs than CTAs: each share ends inside some pair, whose parts are merged."""
+    d = 64
+    g = gen(B)
+    cache = fa.KvCache(B, Hkv, cap, d, fmt)
+    x = randn(g, B, Hkv, cap, d)
+    fa.fa_cache_write(cache, x.bfloat16(), (x.flip(-1) + 0.25).bfloat16())
+    lens = torch.randint(0, cap - T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    q = randn(g, B, Hq, T, d).bfloat16()
+    o, lse = fa.fa_decode_tree(cache, q, lens=lens)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == (0, 0)
+    G = Hq // Hkv
+    j = torch.arange(T, device="cuda")
+    pos = torch.arange(cap, device="cuda")
+    for b0 in range(0, B, 250):
+        b = slice(b0, min(b0 + 250, B))
+        k = values(cache.k[b], None if cache.k_scale is None else cache.k_scale[b])
+        v = values(cache.v[b], None if cache.v_scale is None else cache.v_scale[b])
+        qq = q[b].double().reshape(-1, Hkv, G * T, d)
+        s = qq @ k.transpose(-1, -2) / math.sqrt(d)
+        last = (lens[b, None] + j[None]).repeat(1, G)[:, None, :, None]  # causal drafts
+        s = torch.where(pos <= last, s, -math.inf)
+        want_lse = torch.logsumexp(s, -1)
+        p = torch.softmax(s, -1)
+        want, a = p @ v, p @ v.abs()
+        ds = 2.0 ** -23 * (d + 8) * (qq.abs() @ k.abs().transpose(-1, -2)).amax(-1) / math.sqrt(d)
+        if fmt == "e4m3":
+            ds = ds + 2.0 ** -12.8 * qq.abs().amax(-1) * k.abs().sum(-1).amax(-1)[..., None] / math.sqrt(d)
+        tol = a * (2.0 ** -8 + 2 * ds[..., None] + 2.0 ** -18) + 2.0 ** -8 * want.abs()
+        assert ((o[b].double().reshape(want.shape) - want).abs() <= tol).all(), b0
+        off = (lse[b].double().reshape(want_lse.shape) - want_lse).abs()
+        assert (off <= ds + 2.0 ** -20 * (1 + want_lse.abs())).all(), b0
