@@ -1229,7 +1229,9 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
           ks *= __uint_as_float(kb << 23);
           ev = fmaxf(__uint_as_float(0x4b000000u | vb) - 8388735.0f,  // 2^23 + 127
                      Lazy<F8>::kLeastExponent);
-          wv = __uint_as_float(vb << 23);
+          // (a byte of 255, in a draft that was never written, is not an infinity: rows that
+          // do not see it have p = 0, and 0 times that is NaN)
+          wv = __uint_as_float(min(vb, 254u) << 23);
         }
         if (t + 1 < tiles) load_scales(bh, pos + kTile, end);
         ok = ok && t_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, 0x522);

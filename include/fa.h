@@ -327,7 +327,8 @@ int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, con
  * above cap; positions from cap on do not exist.  A draft that sees nothing has
  * o = 0 and lse = -inf.  What lies in the cache behind the drafts, or in drafts
  * that no row of the sequence sees, never reaches a result, and a NaN or
- * infinity in a draft's value row reaches only the rows that see that draft.
+ * infinity in a draft's value row, or a scale of no value beside it, reaches only
+ * the rows that see that draft.
  *  - 1 <= T <= 64, Hq >= 1, B <= 65536, B * Hq * T below 2^31, B * Hkv *
  *    (ceil(cap / 128) + 4) below 2^30.  scale > 0 and finite.
  *  - workspace: device memory, 256-byte aligned, contents irrelevant, of

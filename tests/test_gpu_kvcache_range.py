@@ -1,6 +1,7 @@
 """Tree decode where a row's weights, values or queries span many binades: one key with
 much of the weight before a long flat tail, value rows of zeros among large ones, an
-infinity in a query; and batches of many more sequences than there are CTAs.
+infinity in a query; drafts whose own rows were never written; and batches of many more
+sequences than there are CTAs.
 
 The bounds are those that the call promises, not the kernel's own: a probability to 2^-8
 of its value, so that their part of o is off by at most 2^-8 sum p|v|, whatever the number
@@ -192,3 +193,27 @@ def test_batches_of_many_short_sequences(fa, fmt, B, Hq, Hkv, T, cap):
         assert ((o[b].double().reshape(want.shape) - want).abs() <= tol).all(), b0
         off = (lse[b].double().reshape(want_lse.shape) - want_lse).abs()
         assert (off <= ds + 2.0 ** -20 * (1 + want_lse.abs())).all(), b0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("Hq,T", ((1, 5), (3, 8), (4, 16)))
+def test_padded_drafts_that_see_their_own_unwritten_rows(fa, fmt, d, Hq, T):
+    """A padded batch over memory that was never written: drafts behind a sequence's own
+    see themselves, whose rows and scales hold anything.  The others' results are right."""
+    lens, real = [130, 7], T - 2
+    cap = 200
+    g = gen(T)
+    cache = fa.KvCache(2, 1, cap, d, fmt)
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        if t is not None:
+            t.view(torch.uint8).fill_(255)  # NaN codes, bf16 NaN, scales of no value
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    k, v = (randn(g, 2, 1, cap, d).bfloat16() for _ in range(2))
+    fa.fa_cache_write(cache, k, v, lens=torch.zeros_like(n), counts=n + real)
+    q = randn(g, 2, Hq, T, d).bfloat16()
+    mask = torch.tensor([(2 << t) - 1 if t < real else 1 << t for t in range(T)], device="cuda").repeat(2, 1)
+    o, lse = fa.fa_decode_tree(cache, q, mask, lens=n)
+    rows = slice(0, real)
+    check(fa, cache, q[:, :, rows], lens, o[:, :, rows], lse[:, :, rows], 1 / math.sqrt(d),
+          [(0, 0), (1, 0)], mask[:, rows])
