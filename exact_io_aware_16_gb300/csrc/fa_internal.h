@@ -256,9 +256,10 @@ constexpr int kTreeTile = 128;  // keys a tile of the tree decode
 constexpr int kTreeRows = 64;   // query rows a row tile, at most
 
 // Units of a pair besides its tiles in the split: its start and end take 3 to 5 us of a
-// CTA, a tile 0.7 to 1 us.  32 sequences of 500 to 4096 tokens x 8 heads, 32 rows, e4m3:
-// 48.5 us with 2, 46.1 with 3, 45.4 with 4; 4 sequences of 32K to 64K tokens x 8 heads,
-// 64 rows: 114.8, 113.6 and 113.0 us.
+// CTA, a tile 0.7 to 1 us.  With 2, 3, 4 and 5: 16 sequences of up to 2048 tokens x 16
+// heads, 5 rows, bf16 22.5, 22.4, 20.5 and 20.5 us; 4 of 32K to 64K tokens x 8 heads, 64 rows,
+// e4m3 119.7, 117.9, 117.3 and 118.2 us; 32 of 500 to 4096 tokens x 8 heads, 32 rows, e4m3
+// 47.1 or 47.2 us with each.
 constexpr int kTreePairCost = 4;
 // Each CTA walks over the lengths of all sequences to find its share.
 constexpr int kTreeMaxBatch = 65536;

@@ -5,8 +5,8 @@
 // query rows against one key/value sequence: o = softmax(scale q k^T) v over the
 // committed tokens and the drafts that the row's mask names.  Every key and
 // value is read once a row tile, and ~4 R FLOPs are done for each of its
-// elements, so the step is bound by HBM up to a few dozen rows and the products
-// run on the tensor core for all of them.
+// elements: HBM's time is the floor up to a hundred rows, and it is reached for the few
+// rows of a decode step over long caches.  The products run on the tensor core for all.
 //
 // Split.  The (sequence, key head) pairs are cut into tiles of 128 keys; a pair
 // counts as many units as it has tiles and kPairCost for its start and end, and
@@ -52,15 +52,17 @@
 // its p_j may be far above 1, and is not lost however large the other rows are.
 //
 // Measured (d = 128, 8 key heads, the cache larger than L2; % of the rate of a plain
-// copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 90 us in e4m3 (89 %) and
-// 163 us in bf16 (97 %): HBM.  64 rows over 4 sequences of 32K to 64K keys in e4m3
-// 119 us (49 %): the softmax, 16 warps that issue half of the cycles (2000 a tile of
+// copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 88 us in e4m3 (90 %; 113 us
+// and 71 % for 64K keys of d = 64) and 163 us in bf16 (97 %): HBM.  64 rows over 4 sequences
+// of 32K to 64K keys in bf16 127 us (92 %), in e4m3 120 us (49 %): the softmax, 16 warps that issue half of the cycles (2000 a tile of
 // 128 keys by 64 rows), with long waits for tensor memory and the group barrier.  256
 // rows over 8 sequences of 4K to 8K keys in bf16 92 us: shared memory, whose 176 KB a
 // tile of 64 rows take 1375 of its 1400 cycles, and starts and ends of pairs (5 us
-// each).  32 rows over 32 sequences of 500 to 4096 keys in e4m3 48 us (48 %): starts
+// each).  32 rows over 32 sequences of 500 to 4096 keys in e4m3 47 us (49 %): starts
 // and ends of pairs, the first loads (5 us) and the merge (5 us).  One token over 1000
-// keys 13 us.
+// keys 13.5 us.  Over 64 rows an e4m3 cache is slower than one in bf16: 128 rows over 8
+// sequences of 32K keys 279 us against 205, the 256 rows above 123 us, since every tile
+// of 64 rows splits all its probabilities into pieces.
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -94,8 +96,8 @@ constexpr float kUnseen = 1e38f;
 // tile's largest element, where each row's own would be at most 2^kNear smaller; a
 // product of an element and a code is then off by at most 2^-12.8 of the row's largest.  Rows
 // that differ by more (a padded row may hold anything) have each its own power of two
-// and the softmax a product more for two scores: 64 rows over 4 x 8 heads of 32K to
-// 64K keys take 127 instead of 113 us so.
+// and the softmax a product more for two scores, through local memory: 64 rows over 4 x 8
+// heads of 32K to 64K keys take 183 instead of 117 us so.
 struct Queries {
   static constexpr int kNear = 4;
   static constexpr float kByRow = -1.0f;  // in place of the factor of all rows

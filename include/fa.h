@@ -344,7 +344,9 @@ int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, con
  *  - What a row of q holds reaches no other row, and a NaN or infinity in it makes
  *    its own row NaN.  Scores are taken in fp32 and
  *    in units of ln 2: a row whose scores are all below -1e38 counts as one that
- *    sees nothing.
+ *    sees nothing.  Over an e4m3 cache a row's largest score has to lie within
+ *    +-4e7 (beyond that fp32 has steps of 8), and scale times the row's largest |q|
+ *    times a key's largest element within fp32.
  */
 #define FA_TREE_MAX_DRAFTS 64
 size_t fa_decode_tree_workspace_size(const fa_cache* cache, int Hq, int T);
