@@ -1378,6 +1378,9 @@ __global__ void __launch_bounds__(TreeLayout<D, F8, NR>::kThreads, TreeLayout<D,
 // block for every pair, each of which added up all lengths, 8 rows x 4 heads of 65536
 // sequences of up to 250 tokens took 75 ms; they take 5.2.
 constexpr int kMergeThreads = 256;
+// The largest weight is 2^-9: a sum of 304 parts of a bf16's largest values stays finite.
+constexpr float kMergeRoom = 9.0f;
+static_assert(kTreeMaxSms * tree_ctas(1) <= 512, "shares");
 
 __device__ __forceinline__ void load_row(const float* src, float (&x)[4]) {
   const float4 z = *reinterpret_cast<const float4*>(src);
@@ -1445,7 +1448,7 @@ __global__ void __launch_bounds__(kMergeThreads)
         if (!there) part[i] = -INFINITY;
       }
       const float old = m;
-      m = fmaxf(fmaxf(fmaxf(m, part[0]), part[1]), fmaxf(part[2], part[3]));
+      m = fmaxf(m, fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) + kMergeRoom);
       const float ref = m == -INFINITY ? 0.0f : m;
       const float keep = ex2_approx(old - ref);
       l *= keep;
