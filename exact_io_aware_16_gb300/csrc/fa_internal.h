@@ -102,7 +102,8 @@ inline int decode_splits_run(long long BH, int Nk, int num_sms) {
 }
 
 // Scale exponents of an e4m3 cache row (fa.h): at least -100, for rows of zeros
-// as for the smallest that are worth their codes; at most 119, so that 448 * 2^119 is still a finite bf16.
+// as for the smallest that are worth their codes; at most 119, so that
+// 448 * 2^119 is still a finite bf16.
 constexpr int kScaleExpMin = -100;
 constexpr int kScaleExpMax = 119;
 
