@@ -54,11 +54,11 @@
 // Measured (d = 128, 8 key heads, the cache larger than L2; % of the rate of a plain
 // copy, 6.79 TB/s): 8 rows over 8 sequences of 32K keys 88 us in e4m3 (90 %; 113 us
 // and 71 % for 64K keys of d = 64) and 163 us in bf16 (97 %): HBM.  64 rows over 4 sequences
-// of 32K to 64K keys in bf16 127 us (92 %), in e4m3 120 us (49 %): the softmax, 16 warps that issue half of the cycles (2000 a tile of
-// 128 keys by 64 rows), with long waits for tensor memory and the group barrier.  256
-// rows over 8 sequences of 4K to 8K keys in bf16 92 us: shared memory, whose 176 KB a
-// tile of 64 rows take 1375 of its 1400 cycles, and starts and ends of pairs (5 us
-// each).  32 rows over 32 sequences of 500 to 4096 keys in e4m3 47 us (49 %): starts
+// of 32K to 64K keys in bf16 127 us (92 %), in e4m3 120 us (49 %): the softmax, 16 warps
+// that issue half of the cycles (2000 a tile of 128 keys by 64 rows), with long waits for
+// tensor memory and the group barrier.  256 rows over 8 sequences of 4K to 8K keys in bf16
+// 91 us: shared memory, whose 176 KB a tile of 64 rows take 1375 of its 1400 cycles, and
+// starts and ends of pairs (5 us each).  32 rows over 32 sequences of 500 to 4096 keys in e4m3 47 us (49 %): starts
 // and ends of pairs, the first loads (5 us) and the merge (5 us).  One token over 1000
 // keys 13.5 us.  Over 64 rows an e4m3 cache is slower than one in bf16: 128 rows over 8
 // sequences of 32K keys 279 us against 205, the 256 rows above 123 us, since every tile
