@@ -337,10 +337,10 @@ int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, con
  *  - Accuracy, bf16: as fa_decode (probabilities rounded to bf16 before the
  *    product with V, whose sums of 2^8 |v| a key have to stay in fp32).  e4m3: the
  *    products run on the cache's codes, with q as the sum of two e4m3 pieces and a
- *    probability as that of three e5m2 pieces.  An element of q is held to 2^-12.8 of the largest finite one of its row or better.
- *    A probability is held to 2^-8 of its value or, where it counts with the scale
- *    of its value row (taken as 2^-82 or more), to 2^-29 of the row's largest: of n
- *    keys together n * 2^-29.  (With value scales above 2^106, 2^-16 in place of 2^-29.)
+ *    probability as that of three e5m2 pieces.  An element of q is held to 2^-12.8
+ *    of the largest finite one of its row or better.  A probability is held to
+ *    2^-8 of its value or, where it counts with the scale of its value row (taken as
+ *    2^-82 or more), to 2^-29 of the row's largest: of n keys together n * 2^-29.  (With value scales above 2^106, 2^-16 in place of 2^-29.)
  *  - What a row of q holds reaches no other row, and a NaN or infinity in it makes
  *    its own row NaN.  Scores are taken in fp32 and
  *    in units of ln 2: a row whose scores are all below -1e38 counts as one that
