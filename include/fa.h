@@ -340,7 +340,8 @@ int fa_cache_read(const fa_cache* cache, void* k, void* v, const int* first, con
  *    probability as that of three e5m2 pieces.  An element of q is held to 2^-12.8
  *    of the largest finite one of its row or better.  A probability is held to
  *    2^-8 of its value or, where it counts with the scale of its value row (taken as
- *    2^-82 or more), to 2^-29 of the row's largest: of n keys together n * 2^-29.  (With value scales above 2^106, 2^-16 in place of 2^-29.)
+ *    2^-82 or more), to 2^-29 of the row's largest: of n keys together n * 2^-29.
+ *    (With value scales above 2^106, 2^-16 in place of 2^-29.)
  *  - What a row of q holds reaches no other row, and a NaN or infinity in it makes
  *    its own row NaN.  Scores are taken in fp32 and
  *    in units of ln 2: a row whose scores are all below -1e38 counts as one that
