@@ -58,7 +58,8 @@ def draw(rng):
         c["Hq"] = c["Hkv"] * rng.choice([1, 1, 2, 3, 4, 6, 7, 8])
         c["seqs"] = _log(rng, 1, 64)
         if op in ("prompt", "train"):
-            c["hi"] = _log(rng, 1, 8192)
+            # gradients of queries and keys are zero where a token sees itself alone
+            c["hi"] = _log(rng, 1 if op == "prompt" else 8, 8192)
             c["lo"] = rng.choice([0, rng.randint(0, c["hi"]), c["hi"]])
             c["past"] = _log(rng, 1, 8192) if op == "prompt" and rng.random() < 0.4 else 0
             c["causal"] = rng.random() < 0.75
