@@ -36,6 +36,19 @@ class _CacheStruct(ctypes.Structure):
                 ("cap", ctypes.c_int), ("d", ctypes.c_int), ("format", ctypes.c_int)]
 
 
+class _HeadsStruct(ctypes.Structure):
+    """fa_heads of include/fa.h."""
+    _fields_ = [("p", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("heads", ctypes.c_int)]
+
+
+class _RotationStruct(ctypes.Structure):
+    """fa_rotation of include/fa.h."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("amplitude", ctypes.c_float)]
+
+
 class FaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -102,6 +115,24 @@ def library():
         lib.fa_decode_tree_workspace_size.restype = sz
         lib.fa_decode_tree.argtypes = [pc, vp, vp, vp, ll, vp, vp, i, i, f, vp, sz, vp]
         lib.fa_decode_tree.restype = i
+        ph, pr, dbl = ctypes.POINTER(_HeadsStruct), ctypes.POINTER(_RotationStruct), ctypes.c_double
+        for fn in (lib.fa_forward_packed_workspace_size, lib.fa_backward_packed_workspace_size):
+            fn.argtypes = [i] * 6
+            fn.restype = sz
+        lib.fa_forward_packed.argtypes = [ph] * 4 + [vp] * 3 + [i] * 4 + [f, i, vp, sz, vp]
+        lib.fa_forward_packed.restype = i
+        lib.fa_backward_packed.argtypes = [ph] * 5 + [vp] + [ph] * 3 + [vp] * 2 + [i] * 4 + \
+            [f, i, vp, sz, vp]
+        lib.fa_backward_packed.restype = i
+        lib.fa_rotary_table.argtypes = [vp, i, dbl, i, dbl, dbl, dbl, dbl]
+        lib.fa_rotary_table.restype = i
+        for fn in (lib.fa_rotary, lib.fa_rotary_backward):
+            fn.argtypes = [pr] + [ph] * 4 + [vp, i, i, i, vp]
+            fn.restype = i
+        lib.fa_norm_rotary.argtypes = [pr] + [ph] * 4 + [vp] * 3 + [i, f, i, i, i, vp]
+        lib.fa_norm_rotary.restype = i
+        lib.fa_norm_rotary_backward.argtypes = [pr] + [ph] * 6 + [vp] * 5 + [i, f, i, i, i, vp, sz, vp]
+        lib.fa_norm_rotary_backward.restype = i
         lib.fa_backward_preprocess.argtypes = [vp, vp, vp, i, i, i, i, vp]
         lib.fa_backward_preprocess.restype = i
         lib.fa_backward_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i,
@@ -709,6 +740,338 @@ def fa_decode_tree(cache: KvCache, q, mask=None, lens=None, scale: float | None 
                 None if mask is None else mask.data_ptr(), stride, o.data_ptr(), lse.data_ptr(),
                 Hq, T, float(scale), workspace.data_ptr(), workspace.numel())
     return o, lse
+
+
+def _alloc(dev, stream):
+    """_alloc_on for a device index."""
+    if stream is None or dev < 0:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _call(dev, fn, stream, *args):
+    """fn(*args, stream) with device `dev` current."""
+    if stream is None and dev >= 0:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = _stream_handle(stream, dev)
+    if dev < 0 or dev == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != FA_OK:
+        raise FaError(st, fn.__name__)
+
+
+def _heads(t, name, dev, shape):
+    """fa_heads of a bf16 tensor of rows on device `dev`: [tokens, heads, d] or
+    [B, heads, N, d] in any strides, as long as each row is contiguous."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not _on_device(t):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if _device_index(t) != dev:
+        raise ValueError(f"{name} is on device {_device_index(t)}, the call's other tensors on "
+                         f"device {dev}")
+    s = t.stride()
+    if s[-1] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous (strides {s})")
+    if len(s) == 3:
+        return _HeadsStruct(t.data_ptr(), 0, s[0], s[1], shape[1])
+    return _HeadsStruct(t.data_ptr(), s[0], s[2], s[1], shape[1])
+
+
+def _vector(t, name, dev, dtype, shape):
+    """_check of a small contiguous tensor, and its device."""
+    _check(t, name, dtype, shape)
+    if _device_index(t) != dev:
+        raise ValueError(f"{name} is on device {_device_index(t)}, the call's other tensors on "
+                         f"device {dev}")
+    return t.data_ptr()
+
+
+def _packed_shapes(q, k, v, cu_q, cu_k):
+    """(total_q, total_k, Hq, Hkv, d, B) of a packed call."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q and k have shapes {tuple(q.shape)} and {tuple(k.shape)}, expected "
+                         "[tokens, heads, d]")
+    if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError(f"cu_q has shape {tuple(cu_q.shape)}, expected [B + 1]")
+    tq, Hq, d = q.shape
+    tk, Hkv, _ = k.shape
+    if cu_k is None and tk != tq:
+        raise ValueError(f"q has {tq} tokens and k {tk}: cu_k is needed")
+    return tq, tk, Hq, Hkv, d, cu_q.shape[0] - 1
+
+
+def _packed_workspace(workspace, need, dev, stream, device):
+    if workspace is None:
+        with _alloc(dev, stream):
+            return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    _check_workspace(workspace)
+    if _device_index(workspace) != dev:
+        raise ValueError(f"workspace is on device {_device_index(workspace)}, the call's other "
+                         f"tensors on device {dev}")
+    return workspace
+
+
+def fa_forward_packed_workspace_size(B: int, total_q: int, total_k: int, Hq: int, Hkv: int,
+                                     d: int) -> int:
+    """Bytes of workspace of fa_forward_packed (0 for an invalid shape)."""
+    return int(library().fa_forward_packed_workspace_size(B, total_q, total_k, Hq, Hkv, d))
+
+
+def fa_backward_packed_workspace_size(B: int, total_q: int, total_k: int, Hq: int, Hkv: int,
+                                      d: int) -> int:
+    """Bytes of workspace of fa_backward_packed (0 for an invalid shape)."""
+    return int(library().fa_backward_packed_workspace_size(B, total_q, total_k, Hq, Hkv, d))
+
+
+def fa_forward_packed(q, k, v, cu_q, cu_k=None, causal: bool = False, scale: float | None = None,
+                      o=None, lse=None, workspace=None, stream=None):
+    """Attention over packed sequences: (o, lse).
+
+    q: bf16 [total_q, Hq, d]; k, v: bf16 [total_k, Hkv, d], Hq a multiple of Hkv;
+    rows contiguous, other strides any multiple of 8 (parts of one projection's
+    output are taken as they lie).  cu_q: int32 [B + 1] on the GPU, the first token
+    of each sequence and the end of the last; cu_k: the same for the keys (None:
+    cu_q).  causal: query i of n sees the keys j <= i + m - n of its m.  o: as q,
+    lse: fp32 [Hq, total_q].  A query that sees no key has o = 0 and lse = -inf;
+    tokens in no sequence are left as they were.  Calls that may overlap on
+    the GPU need workspaces of their own (a new one is allocated by default)."""
+    tq, tk, Hq, Hkv, d, B = _packed_shapes(q, k, v, cu_q, cu_k)
+    dev = _device_index(q)
+    device = q.device
+    hq = _heads(q, "q", dev, (tq, Hq, d))
+    hk = _heads(k, "k", dev, (tk, Hkv, d))
+    hv = _heads(v, "v", dev, (tk, Hkv, d))
+    pq = _vector(cu_q, "cu_q", dev, torch.int32, (B + 1,))
+    pk = None if cu_k is None else _vector(cu_k, "cu_k", dev, torch.int32, (B + 1,))
+    if o is None or lse is None:
+        with _alloc(dev, stream):
+            o = torch.empty((tq, Hq, d), dtype=torch.bfloat16, device=device) if o is None else o
+            lse = torch.empty((Hq, tq), dtype=torch.float32, device=device) if lse is None else lse
+    ho = _heads(o, "o", dev, (tq, Hq, d))
+    pl = _vector(lse, "lse", dev, torch.float32, (Hq, tq))
+    lib = library()
+    workspace = _packed_workspace(
+        workspace, lib.fa_forward_packed_workspace_size(B, tq, tk, Hq, Hkv, d), dev, stream, device)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    _call(dev, lib.fa_forward_packed, stream, ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
+          ctypes.byref(ho), pl, pq, pk, B, tq, tk, d, float(scale), int(bool(causal)),
+          workspace.data_ptr(), workspace.numel())
+    return o, lse
+
+
+def fa_backward_packed(q, k, v, o, dO, lse, cu_q, cu_k=None, causal: bool = False,
+                       scale: float | None = None, dq=None, dk=None, dv=None, workspace=None,
+                       stream=None):
+    """(dq, dk, dv) of fa_forward_packed from the gradient dO of o; dk and dv are sums
+    over the query heads of each key head's group.  Shapes, strides and lengths as
+    there.  Keys that no query sees get zeros; tokens in no sequence are left as
+    they were."""
+    tq, tk, Hq, Hkv, d, B = _packed_shapes(q, k, v, cu_q, cu_k)
+    dev = _device_index(q)
+    device = q.device
+    qs, ks = (tq, Hq, d), (tk, Hkv, d)
+    hq, hk, hv = _heads(q, "q", dev, qs), _heads(k, "k", dev, ks), _heads(v, "v", dev, ks)
+    ho, hg = _heads(o, "o", dev, qs), _heads(dO, "dO", dev, qs)
+    pl = _vector(lse, "lse", dev, torch.float32, (Hq, tq))
+    pq = _vector(cu_q, "cu_q", dev, torch.int32, (B + 1,))
+    pk = None if cu_k is None else _vector(cu_k, "cu_k", dev, torch.int32, (B + 1,))
+    if dq is None or dk is None or dv is None:
+        with _alloc(dev, stream):
+            dq, dk, dv = (torch.empty(s, dtype=torch.bfloat16, device=device) if t is None else t
+                          for t, s in ((dq, qs), (dk, ks), (dv, ks)))
+    hdq, hdk, hdv = _heads(dq, "dq", dev, qs), _heads(dk, "dk", dev, ks), _heads(dv, "dv", dev, ks)
+    lib = library()
+    workspace = _packed_workspace(
+        workspace, lib.fa_backward_packed_workspace_size(B, tq, tk, Hq, Hkv, d), dev, stream, device)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    ref = ctypes.byref
+    _call(dev, lib.fa_backward_packed, stream, ref(hq), ref(hk), ref(hv), ref(ho), ref(hg), pl,
+          ref(hdq), ref(hdk), ref(hdv), pq, pk, B, tq, tk, d, float(scale), int(bool(causal)),
+          workspace.data_ptr(), workspace.numel())
+    return dq, dk, dv
+
+
+class Rotary:
+    """The rotation of heads of d elements by their tokens' positions: the first
+    `rot` elements (all unless given; a multiple of 16) turn in pairs, (i, i + rot / 2)
+    or, interleaved, (2i, 2i + 1), pair i by base^(-2i / rot) radians a position.
+
+    scaling, for contexts longer than those trained on: None; "linear" (all
+    angles divided by factor); "base" (the base raised so that the slowest pair is
+    divided by factor); "turns" or "index" (pairs that turn more than `high` times
+    within the `original` context stay, those below `low` are divided by factor,
+    between them a blend, linear in the turns or in the pair's index).  amplitude
+    multiplies the rotated elements.  turns: the table, torch.int64 [rot / 2] on
+    the GPU (unsigned 64-bit fractions of a turn), which the object keeps."""
+
+    _SCALING = {None: 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
+
+    def __init__(self, d: int, rot: int | None = None, base: float = 10000.0,
+                 interleaved: bool = False, scaling: str | None = None, factor: float = 1.0,
+                 original: float = 0.0, low: float = 1.0, high: float = 32.0,
+                 amplitude: float = 1.0, device=None):
+        rot = d if rot is None else int(rot)
+        if scaling not in self._SCALING:
+            raise ValueError(f"scaling must be one of {list(self._SCALING)}, got {scaling!r}")
+        if not 16 <= rot <= d or rot % 16:
+            raise ValueError(f"rot must be a multiple of 16 up to d = {d}, got {rot}")
+        table = (ctypes.c_ulonglong * (rot // 2))()
+        st = library().fa_rotary_table(table, rot, float(base), self._SCALING[scaling],
+                                       float(factor), float(original), float(low), float(high))
+        if st != FA_OK:
+            raise FaError(st, "fa_rotary_table")
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        self._hold(d, torch.tensor([x - (1 << 64) if x >> 63 else x for x in table],
+                                   dtype=torch.int64).to(dev), interleaved, amplitude)
+
+    @classmethod
+    def from_table(cls, d: int, turns, interleaved: bool = False, amplitude: float = 1.0):
+        """The rotation by a table of the caller's: torch.int64 [rot / 2] on the GPU, the
+        turns of each pair a position times 2^64, modulo 2^64."""
+        self = cls.__new__(cls)
+        if turns.dim() != 1:
+            raise ValueError(f"turns has shape {tuple(turns.shape)}, expected [rot / 2]")
+        _check(turns, "turns", torch.int64)
+        self._hold(d, turns, interleaved, amplitude)
+        return self
+
+    def _hold(self, d, turns, interleaved, amplitude):
+        self.d, self.turns, self.rot = int(d), turns, 2 * turns.shape[0]
+        self.interleaved, self.amplitude = bool(interleaved), float(amplitude)
+        self._dev = _device_index(turns)
+        self._struct = _RotationStruct(turns.data_ptr(), self.rot, int(self.interleaved),
+                                       self.amplitude)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _rotary_shapes(rotary, q, k, positions):
+    """(B, N, shape of k or None, pointer of the positions) of a call on q and k."""
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, heads, d] or "
+                         "[B, heads, N, d]")
+    if q.shape[-1] != rotary.d:
+        raise ValueError(f"q has rows of {q.shape[-1]} elements, the rotation of {rotary.d}")
+    B, N = (1, q.shape[0]) if q.dim() == 3 else (q.shape[0], q.shape[2])
+    ks = None
+    if k is not None:
+        if k.dim() != q.dim():
+            raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+        ks = (N, k.shape[1], rotary.d) if q.dim() == 3 else (B, k.shape[1], N, rotary.d)
+    pos = None
+    if positions is not None:
+        pos = _vector(positions, "positions", rotary._dev, torch.int32,
+                      (N,) if q.dim() == 3 else (B, N))
+    return B, N, ks, pos
+
+
+def _rotary_outputs(rotary, stream, *pairs):
+    """The outputs that were not given, as the inputs without gaps."""
+    if all(y is not None or x is None for x, y in pairs):
+        return [y for _, y in pairs]
+    with _alloc(rotary._dev, stream):
+        return [torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+                if y is None and x is not None else y for x, y in pairs]
+
+
+def _refs(rotary, *named):
+    return [None if t is None else ctypes.byref(_heads(t, name, rotary._dev, shape))
+            for t, name, shape in named]
+
+
+def _rotate(fn, rotary, q, k, positions, names, q_out, k_out, stream):
+    B, N, ks, pos = _rotary_shapes(rotary, q, k, positions)
+    q_out, k_out = _rotary_outputs(rotary, stream, (q, q_out), (k, k_out))
+    refs = _refs(rotary, (q, names[0], q.shape), (k, names[1], ks), (q_out, names[2], q.shape),
+                 (None if k is None else k_out, names[3], ks))
+    _call(rotary._dev, fn, stream, rotary._ref, *refs, pos, B, N, rotary.d)
+    return q_out, (None if k is None else k_out)
+
+
+def fa_rotary(rotary: Rotary, q, k=None, positions=None, q_out=None, k_out=None, stream=None):
+    """(q, k) rotated by their tokens' positions (k None: q alone).
+
+    q, k: bf16 [tokens, heads, d] with positions int32 [tokens], or [B, heads, N, d]
+    with positions int32 [B, N]; None: each token's place, from 0.  Rows
+    contiguous, other strides any multiple of 8.  q_out may be q, and k_out k."""
+    return _rotate(library().fa_rotary, rotary, q, k, positions, ("q", "k", "q_out", "k_out"),
+                   q_out, k_out, stream)
+
+
+def fa_rotary_backward(rotary: Rotary, dq, dk=None, positions=None, dq_in=None, dk_in=None,
+                       stream=None):
+    """The gradients of fa_rotary's inputs from those of its results; arguments as
+    there (dq_in may be dq, and dk_in dk)."""
+    return _rotate(library().fa_rotary_backward, rotary, dq, dk, positions,
+                   ("dq", "dk", "dq_in", "dk_in"), dq_in, dk_in, stream)
+
+
+def _weights(rotary, k, q_weight, k_weight):
+    """(pointers, 1 for bf16) of a norm's weights."""
+    dtype = q_weight.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"q_weight must be torch.float32 or torch.bfloat16, got {dtype}")
+    if k is not None and k_weight is None:
+        raise ValueError("k needs k_weight")
+    return (_vector(q_weight, "q_weight", rotary._dev, dtype, (rotary.d,)),
+            None if k is None else _vector(k_weight, "k_weight", rotary._dev, dtype, (rotary.d,)),
+            int(dtype is torch.bfloat16))
+
+
+def fa_norm_rotary(rotary: Rotary, q, k, positions, q_weight, k_weight=None, eps: float = 1e-6,
+                   q_out=None, k_out=None, stream=None):
+    """(q, k) with each head divided by its root mean square (eps added to the mean
+    square), times q_weight or k_weight ([d], both fp32 or both bf16), and rotated.
+    Otherwise as fa_rotary."""
+    B, N, ks, pos = _rotary_shapes(rotary, q, k, positions)
+    wq, wk, wfmt = _weights(rotary, k, q_weight, k_weight)
+    q_out, k_out = _rotary_outputs(rotary, stream, (q, q_out), (k, k_out))
+    refs = _refs(rotary, (q, "q", q.shape), (k, "k", ks), (q_out, "q_out", q.shape),
+                 (None if k is None else k_out, "k_out", ks))
+    _call(rotary._dev, library().fa_norm_rotary, stream, rotary._ref, *refs, pos, wq, wk, wfmt,
+          float(eps), B, N, rotary.d)
+    return q_out, (None if k is None else k_out)
+
+
+FA_NORM_WORKSPACE = 1048576
+
+
+def fa_norm_rotary_backward(rotary: Rotary, dq, dk, q, k, positions, q_weight, k_weight=None,
+                            eps: float = 1e-6, dq_in=None, dk_in=None, dq_weight=None,
+                            dk_weight=None, workspace=None, stream=None):
+    """(dq_in, dk_in, dq_weight, dk_weight) of fa_norm_rotary from the gradients dq, dk of
+    its results and its inputs q, k.  The weights' gradients are fp32 [d].  dq_in may be
+    dq, and dk_in dk.  Calls that may overlap need workspaces of their own
+    (FA_NORM_WORKSPACE bytes; a new one is allocated by default)."""
+    B, N, ks, pos = _rotary_shapes(rotary, q, k, positions)
+    if k is not None and dk is None:
+        raise ValueError("k needs dk")
+    wq, wk, wfmt = _weights(rotary, k, q_weight, k_weight)
+    q1, k1 = (q, k) if k is not None else (q, None)
+    dq_in, dk_in = _rotary_outputs(rotary, stream, (q1, dq_in), (k1, dk_in))
+    if dq_weight is None or (k is not None and dk_weight is None):
+        with _alloc(rotary._dev, stream):
+            new = [torch.empty(rotary.d, dtype=torch.float32, device=q.device) for _ in range(2)]
+        dq_weight = new[0] if dq_weight is None else dq_weight
+        dk_weight = new[1] if dk_weight is None else dk_weight
+    pwq = _vector(dq_weight, "dq_weight", rotary._dev, torch.float32, (rotary.d,))
+    pwk = None if k is None else _vector(dk_weight, "dk_weight", rotary._dev, torch.float32,
+                                         (rotary.d,))
+    workspace = _packed_workspace(workspace, FA_NORM_WORKSPACE, rotary._dev, stream, q.device)
+    none = k is None
+    refs = _refs(rotary, (dq, "dq", q.shape), (None if none else dk, "dk", ks), (q, "q", q.shape),
+                 (k, "k", ks), (dq_in, "dq_in", q.shape), (None if none else dk_in, "dk_in", ks))
+    _call(rotary._dev, library().fa_norm_rotary_backward, stream, rotary._ref, *refs, pwq, pwk,
+          pos, wq, wk, wfmt, float(eps), B, N, rotary.d, workspace.data_ptr(), workspace.numel())
+    return dq_in, (None if none else dk_in), dq_weight, (None if none else dk_weight)
 
 
 def fa_backward_workspace_size(B: int, H: int, N: int, d: int) -> int:

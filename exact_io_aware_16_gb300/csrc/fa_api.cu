@@ -635,6 +635,263 @@ int fa_decode_tree(const fa_cache* cache, const void* q, const int* lens,
              : FA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- packed sequences
+// A tensor of `heads` heads of B x T token rows as the kernels take it: strides that no
+// element depends on put to what they would be in memory without gaps.
+static int view_heads(const fa_heads* t, int heads, long long B, long long T, int d,
+                      fa::HeadsView* v) {
+  if (!t || (!t->p && T > 0)) return FA_ERR_NULL;
+  if (t->heads != heads || heads < 1) return FA_ERR_SHAPE;
+  v->p = t->p;
+  v->heads = heads;
+  v->head = heads > 1 ? t->head_stride : d;
+  v->token = T > 1 ? t->token_stride : v->head * heads;
+  if (T <= 1 && heads <= 1) v->token = d;
+  v->batch = B > 1 ? t->batch_stride : 0;
+  if (heads > 1 && v->head < d) return FA_ERR_SHAPE;
+  if (T > 1 && v->token < d) return FA_ERR_SHAPE;
+  // 2^31 tokens and heads of at most 2^40 bytes between rows stay within 64 bits
+  const long long most = 1ll << 38;
+  if (v->head > most || v->token > most || v->batch < 0 || v->batch > most) return FA_ERR_SHAPE;
+  const bool heads_inside = v->token >= (heads - 1) * v->head + d;
+  const bool tokens_inside = T < 1 || v->head >= (T - 1) * v->token + d;
+  if (heads > 1 && T > 1 && !heads_inside && !tokens_inside) return FA_ERR_SHAPE;
+  if (B > 1 && v->batch < d) return FA_ERR_SHAPE;
+  if (!aligned16(t->p) || (v->head & 7) || (v->token & 7) || (v->batch & 7)) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+static int check_packed(int B, int total_q, int total_k, int Hq, int Hkv, int d) {
+  if (B < 1 || B >= (1 << 20) || total_q < 0 || total_k < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
+    return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_HEADDIM;
+  if (Hq * (total_q / 8ll + B) > 0x7fffffffll || Hkv * (total_k / 128ll + B) > 0x7fffffffll)
+    return FA_ERR_SHAPE;
+  return FA_OK;
+}
+
+size_t fa_forward_packed_workspace_size(int B, int total_q, int total_k, int Hq, int Hkv, int d) {
+  if (check_packed(B, total_q, total_k, Hq, Hkv, d) != FA_OK) return 0;
+  return fa::packed_workspace_bytes(B, total_q, total_k, Hq, Hkv, false);
+}
+
+size_t fa_backward_packed_workspace_size(int B, int total_q, int total_k, int Hq, int Hkv, int d) {
+  if (check_packed(B, total_q, total_k, Hq, Hkv, d) != FA_OK) return 0;
+  return fa::packed_workspace_bytes(B, total_q, total_k, Hq, Hkv, true);
+}
+
+// What both passes check; the views of q, k, v and o.
+static int packed_args(const fa_heads* q, const fa_heads* k, const fa_heads* v, const fa_heads* o,
+                       const float* lse, const int* cu_q, const int* cu_k, int B, int total_q,
+                       int total_k, int d, float scale, int causal, void* workspace,
+                       size_t workspace_bytes, bool backward, fa::PackedArgs* a) {
+  if (!q || !k || !v || !o || !cu_q || (!lse && total_q > 0)) return FA_ERR_NULL;
+  int st = check_packed(B, total_q, total_k, q->heads, k->heads, d);
+  if (st != FA_OK) return st;
+  if (!cu_k && total_k != total_q) return FA_ERR_SHAPE;
+  if ((st = check_scale(scale)) != FA_OK) return st;
+  if ((st = view_heads(q, q->heads, 1, total_q, d, &a->q)) != FA_OK ||
+      (st = view_heads(k, k->heads, 1, total_k, d, &a->k)) != FA_OK ||
+      (st = view_heads(v, k->heads, 1, total_k, d, &a->v)) != FA_OK ||
+      (st = view_heads(o, q->heads, 1, total_q, d, &a->o)) != FA_OK)
+    return st;
+  if (!aligned4(lse) || !aligned4(cu_q) || !aligned4(cu_k)) return FA_ERR_ALIGN;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < fa::packed_workspace_bytes(B, total_q, total_k, q->heads, k->heads, backward))
+    return FA_ERR_WORKSPACE;
+  a->cu_q = cu_q;
+  a->cu_k = cu_k ? cu_k : cu_q;
+  a->B = B;
+  a->total_q = total_q;
+  a->total_k = total_k;
+  a->d = d;
+  a->scale = scale;
+  a->causal = causal ? 1 : 0;
+  a->workspace = workspace;
+  return FA_OK;
+}
+
+int fa_forward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, const fa_heads* o,
+                      float* lse, const int* cu_q, const int* cu_k, int B, int total_q,
+                      int total_k, int d, float scale, int causal, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  fa::PackedArgs a{};
+  int st = packed_args(q, k, v, o, lse, cu_q, cu_k, B, total_q, total_k, d, scale, causal,
+                       workspace, workspace_bytes, false, &a);
+  if (st != FA_OK) return st;
+  if ((st = check_arch()) != FA_OK) return st;
+  a.lse = lse;
+  a.num_sms = num_sms();
+  if (total_q == 0) return FA_OK;
+  return fa::launch_forward_packed(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+int fa_backward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, const fa_heads* o,
+                       const fa_heads* dO, const float* lse, const fa_heads* dq,
+                       const fa_heads* dk, const fa_heads* dv, const int* cu_q, const int* cu_k,
+                       int B, int total_q, int total_k, int d, float scale, int causal,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  fa::PackedArgs a{};
+  if (!dO || !dq || !dk || !dv) return FA_ERR_NULL;
+  int st = packed_args(q, k, v, o, lse, cu_q, cu_k, B, total_q, total_k, d, scale, causal,
+                       workspace, workspace_bytes, true, &a);
+  if (st != FA_OK) return st;
+  if ((st = view_heads(dO, q->heads, 1, total_q, d, &a.dO)) != FA_OK ||
+      (st = view_heads(dq, q->heads, 1, total_q, d, &a.dq)) != FA_OK ||
+      (st = view_heads(dk, k->heads, 1, total_k, d, &a.dk)) != FA_OK ||
+      (st = view_heads(dv, k->heads, 1, total_k, d, &a.dv)) != FA_OK)
+    return st;
+  if ((st = check_arch()) != FA_OK) return st;
+  a.lse = const_cast<float*>(lse);
+  a.num_sms = num_sms();
+  if (total_q == 0 && total_k == 0) return FA_OK;
+  return fa::launch_backward_packed(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- rotation
+int fa_rotary_table(unsigned long long* turns, int rot, double base, int scaling, double factor,
+                    double original, double low, double high) {
+  if (!turns) return FA_ERR_NULL;
+  if (rot < 16 || rot > 128 || rot % 16 != 0) return FA_ERR_SHAPE;
+  if (!(base > 1.0) || !std::isfinite(base)) return FA_ERR_SHAPE;
+  if (scaling < FA_SCALE_NONE || scaling > FA_SCALE_INDEX) return FA_ERR_SHAPE;
+  const bool blend = scaling == FA_SCALE_TURNS || scaling == FA_SCALE_INDEX;
+  if (scaling != FA_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return FA_ERR_SHAPE;
+  if (blend && (!(original >= 1.0) || !std::isfinite(original) || !(low > 0.0) || !(high > low) ||
+                !std::isfinite(high)))
+    return FA_ERR_SHAPE;
+  const double pi = 3.14159265358979323846;
+  if (scaling == FA_SCALE_BASE) base *= std::pow(factor, rot / (rot - 2.0));
+  if (!std::isfinite(base)) return FA_ERR_SHAPE;
+  // the pair that makes t turns within the original context: original * base^(-2i/rot) = 2 pi t
+  auto pair_of = [&](double t) { return rot * std::log(original / (2.0 * pi * t)) / (2.0 * std::log(base)); };
+  double first = 0.0, last = 1.0;
+  if (scaling == FA_SCALE_INDEX) {
+    first = std::fmax(std::floor(pair_of(high)), 0.0);
+    last = std::fmin(std::ceil(pair_of(low)), rot - 1.0);
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scaling == FA_SCALE_LINEAR) f /= factor;
+    if (blend) {
+      const double g = scaling == FA_SCALE_TURNS
+                           ? (original * f / (2.0 * pi) - low) / (high - low)
+                           : 1.0 - (i - first) / std::fmax(last - first, 1e-3);
+      const double keep = std::fmin(std::fmax(g, 0.0), 1.0);
+      f = keep * f + (1.0 - keep) * f / factor;
+    }
+    turns[i] = static_cast<unsigned long long>(std::nearbyint(f / (2.0 * pi) * 18446744073709551616.0));
+  }
+  return FA_OK;
+}
+
+// What all four calls check; inputs x and, for the norm's backward pass, g.
+static int rotary_args(const fa_rotation* r, const fa_heads* const x[2], const fa_heads* const g[2],
+                       const fa_heads* const y[2], const int* positions, int B, int N, int d,
+                       bool back, fa::RotaryArgs* a) {
+  if (!r || !r->turns || !x[0] || !y[0] || (x[1] && !y[1])) return FA_ERR_NULL;
+  if (back && (!g[0] || (x[1] && !g[1]))) return FA_ERR_NULL;
+  if (d != 64 && d != 128) return FA_ERR_HEADDIM;
+  if (r->rot < 16 || r->rot > d || r->rot % 16 != 0 || !std::isfinite(r->amplitude))
+    return FA_ERR_SHAPE;
+  if (B < 1 || N < 1 || static_cast<long long>(B) * N > 0x7fffffffll) return FA_ERR_SHAPE;
+  for (int t = 0; t < 2; ++t) {
+    a->x[t].heads = a->g[t].heads = a->y[t].heads = 0;
+    if (!x[t]) continue;
+    const int heads = x[t]->heads;
+    if (heads < 1 || static_cast<long long>(B) * N > 0x7fffffffll / heads) return FA_ERR_SHAPE;
+    int st = view_heads(x[t], heads, B, N, d, &a->x[t]);
+    if (st == FA_OK) st = view_heads(y[t], heads, B, N, d, &a->y[t]);
+    if (st == FA_OK && back) st = view_heads(g[t], heads, B, N, d, &a->g[t]);
+    if (st != FA_OK) return st;
+  }
+  if (!aligned4(positions) || (reinterpret_cast<uintptr_t>(r->turns) & 7u) != 0) return FA_ERR_ALIGN;
+  a->positions = positions;
+  a->turns = r->turns;
+  a->rot = r->rot;
+  a->interleaved = r->interleaved != 0;
+  a->amplitude = r->amplitude;
+  a->tokens = static_cast<long long>(B) * N;
+  a->N = N;
+  return FA_OK;
+}
+
+static int run_rotary(fa::RotaryArgs& a, int mode, int d, void* stream) {
+  const int st = check_arch();
+  if (st != FA_OK) return st;
+  a.num_sms = num_sms();
+  return fa::launch_rotary(a, mode, d, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+int fa_rotary(const fa_rotation* r, const fa_heads* q, const fa_heads* k, const fa_heads* q_out,
+              const fa_heads* k_out, const int* positions, int B, int N, int d, void* stream) {
+  const fa_heads *x[2] = {q, k}, *y[2] = {q_out, k_out};
+  fa::RotaryArgs a{};
+  const int st = rotary_args(r, x, x, y, positions, B, N, d, false, &a);
+  return st != FA_OK ? st : run_rotary(a, 0, d, stream);
+}
+
+int fa_rotary_backward(const fa_rotation* r, const fa_heads* dq, const fa_heads* dk,
+                       const fa_heads* dq_in, const fa_heads* dk_in, const int* positions, int B,
+                       int N, int d, void* stream) {
+  const fa_heads *x[2] = {dq, dk}, *y[2] = {dq_in, dk_in};
+  fa::RotaryArgs a{};
+  const int st = rotary_args(r, x, x, y, positions, B, N, d, false, &a);
+  return st != FA_OK ? st : run_rotary(a, 1, d, stream);
+}
+
+static int norm_args(const void* q_weight, const void* k_weight, int weight_bf16, float eps,
+                     bool keys, fa::RotaryArgs* a) {
+  if (!q_weight || (keys && !k_weight)) return FA_ERR_NULL;
+  if ((weight_bf16 != 0 && weight_bf16 != 1) || !(eps >= 0.0f) || !std::isfinite(eps))
+    return FA_ERR_SHAPE;
+  if (!aligned16(q_weight) || (keys && !aligned16(k_weight))) return FA_ERR_ALIGN;
+  a->weight[0] = q_weight;
+  a->weight[1] = k_weight;
+  a->weight_bf16 = weight_bf16 != 0;
+  a->eps = eps;
+  return FA_OK;
+}
+
+int fa_norm_rotary(const fa_rotation* r, const fa_heads* q, const fa_heads* k,
+                   const fa_heads* q_out, const fa_heads* k_out, const int* positions,
+                   const void* q_weight, const void* k_weight, int weight_bf16, float eps, int B,
+                   int N, int d, void* stream) {
+  const fa_heads *x[2] = {q, k}, *y[2] = {q_out, k_out};
+  fa::RotaryArgs a{};
+  int st = rotary_args(r, x, x, y, positions, B, N, d, false, &a);
+  if (st == FA_OK) st = norm_args(q_weight, k_weight, weight_bf16, eps, k != nullptr, &a);
+  return st != FA_OK ? st : run_rotary(a, 2, d, stream);
+}
+
+int fa_norm_rotary_backward(const fa_rotation* r, const fa_heads* dq, const fa_heads* dk,
+                            const fa_heads* q, const fa_heads* k, const fa_heads* dq_in,
+                            const fa_heads* dk_in, float* dq_weight, float* dk_weight,
+                            const int* positions, const void* q_weight, const void* k_weight,
+                            int weight_bf16, float eps, int B, int N, int d, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  const fa_heads *x[2] = {q, k}, *g[2] = {dq, dk}, *y[2] = {dq_in, dk_in};
+  fa::RotaryArgs a{};
+  int st = rotary_args(r, x, g, y, positions, B, N, d, true, &a);
+  if (st == FA_OK) st = norm_args(q_weight, k_weight, weight_bf16, eps, k != nullptr, &a);
+  if (st != FA_OK) return st;
+  if (!dq_weight || (k && !dk_weight)) return FA_ERR_NULL;
+  if (!aligned16(dq_weight) || (k && !aligned16(dk_weight))) return FA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < FA_NORM_WORKSPACE ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return FA_ERR_WORKSPACE;
+  a.dw[0] = dq_weight;
+  a.dw[1] = k ? dk_weight : nullptr;
+  a.partial = static_cast<float*>(workspace);
+  return run_rotary(a, 3, d, stream);
+}
+
 int fa_selftest_wait_timeout(void* stream) {
   const int st = check_arch();
   if (st != FA_OK) return st;

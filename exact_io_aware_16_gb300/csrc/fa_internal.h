@@ -157,7 +157,66 @@ struct TreeArgs {
   int num_sms;
 };
 
+// A tensor of token rows (fa_heads with the strides of single entries put right).
+struct HeadsView {
+  const void* p;
+  long long batch, token, head;
+  int heads;  // 0: not given
+};
+
+// Rotation of q ([0]) and k ([1]); the norm's backward pass reads x and g.
+struct RotaryArgs {
+  HeadsView x[2], g[2], y[2];
+  const int* positions;
+  const unsigned long long* turns;
+  int rot;
+  bool interleaved;
+  float amplitude;
+  const void* weight[2];
+  bool weight_bf16;
+  float eps;
+  float* partial;  // weight gradients of each block
+  float* dw[2];
+  long long tokens;  // B * N
+  int N;
+  int parts;  // set by the launch
+  int num_sms;
+};
+
+// Blocks of the norm's backward pass, at most: 2 d floats each fill its workspace.
+constexpr int kNormMaxBlocks = FA_NORM_WORKSPACE / (2 * 128 * 4);
+
+// Attention over packed sequences (fa.h).
+struct PackedArgs {
+  HeadsView q, k, v, o, dO, dq, dk, dv;
+  float* lse;
+  const int* cu_q;
+  const int* cu_k;
+  int B, total_q, total_k, d;
+  float scale;
+  int causal;
+  void* workspace;
+  int num_sms;
+};
+
+// Heads of a group whose rows share a tile: all of them, or the largest divisor of
+// their number up to 16 (a tile of 128 rows then holds 8 tokens or more).
+inline int packed_heads(int G) {
+  int p = G < 16 ? G : 16;
+  while (G % p) --p;
+  return p;
+}
+
+// Workspace of a packed call.  TODO
+inline size_t packed_workspace_bytes(int B, int total_q, int total_k, int Hq, int Hkv, bool backward) {
+  return 256;
+}
+
 cudaError_t launch_forward(const FwdArgs& a, cudaStream_t s);
+// mode 0: rotation, 1: rotation backwards, 2: norm and rotation, 3: its backward pass
+cudaError_t launch_rotary(const RotaryArgs& a, int mode, int d, cudaStream_t s);
+cudaError_t launch_forward_packed(const PackedArgs& a, cudaStream_t s);
+cudaError_t launch_backward_packed(const PackedArgs& a, cudaStream_t s);
 cudaError_t launch_cache_write(const CacheMoveArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheMoveArgs& a, cudaStream_t s);
 cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t s);

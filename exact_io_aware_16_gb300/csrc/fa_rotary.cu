@@ -1,0 +1,328 @@
+// fa_rotary.cu — rotation of queries and keys by their positions, with or without a
+// norm of each head before it, forward and backward.
+//
+// Rows of d bf16 (a token's head) pass through once: 2 d bytes in, 2 d bytes out and a
+// few operations an element, so every call is bound by memory, and the small ones by
+// the launch.  d / 16 lanes hold a row, sixteen elements each as two 16-byte
+// chunks chosen so that both members of a pair lie in one lane: the chunks at 8 s
+// and rot / 2 + 8 s of lane s where pairs are (i, i + rot / 2), otherwise the two
+// halves of elements 16 s .. 16 s + 15.  Either way lane s needs the angles of
+// pairs 8 s .. 8 s + 7 and nothing from its neighbours.
+//
+// Angles: position * turns[i] modulo 2^64 is the exact angle in units of 2^-64 turns
+// (the table holds f_i / 2 pi to 2^-65), and its upper 32 bits, read as signed, are the
+// angle in (-1/2, 1/2] turns.  sincospif of twice that needs no range reduction; all
+// of it is off by about 2^-23, however far the position.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kRotaryThreads = 256;
+constexpr int kWarps = kRotaryThreads / 32;
+
+struct Row16 {
+  uint4 a, b;  // the lane's two chunks of eight bf16
+};
+
+__device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Where a lane's chunks lie in a row, and whether they turn.
+struct LaneMap {
+  int a, b;
+  bool turns, half;
+};
+
+template <int D>
+__device__ __forceinline__ LaneMap lane_map(int sub, const RotaryArgs& p) {
+  LaneMap m;
+  m.turns = sub < p.rot / 16;
+  m.half = m.turns && !p.interleaved;
+  m.a = m.half ? 8 * sub : 16 * sub;
+  m.b = m.half ? p.rot / 2 + 8 * sub : 16 * sub + 8;
+  return m;
+}
+
+// Cosines and sines (times the amplitude) of pairs 8 sub .. 8 sub + 7 at position
+// `pos`.  The 32 * 16 / D row groups of the warp find an equal share each and hand
+// the others theirs.
+template <int D>
+__device__ __forceinline__ void lane_angles(const RotaryArgs& p, const LaneMap& m, int sub, int grp,
+                                            int pos, float (&c)[8], float (&s)[8]) {
+  constexpr int L = D / 16, E = 8 * L / 32;  // lanes a row, pairs a lane
+  float mc[E], ms[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    mc[e] = 1.0f;
+    ms[e] = 0.0f;
+    if (m.turns) {
+      const unsigned long long turn = p.turns[8 * sub + E * grp + e];
+      const unsigned long long at = static_cast<unsigned long long>(static_cast<long long>(pos)) * turn;
+      const float x = static_cast<float>(static_cast<int>(at >> 32)) * 0x1p-31f;  // half turns
+      sincospif(x, &ms[e], &mc[e]);
+      mc[e] *= p.amplitude;
+      ms[e] *= p.amplitude;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c[j] = __shfl_sync(0xffffffffu, mc[j % E], (j / E) * L + sub);
+    s[j] = __shfl_sync(0xffffffffu, ms[j % E], (j / E) * L + sub);
+  }
+}
+
+// Turns the lane's eight pairs; `sign` -1: backwards.
+__device__ __forceinline__ void turn(const LaneMap& m, float (&a)[8], float (&b)[8],
+                                     const float (&c)[8], const float (&s)[8], float sign) {
+  if (!m.turns) return;
+  if (m.half) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = a[j], y = b[j], sj = sign * s[j];
+      a[j] = x * c[j] - y * sj;
+      b[j] = y * c[j] + x * sj;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x = a[2 * j], y = a[2 * j + 1], sj = sign * s[j];
+      a[2 * j] = x * c[j] - y * sj;
+      a[2 * j + 1] = y * c[j] + x * sj;
+      x = b[2 * j];
+      y = b[2 * j + 1];
+      sj = sign * s[4 + j];
+      b[2 * j] = x * c[4 + j] - y * sj;
+      b[2 * j + 1] = y * c[4 + j] + x * sj;
+    }
+  }
+}
+
+template <int L>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+__device__ __forceinline__ void load_weight8(const RotaryArgs& p, int t, int at, float (&w)[8]) {
+  if (p.weight_bf16) {
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.weight[t]) + at), w);
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.weight[t]) + at);
+    const float4 x = q[0], y = q[1];
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+  }
+}
+
+__device__ __forceinline__ const __nv_bfloat16* row_at(const HeadsView& t, long long b, long long i,
+                                                       long long h) {
+  return static_cast<const __nv_bfloat16*>(t.p) + b * t.batch + i * t.token + h * t.head;
+}
+
+// One warp takes a token, or (p.parts > 1: few tokens) every parts-th group of its
+// heads.  MODE 0: rotation, 1: rotation backwards, 2: norm and rotation, 3: its
+// backward pass, whose weight gradients a warp gathers over all its tokens.
+template <int D, int MODE>
+__global__ void __launch_bounds__(kRotaryThreads) fa_rotary_kernel(const RotaryArgs p) {
+  constexpr int L = D / 16, R = 32 / L;  // lanes a row, rows a step
+  constexpr bool kNorm = MODE >= 2, kBack = MODE == 3;
+  constexpr float kSign = (MODE & 1) ? -1.0f : 1.0f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane % L, grp = lane / L;
+  const LaneMap m = lane_map<D>(sub, p);
+  float dw[kBack ? 2 : 1][16];
+  if (kBack) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) dw[kBack ? t : 0][j] = 0.0f;
+  }
+  const long long units = p.tokens * p.parts;
+  for (long long u = static_cast<long long>(blockIdx.x) * kWarps + warp; u < units;
+       u += static_cast<long long>(gridDim.x) * kWarps) {
+    const long long tok = u / p.parts;
+    const int part = static_cast<int>(u - tok * p.parts);
+    const long long b = tok / p.N, i = tok - b * p.N;
+    const int pos = p.positions ? p.positions[tok] : static_cast<int>(i);
+    float c[8], s[8];
+    lane_angles<D>(p, m, sub, grp, pos, c, s);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      float wa[8], wb[8];
+      if (kNorm && p.x[t].heads > 0) {
+        load_weight8(p, t, m.a, wa);
+        load_weight8(p, t, m.b, wb);
+      }
+      for (int h0 = part * R; h0 < p.x[t].heads; h0 += p.parts * R) {
+        const int h = h0 + grp;
+        const bool on = h < p.x[t].heads;
+        Row16 x = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, g = x;
+        if (on) {
+          const __nv_bfloat16* r = row_at(p.x[t], b, i, h);
+          x.a = *reinterpret_cast<const uint4*>(r + m.a);
+          x.b = *reinterpret_cast<const uint4*>(r + m.b);
+          if (kBack) {
+            const __nv_bfloat16* q = row_at(p.g[t], b, i, h);
+            g.a = *reinterpret_cast<const uint4*>(q + m.a);
+            g.b = *reinterpret_cast<const uint4*>(q + m.b);
+          }
+        }
+        float xa[8], xb[8];
+        unpack8(x.a, xa);
+        unpack8(x.b, xb);
+        if (kNorm) {
+          float ss = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
+          const float r = 1.0f / sqrtf(row_sum<L>(ss) * (1.0f / D) + p.eps);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            xa[j] *= r;
+            xb[j] *= r;
+          }
+          if (kBack) {
+            float ga[8], gb[8];
+            unpack8(g.a, ga);
+            unpack8(g.b, gb);
+            turn(m, ga, gb, c, s, kSign);
+            float dot = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (on) {
+                dw[kBack ? t : 0][j] = fmaf(ga[j], xa[j], dw[kBack ? t : 0][j]);
+                dw[kBack ? t : 0][8 + j] = fmaf(gb[j], xb[j], dw[kBack ? t : 0][8 + j]);
+              }
+              ga[j] *= wa[j];
+              gb[j] *= wb[j];
+              dot = fmaf(ga[j], xa[j], fmaf(gb[j], xb[j], dot));
+            }
+            const float mean = row_sum<L>(dot) * (1.0f / D);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              xa[j] = r * (ga[j] - xa[j] * mean);
+              xb[j] = r * (gb[j] - xb[j] * mean);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              xa[j] *= wa[j];
+              xb[j] *= wb[j];
+            }
+          }
+        }
+        if (!kBack) turn(m, xa, xb, c, s, kSign);
+        if (on) {
+          __nv_bfloat16* y = const_cast<__nv_bfloat16*>(row_at(p.y[t], b, i, h));
+          *reinterpret_cast<uint4*>(y + m.a) = pack8(xa);
+          *reinterpret_cast<uint4*>(y + m.b) = pack8(xb);
+        }
+      }
+    }
+  }
+  if (kBack) {
+    // the block's sums of each weight's gradient: over the row groups of a warp, then over
+    // the warps in order
+    __shared__ float part_s[kWarps][2][D];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float v = dw[kBack ? t : 0][j];
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (grp == 0) part_s[warp][t][j < 8 ? m.a + j : m.b + j - 8] = v;
+      }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * D; e += kRotaryThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += part_s[w][e / D][e % D];
+      p.partial[static_cast<size_t>(blockIdx.x) * 2 * D + e] = v;
+    }
+  }
+}
+
+// dw[t][c] = sum over blocks of partial[block][t][c], in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(256) fa_norm_weight_kernel(const float* __restrict__ partial,
+                                                             int blocks, float* dwq, float* dwk) {
+  // eight columns a block, 32 slices of the blocks each
+  const int col = blockIdx.x * 8 + (threadIdx.x & 7), slice = threadIdx.x >> 3;
+  float v = 0.0f;
+  for (int b = slice; b < blocks; b += 32) v += partial[static_cast<size_t>(b) * 2 * D + col];
+  __shared__ float s[32][8];
+  s[slice][threadIdx.x & 7] = v;
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) sum += s[k][threadIdx.x];
+    float* out = col < D ? dwq : dwk;
+    if (out) out[col < D ? col : col - D] = sum;
+  }
+}
+
+// Parts a token's heads are split into: one where the tokens fill the GPU's warps, as many
+// steps as there are otherwise.
+int rotary_parts(const RotaryArgs& a, int rows) {
+  const int most = max((a.x[0].heads + rows - 1) / rows, (a.x[1].heads + rows - 1) / rows);
+  const long long warps = static_cast<long long>(a.num_sms) * 32;
+  long long parts = (warps + a.tokens - 1) / a.tokens;
+  if (parts > most) parts = most;
+  return static_cast<int>(parts < 1 ? 1 : parts);
+}
+
+template <int D, int MODE>
+cudaError_t launch_t(RotaryArgs a, cudaStream_t s) {
+  a.parts = rotary_parts(a, 32 * 16 / D);
+  const long long blocks = (a.tokens * a.parts + kWarps - 1) / kWarps;
+  const long long most = MODE == 3 ? min(4ll * a.num_sms, static_cast<long long>(kNormMaxBlocks)) : 0x7fffffffll;
+  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  fa_rotary_kernel<D, MODE><<<grid, kRotaryThreads, 0, s>>>(a);
+  if (MODE == 3) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    fa_norm_weight_kernel<D><<<2 * D / 8, 256, 0, s>>>(a.partial, static_cast<int>(grid), a.dw[0], a.dw[1]);
+  }
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const RotaryArgs& a, int mode, cudaStream_t s) {
+  switch (mode) {
+    case 0: return launch_t<D, 0>(a, s);
+    case 1: return launch_t<D, 1>(a, s);
+    case 2: return launch_t<D, 2>(a, s);
+    default: return launch_t<D, 3>(a, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryArgs& a, int mode, int d, cudaStream_t s) {
+  return d == 64 ? launch_d<64>(a, mode, s) : launch_d<128>(a, mode, s);
+}
+
+}  // namespace fa

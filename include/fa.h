@@ -370,6 +370,162 @@ int fa_cache_commit(const fa_cache* cache, const int* lens, const int* path,
                     const int* n_accept, int* new_lens, int T, void* stream);
 
 /*
+ * Rows of several heads, one row of d bf16 for each token and head: element
+ * (b, t, h, c) of a tensor lies at p[b * batch_stride + t * token_stride +
+ * h * head_stride + c].  Strides are in elements and multiples of 8, p is
+ * 16-byte aligned.  So [tokens][heads][d], a part of the heads of a projection's
+ * output and [B][H][N][d] are all read and written as they lie.  A stride is not
+ * looked at where its axis has one entry; rows must not overlap: the tokens of
+ * a head lie within its head_stride, or the heads of a token within its
+ * token_stride (FA_ERR_SHAPE otherwise).  The calls on packed sequences have no
+ * batch axis: their tokens count through all sequences.
+ * The struct is read during the call only.
+ */
+typedef struct fa_heads {
+  void* p;
+  long long batch_stride, token_stride, head_stride;
+  int heads;
+} fa_heads;
+
+/*
+ * Attention over packed sequences: B sequences of different lengths lie one
+ * behind the other, with grouped heads.
+ *  - cu_q: DEVICE int32 [B + 1], ascending: the queries of sequence b are the
+ *    tokens cu_q[b] .. cu_q[b + 1] - 1 of q and o.  cu_k: the same for its keys,
+ *    tokens of k and v; NULL: cu_q (then total_k = total_q).  Sequences may be
+ *    empty.  Entries count as 0 below 0 and as the total above it; where they
+ *    descend, what the sequences concerned get is unspecified, but nothing
+ *    outside the tensors is read or written.
+ *  - With n queries and m keys, query i of a sequence sees its keys j < m, and with
+ *    causal != 0 of those j <= i + m - n: the last query sees all keys (a prompt with
+ *    m = n, a chunk of one over the keys before it with m > n).  A query that
+ *    sees no key has o = 0 and lse = -inf.
+ *  - q, o: Hq = q->heads heads, total_q tokens; k, v: Hkv heads, total_k
+ *    tokens; Hq a multiple of Hkv, query head h reads key head h / (Hq / Hkv).
+ *    o->heads = Hq, v->heads = Hkv.  lse: fp32 [Hq][total_q].
+ *  - What one sequence holds, NaN and infinities included, reaches no other.
+ *    Tokens of o and lse in no sequence (before cu_q[0], from cu_q[B] on) are
+ *    left as they were.  Within a sequence a NaN or infinity in a value row may
+ *    make queries NaN that do not see the row.
+ *  - B >= 1, 0 <= total_q, total_k; d in {64, 128}; Hq * (total_q / 8 + B) and
+ *    Hkv * (total_k / 128 + B) below 2^31, B below 2^20.  scale > 0 and finite.
+ *  - workspace: device memory, 256-byte aligned, contents irrelevant, of
+ *    fa_forward_packed_workspace_size() bytes (0 for an invalid shape).
+ *    Calls that may overlap on the GPU need workspaces of their own.
+ *  - Accuracy as fa_forward: probabilities are rounded to bf16 before the product
+ *    with V; all sums are fp32.
+ */
+size_t fa_forward_packed_workspace_size(int B, int total_q, int total_k, int Hq, int Hkv, int d);
+int fa_forward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, const fa_heads* o,
+                      float* lse, const int* cu_q, const int* cu_k, int B, int total_q,
+                      int total_k, int d, float scale, int causal, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Backward pass of fa_forward_packed: dq (as q), dk and dv (as k and v, the sums
+ * over the query heads of a group) from dO (as o), o and lse of the forward pass.
+ * dP = dO V^T, D_i = sum_c dO_ic o_ic, dS = P o (dP - D), dq = scale dS K, dk = scale
+ * dS^T Q, dv = P^T dO.  A query that sees no key has dq = 0 and adds nothing;
+ * keys that no query sees have dk = dv = 0; tokens in no sequence are left as they
+ * were.  Results do not depend on the order in which the GPU runs the work.
+ * Unlike fa_backward, D is the fp32 sum over the bf16 o alone: it is off by up to
+ * half a bf16 step of o, times dO.  Arguments and errors otherwise as for
+ * fa_forward_packed; workspace: fa_backward_packed_workspace_size() bytes.
+ */
+size_t fa_backward_packed_workspace_size(int B, int total_q, int total_k, int Hq, int Hkv, int d);
+int fa_backward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, const fa_heads* o,
+                       const fa_heads* dO, const float* lse, const fa_heads* dq,
+                       const fa_heads* dk, const fa_heads* dv, const int* cu_q, const int* cu_k,
+                       int B, int total_q, int total_k, int d, float scale, int causal,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotation of queries and keys by their positions: the first `rot` elements of
+ * each row are rot / 2 pairs, and pair i of a token at position p turns by the angle
+ * p * f_i:  (x, y) -> amplitude * (x cos - y sin, y cos + x sin).  The other
+ * elements pass unchanged.  Pairs are (i, i + rot / 2), or (2i, 2i + 1) where
+ * interleaved != 0.
+ *  - turns: DEVICE [rot / 2], f_i in turns a position as a 64-bit binary fraction
+ *    (2^64 is a whole turn), from fa_rotary_table.  The angle's whole turns
+ *    drop out of the integer product p * turns[i], so that it is as exact at
+ *    position 2^31 - 1 as at 1.
+ *  - 16 <= rot <= d, a multiple of 16.  amplitude finite.
+ */
+typedef struct fa_rotation {
+  const unsigned long long* turns;
+  int rot;
+  int interleaved;
+  float amplitude;
+} fa_rotation;
+
+/*
+ * Fills turns (HOST [rot / 2]) from f_i = base^(-2i / rot) radians a position,
+ * scaled for contexts longer than those a model was trained on:
+ *  - FA_SCALE_NONE: as it is;
+ *  - FA_SCALE_LINEAR: f_i / factor;
+ *  - FA_SCALE_BASE: with base * factor^(rot / (rot - 2)), which leaves f_0 and
+ *    divides the last by factor;
+ *  - FA_SCALE_TURNS: g f_i + (1 - g) f_i / factor, where g = (t_i - low) / (high -
+ *    low), kept within 0 .. 1, and t_i = original f_i / 2 pi are the pair's turns
+ *    within the original context;
+ *  - FA_SCALE_INDEX: the same with g falling linearly in i, from 1 at the pair that
+ *    turns `high` times within the original context (rounded down, at least 0)
+ *    to 0 at the one that turns `low` times (rounded up, at most rot - 1).
+ * base > 1, factor >= 1 (where it is used), original >= 1, 0 < low < high, all
+ * finite; FA_ERR_SHAPE otherwise.  Computed in 64 bits; needs no GPU.
+ */
+typedef enum {
+  FA_SCALE_NONE = 0,
+  FA_SCALE_LINEAR = 1,
+  FA_SCALE_BASE = 2,
+  FA_SCALE_TURNS = 3,
+  FA_SCALE_INDEX = 4
+} fa_scaling;
+int fa_rotary_table(unsigned long long* turns, int rot, double base, int scaling, double factor,
+                    double original, double low, double high);
+
+/*
+ * Rotates q into q_out and k into k_out (k NULL: q alone); fa_rotary_backward
+ * rotates their gradients back (the transposed rotation: angles negated, the same
+ * amplitude).  positions: DEVICE int32 [B][N], any values; NULL: token i of each
+ * of the B sequences is at position i.  An output may be its input (the same
+ * pointer and strides); other overlaps are undefined.  bf16 in and out, fp32
+ * between, rounded once.  B, N >= 1 (packed tokens: B = 1), B * N and B * N * heads
+ * below 2^31, d in {64, 128}.
+ */
+int fa_rotary(const fa_rotation* r, const fa_heads* q, const fa_heads* k, const fa_heads* q_out,
+              const fa_heads* k_out, const int* positions, int B, int N, int d, void* stream);
+int fa_rotary_backward(const fa_rotation* r, const fa_heads* dq, const fa_heads* dk,
+                       const fa_heads* dq_in, const fa_heads* dk_in, const int* positions, int B,
+                       int N, int d, void* stream);
+
+/*
+ * A norm of each head before the rotation, in one pass: y = R(w o x * s) with
+ * s = (mean_c x_c^2 + eps)^(-1/2) for each row x.  q_weight, k_weight: DEVICE [d],
+ * fp32 (weight_bf16 = 0) or bf16, 16-byte aligned.  eps >= 0 and finite (with
+ * eps = 0 a row of zeros gives NaN).  Otherwise as fa_rotary.
+ *
+ * The backward pass takes the gradients dq, dk of the results and the inputs q, k
+ * again: g = R^T dy, dw = sum over rows of g o x s, dx = s (w o g - x s mean(w o g o x s)).
+ * dq_in, dk_in may be dq and dk.  dq_weight, dk_weight: fp32 [d], 16-byte aligned,
+ * overwritten; sums in fp32, in an order that depends on the shapes and the GPU's
+ * number of SMs alone.  workspace: device memory, 256-byte aligned, contents irrelevant,
+ * FA_NORM_WORKSPACE bytes; calls that may overlap need workspaces of their own.
+ * Where k is NULL, so are k_weight, dk, dk_in and dk_weight.
+ */
+#define FA_NORM_WORKSPACE 1048576
+int fa_norm_rotary(const fa_rotation* r, const fa_heads* q, const fa_heads* k,
+                   const fa_heads* q_out, const fa_heads* k_out, const int* positions,
+                   const void* q_weight, const void* k_weight, int weight_bf16, float eps, int B,
+                   int N, int d, void* stream);
+int fa_norm_rotary_backward(const fa_rotation* r, const fa_heads* dq, const fa_heads* dk,
+                            const fa_heads* q, const fa_heads* k, const fa_heads* dq_in,
+                            const fa_heads* dk_in, float* dq_weight, float* dk_weight,
+                            const int* positions, const void* q_weight, const void* k_weight,
+                            int weight_bf16, float eps, int B, int N, int d, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
  * Host-buffer runtime: training steps (fa_forward + fa_backward) whose
  * inputs and outputs live in HOST memory.  The paper has no counterpart
  * (its kernels start from tensors in HBM); this is the call a host program
