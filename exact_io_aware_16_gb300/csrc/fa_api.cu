@@ -12,6 +12,7 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
+#include "fa_packed.cuh"
 
 namespace {
 
@@ -650,8 +651,8 @@ static int view_heads(const fa_heads* t, int heads, long long B, long long T, in
   v->batch = B > 1 ? t->batch_stride : 0;
   if (heads > 1 && v->head < d) return FA_ERR_SHAPE;
   if (T > 1 && v->token < d) return FA_ERR_SHAPE;
-  // 2^31 tokens and heads of at most 2^40 bytes between rows stay within 64 bits
-  const long long most = 1ll << 38;
+  // 16 heads of at most 2^35 bytes between rows are a stride that a tensor map takes
+  const long long most = 1ll << 34;
   if (v->head > most || v->token > most || v->batch < 0 || v->batch > most) return FA_ERR_SHAPE;
   const bool heads_inside = v->token >= (heads - 1) * v->head + d;
   const bool tokens_inside = T < 1 || v->head >= (T - 1) * v->token + d;
@@ -659,6 +660,44 @@ static int view_heads(const fa_heads* t, int heads, long long B, long long T, in
   if (B > 1 && v->batch < d) return FA_ERR_SHAPE;
   if (!aligned16(t->p) || (v->head & 7) || (v->token & 7) || (v->batch & 7)) return FA_ERR_ALIGN;
   return FA_OK;
+}
+
+// Key or value rows as (d, tokens, heads), boxes of 64 columns x 128 tokens; query rows
+// as (d, P, tokens, head groups of P), boxes of 64 columns x P heads x TT tokens.  128-byte
+// swizzle.  A tensor of no tokens gets a map that is never read through.
+static int encode_rows(CUtensorMap* map, const fa::HeadsView& t, int tokens, int d, int P, int TT,
+                       const void* otherwise) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return FA_ERR_CUDA;
+  const cuuint64_t n = static_cast<cuuint64_t>(tokens > 0 ? tokens : 1);
+  const cuuint64_t token = static_cast<cuuint64_t>(t.token) * 2, head = static_cast<cuuint64_t>(t.head) * 2;
+  const bool q = P > 0;
+  cuuint64_t kdims[3] = {static_cast<cuuint64_t>(d), n, static_cast<cuuint64_t>(t.heads)};
+  cuuint64_t kstrides[2] = {token, head};
+  cuuint32_t kbox[3] = {fa::kBoxCols, 128, 1};
+  cuuint64_t qdims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(P), n,
+                         static_cast<cuuint64_t>(q ? t.heads / P : 1)};
+  cuuint64_t qstrides[3] = {head, token, head * static_cast<cuuint64_t>(P)};
+  cuuint32_t qbox[4] = {fa::kBoxCols, static_cast<cuuint32_t>(P), static_cast<cuuint32_t>(TT), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  void* base = const_cast<void*>(tokens > 0 ? t.p : otherwise);
+  const CUresult r =
+      enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q ? 4 : 3, base, q ? qdims : kdims,
+          q ? qstrides : kstrides, q ? qbox : kbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// The maps of q, k, v and, for the backward pass, dO.
+static int packed_maps(const fa::PackedArgs& a, bool backward, CUtensorMap maps[4]) {
+  const fa::PackedTiling t = fa::packed_tiling(a.q.heads, a.k.heads);
+  const void* any = a.workspace;
+  int st = encode_rows(&maps[0], a.q, a.total_q, a.d, t.P, t.TT, any);
+  if (st == FA_OK) st = encode_rows(&maps[1], a.k, a.total_k, a.d, 0, 0, any);
+  if (st == FA_OK) st = encode_rows(&maps[2], a.v, a.total_k, a.d, 0, 0, any);
+  if (st == FA_OK && backward) st = encode_rows(&maps[3], a.dO, a.total_q, a.d, t.P, t.TT, any);
+  return st;
 }
 
 static int check_packed(int B, int total_q, int total_k, int Hq, int Hkv, int d) {
@@ -672,12 +711,12 @@ static int check_packed(int B, int total_q, int total_k, int Hq, int Hkv, int d)
 
 size_t fa_forward_packed_workspace_size(int B, int total_q, int total_k, int Hq, int Hkv, int d) {
   if (check_packed(B, total_q, total_k, Hq, Hkv, d) != FA_OK) return 0;
-  return fa::packed_workspace_bytes(B, total_q, total_k, Hq, Hkv, false);
+  return fa::packed_layout(B, total_q, total_k, Hq, Hkv, false).bytes;
 }
 
 size_t fa_backward_packed_workspace_size(int B, int total_q, int total_k, int Hq, int Hkv, int d) {
   if (check_packed(B, total_q, total_k, Hq, Hkv, d) != FA_OK) return 0;
-  return fa::packed_workspace_bytes(B, total_q, total_k, Hq, Hkv, true);
+  return fa::packed_layout(B, total_q, total_k, Hq, Hkv, true).bytes;
 }
 
 // What both passes check; the views of q, k, v and o.
@@ -697,7 +736,7 @@ static int packed_args(const fa_heads* q, const fa_heads* k, const fa_heads* v, 
     return st;
   if (!aligned4(lse) || !aligned4(cu_q) || !aligned4(cu_k)) return FA_ERR_ALIGN;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < fa::packed_workspace_bytes(B, total_q, total_k, q->heads, k->heads, backward))
+      workspace_bytes < fa::packed_layout(B, total_q, total_k, q->heads, k->heads, backward).bytes)
     return FA_ERR_WORKSPACE;
   a->cu_q = cu_q;
   a->cu_k = cu_k ? cu_k : cu_q;
@@ -723,7 +762,9 @@ int fa_forward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, c
   a.lse = lse;
   a.num_sms = num_sms();
   if (total_q == 0) return FA_OK;
-  return fa::launch_forward_packed(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  CUtensorMap maps[4];
+  if ((st = packed_maps(a, false, maps)) != FA_OK) return st;
+  return fa::launch_forward_packed(a, maps, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
@@ -747,7 +788,9 @@ int fa_backward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, 
   a.lse = const_cast<float*>(lse);
   a.num_sms = num_sms();
   if (total_q == 0 && total_k == 0) return FA_OK;
-  return fa::launch_backward_packed(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  CUtensorMap maps[4];
+  if ((st = packed_maps(a, true, maps)) != FA_OK) return st;
+  return fa::launch_backward_packed(a, maps, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
@@ -901,16 +944,17 @@ int fa_selftest_wait_timeout(void* stream) {
 
 int fa_get_device_error(void* stream, uint32_t* detail) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t w_fwd = 0, w_bwd = 0, w_dtc = 0, w_tree = 0, w_st = 0;
+  uint32_t w_fwd = 0, w_bwd = 0, w_dtc = 0, w_tree = 0, w_packed = 0, w_st = 0;
   if (fa::fwd_read_clear_error(&w_fwd, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::bwd_read_clear_error(&w_bwd, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::dtc_read_clear_error(&w_dtc, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::tree_read_clear_error(&w_tree, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (fa::packed_read_clear_error(&w_packed, s) != cudaSuccess) return FA_ERR_CUDA;
   if (fa::st_read_clear_error(&w_st, s) != cudaSuccess) return FA_ERR_CUDA;
   // a launch that gave up may have left its work-item counters dirty
   if (w_fwd && fa::fwd_reset_sched(s) != cudaSuccess) return FA_ERR_CUDA;
   if (w_bwd && fa::bwd_reset_sched(s) != cudaSuccess) return FA_ERR_CUDA;
-  const uint32_t w = w_fwd ? w_fwd : (w_bwd ? w_bwd : (w_dtc ? w_dtc : (w_tree ? w_tree : w_st)));
+  const uint32_t w = w_fwd ? w_fwd : (w_bwd ? w_bwd : (w_dtc ? w_dtc : (w_tree ? w_tree : (w_packed ? w_packed : w_st))));
   if (detail) *detail = w;
   return w ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }

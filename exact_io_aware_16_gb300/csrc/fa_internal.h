@@ -207,16 +207,12 @@ inline int packed_heads(int G) {
   return p;
 }
 
-// Workspace of a packed call.  TODO
-inline size_t packed_workspace_bytes(int B, int total_q, int total_k, int Hq, int Hkv, bool backward) {
-  return 256;
-}
-
 cudaError_t launch_forward(const FwdArgs& a, cudaStream_t s);
 // mode 0: rotation, 1: rotation backwards, 2: norm and rotation, 3: its backward pass
 cudaError_t launch_rotary(const RotaryArgs& a, int mode, int d, cudaStream_t s);
-cudaError_t launch_forward_packed(const PackedArgs& a, cudaStream_t s);
-cudaError_t launch_backward_packed(const PackedArgs& a, cudaStream_t s);
+// maps: q, k, v (and dO) as whole tensors; the plan makes each sequence's from them
+cudaError_t launch_forward_packed(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s);
+cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s);
 cudaError_t launch_cache_write(const CacheMoveArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheMoveArgs& a, cudaStream_t s);
 cudaError_t launch_cache_commit(const CacheMoveArgs& a, cudaStream_t s);
@@ -242,6 +238,7 @@ cudaError_t bwd_reset_sched(cudaStream_t s);
 cudaError_t bwd_read_clear_error(uint32_t* out, cudaStream_t s);
 cudaError_t dtc_read_clear_error(uint32_t* out, cudaStream_t s);
 cudaError_t tree_read_clear_error(uint32_t* out, cudaStream_t s);
+cudaError_t packed_read_clear_error(uint32_t* out, cudaStream_t s);
 
 // Self-test of failure reporting: one CTA whose barrier wait runs out (its
 // code, kSelftestWaitCode, lands in the self-test error word).

@@ -1,0 +1,162 @@
+// fa_packed.cuh — what the forward and backward kernels over packed sequences share:
+// how rows fill tiles, the plan that a first small kernel leaves in the workspace, and how
+// the persistent CTAs take their work from it.
+//
+// Tiles.  A key head serves G query heads, whose rows need the same keys.  A query tile
+// of 128 rows therefore holds P heads of 128 / P tokens (P = packed_heads(G): all of the
+// group where it has up to 16): row r is token r / P, head r % P.  Keys and values are
+// then read once for all of them, and a sequence of few tokens fills a tile with its
+// heads.  Rows that P does not fill (126 of 128 for P = 7) are zero in shared memory.
+//
+// Tensor maps.  Every sequence has its own, whose extent ends where the sequence does:
+// what lies behind reads as zeros, so that neither NaN nor infinities of a
+// neighbour meet a probability of zero in a product.  The plan kernel copies the map of
+// the whole tensor and puts the sequence's address and length in (tensormap.replace).
+//
+// Work.  The lengths are on the device, so the plan kernel also lists all tiles, longest
+// first (a counting sort by key tiles), and persistent CTAs take (tile, head) items off that
+// list: longest-job-first over the whole batch, with the heads of a tile, which share
+// keys, next to each other.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+// One tile of one sequence.
+struct PackedEntry {
+  int seq, tile;
+  int q0, n;  // first query token of the sequence, queries
+  int k0, m;  // first key token, keys
+  int pad[2];
+};
+static_assert(sizeof(PackedEntry) == 32, "two 16-byte loads");
+
+struct PackedHeader {
+  unsigned next[2];  // items taken of each list
+  unsigned count[2];  // entries of each list
+};
+
+// How a call's heads and tokens fill tiles.
+struct PackedTiling {
+  int P;      // query heads a tile
+  int TT;     // query tokens a tile
+  int heads;  // head groups of P query heads
+  int per_kv;  // of them, those of one key head
+};
+
+inline PackedTiling packed_tiling(int Hq, int Hkv) {
+  PackedTiling t;
+  const int G = Hq / Hkv;
+  t.P = packed_heads(G);
+  t.TT = 128 / t.P;
+  t.heads = Hq / t.P;
+  t.per_kv = G / t.P;
+  return t;
+}
+
+// The workspace: header, four tensor maps a sequence (the forward pass uses three), two
+// lists, and the backward pass's D.
+struct PackedLayout {
+  size_t maps, list[2], D, bytes;
+};
+
+inline PackedLayout packed_layout(int B, int total_q, int total_k, int Hq, int Hkv, bool backward) {
+  const PackedTiling t = packed_tiling(Hq, Hkv);
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  PackedLayout l;
+  l.maps = 256;
+  const size_t b = static_cast<size_t>(B);
+  l.list[0] = l.maps + up(b * (backward ? 4 : 3) * 128);
+  // a forward item is two query tiles, a backward one one
+  const size_t q_tiles = static_cast<size_t>(total_q) / (backward ? t.TT : 2 * t.TT) + b;
+  l.list[1] = l.list[0] + up(q_tiles * sizeof(PackedEntry));
+  const size_t k_tiles = backward ? static_cast<size_t>(total_k) / 128 + b : 0;
+  l.D = l.list[1] + up(k_tiles * sizeof(PackedEntry));
+  l.bytes = l.D + (backward ? up(static_cast<size_t>(Hq) * total_q * sizeof(float)) : 0);
+  return l;
+}
+
+struct PackedPlanArgs {
+  CUtensorMap map[4];  // q, k, v, dO of the whole tensors
+  const __nv_bfloat16* base[4];
+  long long token[4];  // elements between tokens
+  int nmaps;
+  const int* cu_q;
+  const int* cu_k;
+  int B, total_q, total_k;
+  int causal;
+  int q_span;   // query tokens an entry of list 0
+  int TT;       // query tokens a tile (costs of list 1)
+  int nlists;
+  unsigned most[2];  // entries the lists have room for
+  int shift[2];      // cost to bucket
+  PackedHeader* header;
+  CUtensorMap* maps;
+  PackedEntry* list[2];
+};
+
+cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward,
+                               cudaStream_t s);
+
+// ---------------------------------------------------------------- device side
+// Keys that query token `tok` of a sequence sees.
+__device__ __forceinline__ int packed_keys(int tok, int n, int m, bool causal) {
+  return causal ? min(max(tok + 1 + m - n, 0), m) : m;
+}
+
+// Waits for the launch before this one (the plan), whose writes are then visible.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The tensor map at `map` was written by generic stores of an earlier kernel.
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                   reinterpret_cast<uint64_t>(map))
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// An item as the roles of a CTA see it: a list entry and one of its heads.
+struct PackedItem {
+  PackedEntry e;
+  int head;  // of PackedTiling::heads, or (dK/dV) key head; -1: no more items
+};
+
+constexpr int kPackedRing = 4;  // items in flight between the roles of a CTA
+
+// The next item of a list (one thread).
+__device__ __forceinline__ PackedItem packed_claim(PackedHeader* h, const PackedEntry* list, int which,
+                                                   int heads) {
+  PackedItem it;
+  const unsigned c = atomicAdd(&h->next[which], 1u);
+  const unsigned entry = c / static_cast<unsigned>(heads);
+  if (entry >= h->count[which]) {
+    it.head = -1;
+    return it;
+  }
+  it.head = static_cast<int>(c - entry * heads);
+  const int4* p = reinterpret_cast<const int4*>(list + entry);
+  const int4 x = p[0], y = p[1];
+  it.e = {x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
+  return it;
+}
+
+}  // namespace fa
