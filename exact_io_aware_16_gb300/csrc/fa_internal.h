@@ -239,6 +239,7 @@ cudaError_t bwd_read_clear_error(uint32_t* out, cudaStream_t s);
 cudaError_t dtc_read_clear_error(uint32_t* out, cudaStream_t s);
 cudaError_t tree_read_clear_error(uint32_t* out, cudaStream_t s);
 cudaError_t packed_read_clear_error(uint32_t* out, cudaStream_t s);
+cudaError_t packed_bwd_read_clear_error(uint32_t* out, cudaStream_t s);
 
 // Self-test of failure reporting: one CTA whose barrier wait runs out (its
 // code, kSelftestWaitCode, lands in the self-test error word).

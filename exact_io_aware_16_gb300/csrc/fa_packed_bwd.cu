@@ -1,150 +1,941 @@
-// fa_packed_bwd.cu — backward pass of attention over packed sequences: the plain kernels, one
-// warp a row.
+// fa_packed_bwd.cu — backward pass of attention over packed sequences with grouped heads.
+//
+//   P = exp(scale Q K^T - lse),  D_i = sum_c dO_ic o_ic,  dP = dO V^T,  dS = P o (dP - D),
+//   dQ = scale dS K,  dK = scale sum_heads dS^T Q,  dV = sum_heads P^T dO.
+//
+// Two kernels over the tiles of fa_packed.cuh, each bound by the tensor core:
+//   * dq: a query tile's Q and dO stay in shared memory while keys and values stream;
+//     three products a tile (S, dP, dQ).  It also finds D, for itself and for the next.
+//   * dk, dv: a key tile's K and V stay while the query tiles of all heads of the group
+//     stream, so that the sums over a group's heads are sums in tensor memory, in a
+//     fixed order and without atomics; four products a tile (S^T, dP^T, dV, dK).
+//     Scores are computed transposed: a thread owns a key.
+// Together seven products where five would do: S and dP are computed twice, which costs
+// less than adding dQ up over key tiles in memory (64 KB a tile pair), and leaves
+// no order to chance.
+//
+// D from the bf16 o is off by up to half a bf16 step of it.  Where a query sees many keys
+// that is below the rounding of dS; where it sees few, dS may be small against D
+// (a query's own key alone: zero).  Query tiles that see one key tile therefore take
+// D = sum_j P_ij dP_ij, which their threads have in registers before dS is needed.
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "fa_internal.h"
+#include "fa_packed.cuh"
+#include "sm103_ptx.cuh"
 
 namespace fa {
 namespace {
 
-__device__ __forceinline__ const __nv_bfloat16* row_of(const HeadsView& t, long long i, int h) {
-  return static_cast<const __nv_bfloat16*>(t.p) + i * t.token + h * t.head;
-}
+__device__ unsigned int g_packed_bwd_error;
 
-// The sequence that token i belongs to (-1: none).
-__device__ __forceinline__ int sequence_of(const int* cu, int B, int i) {
-  if (i < cu[0] || i >= cu[B]) return -1;
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (cu[mid] <= i) lo = mid; else hi = mid;
-  }
-  return lo;
-}
+constexpr int kThreads = 320;  // two compute warpgroups, TMA warp, MMA warp
+constexpr int kCompute = 256;
+constexpr int kTmaWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr float kLog2e = 1.44269504088896340736f;
 
-template <int E>
-__device__ __forceinline__ void load(const __nv_bfloat16* r, int lane, float (&x)[E]) {
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = __bfloat162float(r[lane + 32 * e]);
-}
-
-template <int E>
-__device__ __forceinline__ float dot(const float (&a)[E], const float (&b)[E]) {
-  float s = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) s = fmaf(a[e], b[e], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-struct Span {
-  int q0, n, k0, m;
+struct BwdParams {
+  PackedHeader* header;
+  const PackedEntry* list;
+  const CUtensorMap* maps;  // four a sequence: q, k, v, dO
+  const float* lse;
+  float* D;
+  const __nv_bfloat16* o;
+  const __nv_bfloat16* dO;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  long long o_token, o_head, dO_token, dO_head, dq_token, dq_head, dk_token, dk_head, dv_token, dv_head;
+  int total_q;
+  int P, TT, heads, per_kv, Hkv;
+  float scale, scale_log2;
 };
 
-__device__ __forceinline__ int clamp(int x, int hi) { return min(max(x, 0), hi); }
+// Barriers of both kernels (the dq kernel's rings are apart: a key tile is needed longer than
+// a value tile; the other's q and dO tiles share a ring).
+struct BwdBars {
+  uint64_t res_full, res_empty;
+  uint64_t a_full[4], a_empty[4];  // dq: key tiles; dk, dv: query tiles with their dO
+  uint64_t b_full[4], b_empty[4];  // dq: value tiles
+  uint64_t s_full[2], s_free[2];   // scores computed; read by all threads (dq), P written (dk, dv)
+  uint64_t dp_full, ds_ready, dx_ready;
+  uint64_t acc_done, acc_free;
+  uint64_t item_full[kPackedRing], item_empty[kPackedRing];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  PackedItem item[kPackedRing];
+};
+static_assert(sizeof(BwdBars) <= 768, "barrier block overruns its shared memory");
 
-__device__ __forceinline__ Span span_of(const PackedArgs& a, int b) {
-  Span s;
-  s.q0 = clamp(a.cu_q[b], a.total_q);
-  s.n = max(clamp(a.cu_q[b + 1], a.total_q) - s.q0, 0);
-  const int* ck = a.cu_k ? a.cu_k : a.cu_q;
-  s.k0 = clamp(ck[b], a.total_k);
-  s.m = max(clamp(ck[b + 1], a.total_k) - s.k0, 0);
-  return s;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t par, BwdBars* b, uint32_t code) {
+  return mbar_wait(bar, par, &b->abort_flag, &g_packed_bwd_error, code);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t par, BwdBars* b, uint32_t code) {
+  return __all_sync(0xffffffffu, wait(bar, par, b, code));
 }
 
-__device__ __forceinline__ int keys_of(const PackedArgs& a, const Span& s, int i) {
-  return a.causal ? min(max(i + 1 + s.m - s.n, 0), s.m) : s.m;
+// Adds `bytes` to the transaction count of the current phase of `bar` without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
 }
 
-template <int D>
-__global__ void fa_packed_dq_kernel(const PackedArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-  if (w >= static_cast<long long>(a.total_q) * a.q.heads) return;
-  const int i = static_cast<int>(w / a.q.heads), h = static_cast<int>(w % a.q.heads);
-  const int b = sequence_of(a.cu_q, a.B, i);
-  if (b < 0) return;
-  const Span s = span_of(a, b);
-  const int keys = keys_of(a, s, i - s.q0), kh = h / (a.q.heads / a.k.heads);
-  float q[E], g[E], dq[E], k[E], x[E];
-  load(row_of(a.q, i, h), lane, q);
-  load(row_of(a.dO, i, h), lane, g);
-  load(row_of(a.o, i, h), lane, x);
-  const float Di = dot(g, x), lse = a.lse[static_cast<long long>(h) * a.total_q + i];
-#pragma unroll
-  for (int e = 0; e < E; ++e) dq[e] = 0.0f;
-  for (int j = 0; j < keys; ++j) {
-    load(row_of(a.k, s.k0 + j, kh), lane, k);
-    load(row_of(a.v, s.k0 + j, kh), lane, x);
-    const float p = __expf(dot(q, k) * a.scale - lse), ds = p * (dot(g, x) - Di);
-#pragma unroll
-    for (int e = 0; e < E; ++e) dq[e] = fmaf(ds, k[e], dq[e]);
+// Barriers and tensor memory; rows of [zero, zero + bytes) that no box fills are zeroed.
+// Returns false (for the whole CTA) when an earlier CTA recorded a timeout.
+__device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, uint8_t* zero, uint32_t bytes) {
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->res_full, 1);
+    mbar_init(&bars->res_empty, 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars->a_full[s], 1);
+      mbar_init(&bars->a_empty[s], 1);
+      mbar_init(&bars->b_full[s], 1);
+      mbar_init(&bars->b_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_free[b], kCompute);
+    }
+    mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->ds_ready, kCompute);
+    mbar_init(&bars->dx_ready, kCompute);
+    mbar_init(&bars->acc_done, 1);
+    mbar_init(&bars->acc_free, kCompute);
+    for (int r = 0; r < kPackedRing; ++r) {
+      mbar_init(&bars->item_full[r], 1);
+      mbar_init(&bars->item_empty[r], kCompute + 1);  // compute threads and the MMA thread
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_packed_bwd_error) != 0) ? 1 : 0;
+    fence_mbar_init();
   }
-  __nv_bfloat16* r = const_cast<__nv_bfloat16*>(row_of(a.dq, i, h));
-#pragma unroll
-  for (int e = 0; e < E; ++e) r[lane + 32 * e] = __float2bfloat16(a.scale * dq[e]);
+  if (bytes > 0) {
+    for (uint32_t i = threadIdx.x; i < bytes / 16; i += kThreads)
+      reinterpret_cast<uint4*>(zero)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  if (bars->abort_flag) return false;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  return true;
 }
 
-template <int D>
-__global__ void fa_packed_dkdv_kernel(const PackedArgs a) {
-  constexpr int E = D / 32;
+__device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t tmem) {
+  if (warp == kMmaWarp) wait(&bars->drain, 0, bars, 0x2ff);
+  if (bars->abort_flag) {
+    // let any bulk copy already in flight land before the CTA exits
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) {
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// K-major operand descriptor for k-step kk of a [128 rows][D] swizzled tile.
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t base, int kk) {
+  return sdesc_sw128(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
+}
+// MN-major operand descriptor (rows of the tile are the K dimension) for k-step kk.
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t base, int kk) {
+  return sdesc_sw128(base + kk * 2048, 16384, 1024);
+}
+// Tensor-memory column of k-step kk (16 score columns) of a bf16 operand packed inside the two
+// 64-column halves of a 128-column fp32 region, each in its half's first 32 columns.
+__device__ __forceinline__ uint32_t packed_a_col(int kk) {
+  return static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8);
+}
+
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&r)[64]) {
+  tmem_ld32(addr + 0, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+  tmem_ld32(addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+  tmem_ld_wait();
+  reg_pin(r);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+      "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]),
+      "r"(w[15])
+      : "memory");
+}
+
+// Stores 32 fp32 accumulator columns of this lane's row times `mul` as bf16, at dst + off
+// (off < 0: the row does not exist), the rows of a 4-lane group together.
+__device__ __forceinline__ void store_acc32(uint32_t addr, float mul, __nv_bfloat16* dst, long long off) {
   const int lane = threadIdx.x & 31;
-  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-  if (w >= static_cast<long long>(a.total_k) * a.k.heads) return;
-  const int j = static_cast<int>(w / a.k.heads), kh = static_cast<int>(w % a.k.heads);
-  const int b = sequence_of(a.cu_k ? a.cu_k : a.cu_q, a.B, j);
-  if (b < 0) return;
-  const Span s = span_of(a, b);
-  const int G = a.q.heads / a.k.heads;
-  float k[E], v[E], dk[E], dv[E], q[E], g[E], x[E];
-  load(row_of(a.k, j, kh), lane, k);
-  load(row_of(a.v, j, kh), lane, v);
+  uint32_t r[32], w[16];
+  tmem_ld32(addr, r);
+  tmem_ld_wait();
+  reg_pin(r);
 #pragma unroll
-  for (int e = 0; e < E; ++e) dk[e] = dv[e] = 0.0f;
-  for (int h = kh * G; h < kh * G + G; ++h)
-    for (int i = 0; i < s.n; ++i) {
-      if (j - s.k0 >= keys_of(a, s, i)) continue;
-      load(row_of(a.q, s.q0 + i, h), lane, q);
-      load(row_of(a.dO, s.q0 + i, h), lane, g);
-      load(row_of(a.o, s.q0 + i, h), lane, x);
-      const float lse = a.lse[static_cast<long long>(h) * a.total_q + s.q0 + i];
-      const float p = __expf(dot(q, k) * a.scale - lse), ds = p * (dot(g, v) - dot(g, x));
+  for (int e = 0; e < 16; ++e)
+    w[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * mul, __uint_as_float(r[2 * e + 1]) * mul);
+  transpose_chunks<4>(w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        dv[e] = fmaf(p, g[e], dv[e]);
-        dk[e] = fmaf(ds, q[e], dk[e]);
+  for (int k = 0; k < 4; ++k) {
+    const long long o = __shfl_sync(0xffffffffu, off, (lane & ~3) + k);
+    if (o >= 0)
+      *reinterpret_cast<uint4*>(dst + o + (lane & 3) * 8) =
+          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+}
+
+__device__ __forceinline__ void store_zeros(__nv_bfloat16* dst, int n) {
+  for (int e = 0; e < n / 8; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ============================================================ dQ
+// Tensor memory: two score buffers (step g's in buffer g & 1), dP (dS over it), dQ.  Scores
+// are read into registers and not written back, so step g + 1's product can run while
+// step g is worked on; order of the products: dQ_n, dP_{n+1}, S_{n+2}.  While threads form
+// dS_{n+1} the tensor core has S_{n+2} to do, and P_{n+1} is formed during the other two.
+template <int D>
+struct DqLayout {
+  static constexpr int kChunks = D / 64;
+  static constexpr uint32_t kTile = 128u * D * 2;
+  // a key tile stays from its scores to dQ, two products later than a value tile
+  static constexpr int kK = D == 64 ? 4 : 3, kV = D == 64 ? 4 : 2;
+  static constexpr uint32_t kQ = 0, kDO = kTile, kKs = 2 * kTile, kVs = kKs + kK * kTile;
+  static constexpr uint32_t kDx = kVs + kV * kTile;  // [half][128]
+  static constexpr uint32_t kBar = kDx + 1024;
+  static constexpr uint32_t kUsed = kBar + 768;
+  static constexpr uint32_t kSmem = (kUsed > 118784u ? kUsed : 118784u) + 1024;  // + align slack
+  static constexpr uint32_t kSCol = 0, kDPCol = 256, kAcc = 384;
+};
+static_assert(DqLayout<128>::kSmem <= 232448, "227 KB a CTA");
+
+__device__ __forceinline__ int dq_tiles(const PackedItem& it, int TT, bool causal) {
+  return (packed_keys(min((it.e.tile + 1) * TT, it.e.n) - 1, it.e.n, it.e.m, causal) + 127) >> 7;
+}
+
+template <int D, bool CAUSAL>
+__global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_constant__ BwdParams p) {
+  using L = DqLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!bwd_init(bars, warp, smem, p.P * p.TT < 128 ? 2 * L::kTile : 0)) return;
+  const uint32_t tmem = bars->tmem_base;
+  grid_dependency_wait();
+  grid_dependency_launch();
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT) * 128u * L::kChunks;
+      int kvb = 0, tl = 0;  // key tiles and items with loads so far
+      PackedItem it = packed_claim(p.header, p.list, 0, p.heads);
+      for (int t = 0;; ++t) {
+        const int r = t % kPackedRing;
+        if (!wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, bars, 0x104)) break;
+        bars->item[r] = it;
+        mbar_arrive(&bars->item_full[r]);
+        if (it.head < 0) break;
+        const int n = dq_tiles(it, p.TT, CAUSAL);
+        if (n == 0) {
+          it = packed_claim(p.header, p.list, 0, p.heads);
+          continue;
+        }
+        const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tensormap_acquire(maps + i);
+        const int kh = it.head / p.per_kv;
+        PackedItem next = it;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+          const int ks = (kvb + j) % L::kK, vs = (kvb + j) % L::kV;
+          if (!(ok = wait(&bars->a_empty[ks], (((kvb + j) / L::kK) & 1) ^ 1, bars, 0x101))) break;
+          mbar_arrive_expect_tx(&bars->a_full[ks], L::kTile);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_3d(smem + L::kKs + ks * L::kTile + c * 16384, maps + 1, &bars->a_full[ks], c * 64, j * 128, kh);
+          if (j == 0) {
+            if (tl > 0 && !(ok = wait(&bars->res_empty, (tl - 1) & 1, bars, 0x103))) break;
+            mbar_arrive_expect_tx(&bars->res_full, 2 * q_bytes);
+#pragma unroll
+            for (int c = 0; c < L::kChunks; ++c) {
+              tma_load_4d(smem + L::kQ + c * 16384, maps, &bars->res_full, c * 64, 0, it.e.tile * p.TT, it.head);
+              tma_load_4d(smem + L::kDO + c * 16384, maps + 3, &bars->res_full, c * 64, 0, it.e.tile * p.TT, it.head);
+            }
+          }
+          if (!(ok = wait(&bars->b_empty[vs], (((kvb + j) / L::kV) & 1) ^ 1, bars, 0x102))) break;
+          mbar_arrive_expect_tx(&bars->b_full[vs], L::kTile);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_3d(smem + L::kVs + vs * L::kTile + c * 16384, maps + 2, &bars->b_full[vs], c * 64, j * 128, kh);
+          // the next item is asked for while the last two tiles are under way
+          if (j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads);
+        }
+        if (!ok) break;
+        kvb += n;
+        ++tl;
+        it = next;
       }
     }
-  __nv_bfloat16* rk = const_cast<__nv_bfloat16*>(row_of(a.dk, j, kh));
-  __nv_bfloat16* rv = const_cast<__nv_bfloat16*>(row_of(a.dv, j, kh));
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
+      const uint32_t sQ = smem_u32(smem + L::kQ), sdO = smem_u32(smem + L::kDO);
+      auto sK = [&](int pos) { return smem_u32(smem + L::kKs) + static_cast<uint32_t>(pos % L::kK) * L::kTile; };
+      auto sV = [&](int pos) { return smem_u32(smem + L::kVs) + static_cast<uint32_t>(pos % L::kV) * L::kTile; };
+      // scores of the key tile at ring position pos, once the buffer has been read
+      auto step_s = [&](int pos) {
+        if (!wait(&bars->a_full[pos % L::kK], (pos / L::kK) & 1, bars, 0x211) ||
+            (pos >= 2 && !wait(&bars->s_free[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x212)))
+          return false;
+        tc_fence_after_sync();
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    rk[lane + 32 * e] = __float2bfloat16(a.scale * dk[e]);
-    rv[lane + 32 * e] = __float2bfloat16(dv[e]);
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(tmem + L::kSCol + (pos & 1) * 128u, kmajor_desc(sQ, kk), kmajor_desc(sK(pos), kk), idesc_s,
+                  kk > 0 ? 1u : 0u);
+        umma_commit(&bars->s_full[pos & 1]);
+        return true;
+      };
+      auto step_dp = [&](int pos) {
+        if (!wait(&bars->b_full[pos % L::kV], (pos / L::kV) & 1, bars, 0x213)) return false;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(tmem + L::kDPCol, kmajor_desc(sdO, kk), kmajor_desc(sV(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(&bars->dp_full);
+        umma_commit(&bars->b_empty[pos % L::kV]);
+        return true;
+      };
+      int kvb = 0, tl = 0;
+      for (int t = 0;; ++t) {
+        const int r = t % kPackedRing;
+        if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x21b)) break;
+        const PackedItem it = bars->item[r];
+        mbar_arrive(&bars->item_empty[r]);
+        if (it.head < 0) break;
+        const int n = dq_tiles(it, p.TT, CAUSAL);
+        if (n == 0) continue;
+        bool ok = wait(&bars->res_full, tl & 1, bars, 0x210) && step_s(kvb) && step_dp(kvb) &&
+                  (n < 2 || step_s(kvb + 1));
+        if (!ok) break;
+        if (n == 1) umma_commit(&bars->res_empty);
+        for (int j = 0; j < n; ++j) {
+          const int pos = kvb + j;
+          // dQ += dS K_j (A = dS bf16 in tensor memory over dP); an item's first overwrites the
+          // accumulator that the epilogue before it reads
+          if (!(ok = wait(&bars->ds_ready, pos & 1, bars, 0x214) &&
+                     (j > 0 || tl == 0 || wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216))))
+            break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + L::kAcc, tmem + L::kDPCol + packed_a_col(kk), mnmajor_desc(sK(pos), kk), idesc_acc,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->a_empty[pos % L::kK]);
+          if (j + 1 < n && !(ok = step_dp(pos + 1))) break;
+          if (j + 2 < n && !(ok = step_s(pos + 2))) break;
+          if (j + 2 == n) umma_commit(&bars->res_empty);  // no product of Q or dO is left
+        }
+        if (!ok) break;
+        umma_commit(&bars->acc_done);
+        kvb += n;
+        ++tl;
+      }
+      umma_commit(&bars->drain);
+    }
+    __syncwarp();
+  } else {
+    const int g = threadIdx.x >> 7;    // half of the score columns
+    const int tr = threadIdx.x & 127;  // row within the tile, TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t col0 = 64u * g;
+    const int row_tok = tr / p.P, row_head = tr - row_tok * p.P;
+    // (an item's parts have been read by all threads before any gets to the next: its last dS,
+    // without which its dQ is not done, comes after)
+    float* dx = reinterpret_cast<float*>(smem + L::kDx);
+    int nb = 0, tl = 0;  // steps and items with products so far
+    for (int ti = 0;; ++ti) {
+      const int r = ti % kPackedRing;
+      if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, bars, 0x304)) break;
+      const PackedItem it = bars->item[r];
+      mbar_arrive(&bars->item_empty[r]);
+      if (it.head < 0) break;
+      const int n = dq_tiles(it, p.TT, CAUSAL);
+      const int tok0 = it.e.tile * p.TT, tok = tok0 + row_tok;
+      const bool valid = row_tok < p.TT && tok < it.e.n;
+      const int head = it.head * p.P + row_head, m = it.e.m, off = m - it.e.n;
+      const long long token = it.e.q0 + tok;
+      const long long vec = static_cast<long long>(head) * p.total_q + token;
+      if (n == 0) {  // no key is seen
+        if (valid) {
+          store_zeros(p.dq + token * p.dq_token + head * p.dq_head + (D / 2) * g, D / 2);
+          if (g == 0) p.D[vec] = 0.0f;
+        }
+        continue;
+      }
+      // a row without keys of its own, or behind the sequence: P = 2^-inf
+      float lse2 = valid ? p.lse[vec] * kLog2e : INFINITY;
+      if (lse2 == -INFINITY) lse2 = INFINITY;
+      bool ok = true;
+      float Di = 0.0f;
+      // the halves' parts of D meet in shared memory
+      auto join = [&](float part) {
+        dx[g * 128 + tr] = part;
+        mbar_arrive(&bars->dx_ready);
+        ok = warp_wait(&bars->dx_ready, tl & 1, bars, 0x313);
+        Di = dx[tr] + dx[128 + tr];
+      };
+      if (n > 1) {
+        float part = 0.0f;
+        if (valid) {
+          const uint4* a = reinterpret_cast<const uint4*>(p.o + token * p.o_token + head * p.o_head + (D / 2) * g);
+          const uint4* b = reinterpret_cast<const uint4*>(p.dO + token * p.dO_token + head * p.dO_head + (D / 2) * g);
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            const uint4 x = a[e], y = b[e];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              part = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), part);
+              part = fmaf(__uint_as_float(xs[w] & 0xffff0000u), __uint_as_float(ys[w] & 0xffff0000u), part);
+            }
+          }
+        }
+        join(part);
+        if (!ok) break;
+      }
+      for (int j = 0; j < n; ++j) {
+        const int step = nb + j;
+        if (!(ok = warp_wait(&bars->s_full[step & 1], (step >> 1) & 1, bars, 0x311))) break;
+        tc_fence_after_sync();
+        uint32_t pr[64];
+        tmem_ld64(tmem + lane_off + L::kSCol + (step & 1) * 128u + col0, pr);
+        tc_fence_before_sync();
+        mbar_arrive(&bars->s_free[step & 1]);
+        const int kv0 = j * 128;
+        const bool need_mask = (CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > m;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
+        auto exp_cols = [&](auto masked, int lim) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float2 x =
+                __ffma2_rn(make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])), sc2, nl2);
+            float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+            if (masked) {
+              if (c > lim) p0 = 0.0f;
+              if (c + 1 > lim) p1 = 0.0f;
+            }
+            pr[c] = __float_as_uint(p0);
+            pr[c + 1] = __float_as_uint(p1);
+          }
+        };
+        if (need_mask)
+          exp_cols(std::true_type{}, (CAUSAL ? min(tok + off, m - 1) : m - 1) - kv0 - static_cast<int>(col0));
+        else
+          exp_cols(std::false_type{}, 0);
+        if (!(ok = warp_wait(&bars->dp_full, step & 1, bars, 0x314))) break;
+        tc_fence_after_sync();
+        const uint32_t dp = tmem + lane_off + L::kDPCol + col0;
+        if (n == 1) {  // D = sum_j P_j dP_j
+          float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            uint32_t rr[32];
+            tmem_ld32(dp + c2 * 32, rr);
+            tmem_ld_wait();
+            reg_pin(rr);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              part = __ffma2_rn(make_float2(__uint_as_float(pr[c2 * 32 + e]), __uint_as_float(pr[c2 * 32 + e + 1])),
+                                make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), part);
+          }
+          join(part.x + part.y);
+          if (!ok) break;
+        }
+        const float2 nD2 = make_float2(-Di, -Di);
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+          uint32_t rr[32], w[16];
+          tmem_ld32(dp + c2 * 32, rr);
+          tmem_ld_wait();
+          reg_pin(rr);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = c2 * 32 + 2 * e;
+            const float2 ds = __fmul2_rn(
+                make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])),
+                __fadd2_rn(make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), nD2));
+            w[e] = pack_bf16x2(ds.x, ds.y);
+          }
+          tmem_st16(dp + c2 * 16, w);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&bars->ds_ready);
+      }
+      if (!ok) break;
+      if (g == 0 && valid) p.D[vec] = Di;
+      if (!warp_wait(&bars->acc_done, tl & 1, bars, 0x312)) break;
+      tc_fence_after_sync();
+      const long long at = valid ? token * p.dq_token + head * p.dq_head + (D / 2) * g : -1;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        store_acc32(tmem + lane_off + L::kAcc + (D / 2) * g + c * 32, p.scale, p.dq + c * 32, at);
+      // the accumulator has been read: the next item may overwrite it
+      tc_fence_before_sync();
+      mbar_arrive(&bars->acc_free);
+      nb += n;
+      ++tl;
+    }
   }
+  bwd_teardown(bars, warp, tmem);
 }
 
-unsigned warps_grid(long long warps) { return static_cast<unsigned>((warps * 32 + 255) / 256); }
+// ============================================================ dK / dV
+// Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK; at d = 64 the accumulators
+// leave room for a second score buffer.  Order of the products: dV_n, S^T_{n+1}, dK_n,
+// dP^T_{n+1} (d = 64: S^T_{n+1} first): threads form dS_n during the first two and
+// P_{n+1} during the last two.
+template <int D>
+struct DkLayout {
+  static constexpr int kChunks = D / 64;
+  static constexpr uint32_t kTile = 128u * D * 2;
+  static constexpr int kRing = D == 64 ? 4 : 2;
+  static constexpr uint32_t kK = 0, kV = kTile, kQ = 2 * kTile, kDO = kQ + kRing * kTile;
+  static constexpr uint32_t kVec = kDO + kRing * kTile;  // [stage][lse2 | D][128]
+  static constexpr uint32_t kBar = kVec + kRing * 1024;
+  static constexpr uint32_t kUsed = kBar + 768;
+  static constexpr uint32_t kSmem = (kUsed > 118784u ? kUsed : 118784u) + 1024;  // + align slack
+  static constexpr bool kDouble = D == 64;
+  static constexpr uint32_t kDPCol = 128, kAcc0 = 256, kAcc1 = 256 + D;
+  __host__ __device__ static constexpr uint32_t s_col(int step) { return kDouble && (step & 1) ? 384u : 0u; }
+  __host__ __device__ static constexpr int s_buf(int step) { return kDouble ? step & 1 : 0; }
+  __host__ __device__ static constexpr uint32_t s_par(int step) { return kDouble ? (step >> 1) & 1 : step & 1; }
+};
+
+// Query tiles of a head group that see the item's key tile: the first, and how many.
+__device__ __forceinline__ int dk_first(const PackedItem& it, int TT, bool causal) {
+  return causal ? max(it.e.tile * 128 - (it.e.m - it.e.n), 0) / TT : 0;
+}
+__device__ __forceinline__ int dk_tiles(const PackedItem& it, int TT, bool causal) {
+  return max((it.e.n + TT - 1) / TT - dk_first(it, TT, causal), 0);
+}
+
+template <int D, bool CAUSAL>
+__global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __grid_constant__ BwdParams p) {
+  using L = DkLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!bwd_init(bars, warp, smem + L::kQ, p.P * p.TT < 128 ? 2 * L::kRing * L::kTile : 0)) return;
+  const uint32_t tmem = bars->tmem_base;
+  grid_dependency_wait();
+
+  if (warp == kTmaWarp) {
+    const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT) * 128u * L::kChunks;
+    int row_tok[4], row_head[4];  // of rows lane, lane + 32, ..
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      row_tok[e] = (lane + 32 * e) / p.P;
+      row_head[e] = lane + 32 * e - row_tok[e] * p.P;
+    }
+    int sb = 0, tl = 0;
+    PackedItem it;
+    if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv);
+    for (int t = 0;; ++t) {
+      const int r = t % kPackedRing;
+      if (!warp_wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, bars, 0x104)) break;
+      if (lane == 0) {
+        bars->item[r] = it;
+        mbar_arrive(&bars->item_full[r]);
+      }
+      __syncwarp();
+      it = bars->item[r];
+      if (it.head < 0) break;
+      const int first = dk_first(it, p.TT, CAUSAL), per = dk_tiles(it, p.TT, CAUSAL), n = per * p.per_kv;
+      if (n == 0) {
+        if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv);
+        continue;
+      }
+      const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tensormap_acquire(maps + i);
+      }
+      auto load_res = [&]() {
+        if (lane != 0) return;
+        mbar_arrive_expect_tx(&bars->res_full, 2 * L::kTile);
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c) {
+          tma_load_3d(smem + L::kK + c * 16384, maps + 1, &bars->res_full, c * 64, it.e.tile * 128, it.head);
+          tma_load_3d(smem + L::kV + c * 16384, maps + 2, &bars->res_full, c * 64, it.e.tile * 128, it.head);
+        }
+      };
+      if (tl == 0) load_res();
+      PackedItem next = it;
+      bool ok = true;
+      int sub = 0, tile = first;
+      for (int j = 0; j < n; ++j) {
+        const int s = (sb + j) % L::kRing, group = it.head * p.per_kv + sub;
+        if (!(ok = warp_wait(&bars->a_empty[s], (((sb + j) / L::kRing) & 1) ^ 1, bars, 0x101))) break;
+        // the tiles first, then, while they are in flight, lse and D of their rows; the
+        // stage's one arrival comes after both
+        if (lane == 0) {
+          mbar_expect_tx(&bars->a_full[s], 2 * q_bytes);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c) {
+            tma_load_4d(smem + L::kQ + s * L::kTile + c * 16384, maps, &bars->a_full[s], c * 64, 0, tile * p.TT, group);
+            tma_load_4d(smem + L::kDO + s * L::kTile + c * 16384, maps + 3, &bars->a_full[s], c * 64, 0, tile * p.TT, group);
+          }
+        }
+        float* vec = reinterpret_cast<float*>(smem + L::kVec) + s * 256;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = tile * p.TT + row_tok[e];
+          float l2 = INFINITY, Di = 0.0f;  // rows that do not exist, or see nothing: P = 0
+          if (row_tok[e] < p.TT && tok < it.e.n) {
+            const long long at = static_cast<long long>(group * p.P + row_head[e]) * p.total_q + it.e.q0 + tok;
+            l2 = p.lse[at] * kLog2e;
+            Di = p.D[at];
+            if (l2 == -INFINITY) {
+              l2 = INFINITY;
+              Di = 0.0f;
+            }
+          }
+          vec[lane + 32 * e] = l2;
+          vec[128 + lane + 32 * e] = Di;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->a_full[s]);
+        __syncwarp();
+        if (j == 0 && tl > 0) {
+          if (!(ok = warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x102))) break;
+          load_res();
+          __syncwarp();
+        }
+        if (lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv);
+        if (++tile == first + per) {
+          tile = first;
+          ++sub;
+        }
+      }
+      if (!ok) break;
+      sb += n;
+      ++tl;
+      it = next;
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
+      const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+      auto sQ = [&](int pos) { return smem_u32(smem + L::kQ) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
+      auto sdO = [&](int pos) { return smem_u32(smem + L::kDO) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
+      auto issue_s = [&](int pos) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(tmem + L::s_col(pos), kmajor_desc(sK, kk), kmajor_desc(sQ(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+      };
+      auto issue_dp = [&](int pos) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(tmem + L::kDPCol, kmajor_desc(sV, kk), kmajor_desc(sdO(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+      };
+      auto full = [&](int pos, uint32_t code) {
+        return wait(&bars->a_full[pos % L::kRing], (pos / L::kRing) & 1, bars, code);
+      };
+      int sb = 0, tl = 0;
+      for (int t = 0;; ++t) {
+        const int r = t % kPackedRing;
+        if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x207)) break;
+        const PackedItem it = bars->item[r];
+        mbar_arrive(&bars->item_empty[r]);
+        if (it.head < 0) break;
+        const int n = dk_tiles(it, p.TT, CAUSAL) * p.per_kv;
+        if (n == 0) continue;
+        bool ok = wait(&bars->res_full, tl & 1, bars, 0x201) && full(sb, 0x202);
+        if (!ok) break;
+        tc_fence_after_sync();
+        issue_s(sb);
+        umma_commit(&bars->s_full[L::s_buf(sb)]);
+        issue_dp(sb);
+        umma_commit(&bars->dp_full);
+        for (int j = 0; j < n; ++j) {
+          const int pos = sb + j;
+          const bool more = j + 1 < n;
+          if (L::kDouble && more) {
+            if (!(ok = full(pos + 1, 0x208))) break;
+            tc_fence_after_sync();
+            issue_s(pos + 1);
+            umma_commit(&bars->s_full[L::s_buf(pos + 1)]);
+          }
+          // dV += P^T dO_j (A = P^T bf16 in tensor memory over S^T); an item's first overwrites the
+          // accumulators that the epilogue before it reads
+          if (!(ok = wait(&bars->s_free[L::s_buf(pos)], L::s_par(pos), bars, 0x203) &&
+                     (j > 0 || tl == 0 || wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206))))
+            break;
+          const bool next_in =
+              L::kDouble || !more || mbar_test_wait(&bars->a_full[(pos + 1) % L::kRing], ((pos + 1) / L::kRing) & 1);
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + L::kAcc0, tmem + L::s_col(pos) + packed_a_col(kk), mnmajor_desc(sdO(pos), kk), idesc_acc,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+          if (!L::kDouble && more) {
+            if (!next_in) {
+              if (!(ok = full(pos + 1, 0x205))) break;
+              tc_fence_after_sync();
+            }
+            issue_s(pos + 1);
+          }
+          // dK += dS^T Q_j
+          const bool ds_in = mbar_test_wait(&bars->ds_ready, pos & 1);
+          if (!L::kDouble && more) umma_commit(&bars->s_full[0]);
+          if (!ds_in && !(ok = wait(&bars->ds_ready, pos & 1, bars, 0x204))) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + L::kAcc1, tmem + L::kDPCol + packed_a_col(kk), mnmajor_desc(sQ(pos), kk), idesc_acc,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->a_empty[pos % L::kRing]);
+          if (more) {
+            issue_dp(pos + 1);
+            umma_commit(&bars->dp_full);
+          }
+        }
+        if (!ok) break;
+        umma_commit(&bars->acc_done);
+        umma_commit(&bars->res_empty);
+        sb += n;
+        ++tl;
+      }
+      umma_commit(&bars->drain);
+    }
+    __syncwarp();
+  } else {
+    const int g = threadIdx.x >> 7;    // half of the query columns
+    const int tr = threadIdx.x & 127;  // key within the tile, TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t col0 = 64u * g;
+    int nb = 0, tl = 0;
+    for (int ti = 0;; ++ti) {
+      const int r = ti % kPackedRing;
+      if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, bars, 0x305)) break;
+      const PackedItem it = bars->item[r];
+      mbar_arrive(&bars->item_empty[r]);
+      if (it.head < 0) break;
+      const int first = dk_first(it, p.TT, CAUSAL), per = dk_tiles(it, p.TT, CAUSAL), n = per * p.per_kv;
+      const int key = it.e.tile * 128 + tr;
+      const bool valid = key < it.e.m;
+      const long long token = it.e.k0 + key;
+      const long long at_k = valid ? token * p.dk_token + it.head * p.dk_head + (D / 2) * g : -1;
+      const long long at_v = valid ? token * p.dv_token + it.head * p.dv_head + (D / 2) * g : -1;
+      if (n == 0) {  // no query sees the tile
+        if (valid) {
+          store_zeros(p.dk + at_k, D / 2);
+          store_zeros(p.dv + at_v, D / 2);
+        }
+        continue;
+      }
+      bool ok = true;
+      int tile = first;
+      // causal: query token i sees the key where i >= key - (m - n)
+      const int from = key - (it.e.m - it.e.n);
+      const int last_from = it.e.tile * 128 + 127 - (it.e.m - it.e.n);
+      for (int j = 0; j < n; ++j) {
+        const int step = nb + j;
+        const float* lse2_s = reinterpret_cast<const float*>(smem + L::kVec) + (step % L::kRing) * 256;
+        const float* D_s = lse2_s + 128;
+        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x301))) break;
+        tc_fence_after_sync();
+        uint32_t pr[64];
+        tmem_ld64(tmem + lane_off + L::s_col(step) + col0, pr);
+        const float4* lse4 = reinterpret_cast<const float4*>(lse2_s + col0);
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        auto exp_cols = [&](auto masked, int lim) {
+#pragma unroll
+          for (int c4 = 0; c4 < 16; ++c4) {
+            const float4 l4 = lse4[c4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = 4 * c4 + 2 * h;
+              const float2 nl = h ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y);
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])), sc2, nl);
+              float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+              if (masked) {  // queries before the key
+                if (c < lim) p0 = 0.0f;
+                if (c + 1 < lim) p1 = 0.0f;
+              }
+              pr[c] = __float_as_uint(p0);
+              pr[c + 1] = __float_as_uint(p1);
+            }
+          }
+        };
+        // row r of the tile is token tile * TT + r / P
+        if (CAUSAL && tile * p.TT < last_from)
+          exp_cols(std::true_type{}, min(max(from - tile * p.TT, 0), 128) * p.P - static_cast<int>(col0));
+        else
+          exp_cols(std::false_type{}, 0);
+        {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            pk[c] = pack_bf16x2(__uint_as_float(pr[2 * c]), __uint_as_float(pr[2 * c + 1]));
+          tmem_st32(tmem + lane_off + L::s_col(step) + col0, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&bars->s_free[L::s_buf(step)]);
+        if (!(ok = warp_wait(&bars->dp_full, step & 1, bars, 0x306))) break;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+          uint32_t rr[32], w[16];
+          tmem_ld32(tmem + lane_off + L::kDPCol + col0 + c2 * 32, rr);
+          tmem_ld_wait();
+          reg_pin(rr);
+          const float4* d4 = reinterpret_cast<const float4*>(D_s + col0 + c2 * 32);
+#pragma unroll
+          for (int e4 = 0; e4 < 8; ++e4) {
+            const float4 dd = d4[e4];
+            const int c = c2 * 32 + 4 * e4;
+            const float2 ds01 = __fmul2_rn(
+                make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])),
+                __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4]), __uint_as_float(rr[4 * e4 + 1])),
+                           make_float2(-dd.x, -dd.y)));
+            const float2 ds23 = __fmul2_rn(
+                make_float2(__uint_as_float(pr[c + 2]), __uint_as_float(pr[c + 3])),
+                __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4 + 2]), __uint_as_float(rr[4 * e4 + 3])),
+                           make_float2(-dd.z, -dd.w)));
+            w[2 * e4] = pack_bf16x2(ds01.x, ds01.y);
+            w[2 * e4 + 1] = pack_bf16x2(ds23.x, ds23.y);
+          }
+          tmem_st16(tmem + lane_off + L::kDPCol + col0 + c2 * 16, w);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&bars->ds_ready);
+        if (++tile == first + per) tile = first;
+      }
+      if (!ok || !warp_wait(&bars->acc_done, tl & 1, bars, 0x302)) break;
+      tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        store_acc32(tmem + lane_off + L::kAcc0 + (D / 2) * g + c * 32, 1.0f, p.dv + c * 32, at_v);
+        store_acc32(tmem + lane_off + L::kAcc1 + (D / 2) * g + c * 32, p.scale, p.dk + c * 32, at_k);
+      }
+      // the accumulators have been read: the next item may overwrite them
+      tc_fence_before_sync();
+      mbar_arrive(&bars->acc_free);
+      nb += n;
+      ++tl;
+    }
+  }
+  bwd_teardown(bars, warp, tmem);
+}
+
+// Launched while the kernel before it still runs, for which it waits (griddepcontrol.wait).
+template <typename Kern>
+cudaError_t launch_after(Kern kern, const BwdParams& p, unsigned blocks, uint32_t smem, cudaStream_t s) {
+  if (blocks == 0) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, p);
+}
+
+template <int D, bool CAUSAL>
+cudaError_t launch_t(BwdParams p, const PackedEntry* const list[2], unsigned dq_blocks, unsigned dk_blocks,
+                     cudaStream_t s) {
+  p.list = list[0];
+  const cudaError_t e = launch_after(fa_packed_dq_kernel<D, CAUSAL>, p, dq_blocks, DqLayout<D>::kSmem, s);
+  if (e != cudaSuccess) return e;
+  p.list = list[1];
+  return launch_after(fa_packed_dkdv_kernel<D, CAUSAL>, p, dk_blocks, DkLayout<D>::kSmem, s);
+}
 
 }  // namespace
 
 cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s) {
-  const unsigned gq = warps_grid(static_cast<long long>(a.total_q) * a.q.heads);
-  const unsigned gk = warps_grid(static_cast<long long>(a.total_k) * a.k.heads);
-  if (gq > 0) {
-    if (a.d == 64) fa_packed_dq_kernel<64><<<gq, 256, 0, s>>>(a);
-    else fa_packed_dq_kernel<128><<<gq, 256, 0, s>>>(a);
+  const int Hq = a.q.heads, Hkv = a.k.heads;
+  const PackedTiling t = packed_tiling(Hq, Hkv);
+  const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, Hq, Hkv, true);
+  const cudaError_t e = launch_packed_plan(a, maps, 4, true, s);
+  if (e != cudaSuccess) return e;
+  char* ws = static_cast<char*>(a.workspace);
+  auto out = [](const HeadsView& v) { return static_cast<__nv_bfloat16*>(const_cast<void*>(v.p)); };
+  BwdParams p{};
+  p.header = reinterpret_cast<PackedHeader*>(ws);
+  p.maps = reinterpret_cast<const CUtensorMap*>(ws + l.maps);
+  p.lse = a.lse;
+  p.D = reinterpret_cast<float*>(ws + l.D);
+  p.o = out(a.o), p.o_token = a.o.token, p.o_head = a.o.head;
+  p.dO = out(a.dO), p.dO_token = a.dO.token, p.dO_head = a.dO.head;
+  p.dq = out(a.dq), p.dq_token = a.dq.token, p.dq_head = a.dq.head;
+  p.dk = out(a.dk), p.dk_token = a.dk.token, p.dk_head = a.dk.head;
+  p.dv = out(a.dv), p.dv_token = a.dv.token, p.dv_head = a.dv.head;
+  p.total_q = a.total_q;
+  p.P = t.P;
+  p.TT = t.TT;
+  p.heads = t.heads;
+  p.per_kv = t.per_kv;
+  p.Hkv = Hkv;
+  p.scale = a.scale;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  const PackedEntry* const list[2] = {reinterpret_cast<const PackedEntry*>(ws + l.list[0]),
+                                      reinterpret_cast<const PackedEntry*>(ws + l.list[1])};
+  const long long q_items = a.total_q > 0 ? (a.total_q / t.TT + a.B) * static_cast<long long>(t.heads) : 0;
+  const long long k_items = a.total_k > 0 ? (a.total_k / 128 + a.B) * static_cast<long long>(Hkv) : 0;
+  const unsigned nq = static_cast<unsigned>(std::min<long long>(q_items, a.num_sms));
+  const unsigned nk = static_cast<unsigned>(std::min<long long>(k_items, a.num_sms));
+  if (a.d == 64)
+    return a.causal ? launch_t<64, true>(p, list, nq, nk, s) : launch_t<64, false>(p, list, nq, nk, s);
+  return a.causal ? launch_t<128, true>(p, list, nq, nk, s) : launch_t<128, false>(p, list, nq, nk, s);
+}
+
+cudaError_t packed_bwd_read_clear_error(uint32_t* out, cudaStream_t s) {
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  uint32_t v = 0;
+  e = cudaMemcpyFromSymbol(&v, g_packed_bwd_error, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (v) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_packed_bwd_error, &zero, sizeof(zero));
   }
-  if (gk > 0) {
-    if (a.d == 64) fa_packed_dkdv_kernel<64><<<gk, 256, 0, s>>>(a);
-    else fa_packed_dkdv_kernel<128><<<gk, 256, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  *out = v;
+  return e;
 }
 
 }  // namespace fa
