@@ -56,8 +56,9 @@ __device__ __forceinline__ int bucket_of(const PackedPlanArgs& a, int which, con
 
 // Block b < nlists builds list b: a counting sort of all tiles by bucket, longest first
 // (the order within a bucket is that of the atomics; results do not depend on it).  The
-// other blocks write tensor maps, a thread each.  A warp takes 32 sequences at a time:
-// their spans in one load each, then sequence by sequence with a lane a tile.
+// other blocks write tensor maps, a thread each.  A warp takes up to 32 sequences at a time
+// (few enough that all warps have some): their spans in one load each, then sequence by
+// sequence with a lane a tile.
 __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __grid_constant__ PackedPlanArgs a) {
   grid_dependency_launch();
   if (blockIdx.x >= static_cast<unsigned>(a.nlists)) {
@@ -91,9 +92,10 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
   __syncthreads();
   // every tile in turn: f(bucket, sequence, span, tile)
   auto tiles = [&](auto&& f) {
-    for (int b0 = warp * 32; b0 < a.B; b0 += 32 * (kPlanThreads / 32)) {
+    const int each = min((a.B + kPlanThreads / 32 - 1) / (kPlanThreads / 32), 32);
+    for (int b0 = warp * each; b0 < a.B; b0 += each * (kPlanThreads / 32)) {
       Span mine = {0, 0, 0, 0};
-      if (b0 + lane < a.B) mine = span_of(a, b0 + lane);
+      if (lane < each && b0 + lane < a.B) mine = span_of(a, b0 + lane);
       const int own = which == 0 ? (mine.n + a.q_span - 1) / a.q_span : (mine.m + 127) >> 7;
       unsigned left = __ballot_sync(0xffffffffu, own > 0);
       while (left) {
@@ -202,10 +204,22 @@ struct FwdParams {
   long long o_token, o_head;
   float* lse;
   int total_q;
-  int P, TT, heads, per_kv;
+  int P, TT, heads, per_kv, chunk;
   float scale_log2;
   int causal;
 };
+
+// A wait's loop out of line: the code of the kernel stays small.
+__device__ __noinline__ bool wait_loop(uint64_t* bar, uint32_t par, FwdBars* b, uint32_t code) {
+  return mbar_wait(bar, par, &b->abort_flag, &g_packed_error, code);
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t par, FwdBars* b, uint32_t code) {
+  return mbar_try_wait(smem_u32(bar), par) || wait_loop(bar, par, b, code);
+}
+// The same by a whole warp, with one answer.
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t par, FwdBars* b, uint32_t code) {
+  return __all_sync(0xffffffffu, bar_wait(bar, par, b, code));
+}
 
 __device__ __forceinline__ int ring_slot(int pos) { return static_cast<int>(static_cast<unsigned>(pos) % kStages); }
 __device__ __forceinline__ uint32_t ring_phase(int pos) { return (static_cast<unsigned>(pos) / kStages) & 1u; }
@@ -271,11 +285,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     // ------------------------------------------------ TMA producer
     if (lane == 0) {
       auto wait = [&](uint64_t* bar, uint32_t par, uint32_t code) {
-        return mbar_wait(bar, par, &bars->abort_flag, &g_packed_error, code);
+        return bar_wait(bar, par, bars, code);
       };
       const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT) * 128u * L::kChunks;
       int kvb = 0, tl = 0;  // K / V tiles and items with loads so far
-      PackedItem it = packed_claim(p.header, p.list, 0, p.heads);
+      PackedItem it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
       for (int t = 0;; ++t) {
         const int r = t % kPackedRing;
         if (!wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, 0x104)) break;
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         const int n0 = item_tiles(it, 0, p.TT, CAUSAL), n1 = item_tiles(it, 1, p.TT, CAUSAL);
         const int nmax = max(n0, n1);
         if (nmax == 0) {
-          it = packed_claim(p.header, p.list, 0, p.heads);
+          it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
           continue;
         }
         const CUtensorMap* maps = p.maps + 3ll * it.e.seq;
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
             tma_load_3d(smem + L::kV + s * L::kTileBytes + c * 16384, maps + 2, &bars->v_full[s], c * 64,
                         j * 128, kh);
           // the next item is asked for while the last two tiles are under way
-          if (j == max(nmax - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads);
+          if (j == max(nmax - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
         }
         if (!ok) break;
         kvb += nmax;
@@ -340,99 +354,101 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
-      const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
-      auto wait = [&](uint64_t* bar, uint32_t par, uint32_t code) {
-        return mbar_wait(bar, par, &bars->abort_flag, &g_packed_error, code);
-      };
-      auto issue_s = [&](int g, int pos) {
-        const uint32_t kbase = sK + ring_slot(pos) * L::kTileBytes, qbase = sQ + g * L::kTileBytes;
+    // The whole warp runs the loop on values that are the same in all lanes, so that descriptors
+    // lie in uniform registers, where the instruction wants them; one elected lane issues.
+    // (By one lane in a divergent branch each product took 100 cycles to issue, of 64 that
+    // it runs.)
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
+    const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+    auto wait = [&](uint64_t* bar, uint32_t par, uint32_t code) { return all_wait(bar, par, bars, code); };
+    auto issue_s = [&](int g, int pos) {
+      const uint32_t kbase = sK + ring_slot(pos) * L::kTileBytes, qbase = sQ + g * L::kTileBytes;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          umma_ss(tmem + L::s_col(g), sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + off, 16, 1024),
-                  idesc_qk, kk > 0 ? 1u : 0u);
-        }
-      };
-      auto issue_pv = [&](int g, int pos, bool first) {
-        const uint32_t vbase = sV + ring_slot(pos) * L::kTileBytes;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ts(tmem + L::o_col(g), tmem + L::s_col(g) + kk * 8, sdesc_sw128(vbase + kk * 2048, 16384, 1024),
-                  idesc_pv, (!first || kk > 0) ? 1u : 0u);
-      };
-      // Order of the products for key tile j: PV0_j, S0_{j+1}, PV1_j, S1_{j+1}, each pair a burst
-      // with the waits for all that it reads ahead of it.  A tile may have no work in an
-      // item (it lies behind the sequence, or sees no key), or end before the other.
-      int kvb = 0, tl = 0, base0 = 0, base1 = 0, used0 = 0, used1 = 0;
-      for (int t = 0;; ++t) {
-        const int r = t % kPackedRing;
-        if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, 0x20b)) break;
-        const PackedItem it = bars->item[r];
-        mbar_arrive(&bars->item_empty[r]);
-        if (it.head < 0) break;
-        const int n0 = item_tiles(it, 0, p.TT, CAUSAL), n1 = item_tiles(it, 1, p.TT, CAUSAL);
-        const int nmax = max(n0, n1);
-        if (nmax == 0) continue;
-        bool ok = wait(&bars->q_full, tl & 1, 0x201) && wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202);
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (n0 > 0) {
-          issue_s(0, kvb);
-          umma_commit(&bars->s_full[0]);
-        }
-        if (n1 > 0) {
-          issue_s(1, kvb);
-          umma_commit(&bars->s_full[1]);
-        }
-        umma_commit(&bars->k_empty[ring_slot(kvb)]);
-        for (int j = 0; j < nmax; ++j) {
-          const int pos = kvb + j, s = ring_slot(pos), sn = ring_slot(pos + 1);
-          const uint32_t ph = ring_phase(pos), phn = ring_phase(pos + 1);
-          bool pre1 = false;
-          if (j < n0) {
-            ok = wait(&bars->p_ready[0], (base0 + j) & 1, 0x203) && wait(&bars->v_full[s], ph, 0x204) &&
-                 (j > 0 || used0 == 0 || wait(&bars->o_free[0], (used0 - 1) & 1, 0x209)) &&
-                 (j + 1 >= nmax || wait(&bars->k_full[sn], phn, 0x205));
-            if (!ok) break;
-            tc_fence_after_sync();
-            issue_pv(0, pos, j == 0);
-            umma_commit(&bars->pv_done[0]);
-            if (j + 1 < n0) issue_s(0, pos + 1);
-            pre1 = j < n1 && mbar_test_wait(&bars->p_ready[1], (base1 + j) & 1) &&
-                   (j > 0 || used1 == 0 || mbar_test_wait(&bars->o_free[1], (used1 - 1) & 1));
-            if (j + 1 < n0) umma_commit(&bars->s_full[0]);
-          }
-          if (j < n1) {
-            if (!pre1) {
-              ok = wait(&bars->p_ready[1], (base1 + j) & 1, 0x206) &&
-                   (j < n0 || wait(&bars->v_full[s], ph, 0x207)) &&
-                   (j > 0 || used1 == 0 || wait(&bars->o_free[1], (used1 - 1) & 1, 0x20a)) &&
-                   (j < n0 || j + 1 >= nmax || wait(&bars->k_full[sn], phn, 0x208));
-              if (!ok) break;
-            }
-            tc_fence_after_sync();
-            issue_pv(1, pos, j == 0);
-          }
-          umma_commit(&bars->v_empty[s]);
-          if (j + 1 < n1) issue_s(1, pos + 1);
-          if (j < n1) umma_commit(&bars->pv_done[1]);
-          if (j + 1 < n1) umma_commit(&bars->s_full[1]);
-          if (j + 1 < nmax) umma_commit(&bars->k_empty[sn]);
-        }
-        if (!ok) break;
-        umma_commit(&bars->q_empty);
-        kvb += nmax;
-        ++tl;
-        base0 += n0;
-        base1 += n1;
-        used0 += n0 > 0;
-        used1 += n1 > 0;
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+        umma_ss(tmem + L::s_col(g), sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + off, 16, 1024),
+                idesc_qk, kk > 0 ? 1u : 0u);
       }
-      umma_commit(&bars->drain);
+      umma_commit(&bars->s_full[g]);
+    };
+    auto issue_pv = [&](int g, int pos, bool first) {
+      const uint32_t vbase = sV + ring_slot(pos) * L::kTileBytes;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        umma_ts(tmem + L::o_col(g), tmem + L::s_col(g) + kk * 8, sdesc_sw128(vbase + kk * 2048, 16384, 1024),
+                idesc_pv, (!first || kk > 0) ? 1u : 0u);
+      umma_commit(&bars->pv_done[g]);
+    };
+    // Order of the products for key tile j: PV0_j, S0_{j+1}, PV1_j, S1_{j+1}, each pair a burst
+    // with the waits for all that it reads ahead of it.  A tile may have no work in an
+    // item (it lies behind the sequence, or sees no key), or end before the other.
+    int kvb = 0, tl = 0, base0 = 0, base1 = 0, used0 = 0, used1 = 0;
+    for (int t = 0;; ++t) {
+      const int r = t % kPackedRing;
+      if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, 0x20b)) break;
+      const PackedItem it = bars->item[r];
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&bars->item_empty[r]);
+      if (uniform(it.head) < 0) break;
+      const int n0 = uniform(item_tiles(it, 0, p.TT, CAUSAL)), n1 = uniform(item_tiles(it, 1, p.TT, CAUSAL));
+      const int nmax = max(n0, n1);
+      if (nmax == 0) continue;
+      if (!wait(&bars->q_full, tl & 1, 0x201) || !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202)) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        if (n0 > 0) issue_s(0, kvb);
+        if (n1 > 0) issue_s(1, kvb);
+        umma_commit(&bars->k_empty[ring_slot(kvb)]);
+      }
+      __syncwarp();
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; j < nmax; ++j) {
+        const int pos = kvb + j, s = ring_slot(pos), sn = ring_slot(pos + 1);
+        const uint32_t ph = ring_phase(pos), phn = ring_phase(pos + 1);
+        if (j < n0) {
+          ok = wait(&bars->p_ready[0], (base0 + j) & 1, 0x203) && wait(&bars->v_full[s], ph, 0x204) &&
+               (j > 0 || used0 == 0 || wait(&bars->o_free[0], (used0 - 1) & 1, 0x209)) &&
+               (j + 1 >= nmax || wait(&bars->k_full[sn], phn, 0x205));
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            issue_pv(0, pos, j == 0);
+            if (j + 1 < n0) issue_s(0, pos + 1);
+            if (j >= n1) {
+              umma_commit(&bars->v_empty[s]);
+              if (j + 1 < nmax) umma_commit(&bars->k_empty[sn]);
+            }
+          }
+          __syncwarp();
+        }
+        if (j < n1) {
+          ok = wait(&bars->p_ready[1], (base1 + j) & 1, 0x206) && (j < n0 || wait(&bars->v_full[s], ph, 0x207)) &&
+               (j > 0 || used1 == 0 || wait(&bars->o_free[1], (used1 - 1) & 1, 0x20a)) &&
+               (j < n0 || j + 1 >= nmax || wait(&bars->k_full[sn], phn, 0x208));
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            issue_pv(1, pos, j == 0);
+            umma_commit(&bars->v_empty[s]);
+            if (j + 1 < n1) issue_s(1, pos + 1);
+            if (j + 1 < nmax) umma_commit(&bars->k_empty[sn]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit(&bars->q_empty);
+      kvb += nmax;
+      ++tl;
+      base0 += n0;
+      base1 += n1;
+      used0 += n0 > 0;
+      used1 += n1 > 0;
     }
+    __syncwarp();
+    if (elect_one()) umma_commit(&bars->drain);
     __syncwarp();
   } else {
     // ------------------------------------------------ softmax warpgroups
@@ -442,9 +458,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     const uint32_t scol = tmem + lane_off + L::s_col(g), ocol = tmem + lane_off + L::o_col(g);
     const int row_tok = t / p.P, row_head = t - row_tok * p.P;
     const bool row_in = row_tok < p.TT;
-    auto warp_wait = [&](uint64_t* bar, uint32_t par, uint32_t code) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, par, &bars->abort_flag, &g_packed_error, code));
-    };
+    auto warp_wait = [&](uint64_t* bar, uint32_t par, uint32_t code) { return all_wait(bar, par, bars, code); };
     int tb = 0;  // key tiles of earlier items
     for (int ti = 0;; ++ti) {
       const int r = ti % kPackedRing;
@@ -686,6 +700,7 @@ cudaError_t launch_forward_packed(const PackedArgs& a, const CUtensorMap* maps, 
   p.TT = t.TT;
   p.heads = t.heads;
   p.per_kv = t.per_kv;
+  p.chunk = packed_chunk(a.total_k, a.d, a.k.heads) * t.per_kv;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.causal = a.causal;
   const long long items = (a.total_q / (2ll * t.TT) + a.B) * t.heads;

@@ -60,6 +60,13 @@ inline PackedTiling packed_tiling(int Hq, int Hkv) {
   return t;
 }
 
+// Heads taken together so that what their items stream (two tensors, `tokens` rows of d bf16 a
+// head each) stays in half of the 129 MB L2: at least one, at most all.
+inline int packed_chunk(long long tokens, int d, int heads) {
+  const long long fit = (64ll << 20) / (tokens * d * 4 + 1);
+  return static_cast<int>(fit < 1 ? 1 : (fit > heads ? heads : fit));
+}
+
 // The workspace: header, four tensor maps a sequence (the forward pass uses three), two
 // lists, and the backward pass's D.
 struct PackedLayout {
@@ -134,6 +141,18 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// The value of the first lane, which the compiler knows to be the same in all.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // An item as the roles of a CTA see it: a list entry and one of its heads.
 struct PackedItem {
   PackedEntry e;
@@ -142,17 +161,18 @@ struct PackedItem {
 
 constexpr int kPackedRing = 4;  // items in flight between the roles of a CTA
 
-// The next item of a list (one thread).
+// The next item of a list (one thread): chunks of `chunk` of the `heads` heads one after the
+// other, in each all tiles in the list's order, the chunk's heads of a tile next to each other.
 __device__ __forceinline__ PackedItem packed_claim(PackedHeader* h, const PackedEntry* list, int which,
-                                                   int heads) {
+                                                   int heads, int chunk) {
   PackedItem it;
-  const unsigned c = atomicAdd(&h->next[which], 1u);
-  const unsigned entry = c / static_cast<unsigned>(heads);
-  if (entry >= h->count[which]) {
-    it.head = -1;
-    return it;
-  }
-  it.head = static_cast<int>(c - entry * heads);
+  const unsigned c = atomicAdd(&h->next[which], 1u), count = h->count[which];
+  it.head = -1;
+  if (c >= count * static_cast<unsigned>(heads)) return it;
+  const unsigned before = c / (count * chunk) * chunk;  // heads of earlier chunks
+  const unsigned here = min(static_cast<unsigned>(chunk), heads - before);
+  const unsigned r = c - before * count, entry = r / here;
+  it.head = static_cast<int>(before + r - entry * here);
   const int4* p = reinterpret_cast<const int4*>(list + entry);
   const int4 x = p[0], y = p[1];
   it.e = {x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};

@@ -53,7 +53,7 @@ struct BwdParams {
   __nv_bfloat16* dv;
   long long o_token, o_head, dO_token, dO_head, dq_token, dq_head, dk_token, dk_head, dv_token, dv_head;
   int total_q;
-  int P, TT, heads, per_kv, Hkv;
+  int P, TT, heads, per_kv, Hkv, chunk;
   float scale, scale_log2;
 };
 
@@ -63,8 +63,9 @@ struct BwdBars {
   uint64_t res_full, res_empty;
   uint64_t a_full[4], a_empty[4];  // dq: key tiles; dk, dv: query tiles with their dO
   uint64_t b_full[4], b_empty[4];  // dq: value tiles
-  uint64_t s_full[2], s_free[2];   // scores computed; read by all threads (dq), P written (dk, dv)
-  uint64_t dp_full, ds_ready, dx_ready;
+  uint64_t s_full, s_full_1;  // scores computed (of buffer 1)
+  uint64_t s_free, s_free_1;  // and read by all threads (dq), or P written over them (dk, dv)
+  uint64_t dp_full[2], ds_ready[2], dx_ready;
   uint64_t acc_done, acc_free;
   uint64_t item_full[kPackedRing], item_empty[kPackedRing];
   uint64_t drain;
@@ -74,9 +75,14 @@ struct BwdBars {
 };
 static_assert(sizeof(BwdBars) <= 768, "barrier block overruns its shared memory");
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t par, BwdBars* b, uint32_t code) {
+// A wait's loop out of line: the code of the kernels stays small.
+__device__ __noinline__ bool wait_loop(uint64_t* bar, uint32_t par, BwdBars* b, uint32_t code) {
   return mbar_wait(bar, par, &b->abort_flag, &g_packed_bwd_error, code);
 }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t par, BwdBars* b, uint32_t code) {
+  return mbar_try_wait(smem_u32(bar), par) || wait_loop(bar, par, b, code);
+}
+// The same by a whole warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t par, BwdBars* b, uint32_t code) {
   return __all_sync(0xffffffffu, wait(bar, par, b, code));
 }
@@ -99,12 +105,14 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, uint8_t* zero,
       mbar_init(&bars->b_full[s], 1);
       mbar_init(&bars->b_empty[s], 1);
     }
+    mbar_init(&bars->s_full, 1);
+    mbar_init(&bars->s_full_1, 1);
+    mbar_init(&bars->s_free, kCompute);
+    mbar_init(&bars->s_free_1, kCompute);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&bars->s_full[b], 1);
-      mbar_init(&bars->s_free[b], kCompute);
+      mbar_init(&bars->dp_full[b], 1);
+      mbar_init(&bars->ds_ready[b], kCompute);
     }
-    mbar_init(&bars->dp_full, 1);
-    mbar_init(&bars->ds_ready, kCompute);
     mbar_init(&bars->dx_ready, kCompute);
     mbar_init(&bars->acc_done, 1);
     mbar_init(&bars->acc_free, kCompute);
@@ -206,10 +214,10 @@ __device__ __forceinline__ void store_zeros(__nv_bfloat16* dst, int n) {
 }
 
 // ============================================================ dQ
-// Tensor memory: two score buffers (step g's in buffer g & 1), dP (dS over it), dQ.  Scores
-// are read into registers and not written back, so step g + 1's product can run while
-// step g is worked on; order of the products: dQ_n, dP_{n+1}, S_{n+2}.  While threads form
-// dS_{n+1} the tensor core has S_{n+2} to do, and P_{n+1} is formed during the other two.
+// Tensor memory: scores, dP in two buffers (step g's in buffer g & 1, dS over it), dQ.  Scores are
+// read into registers and not written back, so their buffer is free at a step's start, and
+// S_{n+1} and dP_{n+1} run while threads form P_n and dS_n; then dQ_n.  The tensor core has
+// the two products of one step and dQ of the step before to do while threads work on a step.
 template <int D>
 struct DqLayout {
   static constexpr int kChunks = D / 64;
@@ -221,7 +229,8 @@ struct DqLayout {
   static constexpr uint32_t kBar = kDx + 1024;
   static constexpr uint32_t kUsed = kBar + 768;
   static constexpr uint32_t kSmem = (kUsed > 118784u ? kUsed : 118784u) + 1024;  // + align slack
-  static constexpr uint32_t kSCol = 0, kDPCol = 256, kAcc = 384;
+  static constexpr uint32_t kSCol = 0, kAcc = 384;
+  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 128u * (step & 1); }
 };
 static_assert(DqLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
     if (lane == 0) {
       const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT) * 128u * L::kChunks;
       int kvb = 0, tl = 0;  // key tiles and items with loads so far
-      PackedItem it = packed_claim(p.header, p.list, 0, p.heads);
+      PackedItem it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
       for (int t = 0;; ++t) {
         const int r = t % kPackedRing;
         if (!wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, bars, 0x104)) break;
@@ -255,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
         if (it.head < 0) break;
         const int n = dq_tiles(it, p.TT, CAUSAL);
         if (n == 0) {
-          it = packed_claim(p.header, p.list, 0, p.heads);
+          it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
           continue;
         }
         const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
           for (int c = 0; c < L::kChunks; ++c)
             tma_load_3d(smem + L::kVs + vs * L::kTile + c * 16384, maps + 2, &bars->b_full[vs], c * 64, j * 128, kh);
           // the next item is asked for while the last two tiles are under way
-          if (j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads);
+          if (j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
         }
         if (!ok) break;
         kvb += n;
@@ -296,72 +305,78 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
-      const uint32_t sQ = smem_u32(smem + L::kQ), sdO = smem_u32(smem + L::kDO);
-      auto sK = [&](int pos) { return smem_u32(smem + L::kKs) + static_cast<uint32_t>(pos % L::kK) * L::kTile; };
-      auto sV = [&](int pos) { return smem_u32(smem + L::kVs) + static_cast<uint32_t>(pos % L::kV) * L::kTile; };
-      // scores of the key tile at ring position pos, once the buffer has been read
-      auto step_s = [&](int pos) {
-        if (!wait(&bars->a_full[pos % L::kK], (pos / L::kK) & 1, bars, 0x211) ||
-            (pos >= 2 && !wait(&bars->s_free[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x212)))
-          return false;
-        tc_fence_after_sync();
+    // The whole warp runs the loop on values that are the same in all lanes, so that descriptors
+    // lie in uniform registers, where the instruction wants them; one elected lane issues.
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
+    const uint32_t sQ = smem_u32(smem + L::kQ), sdO = smem_u32(smem + L::kDO);
+    auto sK = [&](int pos) { return smem_u32(smem + L::kKs) + static_cast<uint32_t>(pos % L::kK) * L::kTile; };
+    auto sV = [&](int pos) { return smem_u32(smem + L::kVs) + static_cast<uint32_t>(pos % L::kV) * L::kTile; };
+    // scores and dP of the key tile at ring position pos: the score buffer has been read by then,
+    // and the dP buffer's last dQ is issued
+    auto step = [&](int pos, bool last) {
+      if (!warp_wait(&bars->a_full[pos % L::kK], (pos / L::kK) & 1, bars, 0x211) ||
+          (pos >= 1 && !warp_wait(&bars->s_free, (pos - 1) & 1, bars, 0x212)))
+        return false;
+      tc_fence_after_sync();
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + L::kSCol + (pos & 1) * 128u, kmajor_desc(sQ, kk), kmajor_desc(sK(pos), kk), idesc_s,
-                  kk > 0 ? 1u : 0u);
-        umma_commit(&bars->s_full[pos & 1]);
-        return true;
-      };
-      auto step_dp = [&](int pos) {
-        if (!wait(&bars->b_full[pos % L::kV], (pos / L::kV) & 1, bars, 0x213)) return false;
-        tc_fence_after_sync();
+          umma_ss(tmem + L::kSCol, kmajor_desc(sQ, kk), kmajor_desc(sK(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(&bars->s_full);
+      }
+      __syncwarp();
+      if (!warp_wait(&bars->b_full[pos % L::kV], (pos / L::kV) & 1, bars, 0x213)) return false;
+      tc_fence_after_sync();
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + L::kDPCol, kmajor_desc(sdO, kk), kmajor_desc(sV(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
-        umma_commit(&bars->dp_full);
+          umma_ss(tmem + L::dp_col(pos), kmajor_desc(sdO, kk), kmajor_desc(sV(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(&bars->dp_full[pos & 1]);
         umma_commit(&bars->b_empty[pos % L::kV]);
-        return true;
-      };
-      int kvb = 0, tl = 0;
-      for (int t = 0;; ++t) {
-        const int r = t % kPackedRing;
-        if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x21b)) break;
-        const PackedItem it = bars->item[r];
-        mbar_arrive(&bars->item_empty[r]);
-        if (it.head < 0) break;
-        const int n = dq_tiles(it, p.TT, CAUSAL);
-        if (n == 0) continue;
-        bool ok = wait(&bars->res_full, tl & 1, bars, 0x210) && step_s(kvb) && step_dp(kvb) &&
-                  (n < 2 || step_s(kvb + 1));
-        if (!ok) break;
-        if (n == 1) umma_commit(&bars->res_empty);
-        for (int j = 0; j < n; ++j) {
-          const int pos = kvb + j;
-          // dQ += dS K_j (A = dS bf16 in tensor memory over dP); an item's first overwrites the
-          // accumulator that the epilogue before it reads
-          if (!(ok = wait(&bars->ds_ready, pos & 1, bars, 0x214) &&
-                     (j > 0 || tl == 0 || wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216))))
-            break;
-          tc_fence_after_sync();
+        if (last) umma_commit(&bars->res_empty);  // no product of Q or dO is left
+      }
+      __syncwarp();
+      return true;
+    };
+    int kvb = 0, tl = 0;
+    for (int t = 0;; ++t) {
+      const int r = t % kPackedRing;
+      if (!warp_wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x21b)) break;
+      const PackedItem it = bars->item[r];
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&bars->item_empty[r]);
+      if (uniform(it.head) < 0) break;
+      const int n = uniform(dq_tiles(it, p.TT, CAUSAL));
+      if (n == 0) continue;
+      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x210) || !step(kvb, n == 1)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int pos = kvb + j;
+        if (j + 1 < n && !(ok = step(pos + 1, j + 2 == n))) break;
+        // dQ += dS K_j (A = dS bf16 in tensor memory over dP); an item's first overwrites the
+        // accumulator that the epilogue before it reads
+        if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214) &&
+                   (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216))))
+          break;
+        tc_fence_after_sync();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tmem + L::kAcc, tmem + L::kDPCol + packed_a_col(kk), mnmajor_desc(sK(pos), kk), idesc_acc,
+            umma_ts(tmem + L::kAcc, tmem + L::dp_col(pos) + packed_a_col(kk), mnmajor_desc(sK(pos), kk), idesc_acc,
                     (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&bars->a_empty[pos % L::kK]);
-          if (j + 1 < n && !(ok = step_dp(pos + 1))) break;
-          if (j + 2 < n && !(ok = step_s(pos + 2))) break;
-          if (j + 2 == n) umma_commit(&bars->res_empty);  // no product of Q or dO is left
+          if (j + 1 == n) umma_commit(&bars->acc_done);
         }
-        if (!ok) break;
-        umma_commit(&bars->acc_done);
-        kvb += n;
-        ++tl;
+        __syncwarp();
       }
-      umma_commit(&bars->drain);
+      if (!ok) break;
+      kvb += n;
+      ++tl;
     }
+    __syncwarp();
+    if (elect_one()) umma_commit(&bars->drain);
     __syncwarp();
   } else {
     const int g = threadIdx.x >> 7;    // half of the score columns
@@ -425,12 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       }
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
-        if (!(ok = warp_wait(&bars->s_full[step & 1], (step >> 1) & 1, bars, 0x311))) break;
+        if (!(ok = warp_wait(&bars->s_full, step & 1, bars, 0x311))) break;
         tc_fence_after_sync();
         uint32_t pr[64];
-        tmem_ld64(tmem + lane_off + L::kSCol + (step & 1) * 128u + col0, pr);
+        tmem_ld64(tmem + lane_off + L::kSCol + col0, pr);
         tc_fence_before_sync();
-        mbar_arrive(&bars->s_free[step & 1]);
+        mbar_arrive(&bars->s_free);
         const int kv0 = j * 128;
         const bool need_mask = (CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > m;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
@@ -452,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
           exp_cols(std::true_type{}, (CAUSAL ? min(tok + off, m - 1) : m - 1) - kv0 - static_cast<int>(col0));
         else
           exp_cols(std::false_type{}, 0);
-        if (!(ok = warp_wait(&bars->dp_full, step & 1, bars, 0x314))) break;
+        if (!(ok = warp_wait(&bars->dp_full[step & 1], (step >> 1) & 1, bars, 0x314))) break;
         tc_fence_after_sync();
-        const uint32_t dp = tmem + lane_off + L::kDPCol + col0;
+        const uint32_t dp = tmem + lane_off + L::dp_col(step) + col0;
         if (n == 1) {  // D = sum_j P_j dP_j
           float2 part = make_float2(0.f, 0.f);
 #pragma unroll
@@ -490,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->ds_ready);
+        mbar_arrive(&bars->ds_ready[step & 1]);
       }
       if (!ok) break;
       if (g == 0 && valid) p.D[vec] = Di;
@@ -521,14 +536,15 @@ struct DkLayout {
   static constexpr uint32_t kTile = 128u * D * 2;
   static constexpr int kRing = D == 64 ? 4 : 2;
   static constexpr uint32_t kK = 0, kV = kTile, kQ = 2 * kTile, kDO = kQ + kRing * kTile;
-  static constexpr uint32_t kVec = kDO + kRing * kTile;  // [stage][lse2 | D][128]
+  static constexpr uint32_t kVec = kDO + kRing * kTile;  // [stage][-lse2 | -D][128]
   static constexpr uint32_t kBar = kVec + kRing * 1024;
   static constexpr uint32_t kUsed = kBar + 768;
   static constexpr uint32_t kSmem = (kUsed > 118784u ? kUsed : 118784u) + 1024;  // + align slack
   static constexpr bool kDouble = D == 64;
   static constexpr uint32_t kDPCol = 128, kAcc0 = 256, kAcc1 = 256 + D;
   __host__ __device__ static constexpr uint32_t s_col(int step) { return kDouble && (step & 1) ? 384u : 0u; }
-  __host__ __device__ static constexpr int s_buf(int step) { return kDouble ? step & 1 : 0; }
+  __device__ static uint64_t* s_full(BwdBars* b, int step) { return kDouble && (step & 1) ? &b->s_full_1 : &b->s_full; }
+  __device__ static uint64_t* p_ready(BwdBars* b, int step) { return kDouble && (step & 1) ? &b->s_free_1 : &b->s_free; }
   __host__ __device__ static constexpr uint32_t s_par(int step) { return kDouble ? (step >> 1) & 1 : step & 1; }
 };
 
@@ -562,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
     }
     int sb = 0, tl = 0;
     PackedItem it;
-    if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv);
+    if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
     for (int t = 0;; ++t) {
       const int r = t % kPackedRing;
       if (!warp_wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, bars, 0x104)) break;
@@ -575,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       if (it.head < 0) break;
       const int first = dk_first(it, p.TT, CAUSAL), per = dk_tiles(it, p.TT, CAUSAL), n = per * p.per_kv;
       if (n == 0) {
-        if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv);
+        if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
         continue;
       }
       const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
@@ -613,13 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = tile * p.TT + row_tok[e];
-          float l2 = INFINITY, Di = 0.0f;  // rows that do not exist, or see nothing: P = 0
+          float l2 = -INFINITY, Di = 0.0f;  // rows that do not exist, or see nothing: P = 0
           if (row_tok[e] < p.TT && tok < it.e.n) {
             const long long at = static_cast<long long>(group * p.P + row_head[e]) * p.total_q + it.e.q0 + tok;
-            l2 = p.lse[at] * kLog2e;
-            Di = p.D[at];
-            if (l2 == -INFINITY) {
-              l2 = INFINITY;
+            l2 = -p.lse[at] * kLog2e;
+            Di = -p.D[at];
+            if (l2 == INFINITY) {
+              l2 = -INFINITY;
               Di = 0.0f;
             }
           }
@@ -634,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
           load_res();
           __syncwarp();
         }
-        if (lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv);
+        if (lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
         if (++tile == first + per) {
           tile = first;
           ++sub;
@@ -646,92 +662,96 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       it = next;
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
-      const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
-      auto sQ = [&](int pos) { return smem_u32(smem + L::kQ) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
-      auto sdO = [&](int pos) { return smem_u32(smem + L::kDO) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
-      auto issue_s = [&](int pos) {
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
+    const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+    auto sQ = [&](int pos) { return smem_u32(smem + L::kQ) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
+    auto sdO = [&](int pos) { return smem_u32(smem + L::kDO) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
+    auto issue_s = [&](int pos) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + L::s_col(pos), kmajor_desc(sK, kk), kmajor_desc(sQ(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
-      };
-      auto issue_dp = [&](int pos) {
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_ss(tmem + L::s_col(pos), kmajor_desc(sK, kk), kmajor_desc(sQ(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+      umma_commit(L::s_full(bars, pos));
+    };
+    auto issue_dp = [&](int pos) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + L::kDPCol, kmajor_desc(sV, kk), kmajor_desc(sdO(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
-      };
-      auto full = [&](int pos, uint32_t code) {
-        return wait(&bars->a_full[pos % L::kRing], (pos / L::kRing) & 1, bars, code);
-      };
-      int sb = 0, tl = 0;
-      for (int t = 0;; ++t) {
-        const int r = t % kPackedRing;
-        if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x207)) break;
-        const PackedItem it = bars->item[r];
-        mbar_arrive(&bars->item_empty[r]);
-        if (it.head < 0) break;
-        const int n = dk_tiles(it, p.TT, CAUSAL) * p.per_kv;
-        if (n == 0) continue;
-        bool ok = wait(&bars->res_full, tl & 1, bars, 0x201) && full(sb, 0x202);
-        if (!ok) break;
-        tc_fence_after_sync();
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_ss(tmem + L::kDPCol, kmajor_desc(sV, kk), kmajor_desc(sdO(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+      umma_commit(&bars->dp_full[0]);
+    };
+    auto full = [&](int pos, uint32_t code) {
+      return warp_wait(&bars->a_full[pos % L::kRing], (pos / L::kRing) & 1, bars, code);
+    };
+    int sb = 0, tl = 0;
+    for (int t = 0;; ++t) {
+      const int r = t % kPackedRing;
+      if (!warp_wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x207)) break;
+      const PackedItem it = bars->item[r];
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&bars->item_empty[r]);
+      if (uniform(it.head) < 0) break;
+      const int n = uniform(dk_tiles(it, p.TT, CAUSAL)) * p.per_kv;
+      if (n == 0) continue;
+      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x201) || !full(sb, 0x202)) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
         issue_s(sb);
-        umma_commit(&bars->s_full[L::s_buf(sb)]);
         issue_dp(sb);
-        umma_commit(&bars->dp_full);
-        for (int j = 0; j < n; ++j) {
-          const int pos = sb + j;
-          const bool more = j + 1 < n;
-          if (L::kDouble && more) {
-            if (!(ok = full(pos + 1, 0x208))) break;
-            tc_fence_after_sync();
-            issue_s(pos + 1);
-            umma_commit(&bars->s_full[L::s_buf(pos + 1)]);
-          }
-          // dV += P^T dO_j (A = P^T bf16 in tensor memory over S^T); an item's first overwrites the
-          // accumulators that the epilogue before it reads
-          if (!(ok = wait(&bars->s_free[L::s_buf(pos)], L::s_par(pos), bars, 0x203) &&
-                     (j > 0 || tl == 0 || wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206))))
-            break;
-          const bool next_in =
-              L::kDouble || !more || mbar_test_wait(&bars->a_full[(pos + 1) % L::kRing], ((pos + 1) / L::kRing) & 1);
+      }
+      __syncwarp();
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int pos = sb + j;
+        const bool more = j + 1 < n;
+        if (L::kDouble && more) {
+          if (!(ok = full(pos + 1, 0x208))) break;
           tc_fence_after_sync();
+          if (elect_one()) issue_s(pos + 1);
+          __syncwarp();
+        }
+        // dV += P^T dO_j (A = P^T bf16 in tensor memory over S^T); an item's first overwrites the
+        // accumulators that the epilogue before it reads
+        if (!(ok = warp_wait(L::p_ready(bars, pos), L::s_par(pos), bars, 0x203) &&
+                   (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206))))
+          break;
+        tc_fence_after_sync();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_ts(tmem + L::kAcc0, tmem + L::s_col(pos) + packed_a_col(kk), mnmajor_desc(sdO(pos), kk), idesc_acc,
                     (j > 0 || kk > 0) ? 1u : 0u);
-          if (!L::kDouble && more) {
-            if (!next_in) {
-              if (!(ok = full(pos + 1, 0x205))) break;
-              tc_fence_after_sync();
-            }
-            issue_s(pos + 1);
-          }
-          // dK += dS^T Q_j
-          const bool ds_in = mbar_test_wait(&bars->ds_ready, pos & 1);
-          if (!L::kDouble && more) umma_commit(&bars->s_full[0]);
-          if (!ds_in && !(ok = wait(&bars->ds_ready, pos & 1, bars, 0x204))) break;
+        }
+        __syncwarp();
+        if (!L::kDouble && more) {
+          if (!(ok = full(pos + 1, 0x205))) break;
           tc_fence_after_sync();
+          if (elect_one()) issue_s(pos + 1);
+          __syncwarp();
+        }
+        // dK += dS^T Q_j
+        if (!(ok = warp_wait(&bars->ds_ready[0], pos & 1, bars, 0x204))) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_ts(tmem + L::kAcc1, tmem + L::kDPCol + packed_a_col(kk), mnmajor_desc(sQ(pos), kk), idesc_acc,
                     (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&bars->a_empty[pos % L::kRing]);
-          if (more) {
-            issue_dp(pos + 1);
-            umma_commit(&bars->dp_full);
-          }
+          if (more) issue_dp(pos + 1);
         }
-        if (!ok) break;
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) {
         umma_commit(&bars->acc_done);
         umma_commit(&bars->res_empty);
-        sb += n;
-        ++tl;
       }
-      umma_commit(&bars->drain);
+      sb += n;
+      ++tl;
     }
+    __syncwarp();
+    if (elect_one()) umma_commit(&bars->drain);
     __syncwarp();
   } else {
     const int g = threadIdx.x >> 7;    // half of the query columns
@@ -767,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
         const int step = nb + j;
         const float* lse2_s = reinterpret_cast<const float*>(smem + L::kVec) + (step % L::kRing) * 256;
         const float* D_s = lse2_s + 128;
-        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x301))) break;
+        if (!(ok = warp_wait(L::s_full(bars, step), L::s_par(step), bars, 0x301))) break;
         tc_fence_after_sync();
         uint32_t pr[64];
         tmem_ld64(tmem + lane_off + L::s_col(step) + col0, pr);
@@ -780,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int c = 4 * c4 + 2 * h;
-              const float2 nl = h ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y);
+              const float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
               const float2 x = __ffma2_rn(
                   make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])), sc2, nl);
               float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
@@ -807,8 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->s_free[L::s_buf(step)]);
-        if (!(ok = warp_wait(&bars->dp_full, step & 1, bars, 0x306))) break;
+        mbar_arrive(L::p_ready(bars, step));
+        if (!(ok = warp_wait(&bars->dp_full[0], step & 1, bars, 0x306))) break;
         tc_fence_after_sync();
 #pragma unroll
         for (int c2 = 0; c2 < 2; ++c2) {
@@ -824,11 +844,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
             const float2 ds01 = __fmul2_rn(
                 make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])),
                 __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4]), __uint_as_float(rr[4 * e4 + 1])),
-                           make_float2(-dd.x, -dd.y)));
+                           make_float2(dd.x, dd.y)));
             const float2 ds23 = __fmul2_rn(
                 make_float2(__uint_as_float(pr[c + 2]), __uint_as_float(pr[c + 3])),
                 __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4 + 2]), __uint_as_float(rr[4 * e4 + 3])),
-                           make_float2(-dd.z, -dd.w)));
+                           make_float2(dd.z, dd.w)));
             w[2 * e4] = pack_bf16x2(ds01.x, ds01.y);
             w[2 * e4 + 1] = pack_bf16x2(ds23.x, ds23.y);
           }
@@ -836,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->ds_ready);
+        mbar_arrive(&bars->ds_ready[0]);
         if (++tile == first + per) tile = first;
       }
       if (!ok || !warp_wait(&bars->acc_done, tl & 1, bars, 0x302)) break;
@@ -876,12 +896,14 @@ cudaError_t launch_after(Kern kern, const BwdParams& p, unsigned blocks, uint32_
 }
 
 template <int D, bool CAUSAL>
-cudaError_t launch_t(BwdParams p, const PackedEntry* const list[2], unsigned dq_blocks, unsigned dk_blocks,
-                     cudaStream_t s) {
+cudaError_t launch_t(BwdParams p, const PackedEntry* const list[2], const int chunk[2], unsigned dq_blocks,
+                     unsigned dk_blocks, cudaStream_t s) {
   p.list = list[0];
+  p.chunk = chunk[0];
   const cudaError_t e = launch_after(fa_packed_dq_kernel<D, CAUSAL>, p, dq_blocks, DqLayout<D>::kSmem, s);
   if (e != cudaSuccess) return e;
   p.list = list[1];
+  p.chunk = chunk[1];
   return launch_after(fa_packed_dkdv_kernel<D, CAUSAL>, p, dk_blocks, DkLayout<D>::kSmem, s);
 }
 
@@ -915,13 +937,16 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   const PackedEntry* const list[2] = {reinterpret_cast<const PackedEntry*>(ws + l.list[0]),
                                       reinterpret_cast<const PackedEntry*>(ws + l.list[1])};
+  // the dq kernel streams keys and values, the other the queries and dO of a group's heads
+  const int chunk[2] = {packed_chunk(a.total_k, a.d, Hkv) * t.per_kv,
+                        packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv)};
   const long long q_items = a.total_q > 0 ? (a.total_q / t.TT + a.B) * static_cast<long long>(t.heads) : 0;
   const long long k_items = a.total_k > 0 ? (a.total_k / 128 + a.B) * static_cast<long long>(Hkv) : 0;
   const unsigned nq = static_cast<unsigned>(std::min<long long>(q_items, a.num_sms));
   const unsigned nk = static_cast<unsigned>(std::min<long long>(k_items, a.num_sms));
   if (a.d == 64)
-    return a.causal ? launch_t<64, true>(p, list, nq, nk, s) : launch_t<64, false>(p, list, nq, nk, s);
-  return a.causal ? launch_t<128, true>(p, list, nq, nk, s) : launch_t<128, false>(p, list, nq, nk, s);
+    return a.causal ? launch_t<64, true>(p, list, chunk, nq, nk, s) : launch_t<64, false>(p, list, chunk, nq, nk, s);
+  return a.causal ? launch_t<128, true>(p, list, chunk, nq, nk, s) : launch_t<128, false>(p, list, chunk, nq, nk, s);
 }
 
 cudaError_t packed_bwd_read_clear_error(uint32_t* out, cudaStream_t s) {
