@@ -662,7 +662,7 @@ static int view_heads(const fa_heads* t, int heads, long long B, long long T, in
   return FA_OK;
 }
 
-// Key or value rows as (d, tokens, heads), boxes of 64 columns x 128 tokens; query rows
+// Key or value rows as (d, tokens, heads), boxes of 64 columns x TT tokens; query rows
 // as (d, P, tokens, head groups of P), boxes of 64 columns x P heads x TT tokens.  128-byte
 // swizzle.  A tensor of no tokens gets a map that is never read through.
 static int encode_rows(CUtensorMap* map, const fa::HeadsView& t, int tokens, int d, int P, int TT,
@@ -674,7 +674,7 @@ static int encode_rows(CUtensorMap* map, const fa::HeadsView& t, int tokens, int
   const bool q = P > 0;
   cuuint64_t kdims[3] = {static_cast<cuuint64_t>(d), n, static_cast<cuuint64_t>(t.heads)};
   cuuint64_t kstrides[2] = {token, head};
-  cuuint32_t kbox[3] = {fa::kBoxCols, 128, 1};
+  cuuint32_t kbox[3] = {fa::kBoxCols, static_cast<cuuint32_t>(TT), 1};
   cuuint64_t qdims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(P), n,
                          static_cast<cuuint64_t>(q ? t.heads / P : 1)};
   cuuint64_t qstrides[3] = {head, token, head * static_cast<cuuint64_t>(P)};
@@ -693,10 +693,11 @@ static int encode_rows(CUtensorMap* map, const fa::HeadsView& t, int tokens, int
 static int packed_maps(const fa::PackedArgs& a, bool backward, CUtensorMap maps[4]) {
   const fa::PackedTiling t = fa::packed_tiling(a.q.heads, a.k.heads);
   const void* any = a.workspace;
-  int st = encode_rows(&maps[0], a.q, a.total_q, a.d, t.P, t.TT, any);
-  if (st == FA_OK) st = encode_rows(&maps[1], a.k, a.total_k, a.d, 0, 0, any);
-  if (st == FA_OK) st = encode_rows(&maps[2], a.v, a.total_k, a.d, 0, 0, any);
-  if (st == FA_OK && backward) st = encode_rows(&maps[3], a.dO, a.total_q, a.d, t.P, t.TT, any);
+  const int tokens = backward ? t.TT64 : t.TT, keys = backward ? 64 : 128;
+  int st = encode_rows(&maps[0], a.q, a.total_q, a.d, t.P, tokens, any);
+  if (st == FA_OK) st = encode_rows(&maps[1], a.k, a.total_k, a.d, 0, keys, any);
+  if (st == FA_OK) st = encode_rows(&maps[2], a.v, a.total_k, a.d, 0, keys, any);
+  if (st == FA_OK && backward) st = encode_rows(&maps[3], a.dO, a.total_q, a.d, t.P, tokens, any);
   return st;
 }
 

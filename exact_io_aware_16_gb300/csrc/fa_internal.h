@@ -199,11 +199,11 @@ struct PackedArgs {
   int num_sms;
 };
 
-// Heads of a group whose rows share a tile: all of them, or the largest divisor of
-// their number up to 16 (a tile of 128 rows then holds 8 tokens or more).
+// Heads of a group whose rows share a tile: the largest divisor of their number up to 16 whose
+// tokens fill 56 of 64 rows or more (a tile of 128 rows then holds 8 tokens or more).
 inline int packed_heads(int G) {
   int p = G < 16 ? G : 16;
-  while (G % p) --p;
+  while (G % p != 0 || 64 / p * p < 56) --p;
   return p;
 }
 

@@ -49,7 +49,7 @@ __device__ __forceinline__ int bucket_of(const PackedPlanArgs& a, int which, con
   } else {
     // the first query that sees the tile's first key
     const int first = a.causal ? max(t * 128 - (s.m - s.n), 0) : 0;
-    cost = s.n > first ? (s.n + a.TT - 1) / a.TT - first / a.TT : 0;
+    cost = s.n > first ? (s.n + a.TT64 - 1) / a.TT64 - first / a.TT64 : 0;
   }
   return min(cost >> a.shift[which], kBuckets - 1);
 }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
 static_assert(kBuckets == kPlanThreads, "one bucket a thread in the scan");
 
 // ============================================================ forward
-constexpr int kFwdThreads = 320;
+constexpr int kFwdThreads = 352;  // two softmax warpgroups, a TMA and two MMA warps
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kStages = 2;
@@ -188,6 +188,7 @@ struct FwdBars {
   uint64_t s_full[2], p_ready[2], pv_done[2];
   uint64_t q_empty;    // the S products of an item are done with the Q tiles
   uint64_t item_full[kPackedRing], item_empty[kPackedRing];
+  uint64_t turn[2];    // the other tile's products of a step are issued
   uint64_t o_free[2];  // softmax warpgroup g has read its O for the epilogue
   uint64_t drain;
   uint32_t tmem_base;
@@ -244,22 +245,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     mbar_init(&bars->q_full, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->k_empty[s], 2);  // the two MMA warps
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->v_empty[s], 2);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&bars->s_full[g], 1);
       mbar_init(&bars->p_ready[g], 128);
       mbar_init(&bars->pv_done[g], 1);
       mbar_init(&bars->o_free[g], 128);
+      mbar_init(&bars->turn[g], 1);
     }
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, 2);
     for (int r = 0; r < kPackedRing; ++r) {
       mbar_init(&bars->item_full[r], 1);
-      mbar_init(&bars->item_empty[r], 257);  // the softmax threads and the MMA thread
+      mbar_init(&bars->item_empty[r], 258);  // the softmax threads and the MMA warps
     }
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, 2);
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_packed_error) != 0) ? 1 : 0;
     fence_mbar_init();
   }
@@ -352,38 +354,48 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------ MMA issuer
-    // The whole warp runs the loop on values that are the same in all lanes, so that descriptors
-    // lie in uniform registers, where the instruction wants them; one elected lane issues.
-    // (By one lane in a divergent branch each product took 100 cycles to issue, of 64 that
-    // it runs.)
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------------------------ MMA issuers, one a query tile
+    // Issuing is what the tensor core waited for: 8 products take 210 to 290 cycles to issue, a
+    // commit 50, a wait that is over 70, against 512 cycles that 8 products of 128 columns run.
+    // So each query tile has a warp of its own, which waits while the other issues; they take
+    // turns, because products of both in flight at once would end later for both, and their
+    // softmaxes would meet.  The whole warp runs the loop on values that are the same in all
+    // lanes, so that descriptors lie in uniform registers, where the instruction wants them;
+    // one elected lane issues.
+    const int g = warp - kMmaWarp;
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
-    const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+    const uint32_t tm = uniform(tmem), sc = tm + uniform(L::s_col(g)), oc = tm + uniform(L::o_col(g));
+    const uint32_t qbase = uniform(smem_u32(smem + L::kQ) + g * L::kTileBytes);
+    const uint32_t sK = uniform(smem_u32(smem + L::kK)), sV = uniform(smem_u32(smem + L::kV));
     auto wait = [&](uint64_t* bar, uint32_t par, uint32_t code) { return all_wait(bar, par, bars, code); };
-    auto issue_s = [&](int g, int pos) {
-      const uint32_t kbase = sK + ring_slot(pos) * L::kTileBytes, qbase = sQ + g * L::kTileBytes;
+    auto issue_s = [&](int slot) {
+      const uint32_t kbase = sK + slot * L::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-        umma_ss(tmem + L::s_col(g), sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + off, 16, 1024),
-                idesc_qk, kk > 0 ? 1u : 0u);
+        umma_ss(sc, sdesc_sw128(qbase + off, 16, 1024), sdesc_sw128(kbase + off, 16, 1024), idesc_qk,
+                kk > 0 ? 1u : 0u);
       }
       umma_commit(&bars->s_full[g]);
+      umma_commit(&bars->k_empty[slot]);
     };
-    auto issue_pv = [&](int g, int pos, bool first) {
-      const uint32_t vbase = sV + ring_slot(pos) * L::kTileBytes;
+    auto issue_pv = [&](int slot, bool first) {
+      const uint32_t vbase = sV + slot * L::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        umma_ts(tmem + L::o_col(g), tmem + L::s_col(g) + kk * 8, sdesc_sw128(vbase + kk * 2048, 16384, 1024),
-                idesc_pv, (!first || kk > 0) ? 1u : 0u);
-      umma_commit(&bars->pv_done[g]);
+        umma_ts(oc, sc + kk * 8, sdesc_sw128(vbase + kk * 2048, 16384, 1024), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+      umma_commit(&bars->v_empty[slot]);
     };
-    // Order of the products for key tile j: PV0_j, S0_{j+1}, PV1_j, S1_{j+1}, each pair a burst
-    // with the waits for all that it reads ahead of it.  A tile may have no work in an
-    // item (it lies behind the sequence, or sees no key), or end before the other.
-    int kvb = 0, tl = 0, base0 = 0, base1 = 0, used0 = 0, used1 = 0;
+    // For key tile j: PV_j and S_{j+1}.  A query tile may have no work in an item (it lies
+    // behind the sequence, or sees no key), or end before the other: it then gives the
+    // copied tiles back unread.
+    int kvb = 0, tl = 0, base = 0, used = 0, turns = 0;
+    auto turn = [&]() {  // (the first tile's warp goes first)
+      const uint32_t par = static_cast<uint32_t>(turns++ & 1) ^ (g == 0 ? 1u : 0u);
+      return wait(&bars->turn[g], par, 0x20c);
+    };
     for (int t = 0;; ++t) {
       const int r = t % kPackedRing;
       if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, 0x20b)) break;
@@ -391,61 +403,50 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       __syncwarp();
       if (elect_one()) mbar_arrive(&bars->item_empty[r]);
       if (uniform(it.head) < 0) break;
-      const int n0 = uniform(item_tiles(it, 0, p.TT, CAUSAL)), n1 = uniform(item_tiles(it, 1, p.TT, CAUSAL));
-      const int nmax = max(n0, n1);
+      const int n = uniform(item_tiles(it, g, p.TT, CAUSAL));
+      const int nmax = max(n, uniform(item_tiles(it, 1 - g, p.TT, CAUSAL)));
       if (nmax == 0) continue;
-      if (!wait(&bars->q_full, tl & 1, 0x201) || !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202)) break;
+      if (!wait(&bars->q_full, tl & 1, 0x201) || !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202) || !turn())
+        break;
       tc_fence_after_sync();
       if (elect_one()) {
-        if (n0 > 0) issue_s(0, kvb);
-        if (n1 > 0) issue_s(1, kvb);
-        umma_commit(&bars->k_empty[ring_slot(kvb)]);
+        if (n > 0)
+          issue_s(ring_slot(kvb));
+        else
+          mbar_arrive(&bars->k_empty[ring_slot(kvb)]);
+        mbar_arrive(&bars->turn[1 - g]);
       }
       __syncwarp();
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < nmax; ++j) {
         const int pos = kvb + j, s = ring_slot(pos), sn = ring_slot(pos + 1);
-        const uint32_t ph = ring_phase(pos), phn = ring_phase(pos + 1);
-        if (j < n0) {
-          ok = wait(&bars->p_ready[0], (base0 + j) & 1, 0x203) && wait(&bars->v_full[s], ph, 0x204) &&
-               (j > 0 || used0 == 0 || wait(&bars->o_free[0], (used0 - 1) & 1, 0x209)) &&
-               (j + 1 >= nmax || wait(&bars->k_full[sn], phn, 0x205));
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (elect_one()) {
-            issue_pv(0, pos, j == 0);
-            if (j + 1 < n0) issue_s(0, pos + 1);
-            if (j >= n1) {
-              umma_commit(&bars->v_empty[s]);
-              if (j + 1 < nmax) umma_commit(&bars->k_empty[sn]);
-            }
-          }
-          __syncwarp();
+        ok = wait(&bars->v_full[s], ring_phase(pos), 0x204) &&
+             (j > 0 || n == 0 || used == 0 || wait(&bars->o_free[g], (used - 1) & 1, 0x209)) &&
+             (j + 1 >= nmax || wait(&bars->k_full[sn], ring_phase(pos + 1), 0x205)) &&
+             (j >= n || wait(&bars->p_ready[g], (base + j) & 1, 0x203)) && turn();
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          if (j < n)
+            issue_pv(s, j == 0);
+          else
+            mbar_arrive(&bars->v_empty[s]);
+          if (j + 1 == n) umma_commit(&bars->pv_done[g]);
+          if (j + 1 < n)
+            issue_s(sn);
+          else if (j + 1 < nmax)
+            mbar_arrive(&bars->k_empty[sn]);
+          mbar_arrive(&bars->turn[1 - g]);
         }
-        if (j < n1) {
-          ok = wait(&bars->p_ready[1], (base1 + j) & 1, 0x206) && (j < n0 || wait(&bars->v_full[s], ph, 0x207)) &&
-               (j > 0 || used1 == 0 || wait(&bars->o_free[1], (used1 - 1) & 1, 0x20a)) &&
-               (j < n0 || j + 1 >= nmax || wait(&bars->k_full[sn], phn, 0x208));
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (elect_one()) {
-            issue_pv(1, pos, j == 0);
-            umma_commit(&bars->v_empty[s]);
-            if (j + 1 < n1) issue_s(1, pos + 1);
-            if (j + 1 < nmax) umma_commit(&bars->k_empty[sn]);
-          }
-          __syncwarp();
-        }
+        __syncwarp();
       }
       if (!ok) break;
       if (elect_one()) umma_commit(&bars->q_empty);
       kvb += nmax;
       ++tl;
-      base0 += n0;
-      base1 += n1;
-      used0 += n0 > 0;
-      used1 += n1 > 0;
+      base += n;
+      used += n > 0;
     }
     __syncwarp();
     if (elect_one()) umma_commit(&bars->drain);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     const int row_tok = t / p.P, row_head = t - row_tok * p.P;
     const bool row_in = row_tok < p.TT;
     auto warp_wait = [&](uint64_t* bar, uint32_t par, uint32_t code) { return all_wait(bar, par, bars, code); };
-    int tb = 0;  // key tiles of earlier items
+    int tb = 0, used = 0;  // key tiles of earlier items, and items with any
     for (int ti = 0;; ++ti) {
       const int r = ti % kPackedRing;
       if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, 0x304)) break;
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         continue;
       }
       tb += nkv;
-      if (!warp_wait(&bars->pv_done[g], (tb - 1) & 1, 0x303)) break;
+      if (!warp_wait(&bars->pv_done[g], used++ & 1, 0x303)) break;
       tc_fence_after_sync();
       const float inv_l = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? 0.0f : l_run);
       // rows of this lane's 4-lane group are stored together, row by row
@@ -666,13 +667,13 @@ cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int
   p.total_q = a.total_q;
   p.total_k = a.total_k;
   p.causal = a.causal;
-  p.q_span = backward ? t.TT : 2 * t.TT;
-  p.TT = t.TT;
+  p.q_span = 2 * (backward ? t.TT64 : t.TT);
+  p.TT64 = t.TT64;
   p.nlists = backward ? 2 : 1;
   p.most[0] = static_cast<unsigned>(a.total_q / p.q_span + a.B);
   p.most[1] = static_cast<unsigned>(a.total_k / 128 + a.B);
   p.shift[0] = bucket_shift(a.total_k / 128 + 1);
-  p.shift[1] = bucket_shift(a.total_q / t.TT + 1);
+  p.shift[1] = bucket_shift(a.total_q / t.TT64 + 1);
   p.header = reinterpret_cast<PackedHeader*>(ws);
   p.maps = reinterpret_cast<CUtensorMap*>(ws + l.maps);
   for (int i = 0; i < 2; ++i) p.list[i] = reinterpret_cast<PackedEntry*>(ws + l.list[i]);

@@ -3,10 +3,11 @@
 // the persistent CTAs take their work from it.
 //
 // Tiles.  A key head serves G query heads, whose rows need the same keys.  A query tile
-// of 128 rows therefore holds P heads of 128 / P tokens (P = packed_heads(G): all of the
-// group where it has up to 16): row r is token r / P, head r % P.  Keys and values are
-// then read once for all of them, and a sequence of few tokens fills a tile with its
-// heads.  Rows that P does not fill (126 of 128 for P = 7) are zero in shared memory.
+// of 128 rows therefore holds P heads of 128 / P tokens (P = packed_heads(G), mostly all of the
+// group): row r is token r / P, head r % P.  Keys and values are then read once for all
+// of them, and a sequence of few tokens fills a tile with its heads.  Rows that P does
+// not fill (126 of 128 for P = 7) are zero or not stored.  The backward pass takes query rows
+// in boxes of 64 rows, and its 128-row tile is two of them.
 //
 // Tensor maps.  Every sequence has its own, whose extent ends where the sequence does:
 // what lies behind reads as zeros, so that neither NaN nor infinities of a
@@ -44,9 +45,10 @@ struct PackedHeader {
 
 // How a call's heads and tokens fill tiles.
 struct PackedTiling {
-  int P;      // query heads a tile
-  int TT;     // query tokens a tile
-  int heads;  // head groups of P query heads
+  int P;       // query heads a tile
+  int TT;      // query tokens a tile of the forward kernel
+  int TT64;    // query tokens in 64 rows (backward)
+  int heads;   // head groups of P query heads
   int per_kv;  // of them, those of one key head
 };
 
@@ -55,6 +57,7 @@ inline PackedTiling packed_tiling(int Hq, int Hkv) {
   const int G = Hq / Hkv;
   t.P = packed_heads(G);
   t.TT = 128 / t.P;
+  t.TT64 = 64 / t.P;
   t.heads = Hq / t.P;
   t.per_kv = G / t.P;
   return t;
@@ -80,8 +83,8 @@ inline PackedLayout packed_layout(int B, int total_q, int total_k, int Hq, int H
   l.maps = 256;
   const size_t b = static_cast<size_t>(B);
   l.list[0] = l.maps + up(b * (backward ? 4 : 3) * 128);
-  // a forward item is two query tiles, a backward one one
-  const size_t q_tiles = static_cast<size_t>(total_q) / (backward ? t.TT : 2 * t.TT) + b;
+  // a forward item is two query tiles, a backward one two boxes of 64 rows
+  const size_t q_tiles = static_cast<size_t>(total_q) / (2 * (backward ? t.TT64 : t.TT)) + b;
   l.list[1] = l.list[0] + up(q_tiles * sizeof(PackedEntry));
   const size_t k_tiles = backward ? static_cast<size_t>(total_k) / 128 + b : 0;
   l.D = l.list[1] + up(k_tiles * sizeof(PackedEntry));
@@ -99,7 +102,7 @@ struct PackedPlanArgs {
   int B, total_q, total_k;
   int causal;
   int q_span;   // query tokens an entry of list 0
-  int TT;       // query tokens a tile (costs of list 1)
+  int TT64;     // query tokens in 64 rows (costs of list 1)
   int nlists;
   unsigned most[2];  // entries the lists have room for
   int shift[2];      // cost to bucket

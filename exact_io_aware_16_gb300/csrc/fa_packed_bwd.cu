@@ -4,19 +4,26 @@
 //   dQ = scale dS K,  dK = scale sum_heads dS^T Q,  dV = sum_heads P^T dO.
 //
 // Two kernels over the tiles of fa_packed.cuh, each bound by the tensor core:
-//   * dq: a query tile's Q and dO stay in shared memory while keys and values stream;
-//     three products a tile (S, dP, dQ).  It also finds D, for itself and for the next.
-//   * dk, dv: a key tile's K and V stay while the query tiles of all heads of the group
-//     stream, so that the sums over a group's heads are sums in tensor memory, in a
-//     fixed order and without atomics; four products a tile (S^T, dP^T, dV, dK).
-//     Scores are computed transposed: a thread owns a key.
+//   * dq: 128 query rows stay while 64-row key and value tiles stream; three products a
+//     tile (S, dP, dQ).  It also finds D, for itself and for the next.
+//   * dk, dv: 128 keys stay while 64-row query tiles of all heads of the group stream, so
+//     that the sums over a group's heads are sums in tensor memory, in a fixed order and
+//     without atomics; four products a tile (S^T, dP^T, dV, dK).  Scores are computed
+//     transposed: a thread owns a key.
 // Together seven products where five would do: S and dP are computed twice, which costs
 // less than adding dQ up over key tiles in memory (64 KB a tile pair), and leaves
 // no order to chance.
 //
+// Operands.  A product of two operands in shared memory reads 8 KB for each 64 cycles of
+// the tensor core, all that shared memory delivers; with the tiles' copies it fell behind by
+// a third.  What stays therefore lies in tensor memory, copied there by the compute threads
+// from where TMA put it, as P and dS do: every product reads one operand from shared memory,
+// at half its rate.  (Products of 64 columns run at full rate that way, 33.8 cycles of 32;
+// from shared memory 49.)
+//
 // D from the bf16 o is off by up to half a bf16 step of it.  Where a query sees many keys
 // that is below the rounding of dS; where it sees few, dS may be small against D
-// (a query's own key alone: zero).  Query tiles that see one key tile therefore take
+// (a query's own key alone: zero).  Query tiles that see 64 keys or fewer therefore take
 // D = sum_j P_ij dP_ij, which their threads have in registers before dS is needed.
 #include <algorithm>
 #include <cstdint>
@@ -34,7 +41,7 @@ namespace {
 
 __device__ unsigned int g_packed_bwd_error;
 
-constexpr int kThreads = 320;  // two compute warpgroups, TMA warp, MMA warp
+constexpr int kThreads = 352;  // two compute warpgroups, a TMA and two MMA warps
 constexpr int kCompute = 256;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
@@ -53,27 +60,32 @@ struct BwdParams {
   __nv_bfloat16* dv;
   long long o_token, o_head, dO_token, dO_head, dq_token, dq_head, dk_token, dk_head, dv_token, dv_head;
   int total_q;
-  int P, TT, heads, per_kv, Hkv, chunk;
+  int P, TT, TT64, heads, per_kv, Hkv, chunk;  // TT64: query tokens in 64 rows, TT: in two such boxes
   float scale, scale_log2;
 };
 
-// Barriers of both kernels (the dq kernel's rings are apart: a key tile is needed longer than
-// a value tile; the other's q and dO tiles share a ring).
+constexpr int kBwdRing = 2;  // items in flight between the roles of a CTA
+constexpr int kStages = 5;  // of 64 streamed rows of two tensors
+constexpr uint32_t kBarBytes = 512;
+
+// Barriers of both kernels.  The two halves of a stage have barriers of their own in the dq
+// kernel, where a key tile is needed longer than a value tile.
 struct BwdBars {
-  uint64_t res_full, res_empty;
-  uint64_t a_full[4], a_empty[4];  // dq: key tiles; dk, dv: query tiles with their dO
-  uint64_t b_full[4], b_empty[4];  // dq: value tiles
-  uint64_t s_full, s_full_1;  // scores computed (of buffer 1)
-  uint64_t s_free, s_free_1;  // and read by all threads (dq), or P written over them (dk, dv)
-  uint64_t dp_full[2], ds_ready[2], dx_ready;
-  uint64_t acc_done, acc_free;
-  uint64_t item_full[kPackedRing], item_empty[kPackedRing];
+  uint64_t res_full, res_empty;  // what stays: copied to shared memory; read from there
+  uint64_t a_ready;              // and written to tensor memory
+  uint64_t x_full[kStages], x_empty[kStages];
+  uint64_t y_full[kStages], y_empty[kStages];
+  uint64_t s_full[2], s_done[2];  // scores computed; read (dq), or P written over them (dk, dv)
+  uint64_t dp_full[2], ds_ready[2];
+  uint64_t dx_ready, acc_done, acc_free;
+  uint64_t turn[2];  // the other MMA warp's products of a step are issued
+  uint64_t item_full[kBwdRing], item_empty[kBwdRing];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  PackedItem item[kPackedRing];
+  PackedItem item[kBwdRing];
 };
-static_assert(sizeof(BwdBars) <= 768, "barrier block overruns its shared memory");
+static_assert(sizeof(BwdBars) <= kBarBytes, "barrier block overruns its shared memory");
 
 // A wait's loop out of line: the code of the kernels stays small.
 __device__ __noinline__ bool wait_loop(uint64_t* bar, uint32_t par, BwdBars* b, uint32_t code) {
@@ -95,32 +107,37 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 
 // Barriers and tensor memory; rows of [zero, zero + bytes) that no box fills are zeroed.
 // Returns false (for the whole CTA) when an earlier CTA recorded a timeout.
-__device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, uint8_t* zero, uint32_t bytes) {
+// `users`: MMA warps whose products read a stage, and which write an accumulator.
+__device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t* smem, uint8_t* zero,
+                                         uint32_t bytes, int users) {
   if (threadIdx.x == 0) {
+    // the swizzle of tiles counts from 1024-byte boundaries
+    if ((smem_u32(smem) & 1023u) != 0) atomicCAS(&g_packed_bwd_error, 0u, kDevTimeoutMask | 0x3ffu);
     mbar_init(&bars->res_full, 1);
-    mbar_init(&bars->res_empty, 1);
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&bars->a_full[s], 1);
-      mbar_init(&bars->a_empty[s], 1);
-      mbar_init(&bars->b_full[s], 1);
-      mbar_init(&bars->b_empty[s], 1);
+    mbar_init(&bars->res_empty, kCompute);
+    mbar_init(&bars->a_ready, kCompute);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->x_full[s], 1);
+      mbar_init(&bars->x_empty[s], users);
+      mbar_init(&bars->y_full[s], 1);
+      mbar_init(&bars->y_empty[s], 1);
     }
-    mbar_init(&bars->s_full, 1);
-    mbar_init(&bars->s_full_1, 1);
-    mbar_init(&bars->s_free, kCompute);
-    mbar_init(&bars->s_free_1, kCompute);
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_done[b], kCompute);
       mbar_init(&bars->dp_full[b], 1);
       mbar_init(&bars->ds_ready[b], kCompute);
     }
+    mbar_init(&bars->turn[0], 1);
+    mbar_init(&bars->turn[1], 1);
     mbar_init(&bars->dx_ready, kCompute);
-    mbar_init(&bars->acc_done, 1);
+    mbar_init(&bars->acc_done, users);
     mbar_init(&bars->acc_free, kCompute);
-    for (int r = 0; r < kPackedRing; ++r) {
+    for (int r = 0; r < kBwdRing; ++r) {
       mbar_init(&bars->item_full[r], 1);
-      mbar_init(&bars->item_empty[r], kCompute + 1);  // compute threads and the MMA thread
+      mbar_init(&bars->item_empty[r], kCompute + 2);  // compute threads and the MMA warps
     }
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, 2);
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_packed_bwd_error) != 0) ? 1 : 0;
     fence_mbar_init();
   }
@@ -157,23 +174,22 @@ __device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t t
   }
 }
 
-// K-major operand descriptor for k-step kk of a [128 rows][D] swizzled tile.
+// K-major operand descriptor for k-step kk of a [64 rows][D] swizzled tile.
 __device__ __forceinline__ uint64_t kmajor_desc(uint32_t base, int kk) {
-  return sdesc_sw128(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
+  return sdesc_sw128(base + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024);
 }
-// MN-major operand descriptor (rows of the tile are the K dimension) for k-step kk.
+// MN-major operand descriptor (the tile's 64 rows are the K dimension) for k-step kk.
 __device__ __forceinline__ uint64_t mnmajor_desc(uint32_t base, int kk) {
-  return sdesc_sw128(base + kk * 2048, 16384, 1024);
+  return sdesc_sw128(base + kk * 2048, 8192, 1024);
 }
 // Tensor-memory column of k-step kk (16 score columns) of a bf16 operand packed inside the two
-// 64-column halves of a 128-column fp32 region, each in its half's first 32 columns.
+// 32-column halves of a 64-column fp32 region, each in its half's first 16 columns.
 __device__ __forceinline__ uint32_t packed_a_col(int kk) {
-  return static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8);
+  return static_cast<uint32_t>((kk >> 1) * 32 + (kk & 1) * 8);
 }
 
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&r)[64]) {
-  tmem_ld32(addr + 0, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-  tmem_ld32(addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) {
+  tmem_ld32(addr, r);
   tmem_ld_wait();
   reg_pin(r);
 }
@@ -186,6 +202,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&w)[16]
       "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]),
       "r"(w[15])
       : "memory");
+}
+
+// Half of row tr of a [128 rows][D] swizzled tile in shared memory (zeros unless `valid`), as it
+// lies in registers and, packed as a product's A operand, in tensor memory.
+template <int D>
+__device__ __forceinline__ void load_half_row(const uint8_t* tile, int tr, int half, bool valid,
+                                              uint32_t (&w)[D / 4]) {
+#pragma unroll
+  for (int e = 0; e < D / 16; ++e) {
+    const int c = half * (D / 16) + e;  // 16-byte chunk of the row
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (valid)
+      x = *reinterpret_cast<const uint4*>(tile + (c >> 3) * 16384 + tr * 128 + (((c & 7) ^ (tr & 7)) << 4));
+    w[4 * e] = x.x, w[4 * e + 1] = x.y, w[4 * e + 2] = x.z, w[4 * e + 3] = x.w;
+  }
+}
+template <int D>
+__device__ __forceinline__ void store_half_row(uint32_t addr, int half, const uint32_t (&w)[D / 4]) {
+  if constexpr (D == 128)
+    tmem_st32(addr + 32 * half, w);
+  else
+    tmem_st16(addr + 16 * half, w);
 }
 
 // Stores 32 fp32 accumulator columns of this lane's row times `mul` as bf16, at dst + off
@@ -214,51 +252,48 @@ __device__ __forceinline__ void store_zeros(__nv_bfloat16* dst, int n) {
 }
 
 // ============================================================ dQ
-// Tensor memory: scores, dP in two buffers (step g's in buffer g & 1, dS over it), dQ.  Scores are
-// read into registers and not written back, so their buffer is free at a step's start, and
-// S_{n+1} and dP_{n+1} run while threads form P_n and dS_n; then dQ_n.  The tensor core has
-// the two products of one step and dQ of the step before to do while threads work on a step.
+// Tensor memory: scores and dP (dS over it), each in two buffers of 64 keys (step g's in buffer
+// g & 1), dQ, and Q and dO.  Scores are read into registers and not written back.  Order of
+// the products: S_{n+1}, dP_{n+1}, dQ_n, so that the tensor core works on the next step while
+// threads form P_n and dS_n.
 template <int D>
 struct DqLayout {
   static constexpr int kChunks = D / 64;
-  static constexpr uint32_t kTile = 128u * D * 2;
-  // a key tile stays from its scores to dQ, two products later than a value tile
-  static constexpr int kK = D == 64 ? 4 : 3, kV = D == 64 ? 4 : 2;
-  static constexpr uint32_t kQ = 0, kDO = kTile, kKs = 2 * kTile, kVs = kKs + kK * kTile;
-  static constexpr uint32_t kDx = kVs + kV * kTile;  // [half][128]
+  static constexpr uint32_t kRes = 128u * D * 2, kTile = 64u * D * 2;
+  static constexpr uint32_t kQ = 0, kDO = kRes, kK = 2 * kRes, kV = kK + kStages * kTile;
+  static constexpr uint32_t kDx = kV + kStages * kTile;  // [half][128]
   static constexpr uint32_t kBar = kDx + 1024;
-  static constexpr uint32_t kUsed = kBar + 768;
-  static constexpr uint32_t kSmem = (kUsed > 118784u ? kUsed : 118784u) + 1024;  // + align slack
-  static constexpr uint32_t kSCol = 0, kAcc = 384;
-  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 128u * (step & 1); }
+  static constexpr uint32_t kUsed = kBar + kBarBytes;
+  static constexpr uint32_t kSmem = kUsed > 118784u ? kUsed : 118784u;  // one CTA an SM
+  static constexpr uint32_t kAcc = 256, kQA = 384, kDOA = 384 + D / 2;
+  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * (step & 1); }
+  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 64u * (step & 1); }
 };
 static_assert(DqLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
 __device__ __forceinline__ int dq_tiles(const PackedItem& it, int TT, bool causal) {
-  return (packed_keys(min((it.e.tile + 1) * TT, it.e.n) - 1, it.e.n, it.e.m, causal) + 127) >> 7;
+  return (packed_keys(min((it.e.tile + 1) * TT, it.e.n) - 1, it.e.n, it.e.m, causal) + 63) >> 6;
 }
 
 template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = DqLayout<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (!bwd_init(bars, warp, smem, p.P * p.TT < 128 ? 2 * L::kTile : 0)) return;
+  if (!bwd_init(bars, warp, smem, smem, 0, 1)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
   grid_dependency_launch();
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT) * 128u * L::kChunks;
+      const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT64) * 128u * L::kChunks;
       int kvb = 0, tl = 0;  // key tiles and items with loads so far
       PackedItem it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
       for (int t = 0;; ++t) {
-        const int r = t % kPackedRing;
-        if (!wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, bars, 0x104)) break;
+        const int r = t % kBwdRing;
+        if (!wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
         bars->item[r] = it;
         mbar_arrive(&bars->item_full[r]);
         if (it.head < 0) break;
@@ -271,30 +306,31 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < 4; ++i) tensormap_acquire(maps + i);
         const int kh = it.head / p.per_kv;
+        if (tl > 0 && !wait(&bars->res_empty, (tl - 1) & 1, bars, 0x103)) break;
+        mbar_arrive_expect_tx(&bars->res_full, 4 * q_bytes);
+#pragma unroll
+        for (int c = 0; c < 2 * L::kChunks; ++c) {  // two boxes of 64 rows a column
+          const int col = c >> 1, half = c & 1, tok = it.e.tile * p.TT + half * p.TT64;
+          const uint32_t at = col * 16384 + half * 8192;
+          tma_load_4d(smem + L::kQ + at, maps, &bars->res_full, col * 64, 0, tok, it.head);
+          tma_load_4d(smem + L::kDO + at, maps + 3, &bars->res_full, col * 64, 0, tok, it.head);
+        }
         PackedItem next = it;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-          const int ks = (kvb + j) % L::kK, vs = (kvb + j) % L::kV;
-          if (!(ok = wait(&bars->a_empty[ks], (((kvb + j) / L::kK) & 1) ^ 1, bars, 0x101))) break;
-          mbar_arrive_expect_tx(&bars->a_full[ks], L::kTile);
+          const int s = (kvb + j) % kStages;
+          const uint32_t par = (((kvb + j) / kStages) & 1) ^ 1;
+          if (!(ok = wait(&bars->x_empty[s], par, bars, 0x101))) break;
+          mbar_arrive_expect_tx(&bars->x_full[s], L::kTile);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(smem + L::kKs + ks * L::kTile + c * 16384, maps + 1, &bars->a_full[ks], c * 64, j * 128, kh);
-          if (j == 0) {
-            if (tl > 0 && !(ok = wait(&bars->res_empty, (tl - 1) & 1, bars, 0x103))) break;
-            mbar_arrive_expect_tx(&bars->res_full, 2 * q_bytes);
-#pragma unroll
-            for (int c = 0; c < L::kChunks; ++c) {
-              tma_load_4d(smem + L::kQ + c * 16384, maps, &bars->res_full, c * 64, 0, it.e.tile * p.TT, it.head);
-              tma_load_4d(smem + L::kDO + c * 16384, maps + 3, &bars->res_full, c * 64, 0, it.e.tile * p.TT, it.head);
-            }
-          }
-          if (!(ok = wait(&bars->b_empty[vs], (((kvb + j) / L::kV) & 1) ^ 1, bars, 0x102))) break;
-          mbar_arrive_expect_tx(&bars->b_full[vs], L::kTile);
+            tma_load_3d(smem + L::kK + s * L::kTile + c * 8192, maps + 1, &bars->x_full[s], c * 64, j * 64, kh);
+          if (!(ok = wait(&bars->y_empty[s], par, bars, 0x102))) break;
+          mbar_arrive_expect_tx(&bars->y_full[s], L::kTile);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(smem + L::kVs + vs * L::kTile + c * 16384, maps + 2, &bars->b_full[vs], c * 64, j * 128, kh);
-          // the next item is asked for while the last two tiles are under way
+            tma_load_3d(smem + L::kV + s * L::kTile + c * 8192, maps + 2, &bars->y_full[s], c * 64, j * 64, kh);
+          // the next item is asked for while the last tiles are under way
           if (j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
         }
         if (!ok) break;
@@ -304,72 +340,83 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // The whole warp runs the loop on values that are the same in all lanes, so that descriptors
+  } else if (warp >= kMmaWarp) {
+    // Two warps issue, the first S, the second dP and dQ: 8 products take 210 cycles to issue, a
+    // commit 50, a wait that is over 70, and one warp kept the tensor core waiting.  The
+    // whole warp runs the loop on values that are the same in all lanes, so that descriptors
     // lie in uniform registers, where the instruction wants them; one elected lane issues.
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
-    const uint32_t sQ = smem_u32(smem + L::kQ), sdO = smem_u32(smem + L::kDO);
-    auto sK = [&](int pos) { return smem_u32(smem + L::kKs) + static_cast<uint32_t>(pos % L::kK) * L::kTile; };
-    auto sV = [&](int pos) { return smem_u32(smem + L::kVs) + static_cast<uint32_t>(pos % L::kV) * L::kTile; };
-    // scores and dP of the key tile at ring position pos: the score buffer has been read by then,
-    // and the dP buffer's last dQ is issued
-    auto step = [&](int pos, bool last) {
-      if (!warp_wait(&bars->a_full[pos % L::kK], (pos / L::kK) & 1, bars, 0x211) ||
-          (pos >= 1 && !warp_wait(&bars->s_free, (pos - 1) & 1, bars, 0x212)))
-        return false;
+    const bool scores = warp == kMmaWarp;
+    const uint32_t tm = uniform(tmem), sK = uniform(smem_u32(smem + L::kK)), sV = uniform(smem_u32(smem + L::kV));
+    // dP of the key tile at ring position pos (the last dQ from its buffer is issued)
+    auto step_dp = [&](int pos) {
+      const int s = pos % kStages;
+      if (!warp_wait(&bars->y_full[s], (pos / kStages) & 1, bars, 0x213)) return false;
       tc_fence_after_sync();
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + L::kSCol, kmajor_desc(sQ, kk), kmajor_desc(sK(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
-        umma_commit(&bars->s_full);
-      }
-      __syncwarp();
-      if (!warp_wait(&bars->b_full[pos % L::kV], (pos / L::kV) & 1, bars, 0x213)) return false;
-      tc_fence_after_sync();
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + L::dp_col(pos), kmajor_desc(sdO, kk), kmajor_desc(sV(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
+          umma_ts(tm + L::dp_col(pos), tm + L::kDOA + kk * 8, kmajor_desc(sV + s * L::kTile, kk), idesc_s,
+                  kk > 0 ? 1u : 0u);
         umma_commit(&bars->dp_full[pos & 1]);
-        umma_commit(&bars->b_empty[pos % L::kV]);
-        if (last) umma_commit(&bars->res_empty);  // no product of Q or dO is left
+        umma_commit(&bars->y_empty[s]);
       }
       __syncwarp();
       return true;
     };
     int kvb = 0, tl = 0;
     for (int t = 0;; ++t) {
-      const int r = t % kPackedRing;
-      if (!warp_wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x21b)) break;
+      const int r = t % kBwdRing;
+      if (!warp_wait(&bars->item_full[r], (t / kBwdRing) & 1, bars, 0x21b)) break;
       const PackedItem it = bars->item[r];
       __syncwarp();
       if (elect_one()) mbar_arrive(&bars->item_empty[r]);
       if (uniform(it.head) < 0) break;
       const int n = uniform(dq_tiles(it, p.TT, CAUSAL));
       if (n == 0) continue;
-      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x210) || !step(kvb, n == 1)) break;
+      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x210)) break;
       bool ok = true;
+      if (scores) {
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const int pos = kvb + j;
-        if (j + 1 < n && !(ok = step(pos + 1, j + 2 == n))) break;
-        // dQ += dS K_j (A = dS bf16 in tensor memory over dP); an item's first overwrites the
-        // accumulator that the epilogue before it reads
-        if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214) &&
-                   (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216))))
-          break;
-        tc_fence_after_sync();
-        if (elect_one()) {
+        for (int j = 0; j < n; ++j) {
+          const int pos = kvb + j, s = pos % kStages;
+          // (the buffer's last scores have been read)
+          if (!(ok = warp_wait(&bars->x_full[s], (pos / kStages) & 1, bars, 0x211) &&
+                     (pos < 2 || warp_wait(&bars->s_done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x212))))
+            break;
+          tc_fence_after_sync();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tmem + L::kAcc, tmem + L::dp_col(pos) + packed_a_col(kk), mnmajor_desc(sK(pos), kk), idesc_acc,
-                    (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars->a_empty[pos % L::kK]);
-          if (j + 1 == n) umma_commit(&bars->acc_done);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ts(tm + L::s_col(pos), tm + L::kQA + kk * 8, kmajor_desc(sK + s * L::kTile, kk), idesc_s,
+                      kk > 0 ? 1u : 0u);
+            umma_commit(&bars->s_full[pos & 1]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+        if (!step_dp(kvb)) break;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int pos = kvb + j, s = pos % kStages;
+          if (j + 1 < n && !(ok = step_dp(pos + 1))) break;
+          // dQ += dS K_j (A = dS bf16 in tensor memory over dP); an item's first overwrites the
+          // accumulator that the epilogue before it reads
+          if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214) &&
+                     (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216))))
+            break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ts(tm + L::kAcc, tm + L::dp_col(pos) + packed_a_col(kk), mnmajor_desc(sK + s * L::kTile, kk),
+                      idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bars->x_empty[s]);
+            if (j + 1 == n) umma_commit(&bars->acc_done);
+          }
+          __syncwarp();
+        }
       }
       if (!ok) break;
       kvb += n;
@@ -382,21 +429,23 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
     const int g = threadIdx.x >> 7;    // half of the score columns
     const int tr = threadIdx.x & 127;  // row within the tile, TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t col0 = 64u * g;
-    const int row_tok = tr / p.P, row_head = tr - row_tok * p.P;
+    const uint32_t tm = tmem + lane_off;
+    const int box = tr >> 6, box_tok = (tr & 63) / p.P, row_head = (tr & 63) - box_tok * p.P;
+    const bool row_in = box_tok < p.TT64;
+    const int row_tok = box * p.TT64 + box_tok;
     // (an item's parts have been read by all threads before any gets to the next: its last dS,
     // without which its dQ is not done, comes after)
     float* dx = reinterpret_cast<float*>(smem + L::kDx);
     int nb = 0, tl = 0;  // steps and items with products so far
     for (int ti = 0;; ++ti) {
-      const int r = ti % kPackedRing;
-      if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, bars, 0x304)) break;
+      const int r = ti % kBwdRing;
+      if (!warp_wait(&bars->item_full[r], (ti / kBwdRing) & 1, bars, 0x304)) break;
       const PackedItem it = bars->item[r];
       mbar_arrive(&bars->item_empty[r]);
       if (it.head < 0) break;
       const int n = dq_tiles(it, p.TT, CAUSAL);
       const int tok0 = it.e.tile * p.TT, tok = tok0 + row_tok;
-      const bool valid = row_tok < p.TT && tok < it.e.n;
+      const bool valid = row_in && tok < it.e.n;
       const int head = it.head * p.P + row_head, m = it.e.m, off = m - it.e.n;
       const long long token = it.e.q0 + tok;
       const long long vec = static_cast<long long>(head) * p.total_q + token;
@@ -419,39 +468,51 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
         ok = warp_wait(&bars->dx_ready, tl & 1, bars, 0x313);
         Di = dx[tr] + dx[128 + tr];
       };
+      // Q and dO to tensor memory: the products of the item before that read them are done (its
+      // last scores and dP have been waited for)
+      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x315)) break;
+      uint32_t w[D / 4];
+      load_half_row<D>(smem + L::kQ, tr, g, valid, w);
+      store_half_row<D>(tm + L::kQA, g, w);
+      load_half_row<D>(smem + L::kDO, tr, g, valid, w);
+      store_half_row<D>(tm + L::kDOA, g, w);
+      mbar_arrive(&bars->res_empty);
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&bars->a_ready);
       if (n > 1) {
         float part = 0.0f;
         if (valid) {
           const uint4* a = reinterpret_cast<const uint4*>(p.o + token * p.o_token + head * p.o_head + (D / 2) * g);
-          const uint4* b = reinterpret_cast<const uint4*>(p.dO + token * p.dO_token + head * p.dO_head + (D / 2) * g);
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
-            const uint4 x = a[e], y = b[e];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            const uint4 x = a[e];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              part = fmaf(__uint_as_float(xs[w] << 16), __uint_as_float(ys[w] << 16), part);
-              part = fmaf(__uint_as_float(xs[w] & 0xffff0000u), __uint_as_float(ys[w] & 0xffff0000u), part);
+            for (int i = 0; i < 4; ++i) {
+              part = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(w[4 * e + i] << 16), part);
+              part = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(w[4 * e + i] & 0xffff0000u), part);
             }
           }
         }
         join(part);
         if (!ok) break;
       }
+      const uint32_t col0 = 32u * g;
+      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
-        if (!(ok = warp_wait(&bars->s_full, step & 1, bars, 0x311))) break;
+        if (!(ok = warp_wait(&bars->s_full[step & 1], (step >> 1) & 1, bars, 0x311))) break;
         tc_fence_after_sync();
-        uint32_t pr[64];
-        tmem_ld64(tmem + lane_off + L::kSCol + col0, pr);
+        uint32_t pr[32];
+        tmem_ld(tm + L::s_col(step) + col0, pr);
         tc_fence_before_sync();
-        mbar_arrive(&bars->s_free);
-        const int kv0 = j * 128;
-        const bool need_mask = (CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > m;
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
+        mbar_arrive(&bars->s_done[step & 1]);
+        const int kv0 = j * 64;
+        const bool need_mask = (CAUSAL && kv0 + 63 > tok0 + off) || kv0 + 64 > m;
         auto exp_cols = [&](auto masked, int lim) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
+          for (int c = 0; c < 32; c += 2) {
             const float2 x =
                 __ffma2_rn(make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])), sc2, nl2);
             float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
@@ -469,40 +530,28 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
           exp_cols(std::false_type{}, 0);
         if (!(ok = warp_wait(&bars->dp_full[step & 1], (step >> 1) & 1, bars, 0x314))) break;
         tc_fence_after_sync();
-        const uint32_t dp = tmem + lane_off + L::dp_col(step) + col0;
+        const uint32_t dp = tm + L::dp_col(step) + col0;
+        uint32_t rr[32];
+        tmem_ld(dp, rr);
         if (n == 1) {  // D = sum_j P_j dP_j
           float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c2 = 0; c2 < 2; ++c2) {
-            uint32_t rr[32];
-            tmem_ld32(dp + c2 * 32, rr);
-            tmem_ld_wait();
-            reg_pin(rr);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              part = __ffma2_rn(make_float2(__uint_as_float(pr[c2 * 32 + e]), __uint_as_float(pr[c2 * 32 + e + 1])),
-                                make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), part);
-          }
+          for (int e = 0; e < 32; e += 2)
+            part = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])),
+                              make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), part);
           join(part.x + part.y);
           if (!ok) break;
         }
         const float2 nD2 = make_float2(-Di, -Di);
+        uint32_t ds[16];
 #pragma unroll
-        for (int c2 = 0; c2 < 2; ++c2) {
-          uint32_t rr[32], w[16];
-          tmem_ld32(dp + c2 * 32, rr);
-          tmem_ld_wait();
-          reg_pin(rr);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c = c2 * 32 + 2 * e;
-            const float2 ds = __fmul2_rn(
-                make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])),
-                __fadd2_rn(make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), nD2));
-            w[e] = pack_bf16x2(ds.x, ds.y);
-          }
-          tmem_st16(dp + c2 * 16, w);
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = __fmul2_rn(
+              make_float2(__uint_as_float(pr[2 * e]), __uint_as_float(pr[2 * e + 1])),
+              __fadd2_rn(make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), nD2));
+          ds[e] = pack_bf16x2(x.x, x.y);
         }
+        tmem_st16(dp, ds);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&bars->ds_ready[step & 1]);
@@ -514,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       const long long at = valid ? token * p.dq_token + head * p.dq_head + (D / 2) * g : -1;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
-        store_acc32(tmem + lane_off + L::kAcc + (D / 2) * g + c * 32, p.scale, p.dq + c * 32, at);
+        store_acc32(tm + L::kAcc + (D / 2) * g + c * 32, p.scale, p.dq + c * 32, at);
       // the accumulator has been read: the next item may overwrite it
       tc_fence_before_sync();
       mbar_arrive(&bars->acc_free);
@@ -526,29 +575,30 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
 }
 
 // ============================================================ dK / dV
-// Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK; at d = 64 the accumulators
-// leave room for a second score buffer.  Order of the products: dV_n, S^T_{n+1}, dK_n,
-// dP^T_{n+1} (d = 64: S^T_{n+1} first): threads form dS_n during the first two and
-// P_{n+1} during the last two.
+// Tensor memory: S^T (P^T over it) and dP^T (dS^T over it) of 64 queries, dV, dK, and K and V;
+// at d = 64 there is room for two buffers of the first two.  With one buffer dV_n and S^T_{n+1} run
+// while threads form dS_n, and dK_n and dP^T_{n+1} while they form P_{n+1}; with two, the next
+// step's scores and dP are there when threads come to them.
 template <int D>
 struct DkLayout {
   static constexpr int kChunks = D / 64;
-  static constexpr uint32_t kTile = 128u * D * 2;
-  static constexpr int kRing = D == 64 ? 4 : 2;
-  static constexpr uint32_t kK = 0, kV = kTile, kQ = 2 * kTile, kDO = kQ + kRing * kTile;
-  static constexpr uint32_t kVec = kDO + kRing * kTile;  // [stage][-lse2 | -D][128]
-  static constexpr uint32_t kBar = kVec + kRing * 1024;
-  static constexpr uint32_t kUsed = kBar + 768;
-  static constexpr uint32_t kSmem = (kUsed > 118784u ? kUsed : 118784u) + 1024;  // + align slack
+  static constexpr uint32_t kRes = 128u * D * 2, kTile = 64u * D * 2;
+  static constexpr uint32_t kK = 0, kV = kRes, kQ = 2 * kRes, kDO = kQ + kStages * kTile;
+  static constexpr uint32_t kVec = kDO + kStages * kTile;  // [stage][-lse2 | -D][64]
+  static constexpr uint32_t kBar = kVec + kStages * 512;
+  static constexpr uint32_t kUsed = kBar + kBarBytes;
+  static constexpr uint32_t kSmem = kUsed > 118784u ? kUsed : 118784u;  // one CTA an SM
   static constexpr bool kDouble = D == 64;
-  static constexpr uint32_t kDPCol = 128, kAcc0 = 256, kAcc1 = 256 + D;
-  __host__ __device__ static constexpr uint32_t s_col(int step) { return kDouble && (step & 1) ? 384u : 0u; }
-  __device__ static uint64_t* s_full(BwdBars* b, int step) { return kDouble && (step & 1) ? &b->s_full_1 : &b->s_full; }
-  __device__ static uint64_t* p_ready(BwdBars* b, int step) { return kDouble && (step & 1) ? &b->s_free_1 : &b->s_free; }
-  __host__ __device__ static constexpr uint32_t s_par(int step) { return kDouble ? (step >> 1) & 1 : step & 1; }
+  static constexpr uint32_t kAcc0 = kDouble ? 256 : 128, kAcc1 = kAcc0 + D, kKA = 384, kVA = 384 + D / 2;
+  __host__ __device__ static constexpr int buf(int step) { return kDouble ? step & 1 : 0; }
+  __host__ __device__ static constexpr uint32_t par(int step) { return kDouble ? (step >> 1) & 1 : step & 1; }
+  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * buf(step); }
+  __host__ __device__ static constexpr uint32_t dp_col(int step) { return (kDouble ? 128u : 64u) + 64u * buf(step); }
 };
+static_assert(DkLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
-// Query tiles of a head group that see the item's key tile: the first, and how many.
+// Query tiles (of 64 rows, TT tokens) of a head group that see the item's key tile: the first, and
+// how many.
 __device__ __forceinline__ int dk_first(const PackedItem& it, int TT, bool causal) {
   return causal ? max(it.e.tile * 128 - (it.e.m - it.e.n), 0) / TT : 0;
 }
@@ -559,20 +609,19 @@ __device__ __forceinline__ int dk_tiles(const PackedItem& it, int TT, bool causa
 template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using L = DkLayout<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (!bwd_init(bars, warp, smem + L::kQ, p.P * p.TT < 128 ? 2 * L::kRing * L::kTile : 0)) return;
+  const int TT = p.TT64;
+  if (!bwd_init(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 2)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
 
   if (warp == kTmaWarp) {
-    const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT) * 128u * L::kChunks;
-    int row_tok[4], row_head[4];  // of rows lane, lane + 32, ..
+    const uint32_t q_bytes = static_cast<uint32_t>(p.P * TT) * 128u * L::kChunks;
+    int row_tok[2], row_head[2];  // of rows lane and lane + 32
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
       row_tok[e] = (lane + 32 * e) / p.P;
       row_head[e] = lane + 32 * e - row_tok[e] * p.P;
     }
@@ -580,173 +629,165 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
     PackedItem it;
     if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
     for (int t = 0;; ++t) {
-      const int r = t % kPackedRing;
-      if (!warp_wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, bars, 0x104)) break;
+      const int r = t % kBwdRing;
+      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
       if (lane == 0) {
         bars->item[r] = it;
         mbar_arrive(&bars->item_full[r]);
       }
       __syncwarp();
       it = bars->item[r];
+      __syncwarp();
       if (it.head < 0) break;
-      const int first = dk_first(it, p.TT, CAUSAL), per = dk_tiles(it, p.TT, CAUSAL), n = per * p.per_kv;
+      const int first = dk_first(it, TT, CAUSAL), per = dk_tiles(it, TT, CAUSAL), n = per * p.per_kv;
       if (n == 0) {
         if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
         continue;
       }
       const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
+      if (tl > 0 && !warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x102)) break;
       if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) tensormap_acquire(maps + i);
-      }
-      auto load_res = [&]() {
-        if (lane != 0) return;
-        mbar_arrive_expect_tx(&bars->res_full, 2 * L::kTile);
+        mbar_arrive_expect_tx(&bars->res_full, 2 * L::kRes);
 #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c) {
-          tma_load_3d(smem + L::kK + c * 16384, maps + 1, &bars->res_full, c * 64, it.e.tile * 128, it.head);
-          tma_load_3d(smem + L::kV + c * 16384, maps + 2, &bars->res_full, c * 64, it.e.tile * 128, it.head);
+        for (int c = 0; c < 2 * L::kChunks; ++c) {  // two boxes of 64 keys a column
+          const int col = c >> 1, half = c & 1, key = it.e.tile * 128 + half * 64;
+          tma_load_3d(smem + L::kK + col * 16384 + half * 8192, maps + 1, &bars->res_full, col * 64, key, it.head);
+          tma_load_3d(smem + L::kV + col * 16384 + half * 8192, maps + 2, &bars->res_full, col * 64, key, it.head);
         }
-      };
-      if (tl == 0) load_res();
+      }
+      __syncwarp();
       PackedItem next = it;
       bool ok = true;
       int sub = 0, tile = first;
+      // -lse and -D of this lane's rows of a tile, asked for a tile ahead of their use; rows that do
+      // not exist, or see nothing: P = 0
+      float nl[2], nD[2];
+      auto ask = [&](int tile, int sub) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tok = tile * TT + row_tok[e], group = it.head * p.per_kv + sub;
+          nl[e] = -INFINITY, nD[e] = 0.0f;
+          if (row_tok[e] < TT && tok < it.e.n) {
+            const long long at = static_cast<long long>(group * p.P + row_head[e]) * p.total_q + it.e.q0 + tok;
+            nl[e] = p.lse[at];
+            nD[e] = p.D[at];
+          }
+        }
+      };
+      ask(tile, sub);
       for (int j = 0; j < n; ++j) {
-        const int s = (sb + j) % L::kRing, group = it.head * p.per_kv + sub;
-        if (!(ok = warp_wait(&bars->a_empty[s], (((sb + j) / L::kRing) & 1) ^ 1, bars, 0x101))) break;
-        // the tiles first, then, while they are in flight, lse and D of their rows; the
-        // stage's one arrival comes after both
+        const int s = (sb + j) % kStages, group = it.head * p.per_kv + sub;
+        if (!(ok = warp_wait(&bars->x_empty[s], (((sb + j) / kStages) & 1) ^ 1, bars, 0x101))) break;
         if (lane == 0) {
-          mbar_expect_tx(&bars->a_full[s], 2 * q_bytes);
+          mbar_expect_tx(&bars->x_full[s], 2 * q_bytes);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c) {
-            tma_load_4d(smem + L::kQ + s * L::kTile + c * 16384, maps, &bars->a_full[s], c * 64, 0, tile * p.TT, group);
-            tma_load_4d(smem + L::kDO + s * L::kTile + c * 16384, maps + 3, &bars->a_full[s], c * 64, 0, tile * p.TT, group);
+            tma_load_4d(smem + L::kQ + s * L::kTile + c * 8192, maps, &bars->x_full[s], c * 64, 0, tile * TT, group);
+            tma_load_4d(smem + L::kDO + s * L::kTile + c * 8192, maps + 3, &bars->x_full[s], c * 64, 0, tile * TT, group);
           }
         }
-        float* vec = reinterpret_cast<float*>(smem + L::kVec) + s * 256;
+        float* vec = reinterpret_cast<float*>(smem + L::kVec) + s * 128;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = tile * p.TT + row_tok[e];
-          float l2 = -INFINITY, Di = 0.0f;  // rows that do not exist, or see nothing: P = 0
-          if (row_tok[e] < p.TT && tok < it.e.n) {
-            const long long at = static_cast<long long>(group * p.P + row_head[e]) * p.total_q + it.e.q0 + tok;
-            l2 = -p.lse[at] * kLog2e;
-            Di = -p.D[at];
-            if (l2 == INFINITY) {
-              l2 = -INFINITY;
-              Di = 0.0f;
-            }
-          }
-          vec[lane + 32 * e] = l2;
-          vec[128 + lane + 32 * e] = Di;
+        for (int e = 0; e < 2; ++e) {
+          const bool none = nl[e] == -INFINITY;
+          vec[lane + 32 * e] = none ? -INFINITY : -nl[e] * kLog2e;
+          vec[64 + lane + 32 * e] = none ? 0.0f : -nD[e];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->a_full[s]);
-        __syncwarp();
-        if (j == 0 && tl > 0) {
-          if (!(ok = warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x102))) break;
-          load_res();
-          __syncwarp();
-        }
-        if (lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
+        if (lane == 0) mbar_arrive(&bars->x_full[s]);  // (the stage's one arrival)
         if (++tile == first + per) {
           tile = first;
           ++sub;
         }
+        if (j + 1 < n) ask(tile, sub);
+        if (lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
       }
       if (!ok) break;
       sb += n;
       ++tl;
       it = next;
     }
-  } else if (warp == kMmaWarp) {
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+  } else if (warp >= kMmaWarp) {
+    // Two warps issue (as in the dq kernel), each a chain of products that no other touches: the
+    // first S^T = K Q^T and dV += P^T dO, the second dP^T = V dO^T and dK += dS^T Q.  With one score
+    // buffer they take turns: in flight at once, both chains would end later, and the threads
+    // wait for the end of one while the other could do without.
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
-    const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
-    auto sQ = [&](int pos) { return smem_u32(smem + L::kQ) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
-    auto sdO = [&](int pos) { return smem_u32(smem + L::kDO) + static_cast<uint32_t>(pos % L::kRing) * L::kTile; };
-    auto issue_s = [&](int pos) {
+    const bool first_chain = warp == kMmaWarp;
+    const uint32_t tm = uniform(tmem);
+    const uint32_t score0 = tm + uniform(first_chain ? L::s_col(0) : L::dp_col(0));
+    const uint32_t stays = tm + uniform(first_chain ? L::kKA : L::kVA), acc = tm + uniform(first_chain ? L::kAcc0 : L::kAcc1);
+    const uint32_t sQ = uniform(smem_u32(smem + L::kQ)), sdO = uniform(smem_u32(smem + L::kDO));
+    const uint32_t b_score = uniform(first_chain ? sQ : sdO), b_acc = uniform(first_chain ? sdO : sQ);
+    uint64_t* const full = first_chain ? bars->s_full : bars->dp_full;
+    uint64_t* const ready = first_chain ? bars->s_done : bars->ds_ready;
+    auto stage_in = [&](int pos) { return warp_wait(&bars->x_full[pos % kStages], (pos / kStages) & 1, bars, 0x205); };
+    auto issue_scores = [&](int pos) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        umma_ss(tmem + L::s_col(pos), kmajor_desc(sK, kk), kmajor_desc(sQ(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
-      umma_commit(L::s_full(bars, pos));
+        umma_ts(score0 + 64u * L::buf(pos), stays + kk * 8, kmajor_desc(b_score + pos % kStages * L::kTile, kk), idesc_s,
+                kk > 0 ? 1u : 0u);
+      umma_commit(full + L::buf(pos));
     };
-    auto issue_dp = [&](int pos) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        umma_ss(tmem + L::kDPCol, kmajor_desc(sV, kk), kmajor_desc(sdO(pos), kk), idesc_s, kk > 0 ? 1u : 0u);
-      umma_commit(&bars->dp_full[0]);
+    int sb = 0, tl = 0, turns = 0;
+    auto turn = [&]() {
+      if (L::kDouble) return true;
+      const uint32_t par = static_cast<uint32_t>(turns++ & 1) ^ (first_chain ? 1u : 0u);
+      return warp_wait(&bars->turn[first_chain ? 0 : 1], par, bars, 0x209);
     };
-    auto full = [&](int pos, uint32_t code) {
-      return warp_wait(&bars->a_full[pos % L::kRing], (pos / L::kRing) & 1, bars, code);
+    auto pass_turn = [&]() {
+      if (!L::kDouble) mbar_arrive(&bars->turn[first_chain ? 1 : 0]);
     };
-    int sb = 0, tl = 0;
     for (int t = 0;; ++t) {
-      const int r = t % kPackedRing;
-      if (!warp_wait(&bars->item_full[r], (t / kPackedRing) & 1, bars, 0x207)) break;
+      const int r = t % kBwdRing;
+      if (!warp_wait(&bars->item_full[r], (t / kBwdRing) & 1, bars, 0x207)) break;
       const PackedItem it = bars->item[r];
       __syncwarp();
       if (elect_one()) mbar_arrive(&bars->item_empty[r]);
       if (uniform(it.head) < 0) break;
-      const int n = uniform(dk_tiles(it, p.TT, CAUSAL)) * p.per_kv;
+      const int n = uniform(dk_tiles(it, TT, CAUSAL)) * p.per_kv;
       if (n == 0) continue;
-      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x201) || !full(sb, 0x202)) break;
+      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x201) || !stage_in(sb) || !turn()) break;
       tc_fence_after_sync();
       if (elect_one()) {
-        issue_s(sb);
-        issue_dp(sb);
+        issue_scores(sb);
+        pass_turn();
       }
       __syncwarp();
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        const int pos = sb + j;
+        const int pos = sb + j, s = pos % kStages;
         const bool more = j + 1 < n;
         if (L::kDouble && more) {
-          if (!(ok = full(pos + 1, 0x208))) break;
+          if (!(ok = stage_in(pos + 1))) break;
           tc_fence_after_sync();
-          if (elect_one()) issue_s(pos + 1);
+          if (elect_one()) issue_scores(pos + 1);
           __syncwarp();
         }
-        // dV += P^T dO_j (A = P^T bf16 in tensor memory over S^T); an item's first overwrites the
-        // accumulators that the epilogue before it reads
-        if (!(ok = warp_wait(L::p_ready(bars, pos), L::s_par(pos), bars, 0x203) &&
-                   (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206))))
+        // the accumulator += P^T (dS^T) x the streamed rows (A = bf16 in tensor memory over the
+        // scores); an item's first overwrites what the epilogue before it reads
+        if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206)) &&
+                   (L::kDouble || !more || stage_in(pos + 1)) &&
+                   warp_wait(ready + L::buf(pos), L::par(pos), bars, 0x203) && turn()))
           break;
         tc_fence_after_sync();
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tmem + L::kAcc0, tmem + L::s_col(pos) + packed_a_col(kk), mnmajor_desc(sdO(pos), kk), idesc_acc,
-                    (j > 0 || kk > 0) ? 1u : 0u);
-        }
-        __syncwarp();
-        if (!L::kDouble && more) {
-          if (!(ok = full(pos + 1, 0x205))) break;
-          tc_fence_after_sync();
-          if (elect_one()) issue_s(pos + 1);
-          __syncwarp();
-        }
-        // dK += dS^T Q_j
-        if (!(ok = warp_wait(&bars->ds_ready[0], pos & 1, bars, 0x204))) break;
-        tc_fence_after_sync();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tmem + L::kAcc1, tmem + L::kDPCol + packed_a_col(kk), mnmajor_desc(sQ(pos), kk), idesc_acc,
-                    (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars->a_empty[pos % L::kRing]);
-          if (more) issue_dp(pos + 1);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts(acc, score0 + 64u * L::buf(pos) + packed_a_col(kk), mnmajor_desc(b_acc + s * L::kTile, kk),
+                    idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->x_empty[s]);
+          if (!more) umma_commit(&bars->acc_done);
+          if (!L::kDouble && more) issue_scores(pos + 1);
+          pass_turn();
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (elect_one()) {
-        umma_commit(&bars->acc_done);
-        umma_commit(&bars->res_empty);
-      }
       sb += n;
       ++tl;
     }
@@ -757,15 +798,16 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
     const int g = threadIdx.x >> 7;    // half of the query columns
     const int tr = threadIdx.x & 127;  // key within the tile, TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t col0 = 64u * g;
+    const uint32_t tm = tmem + lane_off;
+    const uint32_t col0 = 32u * g;
     int nb = 0, tl = 0;
     for (int ti = 0;; ++ti) {
-      const int r = ti % kPackedRing;
-      if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, bars, 0x305)) break;
+      const int r = ti % kBwdRing;
+      if (!warp_wait(&bars->item_full[r], (ti / kBwdRing) & 1, bars, 0x305)) break;
       const PackedItem it = bars->item[r];
       mbar_arrive(&bars->item_empty[r]);
       if (it.head < 0) break;
-      const int first = dk_first(it, p.TT, CAUSAL), per = dk_tiles(it, p.TT, CAUSAL), n = per * p.per_kv;
+      const int first = dk_first(it, TT, CAUSAL), per = dk_tiles(it, TT, CAUSAL), n = per * p.per_kv;
       const int key = it.e.tile * 128 + tr;
       const bool valid = key < it.e.m;
       const long long token = it.e.k0 + key;
@@ -778,31 +820,44 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
         }
         continue;
       }
+      // K and V to tensor memory: the products of the item before that read them are done (its last
+      // scores and dP have been waited for)
+      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x307)) break;
+      {
+        uint32_t w[D / 4];
+        load_half_row<D>(smem + L::kK, tr, g, true, w);
+        store_half_row<D>(tm + L::kKA, g, w);
+        load_half_row<D>(smem + L::kV, tr, g, true, w);
+        store_half_row<D>(tm + L::kVA, g, w);
+      }
+      mbar_arrive(&bars->res_empty);
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&bars->a_ready);
       bool ok = true;
       int tile = first;
       // causal: query token i sees the key where i >= key - (m - n)
       const int from = key - (it.e.m - it.e.n);
       const int last_from = it.e.tile * 128 + 127 - (it.e.m - it.e.n);
+      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
-        const float* lse2_s = reinterpret_cast<const float*>(smem + L::kVec) + (step % L::kRing) * 256;
-        const float* D_s = lse2_s + 128;
-        if (!(ok = warp_wait(L::s_full(bars, step), L::s_par(step), bars, 0x301))) break;
+        const float* nlse = reinterpret_cast<const float*>(smem + L::kVec) + (step % kStages) * 128;
+        if (!(ok = warp_wait(&bars->s_full[L::buf(step)], L::par(step), bars, 0x301))) break;
         tc_fence_after_sync();
-        uint32_t pr[64];
-        tmem_ld64(tmem + lane_off + L::s_col(step) + col0, pr);
-        const float4* lse4 = reinterpret_cast<const float4*>(lse2_s + col0);
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        uint32_t pr[32];
+        tmem_ld(tm + L::s_col(step) + col0, pr);
+        const float4* lse4 = reinterpret_cast<const float4*>(nlse + col0);
         auto exp_cols = [&](auto masked, int lim) {
 #pragma unroll
-          for (int c4 = 0; c4 < 16; ++c4) {
+          for (int c4 = 0; c4 < 8; ++c4) {
             const float4 l4 = lse4[c4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int c = 4 * c4 + 2 * h;
-              const float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
-              const float2 x = __ffma2_rn(
-                  make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])), sc2, nl);
+              const float2 x =
+                  __ffma2_rn(make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])), sc2,
+                             h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
               float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
               if (masked) {  // queries before the key
                 if (c < lim) p0 = 0.0f;
@@ -814,57 +869,52 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
           }
         };
         // row r of the tile is token tile * TT + r / P
-        if (CAUSAL && tile * p.TT < last_from)
-          exp_cols(std::true_type{}, min(max(from - tile * p.TT, 0), 128) * p.P - static_cast<int>(col0));
+        if (CAUSAL && tile * TT < last_from)
+          exp_cols(std::true_type{}, min(max(from - tile * TT, 0), 64) * p.P - static_cast<int>(col0));
         else
           exp_cols(std::false_type{}, 0);
         {
-          uint32_t pk[32];
+          uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
+          for (int c = 0; c < 16; ++c)
             pk[c] = pack_bf16x2(__uint_as_float(pr[2 * c]), __uint_as_float(pr[2 * c + 1]));
-          tmem_st32(tmem + lane_off + L::s_col(step) + col0, pk);
+          tmem_st16(tm + L::s_col(step) + col0, pk);
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(L::p_ready(bars, step));
-        if (!(ok = warp_wait(&bars->dp_full[0], step & 1, bars, 0x306))) break;
+        mbar_arrive(&bars->s_done[L::buf(step)]);
+        if (!(ok = warp_wait(&bars->dp_full[L::buf(step)], L::par(step), bars, 0x306))) break;
         tc_fence_after_sync();
+        uint32_t rr[32], ds[16];
+        const uint32_t dp = tm + L::dp_col(step) + col0;
+        tmem_ld(dp, rr);
+        const float4* d4 = reinterpret_cast<const float4*>(nlse + 64 + col0);
 #pragma unroll
-        for (int c2 = 0; c2 < 2; ++c2) {
-          uint32_t rr[32], w[16];
-          tmem_ld32(tmem + lane_off + L::kDPCol + col0 + c2 * 32, rr);
-          tmem_ld_wait();
-          reg_pin(rr);
-          const float4* d4 = reinterpret_cast<const float4*>(D_s + col0 + c2 * 32);
-#pragma unroll
-          for (int e4 = 0; e4 < 8; ++e4) {
-            const float4 dd = d4[e4];
-            const int c = c2 * 32 + 4 * e4;
-            const float2 ds01 = __fmul2_rn(
-                make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1])),
-                __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4]), __uint_as_float(rr[4 * e4 + 1])),
-                           make_float2(dd.x, dd.y)));
-            const float2 ds23 = __fmul2_rn(
-                make_float2(__uint_as_float(pr[c + 2]), __uint_as_float(pr[c + 3])),
-                __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4 + 2]), __uint_as_float(rr[4 * e4 + 3])),
-                           make_float2(dd.z, dd.w)));
-            w[2 * e4] = pack_bf16x2(ds01.x, ds01.y);
-            w[2 * e4 + 1] = pack_bf16x2(ds23.x, ds23.y);
-          }
-          tmem_st16(tmem + lane_off + L::kDPCol + col0 + c2 * 16, w);
+        for (int e4 = 0; e4 < 8; ++e4) {
+          const float4 dd = d4[e4];
+          const float2 ds01 = __fmul2_rn(
+              make_float2(__uint_as_float(pr[4 * e4]), __uint_as_float(pr[4 * e4 + 1])),
+              __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4]), __uint_as_float(rr[4 * e4 + 1])),
+                         make_float2(dd.x, dd.y)));
+          const float2 ds23 = __fmul2_rn(
+              make_float2(__uint_as_float(pr[4 * e4 + 2]), __uint_as_float(pr[4 * e4 + 3])),
+              __fadd2_rn(make_float2(__uint_as_float(rr[4 * e4 + 2]), __uint_as_float(rr[4 * e4 + 3])),
+                         make_float2(dd.z, dd.w)));
+          ds[2 * e4] = pack_bf16x2(ds01.x, ds01.y);
+          ds[2 * e4 + 1] = pack_bf16x2(ds23.x, ds23.y);
         }
+        tmem_st16(dp, ds);
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->ds_ready[0]);
+        mbar_arrive(&bars->ds_ready[L::buf(step)]);
         if (++tile == first + per) tile = first;
       }
       if (!ok || !warp_wait(&bars->acc_done, tl & 1, bars, 0x302)) break;
       tc_fence_after_sync();
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        store_acc32(tmem + lane_off + L::kAcc0 + (D / 2) * g + c * 32, 1.0f, p.dv + c * 32, at_v);
-        store_acc32(tmem + lane_off + L::kAcc1 + (D / 2) * g + c * 32, p.scale, p.dk + c * 32, at_k);
+        store_acc32(tm + L::kAcc0 + (D / 2) * g + c * 32, 1.0f, p.dv + c * 32, at_v);
+        store_acc32(tm + L::kAcc1 + (D / 2) * g + c * 32, p.scale, p.dk + c * 32, at_k);
       }
       // the accumulators have been read: the next item may overwrite them
       tc_fence_before_sync();
@@ -929,7 +979,8 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   p.dv = out(a.dv), p.dv_token = a.dv.token, p.dv_head = a.dv.head;
   p.total_q = a.total_q;
   p.P = t.P;
-  p.TT = t.TT;
+  p.TT = 2 * t.TT64;
+  p.TT64 = t.TT64;
   p.heads = t.heads;
   p.per_kv = t.per_kv;
   p.Hkv = Hkv;
@@ -940,7 +991,7 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   // the dq kernel streams keys and values, the other the queries and dO of a group's heads
   const int chunk[2] = {packed_chunk(a.total_k, a.d, Hkv) * t.per_kv,
                         packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv)};
-  const long long q_items = a.total_q > 0 ? (a.total_q / t.TT + a.B) * static_cast<long long>(t.heads) : 0;
+  const long long q_items = a.total_q > 0 ? (a.total_q / p.TT + a.B) * static_cast<long long>(t.heads) : 0;
   const long long k_items = a.total_k > 0 ? (a.total_k / 128 + a.B) * static_cast<long long>(Hkv) : 0;
   const unsigned nq = static_cast<unsigned>(std::min<long long>(q_items, a.num_sms));
   const unsigned nk = static_cast<unsigned>(std::min<long long>(k_items, a.num_sms));
