@@ -13,6 +13,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -36,11 +37,9 @@ class _CacheStruct(ctypes.Structure):
                 ("cap", ctypes.c_int), ("d", ctypes.c_int), ("format", ctypes.c_int)]
 
 
-class _HeadsStruct(ctypes.Structure):
-    """fa_heads of include/fa.h."""
-    _fields_ = [("p", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong),
-                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
-                ("heads", ctypes.c_int)]
+# fa_heads of include/fa.h, as the bytes that a call passes the address of (a third of what
+# a ctypes structure costs; the small calls are as long as their Python).
+_pack_heads = struct.Struct("Pqqqi4x").pack
 
 
 class _RotationStruct(ctypes.Structure):
@@ -115,7 +114,7 @@ def library():
         lib.fa_decode_tree_workspace_size.restype = sz
         lib.fa_decode_tree.argtypes = [pc, vp, vp, vp, ll, vp, vp, i, i, f, vp, sz, vp]
         lib.fa_decode_tree.restype = i
-        ph, pr, dbl = ctypes.POINTER(_HeadsStruct), ctypes.POINTER(_RotationStruct), ctypes.c_double
+        ph, pr, dbl = vp, ctypes.POINTER(_RotationStruct), ctypes.c_double
         for fn in (lib.fa_forward_packed_workspace_size, lib.fa_backward_packed_workspace_size):
             fn.argtypes = [i] * 6
             fn.restype = sz
@@ -769,6 +768,16 @@ def _call(dev, fn, stream, *args):
 def _heads(t, name, dev, shape):
     """fa_heads of a bf16 tensor of rows on device `dev`: [tokens, heads, d] or
     [B, heads, N, d] in any strides, as long as each row is contiguous."""
+    s = t.stride()
+    if not (t.dtype is torch.bfloat16 and t.shape == shape and _device_index(t) == dev
+            and s[-1] == 1 and _on_device(t)):
+        _bad_heads(t, name, dev, shape)
+    if len(s) == 3:
+        return _pack_heads(t.data_ptr(), 0, s[0], s[1], shape[1])
+    return _pack_heads(t.data_ptr(), s[0], s[2], s[1], shape[1])
+
+
+def _bad_heads(t, name, dev, shape):
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if not _on_device(t):
@@ -778,18 +787,14 @@ def _heads(t, name, dev, shape):
     if _device_index(t) != dev:
         raise ValueError(f"{name} is on device {_device_index(t)}, the call's other tensors on "
                          f"device {dev}")
-    s = t.stride()
-    if s[-1] != 1:
-        raise ValueError(f"the rows of {name} must be contiguous (strides {s})")
-    if len(s) == 3:
-        return _HeadsStruct(t.data_ptr(), 0, s[0], s[1], shape[1])
-    return _HeadsStruct(t.data_ptr(), s[0], s[2], s[1], shape[1])
+    raise ValueError(f"the rows of {name} must be contiguous (strides {t.stride()})")
 
 
 def _vector(t, name, dev, dtype, shape):
-    """_check of a small contiguous tensor, and its device."""
-    _check(t, name, dtype, shape)
-    if _device_index(t) != dev:
+    """Address of a small contiguous tensor, checked."""
+    if not (t.dtype is dtype and t.shape == shape and _device_index(t) == dev
+            and t.is_contiguous() and _on_device(t)):
+        _check(t, name, dtype, shape)
         raise ValueError(f"{name} is on device {_device_index(t)}, the call's other tensors on "
                          f"device {dev}")
     return t.data_ptr()
@@ -862,9 +867,8 @@ def fa_forward_packed(q, k, v, cu_q, cu_k=None, causal: bool = False, scale: flo
     workspace = _packed_workspace(
         workspace, lib.fa_forward_packed_workspace_size(B, tq, tk, Hq, Hkv, d), dev, stream, device)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    _call(dev, lib.fa_forward_packed, stream, ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
-          ctypes.byref(ho), pl, pq, pk, B, tq, tk, d, float(scale), int(bool(causal)),
-          workspace.data_ptr(), workspace.numel())
+    _call(dev, lib.fa_forward_packed, stream, hq, hk, hv, ho, pl, pq, pk, B, tq, tk, d, scale,
+          bool(causal), workspace.data_ptr(), workspace.numel())
     return o, lse
 
 
@@ -893,10 +897,8 @@ def fa_backward_packed(q, k, v, o, dO, lse, cu_q, cu_k=None, causal: bool = Fals
     workspace = _packed_workspace(
         workspace, lib.fa_backward_packed_workspace_size(B, tq, tk, Hq, Hkv, d), dev, stream, device)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    ref = ctypes.byref
-    _call(dev, lib.fa_backward_packed, stream, ref(hq), ref(hk), ref(hv), ref(ho), ref(hg), pl,
-          ref(hdq), ref(hdk), ref(hdv), pq, pk, B, tq, tk, d, float(scale), int(bool(causal)),
-          workspace.data_ptr(), workspace.numel())
+    _call(dev, lib.fa_backward_packed, stream, hq, hk, hv, ho, hg, pl, hdq, hdk, hdv, pq, pk, B,
+          tq, tk, d, scale, bool(causal), workspace.data_ptr(), workspace.numel())
     return dq, dk, dv
 
 
@@ -975,16 +977,16 @@ def _rotary_shapes(rotary, q, k, positions):
 
 def _rotary_outputs(rotary, stream, *pairs):
     """The outputs that were not given, as the inputs without gaps."""
-    if all(y is not None or x is None for x, y in pairs):
-        return [y for _, y in pairs]
-    with _alloc(rotary._dev, stream):
+    if stream is None:
         return [torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
                 if y is None and x is not None else y for x, y in pairs]
+    with _alloc(rotary._dev, stream):
+        return _rotary_outputs(rotary, None, *pairs)
 
 
 def _refs(rotary, *named):
-    return [None if t is None else ctypes.byref(_heads(t, name, rotary._dev, shape))
-            for t, name, shape in named]
+    dev = rotary._dev
+    return [None if t is None else _heads(t, name, dev, shape) for t, name, shape in named]
 
 
 def _rotate(fn, rotary, q, k, positions, names, q_out, k_out, stream):

@@ -179,7 +179,7 @@ struct RotaryArgs {
   float* dw[2];
   long long tokens;  // B * N
   int N;
-  int parts;  // set by the launch
+  int parts[2];  // set by the launch
   int num_sms;
 };
 

@@ -13,6 +13,7 @@
 // (the table holds f_i / 2 pi to 2^-65), and its upper 32 bits, read as signed, are the
 // angle in (-1/2, 1/2] turns.  sincospif of twice that needs no range reduction; all
 // of it is off by about 2^-23, however far the position.
+#include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -136,62 +137,74 @@ __device__ __forceinline__ void load_weight8(const RotaryArgs& p, int t, int at,
   }
 }
 
-__device__ __forceinline__ const __nv_bfloat16* row_at(const HeadsView& t, long long b, long long i,
-                                                       long long h) {
-  return static_cast<const __nv_bfloat16*>(t.p) + b * t.batch + i * t.token + h * t.head;
-}
+constexpr int blocks_per_sm(int mode) { return mode == 3 ? 2 : (mode == 2 ? 3 : 4); }
 
-// One warp takes a token, or (p.parts > 1: few tokens) every parts-th group of its
-// heads.  MODE 0: rotation, 1: rotation backwards, 2: norm and rotation, 3: its
-// backward pass, whose weight gradients a warp gathers over all its tokens.
+// A unit of work is a token's heads of one tensor, or (few tokens) an equal part of them; the
+// units of q come before those of k, and warps take them in turn, so that a warp changes the
+// tensor once and holds one set of weights, and of sums of their gradients, at a time.  A step is
+// 32 * 16 / d heads; the rows of the next are asked for before those of one are worked on.
+// MODE 0: rotation, 1: rotation backwards, 2: norm and rotation, 3: its backward pass.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kRotaryThreads) fa_rotary_kernel(const RotaryArgs p) {
+__global__ void __launch_bounds__(kRotaryThreads, blocks_per_sm(MODE))
+    fa_rotary_kernel(const __grid_constant__ RotaryArgs p) {
   constexpr int L = D / 16, R = 32 / L;  // lanes a row, rows a step
   constexpr bool kNorm = MODE >= 2, kBack = MODE == 3;
   constexpr float kSign = (MODE & 1) ? -1.0f : 1.0f;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % L, grp = lane / L;
   const LaneMap m = lane_map<D>(sub, p);
-  float dw[kBack ? 2 : 1][16];
-  if (kBack) {
+  if (kBack) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float part_s[kBack ? kWarps : 1][2][D];
+  const long long stride = static_cast<long long>(gridDim.x) * kWarps;
+  long long u = static_cast<long long>(blockIdx.x) * kWarps + warp, done = 0;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < 2; ++t) {
+    const HeadsView& tx = p.x[t];
+    const HeadsView& tg = p.g[t];
+    const HeadsView& ty = p.y[t];
+    const long long units = p.tokens * p.parts[t];
+    float wa[8], wb[8], da[8], db[8];  // weights, and sums of their gradients
+    if (kNorm && u - done < units) {
+      load_weight8(p, t, m.a, wa);
+      load_weight8(p, t, m.b, wb);
+    }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) dw[kBack ? t : 0][j] = 0.0f;
-  }
-  const long long units = p.tokens * p.parts;
-  for (long long u = static_cast<long long>(blockIdx.x) * kWarps + warp; u < units;
-       u += static_cast<long long>(gridDim.x) * kWarps) {
-    const long long tok = u / p.parts;
-    const int part = static_cast<int>(u - tok * p.parts);
-    const long long b = tok / p.N, i = tok - b * p.N;
-    const int pos = p.positions ? p.positions[tok] : static_cast<int>(i);
-    float c[8], s[8];
-    lane_angles<D>(p, m, sub, grp, pos, c, s);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      float wa[8], wb[8];
-      if (kNorm && p.x[t].heads > 0) {
-        load_weight8(p, t, m.a, wa);
-        load_weight8(p, t, m.b, wb);
-      }
-      for (int h0 = part * R; h0 < p.x[t].heads; h0 += p.parts * R) {
-        const int h = h0 + grp;
-        const bool on = h < p.x[t].heads;
-        Row16 x = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, g = x;
-        if (on) {
-          const __nv_bfloat16* r = row_at(p.x[t], b, i, h);
-          x.a = *reinterpret_cast<const uint4*>(r + m.a);
-          x.b = *reinterpret_cast<const uint4*>(r + m.b);
+    for (int j = 0; j < 8; ++j) da[j] = db[j] = 0.0f;
+    for (; u - done < units; u += stride) {
+      const long long v = u - done, tok = v / p.parts[t];
+      const int part = static_cast<int>(v - tok * p.parts[t]);
+      const long long b = tok / p.N, i = tok - b * p.N;
+      const __nv_bfloat16* xr = static_cast<const __nv_bfloat16*>(tx.p) + b * tx.batch + i * tx.token;
+      const __nv_bfloat16* gr = static_cast<const __nv_bfloat16*>(tg.p) + b * tg.batch + i * tg.token;
+      __nv_bfloat16* yr = static_cast<__nv_bfloat16*>(const_cast<void*>(ty.p)) + b * ty.batch + i * ty.token;
+      Row16 x, g;  // of the next step
+      auto ask = [&](int h) {
+        x.a = x.b = g.a = g.b = make_uint4(0, 0, 0, 0);
+        if (h < tx.heads) {
+          x.a = *reinterpret_cast<const uint4*>(xr + h * tx.head + m.a);
+          x.b = *reinterpret_cast<const uint4*>(xr + h * tx.head + m.b);
           if (kBack) {
-            const __nv_bfloat16* q = row_at(p.g[t], b, i, h);
-            g.a = *reinterpret_cast<const uint4*>(q + m.a);
-            g.b = *reinterpret_cast<const uint4*>(q + m.b);
+            g.a = *reinterpret_cast<const uint4*>(gr + h * tg.head + m.a);
+            g.b = *reinterpret_cast<const uint4*>(gr + h * tg.head + m.b);
           }
         }
-        float xa[8], xb[8];
+      };
+      const int step = p.parts[t] * R;
+      ask(part * R + grp);
+      const int pos = p.positions ? p.positions[tok] : static_cast<int>(i);
+      float c[8], s[8];
+      lane_angles<D>(p, m, sub, grp, pos, c, s);
+      for (int h0 = part * R; h0 < tx.heads; h0 += step) {
+        const int h = h0 + grp;
+        const bool on = h < tx.heads;
+        float xa[8], xb[8], ga[8], gb[8];
         unpack8(x.a, xa);
         unpack8(x.b, xb);
+        if (kBack) {
+          unpack8(g.a, ga);
+          unpack8(g.b, gb);
+        }
+        if (h0 + step < tx.heads) ask(h + step);
         if (kNorm) {
           float ss = 0.0f;
 #pragma unroll
@@ -203,16 +216,13 @@ __global__ void __launch_bounds__(kRotaryThreads) fa_rotary_kernel(const RotaryA
             xb[j] *= r;
           }
           if (kBack) {
-            float ga[8], gb[8];
-            unpack8(g.a, ga);
-            unpack8(g.b, gb);
             turn(m, ga, gb, c, s, kSign);
             float dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               if (on) {
-                dw[kBack ? t : 0][j] = fmaf(ga[j], xa[j], dw[kBack ? t : 0][j]);
-                dw[kBack ? t : 0][8 + j] = fmaf(gb[j], xb[j], dw[kBack ? t : 0][8 + j]);
+                da[j] = fmaf(ga[j], xa[j], da[j]);
+                db[j] = fmaf(gb[j], xb[j], db[j]);
               }
               ga[j] *= wa[j];
               gb[j] *= wb[j];
@@ -234,31 +244,33 @@ __global__ void __launch_bounds__(kRotaryThreads) fa_rotary_kernel(const RotaryA
         }
         if (!kBack) turn(m, xa, xb, c, s, kSign);
         if (on) {
-          __nv_bfloat16* y = const_cast<__nv_bfloat16*>(row_at(p.y[t], b, i, h));
-          *reinterpret_cast<uint4*>(y + m.a) = pack8(xa);
-          *reinterpret_cast<uint4*>(y + m.b) = pack8(xb);
+          *reinterpret_cast<uint4*>(yr + h * ty.head + m.a) = pack8(xa);
+          *reinterpret_cast<uint4*>(yr + h * ty.head + m.b) = pack8(xb);
+        }
+      }
+    }
+    done += units;
+    if (kBack) {  // over the row groups of the warp
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) {
+          da[j] += __shfl_xor_sync(0xffffffffu, da[j], o);
+          db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
+        }
+        if (grp == 0) {
+          part_s[kBack ? warp : 0][t][m.a + j] = da[j];
+          part_s[kBack ? warp : 0][t][m.b + j] = db[j];
         }
       }
     }
   }
-  if (kBack) {
-    // the block's sums of each weight's gradient: over the row groups of a warp, then over
-    // the warps in order
-    __shared__ float part_s[kWarps][2][D];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float v = dw[kBack ? t : 0][j];
-#pragma unroll
-        for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (grp == 0) part_s[warp][t][j < 8 ? m.a + j : m.b + j - 8] = v;
-      }
+  if (kBack) {  // over the block's warps in order
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * D; e += kRotaryThreads) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += part_s[w][e / D][e % D];
+      for (int w = 0; w < kWarps; ++w) v += part_s[kBack ? w : 0][e / D][e % D];
       p.partial[static_cast<size_t>(blockIdx.x) * 2 * D + e] = v;
     }
   }
@@ -270,6 +282,7 @@ __global__ void __launch_bounds__(256) fa_norm_weight_kernel(const float* __rest
                                                              int blocks, float* dwq, float* dwk) {
   // eight columns a block, 32 slices of the blocks each
   const int col = blockIdx.x * 8 + (threadIdx.x & 7), slice = threadIdx.x >> 3;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float v = 0.0f;
   for (int b = slice; b < blocks; b += 32) v += partial[static_cast<size_t>(b) * 2 * D + col];
   __shared__ float s[32][8];
@@ -284,27 +297,37 @@ __global__ void __launch_bounds__(256) fa_norm_weight_kernel(const float* __rest
   }
 }
 
-// Parts a token's heads are split into: one where the tokens fill the GPU's warps, as many
-// steps as there are otherwise.
-int rotary_parts(const RotaryArgs& a, int rows) {
-  const int most = max((a.x[0].heads + rows - 1) / rows, (a.x[1].heads + rows - 1) / rows);
-  const long long warps = static_cast<long long>(a.num_sms) * 32;
-  long long parts = (warps + a.tokens - 1) / a.tokens;
-  if (parts > most) parts = most;
-  return static_cast<int>(parts < 1 ? 1 : parts);
-}
-
 template <int D, int MODE>
 cudaError_t launch_t(RotaryArgs a, cudaStream_t s) {
-  a.parts = rotary_parts(a, 32 * 16 / D);
-  const long long blocks = (a.tokens * a.parts + kWarps - 1) / kWarps;
-  const long long most = MODE == 3 ? min(4ll * a.num_sms, static_cast<long long>(kNormMaxBlocks)) : 0x7fffffffll;
-  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  // parts a token's heads are split into: one where the tokens alone fill the GPU's warps, as many
+  // as there are steps otherwise
+  constexpr int R = 32 * 16 / D;
+  long long units = 0;
+  for (int t = 0; t < 2; ++t) {
+    const long long most = (a.x[t].heads + R - 1) / R, want = (a.num_sms * 32ll + a.tokens - 1) / a.tokens;
+    a.parts[t] = static_cast<int>(want < most ? want : most);
+    units += a.tokens * a.parts[t];
+  }
+  const long long blocks = (units + kWarps - 1) / kWarps;
+  // as many blocks as run at once (of the backward pass each leaves a partial sum)
+  const long long most = static_cast<long long>(a.num_sms) * blocks_per_sm(MODE);
+  const unsigned grid = static_cast<unsigned>(std::min(blocks, MODE == 3 ? std::min<long long>(most, kNormMaxBlocks) : most));
   fa_rotary_kernel<D, MODE><<<grid, kRotaryThreads, 0, s>>>(a);
   if (MODE == 3) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    fa_norm_weight_kernel<D><<<2 * D / 8, 256, 0, s>>>(a.partial, static_cast<int>(grid), a.dw[0], a.dw[1]);
+    // launched while the blocks still run, for which it waits (griddepcontrol.wait)
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * D / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_norm_weight_kernel<D>, static_cast<const float*>(a.partial),
+                              static_cast<int>(grid), a.dw[0], a.dw[1]);
   }
   return cudaGetLastError();
 }
