@@ -62,6 +62,8 @@ def library_path() -> str:
 def library():
     """Load libfa.so (raises if it has not been built: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -752,15 +754,18 @@ def _alloc(dev, stream):
 
 def _call(dev, fn, stream, *args):
     """fn(*args, stream) with device `dev` current."""
-    if stream is None and dev >= 0:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        stream = _stream_handle(stream, dev)
-    if dev < 0 or dev == torch.cuda.current_device():
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
+    if dev >= 0:
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(dev)
+        elif hasattr(stream, "cuda_stream"):
+            stream = stream.cuda_stream
+        if dev != torch._C._cuda_getDevice():
+            with torch.cuda.device(dev):
+                st = fn(*args, stream)
+        else:
             st = fn(*args, stream)
+    else:
+        st = fn(*args, _stream_handle(stream, dev))
     if st != FA_OK:
         raise FaError(st, fn.__name__)
 
@@ -800,6 +805,16 @@ def _vector(t, name, dev, dtype, shape):
     return t.data_ptr()
 
 
+def _outputs(dev, device, stream, *wanted):
+    """The tensors of (tensor or None, shape, dtype), made where they were not given, by
+    the stream that the call runs on."""
+    if stream is not None and dev >= 0:
+        with _alloc(dev, stream):
+            return _outputs(dev, device, None, *wanted)
+    return [torch.empty(shape, dtype=dtype, device=device) if t is None else t
+            for t, shape, dtype in wanted]
+
+
 def _packed_shapes(q, k, v, cu_q, cu_k):
     """(total_q, total_k, Hq, Hkv, d, B) of a packed call."""
     if q.dim() != 3 or k.dim() != 3:
@@ -816,8 +831,11 @@ def _packed_shapes(q, k, v, cu_q, cu_k):
 
 def _packed_workspace(workspace, need, dev, stream, device):
     if workspace is None:
+        need = max(need, 256)
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=device)
         with _alloc(dev, stream):
-            return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+            return torch.empty(need, dtype=torch.uint8, device=device)
     _check_workspace(workspace)
     if _device_index(workspace) != dev:
         raise ValueError(f"workspace is on device {_device_index(workspace)}, the call's other "
@@ -857,10 +875,8 @@ def fa_forward_packed(q, k, v, cu_q, cu_k=None, causal: bool = False, scale: flo
     hv = _heads(v, "v", dev, (tk, Hkv, d))
     pq = _vector(cu_q, "cu_q", dev, torch.int32, (B + 1,))
     pk = None if cu_k is None else _vector(cu_k, "cu_k", dev, torch.int32, (B + 1,))
-    if o is None or lse is None:
-        with _alloc(dev, stream):
-            o = torch.empty((tq, Hq, d), dtype=torch.bfloat16, device=device) if o is None else o
-            lse = torch.empty((Hq, tq), dtype=torch.float32, device=device) if lse is None else lse
+    o, lse = _outputs(dev, device, stream, (o, (tq, Hq, d), torch.bfloat16),
+                      (lse, (Hq, tq), torch.float32))
     ho = _heads(o, "o", dev, (tq, Hq, d))
     pl = _vector(lse, "lse", dev, torch.float32, (Hq, tq))
     lib = library()
@@ -888,10 +904,8 @@ def fa_backward_packed(q, k, v, o, dO, lse, cu_q, cu_k=None, causal: bool = Fals
     pl = _vector(lse, "lse", dev, torch.float32, (Hq, tq))
     pq = _vector(cu_q, "cu_q", dev, torch.int32, (B + 1,))
     pk = None if cu_k is None else _vector(cu_k, "cu_k", dev, torch.int32, (B + 1,))
-    if dq is None or dk is None or dv is None:
-        with _alloc(dev, stream):
-            dq, dk, dv = (torch.empty(s, dtype=torch.bfloat16, device=device) if t is None else t
-                          for t, s in ((dq, qs), (dk, ks), (dv, ks)))
+    bf16 = torch.bfloat16
+    dq, dk, dv = _outputs(dev, device, stream, (dq, qs, bf16), (dk, ks, bf16), (dv, ks, bf16))
     hdq, hdk, hdv = _heads(dq, "dq", dev, qs), _heads(dk, "dk", dev, ks), _heads(dv, "dv", dev, ks)
     lib = library()
     workspace = _packed_workspace(
@@ -975,27 +989,31 @@ def _rotary_shapes(rotary, q, k, positions):
     return B, N, ks, pos
 
 
-def _rotary_outputs(rotary, stream, *pairs):
-    """The outputs that were not given, as the inputs without gaps."""
+def _rotary_outputs(rotary, stream, q, k, q_out, k_out):
+    """(q_out, k_out), made as the inputs without gaps where not given (k None: None)."""
+    bf16, device = torch.bfloat16, q.device
     if stream is None:
-        return [torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-                if y is None and x is not None else y for x, y in pairs]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=bf16, device=device)
+        if k is None:
+            return q_out, None
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=bf16, device=device)
+        return q_out, k_out
     with _alloc(rotary._dev, stream):
-        return _rotary_outputs(rotary, None, *pairs)
-
-
-def _refs(rotary, *named):
-    dev = rotary._dev
-    return [None if t is None else _heads(t, name, dev, shape) for t, name, shape in named]
+        return _rotary_outputs(rotary, None, q, k, q_out, k_out)
 
 
 def _rotate(fn, rotary, q, k, positions, names, q_out, k_out, stream):
     B, N, ks, pos = _rotary_shapes(rotary, q, k, positions)
-    q_out, k_out = _rotary_outputs(rotary, stream, (q, q_out), (k, k_out))
-    refs = _refs(rotary, (q, names[0], q.shape), (k, names[1], ks), (q_out, names[2], q.shape),
-                 (None if k is None else k_out, names[3], ks))
-    _call(rotary._dev, fn, stream, rotary._ref, *refs, pos, B, N, rotary.d)
-    return q_out, (None if k is None else k_out)
+    q_out, k_out = _rotary_outputs(rotary, stream, q, k, q_out, k_out)
+    dev, qs = rotary._dev, q.shape
+    hk = ho = None
+    if k is not None:
+        hk, ho = _heads(k, names[1], dev, ks), _heads(k_out, names[3], dev, ks)
+    _call(dev, fn, stream, rotary._ref, _heads(q, names[0], dev, qs), hk,
+          _heads(q_out, names[2], dev, qs), ho, pos, B, N, rotary.d)
+    return q_out, k_out
 
 
 def fa_rotary(rotary: Rotary, q, k=None, positions=None, q_out=None, k_out=None, stream=None):
@@ -1035,12 +1053,14 @@ def fa_norm_rotary(rotary: Rotary, q, k, positions, q_weight, k_weight=None, eps
     Otherwise as fa_rotary."""
     B, N, ks, pos = _rotary_shapes(rotary, q, k, positions)
     wq, wk, wfmt = _weights(rotary, k, q_weight, k_weight)
-    q_out, k_out = _rotary_outputs(rotary, stream, (q, q_out), (k, k_out))
-    refs = _refs(rotary, (q, "q", q.shape), (k, "k", ks), (q_out, "q_out", q.shape),
-                 (None if k is None else k_out, "k_out", ks))
-    _call(rotary._dev, library().fa_norm_rotary, stream, rotary._ref, *refs, pos, wq, wk, wfmt,
-          float(eps), B, N, rotary.d)
-    return q_out, (None if k is None else k_out)
+    q_out, k_out = _rotary_outputs(rotary, stream, q, k, q_out, k_out)
+    dev, qs = rotary._dev, q.shape
+    hk = ho = None
+    if k is not None:
+        hk, ho = _heads(k, "k", dev, ks), _heads(k_out, "k_out", dev, ks)
+    _call(dev, library().fa_norm_rotary, stream, rotary._ref, _heads(q, "q", dev, qs), hk,
+          _heads(q_out, "q_out", dev, qs), ho, pos, wq, wk, wfmt, eps, B, N, rotary.d)
+    return q_out, k_out
 
 
 FA_NORM_WORKSPACE = 1048576
@@ -1057,23 +1077,26 @@ def fa_norm_rotary_backward(rotary: Rotary, dq, dk, q, k, positions, q_weight, k
     if k is not None and dk is None:
         raise ValueError("k needs dk")
     wq, wk, wfmt = _weights(rotary, k, q_weight, k_weight)
-    q1, k1 = (q, k) if k is not None else (q, None)
-    dq_in, dk_in = _rotary_outputs(rotary, stream, (q1, dq_in), (k1, dk_in))
+    dq_in, dk_in = _rotary_outputs(rotary, stream, q, k, dq_in, dk_in)
+    dev, qs, wd, f32 = rotary._dev, q.shape, (rotary.d,), torch.float32
     if dq_weight is None or (k is not None and dk_weight is None):
-        with _alloc(rotary._dev, stream):
-            new = [torch.empty(rotary.d, dtype=torch.float32, device=q.device) for _ in range(2)]
+        new = _outputs(dev, q.device, stream, (None, (2, *wd), f32))[0]
         dq_weight = new[0] if dq_weight is None else dq_weight
         dk_weight = new[1] if dk_weight is None else dk_weight
-    pwq = _vector(dq_weight, "dq_weight", rotary._dev, torch.float32, (rotary.d,))
-    pwk = None if k is None else _vector(dk_weight, "dk_weight", rotary._dev, torch.float32,
-                                         (rotary.d,))
-    workspace = _packed_workspace(workspace, FA_NORM_WORKSPACE, rotary._dev, stream, q.device)
-    none = k is None
-    refs = _refs(rotary, (dq, "dq", q.shape), (None if none else dk, "dk", ks), (q, "q", q.shape),
-                 (k, "k", ks), (dq_in, "dq_in", q.shape), (None if none else dk_in, "dk_in", ks))
-    _call(rotary._dev, library().fa_norm_rotary_backward, stream, rotary._ref, *refs, pwq, pwk,
-          pos, wq, wk, wfmt, float(eps), B, N, rotary.d, workspace.data_ptr(), workspace.numel())
-    return dq_in, (None if none else dk_in), dq_weight, (None if none else dk_weight)
+    pwq = _vector(dq_weight, "dq_weight", dev, f32, wd)
+    workspace = _packed_workspace(workspace, FA_NORM_WORKSPACE, dev, stream, q.device)
+    hk = hg = ho = pwk = None
+    if k is None:
+        dk_weight = None
+    else:
+        pwk = _vector(dk_weight, "dk_weight", dev, f32, wd)
+        hk, hg = _heads(k, "k", dev, ks), _heads(dk, "dk", dev, ks)
+        ho = _heads(dk_in, "dk_in", dev, ks)
+    _call(dev, library().fa_norm_rotary_backward, stream, rotary._ref,
+          _heads(dq, "dq", dev, qs), hg, _heads(q, "q", dev, qs), hk,
+          _heads(dq_in, "dq_in", dev, qs), ho, pwq, pwk, pos, wq, wk, wfmt, eps, B, N, rotary.d,
+          workspace.data_ptr(), workspace.numel())
+    return dq_in, dk_in, dq_weight, dk_weight
 
 
 def fa_backward_workspace_size(B: int, H: int, N: int, d: int) -> int:

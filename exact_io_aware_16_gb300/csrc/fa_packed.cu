@@ -621,22 +621,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
 
 template <int D, bool CAUSAL>
 cudaError_t launch_t(const FwdParams& p, unsigned blocks, cudaStream_t s) {
-  auto kern = fa_packed_fwd_kernel<D, CAUSAL>;
-  constexpr uint32_t smem = FwdLayout<D>::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  // started while the plan still runs, for which it waits (griddepcontrol.wait)
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(blocks);
-  c.blockDim = dim3(kFwdThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = &at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, p);
+  static std::atomic<unsigned long long> ready;
+  return launch_behind(fa_packed_fwd_kernel<D, CAUSAL>, p, blocks, kFwdThreads, FwdLayout<D>::kSmem, ready, s);
 }
 
 int bucket_shift(long long most) {

@@ -20,6 +20,7 @@
 // keys, next to each other.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -110,6 +111,34 @@ struct PackedPlanArgs {
   CUtensorMap* maps;
   PackedEntry* list[2];
 };
+
+// Launches `kern` (one CTA an SM, all of its shared memory dynamic) while the kernel before it in
+// the stream still runs, for which it waits itself (griddepcontrol.wait).  `ready` says for which
+// devices the shared memory has been asked for: that call is as long as a launch.
+template <typename Kern, typename Params>
+cudaError_t launch_behind(Kern kern, const Params& p, unsigned blocks, unsigned threads, uint32_t smem,
+                          std::atomic<unsigned long long>& ready, cudaStream_t s) {
+  if (blocks == 0) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, p);
+}
 
 cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward,
                                cudaStream_t s);

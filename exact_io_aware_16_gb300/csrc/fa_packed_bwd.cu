@@ -926,35 +926,18 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
   bwd_teardown(bars, warp, tmem);
 }
 
-// Launched while the kernel before it still runs, for which it waits (griddepcontrol.wait).
-template <typename Kern>
-cudaError_t launch_after(Kern kern, const BwdParams& p, unsigned blocks, uint32_t smem, cudaStream_t s) {
-  if (blocks == 0) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(blocks);
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = &at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, p);
-}
-
 template <int D, bool CAUSAL>
 cudaError_t launch_t(BwdParams p, const PackedEntry* const list[2], const int chunk[2], unsigned dq_blocks,
                      unsigned dk_blocks, cudaStream_t s) {
+  static std::atomic<unsigned long long> ready[2];
   p.list = list[0];
   p.chunk = chunk[0];
-  const cudaError_t e = launch_after(fa_packed_dq_kernel<D, CAUSAL>, p, dq_blocks, DqLayout<D>::kSmem, s);
+  const cudaError_t e =
+      launch_behind(fa_packed_dq_kernel<D, CAUSAL>, p, dq_blocks, kThreads, DqLayout<D>::kSmem, ready[0], s);
   if (e != cudaSuccess) return e;
   p.list = list[1];
   p.chunk = chunk[1];
-  return launch_after(fa_packed_dkdv_kernel<D, CAUSAL>, p, dk_blocks, DkLayout<D>::kSmem, s);
+  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL>, p, dk_blocks, kThreads, DkLayout<D>::kSmem, ready[1], s);
 }
 
 }  // namespace
