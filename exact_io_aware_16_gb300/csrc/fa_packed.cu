@@ -169,8 +169,10 @@ template <int D>
 struct FwdLayout {
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kTileBytes = 128u * D * 2;
-  static constexpr uint32_t kQ = 0;  // two Q tiles
-  static constexpr uint32_t kK = kQ + 2 * kTileBytes;
+  // two Q tiles; at d = 64 there is room for the next item's
+  static constexpr int kQBufs = D == 64 ? 2 : 1;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + kQBufs * 2 * kTileBytes;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
   static constexpr uint32_t kBar = kV + kStages * kTileBytes;
   static constexpr uint32_t kSmemUsed = kBar + 512 + 1024;  // + align slack
@@ -182,11 +184,11 @@ struct FwdLayout {
 };
 
 struct FwdBars {
-  uint64_t q_full;
+  uint64_t q_full[2];
   uint64_t k_full[kStages], k_empty[kStages];
   uint64_t v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_ready[2], pv_done[2];
-  uint64_t q_empty;    // the S products of an item are done with the Q tiles
+  uint64_t q_empty[2]; // the S products of an item are done with the Q tiles
   uint64_t item_full[kPackedRing], item_empty[kPackedRing];
   uint64_t turn[2];    // the other tile's products of a step are issued
   uint64_t o_free[2];  // softmax warpgroup g has read its O for the epilogue
@@ -242,7 +244,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 2);  // the two MMA warps
@@ -250,13 +251,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       mbar_init(&bars->v_empty[s], 2);
     }
     for (int g = 0; g < 2; ++g) {
+      mbar_init(&bars->q_full[g], 1);
+      mbar_init(&bars->q_empty[g], 2);
       mbar_init(&bars->s_full[g], 1);
       mbar_init(&bars->p_ready[g], 128);
       mbar_init(&bars->pv_done[g], 1);
       mbar_init(&bars->o_free[g], 128);
       mbar_init(&bars->turn[g], 1);
     }
-    mbar_init(&bars->q_empty, 2);
     for (int r = 0; r < kPackedRing; ++r) {
       mbar_init(&bars->item_full[r], 1);
       mbar_init(&bars->item_empty[r], 258);  // the softmax threads and the MMA warps
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
   }
   // rows that no box fills stay zero
   if (p.P * p.TT < 128) {
-    for (uint32_t i = threadIdx.x; i < 2 * L::kTileBytes / 16; i += kFwdThreads)
+    for (uint32_t i = threadIdx.x; i < 2 * L::kQBufs * L::kTileBytes / 16; i += kFwdThreads)
       reinterpret_cast<uint4*>(smem + L::kQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
@@ -309,20 +311,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         tensormap_acquire(maps + 1);
         tensormap_acquire(maps + 2);
         const int kh = it.head / p.per_kv, qh = it.head, pair = it.e.tile;
+        const int qb = tl % L::kQBufs;
         auto load_q = [&]() {
-          mbar_arrive_expect_tx(&bars->q_full, ((n0 > 0) + (n1 > 0)) * q_bytes);
+          mbar_arrive_expect_tx(&bars->q_full[qb], ((n0 > 0) + (n1 > 0)) * q_bytes);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if ((g ? n1 : n0) == 0) continue;
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c)
-              tma_load_4d(smem + L::kQ + g * L::kTileBytes + c * 16384, maps, &bars->q_full, c * 64, 0,
-                          (2 * pair + g) * p.TT, qh);
+              tma_load_4d(smem + L::kQ + (2 * qb + g) * L::kTileBytes + c * 16384, maps, &bars->q_full[qb], c * 64,
+                          0, (2 * pair + g) * p.TT, qh);
           }
         };
-        // a CTA's first item: Q right away; later ones: the first K tile first (its ring slot
-        // is free early), then Q once the previous item's products are done with it
-        if (tl == 0) load_q();
+        // a CTA's first items: Q right away; later ones: the first K tile first (its ring slot
+        // is free early), then Q once the products of the buffer's last item are done with it
+        if (tl < L::kQBufs) load_q();
         bool ok = true;
         PackedItem next = it;
         for (int j = 0; j < nmax; ++j) {
@@ -334,8 +337,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
           for (int c = 0; c < L::kChunks; ++c)
             tma_load_3d(smem + L::kK + s * L::kTileBytes + c * 16384, maps + 1, &bars->k_full[s], c * 64,
                         j * 128, kh);
-          if (j == 0 && tl > 0) {
-            if (!(ok = wait(&bars->q_empty, (tl - 1) & 1, 0x103))) break;
+          if (j == 0 && tl >= L::kQBufs) {
+            if (!(ok = wait(&bars->q_empty[qb], (tl / L::kQBufs - 1) & 1, 0x103))) break;
             load_q();
           }
           if (!(ok = wait(&bars->v_empty[s], ph ^ 1, 0x102))) break;
@@ -367,7 +370,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
     const uint32_t tm = uniform(tmem), sc = tm + uniform(L::s_col(g)), oc = tm + uniform(L::o_col(g));
-    const uint32_t qbase = uniform(smem_u32(smem + L::kQ) + g * L::kTileBytes);
+    const uint32_t q0 = uniform(smem_u32(smem + L::kQ) + g * L::kTileBytes);
+    uint32_t qbase = q0;
     const uint32_t sK = uniform(smem_u32(smem + L::kK)), sV = uniform(smem_u32(smem + L::kV));
     auto wait = [&](uint64_t* bar, uint32_t par, uint32_t code) { return all_wait(bar, par, bars, code); };
     auto issue_s = [&](int slot) {
@@ -406,7 +410,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       const int n = uniform(item_tiles(it, g, p.TT, CAUSAL));
       const int nmax = max(n, uniform(item_tiles(it, 1 - g, p.TT, CAUSAL)));
       if (nmax == 0) continue;
-      if (!wait(&bars->q_full, tl & 1, 0x201) || !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202) || !turn())
+      const int qb = tl % L::kQBufs;
+      qbase = q0 + qb * 2 * L::kTileBytes;
+      if (!wait(&bars->q_full[qb], (tl / L::kQBufs) & 1, 0x201) || !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202) || !turn())
         break;
       tc_fence_after_sync();
       if (elect_one()) {
@@ -442,7 +448,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         __syncwarp();
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&bars->q_empty);
+      if (elect_one()) umma_commit(&bars->q_empty[qb]);
       kvb += nmax;
       ++tl;
       base += n;

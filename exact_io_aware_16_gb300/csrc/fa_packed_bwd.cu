@@ -433,16 +433,36 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
     const int box = tr >> 6, box_tok = (tr & 63) / p.P, row_head = (tr & 63) - box_tok * p.P;
     const bool row_in = box_tok < p.TT64;
     const int row_tok = box * p.TT64 + box_tok;
-    // (an item's parts have been read by all threads before any gets to the next: its last dS,
-    // without which its dQ is not done, comes after)
+    // (an item's parts have been read by all threads before any writes the next's: it has waited
+    // for the item's dQ, which needs the last dS of all)
     float* dx = reinterpret_cast<float*>(smem + L::kDx);
     int nb = 0, tl = 0;  // steps and items with products so far
+    // dQ of the item before: stored when the next one's Q and dO lie in tensor memory, so that its
+    // first products run meanwhile
+    bool pending = false;
+    long long pending_at = -1;
+    auto epilogue = [&]() {
+      if (!pending) return true;
+      if (!warp_wait(&bars->acc_done, (tl - 1) & 1, bars, 0x312)) return false;
+      tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        store_acc32(tm + L::kAcc + (D / 2) * g + c * 32, p.scale, p.dq + c * 32, pending_at);
+      // the accumulator has been read: the next item may overwrite it
+      tc_fence_before_sync();
+      mbar_arrive(&bars->acc_free);
+      pending = false;
+      return true;
+    };
     for (int ti = 0;; ++ti) {
       const int r = ti % kBwdRing;
       if (!warp_wait(&bars->item_full[r], (ti / kBwdRing) & 1, bars, 0x304)) break;
       const PackedItem it = bars->item[r];
       mbar_arrive(&bars->item_empty[r]);
-      if (it.head < 0) break;
+      if (it.head < 0) {
+        epilogue();
+        break;
+      }
       const int n = dq_tiles(it, p.TT, CAUSAL);
       const int tok0 = it.e.tile * p.TT, tok = tok0 + row_tok;
       const bool valid = row_in && tok < it.e.n;
@@ -456,9 +476,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
         }
         continue;
       }
-      // a row without keys of its own, or behind the sequence: P = 2^-inf
-      float lse2 = valid ? p.lse[vec] * kLog2e : INFINITY;
-      if (lse2 == -INFINITY) lse2 = INFINITY;
+      // asked for here, used below
+      float lse = valid ? p.lse[vec] : INFINITY;
+      uint4 o_row[D / 16];
+      if (n > 1 && valid) {
+        const uint4* a = reinterpret_cast<const uint4*>(p.o + token * p.o_token + head * p.o_head + (D / 2) * g);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) o_row[e] = a[e];
+      }
       bool ok = true;
       float Di = 0.0f;
       // the halves' parts of D meet in shared memory
@@ -471,23 +496,21 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       // Q and dO to tensor memory: the products of the item before that read them are done (its
       // last scores and dP have been waited for)
       if (!warp_wait(&bars->res_full, tl & 1, bars, 0x315)) break;
-      uint32_t w[D / 4];
-      load_half_row<D>(smem + L::kQ, tr, g, valid, w);
-      store_half_row<D>(tm + L::kQA, g, w);
-      load_half_row<D>(smem + L::kDO, tr, g, valid, w);
-      store_half_row<D>(tm + L::kDOA, g, w);
-      mbar_arrive(&bars->res_empty);
-      tmem_st_wait();
-      tc_fence_before_sync();
-      mbar_arrive(&bars->a_ready);
-      if (n > 1) {
-        float part = 0.0f;
-        if (valid) {
-          const uint4* a = reinterpret_cast<const uint4*>(p.o + token * p.o_token + head * p.o_head + (D / 2) * g);
+      float part = 0.0f;
+      {
+        uint32_t w[D / 4];
+        load_half_row<D>(smem + L::kQ, tr, g, valid, w);
+        store_half_row<D>(tm + L::kQA, g, w);
+        load_half_row<D>(smem + L::kDO, tr, g, valid, w);
+        store_half_row<D>(tm + L::kDOA, g, w);
+        mbar_arrive(&bars->res_empty);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&bars->a_ready);
+        if (n > 1 && valid) {
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
-            const uint4 x = a[e];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t xs[4] = {o_row[e].x, o_row[e].y, o_row[e].z, o_row[e].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               part = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(w[4 * e + i] << 16), part);
@@ -495,9 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
             }
           }
         }
+      }
+      if (!epilogue()) break;
+      if (n > 1) {
         join(part);
         if (!ok) break;
       }
+      // a row without keys of its own, or behind the sequence: P = 2^-inf
+      const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
       const uint32_t col0 = 32u * g;
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
       for (int j = 0; j < n; ++j) {
@@ -558,15 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       }
       if (!ok) break;
       if (g == 0 && valid) p.D[vec] = Di;
-      if (!warp_wait(&bars->acc_done, tl & 1, bars, 0x312)) break;
-      tc_fence_after_sync();
-      const long long at = valid ? token * p.dq_token + head * p.dq_head + (D / 2) * g : -1;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        store_acc32(tm + L::kAcc + (D / 2) * g + c * 32, p.scale, p.dq + c * 32, at);
-      // the accumulator has been read: the next item may overwrite it
-      tc_fence_before_sync();
-      mbar_arrive(&bars->acc_free);
+      pending = true;
+      pending_at = valid ? token * p.dq_token + head * p.dq_head + (D / 2) * g : -1;
       nb += n;
       ++tl;
     }
@@ -801,12 +822,33 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
     const uint32_t tm = tmem + lane_off;
     const uint32_t col0 = 32u * g;
     int nb = 0, tl = 0;
+    // dV and dK of the item before: stored when the next one's K and V lie in tensor memory
+    bool pending = false;
+    long long pending_k = -1, pending_v = -1;
+    auto epilogue = [&]() {
+      if (!pending) return true;
+      if (!warp_wait(&bars->acc_done, (tl - 1) & 1, bars, 0x302)) return false;
+      tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        store_acc32(tm + L::kAcc0 + (D / 2) * g + c * 32, 1.0f, p.dv + c * 32, pending_v);
+        store_acc32(tm + L::kAcc1 + (D / 2) * g + c * 32, p.scale, p.dk + c * 32, pending_k);
+      }
+      // the accumulators have been read: the next item may overwrite them
+      tc_fence_before_sync();
+      mbar_arrive(&bars->acc_free);
+      pending = false;
+      return true;
+    };
     for (int ti = 0;; ++ti) {
       const int r = ti % kBwdRing;
       if (!warp_wait(&bars->item_full[r], (ti / kBwdRing) & 1, bars, 0x305)) break;
       const PackedItem it = bars->item[r];
       mbar_arrive(&bars->item_empty[r]);
-      if (it.head < 0) break;
+      if (it.head < 0) {
+        epilogue();
+        break;
+      }
       const int first = dk_first(it, TT, CAUSAL), per = dk_tiles(it, TT, CAUSAL), n = per * p.per_kv;
       const int key = it.e.tile * 128 + tr;
       const bool valid = key < it.e.m;
@@ -834,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars->a_ready);
+      if (!epilogue()) break;
       bool ok = true;
       int tile = first;
       // causal: query token i sees the key where i >= key - (m - n)
@@ -909,16 +952,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
         mbar_arrive(&bars->ds_ready[L::buf(step)]);
         if (++tile == first + per) tile = first;
       }
-      if (!ok || !warp_wait(&bars->acc_done, tl & 1, bars, 0x302)) break;
-      tc_fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        store_acc32(tm + L::kAcc0 + (D / 2) * g + c * 32, 1.0f, p.dv + c * 32, at_v);
-        store_acc32(tm + L::kAcc1 + (D / 2) * g + c * 32, p.scale, p.dk + c * 32, at_k);
-      }
-      // the accumulators have been read: the next item may overwrite them
-      tc_fence_before_sync();
-      mbar_arrive(&bars->acc_free);
+      if (!ok) break;
+      pending = true;
+      pending_k = at_k;
+      pending_v = at_v;
       nb += n;
       ++tl;
     }
