@@ -48,7 +48,7 @@ __device__ __forceinline__ int bucket_of(const PackedPlanArgs& a, int which, con
     cost = (packed_keys(last, s.n, s.m, a.causal) + 127) >> 7;
   } else {
     // the first query that sees the tile's first key
-    const int first = a.causal ? max(t * 128 - (s.m - s.n), 0) : 0;
+    const int first = a.causal ? max(t * a.k_span - (s.m - s.n), 0) : 0;
     cost = s.n > first ? (s.n + a.TT64 - 1) / a.TT64 - first / a.TT64 : 0;
   }
   return min(cost >> a.shift[which], kBuckets - 1);
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
     for (int b0 = warp * each; b0 < a.B; b0 += each * (kPlanThreads / 32)) {
       Span mine = {0, 0, 0, 0};
       if (lane < each && b0 + lane < a.B) mine = span_of(a, b0 + lane);
-      const int own = which == 0 ? (mine.n + a.q_span - 1) / a.q_span : (mine.m + 127) >> 7;
+      const int own = which == 0 ? (mine.n + a.q_span - 1) / a.q_span : (mine.m + a.k_span - 1) / a.k_span;
       unsigned left = __ballot_sync(0xffffffffu, own > 0);
       while (left) {
         const int src = __ffs(left) - 1;
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
 template <int D, bool CAUSAL>
 cudaError_t launch_t(const FwdParams& p, unsigned blocks, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_fwd_kernel<D, CAUSAL>, p, blocks, kFwdThreads, FwdLayout<D>::kSmem, ready, s);
+  return launch_behind(fa_packed_fwd_kernel<D, CAUSAL>, p, blocks, kFwdThreads, FwdLayout<D>::kSmem, 1, ready, s);
 }
 
 int bucket_shift(long long most) {
@@ -639,8 +639,8 @@ int bucket_shift(long long most) {
 
 }  // namespace
 
-cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward,
-                               cudaStream_t s) {
+cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward, int q_tiles,
+                               int k_tiles, cudaStream_t s) {
   const int Hq = a.q.heads, Hkv = a.k.heads;
   const PackedTiling t = packed_tiling(Hq, Hkv);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, Hq, Hkv, backward);
@@ -659,11 +659,12 @@ cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int
   p.total_q = a.total_q;
   p.total_k = a.total_k;
   p.causal = a.causal;
-  p.q_span = 2 * (backward ? t.TT64 : t.TT);
+  p.q_span = q_tiles * (backward ? 2 * t.TT64 : t.TT);
+  p.k_span = k_tiles * 128;
   p.TT64 = t.TT64;
   p.nlists = backward ? 2 : 1;
   p.most[0] = static_cast<unsigned>(a.total_q / p.q_span + a.B);
-  p.most[1] = static_cast<unsigned>(a.total_k / 128 + a.B);
+  p.most[1] = static_cast<unsigned>(a.total_k / p.k_span + a.B);
   p.shift[0] = bucket_shift(a.total_k / 128 + 1);
   p.shift[1] = bucket_shift(a.total_q / t.TT64 + 1);
   p.header = reinterpret_cast<PackedHeader*>(ws);
@@ -677,7 +678,7 @@ cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int
 cudaError_t launch_forward_packed(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s) {
   const PackedTiling t = packed_tiling(a.q.heads, a.k.heads);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, a.q.heads, a.k.heads, false);
-  cudaError_t e = launch_packed_plan(a, maps, 3, false, s);
+  cudaError_t e = launch_packed_plan(a, maps, 3, false, 2, 1, s);
   if (e != cudaSuccess) return e;
   char* ws = static_cast<char*>(a.workspace);
   FwdParams p{};

@@ -106,8 +106,9 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 }
 
 // Barriers and tensor memory; rows of [zero, zero + bytes) that no box fills are zeroed.
-// Returns false (for the whole CTA) when an earlier CTA recorded a timeout.
 // `users`: MMA warps whose products read a stage, and which write an accumulator.
+// Returns false (for the whole cluster) when an earlier CTA recorded a timeout.
+template <int CL>
 __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t* smem, uint8_t* zero,
                                          uint32_t bytes, int users) {
   if (threadIdx.x == 0) {
@@ -118,9 +119,9 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
     mbar_init(&bars->a_ready, kCompute);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->x_full[s], 1);
-      mbar_init(&bars->x_empty[s], users);
+      mbar_init(&bars->x_empty[s], users * CL);  // each CTA reads what all have loaded
       mbar_init(&bars->y_full[s], 1);
-      mbar_init(&bars->y_empty[s], 1);
+      mbar_init(&bars->y_empty[s], CL);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
@@ -135,7 +136,8 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
     mbar_init(&bars->acc_free, kCompute);
     for (int r = 0; r < kBwdRing; ++r) {
       mbar_init(&bars->item_full[r], 1);
-      mbar_init(&bars->item_empty[r], kCompute + 2);  // compute threads and the MMA warps
+      // the compute and MMA warps; the first CTA's holds those of the second, and its TMA warp
+      mbar_init(&bars->item_empty[r], CL * (kCompute / 32 + 2) + CL - 1);
     }
     mbar_init(&bars->drain, 2);
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_packed_bwd_error) != 0) ? 1 : 0;
@@ -146,8 +148,16 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
       reinterpret_cast<uint4*>(zero)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
-  __syncthreads();
-  if (bars->abort_flag) return false;
+  if constexpr (CL == 1) {
+    __syncthreads();
+    if (bars->abort_flag) return false;
+  } else {
+    cluster_sync();
+    const int other = cluster_load(cluster_map(&bars->abort_flag, cluster_rank() ^ 1u));
+    const bool stop = bars->abort_flag != 0 || other != 0;
+    cluster_sync();  // the flags have been read before either CTA leaves or raises one
+    if (stop) return false;
+  }
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
@@ -158,6 +168,48 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
   return true;
 }
 
+// An item for every role of the cluster: written where each CTA looks for it (by the first CTA's
+// producer), waited for, and given back once it has been read (by whole warps).
+template <int CL>
+__device__ __forceinline__ void item_publish(BwdBars* bars, int r, const PackedItem& it) {
+  bars->item[r] = it;
+  if constexpr (CL == 2) {
+    const uint4* w = reinterpret_cast<const uint4*>(&it);
+    const uint32_t to = cluster_map(&bars->item[r], 1);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) cluster_store16(to + 16 * i, w[i]);
+    cluster_arrive(cluster_map(&bars->item_full[r], 1));
+  }
+  mbar_arrive(&bars->item_full[r]);
+}
+template <int CL>
+__device__ __forceinline__ bool item_wait(BwdBars* bars, int t, uint32_t code) {
+  const int r = t % kBwdRing;
+  const uint32_t par = (t / kBwdRing) & 1;
+  bool ok = wait(&bars->item_full[r], par, bars, code);
+  if (CL == 2 && ok) ok = cluster_try_wait(&bars->item_full[r], par);  // (over: for what it lets see)
+  return __all_sync(0xffffffffu, ok);
+}
+template <int CL>
+__device__ __forceinline__ void item_done(BwdBars* bars, int r) {
+  __syncwarp();
+  if (lane_id() == 0) {
+    if constexpr (CL == 2)
+      cluster_arrive(cluster_map(&bars->item_empty[r], 0));
+    else
+      mbar_arrive(&bars->item_empty[r]);
+  }
+}
+
+template <int CL>
+__device__ __forceinline__ void commit_stage(uint64_t* bar) {
+  if constexpr (CL == 2)
+    umma_commit_all(bar, 3);
+  else
+    umma_commit(bar);
+}
+
+template <int CL>
 __device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t tmem) {
   if (warp == kMmaWarp) wait(&bars->drain, 0, bars, 0x2ff);
   if (bars->abort_flag) {
@@ -167,7 +219,10 @@ __device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t t
     }
   }
   tc_fence_before_sync();
-  __syncthreads();
+  if constexpr (CL == 2)
+    cluster_sync();  // nothing of the other CTA's writes or arrives here any more
+  else
+    __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
@@ -271,73 +326,96 @@ struct DqLayout {
 };
 static_assert(DqLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
+// Key tiles of an item, whose entry holds `TT` query tokens (with two CTAs those of both: they go
+// through the same tiles, and what only one of them sees is masked in the other).
 __device__ __forceinline__ int dq_tiles(const PackedItem& it, int TT, bool causal) {
   return (packed_keys(min((it.e.tile + 1) * TT, it.e.n) - 1, it.e.n, it.e.m, causal) + 63) >> 6;
 }
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, int CL>
 __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = DqLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (!bwd_init(bars, warp, smem, smem, 0, 1)) return;
+  const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
+  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
   grid_dependency_launch();
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {
-      const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT64) * 128u * L::kChunks;
-      int kvb = 0, tl = 0;  // key tiles and items with loads so far
-      PackedItem it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
-      for (int t = 0;; ++t) {
-        const int r = t % kBwdRing;
-        if (!wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
-        bars->item[r] = it;
-        mbar_arrive(&bars->item_full[r]);
-        if (it.head < 0) break;
-        const int n = dq_tiles(it, p.TT, CAUSAL);
-        if (n == 0) {
-          it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
-          continue;
-        }
+    // Of two CTAs the first takes the items and loads keys for both, the second values.
+    const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT64) * 128u * L::kChunks;
+    int kvb = 0, tl = 0;  // key tiles and items with loads so far
+    auto claim = [&]() {
+      PackedItem x;
+      x.head = -1;
+      if (rank == 0 && lane == 0) x = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
+      return x;
+    };
+    PackedItem it = claim();
+    for (int t = 0;; ++t) {
+      const int r = t % kBwdRing;
+      if (rank == 0) {
+        if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
+        if (lane == 0) item_publish<CL>(bars, r, it);
+        __syncwarp();
+        it = bars->item[r];
+        __syncwarp();
+      } else {
+        if (!item_wait<CL>(bars, t, 0x105)) break;
+        it = bars->item[r];
+        item_done<CL>(bars, r);
+      }
+      if (it.head < 0) break;
+      const int n = dq_tiles(it, CL * p.TT, CAUSAL);
+      if (n == 0) {
+        it = claim();
+        continue;
+      }
+      if (tl > 0 && !warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x103)) break;
+      bool ok = true;
+      PackedItem next = it;
+      if (lane == 0) {
         const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
 #pragma unroll
         for (int i = 0; i < 4; ++i) tensormap_acquire(maps + i);
         const int kh = it.head / p.per_kv;
-        if (tl > 0 && !wait(&bars->res_empty, (tl - 1) & 1, bars, 0x103)) break;
         mbar_arrive_expect_tx(&bars->res_full, 4 * q_bytes);
 #pragma unroll
         for (int c = 0; c < 2 * L::kChunks; ++c) {  // two boxes of 64 rows a column
-          const int col = c >> 1, half = c & 1, tok = it.e.tile * p.TT + half * p.TT64;
+          const int col = c >> 1, half = c & 1, tok = (it.e.tile * CL + rank) * p.TT + half * p.TT64;
           const uint32_t at = col * 16384 + half * 8192;
           tma_load_4d(smem + L::kQ + at, maps, &bars->res_full, col * 64, 0, tok, it.head);
           tma_load_4d(smem + L::kDO + at, maps + 3, &bars->res_full, col * 64, 0, tok, it.head);
         }
-        PackedItem next = it;
-        bool ok = true;
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int j) {
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c) {
+            if constexpr (CL == 2)
+              tma_load_3d_all(dst + c * 8192, map, bar, c * 64, j * 64, kh, 3);
+            else
+              tma_load_3d(dst + c * 8192, map, bar, c * 64, j * 64, kh);
+          }
+        };
         for (int j = 0; j < n; ++j) {
           const int s = (kvb + j) % kStages;
           const uint32_t par = (((kvb + j) / kStages) & 1) ^ 1;
           if (!(ok = wait(&bars->x_empty[s], par, bars, 0x101))) break;
           mbar_arrive_expect_tx(&bars->x_full[s], L::kTile);
-#pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(smem + L::kK + s * L::kTile + c * 8192, maps + 1, &bars->x_full[s], c * 64, j * 64, kh);
+          if (CL == 1 || rank == 0) load(smem + L::kK + s * L::kTile, maps + 1, &bars->x_full[s], j);
           if (!(ok = wait(&bars->y_empty[s], par, bars, 0x102))) break;
           mbar_arrive_expect_tx(&bars->y_full[s], L::kTile);
-#pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(smem + L::kV + s * L::kTile + c * 8192, maps + 2, &bars->y_full[s], c * 64, j * 64, kh);
+          if (CL == 1 || rank == 1) load(smem + L::kV + s * L::kTile, maps + 2, &bars->y_full[s], j);
           // the next item is asked for while the last tiles are under way
-          if (j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
+          if (rank == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
         }
-        if (!ok) break;
-        kvb += n;
-        ++tl;
-        it = next;
       }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      kvb += n;
+      ++tl;
+      it = next;
     }
     __syncwarp();
   } else if (warp >= kMmaWarp) {
@@ -360,20 +438,18 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
           umma_ts(tm + L::dp_col(pos), tm + L::kDOA + kk * 8, kmajor_desc(sV + s * L::kTile, kk), idesc_s,
                   kk > 0 ? 1u : 0u);
         umma_commit(&bars->dp_full[pos & 1]);
-        umma_commit(&bars->y_empty[s]);
+        commit_stage<CL>(&bars->y_empty[s]);
       }
       __syncwarp();
       return true;
     };
     int kvb = 0, tl = 0;
     for (int t = 0;; ++t) {
-      const int r = t % kBwdRing;
-      if (!warp_wait(&bars->item_full[r], (t / kBwdRing) & 1, bars, 0x21b)) break;
-      const PackedItem it = bars->item[r];
-      __syncwarp();
-      if (elect_one()) mbar_arrive(&bars->item_empty[r]);
+      if (!item_wait<CL>(bars, t, 0x21b)) break;
+      const PackedItem it = bars->item[t % kBwdRing];
+      item_done<CL>(bars, t % kBwdRing);
       if (uniform(it.head) < 0) break;
-      const int n = uniform(dq_tiles(it, p.TT, CAUSAL));
+      const int n = uniform(dq_tiles(it, CL * p.TT, CAUSAL));
       if (n == 0) continue;
       if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x210)) break;
       bool ok = true;
@@ -412,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
             for (int kk = 0; kk < 4; ++kk)
               umma_ts(tm + L::kAcc, tm + L::dp_col(pos) + packed_a_col(kk), mnmajor_desc(sK + s * L::kTile, kk),
                       idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&bars->x_empty[s]);
+            commit_stage<CL>(&bars->x_empty[s]);
             if (j + 1 == n) umma_commit(&bars->acc_done);
           }
           __syncwarp();
@@ -455,16 +531,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       return true;
     };
     for (int ti = 0;; ++ti) {
-      const int r = ti % kBwdRing;
-      if (!warp_wait(&bars->item_full[r], (ti / kBwdRing) & 1, bars, 0x304)) break;
-      const PackedItem it = bars->item[r];
-      mbar_arrive(&bars->item_empty[r]);
+      if (!item_wait<CL>(bars, ti, 0x304)) break;
+      const PackedItem it = bars->item[ti % kBwdRing];
+      item_done<CL>(bars, ti % kBwdRing);
       if (it.head < 0) {
         epilogue();
         break;
       }
-      const int n = dq_tiles(it, p.TT, CAUSAL);
-      const int tok0 = it.e.tile * p.TT, tok = tok0 + row_tok;
+      const int n = dq_tiles(it, CL * p.TT, CAUSAL);
+      const int tok0 = (it.e.tile * CL + rank) * p.TT, tok = tok0 + row_tok;
       const bool valid = row_in && tok < it.e.n;
       const int head = it.head * p.P + row_head, m = it.e.m, off = m - it.e.n;
       const long long token = it.e.q0 + tok;
@@ -592,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       ++tl;
     }
   }
-  bwd_teardown(bars, warp, tmem);
+  bwd_teardown<CL>(bars, warp, tmem);
 }
 
 // ============================================================ dK / dV
@@ -618,23 +693,24 @@ struct DkLayout {
 };
 static_assert(DkLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
-// Query tiles (of 64 rows, TT tokens) of a head group that see the item's key tile: the first, and
+// Query tiles (of 64 rows, TT tokens) of a head group that see the item's `keys` keys: the first, and
 // how many.
-__device__ __forceinline__ int dk_first(const PackedItem& it, int TT, bool causal) {
-  return causal ? max(it.e.tile * 128 - (it.e.m - it.e.n), 0) / TT : 0;
+__device__ __forceinline__ int dk_first(const PackedItem& it, int keys, int TT, bool causal) {
+  return causal ? max(it.e.tile * keys - (it.e.m - it.e.n), 0) / TT : 0;
 }
-__device__ __forceinline__ int dk_tiles(const PackedItem& it, int TT, bool causal) {
-  return max((it.e.n + TT - 1) / TT - dk_first(it, TT, causal), 0);
+__device__ __forceinline__ int dk_tiles(const PackedItem& it, int keys, int TT, bool causal) {
+  return max((it.e.n + TT - 1) / TT - dk_first(it, keys, TT, causal), 0);
 }
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, int CL>
 __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using L = DkLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int TT = p.TT64;
-  if (!bwd_init(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 2)) return;
+  if (!bwd_init<CL>(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 2)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
 
@@ -647,22 +723,31 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       row_head[e] = lane + 32 * e - row_tok[e] * p.P;
     }
     int sb = 0, tl = 0;
-    PackedItem it;
-    if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
+    // Of two CTAs the first takes the items and loads queries for both, the second dO.
+    auto claim = [&]() {
+      PackedItem x;
+      x.head = -1;
+      if (rank == 0 && lane == 0) x = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
+      return x;
+    };
+    PackedItem it = claim();
     for (int t = 0;; ++t) {
       const int r = t % kBwdRing;
-      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
-      if (lane == 0) {
-        bars->item[r] = it;
-        mbar_arrive(&bars->item_full[r]);
+      if (rank == 0) {
+        if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
+        if (lane == 0) item_publish<CL>(bars, r, it);
+        __syncwarp();
+        it = bars->item[r];
+        __syncwarp();
+      } else {
+        if (!item_wait<CL>(bars, t, 0x105)) break;
+        it = bars->item[r];
+        item_done<CL>(bars, r);
       }
-      __syncwarp();
-      it = bars->item[r];
-      __syncwarp();
       if (it.head < 0) break;
-      const int first = dk_first(it, TT, CAUSAL), per = dk_tiles(it, TT, CAUSAL), n = per * p.per_kv;
+      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL), n = per * p.per_kv;
       if (n == 0) {
-        if (lane == 0) it = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
+        it = claim();
         continue;
       }
       const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
@@ -673,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
         mbar_arrive_expect_tx(&bars->res_full, 2 * L::kRes);
 #pragma unroll
         for (int c = 0; c < 2 * L::kChunks; ++c) {  // two boxes of 64 keys a column
-          const int col = c >> 1, half = c & 1, key = it.e.tile * 128 + half * 64;
+          const int col = c >> 1, half = c & 1, key = (it.e.tile * CL + rank) * 128 + half * 64;
           tma_load_3d(smem + L::kK + col * 16384 + half * 8192, maps + 1, &bars->res_full, col * 64, key, it.head);
           tma_load_3d(smem + L::kV + col * 16384 + half * 8192, maps + 2, &bars->res_full, col * 64, key, it.head);
         }
@@ -705,8 +790,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
           mbar_expect_tx(&bars->x_full[s], 2 * q_bytes);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c) {
-            tma_load_4d(smem + L::kQ + s * L::kTile + c * 8192, maps, &bars->x_full[s], c * 64, 0, tile * TT, group);
-            tma_load_4d(smem + L::kDO + s * L::kTile + c * 8192, maps + 3, &bars->x_full[s], c * 64, 0, tile * TT, group);
+            uint8_t* q = smem + L::kQ + s * L::kTile + c * 8192;
+            uint8_t* o = smem + L::kDO + s * L::kTile + c * 8192;
+            if constexpr (CL == 1) {
+              tma_load_4d(q, maps, &bars->x_full[s], c * 64, 0, tile * TT, group);
+              tma_load_4d(o, maps + 3, &bars->x_full[s], c * 64, 0, tile * TT, group);
+            } else {
+              tma_load_4d_all(rank == 0 ? q : o, rank == 0 ? maps : maps + 3, &bars->x_full[s], c * 64, 0, tile * TT,
+                              group, 3);
+            }
           }
         }
         float* vec = reinterpret_cast<float*>(smem + L::kVec) + s * 128;
@@ -723,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
           ++sub;
         }
         if (j + 1 < n) ask(tile, sub);
-        if (lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
+        if (rank == 0 && lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
       }
       if (!ok) break;
       sb += n;
@@ -763,13 +855,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       if (!L::kDouble) mbar_arrive(&bars->turn[first_chain ? 1 : 0]);
     };
     for (int t = 0;; ++t) {
-      const int r = t % kBwdRing;
-      if (!warp_wait(&bars->item_full[r], (t / kBwdRing) & 1, bars, 0x207)) break;
-      const PackedItem it = bars->item[r];
-      __syncwarp();
-      if (elect_one()) mbar_arrive(&bars->item_empty[r]);
+      if (!item_wait<CL>(bars, t, 0x207)) break;
+      const PackedItem it = bars->item[t % kBwdRing];
+      item_done<CL>(bars, t % kBwdRing);
       if (uniform(it.head) < 0) break;
-      const int n = uniform(dk_tiles(it, TT, CAUSAL)) * p.per_kv;
+      const int n = uniform(dk_tiles(it, CL * 128, TT, CAUSAL)) * p.per_kv;
       if (n == 0) continue;
       if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x201) || !stage_in(sb) || !turn()) break;
       tc_fence_after_sync();
@@ -801,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
           for (int kk = 0; kk < 4; ++kk)
             umma_ts(acc, score0 + 64u * L::buf(pos) + packed_a_col(kk), mnmajor_desc(b_acc + s * L::kTile, kk),
                     idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars->x_empty[s]);
+          commit_stage<CL>(&bars->x_empty[s]);
           if (!more) umma_commit(&bars->acc_done);
           if (!L::kDouble && more) issue_scores(pos + 1);
           pass_turn();
@@ -841,16 +931,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       return true;
     };
     for (int ti = 0;; ++ti) {
-      const int r = ti % kBwdRing;
-      if (!warp_wait(&bars->item_full[r], (ti / kBwdRing) & 1, bars, 0x305)) break;
-      const PackedItem it = bars->item[r];
-      mbar_arrive(&bars->item_empty[r]);
+      if (!item_wait<CL>(bars, ti, 0x305)) break;
+      const PackedItem it = bars->item[ti % kBwdRing];
+      item_done<CL>(bars, ti % kBwdRing);
       if (it.head < 0) {
         epilogue();
         break;
       }
-      const int first = dk_first(it, TT, CAUSAL), per = dk_tiles(it, TT, CAUSAL), n = per * p.per_kv;
-      const int key = it.e.tile * 128 + tr;
+      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL), n = per * p.per_kv;
+      const int key0 = (it.e.tile * CL + rank) * 128, key = key0 + tr;
       const bool valid = key < it.e.m;
       const long long token = it.e.k0 + key;
       const long long at_k = valid ? token * p.dk_token + it.head * p.dk_head + (D / 2) * g : -1;
@@ -881,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       int tile = first;
       // causal: query token i sees the key where i >= key - (m - n)
       const int from = key - (it.e.m - it.e.n);
-      const int last_from = it.e.tile * 128 + 127 - (it.e.m - it.e.n);
+      const int last_from = key0 + 127 - (it.e.m - it.e.n);
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
@@ -960,22 +1049,30 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
       ++tl;
     }
   }
-  bwd_teardown(bars, warp, tmem);
+  bwd_teardown<CL>(bars, warp, tmem);
 }
 
-template <int D, bool CAUSAL>
-cudaError_t launch_t(BwdParams p, const PackedEntry* const list[2], const int chunk[2], unsigned dq_blocks,
-                     unsigned dk_blocks, cudaStream_t s) {
-  static std::atomic<unsigned long long> ready[2];
-  p.list = list[0];
-  p.chunk = chunk[0];
-  const cudaError_t e =
-      launch_behind(fa_packed_dq_kernel<D, CAUSAL>, p, dq_blocks, kThreads, DqLayout<D>::kSmem, ready[0], s);
-  if (e != cudaSuccess) return e;
-  p.list = list[1];
-  p.chunk = chunk[1];
-  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL>, p, dk_blocks, kThreads, DkLayout<D>::kSmem, ready[1], s);
+// Items of a launch as CTAs, at most one an SM.
+unsigned grid_of(long long items, int cluster, int sms) {
+  return static_cast<unsigned>(std::min<long long>(items, sms / cluster)) * cluster;
 }
+
+template <int D, bool CAUSAL, int CL>
+cudaError_t launch_dq(const BwdParams& p, long long items, int sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> ready;
+  return launch_behind(fa_packed_dq_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kThreads, DqLayout<D>::kSmem, CL,
+                       ready, s);
+}
+template <int D, bool CAUSAL, int CL>
+cudaError_t launch_dkdv(const BwdParams& p, long long items, int sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> ready;
+  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kThreads, DkLayout<D>::kSmem, CL,
+                       ready, s);
+}
+
+// Tiles of a sequence, on average, from which two CTAs share what they stream (d = 128): the odd
+// tile at the end of a sequence leaves one of them idle.
+constexpr int kShareTiles = 8;
 
 }  // namespace
 
@@ -983,7 +1080,10 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   const int Hq = a.q.heads, Hkv = a.k.heads;
   const PackedTiling t = packed_tiling(Hq, Hkv);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, Hq, Hkv, true);
-  const cudaError_t e = launch_packed_plan(a, maps, 4, true, s);
+  // CTAs that share a stream: dq, and dk and dv
+  auto share = [&](long long tokens, int tile) { return a.d == 128 && tokens >= 1ll * kShareTiles * tile * a.B ? 2 : 1; };
+  const int cq = share(a.total_q, 2 * t.TT64), ck = share(a.total_k, 128);
+  cudaError_t e = launch_packed_plan(a, maps, 4, true, cq, ck, s);
   if (e != cudaSuccess) return e;
   char* ws = static_cast<char*>(a.workspace);
   auto out = [](const HeadsView& v) { return static_cast<__nv_bfloat16*>(const_cast<void*>(v.p)); };
@@ -1006,18 +1106,25 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   p.Hkv = Hkv;
   p.scale = a.scale;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  const PackedEntry* const list[2] = {reinterpret_cast<const PackedEntry*>(ws + l.list[0]),
-                                      reinterpret_cast<const PackedEntry*>(ws + l.list[1])};
   // the dq kernel streams keys and values, the other the queries and dO of a group's heads
-  const int chunk[2] = {packed_chunk(a.total_k, a.d, Hkv) * t.per_kv,
-                        packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv)};
-  const long long q_items = a.total_q > 0 ? (a.total_q / p.TT + a.B) * static_cast<long long>(t.heads) : 0;
-  const long long k_items = a.total_k > 0 ? (a.total_k / 128 + a.B) * static_cast<long long>(Hkv) : 0;
-  const unsigned nq = static_cast<unsigned>(std::min<long long>(q_items, a.num_sms));
-  const unsigned nk = static_cast<unsigned>(std::min<long long>(k_items, a.num_sms));
+  p.list = reinterpret_cast<const PackedEntry*>(ws + l.list[0]);
+  p.chunk = packed_chunk(a.total_k, a.d, Hkv) * t.per_kv;
+  const long long qi = a.total_q > 0 ? (a.total_q / (1ll * cq * p.TT) + a.B) * t.heads : 0;
   if (a.d == 64)
-    return a.causal ? launch_t<64, true>(p, list, chunk, nq, nk, s) : launch_t<64, false>(p, list, chunk, nq, nk, s);
-  return a.causal ? launch_t<128, true>(p, list, chunk, nq, nk, s) : launch_t<128, false>(p, list, chunk, nq, nk, s);
+    e = a.causal ? launch_dq<64, true, 1>(p, qi, a.num_sms, s) : launch_dq<64, false, 1>(p, qi, a.num_sms, s);
+  else if (cq == 1)
+    e = a.causal ? launch_dq<128, true, 1>(p, qi, a.num_sms, s) : launch_dq<128, false, 1>(p, qi, a.num_sms, s);
+  else
+    e = a.causal ? launch_dq<128, true, 2>(p, qi, a.num_sms, s) : launch_dq<128, false, 2>(p, qi, a.num_sms, s);
+  if (e != cudaSuccess) return e;
+  p.list = reinterpret_cast<const PackedEntry*>(ws + l.list[1]);
+  p.chunk = packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv);
+  const long long ki = a.total_k > 0 ? (a.total_k / (128ll * ck) + a.B) * Hkv : 0;
+  if (a.d == 64)
+    return a.causal ? launch_dkdv<64, true, 1>(p, ki, a.num_sms, s) : launch_dkdv<64, false, 1>(p, ki, a.num_sms, s);
+  if (ck == 1)
+    return a.causal ? launch_dkdv<128, true, 1>(p, ki, a.num_sms, s) : launch_dkdv<128, false, 1>(p, ki, a.num_sms, s);
+  return a.causal ? launch_dkdv<128, true, 2>(p, ki, a.num_sms, s) : launch_dkdv<128, false, 2>(p, ki, a.num_sms, s);
 }
 
 cudaError_t packed_bwd_read_clear_error(uint32_t* out, cudaStream_t s) {

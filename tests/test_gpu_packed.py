@@ -104,6 +104,14 @@ def test_long_sequences(fa, d):
     run_both(fa, [257], [3001], 4, 2, d, True, seed=12)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 1), (7, 1)])
+@pytest.mark.parametrize("lens_q,lens_k,causal", [
+    ([2100, 1030], None, True), ([1537], None, True), ([1300, 1200], None, False), ([1100], [3000], True), ([1300, 0, 1900], [1290, 5, 1900], True)],
+    ids=str)
+def test_sequences_long_enough_for_two_blocks_to_share_their_tiles(fa, lens_q, lens_k, causal, Hq, Hkv):
+    run_both(fa, lens_q, lens_k, Hq, Hkv, 128, causal, seed=30)
+
+
 @pytest.mark.parametrize("scale", (1e-3, 1.0, 4.0))
 def test_scales(fa, scale):
     run_both(fa, [200, 31], None, 4, 2, 64, True, seed=13, scale=scale)
