@@ -41,10 +41,11 @@ namespace {
 
 __device__ unsigned int g_packed_bwd_error;
 
-constexpr int kThreads = 352;  // two compute warpgroups, a TMA and two MMA warps
+constexpr int kDqMma = 3, kDkMma = 2;  // MMA warps
 constexpr int kCompute = 256;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kDqThreads = kCompute + 32 + 32 * kDqMma, kDkThreads = kCompute + 32 + 32 * kDkMma;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct BwdParams {
@@ -77,6 +78,7 @@ struct BwdBars {
   uint64_t y_full[kStages], y_empty[kStages];
   uint64_t s_full[2], s_done[2];  // scores computed; read (dq), or P written over them (dk, dv)
   uint64_t dp_full[2], ds_ready[2];
+  uint64_t dq_done[2];  // the dQ that reads a dP buffer's dS (dq)
   uint64_t dx_ready, acc_done, acc_free;
   uint64_t turn[2];  // the other MMA warp's products of a step are issued
   uint64_t item_full[kBwdRing], item_empty[kBwdRing];
@@ -106,11 +108,11 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 }
 
 // Barriers and tensor memory; rows of [zero, zero + bytes) that no box fills are zeroed.
-// `users`: MMA warps whose products read a stage, and which write an accumulator.
+// `users`: MMA warps whose products read a stage, and which write an accumulator; `mma`: all.
 // Returns false (for the whole cluster) when an earlier CTA recorded a timeout.
 template <int CL>
 __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t* smem, uint8_t* zero,
-                                         uint32_t bytes, int users) {
+                                         uint32_t bytes, int users, int mma) {
   if (threadIdx.x == 0) {
     // the swizzle of tiles counts from 1024-byte boundaries
     if ((smem_u32(smem) & 1023u) != 0) atomicCAS(&g_packed_bwd_error, 0u, kDevTimeoutMask | 0x3ffu);
@@ -127,6 +129,7 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
       mbar_init(&bars->s_full[b], 1);
       mbar_init(&bars->s_done[b], kCompute);
       mbar_init(&bars->dp_full[b], 1);
+      mbar_init(&bars->dq_done[b], 1);
       mbar_init(&bars->ds_ready[b], kCompute);
     }
     mbar_init(&bars->turn[0], 1);
@@ -137,14 +140,14 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
     for (int r = 0; r < kBwdRing; ++r) {
       mbar_init(&bars->item_full[r], 1);
       // the compute and MMA warps; the first CTA's holds those of the second, and its TMA warp
-      mbar_init(&bars->item_empty[r], CL * (kCompute / 32 + 2) + CL - 1);
+      mbar_init(&bars->item_empty[r], CL * (kCompute / 32 + mma) + CL - 1);
     }
-    mbar_init(&bars->drain, 2);
+    mbar_init(&bars->drain, mma);
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_packed_bwd_error) != 0) ? 1 : 0;
     fence_mbar_init();
   }
   if (bytes > 0) {
-    for (uint32_t i = threadIdx.x; i < bytes / 16; i += kThreads)
+    for (uint32_t i = threadIdx.x; i < bytes / 16; i += blockDim.x)
       reinterpret_cast<uint4*>(zero)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
@@ -333,13 +336,13 @@ __device__ __forceinline__ int dq_tiles(const PackedItem& it, int TT, bool causa
 }
 
 template <int D, bool CAUSAL, int CL>
-__global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = DqLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
-  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1)) return;
+  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1, kDqMma)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
   grid_dependency_launch();
@@ -419,30 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
     }
     __syncwarp();
   } else if (warp >= kMmaWarp) {
-    // Two warps issue, the first S, the second dP and dQ: 8 products take 210 cycles to issue, a
-    // commit 50, a wait that is over 70, and one warp kept the tensor core waiting.  The
-    // whole warp runs the loop on values that are the same in all lanes, so that descriptors
-    // lie in uniform registers, where the instruction wants them; one elected lane issues.
+    // Three warps issue, S, dP and dQ each: in this kernel 8 products take 500 cycles to issue (in one
+    // that does nothing else 210), a wait that is over 70, and a warp that issued dP and dQ took
+    // 1350 cycles a step.  The whole warp runs the loop on values that are the same in all
+    // lanes, so that descriptors lie in uniform registers, where the instruction wants them;
+    // one elected lane issues.
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
-    const bool scores = warp == kMmaWarp;
+    const int role = warp - kMmaWarp;
     const uint32_t tm = uniform(tmem), sK = uniform(smem_u32(smem + L::kK)), sV = uniform(smem_u32(smem + L::kV));
-    // dP of the key tile at ring position pos (the last dQ from its buffer is issued)
-    auto step_dp = [&](int pos) {
-      const int s = pos % kStages;
-      if (!warp_wait(&bars->y_full[s], (pos / kStages) & 1, bars, 0x213)) return false;
-      tc_fence_after_sync();
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ts(tm + L::dp_col(pos), tm + L::kDOA + kk * 8, kmajor_desc(sV + s * L::kTile, kk), idesc_s,
-                  kk > 0 ? 1u : 0u);
-        umma_commit(&bars->dp_full[pos & 1]);
-        commit_stage<CL>(&bars->y_empty[s]);
-      }
-      __syncwarp();
-      return true;
-    };
     int kvb = 0, tl = 0;
     for (int t = 0;; ++t) {
       if (!item_wait<CL>(bars, t, 0x21b)) break;
@@ -453,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
       if (n == 0) continue;
       if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x210)) break;
       bool ok = true;
-      if (scores) {
+      if (role == 0) {
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int pos = kvb + j, s = pos % kStages;
@@ -471,16 +459,33 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
           }
           __syncwarp();
         }
-      } else {
-        if (!step_dp(kvb)) break;
+      } else if (role == 1) {
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int pos = kvb + j, s = pos % kStages;
-          if (j + 1 < n && !(ok = step_dp(pos + 1))) break;
+          // (the buffer's last dS has been multiplied)
+          if (!(ok = warp_wait(&bars->y_full[s], (pos / kStages) & 1, bars, 0x213) &&
+                     (pos < 2 || warp_wait(&bars->dq_done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x215))))
+            break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ts(tm + L::dp_col(pos), tm + L::kDOA + kk * 8, kmajor_desc(sV + s * L::kTile, kk), idesc_s,
+                      kk > 0 ? 1u : 0u);
+            umma_commit(&bars->dp_full[pos & 1]);
+            commit_stage<CL>(&bars->y_empty[s]);
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int pos = kvb + j, s = pos % kStages;
           // dQ += dS K_j (A = dS bf16 in tensor memory over dP); an item's first overwrites the
           // accumulator that the epilogue before it reads
-          if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214) &&
-                     (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216))))
+          if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216)) &&
+                     warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214)))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -488,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dq_kernel(const __grid_
             for (int kk = 0; kk < 4; ++kk)
               umma_ts(tm + L::kAcc, tm + L::dp_col(pos) + packed_a_col(kk), mnmajor_desc(sK + s * L::kTile, kk),
                       idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bars->dq_done[pos & 1]);
             commit_stage<CL>(&bars->x_empty[s]);
             if (j + 1 == n) umma_commit(&bars->acc_done);
           }
@@ -703,14 +709,14 @@ __device__ __forceinline__ int dk_tiles(const PackedItem& it, int keys, int TT, 
 }
 
 template <int D, bool CAUSAL, int CL>
-__global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using L = DkLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int TT = p.TT64;
-  if (!bwd_init<CL>(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 2)) return;
+  if (!bwd_init<CL>(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 2, kDkMma)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
 
@@ -882,8 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_packed_dkdv_kernel(const __gri
         // the accumulator += P^T (dS^T) x the streamed rows (A = bf16 in tensor memory over the
         // scores); an item's first overwrites what the epilogue before it reads
         if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206)) &&
-                   (L::kDouble || !more || stage_in(pos + 1)) &&
-                   warp_wait(ready + L::buf(pos), L::par(pos), bars, 0x203) && turn()))
+                   (L::kDouble || !more || stage_in(pos + 1)) && turn() &&
+                   warp_wait(ready + L::buf(pos), L::par(pos), bars, 0x203)))
           break;
         tc_fence_after_sync();
         if (elect_one()) {
@@ -1060,13 +1066,13 @@ unsigned grid_of(long long items, int cluster, int sms) {
 template <int D, bool CAUSAL, int CL>
 cudaError_t launch_dq(const BwdParams& p, long long items, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_dq_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kThreads, DqLayout<D>::kSmem, CL,
+  return launch_behind(fa_packed_dq_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDqThreads, DqLayout<D>::kSmem, CL,
                        ready, s);
 }
 template <int D, bool CAUSAL, int CL>
 cudaError_t launch_dkdv(const BwdParams& p, long long items, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kThreads, DkLayout<D>::kSmem, CL,
+  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDkThreads, DkLayout<D>::kSmem, CL,
                        ready, s);
 }
 
