@@ -41,7 +41,7 @@ namespace {
 
 __device__ unsigned int g_packed_bwd_error;
 
-constexpr int kDqMma = 3, kDkMma = 2;  // MMA warps
+constexpr int kDqMma = 3, kDkMma = 3;  // MMA warps
 constexpr int kCompute = 256;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
@@ -78,9 +78,9 @@ struct BwdBars {
   uint64_t y_full[kStages], y_empty[kStages];
   uint64_t s_full[2], s_done[2];  // scores computed; read (dq), or P written over them (dk, dv)
   uint64_t dp_full[2], ds_ready[2];
-  uint64_t dq_done[2];  // the dQ that reads a dP buffer's dS (dq)
+  uint64_t dp_read[2];  // (dk, dv)
+  uint64_t done[2];  // the products that read a buffer's dS (dq), or P and dS (dk, dv)
   uint64_t dx_ready, acc_done, acc_free;
-  uint64_t turn[2];  // the other MMA warp's products of a step are issued
   uint64_t item_full[kBwdRing], item_empty[kBwdRing];
   uint64_t drain;
   uint32_t tmem_base;
@@ -108,16 +108,17 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 }
 
 // Barriers and tensor memory; rows of [zero, zero + bytes) that no box fills are zeroed.
-// `users`: MMA warps whose products read a stage, and which write an accumulator; `mma`: all.
+// `users`: MMA warps whose products read a stage, and which write an accumulator; `mma`: all;
+// `resident`: those that read what stays from shared memory.
 // Returns false (for the whole cluster) when an earlier CTA recorded a timeout.
 template <int CL>
 __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t* smem, uint8_t* zero,
-                                         uint32_t bytes, int users, int mma) {
+                                         uint32_t bytes, int users, int mma, int resident) {
   if (threadIdx.x == 0) {
     // the swizzle of tiles counts from 1024-byte boundaries
     if ((smem_u32(smem) & 1023u) != 0) atomicCAS(&g_packed_bwd_error, 0u, kDevTimeoutMask | 0x3ffu);
     mbar_init(&bars->res_full, 1);
-    mbar_init(&bars->res_empty, kCompute);
+    mbar_init(&bars->res_empty, kCompute + resident);
     mbar_init(&bars->a_ready, kCompute);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->x_full[s], 1);
@@ -129,11 +130,10 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
       mbar_init(&bars->s_full[b], 1);
       mbar_init(&bars->s_done[b], kCompute);
       mbar_init(&bars->dp_full[b], 1);
-      mbar_init(&bars->dq_done[b], 1);
+      mbar_init(&bars->dp_read[b], kCompute);
+      mbar_init(&bars->done[b], 1);
       mbar_init(&bars->ds_ready[b], kCompute);
     }
-    mbar_init(&bars->turn[0], 1);
-    mbar_init(&bars->turn[1], 1);
     mbar_init(&bars->dx_ready, kCompute);
     mbar_init(&bars->acc_done, users);
     mbar_init(&bars->acc_free, kCompute);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
-  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1, kDqMma)) return;
+  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1, kDqMma, 0)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
   grid_dependency_launch();
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
           const int pos = kvb + j, s = pos % kStages;
           // (the buffer's last dS has been multiplied)
           if (!(ok = warp_wait(&bars->y_full[s], (pos / kStages) & 1, bars, 0x213) &&
-                     (pos < 2 || warp_wait(&bars->dq_done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x215))))
+                     (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x215))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
             for (int kk = 0; kk < 4; ++kk)
               umma_ts(tm + L::kAcc, tm + L::dp_col(pos) + packed_a_col(kk), mnmajor_desc(sK + s * L::kTile, kk),
                       idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&bars->dq_done[pos & 1]);
+            umma_commit(&bars->done[pos & 1]);
             commit_stage<CL>(&bars->x_empty[s]);
             if (j + 1 == n) umma_commit(&bars->acc_done);
           }
@@ -677,10 +677,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
 }
 
 // ============================================================ dK / dV
-// Tensor memory: S^T (P^T over it) and dP^T (dS^T over it) of 64 queries, dV, dK, and K and V;
-// at d = 64 there is room for two buffers of the first two.  With one buffer dV_n and S^T_{n+1} run
-// while threads form dS_n, and dK_n and dP^T_{n+1} while they form P_{n+1}; with two, the next
-// step's scores and dP are there when threads come to them.
+// Tensor memory: S^T of 64 queries in two buffers, dP^T, dV, dK and K; at d = 64 there is room for V
+// and a second dP^T, at d = 128 V stays in shared memory (its product then runs at the speed
+// of shared memory, 49 cycles where 33 would do).  P^T and dS^T lie over S^T, whose bits
+// they take half of: so dP^T is free again once it has been read, and its next product does
+// not wait for dK.
 template <int D>
 struct DkLayout {
   static constexpr int kChunks = D / 64;
@@ -690,12 +691,14 @@ struct DkLayout {
   static constexpr uint32_t kBar = kVec + kStages * 512;
   static constexpr uint32_t kUsed = kBar + kBarBytes;
   static constexpr uint32_t kSmem = kUsed > 118784u ? kUsed : 118784u;  // one CTA an SM
-  static constexpr bool kDouble = D == 64;
-  static constexpr uint32_t kAcc0 = kDouble ? 256 : 128, kAcc1 = kAcc0 + D, kKA = 384, kVA = 384 + D / 2;
-  __host__ __device__ static constexpr int buf(int step) { return kDouble ? step & 1 : 0; }
-  __host__ __device__ static constexpr uint32_t par(int step) { return kDouble ? (step >> 1) & 1 : step & 1; }
-  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * buf(step); }
-  __host__ __device__ static constexpr uint32_t dp_col(int step) { return (kDouble ? 128u : 64u) + 64u * buf(step); }
+  static constexpr bool kVInTmem = D == 64;  // and two dP^T buffers
+  static constexpr uint32_t kAcc0 = kVInTmem ? 256 : 192, kAcc1 = kAcc0 + D, kKA = kAcc1 + D;
+  [[maybe_unused]] static constexpr uint32_t kVA = kKA + D / 2;
+  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * (step & 1); }
+  static constexpr int kDpBufs = kVInTmem ? 2 : 1;
+  __host__ __device__ static constexpr int dp_buf(int step) { return kVInTmem ? step & 1 : 0; }
+  __host__ __device__ static constexpr uint32_t dp_par(int step) { return kVInTmem ? (step >> 1) & 1 : step & 1; }
+  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 64u * dp_buf(step); }
 };
 static_assert(DkLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
@@ -716,7 +719,9 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int TT = p.TT64;
-  if (!bwd_init<CL>(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 2, kDkMma)) return;
+  if (!bwd_init<CL>(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 1, kDkMma,
+                    L::kVInTmem ? 0 : 1))
+    return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
 
@@ -829,37 +834,33 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       it = next;
     }
   } else if (warp >= kMmaWarp) {
-    // Two warps issue (as in the dq kernel), each a chain of products that no other touches: the
-    // first S^T = K Q^T and dV += P^T dO, the second dP^T = V dO^T and dK += dS^T Q.  With one score
-    // buffer they take turns: in flight at once, both chains would end later, and the threads
-    // wait for the end of one while the other could do without.
+    // Three warps issue (as in the dq kernel): S^T = K Q^T; dP^T = V dO^T; dV += P^T dO and dK += dS^T Q.
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
-    const bool first_chain = warp == kMmaWarp;
-    const uint32_t tm = uniform(tmem);
-    const uint32_t score0 = tm + uniform(first_chain ? L::s_col(0) : L::dp_col(0));
-    const uint32_t stays = tm + uniform(first_chain ? L::kKA : L::kVA), acc = tm + uniform(first_chain ? L::kAcc0 : L::kAcc1);
+    const int role = warp - kMmaWarp;
+    const uint32_t tm = uniform(tmem), sV = uniform(smem_u32(smem + L::kV));
     const uint32_t sQ = uniform(smem_u32(smem + L::kQ)), sdO = uniform(smem_u32(smem + L::kDO));
-    const uint32_t b_score = uniform(first_chain ? sQ : sdO), b_acc = uniform(first_chain ? sdO : sQ);
-    uint64_t* const full = first_chain ? bars->s_full : bars->dp_full;
-    uint64_t* const ready = first_chain ? bars->s_done : bars->ds_ready;
     auto stage_in = [&](int pos) { return warp_wait(&bars->x_full[pos % kStages], (pos / kStages) & 1, bars, 0x205); };
-    auto issue_scores = [&](int pos) {
+    auto issue_dp = [&](int pos, bool last) {
+      const uint32_t o = sdO + pos % kStages * L::kTile;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        umma_ts(score0 + 64u * L::buf(pos), stays + kk * 8, kmajor_desc(b_score + pos % kStages * L::kTile, kk), idesc_s,
-                kk > 0 ? 1u : 0u);
-      umma_commit(full + L::buf(pos));
+      for (int kk = 0; kk < D / 16; ++kk) {
+        if constexpr (L::kVInTmem)
+          umma_ts(tm + L::dp_col(pos), tm + L::kVA + kk * 8, kmajor_desc(o, kk), idesc_s, kk > 0 ? 1u : 0u);
+        else
+          umma_ss(tm + L::dp_col(pos), sdesc_sw128(sV + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
+                  kmajor_desc(o, kk), idesc_s, kk > 0 ? 1u : 0u);
+      }
+      umma_commit(&bars->dp_full[L::dp_buf(pos)]);
+      if (!L::kVInTmem && last) umma_commit(&bars->res_empty);
     };
-    int sb = 0, tl = 0, turns = 0;
-    auto turn = [&]() {
-      if (L::kDouble) return true;
-      const uint32_t par = static_cast<uint32_t>(turns++ & 1) ^ (first_chain ? 1u : 0u);
-      return warp_wait(&bars->turn[first_chain ? 0 : 1], par, bars, 0x209);
+    // acc (+)= A x the rows at `tile` (A = bf16 in tensor memory at `a`)
+    auto issue_acc = [&](uint32_t acc, uint32_t a, uint32_t tile, bool first) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        umma_ts(acc, a + packed_a_col(kk), mnmajor_desc(tile, kk), idesc_acc, (!first || kk > 0) ? 1u : 0u);
     };
-    auto pass_turn = [&]() {
-      if (!L::kDouble) mbar_arrive(&bars->turn[first_chain ? 1 : 0]);
-    };
+    int sb = 0, tl = 0;
     for (int t = 0;; ++t) {
       if (!item_wait<CL>(bars, t, 0x207)) break;
       const PackedItem it = bars->item[t % kBwdRing];
@@ -867,42 +868,59 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       if (uniform(it.head) < 0) break;
       const int n = uniform(dk_tiles(it, CL * 128, TT, CAUSAL)) * p.per_kv;
       if (n == 0) continue;
-      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x201) || !stage_in(sb) || !turn()) break;
-      tc_fence_after_sync();
-      if (elect_one()) {
-        issue_scores(sb);
-        pass_turn();
-      }
-      __syncwarp();
+      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x201)) break;
       bool ok = true;
+      if (role == 0) {
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const int pos = sb + j, s = pos % kStages;
-        const bool more = j + 1 < n;
-        if (L::kDouble && more) {
-          if (!(ok = stage_in(pos + 1))) break;
+        for (int j = 0; j < n; ++j) {
+          const int pos = sb + j;
+          // (the P and dS in the buffer have been multiplied)
+          if (!(ok = stage_in(pos) && (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x202))))
+            break;
           tc_fence_after_sync();
-          if (elect_one()) issue_scores(pos + 1);
+          if (elect_one()) {
+            const uint32_t q = sQ + pos % kStages * L::kTile;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ts(tm + L::s_col(pos), tm + L::kKA + kk * 8, kmajor_desc(q, kk), idesc_s, kk > 0 ? 1u : 0u);
+            umma_commit(&bars->s_full[pos & 1]);
+          }
           __syncwarp();
         }
-        // the accumulator += P^T (dS^T) x the streamed rows (A = bf16 in tensor memory over the
-        // scores); an item's first overwrites what the epilogue before it reads
-        if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206)) &&
-                   (L::kDouble || !more || stage_in(pos + 1)) && turn() &&
-                   warp_wait(ready + L::buf(pos), L::par(pos), bars, 0x203)))
-          break;
-        tc_fence_after_sync();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts(acc, score0 + 64u * L::buf(pos) + packed_a_col(kk), mnmajor_desc(b_acc + s * L::kTile, kk),
-                    idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
-          commit_stage<CL>(&bars->x_empty[s]);
-          if (!more) umma_commit(&bars->acc_done);
-          if (!L::kDouble && more) issue_scores(pos + 1);
-          pass_turn();
+      } else if (role == 1) {
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int pos = sb + j, before = pos - L::kDpBufs;
+          // (the buffer's last dP has been read)
+          if (!(ok = stage_in(pos) &&
+                     (before < 0 || warp_wait(&bars->dp_read[L::dp_buf(before)], L::dp_par(before), bars, 0x208))))
+            break;
+          tc_fence_after_sync();
+          if (elect_one()) issue_dp(pos, j + 1 == n);
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int pos = sb + j;
+          const uint32_t stage = pos % kStages * L::kTile;
+          // an item's first overwrites the accumulators that the epilogue before it reads
+          if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206)) &&
+                     warp_wait(&bars->s_done[pos & 1], (pos >> 1) & 1, bars, 0x203)))
+            break;
+          tc_fence_after_sync();
+          if (elect_one()) issue_acc(tm + L::kAcc0, tm + L::s_col(pos), sdO + stage, j == 0);
+          __syncwarp();
+          if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x204))) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            issue_acc(tm + L::kAcc1, tm + L::s_col(pos) + 16, sQ + stage, j == 0);
+            umma_commit(&bars->done[pos & 1]);
+            commit_stage<CL>(&bars->x_empty[pos % kStages]);
+            if (j + 1 == n) umma_commit(&bars->acc_done);
+          }
+          __syncwarp();
+        }
       }
       if (!ok) break;
       sb += n;
@@ -957,15 +975,17 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         }
         continue;
       }
-      // K and V to tensor memory: the products of the item before that read them are done (its last
+      // K (and V) to tensor memory: the products of the item before that read them are done (its last
       // scores and dP have been waited for)
       if (!warp_wait(&bars->res_full, tl & 1, bars, 0x307)) break;
       {
         uint32_t w[D / 4];
         load_half_row<D>(smem + L::kK, tr, g, true, w);
         store_half_row<D>(tm + L::kKA, g, w);
-        load_half_row<D>(smem + L::kV, tr, g, true, w);
-        store_half_row<D>(tm + L::kVA, g, w);
+        if constexpr (L::kVInTmem) {
+          load_half_row<D>(smem + L::kV, tr, g, true, w);
+          store_half_row<D>(tm + L::kVA, g, w);
+        }
       }
       mbar_arrive(&bars->res_empty);
       tmem_st_wait();
@@ -981,7 +1001,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
         const float* nlse = reinterpret_cast<const float*>(smem + L::kVec) + (step % kStages) * 128;
-        if (!(ok = warp_wait(&bars->s_full[L::buf(step)], L::par(step), bars, 0x301))) break;
+        if (!(ok = warp_wait(&bars->s_full[step & 1], (step >> 1) & 1, bars, 0x301))) break;
         tc_fence_after_sync();
         uint32_t pr[32];
         tmem_ld(tm + L::s_col(step) + col0, pr);
@@ -1020,12 +1040,14 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->s_done[L::buf(step)]);
-        if (!(ok = warp_wait(&bars->dp_full[L::buf(step)], L::par(step), bars, 0x306))) break;
+        mbar_arrive(&bars->s_done[step & 1]);
+        if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x306))) break;
         tc_fence_after_sync();
         uint32_t rr[32], ds[16];
         const uint32_t dp = tm + L::dp_col(step) + col0;
         tmem_ld(dp, rr);
+        tc_fence_before_sync();
+        mbar_arrive(&bars->dp_read[L::dp_buf(step)]);
         const float4* d4 = reinterpret_cast<const float4*>(nlse + 64 + col0);
 #pragma unroll
         for (int e4 = 0; e4 < 8; ++e4) {
@@ -1041,10 +1063,10 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
           ds[2 * e4] = pack_bf16x2(ds01.x, ds01.y);
           ds[2 * e4 + 1] = pack_bf16x2(ds23.x, ds23.y);
         }
-        tmem_st16(dp, ds);
+        tmem_st16(tm + L::s_col(step) + col0 + 16, ds);
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->ds_ready[L::buf(step)]);
+        mbar_arrive(&bars->ds_ready[step & 1]);
         if (++tile == first + per) tile = first;
       }
       if (!ok) break;
