@@ -694,10 +694,10 @@ cudaError_t launch_forward_packed(const PackedArgs& a, const CUtensorMap* maps, 
   p.TT = t.TT;
   p.heads = t.heads;
   p.per_kv = t.per_kv;
-  p.chunk = packed_chunk(a.total_k, a.d, a.k.heads) * t.per_kv;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.causal = a.causal;
   const long long items = (a.total_q / (2ll * t.TT) + a.B) * t.heads;
+  p.chunk = packed_chunk(a.total_k, a.d, a.k.heads, items, a.num_sms) * t.per_kv;
   const unsigned blocks = static_cast<unsigned>(std::min<long long>(items, a.num_sms));
   if (a.d == 64) return a.causal ? launch_t<64, true>(p, blocks, s) : launch_t<64, false>(p, blocks, s);
   return a.causal ? launch_t<128, true>(p, blocks, s) : launch_t<128, false>(p, blocks, s);

@@ -64,9 +64,13 @@ inline PackedTiling packed_tiling(int Hq, int Hkv) {
   return t;
 }
 
-// Heads taken together so that what their items stream (two tensors, `tokens` rows of d bf16 a
-// head each) stays in half of the 129 MB L2: at least one, at most all.
-inline int packed_chunk(long long tokens, int d, int heads) {
+// Heads taken together.  Where CTAs have many items (16 or more), as many heads as keep what their
+// items stream (two tensors, `tokens` rows of d bf16 a head each) in half of the 129 MB L2:
+// 65536 tokens, 32 / 8 heads of 128, forward 20.0 -> 19.6 ms, backward 70.9 -> 69.1 ms.  Where
+// they have few, all of them, so that the longest tiles of all heads come first: chunks of one
+// head cost the dk, dv kernel of 1000 to 8192 tokens, 7 items a CTA, 16 %.
+inline int packed_chunk(long long tokens, int d, int heads, long long items, int ctas) {
+  if (items < 16ll * ctas) return heads;
   const long long fit = (64ll << 20) / (tokens * d * 4 + 1);
   return static_cast<int>(fit < 1 ? 1 : (fit > heads ? heads : fit));
 }

@@ -1136,8 +1136,8 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   // the dq kernel streams keys and values, the other the queries and dO of a group's heads
   p.list = reinterpret_cast<const PackedEntry*>(ws + l.list[0]);
-  p.chunk = packed_chunk(a.total_k, a.d, Hkv) * t.per_kv;
   const long long qi = a.total_q > 0 ? (a.total_q / (1ll * cq * p.TT) + a.B) * t.heads : 0;
+  p.chunk = packed_chunk(a.total_k, a.d, Hkv, qi, a.num_sms / cq) * t.per_kv;
   if (a.d == 64)
     e = a.causal ? launch_dq<64, true, 1>(p, qi, a.num_sms, s) : launch_dq<64, false, 1>(p, qi, a.num_sms, s);
   else if (cq == 1)
@@ -1146,8 +1146,8 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
     e = a.causal ? launch_dq<128, true, 2>(p, qi, a.num_sms, s) : launch_dq<128, false, 2>(p, qi, a.num_sms, s);
   if (e != cudaSuccess) return e;
   p.list = reinterpret_cast<const PackedEntry*>(ws + l.list[1]);
-  p.chunk = packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv);
   const long long ki = a.total_k > 0 ? (a.total_k / (128ll * ck) + a.B) * Hkv : 0;
+  p.chunk = packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv, ki, a.num_sms / ck);
   if (a.d == 64)
     return a.causal ? launch_dkdv<64, true, 1>(p, ki, a.num_sms, s) : launch_dkdv<64, false, 1>(p, ki, a.num_sms, s);
   if (ck == 1)
