@@ -169,10 +169,11 @@ template <int D>
 struct FwdLayout {
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kTileBytes = 128u * D * 2;
-  // two Q tiles; at d = 64 there is room for the next item's
-  static constexpr int kQBufs = D == 64 ? 2 : 1;
+  // Two Q tiles, and room for one or both of the next item's, copied while this one's products run
+  // (at d = 128, 24 prompts of up to 2048 tokens take 259 us, and 268 with two Q tiles in all).
+  static constexpr int kQTiles = D == 64 ? 4 : 3;
   static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kK = kQ + kQBufs * 2 * kTileBytes;
+  static constexpr uint32_t kK = kQ + kQTiles * kTileBytes;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
   static constexpr uint32_t kBar = kV + kStages * kTileBytes;
   static constexpr uint32_t kSmemUsed = kBar + 512 + 1024;  // + align slack
@@ -184,11 +185,12 @@ struct FwdLayout {
 };
 
 struct FwdBars {
-  uint64_t q_full[2];
+  // Q tiles. Copied: by group, for its tile number t at t % 4, so that a group sees every phase of its
+  // barriers and none twice (four tiles at most are unread). The S products that read it are done: by slot.
+  uint64_t q_full[2][4], q_empty[4];
   uint64_t k_full[kStages], k_empty[kStages];
   uint64_t v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_ready[2], pv_done[2];
-  uint64_t q_empty[2]; // the S products of an item are done with the Q tiles
   uint64_t item_full[kPackedRing], item_empty[kPackedRing];
   uint64_t turn[2];    // the other tile's products of a step are issued
   uint64_t o_free[2];  // softmax warpgroup g has read its O for the epilogue
@@ -250,9 +252,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 2);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->q_full[0][i], 1);
+      mbar_init(&bars->q_full[1][i], 1);
+      mbar_init(&bars->q_empty[i], 1);
+    }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&bars->q_full[g], 1);
-      mbar_init(&bars->q_empty[g], 2);
       mbar_init(&bars->s_full[g], 1);
       mbar_init(&bars->p_ready[g], 128);
       mbar_init(&bars->pv_done[g], 1);
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
   }
   // rows that no box fills stay zero
   if (p.P * p.TT < 128) {
-    for (uint32_t i = threadIdx.x; i < 2 * L::kQBufs * L::kTileBytes / 16; i += kFwdThreads)
+    for (uint32_t i = threadIdx.x; i < L::kQTiles * L::kTileBytes / 16; i += kFwdThreads)
       reinterpret_cast<uint4*>(smem + L::kQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         return bar_wait(bar, par, bars, code);
       };
       const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT) * 128u * L::kChunks;
-      int kvb = 0, tl = 0;  // K / V tiles and items with loads so far
+      int kvb = 0, qc = 0, qt[2] = {0, 0};  // K / V tiles, Q tiles, Q tiles of a group so far
       PackedItem it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
       for (int t = 0;; ++t) {
         const int r = t % kPackedRing;
@@ -311,24 +316,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         tensormap_acquire(maps + 1);
         tensormap_acquire(maps + 2);
         const int kh = it.head / p.per_kv, qh = it.head, pair = it.e.tile;
-        const int qb = tl % L::kQBufs;
-        auto load_q = [&]() {
-          mbar_arrive_expect_tx(&bars->q_full[qb], ((n0 > 0) + (n1 > 0)) * q_bytes);
+        auto load_q = [&](int g) {
+          if ((g ? n1 : n0) == 0) return true;
+          const int slot = qc % L::kQTiles;
+          if (!wait(&bars->q_empty[slot], ((qc / L::kQTiles) & 1) ^ 1, 0x103)) return false;
+          uint64_t *full = &bars->q_full[g][qt[g]++ & 3];
+          mbar_arrive_expect_tx(full, q_bytes);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if ((g ? n1 : n0) == 0) continue;
-#pragma unroll
-            for (int c = 0; c < L::kChunks; ++c)
-              tma_load_4d(smem + L::kQ + (2 * qb + g) * L::kTileBytes + c * 16384, maps, &bars->q_full[qb], c * 64,
-                          0, (2 * pair + g) * p.TT, qh);
-          }
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_4d(smem + L::kQ + slot * L::kTileBytes + c * 16384, maps, full, c * 64, 0,
+                        (2 * pair + g) * p.TT, qh);
+          ++qc;
+          return true;
         };
-        // a CTA's first items: Q right away; later ones: the first K tile first (its ring slot
-        // is free early), then Q once the products of the buffer's last item are done with it
-        if (tl < L::kQBufs) load_q();
         bool ok = true;
         PackedItem next = it;
-        for (int j = 0; j < nmax; ++j) {
+        ok = load_q(0);
+        for (int j = 0; ok && j < nmax; ++j) {
           const int s = ring_slot(kvb + j);
           const uint32_t ph = ring_phase(kvb + j);
           if (!(ok = wait(&bars->k_empty[s], ph ^ 1, 0x101))) break;
@@ -337,10 +341,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
           for (int c = 0; c < L::kChunks; ++c)
             tma_load_3d(smem + L::kK + s * L::kTileBytes + c * 16384, maps + 1, &bars->k_full[s], c * 64,
                         j * 128, kh);
-          if (j == 0 && tl >= L::kQBufs) {
-            if (!(ok = wait(&bars->q_empty[qb], (tl / L::kQBufs - 1) & 1, 0x103))) break;
-            load_q();
-          }
+          if (j == 0 && !(ok = load_q(1))) break;
           if (!(ok = wait(&bars->v_empty[s], ph ^ 1, 0x102))) break;
           mbar_arrive_expect_tx(&bars->v_full[s], L::kTileBytes);
 #pragma unroll
@@ -352,7 +353,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         }
         if (!ok) break;
         kvb += nmax;
-        ++tl;
         it = next;
       }
     }
@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
     const uint32_t tm = uniform(tmem), sc = tm + uniform(L::s_col(g)), oc = tm + uniform(L::o_col(g));
-    const uint32_t q0 = uniform(smem_u32(smem + L::kQ) + g * L::kTileBytes);
-    uint32_t qbase = q0;
+    const uint32_t sQ = uniform(smem_u32(smem + L::kQ));
+    uint32_t qbase = sQ;
     const uint32_t sK = uniform(smem_u32(smem + L::kK)), sV = uniform(smem_u32(smem + L::kV));
     auto wait = [&](uint64_t* bar, uint32_t par, uint32_t code) { return all_wait(bar, par, bars, code); };
     auto issue_s = [&](int slot) {
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     // For key tile j: PV_j and S_{j+1}.  A query tile may have no work in an item (it lies
     // behind the sequence, or sees no key), or end before the other: it then gives the
     // copied tiles back unread.
-    int kvb = 0, tl = 0, base = 0, used = 0, turns = 0;
+    int kvb = 0, qc = 0, qt = 0, base = 0, used = 0, turns = 0;
     auto turn = [&]() {  // (the first tile's warp goes first)
       const uint32_t par = static_cast<uint32_t>(turns++ & 1) ^ (g == 0 ? 1u : 0u);
       return wait(&bars->turn[g], par, 0x20c);
@@ -407,12 +407,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       __syncwarp();
       if (elect_one()) mbar_arrive(&bars->item_empty[r]);
       if (uniform(it.head) < 0) break;
-      const int n = uniform(item_tiles(it, g, p.TT, CAUSAL));
-      const int nmax = max(n, uniform(item_tiles(it, 1 - g, p.TT, CAUSAL)));
+      const int n0 = uniform(item_tiles(it, 0, p.TT, CAUSAL)), n1 = uniform(item_tiles(it, 1, p.TT, CAUSAL));
+      const int n = g == 0 ? n0 : n1, nmax = max(n0, n1);
       if (nmax == 0) continue;
-      const int qb = tl % L::kQBufs;
-      qbase = q0 + qb * 2 * L::kTileBytes;
-      if (!wait(&bars->q_full[qb], (tl / L::kQBufs) & 1, 0x201) || !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202) || !turn())
+      const int slot = (qc + (g == 1 && n0 > 0 ? 1 : 0)) % L::kQTiles;
+      qbase = sQ + slot * L::kTileBytes;
+      if ((n > 0 && !wait(&bars->q_full[g][qt & 3], (qt >> 2) & 1, 0x201)) ||
+          !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202) || !turn())
         break;
       tc_fence_after_sync();
       if (elect_one()) {
@@ -420,17 +421,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
           issue_s(ring_slot(kvb));
         else
           mbar_arrive(&bars->k_empty[ring_slot(kvb)]);
+        if (n == 1) umma_commit(&bars->q_empty[slot]);
         mbar_arrive(&bars->turn[1 - g]);
       }
       __syncwarp();
       bool ok = true;
+      // At d = 64 the turn is taken before P is waited for, so that one wait fewer follows P (31
+      // sequences of up to 1500 tokens, 16 heads on 2, full: 125 us, and 131 the other way round);
+      // at d = 128, where the products take longer than the waits, that other way is 1 to 2 % faster.
+      auto p_wait = [&](int j) { return j >= n || wait(&bars->p_ready[g], (base + j) & 1, 0x203); };
 #pragma unroll 1
       for (int j = 0; j < nmax; ++j) {
         const int pos = kvb + j, s = ring_slot(pos), sn = ring_slot(pos + 1);
         ok = wait(&bars->v_full[s], ring_phase(pos), 0x204) &&
              (j > 0 || n == 0 || used == 0 || wait(&bars->o_free[g], (used - 1) & 1, 0x209)) &&
              (j + 1 >= nmax || wait(&bars->k_full[sn], ring_phase(pos + 1), 0x205)) &&
-             (j >= n || wait(&bars->p_ready[g], (base + j) & 1, 0x203)) && turn();
+             (D == 64 ? turn() && p_wait(j) : p_wait(j) && turn());
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
@@ -443,14 +449,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
             issue_s(sn);
           else if (j + 1 < nmax)
             mbar_arrive(&bars->k_empty[sn]);
+          if (j + 2 == n) umma_commit(&bars->q_empty[slot]);
           mbar_arrive(&bars->turn[1 - g]);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&bars->q_empty[qb]);
+      qt += n > 0;
+      qc += (n0 > 0) + (n1 > 0);
       kvb += nmax;
-      ++tl;
       base += n;
       used += n > 0;
     }
