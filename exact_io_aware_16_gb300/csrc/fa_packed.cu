@@ -157,7 +157,7 @@ static_assert(kBuckets == kPlanThreads, "one bucket a thread in the scan");
 constexpr int kFwdThreads = 352;  // two softmax warpgroups, a TMA and two MMA warps
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kStages = 2;
+constexpr int kMaxStages = 4;
 constexpr float kLn2 = 0.69314718055994530942f;
 // As in fa_fwd.cu: the running maximum moves when a tile's exceeds it by 2^8, and a tile taken
 // against the old one stands while a row's sum of P is at most 2^16 (bf16 rounds
@@ -169,6 +169,7 @@ template <int D>
 struct FwdLayout {
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kTileBytes = 128u * D * 2;
+  static constexpr int kStages = D == 64 ? 4 : 2;  // key and value tiles under way
   // Two Q tiles, and room for one or both of the next item's, copied while this one's products run
   // (at d = 128, 24 prompts of up to 2048 tokens take 259 us, and 268 with two Q tiles in all).
   static constexpr int kQTiles = D == 64 ? 4 : 3;
@@ -176,7 +177,7 @@ struct FwdLayout {
   static constexpr uint32_t kK = kQ + kQTiles * kTileBytes;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
   static constexpr uint32_t kBar = kV + kStages * kTileBytes;
-  static constexpr uint32_t kSmemUsed = kBar + 512 + 1024;  // + align slack
+  static constexpr uint32_t kSmemUsed = kBar + 1024 + 1024;  // + align slack
   // at least 116 KB, so two CTAs never share an SM (each takes all 512 TMEM columns)
   static constexpr uint32_t kSmem = kSmemUsed > 118784u ? kSmemUsed : 118784u;
   static constexpr uint32_t kTmemCols = 512;  // S0, S1, O0, O1
@@ -188,8 +189,8 @@ struct FwdBars {
   // Q tiles. Copied: by group, for its tile number t at t % 4, so that a group sees every phase of its
   // barriers and none twice (four tiles at most are unread). The S products that read it are done: by slot.
   uint64_t q_full[2][4], q_empty[4];
-  uint64_t k_full[kStages], k_empty[kStages];
-  uint64_t v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages];
+  uint64_t v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[2], p_ready[2], pv_done[2];
   uint64_t item_full[kPackedRing], item_empty[kPackedRing];
   uint64_t turn[2];    // the other tile's products of a step are issued
@@ -199,7 +200,7 @@ struct FwdBars {
   int abort_flag;
   PackedItem item[kPackedRing];
 };
-static_assert(sizeof(FwdBars) <= 512, "barrier block overruns its shared memory");
+static_assert(sizeof(FwdBars) <= 1024, "barrier block overruns its shared memory");
 
 struct FwdParams {
   PackedHeader* header;
@@ -226,8 +227,14 @@ __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t par, FwdBars* b
   return __all_sync(0xffffffffu, bar_wait(bar, par, b, code));
 }
 
-__device__ __forceinline__ int ring_slot(int pos) { return static_cast<int>(static_cast<unsigned>(pos) % kStages); }
-__device__ __forceinline__ uint32_t ring_phase(int pos) { return (static_cast<unsigned>(pos) / kStages) & 1u; }
+template <int D>
+__device__ __forceinline__ int ring_slot(int pos) {
+  return static_cast<int>(static_cast<unsigned>(pos) % FwdLayout<D>::kStages);
+}
+template <int D>
+__device__ __forceinline__ uint32_t ring_phase(int pos) {
+  return (static_cast<unsigned>(pos) / FwdLayout<D>::kStages) & 1u;
+}
 
 // Key tiles that query tile 2 * pair + g of an item goes through.
 __device__ __forceinline__ int item_tiles(const PackedItem& it, int g, int TT, bool causal) {
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 2);  // the two MMA warps
       mbar_init(&bars->v_full[s], 1);
@@ -333,8 +340,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         PackedItem next = it;
         ok = load_q(0);
         for (int j = 0; ok && j < nmax; ++j) {
-          const int s = ring_slot(kvb + j);
-          const uint32_t ph = ring_phase(kvb + j);
+          const int s = ring_slot<D>(kvb + j);
+          const uint32_t ph = ring_phase<D>(kvb + j);
           if (!(ok = wait(&bars->k_empty[s], ph ^ 1, 0x101))) break;
           mbar_arrive_expect_tx(&bars->k_full[s], L::kTileBytes);
 #pragma unroll
@@ -413,14 +420,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       const int slot = (qc + (g == 1 && n0 > 0 ? 1 : 0)) % L::kQTiles;
       qbase = sQ + slot * L::kTileBytes;
       if ((n > 0 && !wait(&bars->q_full[g][qt & 3], (qt >> 2) & 1, 0x201)) ||
-          !wait(&bars->k_full[ring_slot(kvb)], ring_phase(kvb), 0x202) || !turn())
+          !wait(&bars->k_full[ring_slot<D>(kvb)], ring_phase<D>(kvb), 0x202) || !turn())
         break;
       tc_fence_after_sync();
       if (elect_one()) {
         if (n > 0)
-          issue_s(ring_slot(kvb));
+          issue_s(ring_slot<D>(kvb));
         else
-          mbar_arrive(&bars->k_empty[ring_slot(kvb)]);
+          mbar_arrive(&bars->k_empty[ring_slot<D>(kvb)]);
         if (n == 1) umma_commit(&bars->q_empty[slot]);
         mbar_arrive(&bars->turn[1 - g]);
       }
@@ -432,10 +439,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       auto p_wait = [&](int j) { return j >= n || wait(&bars->p_ready[g], (base + j) & 1, 0x203); };
 #pragma unroll 1
       for (int j = 0; j < nmax; ++j) {
-        const int pos = kvb + j, s = ring_slot(pos), sn = ring_slot(pos + 1);
-        ok = wait(&bars->v_full[s], ring_phase(pos), 0x204) &&
+        const int pos = kvb + j, s = ring_slot<D>(pos), sn = ring_slot<D>(pos + 1);
+        ok = wait(&bars->v_full[s], ring_phase<D>(pos), 0x204) &&
              (j > 0 || n == 0 || used == 0 || wait(&bars->o_free[g], (used - 1) & 1, 0x209)) &&
-             (j + 1 >= nmax || wait(&bars->k_full[sn], ring_phase(pos + 1), 0x205)) &&
+             (j + 1 >= nmax || wait(&bars->k_full[sn], ring_phase<D>(pos + 1), 0x205)) &&
              (D == 64 ? turn() && p_wait(j) : p_wait(j) && turn());
         if (!ok) break;
         tc_fence_after_sync();
