@@ -21,6 +21,11 @@
 // at half its rate.  (Products of 64 columns run at full rate that way, 33.8 cycles of 32;
 // from shared memory 49.)
 //
+// Measured, four causal samples of 1000 to 8192 tokens (17335), 32 heads on 8, d = 128: dq 790 us, dk and
+// dv 1004 us, the tensor core busy for 71 and 76 % of them; 1.68 PFLOP/s of the seven products,
+// near what the power limit leaves. 31 samples of up to 1500 tokens, 16 heads on 2, d = 64, full:
+// 199 and 218 us, 34 and 43 % busy; there the threads' part of a tile takes longer than its products.
+//
 // D from the bf16 o is off by up to half a bf16 step of it.  Where a query sees many keys
 // that is below the rounding of dS; where it sees few, dS may be small against D
 // (a query's own key alone: zero).  Query tiles that see 64 keys or fewer therefore take

@@ -9,6 +9,11 @@
 // halves of elements 16 s .. 16 s + 15.  Either way lane s needs the angles of
 // pairs 8 s .. 8 s + 7 and nothing from its neighbours.
 //
+// Measured, 16384 tokens of 32 and 8 heads of 128 (335 MB in and out): the rotation 53 us,
+// 6.3 TB/s, as fast as a copy; with the norm 60 us, 5.6 TB/s, where the lanes' arithmetic and
+// shuffles fill two thirds of the issue slots; the norm's backward pass (503 MB) 93 us and 5 us for
+// the weights' gradients, 5.4 TB/s. The next tokens of some sequences take 4 us.
+//
 // Angles: position * turns[i] modulo 2^64 is the exact angle in units of 2^-64 turns
 // (the table holds f_i / 2 pi to 2^-65), and its upper 32 bits, read as signed, are the
 // angle in (-1/2, 1/2] turns.  sincospif of twice that needs no range reduction; all

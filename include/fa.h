@@ -429,7 +429,10 @@ int fa_forward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, c
  * keys that no query sees have dk = dv = 0; tokens in no sequence are left as they
  * were.  Results do not depend on the order in which the GPU runs the work.
  * Unlike fa_backward, D is the fp32 sum over the bf16 o alone: it is off by up to
- * half a bf16 step of o, times dO.  Arguments and errors otherwise as for
+ * half a bf16 step of o, times dO.  (Where that would tell most, for the first queries
+ * of a sequence, D is the sum of P o dP instead: 128 rows of queries and heads none of
+ * which sees more than 64 keys.)  P and dS are rounded to bf16 before their products,
+ * all sums are fp32.  Arguments and errors otherwise as for
  * fa_forward_packed; workspace: fa_backward_packed_workspace_size() bytes.
  */
 size_t fa_backward_packed_workspace_size(int B, int total_q, int total_k, int Hq, int Hkv, int d);
