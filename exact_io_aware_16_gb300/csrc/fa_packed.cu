@@ -8,9 +8,9 @@
 //
 // Bound by the tensor core at d = 128: two causal sequences of 8192, 32 heads on 8, take 645 us on a
 // cool GPU, 1.70 PFLOP/s of the triangle, and 710 us in a loop, under the power limit. 24 prompts
-// of 1 to 2048 tokens take 259 us: their diagonal and last tiles are partly empty. At d = 64 the
+// of 1 to 2048 tokens take 250 us: their diagonal and last tiles are partly empty. At d = 64 the
 // products are half as long, and the chain S, softmax, P V of a tile is what takes the time: 31
-// sequences of up to 1500 tokens, 16 heads on 2, full, take 118 us with the tensor core busy for
+// sequences of up to 1500 tokens, 16 heads on 2, full, take 116 us with the tensor core busy for
 // 40 % of them, and 64 causal samples of up to 512 tokens, 12 heads, 48 us.
 #include <algorithm>
 #include <cstdint>
@@ -485,19 +485,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     const int t = threadIdx.x & 127;  // row within the tile, TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scol = tmem + lane_off + L::s_col(g), ocol = tmem + lane_off + L::o_col(g);
-    const int row_tok = t / p.P, row_head = t - row_tok * p.P;
-    const bool row_in = row_tok < p.TT;
     auto warp_wait = [&](uint64_t* bar, uint32_t par, uint32_t code) { return all_wait(bar, par, bars, code); };
     int tb = 0, used = 0;  // key tiles of earlier items, and items with any
     for (int ti = 0;; ++ti) {
       const int r = ti % kPackedRing;
       if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, 0x304)) break;
-      const PackedItem it = bars->item[r];
-      mbar_arrive(&bars->item_empty[r]);
-      if (it.head < 0) break;
-      const int nkv = item_tiles(it, g, p.TT, CAUSAL);
-      const int tok0 = (2 * it.e.tile + g) * p.TT, tok = tok0 + row_tok;
-      const int m = it.e.m, off = m - it.e.n;  // causal: keys j <= tok + off
+      // (what only the end of the item wants is read again there: with it the loop over key tiles
+      // spills, and 24 prompts of up to 2048 tokens take 259 us, not 250)
+      int nkv, tok0, m, off;
+      {
+        const PackedItem it = bars->item[r];
+        if (it.head < 0) break;
+        nkv = item_tiles(it, g, p.TT, CAUSAL);
+        tok0 = (2 * it.e.tile + g) * p.TT;
+        m = it.e.m;
+        off = m - it.e.n;  // causal: keys j <= tok + off
+      }
+      const int tok = tok0 + t / p.P;
       float m_run = -INFINITY;  // running (lazily moved) max of s * scale * log2(e)
       float l_run = 0.0f;
       bool ok = true;
@@ -584,8 +588,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       }
       if (!ok) break;
       // ------------------------------------------------ epilogue
-      const bool stores = row_in && tok < it.e.n;
-      const int head = it.head * p.P + row_head;
+      const PackedItem it = bars->item[r];
+      mbar_arrive(&bars->item_empty[r]);
+      const bool stores = t < p.P * p.TT && tok < it.e.n;
+      const int head = it.head * p.P + t % p.P;
       const long long off_o =
           stores ? static_cast<long long>(it.e.q0 + tok) * p.o_token + head * p.o_head : -1;
       if (nkv == 0) {
