@@ -333,3 +333,40 @@ def test_two_calls_at_once_have_workspaces_of_their_own(fa):
     for pair in both:
         for a, b in zip(pair, alone):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_heads_in_chunks(fa):
+    """Many items: the heads are taken some at a time (of 32 here six, five times, and two), which
+    changes the order of the work and no bit of its results."""
+    lens = [241 + b % 31 for b in range(80)]
+    cu = ref.starts(lens)
+    q, k, v, dO = (rnd(40 + i, cu[-1], 32, 128).cuda() for i in range(4))
+    o, lse = fa.fa_forward_packed(q, k, v, i32(cu), causal=True)
+    grads = fa.fa_backward_packed(q, k, v, o, dO, lse, i32(cu), causal=True)
+    for h in range(0, 32, 8):
+        p = slice(h, h + 8)
+        o8, lse8 = fa.fa_forward_packed(q[:, p], k[:, p], v[:, p], i32(cu), causal=True)
+        g8 = fa.fa_backward_packed(q[:, p], k[:, p], v[:, p], o8, dO[:, p], lse8, i32(cu), causal=True)
+        ok(fa)
+        assert torch.equal(o[:, p], o8) and torch.equal(lse[p], lse8)
+        assert all(torch.equal(a[:, p], b) for a, b in zip(grads, g8))
+
+
+@pytest.mark.slow
+def test_tokens_beyond_4_GiB(fa):
+    """The last of 17 million tokens, 4.4 GB into each tensor; about 36 GB of device memory."""
+    n, lens, d = 17_000_000, [200, 100], 128
+    assert (n - 300) * d * 2 > 2 ** 32
+    near = [rnd(50 + i, 300, 1, d).cuda() for i in range(4)]
+    cu = ref.starts(lens)
+    o1, lse1 = fa.fa_forward_packed(*near[:3], i32(cu), causal=True)
+    want = fa.fa_backward_packed(*near[:3], o1, near[3], lse1, i32(cu), causal=True)
+    far = [torch.empty(n, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for t, s in zip(far, near):
+        t[-300:] = s
+    at = i32(ref.starts(lens, n - 300))
+    o, lse = fa.fa_forward_packed(*far[:3], at, causal=True)
+    got = fa.fa_backward_packed(*far[:3], o, far[3], lse, at, causal=True)
+    ok(fa)
+    assert torch.equal(o[-300:], o1) and torch.equal(lse[:, -300:], lse1)
+    assert all(torch.equal(a[-300:], b) for a, b in zip(got, want))

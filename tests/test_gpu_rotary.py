@@ -335,3 +335,25 @@ def test_serving_step(fa):
     o, _ = fa.fa_forward_packed(qr[prompt:], kr, v, cq, ck, causal=True)
     ok(fa)
     assert (o.float() - want[prompt:].float()).norm() <= 5e-3 * want[prompt:].float().norm()
+
+
+@pytest.mark.slow
+def test_tokens_beyond_4_GiB(fa):
+    """The last of 17 million tokens, 4.4 GB into each tensor."""
+    n, d = 17_000_000, 128
+    r = fa.Rotary(d)
+    g = torch.Generator().manual_seed(3)
+    x, y = (torch.randn(50, 1, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    q, dq = (torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q[-50:], dq[-50:] = x, y
+    last = pos[-50:].contiguous()
+    assert torch.equal(fa.fa_rotary(r, q, None, pos)[0][-50:], fa.fa_rotary(r, x, None, last)[0])
+    assert torch.equal(fa.fa_norm_rotary(r, q, None, pos, w)[0][-50:], fa.fa_norm_rotary(r, x, None, last, w)[0])
+    far, _, dw, _ = fa.fa_norm_rotary_backward(r, dq, None, q, None, pos, w)
+    near, _, dw1, _ = fa.fa_norm_rotary_backward(r, y, None, x, None, last, w)
+    assert torch.equal(far[-50:], near)
+    # the same 50 addends in another order: 2^-23 of their sizes' sum each time
+    assert ((dw - dw1).abs() <= 100 * 2.0 ** -23 * 50 * 6 * 6).all()
+    assert (torch.cuda.synchronize(), fa.fa_get_device_error())[1] == (0, 0)
