@@ -217,6 +217,18 @@ __device__ __forceinline__ void commit_stage(uint64_t* bar) {
     umma_commit(bar);
 }
 
+// The stages of the last `kStages` of `used` tiles are free in this CTA: by the end of its work the
+// other's commits have arrived on these barriers too.  (One that arrived after this CTA had left would
+// reach shared memory that is no longer its own; the cluster's barrier does not wait for them.)
+template <int CL>
+__device__ __forceinline__ bool stages_free(BwdBars* bars, uint64_t* empty, int used, uint32_t code) {
+  bool ok = true;
+  if constexpr (CL == 2)
+    for (int j = max(used - kStages, 0); ok && j < used; ++j)
+      ok = warp_wait(&empty[j % kStages], (j / kStages) & 1, bars, code);
+  return ok;
+}
+
 template <int CL>
 __device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t tmem) {
   if (warp == kMmaWarp) wait(&bars->drain, 0, bars, 0x2ff);
@@ -226,9 +238,10 @@ __device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t t
     while (globaltimer_ns() - t0 < 200000ull) {
     }
   }
+  __syncwarp();
   tc_fence_before_sync();
   if constexpr (CL == 2)
-    cluster_sync();  // nothing of the other CTA's writes or arrives here any more
+    cluster_sync();  // nothing of the other CTA's writes or arrives here any more (stages_free)
   else
     __syncthreads();
   if (warp == kMmaWarp) {
@@ -425,6 +438,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       ++tl;
       it = next;
     }
+    __syncwarp();
+    if (!bars->abort_flag && stages_free<CL>(bars, bars->x_empty, kvb, 0x106))
+      stages_free<CL>(bars, bars->y_empty, kvb, 0x107);
     __syncwarp();
   } else if (warp >= kMmaWarp) {
     // Three warps issue, S, dP and dQ each: in this kernel 8 products take 500 cycles to issue (in one
@@ -838,6 +854,9 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       ++tl;
       it = next;
     }
+    __syncwarp();
+    if (!bars->abort_flag) stages_free<CL>(bars, bars->x_empty, sb, 0x106);
+    __syncwarp();
   } else if (warp >= kMmaWarp) {
     // Three warps issue (as in the dq kernel): S^T = K Q^T; dP^T = V dO^T; dV += P^T dO and dK += dS^T Q.
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);

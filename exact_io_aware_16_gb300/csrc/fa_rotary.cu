@@ -131,6 +131,18 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// A row's mean square leaves fp32 above 2^120 (and below 2^-100, where eps does not hide it): the
+// power of two that brings the larger of its greatest element and sqrt(eps) to about one.
+template <int L>
+__device__ __noinline__ float row_scale(float most, float eps) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  most = fmaxf(most, sqrtf(eps));
+  if (!(most > 0.0f && most < INFINITY)) return 1.0f;
+  const int e = (__float_as_int(most) >> 23) - 127;
+  return __int_as_float((127 - min(max(e, -126), 126)) << 23);
+}
+
 __device__ __forceinline__ void load_weight8(const RotaryArgs& p, int t, int at, float (&w)[8]) {
   if (p.weight_bf16) {
     unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.weight[t]) + at), w);
@@ -214,13 +226,30 @@ __global__ void __launch_bounds__(kRotaryThreads, blocks_per_sm(MODE))
           float ss = 0.0f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
-          const float r = 1.0f / sqrtf(row_sum<L>(ss) * (1.0f / D) + p.eps);
+          ss = row_sum<L>(ss);
+          float scale = 1.0f;
+          if (__any_sync(0xffffffffu, !(ss <= 0x1p120f) || (ss < 0x1p-100f && p.eps < 0x1p-76f))) {
+            float most = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = fmaxf(most, fmaxf(fabsf(xa[j]), fabsf(xb[j])));
+            scale = row_scale<L>(most, p.eps);
+            ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              xa[j] *= scale;
+              xb[j] *= scale;
+              ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
+            }
+            ss = row_sum<L>(ss);
+          }
+          float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps * scale * scale);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             xa[j] *= r;
             xb[j] *= r;
           }
           if (kBack) {
+            r *= scale;
             turn(m, ga, gb, c, s, kSign);
             float dot = 0.0f;
 #pragma unroll
