@@ -667,16 +667,15 @@ static int view_heads(const fa_heads* t, int heads, long long B, long long T, in
 // swizzle.  A tensor of no tokens gets a map that is never read through.
 static int encode_rows(CUtensorMap* map, const fa::HeadsView& t, int tokens, int d, int P, int TT,
                        const void* otherwise) {
+  // extents of one token and head (see fa_packed.cuh); the plan sets each sequence's
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return FA_ERR_CUDA;
-  const cuuint64_t n = static_cast<cuuint64_t>(tokens > 0 ? tokens : 1);
   const cuuint64_t token = static_cast<cuuint64_t>(t.token) * 2, head = static_cast<cuuint64_t>(t.head) * 2;
   const bool q = P > 0;
-  cuuint64_t kdims[3] = {static_cast<cuuint64_t>(d), n, static_cast<cuuint64_t>(t.heads)};
+  cuuint64_t kdims[3] = {static_cast<cuuint64_t>(d), 1, 1};
   cuuint64_t kstrides[2] = {token, head};
   cuuint32_t kbox[3] = {fa::kBoxCols, static_cast<cuuint32_t>(TT), 1};
-  cuuint64_t qdims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(P), n,
-                         static_cast<cuuint64_t>(q ? t.heads / P : 1)};
+  cuuint64_t qdims[4] = {static_cast<cuuint64_t>(d), 1, 1, 1};
   cuuint64_t qstrides[3] = {head, token, head * static_cast<cuuint64_t>(P)};
   cuuint32_t qbox[4] = {fa::kBoxCols, static_cast<cuuint32_t>(P), static_cast<cuuint32_t>(TT), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};

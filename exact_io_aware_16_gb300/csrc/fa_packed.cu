@@ -83,12 +83,20 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
     const uint32_t len = static_cast<uint32_t>(max(keys ? s.m : s.n, 1));
     asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;" ::"l"(out), "l"(at)
                  : "memory");
-    if (keys)  // (d, tokens, heads)
-      asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(out), "r"(len)
-                   : "memory");
-    else  // (d, heads of a tile, tokens, head groups)
-      asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 2, %1;" ::"l"(out), "r"(len)
-                   : "memory");
+    if (keys) {  // (d, tokens, heads)
+      asm volatile(
+          "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;\n\t"
+          "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 2, %2;" ::"l"(out),
+          "r"(len), "r"(a.Hkv)
+          : "memory");
+    } else {  // (d, heads of a tile, tokens, head groups)
+      asm volatile(
+          "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;\n\t"
+          "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 2, %2;\n\t"
+          "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 3, %3;" ::"l"(out),
+          "r"(a.P), "r"(len), "r"(a.groups)
+          : "memory");
+    }
     asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
     return;
   }
@@ -683,6 +691,9 @@ cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int
     p.token[i] = views[i]->token;
   }
   p.nmaps = nmaps;
+  p.P = t.P;
+  p.groups = t.heads;
+  p.Hkv = Hkv;
   p.cu_q = a.cu_q;
   p.cu_k = a.cu_k;
   p.B = a.B;

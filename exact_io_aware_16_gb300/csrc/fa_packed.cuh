@@ -11,8 +11,12 @@
 //
 // Tensor maps.  Every sequence has its own, whose extent ends where the sequence does:
 // what lies behind reads as zeros, so that neither NaN nor infinities of a
-// neighbour meet a probability of zero in a product.  The plan kernel copies the map of
-// the whole tensor and puts the sequence's address and length in (tensormap.replace).
+// neighbour meet a probability of zero in a product.  The plan kernel copies a map
+// encoded for one token of one head and puts the sequence's address and extents in
+// (tensormap.replace).  Encoded for one token: a map encoded for 128 KB or more makes TMA read for
+// rows outside its extents too, near the map's address (512 boxes with 40 of 128 rows inside: 8.7 MB
+// from L2, and 4.1 MB this way), which is behind the tensor where a short sequence ends it, and
+// need not be mapped.
 //
 // Work.  The lengths are on the device, so the plan kernel also lists all tiles, longest
 // first (a counting sort by key tiles), and persistent CTAs take (tile, head) items off that
@@ -98,10 +102,11 @@ inline PackedLayout packed_layout(int B, int total_q, int total_k, int Hq, int H
 }
 
 struct PackedPlanArgs {
-  CUtensorMap map[4];  // q, k, v, dO of the whole tensors
+  CUtensorMap map[4];  // q, k, v, dO, with extents of one token and head
   const __nv_bfloat16* base[4];
   long long token[4];  // elements between tokens
   int nmaps;
+  int P, groups, Hkv;      // extents: of q and dO (heads of a tile, tiles' heads), of k and v
   const int* cu_q;
   const int* cu_k;
   int B, total_q, total_k;

@@ -335,6 +335,26 @@ def test_two_calls_at_once_have_workspaces_of_their_own(fa):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("d", (64, 128))
+def test_a_short_sequence_ends_an_allocation(fa, d):
+    """The last token ends a block of memory of its own: nothing behind it is read (what lies there
+    need not be mapped)."""
+    n, lens = 12 * 2 ** 20 // (2 * d * 2), [200, 70, 3, 1]
+    cu = ref.starts(lens)
+    near = [rnd(60 + i, cu[-1], 2, d).cuda() for i in range(4)]
+    o1, lse1 = fa.fa_forward_packed(*near[:3], i32(cu), causal=True)
+    want = fa.fa_backward_packed(*near[:3], o1, near[3], lse1, i32(cu), causal=True)
+    whole = [torch.zeros(n, 2, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for t, s in zip(whole, near):
+        t[-cu[-1]:] = s
+    at = i32(ref.starts(lens, n - cu[-1]))
+    o, lse = fa.fa_forward_packed(*whole[:3], at, causal=True)
+    got = fa.fa_backward_packed(*whole[:3], o, whole[3], lse, at, causal=True)
+    ok(fa)
+    assert torch.equal(o[-cu[-1]:], o1) and torch.equal(lse[:, -cu[-1]:], lse1)
+    assert all(torch.equal(a[-cu[-1]:], b) for a, b in zip(got, want))
+
+
 def test_heads_in_chunks(fa):
     """Many items: the heads are taken some at a time (of 32 here six, five times, and two), which
     changes the order of the work and no bit of its results."""
