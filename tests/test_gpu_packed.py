@@ -355,6 +355,29 @@ def test_a_short_sequence_ends_an_allocation(fa, d):
     assert all(torch.equal(a[-cu[-1]:], b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("causal", (True, False))
+@pytest.mark.parametrize("d", (64, 128))
+def test_a_row_whose_scores_are_all_minus_infinity_is_nan(fa, d, causal):
+    """By the definition, exp(-inf - -inf); a row that sees no key stays 0, and no other changes."""
+    lens_q, lens_k, Hq, Hkv = [150, 9], [140, 30], 4, 2
+    cu_q, cu_k = ref.starts(lens_q), ref.starts(lens_k)
+    q, k, v = rnd(70, cu_q[-1], Hq, d), rnd(71, cu_k[-1], Hkv, d), rnd(72, cu_k[-1], Hkv, d)
+    k[:, :, 0] = -k[:, :, 0].abs() - 0.5
+    args = [t.cuda() for t in (q, k, v)]
+    o0, lse0 = fa.fa_forward_packed(*args, i32(cu_q), i32(cu_k), causal=causal)
+    rows, head = [100, 152], 1
+    args[0][rows, head] = 0.0
+    args[0][rows, head, 0] = math.inf
+    o, lse = fa.fa_forward_packed(*args, i32(cu_q), i32(cu_k), causal=causal)
+    ok(fa)
+    for i in rows:
+        assert torch.isnan(o[i, head]).all() and torch.isneginf(lse[head, i])
+    o[rows, head], lse[head, rows] = o0[rows, head], lse0[head, rows]
+    assert torch.equal(o, o0) and torch.equal(lse, lse0)
+    if causal:  # queries 0 to 9 of the first sequence see no key
+        assert (o[:10] == 0).all() and torch.isneginf(lse[:, :10]).all()
+
+
 def test_heads_in_chunks(fa):
     """Many items: the heads are taken some at a time (of 32 here six, five times, and two), which
     changes the order of the work and no bit of its results."""

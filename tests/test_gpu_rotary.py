@@ -357,3 +357,36 @@ def test_tokens_beyond_4_GiB(fa):
     # the same 50 addends in another order: 2^-23 of their sizes' sum each time
     assert ((dw - dw1).abs() <= 100 * 2.0 ** -23 * 50 * 6 * 6).all()
     assert (torch.cuda.synchronize(), fa.fa_get_device_error())[1] == (0, 0)
+
+
+@pytest.mark.parametrize("eps", (1e-6, 0.0, 1e-30))
+@pytest.mark.parametrize("d", (64, 128))
+def test_norm_of_the_largest_and_smallest_rows(fa, d, eps):
+    """Rows whose squares leave fp32, or (where eps does not hide them) vanish in it, beside
+    ordinary ones; their gradients."""
+    r = fa.Rotary(d)
+    g = torch.Generator().manual_seed(8)
+    n = 9
+    sizes = torch.tensor([1.0, 2.0 ** 126, 2.0 ** 70, 2.0 ** 61, 1.0, 2.0 ** -40, 2.0 ** -70, 2.0 ** -120, 2.0 ** 10])
+    x = (torch.randn(n, 3, d, generator=g).clamp(-1.9, 1.9) * sizes[:, None, None]).to(torch.bfloat16)
+    dy = torch.randn(n, 3, d, generator=g).to(torch.bfloat16)
+    w = torch.linspace(0.5, 1.5, d)
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")  # (no turn: the norm alone)
+    y, _ = fa.fa_norm_rotary(r, x.cuda(), None, pos, w.cuda(), eps=eps)
+    # the gradient of rows below 2^-20 or so leaves bf16 for the smallest eps: those of the others
+    keep = sizes >= 2.0 ** -40
+    dx, _, dw, _ = fa.fa_norm_rotary_backward(r, dy.cuda(), None, x.cuda(), None, pos, w.cuda(), eps=eps)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == (0, 0)
+    xd, gd, wd = x.double(), dy.double(), w.double()
+    s = (xd.square().mean(-1, keepdim=True) + float(torch.tensor(eps))) ** -0.5
+    want = wd * xd * s
+    # one rounding to bf16, and 2^-18 for the fp32 steps before it
+    assert ((y.cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -18) * want.abs() + 2.0 ** -133).all()
+    h = xd * s
+    inner = (wd * gd * h).mean(-1, keepdim=True)
+    wdx = s * (wd * gd - h * inner)
+    room = (2.0 ** -8) * wdx.abs() + 2.0 ** -16 * s * ((wd * gd).abs() + (h * inner).abs()) + 2.0 ** -133
+    assert ((dx.cpu().double() - wdx).abs() <= room)[keep].all()
+    wdw = (gd * h).sum((0, 1))
+    assert ((dw.cpu().double() - wdw).abs() <= 2.0 ** -16 * (gd * h).abs().sum((0, 1))).all()
