@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       if (!warp_wait(&bars->pv_done[g], used++ & 1, 0x303)) break;
       tc_fence_after_sync();
       // (a row whose keys all have a score of -inf is NaN, one that sees none is 0)
-      const bool sees = !CAUSAL || tok + off >= 0;
+      const bool sees = !CAUSAL || tok + it.e.m >= it.e.n;
       const float inv_l = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? (sees ? NAN : 0.0f) : l_run);
       // rows of this lane's 4-lane group are stored together, row by row
       long long dst[4];
