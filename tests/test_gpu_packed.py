@@ -112,6 +112,12 @@ def test_sequences_long_enough_for_two_blocks_to_share_their_tiles(fa, lens_q, l
     run_both(fa, lens_q, lens_k, Hq, Hkv, 128, causal, seed=30)
 
 
+@pytest.mark.parametrize("d", (64, 128))
+def test_thousands_of_short_sequences(fa, d):
+    run_both(fa, [b * b % 7 for b in range(2500)], None, 2, 1, d, True, seed=31)
+    run_both(fa, [b % 3 for b in range(1100)], [b % 5 for b in range(1100)], 2, 2, d, False, seed=32)
+
+
 @pytest.mark.parametrize("scale", (1e-3, 1.0, 4.0))
 def test_scales(fa, scale):
     run_both(fa, [200, 31], None, 4, 2, 64, True, seed=13, scale=scale)
