@@ -125,18 +125,18 @@ __device__ __forceinline__ void turn(const LaneMap& m, float (&a)[8], float (&b)
 }
 
 template <int L>
-__device__ __forceinline__ float row_sum(float x) {
+__device__ __forceinline__ float row_sum(float x, unsigned lanes = 0xffffffffu) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(lanes, x, o);
   return x;
 }
 
 // A row's mean square leaves fp32 above 2^120 (and below 2^-100, where eps does not hide it): the
 // power of two that brings the larger of its greatest element and sqrt(eps) to about one.
 template <int L>
-__device__ __noinline__ float row_scale(float most, float eps) {
+__device__ __noinline__ float row_scale(float most, float eps, unsigned lanes) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(lanes, most, o));
   most = fmaxf(most, sqrtf(eps));
   if (!(most > 0.0f && most < INFINITY)) return 1.0f;
   const int e = (__float_as_int(most) >> 23) - 127;
@@ -228,11 +228,12 @@ __global__ void __launch_bounds__(kRotaryThreads, blocks_per_sm(MODE))
           for (int j = 0; j < 8; ++j) ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
           ss = row_sum<L>(ss);
           float scale = 1.0f;
-          if (__any_sync(0xffffffffu, !(ss <= 0x1p120f) || (ss < 0x1p-100f && p.eps < 0x1p-76f))) {
+          if (!(ss <= 0x1p120f && (ss >= 0x1p-100f || p.eps >= 0x1p-76f))) {  // (all lanes of a row)
             float most = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) most = fmaxf(most, fmaxf(fabsf(xa[j]), fabsf(xb[j])));
-            scale = row_scale<L>(most, p.eps);
+            const unsigned lanes = ((1u << L) - 1u) << (lane & ~(L - 1));
+            scale = row_scale<L>(most, p.eps, lanes);
             ss = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kRotaryThreads, blocks_per_sm(MODE))
               xb[j] *= scale;
               ss = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], ss));
             }
-            ss = row_sum<L>(ss);
+            ss = row_sum<L>(ss, lanes);
           }
           float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps * scale * scale);
 #pragma unroll
