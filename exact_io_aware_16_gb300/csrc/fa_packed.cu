@@ -6,8 +6,8 @@
 // a row, with a running maximum that moves only when a row needs it. The next item's tiles are
 // copied while one's products run.
 //
-// Bound by the tensor core at d = 128: two causal sequences of 8192, 32 heads on 8, take 645 us on a
-// cool GPU, 1.70 PFLOP/s of the triangle, and 710 us in a loop, under the power limit. 24 prompts
+// Bound by the tensor core at d = 128: two causal sequences of 8192, 32 heads on 8, take 640 us on a
+// cool GPU, 1.72 PFLOP/s of the triangle, and 710 us in a loop, under the power limit. 24 prompts
 // of 1 to 2048 tokens take 250 us: their diagonal and last tiles are partly empty. At d = 64 the
 // products are half as long, and the chain S, softmax, P V of a tile is what takes the time: 31
 // sequences of up to 1500 tokens, 16 heads on 2, full, take 116 us with the tensor core busy for
