@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
           if ((g ? n1 : n0) == 0) return true;
           const int slot = qc % L::kQTiles;
           if (!wait(&bars->q_empty[slot], ((qc / L::kQTiles) & 1) ^ 1, 0x103)) return false;
-          uint64_t *full = &bars->q_full[g][qt[g]++ & 3];
+          uint64_t* full = &bars->q_full[g][qt[g]++ & 3];
           mbar_arrive_expect_tx(full, q_bytes);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c)
@@ -351,9 +351,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
           ++qc;
           return true;
         };
-        bool ok = true;
         PackedItem next = it;
-        ok = load_q(0);
+        bool ok = load_q(0);
         for (int j = 0; ok && j < nmax; ++j) {
           const int s = ring_slot<D>(kvb + j);
           const uint32_t ph = ring_phase<D>(kvb + j);

@@ -121,8 +121,8 @@ struct PackedPlanArgs {
   PackedEntry* list[2];
 };
 
-// Launches `kern` (one CTA an SM, all of its shared memory dynamic; `cluster` CTAs share tiles) while the kernel before it in
-// the stream still runs, for which it waits itself (griddepcontrol.wait).  `ready` says for which
+// Launches `kern` (one CTA an SM, all of its shared memory dynamic; `cluster` CTAs share tiles)
+// while the kernel before it in the stream still runs, for which it waits itself (griddepcontrol.wait).  `ready` says for which
 // devices the shared memory has been asked for: that call is as long as a launch.
 template <typename Kern, typename Params>
 cudaError_t launch_behind(Kern kern, const Params& p, unsigned blocks, unsigned threads, uint32_t smem,

@@ -21,8 +21,8 @@
 // at half its rate.  (Products of 64 columns run at full rate that way, 33.8 cycles of 32;
 // from shared memory 49.)
 //
-// Measured, four causal samples of 1000 to 8192 tokens (17335), 32 heads on 8, d = 128: dq 790 us, dk and
-// dv 1004 us, the tensor core busy for 71 and 76 % of them; 1.68 PFLOP/s of the seven products,
+// Measured, four causal samples of 1000 to 8192 tokens (17335), 32 heads on 8, d = 128: dq 806 us, dk and
+// dv 1004 us, the tensor core busy for 70 and 76 % of them; 1.66 PFLOP/s of the seven products,
 // near what the power limit leaves. 31 samples of up to 1500 tokens, 16 heads on 2, d = 64, full:
 // 199 and 218 us, 34 and 43 % busy; there the threads' part of a tile takes longer than its products.
 //
@@ -777,7 +777,8 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         item_done<CL>(bars, r);
       }
       if (it.head < 0) break;
-      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL), n = per * p.per_kv;
+      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL);
+      const int n = per * p.per_kv;
       if (n == 0) {
         it = claim();
         continue;
@@ -864,7 +865,9 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
     const int role = warp - kMmaWarp;
     const uint32_t tm = uniform(tmem), sV = uniform(smem_u32(smem + L::kV));
     const uint32_t sQ = uniform(smem_u32(smem + L::kQ)), sdO = uniform(smem_u32(smem + L::kDO));
-    auto stage_in = [&](int pos) { return warp_wait(&bars->x_full[pos % kStages], (pos / kStages) & 1, bars, 0x205); };
+    auto stage_in = [&](int pos) {
+      return warp_wait(&bars->x_full[pos % kStages], (pos / kStages) & 1, bars, 0x205);
+    };
     auto issue_dp = [&](int pos, bool last) {
       const uint32_t o = sdO + pos % kStages * L::kTile;
 #pragma unroll
@@ -899,7 +902,8 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         for (int j = 0; j < n; ++j) {
           const int pos = sb + j;
           // (the P and dS in the buffer have been multiplied)
-          if (!(ok = stage_in(pos) && (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x202))))
+          if (!(ok = stage_in(pos) &&
+                     (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x202))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -986,7 +990,8 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         epilogue();
         break;
       }
-      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL), n = per * p.per_kv;
+      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL);
+      const int n = per * p.per_kv;
       const int key0 = (it.e.tile * CL + rank) * 128, key = key0 + tr;
       const bool valid = key < it.e.m;
       const long long token = it.e.k0 + key;
@@ -1112,14 +1117,14 @@ unsigned grid_of(long long items, int cluster, int sms) {
 template <int D, bool CAUSAL, int CL>
 cudaError_t launch_dq(const BwdParams& p, long long items, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_dq_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDqThreads, DqLayout<D>::kSmem, CL,
-                       ready, s);
+  return launch_behind(fa_packed_dq_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDqThreads,
+                       DqLayout<D>::kSmem, CL, ready, s);
 }
 template <int D, bool CAUSAL, int CL>
 cudaError_t launch_dkdv(const BwdParams& p, long long items, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDkThreads, DkLayout<D>::kSmem, CL,
-                       ready, s);
+  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDkThreads,
+                       DkLayout<D>::kSmem, CL, ready, s);
 }
 
 // Tiles of a sequence, on average, from which two CTAs share what they stream (d = 128): the odd
@@ -1133,7 +1138,9 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   const PackedTiling t = packed_tiling(Hq, Hkv);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, Hq, Hkv, true);
   // CTAs that share a stream: dq, and dk and dv
-  auto share = [&](long long tokens, int tile) { return a.d == 128 && tokens >= 1ll * kShareTiles * tile * a.B ? 2 : 1; };
+  auto share = [&](long long tokens, int tile) {
+    return a.d == 128 && tokens >= 1ll * kShareTiles * tile * a.B ? 2 : 1;
+  };
   const int cq = share(a.total_q, 2 * t.TT64), ck = share(a.total_k, 128);
   cudaError_t e = launch_packed_plan(a, maps, 4, true, cq, ck, s);
   if (e != cudaSuccess) return e;

@@ -346,7 +346,8 @@ cudaError_t launch_t(RotaryArgs a, cudaStream_t s) {
   const long long blocks = (units + kWarps - 1) / kWarps;
   // as many blocks as run at once (of the backward pass each leaves a partial sum)
   const long long most = static_cast<long long>(a.num_sms) * blocks_per_sm(MODE);
-  const unsigned grid = static_cast<unsigned>(std::min(blocks, MODE == 3 ? std::min<long long>(most, kNormMaxBlocks) : most));
+  const unsigned grid =
+      static_cast<unsigned>(std::min(blocks, MODE == 3 ? std::min<long long>(most, kNormMaxBlocks) : most));
   fa_rotary_kernel<D, MODE><<<grid, kRotaryThreads, 0, s>>>(a);
   if (MODE == 3) {
     const cudaError_t e = cudaGetLastError();
