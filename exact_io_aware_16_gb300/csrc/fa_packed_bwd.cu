@@ -1,35 +1,36 @@
 // fa_packed_bwd.cu — backward pass of attention over packed sequences with grouped heads.
 //
-//   P = exp(scale Q K^T - lse),  D_i = sum_c dO_ic o_ic,  dP = dO V^T,  dS = P o (dP - D),
+//   P = exp(scale Q K^T - lse),  dP = dO V^T,  D_i = sum_j P_ij dP_ij,  dS = P o (dP - D),
 //   dQ = scale dS K,  dK = scale sum_heads dS^T Q,  dV = sum_heads P^T dO.
 //
 // Two kernels over the tiles of fa_packed.cuh, each bound by the tensor core:
-//   * dq: 128 query rows stay while 64-row key and value tiles stream; three products a
-//     tile (S, dP, dQ).  It also finds D, for itself and for the next.
+//   * dq: 128 query rows stay while 64-row key and value tiles stream; four products a
+//     tile (S, dP, P K, dS K).  It also finds D, for itself and for the next.
 //   * dk, dv: 128 keys stay while 64-row query tiles of all heads of the group stream, so
 //     that the sums over a group's heads are sums in tensor memory, in a fixed order and
 //     without atomics; four products a tile (S^T, dP^T, dV, dK).  Scores are computed
 //     transposed: a thread owns a key.
-// Together seven products where five would do: S and dP are computed twice, which costs
+// Together eight products where five would do: S and dP are computed twice, which costs
 // less than adding dQ up over key tiles in memory (64 KB a tile pair), and leaves
-// no order to chance.
+// no order to chance; P K makes dQ as exact as D is (below).
 //
 // Operands.  A product of two operands in shared memory reads 8 KB for each 64 cycles of
 // the tensor core, all that shared memory delivers; with the tiles' copies it fell behind by
 // a third.  What stays therefore lies in tensor memory, copied there by the compute threads
-// from where TMA put it, as P and dS do: every product reads one operand from shared memory,
-// at half its rate.  (Products of 64 columns run at full rate that way, 33.8 cycles of 32;
-// from shared memory 49.)
+// from where TMA put it, as P and dS do: a product then reads one operand from shared memory,
+// at half its rate, and those of 64 columns run at full rate (33.8 cycles of 32; from shared memory 49).
+// Tensor memory has room for all that stays at d = 64, and for one of its two tensors at d = 128.
 //
-// Measured, four causal samples of 1000 to 8192 tokens (17335), 32 heads on 8, d = 128: dq 806 us, dk and
-// dv 1004 us, the tensor core busy for 70 and 76 % of them; 1.66 PFLOP/s of the seven products,
-// near what the power limit leaves. 31 samples of up to 1500 tokens, 16 heads on 2, d = 64, full:
-// 199 and 218 us, 34 and 43 % busy; there the threads' part of a tile takes longer than its products.
+// Measured, four causal samples of 1000 to 8192 tokens (17335), 32 heads on 8, d = 128: dq 1090 us, dk and
+// dv 1010 us, 1.64 PFLOP/s of the eight products. 31 samples of up to 1500 tokens, 16 heads on 2, d = 64, full:
+// 234 and 238 us; there the threads' part of a tile takes longer than its products.
 //
-// D from the bf16 o is off by up to half a bf16 step of it.  Where a query sees many keys
-// that is below the rounding of dS; where it sees few, dS may be small against D
-// (a query's own key alone: zero).  Query tiles that see 64 keys or fewer therefore take
-// D = sum_j P_ij dP_ij, which their threads have in registers before dS is needed.
+// D from the bf16 o is off by half a bf16 step of it, and by what the rounding of P cost o.  A row's dS
+// have that error in common: it moves dq by as much times the row's mean key, which for
+// scores that single out a few keys, or keys that lie far to one side, is more than all other roundings
+// together.  The dq kernel therefore corrects dq for the difference to D = sum_j P_ij dP_ij (see there).
+// Query tiles that see 64 keys or fewer take that sum as D from the start, which their threads have
+// in registers before dS is needed: where a query sees its own key alone, dS is zero.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -81,11 +82,12 @@ struct BwdBars {
   uint64_t a_ready;              // and written to tensor memory
   uint64_t x_full[kStages], x_empty[kStages];
   uint64_t y_full[kStages], y_empty[kStages];
-  uint64_t s_full[2], s_done[2];  // scores computed; read (dq), or P written over them (dk, dv)
+  uint64_t s_full[2], s_done[2];  // scores computed; P written over them
   uint64_t dp_full[2], ds_ready[2];
-  uint64_t dp_read[2];  // (dk, dv)
-  uint64_t done[2];  // the products that read a buffer's dS (dq), or P and dS (dk, dv)
-  uint64_t dx_ready, acc_done, acc_free;
+  uint64_t dp_read[2];
+  uint64_t done[2];  // the products that read a buffer's P and dS
+  uint64_t dx_ready, de_ready;  // (dq) halves of a row's D from o, and of its exact D
+  uint64_t acc_done, acc_free;
   uint64_t item_full[kBwdRing], item_empty[kBwdRing];
   uint64_t drain;
   uint32_t tmem_base;
@@ -140,6 +142,7 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
       mbar_init(&bars->ds_ready[b], kCompute);
     }
     mbar_init(&bars->dx_ready, kCompute);
+    mbar_init(&bars->de_ready, kCompute);
     mbar_init(&bars->acc_done, users);
     mbar_init(&bars->acc_free, kCompute);
     for (int r = 0; r < kBwdRing; ++r) {
@@ -323,27 +326,67 @@ __device__ __forceinline__ void store_acc32(uint32_t addr, float mul, __nv_bfloa
   }
 }
 
+// The same of x - d y for two accumulators x and y.
+__device__ __forceinline__ void store_acc32(uint32_t x_addr, uint32_t y_addr, float d, float mul, __nv_bfloat16* dst,
+                                            long long off) {
+  const int lane = threadIdx.x & 31;
+  uint32_t x[32], y[32], w[16];
+  tmem_ld32(x_addr, x);
+  tmem_ld32(y_addr, y);
+  tmem_ld_wait();
+  reg_pin(x);
+  reg_pin(y);
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    x[e] = __float_as_uint(mul * fmaf(-d, __uint_as_float(y[e]), __uint_as_float(x[e])));
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+  transpose_chunks<4>(w);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const long long o = __shfl_sync(0xffffffffu, off, (lane & ~3) + k);
+    if (o >= 0)
+      *reinterpret_cast<uint4*>(dst + o + (lane & 3) * 8) =
+          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+}
+
 __device__ __forceinline__ void store_zeros(__nv_bfloat16* dst, int n) {
   for (int e = 0; e < n / 8; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// ============================================================ dQ
-// Tensor memory: scores and dP (dS over it), each in two buffers of 64 keys (step g's in buffer
-// g & 1), dQ, and Q and dO.  Scores are read into registers and not written back.  Order of
-// the products: S_{n+1}, dP_{n+1}, dQ_n, so that the tensor core works on the next step while
-// threads form P_n and dS_n.
+// Tensor memory of both kernels: scores of 64 streamed rows in two buffers (step g's in buffer g & 1), dP,
+// two accumulators, and what stays: at d = 64 both its tensors and a second dP, at d = 128 one of them; the
+// other stays in shared memory (its product then runs at the speed of shared memory, 49 cycles where
+// 33 would do).  P and dS lie over the scores, whose bits they take half of: so dP is free again
+// once it has been read, and its next product does not wait for those of P and dS.
 template <int D>
-struct DqLayout {
+struct BwdTmem {
+  static constexpr bool kBothStay = D == 64;  // and two dP buffers
+  static constexpr int kDpBufs = kBothStay ? 2 : 1;
+  static constexpr uint32_t kAcc0 = 128 + 64 * kDpBufs, kAcc1 = kAcc0 + D;
+  static constexpr uint32_t kStay0 = kAcc1 + D;  // Q or K, the scores' operand
+  __host__ __device__ static constexpr uint32_t stay1_col() { return kStay0 + D / 2; }  // dO or V, dP's
+  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * (step & 1); }
+  __host__ __device__ static constexpr int dp_buf(int step) { return kBothStay ? step & 1 : 0; }
+  __host__ __device__ static constexpr uint32_t dp_par(int step) { return kBothStay ? (step >> 1) & 1 : step & 1; }
+  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 64u * dp_buf(step); }
+};
+
+// ============================================================ dQ
+// D is needed before the loop over key tiles has seen the whole row.  The loop therefore takes D' = sum_c
+// dO o from the bf16 o, and beside dQ' = sum_j P_ij (dP_ij - D') k_j it finds D = sum_j P_ij dP_ij in fp32 and
+// R = sum_j P_ij k_j, one more product; dQ = scale (dQ' - (D - D') R) is then free of the error that o's and P's
+// rounding put into D', and D goes to the dk, dv kernel.
+template <int D>
+struct DqLayout : BwdTmem<D> {
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kRes = 128u * D * 2, kTile = 64u * D * 2;
   static constexpr uint32_t kQ = 0, kDO = kRes, kK = 2 * kRes, kV = kK + kStages * kTile;
-  static constexpr uint32_t kDx = kV + kStages * kTile;  // [half][128]
-  static constexpr uint32_t kBar = kDx + 1024;
+  static constexpr uint32_t kDx = kV + kStages * kTile;  // [D' | D][half][128]
+  static constexpr uint32_t kBar = kDx + 2048;
   static constexpr uint32_t kUsed = kBar + kBarBytes;
   static constexpr uint32_t kSmem = kUsed > 118784u ? kUsed : 118784u;  // one CTA an SM
-  static constexpr uint32_t kAcc = 256, kQA = 384, kDOA = 384 + D / 2;
-  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * (step & 1); }
-  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 64u * (step & 1); }
 };
 static_assert(DqLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
@@ -360,7 +403,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
-  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1, kDqMma, 0)) return;
+  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1, kDqMma, L::kBothStay ? 0 : 1)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
   grid_dependency_launch();
@@ -443,15 +486,16 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       stages_free<CL>(bars, bars->y_empty, kvb, 0x107);
     __syncwarp();
   } else if (warp >= kMmaWarp) {
-    // Three warps issue, S, dP and dQ each: in this kernel 8 products take 500 cycles to issue (in one
-    // that does nothing else 210), a wait that is over 70, and a warp that issued dP and dQ took
-    // 1350 cycles a step.  The whole warp runs the loop on values that are the same in all
+    // Three warps issue, S, dP, and P K and dS K: 8 products take 210 cycles to issue in a kernel that does
+    // nothing else and up to 500 in one like this, a wait that is over 70; where one warp issued dP and dQ
+    // it took 1350 cycles a step.  The whole warp runs the loop on values that are the same in all
     // lanes, so that descriptors lie in uniform registers, where the instruction wants them;
     // one elected lane issues.
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D, false, true);
     const int role = warp - kMmaWarp;
     const uint32_t tm = uniform(tmem), sK = uniform(smem_u32(smem + L::kK)), sV = uniform(smem_u32(smem + L::kV));
+    [[maybe_unused]] const uint32_t sdO = uniform(smem_u32(smem + L::kDO));
     int kvb = 0, tl = 0;
     for (int t = 0;; ++t) {
       if (!item_wait<CL>(bars, t, 0x21b)) break;
@@ -466,15 +510,15 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int pos = kvb + j, s = pos % kStages;
-          // (the buffer's last scores have been read)
+          // (the P and dS in the buffer have been multiplied)
           if (!(ok = warp_wait(&bars->x_full[s], (pos / kStages) & 1, bars, 0x211) &&
-                     (pos < 2 || warp_wait(&bars->s_done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x212))))
+                     (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x212))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_ts(tm + L::s_col(pos), tm + L::kQA + kk * 8, kmajor_desc(sK + s * L::kTile, kk), idesc_s,
+              umma_ts(tm + L::s_col(pos), tm + L::kStay0 + kk * 8, kmajor_desc(sK + s * L::kTile, kk), idesc_s,
                       kk > 0 ? 1u : 0u);
             umma_commit(&bars->s_full[pos & 1]);
           }
@@ -483,37 +527,50 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       } else if (role == 1) {
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int pos = kvb + j, s = pos % kStages;
-          // (the buffer's last dS has been multiplied)
+          const int pos = kvb + j, s = pos % kStages, before = pos - L::kDpBufs;
+          // (the buffer's last dP has been read)
           if (!(ok = warp_wait(&bars->y_full[s], (pos / kStages) & 1, bars, 0x213) &&
-                     (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x215))))
+                     (before < 0 || warp_wait(&bars->dp_read[L::dp_buf(before)], L::dp_par(before), bars, 0x215))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ts(tm + L::dp_col(pos), tm + L::kDOA + kk * 8, kmajor_desc(sV + s * L::kTile, kk), idesc_s,
-                      kk > 0 ? 1u : 0u);
-            umma_commit(&bars->dp_full[pos & 1]);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              if constexpr (L::kBothStay)
+                umma_ts(tm + L::dp_col(pos), tm + L::stay1_col() + kk * 8, kmajor_desc(sV + s * L::kTile, kk), idesc_s,
+                        kk > 0 ? 1u : 0u);
+              else
+                umma_ss(tm + L::dp_col(pos), sdesc_sw128(sdO + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
+                        kmajor_desc(sV + s * L::kTile, kk), idesc_s, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bars->dp_full[L::dp_buf(pos)]);
             commit_stage<CL>(&bars->y_empty[s]);
+            if (!L::kBothStay && j + 1 == n) umma_commit(&bars->res_empty);
           }
           __syncwarp();
         }
       } else {
+        // R += P K_j and dQ' += dS K_j (A = bf16 in tensor memory over the scores)
+        auto issue_acc = [&](uint32_t acc, uint32_t a, int s, bool first) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts(acc, a + packed_a_col(kk), mnmajor_desc(sK + s * L::kTile, kk), idesc_acc,
+                    (!first || kk > 0) ? 1u : 0u);
+        };
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int pos = kvb + j, s = pos % kStages;
-          // dQ += dS K_j (A = dS bf16 in tensor memory over dP); an item's first overwrites the
-          // accumulator that the epilogue before it reads
+          // an item's first overwrite the accumulators that the epilogue before it reads
           if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216)) &&
-                     warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214)))
+                     warp_wait(&bars->s_done[pos & 1], (pos >> 1) & 1, bars, 0x217)))
             break;
           tc_fence_after_sync();
+          if (elect_one()) issue_acc(tm + L::kAcc0, tm + L::s_col(pos), s, j == 0);
+          __syncwarp();
+          if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214))) break;
+          tc_fence_after_sync();
           if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ts(tm + L::kAcc, tm + L::dp_col(pos) + packed_a_col(kk), mnmajor_desc(sK + s * L::kTile, kk),
-                      idesc_acc, (j > 0 || kk > 0) ? 1u : 0u);
+            issue_acc(tm + L::kAcc1, tm + L::s_col(pos) + 16, s, j == 0);
             umma_commit(&bars->done[pos & 1]);
             commit_stage<CL>(&bars->x_empty[s]);
             if (j + 1 == n) umma_commit(&bars->acc_done);
@@ -536,22 +593,32 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
     const int box = tr >> 6, box_tok = (tr & 63) / p.P, row_head = (tr & 63) - box_tok * p.P;
     const bool row_in = box_tok < p.TT64;
     const int row_tok = box * p.TT64 + box_tok;
-    // (an item's parts have been read by all threads before any writes the next's: it has waited
-    // for the item's dQ, which needs the last dS of all)
+    // (an item's parts of D' have been read by all threads before any writes the next's: it has waited
+    // for the item's dQ, which needs the last dS of all; and its parts of D before any writes the
+    // next's, since all read them before they give that item's parts of D')
     float* dx = reinterpret_cast<float*>(smem + L::kDx);
-    int nb = 0, tl = 0;  // steps and items with products so far
+    float* de = dx + 256;
+    int nb = 0, tl = 0, te = 0;  // steps, items with products, and of those with D in parts so far
     // dQ of the item before: stored when the next one's Q and dO lie in tensor memory, so that its
     // first products run meanwhile
-    bool pending = false;
-    long long pending_at = -1;
+    bool pending = false, in_parts = false;
+    long long pending_at = -1, pending_vec = -1;
+    float D0 = 0.0f;  // its D'
     auto epilogue = [&]() {
       if (!pending) return true;
+      float Di = D0;
+      if (in_parts) {
+        if (!warp_wait(&bars->de_ready, te++ & 1, bars, 0x316)) return false;
+        Di = de[tr] + de[128 + tr];
+      }
+      if (g == 0 && pending_at >= 0) p.D[pending_vec] = Di;
       if (!warp_wait(&bars->acc_done, (tl - 1) & 1, bars, 0x312)) return false;
       tc_fence_after_sync();
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
-        store_acc32(tm + L::kAcc + (D / 2) * g + c * 32, p.scale, p.dq + c * 32, pending_at);
-      // the accumulator has been read: the next item may overwrite it
+        store_acc32(tm + L::kAcc1 + (D / 2) * g + c * 32, tm + L::kAcc0 + (D / 2) * g + c * 32, Di - D0, p.scale,
+                    p.dq + c * 32, pending_at);
+      // the accumulators have been read: the next item may overwrite them
       tc_fence_before_sync();
       mbar_arrive(&bars->acc_free);
       pending = false;
@@ -588,7 +655,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       }
       bool ok = true;
       float Di = 0.0f;
-      // the halves' parts of D meet in shared memory
+      // the halves' parts of D' (of D itself in an item of one step) meet in shared memory
       auto join = [&](float part) {
         dx[g * 128 + tr] = part;
         mbar_arrive(&bars->dx_ready);
@@ -602,9 +669,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       {
         uint32_t w[D / 4];
         load_half_row<D>(smem + L::kQ, tr, g, valid, w);
-        store_half_row<D>(tm + L::kQA, g, w);
+        store_half_row<D>(tm + L::kStay0, g, w);
         load_half_row<D>(smem + L::kDO, tr, g, valid, w);
-        store_half_row<D>(tm + L::kDOA, g, w);
+        if constexpr (L::kBothStay) store_half_row<D>(tm + L::stay1_col(), g, w);
         mbar_arrive(&bars->res_empty);
         tmem_st_wait();
         tc_fence_before_sync();
@@ -630,14 +697,13 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
       const uint32_t col0 = 32u * g;
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
+      float2 exact = make_float2(0.f, 0.f);  // sum of P dP
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
         if (!(ok = warp_wait(&bars->s_full[step & 1], (step >> 1) & 1, bars, 0x311))) break;
         tc_fence_after_sync();
         uint32_t pr[32];
         tmem_ld(tm + L::s_col(step) + col0, pr);
-        tc_fence_before_sync();
-        mbar_arrive(&bars->s_done[step & 1]);
         const int kv0 = j * 64;
         const bool need_mask = (CAUSAL && kv0 + 63 > tok0 + off) || kv0 + 64 > m;
         auto exp_cols = [&](auto masked, int lim) {
@@ -658,18 +724,31 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
           exp_cols(std::true_type{}, (CAUSAL ? min(tok + off, m - 1) : m - 1) - kv0 - static_cast<int>(col0));
         else
           exp_cols(std::false_type{}, 0);
-        if (!(ok = warp_wait(&bars->dp_full[step & 1], (step >> 1) & 1, bars, 0x314))) break;
+        {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16x2(__uint_as_float(pr[2 * c]), __uint_as_float(pr[2 * c + 1]));
+          tmem_st16(tm + L::s_col(step) + col0, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&bars->s_done[step & 1]);
+        if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x314))) break;
         tc_fence_after_sync();
-        const uint32_t dp = tm + L::dp_col(step) + col0;
         uint32_t rr[32];
-        tmem_ld(dp, rr);
-        if (n == 1) {  // D = sum_j P_j dP_j
-          float2 part = make_float2(0.f, 0.f);
+        tmem_ld(tm + L::dp_col(step) + col0, rr);
+        tc_fence_before_sync();
+        mbar_arrive(&bars->dp_read[L::dp_buf(step)]);
+        auto add_exact = [&]() {
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
-            part = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])),
-                              make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), part);
-          join(part.x + part.y);
+            exact = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])),
+                               make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), exact);
+        };
+        if (D == 64 || n == 1) add_exact();
+        if (n == 1) {
+          join(exact.x + exact.y);
           if (!ok) break;
         }
         const float2 nD2 = make_float2(-Di, -Di);
@@ -681,14 +760,23 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
               __fadd2_rn(make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), nD2));
           ds[e] = pack_bf16x2(x.x, x.y);
         }
-        tmem_st16(dp, ds);
+        tmem_st16(tm + L::s_col(step) + col0 + 16, ds);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&bars->ds_ready[step & 1]);
+        // (at d = 128 while the products run, 1.6 % faster there; at d = 64, where the threads bound the
+        // kernel, 31 full samples of up to 1500 tokens take 254 us that way, and 234 the other)
+        if (D == 128 && n > 1) add_exact();
       }
       if (!ok) break;
-      if (g == 0 && valid) p.D[vec] = Di;
+      if (n > 1) {
+        de[g * 128 + tr] = exact.x + exact.y;
+        mbar_arrive(&bars->de_ready);
+      }
       pending = true;
+      in_parts = n > 1;
+      D0 = Di;
+      pending_vec = vec;
       pending_at = valid ? token * p.dq_token + head * p.dq_head + (D / 2) * g : -1;
       nb += n;
       ++tl;
@@ -698,13 +786,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
 }
 
 // ============================================================ dK / dV
-// Tensor memory: S^T of 64 queries in two buffers, dP^T, dV, dK and K; at d = 64 there is room for V
-// and a second dP^T, at d = 128 V stays in shared memory (its product then runs at the speed
-// of shared memory, 49 cycles where 33 would do).  P^T and dS^T lie over S^T, whose bits
-// they take half of: so dP^T is free again once it has been read, and its next product does
-// not wait for dK.
 template <int D>
-struct DkLayout {
+struct DkLayout : BwdTmem<D> {
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kRes = 128u * D * 2, kTile = 64u * D * 2;
   static constexpr uint32_t kK = 0, kV = kRes, kQ = 2 * kRes, kDO = kQ + kStages * kTile;
@@ -712,14 +795,6 @@ struct DkLayout {
   static constexpr uint32_t kBar = kVec + kStages * 512;
   static constexpr uint32_t kUsed = kBar + kBarBytes;
   static constexpr uint32_t kSmem = kUsed > 118784u ? kUsed : 118784u;  // one CTA an SM
-  static constexpr bool kVInTmem = D == 64;  // and two dP^T buffers
-  static constexpr uint32_t kAcc0 = kVInTmem ? 256 : 192, kAcc1 = kAcc0 + D, kKA = kAcc1 + D;
-  [[maybe_unused]] static constexpr uint32_t kVA = kKA + D / 2;
-  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * (step & 1); }
-  static constexpr int kDpBufs = kVInTmem ? 2 : 1;
-  __host__ __device__ static constexpr int dp_buf(int step) { return kVInTmem ? step & 1 : 0; }
-  __host__ __device__ static constexpr uint32_t dp_par(int step) { return kVInTmem ? (step >> 1) & 1 : step & 1; }
-  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 64u * dp_buf(step); }
 };
 static_assert(DkLayout<128>::kSmem <= 232448, "227 KB a CTA");
 
@@ -741,7 +816,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
   const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int TT = p.TT64;
   if (!bwd_init<CL>(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 1, kDkMma,
-                    L::kVInTmem ? 0 : 1))
+                    L::kBothStay ? 0 : 1))
     return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
@@ -872,14 +947,14 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       const uint32_t o = sdO + pos % kStages * L::kTile;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        if constexpr (L::kVInTmem)
-          umma_ts(tm + L::dp_col(pos), tm + L::kVA + kk * 8, kmajor_desc(o, kk), idesc_s, kk > 0 ? 1u : 0u);
+        if constexpr (L::kBothStay)
+          umma_ts(tm + L::dp_col(pos), tm + L::stay1_col() + kk * 8, kmajor_desc(o, kk), idesc_s, kk > 0 ? 1u : 0u);
         else
           umma_ss(tm + L::dp_col(pos), sdesc_sw128(sV + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
                   kmajor_desc(o, kk), idesc_s, kk > 0 ? 1u : 0u);
       }
       umma_commit(&bars->dp_full[L::dp_buf(pos)]);
-      if (!L::kVInTmem && last) umma_commit(&bars->res_empty);
+      if (!L::kBothStay && last) umma_commit(&bars->res_empty);
     };
     // acc (+)= A x the rows at `tile` (A = bf16 in tensor memory at `a`)
     auto issue_acc = [&](uint32_t acc, uint32_t a, uint32_t tile, bool first) {
@@ -910,7 +985,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
             const uint32_t q = sQ + pos % kStages * L::kTile;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_ts(tm + L::s_col(pos), tm + L::kKA + kk * 8, kmajor_desc(q, kk), idesc_s, kk > 0 ? 1u : 0u);
+              umma_ts(tm + L::s_col(pos), tm + L::kStay0 + kk * 8, kmajor_desc(q, kk), idesc_s, kk > 0 ? 1u : 0u);
             umma_commit(&bars->s_full[pos & 1]);
           }
           __syncwarp();
@@ -1010,10 +1085,10 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       {
         uint32_t w[D / 4];
         load_half_row<D>(smem + L::kK, tr, g, true, w);
-        store_half_row<D>(tm + L::kKA, g, w);
-        if constexpr (L::kVInTmem) {
+        store_half_row<D>(tm + L::kStay0, g, w);
+        if constexpr (L::kBothStay) {
           load_half_row<D>(smem + L::kV, tr, g, true, w);
-          store_half_row<D>(tm + L::kVA, g, w);
+          store_half_row<D>(tm + L::stay1_col(), g, w);
         }
       }
       mbar_arrive(&bars->res_empty);

@@ -426,14 +426,12 @@ int fa_forward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, c
 /*
  * Backward pass of fa_forward_packed: dq (as q), dk and dv (as k and v, the sums
  * over the query heads of a group) from dO (as o), o and lse of the forward pass.
- * dP = dO V^T, D_i = sum_c dO_ic o_ic, dS = P o (dP - D), dq = scale dS K, dk = scale
+ * dP = dO V^T, D_i = sum_j P_ij dP_ij, dS = P o (dP - D), dq = scale dS K, dk = scale
  * dS^T Q, dv = P^T dO.  A query that sees no key has dq = 0 and adds nothing;
  * keys that no query sees have dk = dv = 0; tokens in no sequence are left as they
  * were.  Results do not depend on the order in which the GPU runs the work.
- * Unlike fa_backward, D is the fp32 sum over the bf16 o alone: it is off by up to
- * half a bf16 step of o, times dO.  (Where that would tell most, for the first queries
- * of a sequence, D is the sum of P o dP instead: 128 rows of queries and heads none of
- * which sees more than 64 keys.)  P and dS are rounded to bf16 before their products,
+ * As in fa_backward, D_i is the definition sum_j P_ij dP_ij in fp32, to which dq and dk are
+ * corrected (o enters as an estimate of it).  P and dS are rounded to bf16 before their products,
  * all sums are fp32.  Arguments and errors otherwise as for
  * fa_forward_packed; workspace: fa_backward_packed_workspace_size() bytes.
  */
