@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
 template <int D, bool CAUSAL>
 cudaError_t launch_t(const FwdParams& p, unsigned blocks, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_fwd_kernel<D, CAUSAL>, p, blocks, kFwdThreads, FwdLayout<D>::kSmem, 1, ready, s);
+  return launch_behind(fa_packed_fwd_kernel<D, CAUSAL>, p, blocks, kFwdThreads, FwdLayout<D>::kSmem, ready, s);
 }
 
 int bucket_shift(long long most) {
@@ -676,8 +676,8 @@ int bucket_shift(long long most) {
 
 }  // namespace
 
-cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward, int q_tiles,
-                               int k_tiles, cudaStream_t s) {
+cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward,
+                               cudaStream_t s) {
   const int Hq = a.q.heads, Hkv = a.k.heads;
   const PackedTiling t = packed_tiling(Hq, Hkv);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, Hq, Hkv, backward);
@@ -699,8 +699,8 @@ cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int
   p.total_q = a.total_q;
   p.total_k = a.total_k;
   p.causal = a.causal;
-  p.q_span = q_tiles * (backward ? 2 * t.TT64 : t.TT);
-  p.k_span = k_tiles * 128;
+  p.q_span = 2 * (backward ? t.TT64 : t.TT);  // an entry of the forward pass is two tiles, each of 128 rows
+  p.k_span = 128;
   p.TT64 = t.TT64;
   p.nlists = backward ? 2 : 1;
   p.most[0] = static_cast<unsigned>(a.total_q / p.q_span + a.B);
@@ -718,7 +718,7 @@ cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int
 cudaError_t launch_forward_packed(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s) {
   const PackedTiling t = packed_tiling(a.q.heads, a.k.heads);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, a.q.heads, a.k.heads, false);
-  cudaError_t e = launch_packed_plan(a, maps, 3, false, 2, 1, s);
+  cudaError_t e = launch_packed_plan(a, maps, 3, false, s);
   if (e != cudaSuccess) return e;
   char* ws = static_cast<char*>(a.workspace);
   FwdParams p{};

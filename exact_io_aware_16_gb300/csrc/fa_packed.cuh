@@ -121,12 +121,12 @@ struct PackedPlanArgs {
   PackedEntry* list[2];
 };
 
-// Launches `kern` (one CTA an SM, all of its shared memory dynamic; `cluster` CTAs share tiles)
-// while the kernel before it in the stream still runs, for which it waits itself (griddepcontrol.wait).  `ready` says for which
+// Launches `kern` (one CTA an SM, all of its shared memory dynamic) while the kernel before it in the stream
+// still runs, for which it waits itself (griddepcontrol.wait).  `ready` says for which
 // devices the shared memory has been asked for: that call is as long as a launch.
 template <typename Kern, typename Params>
 cudaError_t launch_behind(Kern kern, const Params& p, unsigned blocks, unsigned threads, uint32_t smem,
-                          unsigned cluster, std::atomic<unsigned long long>& ready, cudaStream_t s) {
+                          std::atomic<unsigned long long>& ready, cudaStream_t s) {
   if (blocks == 0) return cudaSuccess;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -136,25 +136,21 @@ cudaError_t launch_behind(Kern kern, const Params& p, unsigned blocks, unsigned 
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(blocks);
   c.blockDim = dim3(threads);
   c.dynamicSmemBytes = smem;
   c.stream = s;
-  c.attrs = at;
-  c.numAttrs = cluster > 1 ? 2 : 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, kern, p);
 }
 
-// q_tiles, k_tiles: tiles that an entry of list 0 and 1 holds.
-cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward, int q_tiles,
-                               int k_tiles, cudaStream_t s);
+cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int nmaps, bool backward,
+                               cudaStream_t s);
 
 // ---------------------------------------------------------------- device side
 // Keys that query token `tok` of a sequence sees.
@@ -183,73 +179,6 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-
-// ---------------------------------------------------------------- clusters
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// All threads of all CTAs of the cluster.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of the same shared memory in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_map(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ int cluster_load(uint32_t addr) {
-  int x;
-  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
-  return x;
-}
-__device__ __forceinline__ void cluster_store16(uint32_t addr, const uint4& x) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z),
-               "r"(x.w)
-               : "memory");
-}
-__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// mbar_try_wait that also sees what another CTA of the cluster wrote before it arrived.
-__device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// The loads below write the same place of every CTA in `mask`, and count on its barrier there.
-__device__ __forceinline__ void tma_load_3d_all(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                                int y, int z, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "h"(mask)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_4d_all(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                                int y, int z, int w, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "h"(mask)
-      : "memory");
-}
-// umma_commit that arrives on the barrier at this place of every CTA in `mask`.
-__device__ __forceinline__ void umma_commit_all(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
       : "memory");
 }
 

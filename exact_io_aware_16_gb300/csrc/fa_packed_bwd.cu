@@ -117,8 +117,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 // Barriers and tensor memory; rows of [zero, zero + bytes) that no box fills are zeroed.
 // `users`: MMA warps whose products read a stage, and which write an accumulator; `mma`: all;
 // `resident`: those that read what stays from shared memory.
-// Returns false (for the whole cluster) when an earlier CTA recorded a timeout.
-template <int CL>
+// Returns false when an earlier CTA recorded a timeout.
 __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t* smem, uint8_t* zero,
                                          uint32_t bytes, int users, int mma, int resident) {
   if (threadIdx.x == 0) {
@@ -129,9 +128,9 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
     mbar_init(&bars->a_ready, kCompute);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->x_full[s], 1);
-      mbar_init(&bars->x_empty[s], users * CL);  // each CTA reads what all have loaded
+      mbar_init(&bars->x_empty[s], users);
       mbar_init(&bars->y_full[s], 1);
-      mbar_init(&bars->y_empty[s], CL);
+      mbar_init(&bars->y_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
@@ -147,8 +146,7 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
     mbar_init(&bars->acc_free, kCompute);
     for (int r = 0; r < kBwdRing; ++r) {
       mbar_init(&bars->item_full[r], 1);
-      // the compute and MMA warps; the first CTA's holds those of the second, and its TMA warp
-      mbar_init(&bars->item_empty[r], CL * (kCompute / 32 + mma) + CL - 1);
+      mbar_init(&bars->item_empty[r], kCompute / 32 + mma);  // the compute and MMA warps
     }
     mbar_init(&bars->drain, mma);
     bars->abort_flag = (*static_cast<volatile unsigned int*>(&g_packed_bwd_error) != 0) ? 1 : 0;
@@ -159,16 +157,8 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
       reinterpret_cast<uint4*>(zero)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
-  if constexpr (CL == 1) {
-    __syncthreads();
-    if (bars->abort_flag) return false;
-  } else {
-    cluster_sync();
-    const int other = cluster_load(cluster_map(&bars->abort_flag, cluster_rank() ^ 1u));
-    const bool stop = bars->abort_flag != 0 || other != 0;
-    cluster_sync();  // the flags have been read before either CTA leaves or raises one
-    if (stop) return false;
-  }
+  __syncthreads();
+  if (bars->abort_flag) return false;
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
@@ -179,60 +169,15 @@ __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t*
   return true;
 }
 
-// An item for every role of the cluster: written where each CTA looks for it (by the first CTA's
-// producer), waited for, and given back once it has been read (by whole warps).
-template <int CL>
-__device__ __forceinline__ void item_publish(BwdBars* bars, int r, const PackedItem& it) {
-  bars->item[r] = it;
-  if constexpr (CL == 2) {
-    const uint4* w = reinterpret_cast<const uint4*>(&it);
-    const uint32_t to = cluster_map(&bars->item[r], 1);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) cluster_store16(to + 16 * i, w[i]);
-    cluster_arrive(cluster_map(&bars->item_full[r], 1));
-  }
-  mbar_arrive(&bars->item_full[r]);
-}
-template <int CL>
+// An item, waited for, and given back once it has been read (by whole warps).
 __device__ __forceinline__ bool item_wait(BwdBars* bars, int t, uint32_t code) {
-  const int r = t % kBwdRing;
-  const uint32_t par = (t / kBwdRing) & 1;
-  bool ok = wait(&bars->item_full[r], par, bars, code);
-  if (CL == 2 && ok) ok = cluster_try_wait(&bars->item_full[r], par);  // (over: for what it lets see)
-  return __all_sync(0xffffffffu, ok);
+  return warp_wait(&bars->item_full[t % kBwdRing], (t / kBwdRing) & 1, bars, code);
 }
-template <int CL>
 __device__ __forceinline__ void item_done(BwdBars* bars, int r) {
   __syncwarp();
-  if (lane_id() == 0) {
-    if constexpr (CL == 2)
-      cluster_arrive(cluster_map(&bars->item_empty[r], 0));
-    else
-      mbar_arrive(&bars->item_empty[r]);
-  }
+  if (lane_id() == 0) mbar_arrive(&bars->item_empty[r]);
 }
 
-template <int CL>
-__device__ __forceinline__ void commit_stage(uint64_t* bar) {
-  if constexpr (CL == 2)
-    umma_commit_all(bar, 3);
-  else
-    umma_commit(bar);
-}
-
-// The stages of the last `kStages` of `used` tiles are free in this CTA: by the end of its work the
-// other's commits have arrived on these barriers too.  (One that arrived after this CTA had left would
-// reach shared memory that is no longer its own; the cluster's barrier does not wait for them.)
-template <int CL>
-__device__ __forceinline__ bool stages_free(BwdBars* bars, uint64_t* empty, int used, uint32_t code) {
-  bool ok = true;
-  if constexpr (CL == 2)
-    for (int j = max(used - kStages, 0); ok && j < used; ++j)
-      ok = warp_wait(&empty[j % kStages], (j / kStages) & 1, bars, code);
-  return ok;
-}
-
-template <int CL>
 __device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t tmem) {
   if (warp == kMmaWarp) wait(&bars->drain, 0, bars, 0x2ff);
   if (bars->abort_flag) {
@@ -243,10 +188,7 @@ __device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t t
   }
   __syncwarp();
   tc_fence_before_sync();
-  if constexpr (CL == 2)
-    cluster_sync();  // nothing of the other CTA's writes or arrives here any more (stages_free)
-  else
-    __syncthreads();
+  __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
@@ -355,31 +297,40 @@ __device__ __forceinline__ void store_zeros(__nv_bfloat16* dst, int n) {
   for (int e = 0; e < n / 8; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Tensor memory of both kernels: scores of 64 streamed rows in two buffers (step g's in buffer g & 1), dP,
-// two accumulators, and what stays: at d = 64 both its tensors and a second dP, at d = 128 one of them; the
-// other stays in shared memory (its product then runs at the speed of shared memory, 49 cycles where
-// 33 would do).  P and dS lie over the scores, whose bits they take half of: so dP is free again
-// once it has been read, and its next product does not wait for those of P and dS.
-template <int D>
+// Tensor memory of both kernels: scores of 64 streamed rows, dP, two accumulators, and what stays.  P and dS lie
+// over the scores, whose bits they take half of: so dP is free again once it has been read, and its next
+// product does not wait for those of P and dS.  At d = 64 there are two buffers of scores and of dP (step
+// g's in buffer g & 1).  At d = 128 there is room for two of scores or for both tensors that stay, by DP_SMEM,
+// the operands that dP's product reads from shared memory: 1, scores in one buffer; 2, one tensor stays in
+// shared memory until the item's last dP, and its product runs at the speed of shared memory (49 cycles where
+// 33 would do).
+template <int D, int DP_SMEM>
 struct BwdTmem {
-  static constexpr bool kBothStay = D == 64;  // and two dP buffers
-  static constexpr int kDpBufs = kBothStay ? 2 : 1;
-  static constexpr uint32_t kAcc0 = 128 + 64 * kDpBufs, kAcc1 = kAcc0 + D;
+  static constexpr bool kBothStay = DP_SMEM == 1;
+  static constexpr int kSBufs = D == 128 && kBothStay ? 1 : 2, kDpBufs = D == 64 ? 2 : 1;
+  static constexpr uint32_t kDp = 64 * kSBufs;
+  static constexpr uint32_t kAcc0 = kDp + 64 * kDpBufs, kAcc1 = kAcc0 + D;
   static constexpr uint32_t kStay0 = kAcc1 + D;  // Q or K, the scores' operand
   __host__ __device__ static constexpr uint32_t stay1_col() { return kStay0 + D / 2; }  // dO or V, dP's
-  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * (step & 1); }
-  __host__ __device__ static constexpr int dp_buf(int step) { return kBothStay ? step & 1 : 0; }
-  __host__ __device__ static constexpr uint32_t dp_par(int step) { return kBothStay ? (step >> 1) & 1 : step & 1; }
-  __host__ __device__ static constexpr uint32_t dp_col(int step) { return 128u + 64u * dp_buf(step); }
+  // a step's buffers, and the parities of their barriers
+  __host__ __device__ static constexpr int s_buf(int step) { return kSBufs == 2 ? step & 1 : 0; }
+  __host__ __device__ static constexpr uint32_t s_par(int step) { return kSBufs == 2 ? (step >> 1) & 1 : step & 1; }
+  __host__ __device__ static constexpr uint32_t s_col(int step) { return 64u * s_buf(step); }
+  __host__ __device__ static constexpr int dp_buf(int step) { return kDpBufs == 2 ? step & 1 : 0; }
+  __host__ __device__ static constexpr uint32_t dp_par(int step) { return kDpBufs == 2 ? (step >> 1) & 1 : step & 1; }
+  __host__ __device__ static constexpr uint32_t dp_col(int step) { return kDp + 64u * dp_buf(step); }
 };
+static_assert(BwdTmem<64, 1>::stay1_col() + 32 <= 512 && BwdTmem<128, 1>::stay1_col() + 64 <= 512 &&
+                  BwdTmem<128, 2>::kStay0 + 64 <= 512,
+              "512 columns");
 
 // ============================================================ dQ
 // D is needed before the loop over key tiles has seen the whole row.  The loop therefore takes D' = sum_c
 // dO o from the bf16 o, and beside dQ' = sum_j P_ij (dP_ij - D') k_j it finds D = sum_j P_ij dP_ij in fp32 and
 // R = sum_j P_ij k_j, one more product; dQ = scale (dQ' - (D - D') R) is then free of the error that o's and P's
 // rounding put into D', and D goes to the dk, dv kernel.
-template <int D>
-struct DqLayout : BwdTmem<D> {
+template <int D, int DP_SMEM>
+struct DqLayout : BwdTmem<D, DP_SMEM> {
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kRes = 128u * D * 2, kTile = 64u * D * 2;
   static constexpr uint32_t kQ = 0, kDO = kRes, kK = 2 * kRes, kV = kK + kStages * kTile;
@@ -388,52 +339,46 @@ struct DqLayout : BwdTmem<D> {
   static constexpr uint32_t kUsed = kBar + kBarBytes;
   static constexpr uint32_t kSmem = kUsed > 118784u ? kUsed : 118784u;  // one CTA an SM
 };
-static_assert(DqLayout<128>::kSmem <= 232448, "227 KB a CTA");
+static_assert(DqLayout<128, 1>::kSmem <= 232448, "227 KB a CTA");
 
-// Key tiles of an item, whose entry holds `TT` query tokens (with two CTAs those of both: they go
-// through the same tiles, and what only one of them sees is masked in the other).
+// Key tiles of an item.
 __device__ __forceinline__ int dq_tiles(const PackedItem& it, int TT, bool causal) {
   return (packed_keys(min((it.e.tile + 1) * TT, it.e.n) - 1, it.e.n, it.e.m, causal) + 63) >> 6;
 }
 
-template <int D, bool CAUSAL, int CL>
+template <int D, bool CAUSAL, int DP_SMEM>
 __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __grid_constant__ BwdParams p) {
-  using L = DqLayout<D>;
+  using L = DqLayout<D, DP_SMEM>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
-  if (!bwd_init<CL>(bars, warp, smem, smem, 0, 1, kDqMma, L::kBothStay ? 0 : 1)) return;
+  if (!bwd_init(bars, warp, smem, smem, 0, 1, kDqMma, L::kBothStay ? 0 : 1)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
   grid_dependency_launch();
 
   if (warp == kTmaWarp) {
-    // Of two CTAs the first takes the items and loads keys for both, the second values.
     const uint32_t q_bytes = static_cast<uint32_t>(p.P * p.TT64) * 128u * L::kChunks;
     int kvb = 0, tl = 0;  // key tiles and items with loads so far
     auto claim = [&]() {
       PackedItem x;
       x.head = -1;
-      if (rank == 0 && lane == 0) x = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
+      if (lane == 0) x = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
       return x;
     };
     PackedItem it = claim();
     for (int t = 0;; ++t) {
       const int r = t % kBwdRing;
-      if (rank == 0) {
-        if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
-        if (lane == 0) item_publish<CL>(bars, r, it);
-        __syncwarp();
-        it = bars->item[r];
-        __syncwarp();
-      } else {
-        if (!item_wait<CL>(bars, t, 0x105)) break;
-        it = bars->item[r];
-        item_done<CL>(bars, r);
+      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
+      if (lane == 0) {
+        bars->item[r] = it;
+        mbar_arrive(&bars->item_full[r]);
       }
+      __syncwarp();
+      it = bars->item[r];
+      __syncwarp();
       if (it.head < 0) break;
-      const int n = dq_tiles(it, CL * p.TT, CAUSAL);
+      const int n = dq_tiles(it, p.TT, CAUSAL);
       if (n == 0) {
         it = claim();
         continue;
@@ -449,31 +394,26 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         mbar_arrive_expect_tx(&bars->res_full, 4 * q_bytes);
 #pragma unroll
         for (int c = 0; c < 2 * L::kChunks; ++c) {  // two boxes of 64 rows a column
-          const int col = c >> 1, half = c & 1, tok = (it.e.tile * CL + rank) * p.TT + half * p.TT64;
+          const int col = c >> 1, half = c & 1, tok = it.e.tile * p.TT + half * p.TT64;
           const uint32_t at = col * 16384 + half * 8192;
           tma_load_4d(smem + L::kQ + at, maps, &bars->res_full, col * 64, 0, tok, it.head);
           tma_load_4d(smem + L::kDO + at, maps + 3, &bars->res_full, col * 64, 0, tok, it.head);
         }
         auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int j) {
 #pragma unroll
-          for (int c = 0; c < L::kChunks; ++c) {
-            if constexpr (CL == 2)
-              tma_load_3d_all(dst + c * 8192, map, bar, c * 64, j * 64, kh, 3);
-            else
-              tma_load_3d(dst + c * 8192, map, bar, c * 64, j * 64, kh);
-          }
+          for (int c = 0; c < L::kChunks; ++c) tma_load_3d(dst + c * 8192, map, bar, c * 64, j * 64, kh);
         };
         for (int j = 0; j < n; ++j) {
           const int s = (kvb + j) % kStages;
           const uint32_t par = (((kvb + j) / kStages) & 1) ^ 1;
           if (!(ok = wait(&bars->x_empty[s], par, bars, 0x101))) break;
           mbar_arrive_expect_tx(&bars->x_full[s], L::kTile);
-          if (CL == 1 || rank == 0) load(smem + L::kK + s * L::kTile, maps + 1, &bars->x_full[s], j);
+          load(smem + L::kK + s * L::kTile, maps + 1, &bars->x_full[s], j);
           if (!(ok = wait(&bars->y_empty[s], par, bars, 0x102))) break;
           mbar_arrive_expect_tx(&bars->y_full[s], L::kTile);
-          if (CL == 1 || rank == 1) load(smem + L::kV + s * L::kTile, maps + 2, &bars->y_full[s], j);
+          load(smem + L::kV + s * L::kTile, maps + 2, &bars->y_full[s], j);
           // the next item is asked for while the last tiles are under way
-          if (rank == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
+          if (j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
         }
       }
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -481,9 +421,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       ++tl;
       it = next;
     }
-    __syncwarp();
-    if (!bars->abort_flag && stages_free<CL>(bars, bars->x_empty, kvb, 0x106))
-      stages_free<CL>(bars, bars->y_empty, kvb, 0x107);
     __syncwarp();
   } else if (warp >= kMmaWarp) {
     // Three warps issue, S, dP, and P K and dS K: 8 products take 210 cycles to issue in a kernel that does
@@ -498,21 +435,21 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
     [[maybe_unused]] const uint32_t sdO = uniform(smem_u32(smem + L::kDO));
     int kvb = 0, tl = 0;
     for (int t = 0;; ++t) {
-      if (!item_wait<CL>(bars, t, 0x21b)) break;
+      if (!item_wait(bars, t, 0x21b)) break;
       const PackedItem it = bars->item[t % kBwdRing];
-      item_done<CL>(bars, t % kBwdRing);
+      item_done(bars, t % kBwdRing);
       if (uniform(it.head) < 0) break;
-      const int n = uniform(dq_tiles(it, CL * p.TT, CAUSAL));
+      const int n = uniform(dq_tiles(it, p.TT, CAUSAL));
       if (n == 0) continue;
       if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x210)) break;
       bool ok = true;
       if (role == 0) {
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int pos = kvb + j, s = pos % kStages;
+          const int pos = kvb + j, s = pos % kStages, before = pos - L::kSBufs;
           // (the P and dS in the buffer have been multiplied)
           if (!(ok = warp_wait(&bars->x_full[s], (pos / kStages) & 1, bars, 0x211) &&
-                     (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x212))))
+                     (before < 0 || warp_wait(&bars->done[L::s_buf(before)], L::s_par(before), bars, 0x212))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -520,7 +457,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
             for (int kk = 0; kk < D / 16; ++kk)
               umma_ts(tm + L::s_col(pos), tm + L::kStay0 + kk * 8, kmajor_desc(sK + s * L::kTile, kk), idesc_s,
                       kk > 0 ? 1u : 0u);
-            umma_commit(&bars->s_full[pos & 1]);
+            umma_commit(&bars->s_full[L::s_buf(pos)]);
           }
           __syncwarp();
         }
@@ -544,7 +481,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
                         kmajor_desc(sV + s * L::kTile, kk), idesc_s, kk > 0 ? 1u : 0u);
             }
             umma_commit(&bars->dp_full[L::dp_buf(pos)]);
-            commit_stage<CL>(&bars->y_empty[s]);
+            umma_commit(&bars->y_empty[s]);
             if (!L::kBothStay && j + 1 == n) umma_commit(&bars->res_empty);
           }
           __syncwarp();
@@ -562,17 +499,17 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
           const int pos = kvb + j, s = pos % kStages;
           // an item's first overwrite the accumulators that the epilogue before it reads
           if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216)) &&
-                     warp_wait(&bars->s_done[pos & 1], (pos >> 1) & 1, bars, 0x217)))
+                     warp_wait(&bars->s_done[L::s_buf(pos)], L::s_par(pos), bars, 0x217)))
             break;
           tc_fence_after_sync();
           if (elect_one()) issue_acc(tm + L::kAcc0, tm + L::s_col(pos), s, j == 0);
           __syncwarp();
-          if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x214))) break;
+          if (!(ok = warp_wait(&bars->ds_ready[L::s_buf(pos)], L::s_par(pos), bars, 0x214))) break;
           tc_fence_after_sync();
           if (elect_one()) {
             issue_acc(tm + L::kAcc1, tm + L::s_col(pos) + 16, s, j == 0);
-            umma_commit(&bars->done[pos & 1]);
-            commit_stage<CL>(&bars->x_empty[s]);
+            umma_commit(&bars->done[L::s_buf(pos)]);
+            umma_commit(&bars->x_empty[s]);
             if (j + 1 == n) umma_commit(&bars->acc_done);
           }
           __syncwarp();
@@ -625,15 +562,15 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       return true;
     };
     for (int ti = 0;; ++ti) {
-      if (!item_wait<CL>(bars, ti, 0x304)) break;
+      if (!item_wait(bars, ti, 0x304)) break;
       const PackedItem it = bars->item[ti % kBwdRing];
-      item_done<CL>(bars, ti % kBwdRing);
+      item_done(bars, ti % kBwdRing);
       if (it.head < 0) {
         epilogue();
         break;
       }
-      const int n = dq_tiles(it, CL * p.TT, CAUSAL);
-      const int tok0 = (it.e.tile * CL + rank) * p.TT, tok = tok0 + row_tok;
+      const int n = dq_tiles(it, p.TT, CAUSAL);
+      const int tok0 = it.e.tile * p.TT, tok = tok0 + row_tok;
       const bool valid = row_in && tok < it.e.n;
       const int head = it.head * p.P + row_head, m = it.e.m, off = m - it.e.n;
       const long long token = it.e.q0 + tok;
@@ -700,7 +637,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       float2 exact = make_float2(0.f, 0.f);  // sum of P dP
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
-        if (!(ok = warp_wait(&bars->s_full[step & 1], (step >> 1) & 1, bars, 0x311))) break;
+        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x311))) break;
         tc_fence_after_sync();
         uint32_t pr[32];
         tmem_ld(tm + L::s_col(step) + col0, pr);
@@ -733,7 +670,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->s_done[step & 1]);
+        mbar_arrive(&bars->s_done[L::s_buf(step)]);
         if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x314))) break;
         tc_fence_after_sync();
         uint32_t rr[32];
@@ -763,7 +700,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         tmem_st16(tm + L::s_col(step) + col0 + 16, ds);
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->ds_ready[step & 1]);
+        mbar_arrive(&bars->ds_ready[L::s_buf(step)]);
         // (at d = 128 while the products run, 1.6 % faster there; at d = 64, where the threads bound the
         // kernel, 31 full samples of up to 1500 tokens take 254 us that way, and 234 the other)
         if (D == 128 && n > 1) add_exact();
@@ -782,12 +719,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       ++tl;
     }
   }
-  bwd_teardown<CL>(bars, warp, tmem);
+  bwd_teardown(bars, warp, tmem);
 }
 
 // ============================================================ dK / dV
-template <int D>
-struct DkLayout : BwdTmem<D> {
+template <int D, int DP_SMEM>
+struct DkLayout : BwdTmem<D, DP_SMEM> {
   static constexpr int kChunks = D / 64;
   static constexpr uint32_t kRes = 128u * D * 2, kTile = 64u * D * 2;
   static constexpr uint32_t kK = 0, kV = kRes, kQ = 2 * kRes, kDO = kQ + kStages * kTile;
@@ -796,7 +733,7 @@ struct DkLayout : BwdTmem<D> {
   static constexpr uint32_t kUsed = kBar + kBarBytes;
   static constexpr uint32_t kSmem = kUsed > 118784u ? kUsed : 118784u;  // one CTA an SM
 };
-static_assert(DkLayout<128>::kSmem <= 232448, "227 KB a CTA");
+static_assert(DkLayout<128, 1>::kSmem <= 232448, "227 KB a CTA");
 
 // Query tiles (of 64 rows, TT tokens) of a head group that see the item's `keys` keys: the first, and
 // how many.
@@ -807,15 +744,14 @@ __device__ __forceinline__ int dk_tiles(const PackedItem& it, int keys, int TT, 
   return max((it.e.n + TT - 1) / TT - dk_first(it, keys, TT, causal), 0);
 }
 
-template <int D, bool CAUSAL, int CL>
+template <int D, bool CAUSAL, int DP_SMEM>
 __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __grid_constant__ BwdParams p) {
-  using L = DkLayout<D>;
+  using L = DkLayout<D, DP_SMEM>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CL == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int TT = p.TT64;
-  if (!bwd_init<CL>(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 1, kDkMma,
+  if (!bwd_init(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 1, kDkMma,
                     L::kBothStay ? 0 : 1))
     return;
   const uint32_t tmem = bars->tmem_base;
@@ -830,29 +766,25 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       row_head[e] = lane + 32 * e - row_tok[e] * p.P;
     }
     int sb = 0, tl = 0;
-    // Of two CTAs the first takes the items and loads queries for both, the second dO.
     auto claim = [&]() {
       PackedItem x;
       x.head = -1;
-      if (rank == 0 && lane == 0) x = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
+      if (lane == 0) x = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
       return x;
     };
     PackedItem it = claim();
     for (int t = 0;; ++t) {
       const int r = t % kBwdRing;
-      if (rank == 0) {
-        if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
-        if (lane == 0) item_publish<CL>(bars, r, it);
-        __syncwarp();
-        it = bars->item[r];
-        __syncwarp();
-      } else {
-        if (!item_wait<CL>(bars, t, 0x105)) break;
-        it = bars->item[r];
-        item_done<CL>(bars, r);
+      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
+      if (lane == 0) {
+        bars->item[r] = it;
+        mbar_arrive(&bars->item_full[r]);
       }
+      __syncwarp();
+      it = bars->item[r];
+      __syncwarp();
       if (it.head < 0) break;
-      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL);
+      const int first = dk_first(it, 128, TT, CAUSAL), per = dk_tiles(it, 128, TT, CAUSAL);
       const int n = per * p.per_kv;
       if (n == 0) {
         it = claim();
@@ -866,7 +798,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         mbar_arrive_expect_tx(&bars->res_full, 2 * L::kRes);
 #pragma unroll
         for (int c = 0; c < 2 * L::kChunks; ++c) {  // two boxes of 64 keys a column
-          const int col = c >> 1, half = c & 1, key = (it.e.tile * CL + rank) * 128 + half * 64;
+          const int col = c >> 1, half = c & 1, key = it.e.tile * 128 + half * 64;
           tma_load_3d(smem + L::kK + col * 16384 + half * 8192, maps + 1, &bars->res_full, col * 64, key, it.head);
           tma_load_3d(smem + L::kV + col * 16384 + half * 8192, maps + 2, &bars->res_full, col * 64, key, it.head);
         }
@@ -900,13 +832,8 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
           for (int c = 0; c < L::kChunks; ++c) {
             uint8_t* q = smem + L::kQ + s * L::kTile + c * 8192;
             uint8_t* o = smem + L::kDO + s * L::kTile + c * 8192;
-            if constexpr (CL == 1) {
-              tma_load_4d(q, maps, &bars->x_full[s], c * 64, 0, tile * TT, group);
-              tma_load_4d(o, maps + 3, &bars->x_full[s], c * 64, 0, tile * TT, group);
-            } else {
-              tma_load_4d_all(rank == 0 ? q : o, rank == 0 ? maps : maps + 3, &bars->x_full[s], c * 64, 0, tile * TT,
-                              group, 3);
-            }
+            tma_load_4d(q, maps, &bars->x_full[s], c * 64, 0, tile * TT, group);
+            tma_load_4d(o, maps + 3, &bars->x_full[s], c * 64, 0, tile * TT, group);
           }
         }
         float* vec = reinterpret_cast<float*>(smem + L::kVec) + s * 128;
@@ -923,15 +850,13 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
           ++sub;
         }
         if (j + 1 < n) ask(tile, sub);
-        if (rank == 0 && lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
+        if (lane == 0 && j == max(n - 2, 0)) next = packed_claim(p.header, p.list, 1, p.Hkv, p.chunk);
       }
       if (!ok) break;
       sb += n;
       ++tl;
       it = next;
     }
-    __syncwarp();
-    if (!bars->abort_flag) stages_free<CL>(bars, bars->x_empty, sb, 0x106);
     __syncwarp();
   } else if (warp >= kMmaWarp) {
     // Three warps issue (as in the dq kernel): S^T = K Q^T; dP^T = V dO^T; dV += P^T dO and dK += dS^T Q.
@@ -964,21 +889,21 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
     };
     int sb = 0, tl = 0;
     for (int t = 0;; ++t) {
-      if (!item_wait<CL>(bars, t, 0x207)) break;
+      if (!item_wait(bars, t, 0x207)) break;
       const PackedItem it = bars->item[t % kBwdRing];
-      item_done<CL>(bars, t % kBwdRing);
+      item_done(bars, t % kBwdRing);
       if (uniform(it.head) < 0) break;
-      const int n = uniform(dk_tiles(it, CL * 128, TT, CAUSAL)) * p.per_kv;
+      const int n = uniform(dk_tiles(it, 128, TT, CAUSAL)) * p.per_kv;
       if (n == 0) continue;
       if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x201)) break;
       bool ok = true;
       if (role == 0) {
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int pos = sb + j;
+          const int pos = sb + j, before = pos - L::kSBufs;
           // (the P and dS in the buffer have been multiplied)
           if (!(ok = stage_in(pos) &&
-                     (pos < 2 || warp_wait(&bars->done[pos & 1], ((pos >> 1) - 1) & 1, bars, 0x202))))
+                     (before < 0 || warp_wait(&bars->done[L::s_buf(before)], L::s_par(before), bars, 0x202))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -986,7 +911,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               umma_ts(tm + L::s_col(pos), tm + L::kStay0 + kk * 8, kmajor_desc(q, kk), idesc_s, kk > 0 ? 1u : 0u);
-            umma_commit(&bars->s_full[pos & 1]);
+            umma_commit(&bars->s_full[L::s_buf(pos)]);
           }
           __syncwarp();
         }
@@ -1009,17 +934,17 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
           const uint32_t stage = pos % kStages * L::kTile;
           // an item's first overwrites the accumulators that the epilogue before it reads
           if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206)) &&
-                     warp_wait(&bars->s_done[pos & 1], (pos >> 1) & 1, bars, 0x203)))
+                     warp_wait(&bars->s_done[L::s_buf(pos)], L::s_par(pos), bars, 0x203)))
             break;
           tc_fence_after_sync();
           if (elect_one()) issue_acc(tm + L::kAcc0, tm + L::s_col(pos), sdO + stage, j == 0);
           __syncwarp();
-          if (!(ok = warp_wait(&bars->ds_ready[pos & 1], (pos >> 1) & 1, bars, 0x204))) break;
+          if (!(ok = warp_wait(&bars->ds_ready[L::s_buf(pos)], L::s_par(pos), bars, 0x204))) break;
           tc_fence_after_sync();
           if (elect_one()) {
             issue_acc(tm + L::kAcc1, tm + L::s_col(pos) + 16, sQ + stage, j == 0);
-            umma_commit(&bars->done[pos & 1]);
-            commit_stage<CL>(&bars->x_empty[pos % kStages]);
+            umma_commit(&bars->done[L::s_buf(pos)]);
+            umma_commit(&bars->x_empty[pos % kStages]);
             if (j + 1 == n) umma_commit(&bars->acc_done);
           }
           __syncwarp();
@@ -1058,16 +983,16 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       return true;
     };
     for (int ti = 0;; ++ti) {
-      if (!item_wait<CL>(bars, ti, 0x305)) break;
+      if (!item_wait(bars, ti, 0x305)) break;
       const PackedItem it = bars->item[ti % kBwdRing];
-      item_done<CL>(bars, ti % kBwdRing);
+      item_done(bars, ti % kBwdRing);
       if (it.head < 0) {
         epilogue();
         break;
       }
-      const int first = dk_first(it, CL * 128, TT, CAUSAL), per = dk_tiles(it, CL * 128, TT, CAUSAL);
+      const int first = dk_first(it, 128, TT, CAUSAL), per = dk_tiles(it, 128, TT, CAUSAL);
       const int n = per * p.per_kv;
-      const int key0 = (it.e.tile * CL + rank) * 128, key = key0 + tr;
+      const int key0 = it.e.tile * 128, key = key0 + tr;
       const bool valid = key < it.e.m;
       const long long token = it.e.k0 + key;
       const long long at_k = valid ? token * p.dk_token + it.head * p.dk_head + (D / 2) * g : -1;
@@ -1105,7 +1030,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
         const float* nlse = reinterpret_cast<const float*>(smem + L::kVec) + (step % kStages) * 128;
-        if (!(ok = warp_wait(&bars->s_full[step & 1], (step >> 1) & 1, bars, 0x301))) break;
+        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x301))) break;
         tc_fence_after_sync();
         uint32_t pr[32];
         tmem_ld(tm + L::s_col(step) + col0, pr);
@@ -1144,7 +1069,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->s_done[step & 1]);
+        mbar_arrive(&bars->s_done[L::s_buf(step)]);
         if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x306))) break;
         tc_fence_after_sync();
         uint32_t rr[32], ds[16];
@@ -1170,7 +1095,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         tmem_st16(tm + L::s_col(step) + col0 + 16, ds);
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&bars->ds_ready[step & 1]);
+        mbar_arrive(&bars->ds_ready[L::s_buf(step)]);
         if (++tile == first + per) tile = first;
       }
       if (!ok) break;
@@ -1181,30 +1106,32 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       ++tl;
     }
   }
-  bwd_teardown<CL>(bars, warp, tmem);
+  bwd_teardown(bars, warp, tmem);
 }
 
 // Items of a launch as CTAs, at most one an SM.
-unsigned grid_of(long long items, int cluster, int sms) {
-  return static_cast<unsigned>(std::min<long long>(items, sms / cluster)) * cluster;
-}
+unsigned grid_of(long long items, int sms) { return static_cast<unsigned>(std::min<long long>(items, sms)); }
 
-template <int D, bool CAUSAL, int CL>
+template <int D, bool CAUSAL, int DP_SMEM>
 cudaError_t launch_dq(const BwdParams& p, long long items, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_dq_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDqThreads,
-                       DqLayout<D>::kSmem, CL, ready, s);
+  return launch_behind(fa_packed_dq_kernel<D, CAUSAL, DP_SMEM>, p, grid_of(items, sms), kDqThreads,
+                       DqLayout<D, DP_SMEM>::kSmem, ready, s);
 }
-template <int D, bool CAUSAL, int CL>
+template <int D, bool CAUSAL, int DP_SMEM>
 cudaError_t launch_dkdv(const BwdParams& p, long long items, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> ready;
-  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL, CL>, p, grid_of(items, CL, sms), kDkThreads,
-                       DkLayout<D>::kSmem, CL, ready, s);
+  return launch_behind(fa_packed_dkdv_kernel<D, CAUSAL, DP_SMEM>, p, grid_of(items, sms), kDkThreads,
+                       DkLayout<D, DP_SMEM>::kSmem, ready, s);
 }
 
-// Tiles of a sequence, on average, from which two CTAs share what they stream (d = 128): the odd
-// tile at the end of a sequence leaves one of them idle.
-constexpr int kShareTiles = 8;
+// DP_SMEM at d = 128, by the steps that an item has on average.  Where they are few, it counts for more that
+// shared memory is free at once for the next item's tensors (1), which then arrive while this one's products
+// run, than a second buffer of scores (2).  Measured: 400 samples of 64 tokens, 32 heads on 8, one step an item of
+// dq, 156 us with 1 and 175 with 2; 300 of 65 to 100 tokens, 16 on 16, 173 and 166; two of 8192, 1960 and 1330.
+// dk and dv: 100 samples of 256 tokens, 16 on 16, four steps at most, 136 and 148; 300 of 65 to 100, 32 on 8, up
+// to seven, 147 and 140; two of 8192, 2042 and 1298.
+constexpr int kShortDq = 1, kShortDk = 4;
 
 }  // namespace
 
@@ -1212,12 +1139,9 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   const int Hq = a.q.heads, Hkv = a.k.heads;
   const PackedTiling t = packed_tiling(Hq, Hkv);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, Hq, Hkv, true);
-  // CTAs that share a stream: dq, and dk and dv
-  auto share = [&](long long tokens, int tile) {
-    return a.d == 128 && tokens >= 1ll * kShareTiles * tile * a.B ? 2 : 1;
-  };
-  const int cq = share(a.total_q, 2 * t.TT64), ck = share(a.total_k, 128);
-  cudaError_t e = launch_packed_plan(a, maps, 4, true, cq, ck, s);
+  const bool dq_short = a.total_k <= 64ll * kShortDq * a.B;
+  const bool dk_short = 1ll * a.total_q * t.per_kv <= 1ll * t.TT64 * kShortDk * a.B;
+  cudaError_t e = launch_packed_plan(a, maps, 4, true, s);
   if (e != cudaSuccess) return e;
   char* ws = static_cast<char*>(a.workspace);
   auto out = [](const HeadsView& v) { return static_cast<__nv_bfloat16*>(const_cast<void*>(v.p)); };
@@ -1242,21 +1166,21 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   // the dq kernel streams keys and values, the other the queries and dO of a group's heads
   p.list = reinterpret_cast<const PackedEntry*>(ws + l.list[0]);
-  const long long qi = a.total_q > 0 ? (a.total_q / (1ll * cq * p.TT) + a.B) * t.heads : 0;
-  p.chunk = packed_chunk(a.total_k, a.d, Hkv, qi, a.num_sms / cq) * t.per_kv;
+  const long long qi = a.total_q > 0 ? (a.total_q / p.TT + static_cast<long long>(a.B)) * t.heads : 0;
+  p.chunk = packed_chunk(a.total_k, a.d, Hkv, qi, a.num_sms) * t.per_kv;
   if (a.d == 64)
     e = a.causal ? launch_dq<64, true, 1>(p, qi, a.num_sms, s) : launch_dq<64, false, 1>(p, qi, a.num_sms, s);
-  else if (cq == 1)
+  else if (dq_short)
     e = a.causal ? launch_dq<128, true, 1>(p, qi, a.num_sms, s) : launch_dq<128, false, 1>(p, qi, a.num_sms, s);
   else
     e = a.causal ? launch_dq<128, true, 2>(p, qi, a.num_sms, s) : launch_dq<128, false, 2>(p, qi, a.num_sms, s);
   if (e != cudaSuccess) return e;
   p.list = reinterpret_cast<const PackedEntry*>(ws + l.list[1]);
-  const long long ki = a.total_k > 0 ? (a.total_k / (128ll * ck) + a.B) * Hkv : 0;
-  p.chunk = packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv, ki, a.num_sms / ck);
+  const long long ki = a.total_k > 0 ? (a.total_k / 128ll + a.B) * Hkv : 0;
+  p.chunk = packed_chunk(static_cast<long long>(a.total_q) * (Hq / Hkv), a.d, Hkv, ki, a.num_sms);
   if (a.d == 64)
     return a.causal ? launch_dkdv<64, true, 1>(p, ki, a.num_sms, s) : launch_dkdv<64, false, 1>(p, ki, a.num_sms, s);
-  if (ck == 1)
+  if (dk_short)
     return a.causal ? launch_dkdv<128, true, 1>(p, ki, a.num_sms, s) : launch_dkdv<128, false, 1>(p, ki, a.num_sms, s);
   return a.causal ? launch_dkdv<128, true, 2>(p, ki, a.num_sms, s) : launch_dkdv<128, false, 2>(p, ki, a.num_sms, s);
 }

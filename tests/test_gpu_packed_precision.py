@@ -79,3 +79,30 @@ def test_gradients_are_as_exact_as_their_roundings(fa, kind, lens, Hq, Hkv, d, c
         print(name, kind, "error %.2f of its roundings', %.4f of its norm" % (err / room, err / want[name].norm()))
         # 1.2: the spread of a sum over some thousand rows of few keys, and the fp32 steps
         assert err <= 1.2 * room, name
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (3, 1), (7, 1)])
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("causal", (True, False))
+def test_a_sequence_has_the_same_bits_whatever_else_is_in_the_batch(fa, d, Hq, Hkv, causal):
+    """Alone, among shorter sequences and beside a long one: the same results, to the bit."""
+    lens = [130, 64, 21]
+    alone = {}
+    for others in ([], [9] * 40, [2300], [700] * 3):
+        cu = ref.starts(lens + others)
+        q, k, v, dO = inputs("sharp", cu[-1], Hq, Hkv, d)
+        n = sum(lens)
+        if not alone:
+            first = [t.clone() for t in (q, k, v, dO)]
+        for t, x in zip((q, k, v, dO), first):
+            t[:n] = x
+        g = [t.cuda() for t in (q, k, v, dO)]
+        starts = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        o, lse = fa.fa_forward_packed(*g[:3], starts, causal=causal)
+        dq, dk, dv = fa.fa_backward_packed(*g[:3], o, g[3], lse, starts, causal=causal)
+        torch.cuda.synchronize()
+        assert fa.fa_get_device_error() == (0, 0)
+        got = dict(o=o[:n], lse=lse[:, :n], dq=dq[:n], dk=dk[:n], dv=dv[:n])
+        alone = alone or got
+        for name in got:
+            assert torch.equal(got[name], alone[name]), (name, len(others))
