@@ -630,8 +630,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         join(part);
         if (!ok) break;
       }
-      // a row without keys of its own, or behind the sequence: P = 2^-inf
-      const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+      // a row without keys of its own, or behind the sequence: P = 2^-inf (one that sees keys whose scores are
+      // all -inf has lse = -inf, and P = 2^(-inf + inf), NaN by the definition)
+      const float lse2 = !CAUSAL || tok + off >= 0 ? lse * kLog2e : INFINITY;
       const uint32_t col0 = 32u * g;
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
       float2 exact = make_float2(0.f, 0.f);  // sum of P dP
@@ -807,18 +808,18 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       PackedItem next = it;
       bool ok = true;
       int sub = 0, tile = first;
-      // -lse and -D of this lane's rows of a tile, asked for a tile ahead of their use; rows that do
-      // not exist, or see nothing: P = 0
-      float nl[2], nD[2];
+      // lse and D of this lane's rows of a tile, asked for a tile ahead of their use; rows that do
+      // not exist, or see nothing: P = 2^-inf
+      float lse[2], Dv[2];
       auto ask = [&](int tile, int sub) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int tok = tile * TT + row_tok[e], group = it.head * p.per_kv + sub;
-          nl[e] = -INFINITY, nD[e] = 0.0f;
-          if (row_tok[e] < TT && tok < it.e.n) {
+          lse[e] = INFINITY, Dv[e] = 0.0f;
+          if (row_tok[e] < TT && tok < it.e.n && (!CAUSAL || tok + it.e.m >= it.e.n)) {
             const long long at = static_cast<long long>(group * p.P + row_head[e]) * p.total_q + it.e.q0 + tok;
-            nl[e] = p.lse[at];
-            nD[e] = p.D[at];
+            lse[e] = p.lse[at];
+            Dv[e] = p.D[at];
           }
         }
       };
@@ -839,9 +840,8 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         float* vec = reinterpret_cast<float*>(smem + L::kVec) + s * 128;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const bool none = nl[e] == -INFINITY;
-          vec[lane + 32 * e] = none ? -INFINITY : -nl[e] * kLog2e;
-          vec[64 + lane + 32 * e] = none ? 0.0f : -nD[e];
+          vec[lane + 32 * e] = -lse[e] * kLog2e;
+          vec[64 + lane + 32 * e] = -Dv[e];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->x_full[s]);  // (the stage's one arrival)

@@ -400,7 +400,7 @@ typedef struct fa_heads {
  *    causal != 0 of those j <= i + m - n: the last query sees all keys (a prompt with
  *    m = n, a chunk of one over the keys before it with m > n).  A query that
  *    sees no key has o = 0 and lse = -inf (one that sees keys whose scores are all
- *    -inf has o = NaN).
+ *    -inf has o = NaN, and in the backward pass dq and the dk and dv of those keys are NaN).
  *  - q, o: Hq = q->heads heads, total_q tokens; k, v: Hkv heads, total_k
  *    tokens; Hq a multiple of Hkv, query head h reads key head h / (Hq / Hkv).
  *    o->heads = Hq, v->heads = Hkv.  lse: fp32 [Hq][total_q].
