@@ -239,6 +239,17 @@ __device__ __forceinline__ void load_half_row(const uint8_t* tile, int tr, int h
     w[4 * e] = x.x, w[4 * e + 1] = x.y, w[4 * e + 2] = x.z, w[4 * e + 3] = x.w;
   }
 }
+// Zeros there, for products that read the tile from shared memory.
+template <int D>
+__device__ __forceinline__ void zero_half_row(uint8_t* tile, int tr, int half) {
+#pragma unroll
+  for (int e = 0; e < D / 16; ++e) {
+    const int c = half * (D / 16) + e;
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + tr * 128 + (((c & 7) ^ (tr & 7)) << 4)) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+}
 template <int D>
 __device__ __forceinline__ void store_half_row(uint32_t addr, int half, const uint32_t (&w)[D / 4]) {
   if constexpr (D == 128)
@@ -582,10 +593,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         }
         continue;
       }
+      // (a row that sees no key counts as one of zeros, whatever its q and dO hold)
+      const bool live = valid && (!CAUSAL || tok + off >= 0);
       // asked for here, used below
-      float lse = valid ? p.lse[vec] : INFINITY;
+      float lse = live ? p.lse[vec] : INFINITY;
       uint4 o_row[D / 16];
-      if (n > 1 && valid) {
+      if (n > 1 && live) {
         const uint4* a = reinterpret_cast<const uint4*>(p.o + token * p.o_token + head * p.o_head + (D / 2) * g);
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) o_row[e] = a[e];
@@ -605,15 +618,18 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       float part = 0.0f;
       {
         uint32_t w[D / 4];
-        load_half_row<D>(smem + L::kQ, tr, g, valid, w);
+        load_half_row<D>(smem + L::kQ, tr, g, live, w);
         store_half_row<D>(tm + L::kStay0, g, w);
-        load_half_row<D>(smem + L::kDO, tr, g, valid, w);
-        if constexpr (L::kBothStay) store_half_row<D>(tm + L::stay1_col(), g, w);
+        load_half_row<D>(smem + L::kDO, tr, g, live, w);
+        if constexpr (L::kBothStay)
+          store_half_row<D>(tm + L::stay1_col(), g, w);
+        else if (valid && !live)
+          zero_half_row<D>(smem + L::kDO, tr, g);
         mbar_arrive(&bars->res_empty);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&bars->a_ready);
-        if (n > 1 && valid) {
+        if (n > 1 && live) {
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
             const uint32_t xs[4] = {o_row[e].x, o_row[e].y, o_row[e].z, o_row[e].w};
@@ -632,7 +648,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       }
       // a row without keys of its own, or behind the sequence: P = 2^-inf (one that sees keys whose scores are
       // all -inf has lse = -inf, and P = 2^(-inf + inf), NaN by the definition)
-      const float lse2 = !CAUSAL || tok + off >= 0 ? lse * kLog2e : INFINITY;
+      const float lse2 = lse * kLog2e;
       const uint32_t col0 = 32u * g;
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
       float2 exact = make_float2(0.f, 0.f);  // sum of P dP

@@ -46,3 +46,16 @@ def test_gradients_of_a_row_whose_scores_are_all_minus_infinity(fa, d, lens_q, l
     if causal and lens_k[0] < lens_q[0]:  # the first queries see nothing
         none = lens_q[0] - lens_k[0]
         assert (got["dq"][:none] == 0).all() and torch.isneginf(got["lse"][:, :none]).all()
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([150], [140]), ([90, 200], [30, 170])], ids=str)
+@pytest.mark.parametrize("d", (64, 128))
+def test_a_query_that_sees_no_key_has_no_gradient_whatever_it_holds(fa, d, lens_q, lens_k):  # noqa: F811
+    cu_q, cu_k = ref.starts(lens_q), ref.starts(lens_k)
+    q, k, v, dO = (rnd(80 + i, n, h, d).cuda() for i, (n, h) in
+                   enumerate(((cu_q[-1], 4), (cu_k[-1], 2), (cu_k[-1], 2), (cu_q[-1], 4))))
+    want = both(fa, (q, k, v, dO), cu_q, cu_k, True)
+    q[cu_q[-2] + 2], dO[cu_q[-2] + 3], dO[cu_q[-2] + 4] = math.nan, math.inf, math.nan
+    got = both(fa, (q, k, v, dO), cu_q, cu_k, True)
+    for x in ("o", "lse", "dq"):
+        assert torch.equal(got[x], want[x]), x
