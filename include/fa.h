@@ -406,9 +406,10 @@ typedef struct fa_heads {
  *    o->heads = Hq, v->heads = Hkv.  lse: fp32 [Hq][total_q].
  *  - What one sequence holds, NaN and infinities included, reaches no other.
  *    Tokens of o and lse in no sequence (before cu_q[0], from cu_q[B] on) are
- *    left as they were.  Within a sequence a NaN or infinity in a value row may
- *    make queries NaN that do not see the row (and, in the backward pass, one in a row of
- *    q or dO the gradients of keys that it does not see).  Outputs overlap no input.
+ *    left as they were.  Within a sequence, and for a key head and its query
+ *    heads, a NaN or infinity reaches what sees it, and may reach: from a value row the o and dq, from a
+ *    key row the dq (o and lse not) of queries that do not see the row; from a row of q or dO the
+ *    dk and dv of keys that it does not see.  Outputs overlap no input.
  *  - B >= 1, 0 <= total_q, total_k; d in {64, 128}; Hq * (total_q / 8 + B) and
  *    Hkv * (total_k / 128 + B) below 2^31, B below 2^20.  scale > 0 and finite.
  *  - workspace: device memory, 256-byte aligned, contents irrelevant, of

@@ -59,3 +59,38 @@ def test_a_query_that_sees_no_key_has_no_gradient_whatever_it_holds(fa, d, lens_
     got = both(fa, (q, k, v, dO), cu_q, cu_k, True)
     for x in ("o", "lse", "dq"):
         assert torch.equal(got[x], want[x]), x
+
+
+@pytest.mark.parametrize("bad", (math.nan, math.inf))
+@pytest.mark.parametrize("which", ("q", "k", "v", "dO"))
+@pytest.mark.parametrize("d", (64, 128))
+def test_how_far_a_row_that_is_not_finite_reaches(fa, d, which, bad):  # noqa: F811
+    """Other sequences and other key heads' groups never change; of its own, only what the row can reach."""
+    lens, at = [70, 300, 45], 170  # a token of the second sequence
+    cu = ref.starts(lens)
+    t = dict(q=rnd(90, cu[-1], 4, d), k=rnd(91, cu[-1], 2, d), v=rnd(92, cu[-1], 2, d), dO=rnd(93, cu[-1], 4, d))
+    t = {x: y.cuda() for x, y in t.items()}
+    want = both(fa, list(t.values()), cu, cu, True)
+    t[which][cu[1] + at, 0] = bad
+    got = both(fa, list(t.values()), cu, cu, True)
+    own = slice(cu[1], cu[2])
+    keep = {x: torch.ones(y.shape[:2] if x != "lse" else y.T.shape, dtype=torch.bool, device="cuda") for x, y in got.items()}
+    heads = dict(o=slice(0, 2), lse=slice(0, 2), dq=slice(0, 2), dk=slice(0, 1), dv=slice(0, 1))
+    if which in ("q", "dO"):  # a row of query head 0: of o, lse and dq its own alone
+        for x in ("o", "lse", "dq") if which == "q" else ("dq",):
+            keep[x][cu[1] + at, 0] = False
+        keep["dk"][own, 0] = keep["dv"][own, 0] = False
+    elif which == "k":  # o and lse of the queries that see it
+        for x in ("o", "lse"):
+            keep[x][cu[1] + at: cu[2], heads[x]] = False
+        for x in ("dq", "dk", "dv"):
+            keep[x][own, heads[x]] = False
+    else:  # neither lse nor dv depends on the values
+        for x in ("o", "dq", "dk"):
+            keep[x][own, heads[x]] = False
+    for x in got:
+        a, b = (y.T if x == "lse" else y for y in (got[x], want[x]))
+        assert torch.equal(a[keep[x]], b[keep[x]]), x
+    # and the row's own result says so
+    mine = dict(q="dq", k="dk", v="dk", dO="dq")[which]
+    assert not torch.isfinite(got[mine][cu[1] + at, 0]).all()
