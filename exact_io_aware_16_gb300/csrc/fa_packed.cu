@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       PackedItem it = packed_claim(p.header, p.list, 0, p.heads, p.chunk);
       for (int t = 0;; ++t) {
         const int r = t % kPackedRing;
-        if (!wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, 0x104)) break;
+        if (!wait(&bars->item_empty[r], ((t / kPackedRing) & 1) ^ 1, 0x1104)) break;
         bars->item[r] = it;
         mbar_arrive(&bars->item_full[r]);
         if (it.head < 0) break;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         auto load_q = [&](int g) {
           if ((g ? n1 : n0) == 0) return true;
           const int slot = qc % L::kQTiles;
-          if (!wait(&bars->q_empty[slot], ((qc / L::kQTiles) & 1) ^ 1, 0x103)) return false;
+          if (!wait(&bars->q_empty[slot], ((qc / L::kQTiles) & 1) ^ 1, 0x1103)) return false;
           uint64_t* full = &bars->q_full[g][qt[g]++ & 3];
           mbar_arrive_expect_tx(full, q_bytes);
 #pragma unroll
@@ -356,14 +356,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         for (int j = 0; ok && j < nmax; ++j) {
           const int s = ring_slot<D>(kvb + j);
           const uint32_t ph = ring_phase<D>(kvb + j);
-          if (!(ok = wait(&bars->k_empty[s], ph ^ 1, 0x101))) break;
+          if (!(ok = wait(&bars->k_empty[s], ph ^ 1, 0x1101))) break;
           mbar_arrive_expect_tx(&bars->k_full[s], L::kTileBytes);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c)
             tma_load_3d(smem + L::kK + s * L::kTileBytes + c * 16384, maps + 1, &bars->k_full[s], c * 64,
                         j * 128, kh);
           if (j == 0 && !(ok = load_q(1))) break;
-          if (!(ok = wait(&bars->v_empty[s], ph ^ 1, 0x102))) break;
+          if (!(ok = wait(&bars->v_empty[s], ph ^ 1, 0x1102))) break;
           mbar_arrive_expect_tx(&bars->v_full[s], L::kTileBytes);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c)
@@ -419,11 +419,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     int kvb = 0, qc = 0, qt = 0, base = 0, used = 0, turns = 0;
     auto turn = [&]() {  // (the first tile's warp goes first)
       const uint32_t par = static_cast<uint32_t>(turns++ & 1) ^ (g == 0 ? 1u : 0u);
-      return wait(&bars->turn[g], par, 0x20c);
+      return wait(&bars->turn[g], par, 0x120c);
     };
     for (int t = 0;; ++t) {
       const int r = t % kPackedRing;
-      if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, 0x20b)) break;
+      if (!wait(&bars->item_full[r], (t / kPackedRing) & 1, 0x120b)) break;
       const PackedItem it = bars->item[r];
       __syncwarp();
       if (elect_one()) mbar_arrive(&bars->item_empty[r]);
@@ -433,8 +433,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       if (nmax == 0) continue;
       const int slot = (qc + (g == 1 && n0 > 0 ? 1 : 0)) % L::kQTiles;
       qbase = sQ + slot * L::kTileBytes;
-      if ((n > 0 && !wait(&bars->q_full[g][qt & 3], (qt >> 2) & 1, 0x201)) ||
-          !wait(&bars->k_full[ring_slot<D>(kvb)], ring_phase<D>(kvb), 0x202) || !turn())
+      if ((n > 0 && !wait(&bars->q_full[g][qt & 3], (qt >> 2) & 1, 0x1201)) ||
+          !wait(&bars->k_full[ring_slot<D>(kvb)], ring_phase<D>(kvb), 0x1202) || !turn())
         break;
       tc_fence_after_sync();
       if (elect_one()) {
@@ -451,13 +451,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       // sequences of up to 1500 tokens, 16 heads on 2, full, with two key and value tiles under way: 125
       // us, and 131 the other way round; with four 118); at d = 128, where the products take
       // longer than the waits, that other way is 1 to 2 % faster.
-      auto p_wait = [&](int j) { return j >= n || wait(&bars->p_ready[g], (base + j) & 1, 0x203); };
+      auto p_wait = [&](int j) { return j >= n || wait(&bars->p_ready[g], (base + j) & 1, 0x1203); };
 #pragma unroll 1
       for (int j = 0; j < nmax; ++j) {
         const int pos = kvb + j, s = ring_slot<D>(pos), sn = ring_slot<D>(pos + 1);
-        ok = wait(&bars->v_full[s], ring_phase<D>(pos), 0x204) &&
-             (j > 0 || n == 0 || used == 0 || wait(&bars->o_free[g], (used - 1) & 1, 0x209)) &&
-             (j + 1 >= nmax || wait(&bars->k_full[sn], ring_phase<D>(pos + 1), 0x205)) &&
+        ok = wait(&bars->v_full[s], ring_phase<D>(pos), 0x1204) &&
+             (j > 0 || n == 0 || used == 0 || wait(&bars->o_free[g], (used - 1) & 1, 0x1209)) &&
+             (j + 1 >= nmax || wait(&bars->k_full[sn], ring_phase<D>(pos + 1), 0x1205)) &&
              (D == 64 ? turn() && p_wait(j) : p_wait(j) && turn());
         if (!ok) break;
         tc_fence_after_sync();
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
     int tb = 0, used = 0;  // key tiles of earlier items, and items with any
     for (int ti = 0;; ++ti) {
       const int r = ti % kPackedRing;
-      if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, 0x304)) break;
+      if (!warp_wait(&bars->item_full[r], (ti / kPackedRing) & 1, 0x1304)) break;
       // (what only the end of the item wants is read again there: with it the loop over key tiles
       // spills, and 24 prompts of up to 2048 tokens take 259 us, not 250)
       int nkv, tok0, m, off;
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
       float l_run = 0.0f;
       bool ok = true;
       for (int j = 0; j < nkv; ++j) {
-        if (!(ok = warp_wait(&bars->s_full[g], (tb + j) & 1, 0x301))) break;
+        if (!(ok = warp_wait(&bars->s_full[g], (tb + j) & 1, 0x1301))) break;
         tc_fence_after_sync();
         uint32_t sr[128];
         const int kv0 = j * 128;
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
         continue;
       }
       tb += nkv;
-      if (!warp_wait(&bars->pv_done[g], used++ & 1, 0x303)) break;
+      if (!warp_wait(&bars->pv_done[g], used++ & 1, 0x1303)) break;
       tc_fence_after_sync();
       // (a row whose keys all have a score of -inf is NaN, one that sees none is 0)
       const bool sees = !CAUSAL || tok + it.e.m >= it.e.n;
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_packed_fwd_kernel(const __g
   }
 
   // ------------------------------------------------ teardown
-  if (warp == kMmaWarp) mbar_wait(&bars->drain, 0, &bars->abort_flag, &g_packed_error, 0x20f);
+  if (warp == kMmaWarp) mbar_wait(&bars->drain, 0, &bars->abort_flag, &g_packed_error, 0x120f);
   if (bars->abort_flag) {
     // let any bulk copy already in flight land before the CTA exits
     const uint64_t t0 = globaltimer_ns();

@@ -117,12 +117,13 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 // Barriers and tensor memory; rows of [zero, zero + bytes) that no box fills are zeroed.
 // `users`: MMA warps whose products read a stage, and which write an accumulator; `mma`: all;
 // `resident`: those that read what stays from shared memory.
+// `code`: of the record where shared memory does not lie as the tiles' swizzle needs it.
 // Returns false when an earlier CTA recorded a timeout.
 __device__ __forceinline__ bool bwd_init(BwdBars* bars, int warp, const uint8_t* smem, uint8_t* zero,
-                                         uint32_t bytes, int users, int mma, int resident) {
+                                         uint32_t bytes, int users, int mma, int resident, uint32_t code) {
   if (threadIdx.x == 0) {
     // the swizzle of tiles counts from 1024-byte boundaries
-    if ((smem_u32(smem) & 1023u) != 0) atomicCAS(&g_packed_bwd_error, 0u, kDevTimeoutMask | 0x3ffu);
+    if ((smem_u32(smem) & 1023u) != 0) atomicCAS(&g_packed_bwd_error, 0u, kDevTimeoutMask | code);
     mbar_init(&bars->res_full, 1);
     mbar_init(&bars->res_empty, kCompute + resident);
     mbar_init(&bars->a_ready, kCompute);
@@ -178,8 +179,8 @@ __device__ __forceinline__ void item_done(BwdBars* bars, int r) {
   if (lane_id() == 0) mbar_arrive(&bars->item_empty[r]);
 }
 
-__device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t tmem) {
-  if (warp == kMmaWarp) wait(&bars->drain, 0, bars, 0x2ff);
+__device__ __forceinline__ void bwd_teardown(BwdBars* bars, int warp, uint32_t tmem, uint32_t code) {
+  if (warp == kMmaWarp) wait(&bars->drain, 0, bars, code);
   if (bars->abort_flag) {
     // let any bulk copy already in flight land before the CTA exits
     const uint64_t t0 = globaltimer_ns();
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + L::kBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (!bwd_init(bars, warp, smem, smem, 0, 1, kDqMma, L::kBothStay ? 0 : 1)) return;
+  if (!bwd_init(bars, warp, smem, smem, 0, 1, kDqMma, L::kBothStay ? 0 : 1, 0x23ff)) return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
   grid_dependency_launch();
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
     PackedItem it = claim();
     for (int t = 0;; ++t) {
       const int r = t % kBwdRing;
-      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
+      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x2104)) break;
       if (lane == 0) {
         bars->item[r] = it;
         mbar_arrive(&bars->item_full[r]);
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         it = claim();
         continue;
       }
-      if (tl > 0 && !warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x103)) break;
+      if (tl > 0 && !warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x2103)) break;
       bool ok = true;
       PackedItem next = it;
       if (lane == 0) {
@@ -417,10 +418,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         for (int j = 0; j < n; ++j) {
           const int s = (kvb + j) % kStages;
           const uint32_t par = (((kvb + j) / kStages) & 1) ^ 1;
-          if (!(ok = wait(&bars->x_empty[s], par, bars, 0x101))) break;
+          if (!(ok = wait(&bars->x_empty[s], par, bars, 0x2101))) break;
           mbar_arrive_expect_tx(&bars->x_full[s], L::kTile);
           load(smem + L::kK + s * L::kTile, maps + 1, &bars->x_full[s], j);
-          if (!(ok = wait(&bars->y_empty[s], par, bars, 0x102))) break;
+          if (!(ok = wait(&bars->y_empty[s], par, bars, 0x2102))) break;
           mbar_arrive_expect_tx(&bars->y_full[s], L::kTile);
           load(smem + L::kV + s * L::kTile, maps + 2, &bars->y_full[s], j);
           // the next item is asked for while the last tiles are under way
@@ -446,21 +447,21 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
     [[maybe_unused]] const uint32_t sdO = uniform(smem_u32(smem + L::kDO));
     int kvb = 0, tl = 0;
     for (int t = 0;; ++t) {
-      if (!item_wait(bars, t, 0x21b)) break;
+      if (!item_wait(bars, t, 0x221b)) break;
       const PackedItem it = bars->item[t % kBwdRing];
       item_done(bars, t % kBwdRing);
       if (uniform(it.head) < 0) break;
       const int n = uniform(dq_tiles(it, p.TT, CAUSAL));
       if (n == 0) continue;
-      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x210)) break;
+      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x2210)) break;
       bool ok = true;
       if (role == 0) {
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int pos = kvb + j, s = pos % kStages, before = pos - L::kSBufs;
           // (the P and dS in the buffer have been multiplied)
-          if (!(ok = warp_wait(&bars->x_full[s], (pos / kStages) & 1, bars, 0x211) &&
-                     (before < 0 || warp_wait(&bars->done[L::s_buf(before)], L::s_par(before), bars, 0x212))))
+          if (!(ok = warp_wait(&bars->x_full[s], (pos / kStages) & 1, bars, 0x2211) &&
+                     (before < 0 || warp_wait(&bars->done[L::s_buf(before)], L::s_par(before), bars, 0x2212))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -477,8 +478,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         for (int j = 0; j < n; ++j) {
           const int pos = kvb + j, s = pos % kStages, before = pos - L::kDpBufs;
           // (the buffer's last dP has been read)
-          if (!(ok = warp_wait(&bars->y_full[s], (pos / kStages) & 1, bars, 0x213) &&
-                     (before < 0 || warp_wait(&bars->dp_read[L::dp_buf(before)], L::dp_par(before), bars, 0x215))))
+          if (!(ok = warp_wait(&bars->y_full[s], (pos / kStages) & 1, bars, 0x2213) &&
+                     (before < 0 || warp_wait(&bars->dp_read[L::dp_buf(before)], L::dp_par(before), bars, 0x2215))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -509,13 +510,13 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         for (int j = 0; j < n; ++j) {
           const int pos = kvb + j, s = pos % kStages;
           // an item's first overwrite the accumulators that the epilogue before it reads
-          if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x216)) &&
-                     warp_wait(&bars->s_done[L::s_buf(pos)], L::s_par(pos), bars, 0x217)))
+          if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x2216)) &&
+                     warp_wait(&bars->s_done[L::s_buf(pos)], L::s_par(pos), bars, 0x2217)))
             break;
           tc_fence_after_sync();
           if (elect_one()) issue_acc(tm + L::kAcc0, tm + L::s_col(pos), s, j == 0);
           __syncwarp();
-          if (!(ok = warp_wait(&bars->ds_ready[L::s_buf(pos)], L::s_par(pos), bars, 0x214))) break;
+          if (!(ok = warp_wait(&bars->ds_ready[L::s_buf(pos)], L::s_par(pos), bars, 0x2214))) break;
           tc_fence_after_sync();
           if (elect_one()) {
             issue_acc(tm + L::kAcc1, tm + L::s_col(pos) + 16, s, j == 0);
@@ -556,11 +557,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       if (!pending) return true;
       float Di = D0;
       if (in_parts) {
-        if (!warp_wait(&bars->de_ready, te++ & 1, bars, 0x316)) return false;
+        if (!warp_wait(&bars->de_ready, te++ & 1, bars, 0x2316)) return false;
         Di = de[tr] + de[128 + tr];
       }
       if (g == 0 && pending_at >= 0) p.D[pending_vec] = Di;
-      if (!warp_wait(&bars->acc_done, (tl - 1) & 1, bars, 0x312)) return false;
+      if (!warp_wait(&bars->acc_done, (tl - 1) & 1, bars, 0x2312)) return false;
       tc_fence_after_sync();
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       return true;
     };
     for (int ti = 0;; ++ti) {
-      if (!item_wait(bars, ti, 0x304)) break;
+      if (!item_wait(bars, ti, 0x2304)) break;
       const PackedItem it = bars->item[ti % kBwdRing];
       item_done(bars, ti % kBwdRing);
       if (it.head < 0) {
@@ -609,12 +610,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       auto join = [&](float part) {
         dx[g * 128 + tr] = part;
         mbar_arrive(&bars->dx_ready);
-        ok = warp_wait(&bars->dx_ready, tl & 1, bars, 0x313);
+        ok = warp_wait(&bars->dx_ready, tl & 1, bars, 0x2313);
         Di = dx[tr] + dx[128 + tr];
       };
       // Q and dO to tensor memory: the products of the item before that read them are done (its
       // last scores and dP have been waited for)
-      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x315)) break;
+      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x2315)) break;
       float part = 0.0f;
       {
         uint32_t w[D / 4];
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       float2 exact = make_float2(0.f, 0.f);  // sum of P dP
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
-        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x311))) break;
+        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x2311))) break;
         tc_fence_after_sync();
         uint32_t pr[32];
         tmem_ld(tm + L::s_col(step) + col0, pr);
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&bars->s_done[L::s_buf(step)]);
-        if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x314))) break;
+        if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x2314))) break;
         tc_fence_after_sync();
         uint32_t rr[32];
         tmem_ld(tm + L::dp_col(step) + col0, rr);
@@ -736,7 +737,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       ++tl;
     }
   }
-  bwd_teardown(bars, warp, tmem);
+  bwd_teardown(bars, warp, tmem, 0x22ff);
 }
 
 // ============================================================ dK / dV
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int TT = p.TT64;
   if (!bwd_init(bars, warp, smem, smem + L::kQ, p.P * TT < 64 ? 2 * kStages * L::kTile : 0, 1, kDkMma,
-                    L::kBothStay ? 0 : 1))
+                    L::kBothStay ? 0 : 1, 0x33ff))
     return;
   const uint32_t tmem = bars->tmem_base;
   grid_dependency_wait();
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
     PackedItem it = claim();
     for (int t = 0;; ++t) {
       const int r = t % kBwdRing;
-      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x104)) break;
+      if (!warp_wait(&bars->item_empty[r], ((t / kBwdRing) & 1) ^ 1, bars, 0x3104)) break;
       if (lane == 0) {
         bars->item[r] = it;
         mbar_arrive(&bars->item_full[r]);
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         continue;
       }
       const CUtensorMap* maps = p.maps + 4ll * it.e.seq;
-      if (tl > 0 && !warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x102)) break;
+      if (tl > 0 && !warp_wait(&bars->res_empty, (tl - 1) & 1, bars, 0x3102)) break;
       if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) tensormap_acquire(maps + i);
@@ -842,7 +843,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       ask(tile, sub);
       for (int j = 0; j < n; ++j) {
         const int s = (sb + j) % kStages, group = it.head * p.per_kv + sub;
-        if (!(ok = warp_wait(&bars->x_empty[s], (((sb + j) / kStages) & 1) ^ 1, bars, 0x101))) break;
+        if (!(ok = warp_wait(&bars->x_empty[s], (((sb + j) / kStages) & 1) ^ 1, bars, 0x3101))) break;
         if (lane == 0) {
           mbar_expect_tx(&bars->x_full[s], 2 * q_bytes);
 #pragma unroll
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
     const uint32_t tm = uniform(tmem), sV = uniform(smem_u32(smem + L::kV));
     const uint32_t sQ = uniform(smem_u32(smem + L::kQ)), sdO = uniform(smem_u32(smem + L::kDO));
     auto stage_in = [&](int pos) {
-      return warp_wait(&bars->x_full[pos % kStages], (pos / kStages) & 1, bars, 0x205);
+      return warp_wait(&bars->x_full[pos % kStages], (pos / kStages) & 1, bars, 0x3205);
     };
     auto issue_dp = [&](int pos, bool last) {
       const uint32_t o = sdO + pos % kStages * L::kTile;
@@ -905,13 +906,13 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
     };
     int sb = 0, tl = 0;
     for (int t = 0;; ++t) {
-      if (!item_wait(bars, t, 0x207)) break;
+      if (!item_wait(bars, t, 0x3207)) break;
       const PackedItem it = bars->item[t % kBwdRing];
       item_done(bars, t % kBwdRing);
       if (uniform(it.head) < 0) break;
       const int n = uniform(dk_tiles(it, 128, TT, CAUSAL)) * p.per_kv;
       if (n == 0) continue;
-      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x201)) break;
+      if (!warp_wait(&bars->a_ready, tl & 1, bars, 0x3201)) break;
       bool ok = true;
       if (role == 0) {
 #pragma unroll 1
@@ -919,7 +920,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
           const int pos = sb + j, before = pos - L::kSBufs;
           // (the P and dS in the buffer have been multiplied)
           if (!(ok = stage_in(pos) &&
-                     (before < 0 || warp_wait(&bars->done[L::s_buf(before)], L::s_par(before), bars, 0x202))))
+                     (before < 0 || warp_wait(&bars->done[L::s_buf(before)], L::s_par(before), bars, 0x3202))))
             break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -937,7 +938,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
           const int pos = sb + j, before = pos - L::kDpBufs;
           // (the buffer's last dP has been read)
           if (!(ok = stage_in(pos) &&
-                     (before < 0 || warp_wait(&bars->dp_read[L::dp_buf(before)], L::dp_par(before), bars, 0x208))))
+                     (before < 0 || warp_wait(&bars->dp_read[L::dp_buf(before)], L::dp_par(before), bars, 0x3208))))
             break;
           tc_fence_after_sync();
           if (elect_one()) issue_dp(pos, j + 1 == n);
@@ -949,13 +950,13 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
           const int pos = sb + j;
           const uint32_t stage = pos % kStages * L::kTile;
           // an item's first overwrites the accumulators that the epilogue before it reads
-          if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x206)) &&
-                     warp_wait(&bars->s_done[L::s_buf(pos)], L::s_par(pos), bars, 0x203)))
+          if (!(ok = (j > 0 || tl == 0 || warp_wait(&bars->acc_free, (tl - 1) & 1, bars, 0x3206)) &&
+                     warp_wait(&bars->s_done[L::s_buf(pos)], L::s_par(pos), bars, 0x3203)))
             break;
           tc_fence_after_sync();
           if (elect_one()) issue_acc(tm + L::kAcc0, tm + L::s_col(pos), sdO + stage, j == 0);
           __syncwarp();
-          if (!(ok = warp_wait(&bars->ds_ready[L::s_buf(pos)], L::s_par(pos), bars, 0x204))) break;
+          if (!(ok = warp_wait(&bars->ds_ready[L::s_buf(pos)], L::s_par(pos), bars, 0x3204))) break;
           tc_fence_after_sync();
           if (elect_one()) {
             issue_acc(tm + L::kAcc1, tm + L::s_col(pos) + 16, sQ + stage, j == 0);
@@ -985,7 +986,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
     long long pending_k = -1, pending_v = -1;
     auto epilogue = [&]() {
       if (!pending) return true;
-      if (!warp_wait(&bars->acc_done, (tl - 1) & 1, bars, 0x302)) return false;
+      if (!warp_wait(&bars->acc_done, (tl - 1) & 1, bars, 0x3302)) return false;
       tc_fence_after_sync();
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -999,7 +1000,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       return true;
     };
     for (int ti = 0;; ++ti) {
-      if (!item_wait(bars, ti, 0x305)) break;
+      if (!item_wait(bars, ti, 0x3305)) break;
       const PackedItem it = bars->item[ti % kBwdRing];
       item_done(bars, ti % kBwdRing);
       if (it.head < 0) {
@@ -1022,7 +1023,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       }
       // K (and V) to tensor memory: the products of the item before that read them are done (its last
       // scores and dP have been waited for)
-      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x307)) break;
+      if (!warp_wait(&bars->res_full, tl & 1, bars, 0x3307)) break;
       {
         uint32_t w[D / 4];
         load_half_row<D>(smem + L::kK, tr, g, true, w);
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       for (int j = 0; j < n; ++j) {
         const int step = nb + j;
         const float* nlse = reinterpret_cast<const float*>(smem + L::kVec) + (step % kStages) * 128;
-        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x301))) break;
+        if (!(ok = warp_wait(&bars->s_full[L::s_buf(step)], L::s_par(step), bars, 0x3301))) break;
         tc_fence_after_sync();
         uint32_t pr[32];
         tmem_ld(tm + L::s_col(step) + col0, pr);
@@ -1086,7 +1087,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&bars->s_done[L::s_buf(step)]);
-        if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x306))) break;
+        if (!(ok = warp_wait(&bars->dp_full[L::dp_buf(step)], L::dp_par(step), bars, 0x3306))) break;
         tc_fence_after_sync();
         uint32_t rr[32], ds[16];
         const uint32_t dp = tm + L::dp_col(step) + col0;
@@ -1122,7 +1123,7 @@ __global__ void __launch_bounds__(kDkThreads, 1) fa_packed_dkdv_kernel(const __g
       ++tl;
     }
   }
-  bwd_teardown(bars, warp, tmem);
+  bwd_teardown(bars, warp, tmem, 0x32ff);
 }
 
 // Items of a launch as CTAs, at most one an SM.

@@ -19,7 +19,7 @@ namespace fa {
 // Device error codes (stored in the library's device error word).
 enum : uint32_t {
   kDevOk = 0,
-  kDevTimeoutMask = 0x80000000u,  // | (site id << 8) | role
+  kDevTimeoutMask = 0x80000000u,  // | the code of the wait that gave up
 };
 
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;  // 2 s
