@@ -796,6 +796,49 @@ int fa_backward_packed(const fa_heads* q, const fa_heads* k, const fa_heads* v, 
 }
 
 // ---------------------------------------------------------------- rotation
+// The tables hold 64 bits of a turn, more than a double has: numbers as sums of two doubles, after Dekker
+// ("A floating-point technique for extending the available precision", 1971), good to about 2^-100 of
+// the value.  Every product that is added to something is an explicit fma, so that no compiler
+// has one to contract.
+struct Twofold {
+  double hi, lo;
+};
+static Twofold tf_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+static Twofold operator+(const Twofold& a, const Twofold& b) {
+  const Twofold s = tf_sum(a.hi, b.hi);
+  return tf_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+static Twofold operator*(const Twofold& a, const Twofold& b) {
+  const double p = std::fma(a.hi, b.hi, 0.0), e = std::fma(a.hi, b.hi, -p);
+  return tf_sum(p, std::fma(a.hi, b.lo, std::fma(a.lo, b.hi, e)));
+}
+static Twofold operator/(const Twofold& a, const Twofold& b) {
+  Twofold q = {a.hi / b.hi, 0.0};
+  for (int i = 0; i < 2; ++i) {
+    const Twofold r = a + b * Twofold{-q.hi, -q.lo};
+    q = q + Twofold{r.hi / b.hi, 0.0};
+  }
+  return q;
+}
+static Twofold tf_power(const Twofold& x, int n) {
+  Twofold y = {1.0, 0.0};
+  for (int i = 0; i < n; ++i) y = y * x;
+  return y;
+}
+// x^(1/n): one step of Newton's method from a root that is right to a double.
+static Twofold tf_root(double x, int n) {
+  const Twofold r = {std::pow(x, 1.0 / n), 0.0};
+  const Twofold q = Twofold{x, 0.0} / tf_power(r, n);
+  return r + r * ((q + Twofold{-1.0, 0.0}) / Twofold{static_cast<double>(n), 0.0});
+}
+static Twofold tf_within_one(const Twofold& x) {
+  if (!(x.hi > 0.0)) return {0.0, 0.0};
+  return x.hi >= 1.0 ? Twofold{1.0, 0.0} : x;
+}
+
 int fa_rotary_table(unsigned long long* turns, int rot, double base, int scaling, double factor,
                     double original, double low, double high) {
   if (!turns) return FA_ERR_NULL;
@@ -807,27 +850,36 @@ int fa_rotary_table(unsigned long long* turns, int rot, double base, int scaling
   if (blend && (!(original >= 1.0) || !std::isfinite(original) || !(low > 0.0) || !(high > low) ||
                 !std::isfinite(high)))
     return FA_ERR_SHAPE;
-  const double pi = 3.14159265358979323846;
-  if (scaling == FA_SCALE_BASE) base *= std::pow(factor, rot / (rot - 2.0));
-  if (!std::isfinite(base)) return FA_ERR_SHAPE;
-  // the pair that makes t turns within the original context: original * base^(-2i/rot) = 2 pi t
-  auto pair_of = [&](double t) { return rot * std::log(original / (2.0 * pi * t)) / (2.0 * std::log(base)); };
+  if (scaling == FA_SCALE_BASE && !std::isfinite(base * std::pow(factor, rot / (rot - 2.0)))) return FA_ERR_SHAPE;
+  const Twofold one = {1.0, 0.0}, two_pi = {6.283185307179586232, 2.4492935982947063545e-16};
+  const int pairs = rot / 2;
+  // f_i = step^-i
+  Twofold step = tf_root(base, pairs);
+  if (scaling == FA_SCALE_BASE) step = step * tf_root(factor, pairs - 1);
   double first = 0.0, last = 1.0;
   if (scaling == FA_SCALE_INDEX) {
+    // the pair that makes t turns within the original context: original * base^(-2i/rot) = 2 pi t
+    auto pair_of = [&](double t) { return rot * std::log(original / (two_pi.hi * t)) / (2.0 * std::log(base)); };
     first = std::fmax(std::floor(pair_of(high)), 0.0);
     last = std::fmin(std::ceil(pair_of(low)), rot - 1.0);
   }
-  for (int i = 0; i < rot / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / rot);
-    if (scaling == FA_SCALE_LINEAR) f /= factor;
+  Twofold turns_back = two_pi;  // positions a turn, 2 pi / f_i
+  for (int i = 0; i < pairs; ++i) {
+    Twofold t = one / turns_back;
+    turns_back = turns_back * step;
+    if (scaling == FA_SCALE_LINEAR) t = t / Twofold{factor, 0.0};
     if (blend) {
-      const double g = scaling == FA_SCALE_TURNS
-                           ? (original * f / (2.0 * pi) - low) / (high - low)
-                           : 1.0 - (i - first) / std::fmax(last - first, 1e-3);
-      const double keep = std::fmin(std::fmax(g, 0.0), 1.0);
-      f = keep * f + (1.0 - keep) * f / factor;
+      const Twofold g =
+          scaling == FA_SCALE_TURNS
+              ? (t * Twofold{original, 0.0} + Twofold{-low, 0.0}) / tf_sum(high, -low)
+              : one + Twofold{first - i, 0.0} / Twofold{std::fmax(last - first, 1e-3), 0.0};
+      const Twofold keep = tf_within_one(g);
+      t = t * (keep + (one + Twofold{-keep.hi, -keep.lo}) / Twofold{factor, 0.0});
     }
-    turns[i] = static_cast<unsigned long long>(std::nearbyint(f / (2.0 * pi) * 18446744073709551616.0));
+    // below 2^62 of 2^64; the higher part may be no whole number, the lower one as large as 2^9
+    const double hi = std::ldexp(t.hi, 64), whole = std::floor(hi);
+    turns[i] = static_cast<unsigned long long>(whole) +
+               static_cast<long long>(std::floor((hi - whole) + std::ldexp(t.lo, 64) + 0.5));
   }
   return FA_OK;
 }
