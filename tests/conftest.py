@@ -22,6 +22,11 @@ def pytest_collection_modifyitems(config, items):
     except Exception:  # pragma: no cover
         pass
     if have_gpu:
+        # calls with such addresses are refused, or end at the check of the GPU where there is none
+        skip = pytest.mark.skip(reason="passes addresses of no memory: only where there is no CUDA device")
+        for it in items:
+            if "gpu" not in it.keywords and hasattr(getattr(it, "module", None), "FAKE"):
+                it.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA device")
     for it in items:
