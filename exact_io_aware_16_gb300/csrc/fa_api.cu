@@ -638,7 +638,7 @@ int fa_decode_tree(const fa_cache* cache, const void* q, const int* lens,
 
 // ---------------------------------------------------------------- packed sequences
 // A tensor of `heads` heads of B x T token rows as the kernels take it: strides that no
-// element depends on put to what they would be in memory without gaps.
+// element depends on put to d.
 static int view_heads(const fa_heads* t, int heads, long long B, long long T, int d,
                       fa::HeadsView* v) {
   if (!t || (!t->p && T > 0)) return FA_ERR_NULL;
@@ -646,8 +646,7 @@ static int view_heads(const fa_heads* t, int heads, long long B, long long T, in
   v->p = t->p;
   v->heads = heads;
   v->head = heads > 1 ? t->head_stride : d;
-  v->token = T > 1 ? t->token_stride : v->head * heads;
-  if (T <= 1 && heads <= 1) v->token = d;
+  v->token = T > 1 ? t->token_stride : d;
   v->batch = B > 1 ? t->batch_stride : 0;
   if (heads > 1 && v->head < d) return FA_ERR_SHAPE;
   if (T > 1 && v->token < d) return FA_ERR_SHAPE;
