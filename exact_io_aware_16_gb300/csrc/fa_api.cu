@@ -1,6 +1,7 @@
 // fa_api.cu — the C ABI of libfa: argument validation, TMA tensor-map
 // construction and kernel launches.  No device memory is allocated here.
 #include <atomic>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -653,10 +654,17 @@ static int view_heads(const fa_heads* t, int heads, long long B, long long T, in
   // 16 heads of at most 2^35 bytes between rows are a stride that a tensor map takes
   const long long most = 1ll << 34;
   if (v->head > most || v->token > most || v->batch < 0 || v->batch > most) return FA_ERR_SHAPE;
-  const bool heads_inside = v->token >= (heads - 1) * v->head + d;
-  const bool tokens_inside = T < 1 || v->head >= (T - 1) * v->token + d;
-  if (heads > 1 && T > 1 && !heads_inside && !tokens_inside) return FA_ERR_SHAPE;
-  if (B > 1 && v->batch < d) return FA_ERR_SHAPE;
+  // no two rows overlap: each axis steps over all that the axes of smaller steps reach
+  struct {
+    long long step, count;
+  } axis[3] = {{v->head, heads}, {v->token, T}, {v->batch, B}};
+  std::sort(axis, axis + 3, [](const auto& x, const auto& y) { return x.step < y.step; });
+  __int128 reach = d;
+  for (const auto& x : axis) {
+    if (x.count <= 1) continue;
+    if (x.step < reach) return FA_ERR_SHAPE;
+    reach += static_cast<__int128>(x.count - 1) * x.step;
+  }
   if (!aligned16(t->p) || (v->head & 7) || (v->token & 7) || (v->batch & 7)) return FA_ERR_ALIGN;
   return FA_OK;
 }

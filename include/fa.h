@@ -375,9 +375,10 @@ int fa_cache_commit(const fa_cache* cache, const int* lens, const int* path,
  * h * head_stride + c].  Strides are in elements and multiples of 8, p is
  * 16-byte aligned.  So [tokens][heads][d], a part of the heads of a projection's
  * output and [B][H][N][d] are all read and written as they lie.  A stride is not
- * looked at where its axis has one entry; rows must not overlap: the tokens of
- * a head lie within its head_stride, or the heads of a token within its
- * token_stride (FA_ERR_SHAPE otherwise).  The calls on packed sequences have no
+ * looked at where its axis has one entry; rows must not overlap: each stride is at
+ * least what the axes of smaller strides span together (the heads of a token within
+ * its token_stride, or the tokens of a head within its head_stride, and either within
+ * or around the sequences of a batch; FA_ERR_SHAPE otherwise).  The calls on packed sequences have no
  * batch axis: their tokens count through all sequences.
  * The struct is read during the call only.
  */
