@@ -13,6 +13,7 @@
 // sequences of up to 1500 tokens, 16 heads on 2, full, take 116 us with the tensor core busy for
 // 40 % of them, and 64 causal samples of up to 512 tokens, 12 heads, 48 us.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -26,6 +27,8 @@ namespace fa {
 namespace {
 
 __device__ unsigned int g_packed_error;
+// Set by the first launch: until then the record above is clean and need not be copied, which takes 10 us.
+std::atomic<bool> g_packed_used{false};
 
 // ============================================================ plan
 constexpr int kPlanThreads = 1024;
@@ -716,6 +719,7 @@ cudaError_t launch_packed_plan(const PackedArgs& a, const CUtensorMap* maps, int
 }
 
 cudaError_t launch_forward_packed(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s) {
+  g_packed_used.store(true, std::memory_order_release);
   const PackedTiling t = packed_tiling(a.q.heads, a.k.heads);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, a.q.heads, a.k.heads, false);
   cudaError_t e = launch_packed_plan(a, maps, 3, false, s);
@@ -744,6 +748,8 @@ cudaError_t launch_forward_packed(const PackedArgs& a, const CUtensorMap* maps, 
 }
 
 cudaError_t packed_read_clear_error(uint32_t* out, cudaStream_t s) {
+  *out = 0;
+  if (!g_packed_used.load(std::memory_order_acquire)) return cudaSuccess;
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return e;
   uint32_t v = 0;

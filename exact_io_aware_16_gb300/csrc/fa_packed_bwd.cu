@@ -32,6 +32,7 @@
 // Query tiles that see 64 keys or fewer take that sum as D from the start, which their threads have
 // in registers before dS is needed: where a query sees its own key alone, dS is zero.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 #include <cuda.h>
@@ -46,6 +47,8 @@ namespace fa {
 namespace {
 
 __device__ unsigned int g_packed_bwd_error;
+// Set by the first launch: until then the record above is clean and need not be copied, which takes 10 us.
+std::atomic<bool> g_packed_bwd_used{false};
 
 constexpr int kDqMma = 3, kDkMma = 3;  // MMA warps
 constexpr int kCompute = 256;
@@ -1153,6 +1156,7 @@ constexpr int kShortDq = 1, kShortDk = 4;
 }  // namespace
 
 cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s) {
+  g_packed_bwd_used.store(true, std::memory_order_release);
   const int Hq = a.q.heads, Hkv = a.k.heads;
   const PackedTiling t = packed_tiling(Hq, Hkv);
   const PackedLayout l = packed_layout(a.B, a.total_q, a.total_k, Hq, Hkv, true);
@@ -1203,6 +1207,8 @@ cudaError_t launch_backward_packed(const PackedArgs& a, const CUtensorMap* maps,
 }
 
 cudaError_t packed_bwd_read_clear_error(uint32_t* out, cudaStream_t s) {
+  *out = 0;
+  if (!g_packed_bwd_used.load(std::memory_order_acquire)) return cudaSuccess;
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return e;
   uint32_t v = 0;
