@@ -597,12 +597,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         }
         continue;
       }
-      // (a row that sees no key counts as one of zeros, whatever its q and dO hold)
-      const bool live = valid && (!CAUSAL || tok + off >= 0);
       // asked for here, used below
-      float lse = live ? p.lse[vec] : INFINITY;
+      float lse = valid ? p.lse[vec] : INFINITY;
       uint4 o_row[D / 16];
-      if (n > 1 && live) {
+      if (n > 1 && valid) {
         const uint4* a = reinterpret_cast<const uint4*>(p.o + token * p.o_token + head * p.o_head + (D / 2) * g);
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) o_row[e] = a[e];
@@ -622,8 +620,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       float part = 0.0f;
       {
         uint32_t w[D / 4];
-        load_half_row<D>(smem + L::kQ, tr, g, live, w);
+        load_half_row<D>(smem + L::kQ, tr, g, valid, w);
         store_half_row<D>(tm + L::kStay0, g, w);
+        // (a row that sees no key counts as one of zeros, whatever its dO holds)
+        const bool live = valid && (!CAUSAL || tok + off >= 0);
         load_half_row<D>(smem + L::kDO, tr, g, live, w);
         if constexpr (L::kBothStay)
           store_half_row<D>(tm + L::stay1_col(), g, w);
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&bars->a_ready);
-        if (n > 1 && live) {
+        if (n > 1 && valid) {
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
             const uint32_t xs[4] = {o_row[e].x, o_row[e].y, o_row[e].z, o_row[e].w};
@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
       }
       // a row without keys of its own, or behind the sequence: P = 2^-inf (one that sees keys whose scores are
       // all -inf has lse = -inf, and P = 2^(-inf + inf), NaN by the definition)
+      asm volatile("" : "+f"(lse));  // (not multiplied where it was asked for, which would wait for it there)
       const float lse2 = lse * kLog2e;
       const uint32_t col0 = 32u * g;
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(-lse2, -lse2);
