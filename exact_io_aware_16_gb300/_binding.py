@@ -927,7 +927,8 @@ class Rotary:
     within the `original` context stay, those below `low` are divided by factor,
     between them a blend, linear in the turns or in the pair's index).  amplitude
     multiplies the rotated elements.  turns: the table, torch.int64 [rot / 2] on
-    the GPU (unsigned 64-bit fractions of a turn), which the object keeps."""
+    the GPU (unsigned 64-bit fractions of a turn), which the object keeps: keep the
+    object until the calls that use it have run."""
 
     _SCALING = {None: 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
 

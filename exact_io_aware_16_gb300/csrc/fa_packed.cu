@@ -8,7 +8,8 @@
 //
 // Bound by the tensor core at d = 128: two causal sequences of 8192, 32 heads on 8, take 640 us on a
 // cool GPU, 1.72 PFLOP/s of the triangle, and 710 us in a loop, under the power limit. 24 prompts
-// of 1 to 2048 tokens take 250 us: their diagonal and last tiles are partly empty. At d = 64 the
+// of 1 to 2048 tokens take 250 us: 21 items a CTA, whose starts and ends take 2.7 us each (the tiles themselves are
+// 90 % useful). At d = 64 the
 // products are half as long, and the chain S, softmax, P V of a tile is what takes the time: 31
 // sequences of up to 1500 tokens, 16 heads on 2, full, take 116 us with the tensor core busy for
 // 40 % of them, and 64 causal samples of up to 512 tokens, 12 heads, 48 us.

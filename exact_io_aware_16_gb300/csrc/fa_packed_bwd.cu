@@ -21,9 +21,10 @@
 // at half its rate, and those of 64 columns run at full rate (33.8 cycles of 32; from shared memory 49).
 // Tensor memory has room for all that stays at d = 64, and for one of its two tensors at d = 128.
 //
-// Measured, four causal samples of 1000 to 8192 tokens (17335), 32 heads on 8, d = 128: dq 1090 us, dk and
-// dv 1010 us, 1.64 PFLOP/s of the eight products. 31 samples of up to 1500 tokens, 16 heads on 2, d = 64, full:
-// 234 and 238 us; there the threads' part of a tile takes longer than its products.
+// Measured, four causal samples of 1000 to 8192 tokens (17335), 32 heads on 8, d = 128: dq 1060 us, dk and
+// dv 1005 us, the tensor core busy for 70 and 76 % of them; 1.66 PFLOP/s of the eight products,
+// near what the power limit leaves. 31 samples of up to 1500 tokens, 16 heads on 2, d = 64, full:
+// 230 and 232 us, 39 and 44 % busy; there the threads' part of a tile takes longer than its products.
 //
 // D from the bf16 o is off by half a bf16 step of it, and by what the rounding of P cost o.  A row's dS
 // have that error in common: it moves dq by as much times the row's mean key, which for
