@@ -39,9 +39,11 @@
  *    returns FA_ERR_CUDA.  A device-side pipeline timeout is reported later
  *    by fa_get_device_error().
  *  - A recorded timeout is sticky: until fa_get_device_error() reads and
- *    clears it, every later launch of this library on the device exits at
- *    entry without computing anything, while the calls that made those
- *    launches still return FA_OK.  Outputs written after a timeout are
+ *    clears it, every later launch on the device of a kernel that shares the
+ *    record (one each for the forward kernels, the backward kernels, the
+ *    decode, the tree decode, and the packed forward and backward kernels)
+ *    exits at entry without computing anything, while the calls that made
+ *    those launches still return FA_OK.  Outputs written after a timeout are
  *    therefore stale until the record is cleared: check fa_get_device_error()
  *    (or fa_host_wait(), which does the same) before trusting results.
  *  - Only sm_103 (GB300) devices are accepted (FA_ERR_ARCH otherwise).
@@ -378,8 +380,8 @@ int fa_cache_commit(const fa_cache* cache, const int* lens, const int* path,
  * looked at where its axis has one entry; rows must not overlap: each stride is at
  * least what the axes of smaller strides span together (the heads of a token within
  * its token_stride, or the tokens of a head within its head_stride, and either within
- * or around the sequences of a batch; FA_ERR_SHAPE otherwise).  The calls on packed sequences have no
- * batch axis: their tokens count through all sequences.
+ * or around the sequences of a batch; FA_ERR_SHAPE otherwise).  The calls on packed
+ * sequences have no batch axis: their tokens count through all sequences.
  * The struct is read during the call only.
  */
 typedef struct fa_heads {
@@ -408,9 +410,10 @@ typedef struct fa_heads {
  *  - What one sequence holds, NaN and infinities included, reaches no other.
  *    Tokens of o and lse in no sequence (before cu_q[0], from cu_q[B] on) are
  *    left as they were.  Within a sequence, and for a key head and its query
- *    heads, a NaN or infinity reaches what sees it, and may reach: from a value row the o and dq, from a
- *    key row the dq (o and lse not) of queries that do not see the row; from a row of q or dO the
- *    dk and dv of keys that it does not see.  Outputs overlap no input.
+ *    heads, a NaN or infinity reaches what sees it, and may reach: from a value row
+ *    the o and dq, from a key row the dq (o and lse not) of queries that do not see
+ *    the row; from a row of q or dO the dk and dv of keys that it does not see.
+ *    Outputs overlap no input.
  *  - B >= 1, 0 <= total_q, total_k; d in {64, 128}; Hq * (total_q / 8 + B) and
  *    Hkv * (total_k / 128 + B) below 2^31, B below 2^20.  scale > 0 and finite.
  *  - workspace: device memory, 256-byte aligned, contents irrelevant, of
