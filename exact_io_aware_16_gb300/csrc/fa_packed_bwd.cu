@@ -651,8 +651,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) fa_packed_dq_kernel(const __gri
         join(part);
         if (!ok) break;
       }
-      // a row without keys of its own, or behind the sequence: P = 2^-inf (one that sees keys whose scores are
-      // all -inf has lse = -inf, and P = 2^(-inf + inf), NaN by the definition)
+      // a row behind the sequence: P = 2^-inf; one that sees no key: all of it is masked; one that sees keys whose
+      // scores are all -inf: lse = -inf, P = 2^(-inf + inf), NaN by the definition
       asm volatile("" : "+f"(lse));  // (not multiplied where it was asked for, which would wait for it there)
       const float lse2 = lse * kLog2e;
       const uint32_t col0 = 32u * g;
